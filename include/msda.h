@@ -362,6 +362,68 @@ MSDA_API const char *msda_status_string(msda_status_t status);
 /* Library version, major*10000 + minor*100 + patch. Host only. */
 MSDA_API int msda_version(void);
 
+/* ---------------------------------------------------------------------------
+ * Around the operator in a training step: layer norm with the residual added
+ * on the way in, and the global gradient norm with clipping. A Deformable-DETR
+ * encoder layer ends each sublayer in norm(input + sublayer(input)) and trains
+ * with its gradients clipped to a global norm. */
+
+/* N rows of C channels, contiguous. Supported: N >= 0 (zero is a valid empty
+ * call), 1 <= C <= 2^20, N*C <= 2^60. Every C and every element alignment is
+ * accepted; rows that all start on 16-byte boundaries (C a multiple of
+ * 16 / element size, pointers 16-byte aligned) are read in 16-byte vectors. */
+typedef struct {
+    int64_t N, C;
+} msda_norm_dims_t;
+
+/* Layer norm, forward. With s = x + residual (residual NULL: s = x), and per
+ * row mean = sum_c(s) / C, var = sum_c((s - mean)^2) / C:
+ *   out = (s - mean) * rstd * weight + bias,   rstd = 1 / sqrt(var + eps).
+ * s is held in fp32 (fp64 for MSDA_F64) and not rounded before it is
+ * normalised; out is rounded once.
+ *   x, residual, out  (N, C) `dtype`; residual may be NULL
+ *   weight, bias      (C,) `param_dtype`; NULL: ones / zeros
+ *   sum               (N, C) `dtype`: receives s, rounded; NULL: not wanted
+ *   mean, rstd        (N,) float (double for MSDA_F64): what the backward
+ *                     needs; both NULL or neither
+ * param_dtype: `dtype`, or MSDA_F32 with 16-bit data. eps >= 0; a row of
+ * equal entries with eps = 0 gives NaN. A row with a non-finite entry, or
+ * whose squared distances from the mean leave fp32's range, gives non-finite
+ * results in that row alone. Outputs must not overlap inputs.
+ * Alignment: element size. Errors: MSDA_ERR_NULL, _SHAPE (also eps < 0 or
+ * NaN), _DTYPE, _ALIGN before any launch; MSDA_ERR_CUDA. */
+MSDA_API msda_status_t msda_layer_norm_forward(const void *x, const void *residual,
+                                               const void *weight, const void *bias, void *out,
+                                               void *sum, void *mean, void *rstd, double eps,
+                                               const msda_norm_dims_t *dims, msda_dtype_t dtype,
+                                               msda_dtype_t param_dtype, void *stream);
+
+/* Bytes of device workspace msda_layer_norm_backward needs for the weight and
+ * bias gradients. Returns 0 for invalid dims or dtype. */
+MSDA_API size_t msda_layer_norm_backward_workspace_bytes(const msda_norm_dims_t *dims,
+                                                         msda_dtype_t dtype);
+
+/* Layer norm, backward. grad_out (N, C) is the gradient of out and grad_sum
+ * (N, C; NULL: none) that of sum; x, residual, weight, mean and rstd as the
+ * forward had and wrote them. With xh = (s - mean) * rstd, g = grad_out * weight:
+ *   grad_x      (N, C) = rstd * (g - mean_c(g) - xh * mean_c(g * xh)) + grad_sum,
+ *                        the gradient of x and of residual alike
+ *   grad_weight (C,)   = sum over rows of grad_out * xh, `param_dtype`
+ *   grad_bias   (C,)   = sum over rows of grad_out, `param_dtype`
+ * All three are OVERWRITTEN; any of them may be NULL. The column sums are held
+ * in fp32 (fp64 for MSDA_F64) and added in an order that the sizes alone fix:
+ * the same call gives the same bits. N = 0 writes zeros to grad_weight and
+ * grad_bias.
+ * workspace: at least msda_layer_norm_backward_workspace_bytes(...) bytes,
+ *   16-byte aligned, owned by the caller, overwritten (may be NULL when
+ *   neither grad_weight nor grad_bias is wanted).
+ * Errors: as the forward, plus MSDA_ERR_WORKSPACE. */
+MSDA_API msda_status_t msda_layer_norm_backward(
+    const void *grad_out, const void *grad_sum, const void *x, const void *residual,
+    const void *weight, const void *mean, const void *rstd, void *grad_x, void *grad_weight,
+    void *grad_bias, void *workspace, size_t workspace_bytes, const msda_norm_dims_t *dims,
+    msda_dtype_t dtype, msda_dtype_t param_dtype, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -8,6 +8,7 @@ the call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -29,11 +30,16 @@ EXPORTED = ("msda_forward", "msda_backward_workspace_bytes", "msda_backward",
             "msda_backward_static_workspace", "msda_forward_softmax", "msda_backward_softmax",
             "msda_debug_corners", "msda_checked_build", "msda_device_check",
             "msda_debug_bounds_self_test", "msda_set_sample_split", "msda_status_string",
-            "msda_version")
+            "msda_version", "msda_layer_norm_forward", "msda_layer_norm_backward_workspace_bytes",
+            "msda_layer_norm_backward")
 
 
 class msda_dims_t(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int64) for n in ("B", "S", "Q", "M", "D", "L", "K")]
+
+
+class msda_norm_dims_t(ctypes.Structure):
+    _fields_ = [("N", ctypes.c_int64), ("C", ctypes.c_int64)]
 
 
 class MSDAError(RuntimeError):
@@ -93,6 +99,15 @@ def load(path: str | None = None):
     so.msda_set_sample_split.restype = ctypes.c_int
     so.msda_status_string.argtypes = [ctypes.c_int]
     so.msda_status_string.restype = ctypes.c_char_p
+    norm_dims = ctypes.POINTER(msda_norm_dims_t)
+    so.msda_layer_norm_forward.argtypes = [vp] * 8 + [ctypes.c_double, norm_dims, ctypes.c_int,
+                                                      ctypes.c_int, vp]
+    so.msda_layer_norm_forward.restype = ctypes.c_int
+    so.msda_layer_norm_backward_workspace_bytes.argtypes = [norm_dims, ctypes.c_int]
+    so.msda_layer_norm_backward_workspace_bytes.restype = ctypes.c_size_t
+    so.msda_layer_norm_backward.argtypes = [vp] * 11 + [ctypes.c_size_t, norm_dims, ctypes.c_int,
+                                                        ctypes.c_int, vp]
+    so.msda_layer_norm_backward.restype = ctypes.c_int
     so.msda_version.argtypes = []
     so.msda_version.restype = ctypes.c_int
     return so
@@ -322,3 +337,161 @@ def multi_scale_deformable_attention(value, spatial_shapes, level_start_index,
     attn = attention_weights.reshape(B, Q, M, L, K).contiguous()
     return MSDAFunction.apply(value.contiguous(), spatial_shapes, level_start_index,
                               sampling_locations.contiguous(), attn, accum, softmax)
+
+
+# ------------------------------------------------------- layer norm, residual
+
+def _at(t):
+    return t.data_ptr() if t is not None else None
+
+
+@contextlib.contextmanager
+def _on(device, stream):
+    """Make `device` current, and `stream` (None: its current stream), so that what is
+    allocated belongs to the stream the kernels run on; yields the stream's handle."""
+    if stream is not None and stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
+    with torch.cuda.device(device):
+        if stream is None:
+            yield torch.cuda.current_stream(device).cuda_stream
+        else:
+            with torch.cuda.stream(stream):
+                yield stream.cuda_stream
+
+
+def _check_like(name, t, shape, dtype, device):
+    if t is None:
+        return
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, x is on {device}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} is {t.dtype}, expected {dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} is not contiguous: libmsda needs contiguous tensors")
+
+
+def _norm_operands(x, residual, weight, bias):
+    """Checks of the operands the forward and the backward share; (dims, type of the
+    parameters, type of the statistics)."""
+    if not x.is_cuda:
+        raise ValueError("libmsda runs on CUDA tensors only (no CPU path)")
+    if x.dim() < 1:
+        raise ValueError("x needs a channel dimension")
+    _dtype(x)
+    _check_like("x", x, x.shape, x.dtype, x.device)
+    _check_like("residual", residual, x.shape, x.dtype, x.device)
+    params = weight if weight is not None else bias
+    pdt = params.dtype if params is not None else x.dtype
+    if pdt != x.dtype and not (pdt == torch.float32 and x.dtype in (torch.bfloat16, torch.float16)):
+        raise ValueError(f"parameters of {pdt} with data of {x.dtype}: give the data's type, or "
+                         "float32 with 16-bit data")
+    C = x.shape[-1]
+    for name, t in (("weight", weight), ("bias", bias)):
+        _check_like(name, t, (C,), pdt, x.device)
+    dims = msda_norm_dims_t(x.numel() // C if C else 0, C)
+    return dims, pdt, torch.float64 if x.dtype == torch.float64 else torch.float32
+
+
+def _apart(outs, ins):
+    """Refuse an output the caller gave that shares memory with an input or another output."""
+    spans = [(t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for t in outs + ins
+             if t is not None]
+    n = len([t for t in outs if t is not None])
+    for i, (lo, hi) in enumerate(spans[:n]):
+        for lo2, hi2 in spans[i + 1:]:
+            if lo < hi2 and lo2 < hi:
+                raise ValueError("an output overlaps an input or another output")
+
+
+def msda_layer_norm_forward(x, weight=None, bias=None, residual=None, eps: float = 1e-5,
+                            return_sum: bool = False, stats: bool = True, out=None, stream=None):
+    """(out, sum, mean, rstd) of the rows of x + residual over x's last dimension; sum is
+    None unless return_sum, mean and rstd are None unless stats (the backward needs them).
+    See msda_layer_norm_forward in include/msda.h."""
+    dims, pdt, sdt = _norm_operands(x, residual, weight, bias)
+    if out is not None:
+        _check_like("out", out, x.shape, x.dtype, x.device)
+        _apart([out], [x, residual, weight, bias])
+    with _on(x.device, stream) as s:
+        if out is None:
+            out = torch.empty_like(x)
+        total = torch.empty_like(x) if return_sum else None
+        mean = torch.empty(x.shape[:-1], dtype=sdt, device=x.device) if stats else None
+        rstd = torch.empty_like(mean) if stats else None
+        _call("msda_layer_norm_forward", lib().msda_layer_norm_forward(
+            _at(x), _at(residual), _at(weight), _at(bias), _at(out), _at(total), _at(mean),
+            _at(rstd), eps, ctypes.byref(dims), _dtype(x), _DTYPES[pdt], s))
+    return out, total, mean, rstd
+
+
+def msda_layer_norm_backward(grad_out, x, mean, rstd, weight=None, residual=None, grad_sum=None,
+                             param_dtype=None, want=(True, True, True), stream=None):
+    """(grad_x, grad_weight, grad_bias), None where `want` says so; grad_x is the gradient of
+    x and of residual alike. param_dtype: the parameters' type where weight is None. See
+    msda_layer_norm_backward in include/msda.h."""
+    dims, pdt, sdt = _norm_operands(x, residual, weight, None)
+    if weight is None and param_dtype is not None:
+        pdt = param_dtype
+    _check_like("grad_out", grad_out, x.shape, x.dtype, x.device)
+    _check_like("grad_sum", grad_sum, x.shape, x.dtype, x.device)
+    _check_like("mean", mean, x.shape[:-1], sdt, x.device)
+    _check_like("rstd", rstd, x.shape[:-1], sdt, x.device)
+    with _on(x.device, stream) as s:
+        grad_x = torch.empty_like(x) if want[0] else None
+        grad_weight = torch.empty((dims.C,), dtype=pdt, device=x.device) if want[1] else None
+        grad_bias = torch.empty((dims.C,), dtype=pdt, device=x.device) if want[2] else None
+        need, workspace = 0, None
+        if want[1] or want[2]:
+            need = lib().msda_layer_norm_backward_workspace_bytes(ctypes.byref(dims), _dtype(x))
+            workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+        _call("msda_layer_norm_backward", lib().msda_layer_norm_backward(
+            _at(grad_out), _at(grad_sum), _at(x), _at(residual), _at(weight), _at(mean), _at(rstd),
+            _at(grad_x), _at(grad_weight), _at(grad_bias), _at(workspace), need,
+            ctypes.byref(dims), _dtype(x), _DTYPES.get(pdt, -1), s))
+    return grad_x, grad_weight, grad_bias
+
+
+class LayerNormFunction(torch.autograd.Function):
+    """Autograd wrapper of the two calls above (first derivatives only)."""
+
+    @staticmethod
+    def forward(ctx, x, residual, weight, bias, eps, return_sum):
+        out, total, mean, rstd = msda_layer_norm_forward(x, weight, bias, residual, eps, return_sum)
+        ctx.save_for_backward(x, residual, weight, mean, rstd)
+        ctx.param_dtype = weight.dtype if weight is not None else bias.dtype if bias is not None else None
+        ctx.set_materialize_grads(False)
+        return (out, total) if return_sum else out
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad_out, grad_sum=None):
+        x, residual, weight, mean, rstd = ctx.saved_tensors
+        need_x, need_res, need_w, need_b = ctx.needs_input_grad[:4]
+        if grad_sum is not None:
+            grad_sum = grad_sum.contiguous()
+        if grad_out is None:             # the normalised rows were not used
+            gx, gw, gb = grad_sum, None, None
+        else:
+            gx, gw, gb = msda_layer_norm_backward(
+                grad_out.contiguous(), x, mean, rstd, weight, residual, grad_sum, ctx.param_dtype,
+                (need_x or need_res, need_w, need_b))
+        return gx if need_x else None, gx if need_res else None, gw, gb, None, None
+
+
+def layer_norm(x, weight=None, bias=None, residual=None, eps: float = 1e-5, return_sum: bool = False):
+    """Differentiable layer norm over x's last dimension, of x + residual where a residual is
+    given (same shape as x; the sum is not rounded before it is normalised). weight and bias
+    (C,) of x's type, or float32 with 16-bit x. return_sum: (normalised, x + residual)."""
+    if return_sum and residual is None:
+        raise ValueError("return_sum needs a residual")
+    x = x.contiguous()
+    residual = residual.contiguous() if residual is not None else None
+    weight = weight.contiguous() if weight is not None else None
+    bias = bias.contiguous() if bias is not None else None
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad
+                                       for t in (x, residual, weight, bias)):
+        return LayerNormFunction.apply(x, residual, weight, bias, eps, return_sum)
+    out, total, _, _ = msda_layer_norm_forward(x, weight, bias, residual, eps, return_sum, stats=False)
+    return (out, total) if return_sum else out
