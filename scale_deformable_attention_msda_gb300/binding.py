@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 import threading
 
@@ -342,21 +343,26 @@ def multi_scale_deformable_attention(value, spatial_shapes, level_start_index,
 # ------------------------------------------------------- layer norm, residual
 
 def _at(t):
-    return t.data_ptr() if t is not None else None
+    return None if t is None else t.data_ptr()
+
+
+def _current_stream(index):
+    """Handle of device `index`'s current stream (without building a Stream object)."""
+    return torch._C._cuda_getCurrentRawStream(index)
 
 
 @contextlib.contextmanager
 def _on(device, stream):
     """Make `device` current, and `stream` (None: its current stream), so that what is
-    allocated belongs to the stream the kernels run on; yields the stream's handle."""
+    allocated belongs to the stream the kernels run on."""
     if stream is not None and stream.device != device:
         raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
     with torch.cuda.device(device):
         if stream is None:
-            yield torch.cuda.current_stream(device).cuda_stream
+            yield
         else:
             with torch.cuda.stream(stream):
-                yield stream.cuda_stream
+                yield
 
 
 def _check_like(name, t, shape, dtype, device):
@@ -372,26 +378,44 @@ def _check_like(name, t, shape, dtype, device):
         raise ValueError(f"{name} is not contiguous: libmsda needs contiguous tensors")
 
 
-def _norm_operands(x, residual, weight, bias):
-    """Checks of the operands the forward and the backward share; (dims, type of the
-    parameters, type of the statistics)."""
-    if not x.is_cuda:
-        raise ValueError("libmsda runs on CUDA tensors only (no CPU path)")
-    if x.dim() < 1:
-        raise ValueError("x needs a channel dimension")
-    _dtype(x)
-    _check_like("x", x, x.shape, x.dtype, x.device)
-    _check_like("residual", residual, x.shape, x.dtype, x.device)
+def _like(t, shape, dtype, device):
+    """The same question as _check_like's, without the answer's wording."""
+    return t is None or (t.dtype is dtype and t.shape == shape and t.device == device and
+                         t.is_contiguous())
+
+
+@functools.lru_cache(maxsize=256)
+def _norm_dims(numel, C):
+    return ctypes.byref(msda_norm_dims_t(numel // C if C else 0, C))
+
+
+def _param_dtype(x, weight, bias, given=None):
     params = weight if weight is not None else bias
-    pdt = params.dtype if params is not None else x.dtype
-    if pdt != x.dtype and not (pdt == torch.float32 and x.dtype in (torch.bfloat16, torch.float16)):
+    pdt = params.dtype if params is not None else given if given is not None else x.dtype
+    if pdt is not x.dtype and not (pdt is torch.float32 and x.dtype in (torch.bfloat16, torch.float16)):
         raise ValueError(f"parameters of {pdt} with data of {x.dtype}: give the data's type, or "
                          "float32 with 16-bit data")
-    C = x.shape[-1]
+    return pdt
+
+
+def _norm_operands(x, rows, weight, bias, pdt):
+    """Raise unless x is a contiguous CUDA tensor with a channel dimension, `rows` (by name)
+    are like it and weight and bias hold a value of type pdt for each channel."""
+    if not x.is_cuda:
+        raise ValueError("libmsda runs on CUDA tensors only (no CPU path)")
+    shape, dtype, device = x.shape, x.dtype, x.device
+    if not shape:
+        raise ValueError("x needs a channel dimension")
+    if dtype not in _DTYPES:
+        raise ValueError(f"unsupported dtype {dtype}")
+    if not x.is_contiguous():
+        _check_like("x", x, shape, dtype, device)
+    for name, t in rows:
+        if not _like(t, shape, dtype, device):
+            _check_like(name, t, shape, dtype, device)
     for name, t in (("weight", weight), ("bias", bias)):
-        _check_like(name, t, (C,), pdt, x.device)
-    dims = msda_norm_dims_t(x.numel() // C if C else 0, C)
-    return dims, pdt, torch.float64 if x.dtype == torch.float64 else torch.float32
+        if not _like(t, shape[-1:], pdt, device):
+            _check_like(name, t, shape[-1:], pdt, device)
 
 
 def _apart(outs, ins):
@@ -405,25 +429,75 @@ def _apart(outs, ins):
                 raise ValueError("an output overlaps an input or another output")
 
 
+def _stats_dtype(x):
+    return torch.float64 if x.dtype is torch.float64 else torch.float32
+
+
+def _norm_forward(x, weight, bias, residual, eps, return_sum, stats, out, pdt):
+    """The launch, on the current device and stream, of operands already checked. `stats`:
+    None, or True for (mean, rstd) as one tensor of two halves."""
+    if out is None:
+        out = torch.empty_like(x)
+    total = torch.empty_like(x) if return_sum else None
+    mean = rstd = None
+    if stats:
+        stats = torch.empty((2, *x.shape[:-1]), dtype=_stats_dtype(x), device=x.device)
+        mean = stats.data_ptr()
+        rstd = mean + stats.numel() // 2 * stats.element_size()
+    status = lib().msda_layer_norm_forward(
+        x.data_ptr(), _at(residual), _at(weight), _at(bias), out.data_ptr(), _at(total), mean, rstd,
+        eps, _norm_dims(x.numel(), x.shape[-1]), _DTYPES[x.dtype], _DTYPES[pdt],
+        _current_stream(x.get_device()))
+    if status:
+        raise MSDAError(status, "msda_layer_norm_forward")
+    return out, total, stats
+
+
+def _norm_backward(grad_out, x, mean, rstd, weight, residual, grad_sum, pdt, want):
+    """The launch, on the current device and stream, of operands already checked; mean and
+    rstd are addresses."""
+    dims, dt = _norm_dims(x.numel(), x.shape[-1]), _DTYPES[x.dtype]
+    grad_x = torch.empty_like(x) if want[0] else None
+    grad_weight = grad_bias = workspace = None
+    need = 0
+    if want[1] or want[2]:
+        C, device = x.shape[-1], x.device
+        if want[1]:
+            grad_weight = torch.empty(C, dtype=pdt, device=device)
+        if want[2]:
+            grad_bias = torch.empty(C, dtype=pdt, device=device)
+        need = lib().msda_layer_norm_backward_workspace_bytes(dims, dt)
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    status = lib().msda_layer_norm_backward(
+        grad_out.data_ptr(), _at(grad_sum), x.data_ptr(), _at(residual), _at(weight),
+        mean, rstd, _at(grad_x), _at(grad_weight), _at(grad_bias),
+        _at(workspace), need, dims, dt, _DTYPES[pdt], _current_stream(x.get_device()))
+    if status:
+        raise MSDAError(status, "msda_layer_norm_backward")
+    return grad_x, grad_weight, grad_bias
+
+
+def _elsewhere(x, stream):
+    """Whether the launch needs another device or stream than the current ones."""
+    return stream is not None or torch._C._cuda_getDevice() != x.get_device()
+
+
 def msda_layer_norm_forward(x, weight=None, bias=None, residual=None, eps: float = 1e-5,
                             return_sum: bool = False, stats: bool = True, out=None, stream=None):
     """(out, sum, mean, rstd) of the rows of x + residual over x's last dimension; sum is
     None unless return_sum, mean and rstd are None unless stats (the backward needs them).
     See msda_layer_norm_forward in include/msda.h."""
-    dims, pdt, sdt = _norm_operands(x, residual, weight, bias)
+    pdt = _param_dtype(x, weight, bias)
+    _norm_operands(x, (("residual", residual), ("out", out)), weight, bias, pdt)
     if out is not None:
-        _check_like("out", out, x.shape, x.dtype, x.device)
         _apart([out], [x, residual, weight, bias])
-    with _on(x.device, stream) as s:
-        if out is None:
-            out = torch.empty_like(x)
-        total = torch.empty_like(x) if return_sum else None
-        mean = torch.empty(x.shape[:-1], dtype=sdt, device=x.device) if stats else None
-        rstd = torch.empty_like(mean) if stats else None
-        _call("msda_layer_norm_forward", lib().msda_layer_norm_forward(
-            _at(x), _at(residual), _at(weight), _at(bias), _at(out), _at(total), _at(mean),
-            _at(rstd), eps, ctypes.byref(dims), _dtype(x), _DTYPES[pdt], s))
-    return out, total, mean, rstd
+    args = (x, weight, bias, residual, eps, return_sum, stats, out, pdt)
+    if _elsewhere(x, stream):
+        with _on(x.device, stream):
+            out, total, both = _norm_forward(*args)
+    else:
+        out, total, both = _norm_forward(*args)
+    return (out, total, both[0], both[1]) if stats else (out, total, None, None)
 
 
 def msda_layer_norm_backward(grad_out, x, mean, rstd, weight=None, residual=None, grad_sum=None,
@@ -431,26 +505,16 @@ def msda_layer_norm_backward(grad_out, x, mean, rstd, weight=None, residual=None
     """(grad_x, grad_weight, grad_bias), None where `want` says so; grad_x is the gradient of
     x and of residual alike. param_dtype: the parameters' type where weight is None. See
     msda_layer_norm_backward in include/msda.h."""
-    dims, pdt, sdt = _norm_operands(x, residual, weight, None)
-    if weight is None and param_dtype is not None:
-        pdt = param_dtype
-    _check_like("grad_out", grad_out, x.shape, x.dtype, x.device)
-    _check_like("grad_sum", grad_sum, x.shape, x.dtype, x.device)
-    _check_like("mean", mean, x.shape[:-1], sdt, x.device)
-    _check_like("rstd", rstd, x.shape[:-1], sdt, x.device)
-    with _on(x.device, stream) as s:
-        grad_x = torch.empty_like(x) if want[0] else None
-        grad_weight = torch.empty((dims.C,), dtype=pdt, device=x.device) if want[1] else None
-        grad_bias = torch.empty((dims.C,), dtype=pdt, device=x.device) if want[2] else None
-        need, workspace = 0, None
-        if want[1] or want[2]:
-            need = lib().msda_layer_norm_backward_workspace_bytes(ctypes.byref(dims), _dtype(x))
-            workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
-        _call("msda_layer_norm_backward", lib().msda_layer_norm_backward(
-            _at(grad_out), _at(grad_sum), _at(x), _at(residual), _at(weight), _at(mean), _at(rstd),
-            _at(grad_x), _at(grad_weight), _at(grad_bias), _at(workspace), need,
-            ctypes.byref(dims), _dtype(x), _DTYPES.get(pdt, -1), s))
-    return grad_x, grad_weight, grad_bias
+    pdt = _param_dtype(x, weight, None, param_dtype)
+    _norm_operands(x, (("grad_out", grad_out), ("residual", residual), ("grad_sum", grad_sum)),
+                   weight, None, pdt)
+    for name, t in (("mean", mean), ("rstd", rstd)):
+        _check_like(name, t, x.shape[:-1], _stats_dtype(x), x.device)
+    args = (grad_out, x, mean.data_ptr(), rstd.data_ptr(), weight, residual, grad_sum, pdt, want)
+    if _elsewhere(x, stream):
+        with _on(x.device, stream):
+            return _norm_backward(*args)
+    return _norm_backward(*args)
 
 
 class LayerNormFunction(torch.autograd.Function):
@@ -458,25 +522,36 @@ class LayerNormFunction(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, x, residual, weight, bias, eps, return_sum):
-        out, total, mean, rstd = msda_layer_norm_forward(x, weight, bias, residual, eps, return_sum)
-        ctx.save_for_backward(x, residual, weight, mean, rstd)
-        ctx.param_dtype = weight.dtype if weight is not None else bias.dtype if bias is not None else None
+        pdt = ctx.param_dtype = _param_dtype(x, weight, bias)
+        _norm_operands(x, (("residual", residual),), weight, bias, pdt)
+        args = (x, weight, bias, residual, eps, return_sum, True, None, pdt)
+        if _elsewhere(x, None):
+            with _on(x.device, None):
+                out, total, stats = _norm_forward(*args)
+        else:
+            out, total, stats = _norm_forward(*args)
+        ctx.save_for_backward(x, residual, weight, stats)
         ctx.set_materialize_grads(False)
         return (out, total) if return_sum else out
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, grad_out, grad_sum=None):
-        x, residual, weight, mean, rstd = ctx.saved_tensors
-        need_x, need_res, need_w, need_b = ctx.needs_input_grad[:4]
+        need_x, need_res, need_w, need_b, _, _ = ctx.needs_input_grad
         if grad_sum is not None:
             grad_sum = grad_sum.contiguous()
         if grad_out is None:             # the normalised rows were not used
             gx, gw, gb = grad_sum, None, None
         else:
-            gx, gw, gb = msda_layer_norm_backward(
-                grad_out.contiguous(), x, mean, rstd, weight, residual, grad_sum, ctx.param_dtype,
-                (need_x or need_res, need_w, need_b))
+            x, residual, weight, stats = ctx.saved_tensors
+            mean = stats.data_ptr()
+            args = (grad_out.contiguous(), x, mean, mean + stats.numel() // 2 * stats.element_size(),
+                    weight, residual, grad_sum, ctx.param_dtype, (need_x or need_res, need_w, need_b))
+            if _elsewhere(x, None):
+                with _on(x.device, None):
+                    gx, gw, gb = _norm_backward(*args)
+            else:
+                gx, gw, gb = _norm_backward(*args)
         return gx if need_x else None, gx if need_res else None, gw, gb, None, None
 
 
@@ -487,11 +562,17 @@ def layer_norm(x, weight=None, bias=None, residual=None, eps: float = 1e-5, retu
     if return_sum and residual is None:
         raise ValueError("return_sum needs a residual")
     x = x.contiguous()
-    residual = residual.contiguous() if residual is not None else None
-    weight = weight.contiguous() if weight is not None else None
-    bias = bias.contiguous() if bias is not None else None
-    if torch.is_grad_enabled() and any(t is not None and t.requires_grad
-                                       for t in (x, residual, weight, bias)):
+    grad = x.requires_grad
+    if residual is not None:
+        residual = residual.contiguous()
+        grad = grad or residual.requires_grad
+    if weight is not None:
+        weight = weight.contiguous()
+        grad = grad or weight.requires_grad
+    if bias is not None:
+        bias = bias.contiguous()
+        grad = grad or bias.requires_grad
+    if grad and torch.is_grad_enabled():
         return LayerNormFunction.apply(x, residual, weight, bias, eps, return_sum)
     out, total, _, _ = msda_layer_norm_forward(x, weight, bias, residual, eps, return_sum, stats=False)
     return (out, total) if return_sum else out

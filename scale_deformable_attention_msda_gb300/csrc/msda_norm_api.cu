@@ -29,79 +29,69 @@ msda_status_t check(const msda_norm_dims_t *d, msda_dtype_t dt, msda_dtype_t pdt
     return MSDA_OK;
 }
 
-// How rows of C elements are held (see msda_norm.cuh). Up to 32 vectors fill
-// part of a warp or one warp, up to 64 a warp twice over; longer rows take a
-// block of as few threads as hold them in 1, 2 or 4 vectors each. Rows that
-// are not 16-byte aligned go by single elements, 4 or 8 a thread.
-NormPlan row_plan(const msda_norm_dims_t &d, msda_dtype_t dt, bool vec) {
+// How rows of C elements are held (see msda_norm.cuh). `aligned16`: every
+// tensor of rows starts on a 16-byte boundary. Two granules a thread: measured
+// against one, two, three and four on rows of 64 to 8192 channels, they were the
+// fastest or within 3% (one spends more on the row's sums, four leave too few
+// warps); rows past 512 * 2 granules take four.
+NormPlan row_plan(const msda_norm_dims_t &d, msda_dtype_t dt, bool aligned16, int threads) {
     NormPlan p = {};
-    const int per = vec ? 16 / elem_bytes(dt) : 1;
-    const int64_t n = (d.C + per - 1) / per;
-    p.vec = vec;
-    p.threads = 256;
-    auto block = [&](int kv) {
-        p.G = 0;
-        p.KV = kv;
-        p.threads = (int)((n + kv - 1) / kv + 31) / 32 * 32;
-    };
-    auto warp = [&](int g, int kv) { p.G = g; p.KV = kv; };
-    if (dt == MSDA_F64) p.general = true;
-    else if (vec) {
-        if (n <= 4) warp(4, 1);
-        else if (n <= 8) warp(8, 1);
-        else if (n <= 16) warp(16, 1);
-        else if (n <= 32) warp(32, 1);
-        else if (n <= 64) warp(32, 2);
-        else if (n <= 512) block(1);
-        else if (n <= 1024) block(2);
-        else if (n <= 2048) block(4);
-        else p.general = true;
+    const int V = 16 / elem_bytes(dt);
+    p.ragged = d.C % V != 0;
+    // granules of a row, the most that any phase touches
+    const int64_t n = p.ragged ? (d.C + V - 1 + V - 1) / V : d.C / V;
+    p.KV = n <= 1024 ? 2 : 4;
+    if (dt == MSDA_F64 || !aligned16 || n > 2048) {
+        p.general = true;
+        return p;
+    }
+    if (n <= 64) {
+        p.G = n <= 4 ? 2 : n <= 8 ? 4 : n <= 16 ? 8 : n <= 32 ? 16 : 32;
+        p.group = p.G;
+        p.threads = threads;
     } else {
-        if (n <= 32) warp(32, 1);
-        else if (n <= 128) warp(32, 4);
-        else if (n <= 256) warp(32, 8);
-        else if (n <= 2048) block(4);
-        else if (n <= 8192) block(8);
-        else p.general = true;
+        p.group = (int)((n + p.KV - 1) / p.KV + 31) / 32 * 32;
+        p.threads = p.group >= threads ? p.group : threads / p.group * p.group;
     }
     return p;
 }
 
-NormPlan forward_plan(const msda_norm_dims_t &d, msda_dtype_t dt, bool vec) {
-    NormPlan p = row_plan(d, dt, vec);
-    const int64_t per_block = p.general || p.G == 0 ? 1 : p.threads / p.G;
-    const int64_t want = (d.N + per_block - 1) / per_block;
-    if (p.general) p.threads = 512;
-    p.blocks = (int)(want < (1 << 30) ? want : (1 << 30));
+NormPlan forward_plan(const msda_norm_dims_t &d, msda_dtype_t dt, bool aligned16) {
+    NormPlan p = row_plan(d, dt, aligned16, msda::kForwardThreads);
+    if (p.general) {
+        p.threads = 512;
+        p.blocks = (int)(d.N < (1 << 30) ? d.N : (1 << 30));
+        return p;
+    }
+    const int64_t per_block = p.threads / p.group, want = (d.N + per_block - 1) / per_block;
+    const int64_t cap = msda::kSMs * (1024 / p.threads);
+    p.blocks = (int)(want < cap ? want : cap);
     return p;
 }
 
 // The backward's blocks walk many rows each, since each leaves a row of
 // partial column sums (general: the count of row chunks).
-NormPlan backward_plan(const msda_norm_dims_t &d, msda_dtype_t dt, bool vec) {
-    NormPlan p = row_plan(d, dt, vec);
+NormPlan backward_plan(const msda_norm_dims_t &d, msda_dtype_t dt, bool aligned16) {
+    NormPlan p = row_plan(d, dt, aligned16, msda::kBackwardThreads);
     if (p.general) {
         p.threads = 512;
         p.blocks = (int)(d.N < 1 ? 1 : d.N < 256 ? d.N : 256);
         return p;
     }
-    const int64_t per_block = p.G == 0 ? 1 : p.threads / p.G;
-    const int64_t want = (d.N + per_block - 1) / per_block;
-    const int64_t cap = msda::kSMs * (p.G > 0 ? 3 : p.threads <= 128 ? 6 : p.threads <= 256 ? 3 : 2);
+    const int64_t per_block = p.threads / p.group, want = (d.N + per_block - 1) / per_block;
+    const int64_t cap = msda::kSMs * (p.threads > 256 ? 1 : 512 / p.threads);
     p.blocks = (int)(want < 1 ? 1 : want < cap ? want : cap);
     return p;
 }
 
-// The most blocks any plan of these sizes takes: vectors or single elements
-// depend on the pointers' alignment, which the size query does not see.
+// The most blocks any plan of these sizes takes: which one depends on the
+// pointers' alignment, which the size query does not see.
 size_t backward_bytes(const msda_norm_dims_t &d, msda_dtype_t dt) {
     const int a = backward_plan(d, dt, true).blocks, b = backward_plan(d, dt, false).blocks;
     return (size_t)(a > b ? a : b) * 2 * (size_t)d.C * (dt == MSDA_F64 ? 8 : 4);
 }
 
-// Whether every row of every tensor given starts on a 16-byte boundary.
-bool vectors(const msda_norm_dims_t &d, msda_dtype_t dt, const void *const *p, int count) {
-    if (d.C % (16 / elem_bytes(dt)) != 0) return false;
+bool aligned16(const void *const *p, int count) {
     for (int i = 0; i < count; ++i)
         if (!aligned(p[i], 16)) return false;
     return true;
@@ -128,7 +118,7 @@ msda_status_t msda_layer_norm_forward(const void *x, const void *residual, const
         !aligned(weight, pe) || !aligned(bias, pe) || !aligned(mean, se) || !aligned(rstd, se))
         return MSDA_ERR_ALIGN;
     const void *const all[] = {x, residual, out, sum, weight, bias};
-    const NormPlan p = forward_plan(d, dtype, vectors(d, dtype, all, 6));
+    const NormPlan p = forward_plan(d, dtype, aligned16(all, 6));
     NormArgs a = {};
     if (msda::fault_word_for_launch(&a.err) != cudaSuccess) return MSDA_ERR_CUDA;
     a.x = x;
@@ -142,6 +132,7 @@ msda_status_t msda_layer_norm_forward(const void *x, const void *residual, const
     a.eps = eps;
     a.N = d.N;
     a.C = (int)d.C;
+    a.group = p.group;
     return from_cuda(msda::launch_norm_forward(a, p, dtype, param_dtype,
                                                static_cast<cudaStream_t>(stream)));
 }
@@ -173,7 +164,7 @@ msda_status_t msda_layer_norm_backward(const void *grad_out, const void *grad_su
     if (columns && !aligned(workspace, 16)) return MSDA_ERR_ALIGN;
     if (d.N == 0 && !columns) return MSDA_OK;   // N = 0 with columns: they are written as zeros
     const void *const all[] = {grad_out, grad_sum, x, residual, weight, grad_x};
-    const NormPlan p = backward_plan(d, dtype, vectors(d, dtype, all, 6));
+    const NormPlan p = backward_plan(d, dtype, aligned16(all, 6));
     NormArgs a = {};
     if (msda::fault_word_for_launch(&a.err) != cudaSuccess) return MSDA_ERR_CUDA;
     a.x = x;
@@ -189,6 +180,7 @@ msda_status_t msda_layer_norm_backward(const void *grad_out, const void *grad_su
     a.partial = columns ? static_cast<float *>(workspace) : nullptr;
     a.N = d.N;
     a.C = (int)d.C;
+    a.group = p.group;
     return from_cuda(msda::launch_norm_backward(a, p, dtype, param_dtype,
                                                 static_cast<cudaStream_t>(stream)));
 }

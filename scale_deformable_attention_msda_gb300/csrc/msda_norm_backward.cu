@@ -12,183 +12,202 @@
 
 namespace msda {
 
-template <typename T, typename W, int G, int KV, int VEC>
-__global__ void __launch_bounds__(G > 0 ? 256 : (VEC == 1 ? 1024 : 512))
-norm_backward_kernel(const NormArgs a) {
+// S: rows whose copies are under way while one is worked on. A thread copies
+// what it reads itself, so its own wait is all the order the copies need.
+template <typename T, typename W, int G, int KV, bool RAGGED, int S, int TH>
+__global__ void __launch_bounds__(TH) norm_backward_kernel(const NormArgs a) {
+    constexpr int V = Vec16<T>::N, P = V / 2;
     __shared__ BlockScratch<2> scratch;
-    extern __shared__ float columns[];   // G > 0: (groups of the block, 2, C)
+    extern __shared__ uint4 ring[];      // (S, tensors, KV, threads); at the end (warps, 2, C) floats
     int turn = 0;
-    const int threads = G == 0 ? blockDim.x : G;
-    const int t = G == 0 ? threadIdx.x : threadIdx.x % G;
-    const int64_t first = G == 0 ? blockIdx.x : (int64_t)blockIdx.x * (blockDim.x / G) + threadIdx.x / G;
-    const int64_t step = G == 0 ? gridDim.x : (int64_t)gridDim.x * (blockDim.x / G);
+    cudaTriggerProgrammaticLaunchCompletion();   // the column kernel may be launched; it waits for this one's end
+    const int C = a.C;
+    const RowMap<G, KV, V, RAGGED, TH> map(a);
     const T *x = static_cast<const T *>(a.x), *res = static_cast<const T *>(a.residual);
     const T *dy = static_cast<const T *>(a.grad_out), *ds = static_cast<const T *>(a.grad_sum);
     const W *w = static_cast<const W *>(a.weight);
     T *dx = static_cast<T *>(a.grad_x);
     const float *mean = static_cast<const float *>(a.mean), *rstd = static_cast<const float *>(a.rstd);
-    const int C = a.C;
-    const int64_t extent = a.N * C;
+    const int64_t extent = a.N * C, hop = map.step * C;
     const float inv_C = 1.0f / (float)C;
-    float dw[KV][VEC], db[KV][VEC];
-    bool held[KV];                       // the thread has channels of this vector
+    const int plane = G == 0 ? blockDim.x : TH;   // a thread's slots are this far apart
+    const int tensors = 2 + (res ? 1 : 0) + (ds ? 1 : 0), tall = tensors * KV * plane;
+    const int ds_at = (tensors - 1) * KV;
+    int64_t here = map.start(C), ahead = here;
+    int64_t coming = map.first;          // the row at `ahead`
+    auto fetch = [&](uint4 *to) {
+        const bool there = coming < a.N;
+#pragma unroll
+        for (int k = 0; k < KV; ++k) {
+            map.fetch(to + k * plane, x, ahead, k, there, extent, a.err);
+            map.fetch(to + (KV + k) * plane, dy, ahead, k, there, extent, a.err);
+            if (res) map.fetch(to + (2 * KV + k) * plane, res, ahead, k, there, extent, a.err);
+            if (ds) map.fetch(to + (ds_at + k) * plane, ds, ahead, k, there, extent, a.err);
+        }
+        coming += map.step;
+        ahead += hop;
+        fetch_commit();
+    };
+    uint4 *const begin = ring + threadIdx.x, *slot = begin;
+#pragma unroll
+    for (int i = 0; i < S; ++i) fetch(begin + i * tall);
+    float2 pw[KV][P], dw[KV][P], db[KV][P];
 #pragma unroll
     for (int k = 0; k < KV; ++k) {
-        held[k] = (k * threads + t) * VEC < C;
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) dw[k][i] = db[k][i] = 0.0f;
+        for (int i = 0; i < P; ++i) dw[k][i] = db[k][i] = both(0.0f);
+        if (RAGGED) load_params_masked<W, V>(pw[k], w, map.channel(k), C, 1.0f);
+        else load_params<W, V>(pw[k], map.held(k) ? w : nullptr, map.channel(k), 1.0f);
     }
-    const int64_t warp_first = G == 0 ? first : (int64_t)blockIdx.x * (blockDim.x / G) + (threadIdx.x & ~31) / (G == 0 ? 1 : G);
-
-    Raw<T, VEC> rx[KV], rr[KV], rd[KV], re[KV];
     float mu = 0.0f, rs = 0.0f;
-    auto fetch = [&](int64_t row) {
-        const bool valid = row < a.N && span_ok(a.err, row * C, C, extent);
-        const int64_t base = row * C;
-        mu = valid ? __ldg(mean + row) : 0.0f;
-        rs = valid ? __ldg(rstd + row) : 0.0f;
-#pragma unroll
-        for (int k = 0; k < KV; ++k) {
-            const int c = (k * threads + t) * VEC;
-            const bool mine = valid && held[k];
-            rx[k].zero(); rr[k].zero(); rd[k].zero(); re[k].zero();
-            if (mine) {
-                rx[k].load(x + base + c);
-                rd[k].load(dy + base + c);
-                if (res) rr[k].load(res + base + c);
-                if (ds) re[k].load(ds + base + c);
-            }
-        }
-    };
-    fetch(first);
-    for (int64_t row = first, lead = warp_first; lead < a.N; row += step, lead += step) {
-        const bool valid = row < a.N;
-        const int64_t base = row * C;
+    if (map.first < a.N) {
+        mu = __ldg(mean + map.first);
+        rs = __ldg(rstd + map.first);
+    }
+    for (int64_t row = map.first, lead = map.lead; lead < a.N; row += map.step, lead += map.step, here += hop) {
+        // a row past the last, and a granule the thread does not have, were
+        // filled with zeros: grad_out = 0 there, and nothing is added
+        const bool valid = G == 0 || G == 32 || row < a.N;
         const float m = mu, r = rs;
-        float xh[KV][VEC], g[KV][VEC], e[KV][VEC];
-        float v[2] = {0.0f, 0.0f};
+        if (row + map.step < a.N) {
+            mu = __ldg(mean + row + map.step);
+            rs = __ldg(rstd + row + map.step);
+        }
+        float2 xh[KV][P], g[KV][P];
+        float2 v0 = both(0.0f), v1 = both(0.0f);
+        fetch_wait<S - 1>();
 #pragma unroll
         for (int k = 0; k < KV; ++k) {
-            const int c = (k * threads + t) * VEC;
-            rx[k].unpack(xh[k]);
-            rd[k].unpack(g[k]);
+            unpack_pairs<T>(xh[k], slot[k * plane]);
+            unpack_pairs<T>(g[k], slot[(KV + k) * plane]);
             if (res) {
-                rr[k].unpack(e[k]);
+                float2 e[P];
+                unpack_pairs<T>(e, slot[(2 * KV + k) * plane]);
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) xh[k][i] += e[k][i];
+                for (int i = 0; i < P; ++i) xh[k][i] = add2(xh[k][i], e[i]);
             }
-            if (ds) re[k].unpack(e[k]);
+            if (RAGGED && !map.whole(k, C)) {      // a neighbour's elements: s = mean, grad_out = 0
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                // a row past the end has m = r = 0 and grad_out 0: it adds nothing
-                xh[k][i] = held[k] ? (xh[k][i] - m) * r : 0.0f;
-                dw[k][i] = fmaf(g[k][i], xh[k][i], dw[k][i]);
-                db[k][i] += g[k][i];
-            }
-            if (w && held[k]) {
-                Raw<W, VEC> rw;
-                float f[VEC];
-                rw.load(w + c);
-                rw.unpack(f);
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) g[k][i] *= f[i];
+                for (int i = 0; i < P; ++i) {
+                    if (!map.has(k, 2 * i, C)) { xh[k][i].x = m; g[k][i].x = 0.0f; }
+                    if (!map.has(k, 2 * i + 1, C)) { xh[k][i].y = m; g[k][i].y = 0.0f; }
+                }
             }
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                v[0] += g[k][i];
-                v[1] = fmaf(g[k][i], xh[k][i], v[1]);
+            for (int i = 0; i < P; ++i) {
+                xh[k][i] = mul2(add2(xh[k][i], both(-m)), both(r));
+                dw[k][i] = fma2(g[k][i], xh[k][i], dw[k][i]);
+                db[k][i] = add2(db[k][i], g[k][i]);
+                g[k][i] = mul2(g[k][i], pw[k][i]);
+                v0 = add2(v0, g[k][i]);
+                v1 = fma2(g[k][i], xh[k][i], v1);
             }
         }
-        fetch(row + step);               // the next row's loads run under this row's sums
-        row_sum<G>(v, &scratch, turn);
-        const float c1 = v[0] * inv_C, c2 = v[1] * inv_C;
+        float v[2] = {v0.x + v0.y, v1.x + v1.y};
+        row_sum<G>(v, &scratch, turn, map.threads, map.index);
         if (dx) {
+            const float2 c1 = both(-v[0] * inv_C), c2 = both(-v[1] * inv_C);
 #pragma unroll
             for (int k = 0; k < KV; ++k) {
-                const int c = (k * threads + t) * VEC;
-                if (!valid || !held[k] || !span_ok(a.err, base + c, VEC, extent)) continue;
-                float o[VEC];
+                float2 e[P];
+                if (ds) unpack_pairs<T>(e, slot[(ds_at + k) * plane]);
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) {
-                    o[i] = r * (g[k][i] - c1 - xh[k][i] * c2);
-                    if (ds) o[i] += e[k][i];
+                for (int i = 0; i < P; ++i) {
+                    g[k][i] = mul2(fma2(xh[k][i], c2, add2(g[k][i], c1)), both(r));
+                    if (ds) g[k][i] = add2(g[k][i], e[i]);
                 }
-                Raw<T, VEC>::store(dx + base + c, o);
+                if (valid && map.held(k)) map.store(dx, here, k, C, g[k]);
             }
         }
+        fetch(slot);
+        slot = slot + tall == begin + S * tall ? begin : slot + tall;
     }
+    fetch_wait<0>();
     if (!a.partial) return;
-    float *mine = a.partial + (int64_t)blockIdx.x * 2 * C;
-    if (G == 0) {
+    // the block's sums: each group leaves its own in shared memory, or, where
+    // all rows have the same phase, each warp after adding its groups' sums
+    constexpr bool FOLD = !RAGGED && G > 0 && G < 32;
+    if constexpr (FOLD) {
 #pragma unroll
         for (int k = 0; k < KV; ++k) {
-            const int c = (k * threads + t) * VEC;
-            if (!held[k]) continue;
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                mine[c + i] = dw[k][i];
-                mine[C + c + i] = db[k][i];
-            }
-        }
-        return;
-    }
-    // the block's groups: lanes of one warp with shuffles, warps through shared memory
+            for (int i = 0; i < P; ++i) {
 #pragma unroll
-    for (int k = 0; k < KV; ++k) {
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-#pragma unroll
-            for (int off = G == 0 ? 32 : G; off < 32; off <<= 1) {
-                dw[k][i] += __shfl_xor_sync(0xffffffffu, dw[k][i], off);
-                db[k][i] += __shfl_xor_sync(0xffffffffu, db[k][i], off);
+                for (int off = G; off < 32; off <<= 1) {
+                    dw[k][i].x += __shfl_xor_sync(0xffffffffu, dw[k][i].x, off);
+                    dw[k][i].y += __shfl_xor_sync(0xffffffffu, dw[k][i].y, off);
+                    db[k][i].x += __shfl_xor_sync(0xffffffffu, db[k][i].x, off);
+                    db[k][i].y += __shfl_xor_sync(0xffffffffu, db[k][i].y, off);
+                }
             }
         }
     }
-    const int warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    if ((threadIdx.x & 31) < (G == 0 ? 32 : G)) {
-        float *to = columns + (int64_t)warp * 2 * C;
+    __syncthreads();                     // the ring's space is used again
+    float *columns = reinterpret_cast<float *>(ring);
+    const int writer = FOLD ? threadIdx.x >> 5 : map.index;
+    const int writers = FOLD ? blockDim.x >> 5 : blockDim.x / map.threads;
+    if (!FOLD || (threadIdx.x & 31) < G) {
+        float *to = columns + writer * 2 * C;
 #pragma unroll
         for (int k = 0; k < KV; ++k) {
-            const int c = (k * threads + t) * VEC;
-            if (!held[k]) continue;
+            if (!map.held(k)) continue;
+            const int c = map.channel(k);
+            if constexpr (!RAGGED) {
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                to[c + i] = dw[k][i];
-                to[C + c + i] = db[k][i];
+                for (int i = 0; i < P / 2; ++i) {
+                    reinterpret_cast<float4 *>(to + c)[i] =
+                        make_float4(dw[k][2 * i].x, dw[k][2 * i].y, dw[k][2 * i + 1].x, dw[k][2 * i + 1].y);
+                    reinterpret_cast<float4 *>(to + C + c)[i] =
+                        make_float4(db[k][2 * i].x, db[k][2 * i].y, db[k][2 * i + 1].x, db[k][2 * i + 1].y);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    if (!map.has(k, i, C)) continue;
+                    to[c + i] = i & 1 ? dw[k][i / 2].y : dw[k][i / 2].x;
+                    to[C + c + i] = i & 1 ? db[k][i / 2].y : db[k][i / 2].x;
+                }
             }
         }
     }
     __syncthreads();
+    float *mine = a.partial + (int64_t)blockIdx.x * 2 * C;
     for (int j = threadIdx.x; j < 2 * C; j += blockDim.x) {
         float v = 0.0f;
-        for (int i = 0; i < warps; ++i) v += columns[i * 2 * C + j];
+        for (int i = 0; i < writers; ++i) v += columns[i * 2 * C + j];
         mine[j] = v;
     }
 }
 
-// grad_weight and grad_bias from the blocks' partial sums: a block adds 32 of
-// the 2*C columns, its warps every 32nd row of partials each, in a fixed order.
-template <typename W, typename A>
+// grad_weight and grad_bias from the blocks' partial sums, added in a fixed
+// order: a block takes TW of the 2*C columns, its threads every
+// (threads / TW)th row of partials each. TW = 8 (one 32-byte sector) spreads
+// few channels over more SMs; the rows' reads are what it waits for.
+template <typename W, typename A, int TW>
 __global__ void __launch_bounds__(1024) norm_columns_kernel(const A *partial, int rows, int C,
                                                             W *grad_weight, W *grad_bias) {
-    __shared__ A part[32][33];
+    __shared__ A part[32][TW];
     cudaGridDependencySynchronize();
-    const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    const int64_t j = (int64_t)blockIdx.x * 32 + tx, n = 2 * (int64_t)C;
+    const int tx = threadIdx.x % TW, ty = threadIdx.x / TW, step = blockDim.x / TW;
+    const int64_t j = (int64_t)blockIdx.x * TW + tx;
+    const bool mine = j < 2 * (int64_t)C;
+    const int64_t c = j < C ? j : j - C;
     A v = 0;
-    if (j < n) {
-#pragma unroll 4
-        for (int r = ty; r < rows; r += warps) v += partial[(int64_t)r * n + j];
+    if (mine) {
+#pragma unroll 8
+        for (int r = ty; r < rows; r += step) v += partial[r * 2 * (int64_t)C + j];
     }
-    part[ty][tx] = v;
+#pragma unroll
+    for (int off = TW; off < 32; off <<= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    if ((threadIdx.x & 31) < TW) part[threadIdx.x >> 5][tx] = v;
     __syncthreads();
-    if (ty != 0 || j >= n) return;
+    if (threadIdx.x >= TW || !mine) return;
     v = 0;
-    for (int i = 0; i < warps; ++i) v += part[i][tx];
+    for (int i = 0; i < (int)(blockDim.x >> 5); ++i) v += part[i][tx];
     W *to = j < C ? grad_weight : grad_bias;
     if (!to) return;
-    if constexpr (sizeof(W) == 8) to[j < C ? j : j - C] = v;
-    else to[j < C ? j : j - C] = Elem<W>::from_f((float)v);
+    if constexpr (sizeof(W) == 8) to[c] = v;
+    else to[c] = Elem<W>::from_f((float)v);
 }
 
 // ---------------------------------------------------------------- general
@@ -272,17 +291,19 @@ __global__ void __launch_bounds__(128) norm_backward_columns_general_kernel(cons
 
 template <typename W, typename A>
 static cudaError_t launch_columns(const NormArgs &a, int rows, cudaStream_t stream) {
+    const bool narrow = a.C < 2048;
+    const int tw = narrow ? 8 : 32;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((2 * (int64_t)a.C + 31) / 32));
-    cfg.blockDim = dim3(rows >= 64 ? 1024 : 256);
+    cfg.gridDim = dim3((unsigned)((2 * (int64_t)a.C + tw - 1) / tw));
+    cfg.blockDim = dim3(rows >= 8 * 1024 / tw ? 1024 : rows >= 2 * 1024 / tw ? 512 : 256);
     cfg.stream = stream;
-    // launched while the rows' kernel drains; the kernel waits for its results
+    // launched while the rows' kernel runs; the kernel waits for its results
     cudaLaunchAttribute early;
     early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     early.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &early;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, norm_columns_kernel<W, A>,
+    return cudaLaunchKernelEx(&cfg, narrow ? norm_columns_kernel<W, A, 8> : norm_columns_kernel<W, A, 32>,
                               reinterpret_cast<const A *>(a.partial), rows, a.C,
                               static_cast<W *>(a.grad_weight), static_cast<W *>(a.grad_bias));
 }
@@ -303,27 +324,38 @@ static cudaError_t launch_general(const NormArgs &a, const NormPlan &p, cudaStre
     return e != cudaSuccess ? e : launch_columns<W, A>(a, p.blocks, stream);
 }
 
-template <typename T, typename W, int G, int KV, int VEC>
+template <typename T, typename W, int G, int KV, bool RAGGED, int S, int TH>
 static cudaError_t launch_rows(const NormArgs &a, const NormPlan &p, cudaStream_t stream) {
-    const size_t smem = G == 0 || !a.partial ? 0 : (size_t)(p.threads / 32) * 2 * a.C * sizeof(float);
-    static_assert(G == 0 || KV * VEC * G * 2 * 8 * 4 <= 48 * 1024, "columns fit the default shared memory");
-    norm_backward_kernel<T, W, G, KV, VEC><<<p.blocks, p.threads, smem, stream>>>(a);
+    auto kernel = norm_backward_kernel<T, W, G, KV, RAGGED, S, TH>;
+    const int tensors = 2 + (a.residual ? 1 : 0) + (a.grad_sum ? 1 : 0);
+    size_t smem = (size_t)S * tensors * KV * p.threads * 16;
+    if (a.partial) {
+        const int writers = G > 0 && !RAGGED ? p.threads / 32 : p.threads / p.group;
+        const size_t columns = (size_t)writers * 2 * a.C * sizeof(float);
+        smem = smem > columns ? smem : columns;
+    }
+    if (smem > kDefaultShared) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+    }
+    kernel<<<p.blocks, p.threads, smem, stream>>>(a);
     const cudaError_t e = cudaGetLastError();
     return e != cudaSuccess || !a.partial ? e : launch_columns<W, float>(a, p.blocks, stream);
 }
 
 template <typename T, typename W>
 static cudaError_t launch_backward_t(const NormArgs &a, const NormPlan &p, cudaStream_t stream) {
-#define BWD(g, kv, vec) \
-    if (p.G == g && p.KV == kv) return launch_rows<T, W, g, kv, vec>(a, p, stream);
+#define BWD(g, kv, r, s) \
+    if (p.G == g && p.KV == kv && p.ragged == r) return launch_rows<T, W, g, kv, r, s, g == 0 ? 512 : kBackwardThreads>(a, p, stream);
     if (p.general) return launch_general<T, W>(a, p, stream);
-    if (p.vec) {
-        constexpr int V = Vec16<T>::N;
-        BWD(4, 1, V) BWD(8, 1, V) BWD(16, 1, V) BWD(32, 1, V) BWD(32, 2, V)
-        BWD(0, 1, V) BWD(0, 2, V) BWD(0, 4, V)
-    } else {
-        BWD(32, 1, 1) BWD(32, 4, 1) BWD(32, 8, 1) BWD(0, 4, 1) BWD(0, 8, 1)
-    }
+#ifdef NORM_TUNE
+    NORM_TUNE
+#else
+    BWD(2, 2, false, 2) BWD(4, 2, false, 2) BWD(8, 2, false, 2) BWD(16, 2, false, 2) BWD(32, 2, false, 2)
+    BWD(0, 2, false, 2) BWD(0, 4, false, 1)
+    BWD(2, 2, true, 2) BWD(4, 2, true, 2) BWD(8, 2, true, 2) BWD(16, 2, true, 2) BWD(32, 2, true, 2)
+    BWD(0, 2, true, 2) BWD(0, 4, true, 1)
+#endif
 #undef BWD
     return cudaErrorInvalidValue;
 }

@@ -8,103 +8,111 @@
 
 namespace msda {
 
-template <typename T, typename W, int G, int KV, int VEC>
-__global__ void __launch_bounds__(G > 0 ? 256 : (VEC == 1 ? 1024 : 512))
-norm_forward_kernel(const NormArgs a) {
+// S: rows whose copies are under way while one is worked on. A thread copies
+// what it reads itself, so its own wait is all the order the copies need.
+template <typename T, typename W, int G, int KV, bool RAGGED, int S, int TH>
+__global__ void __launch_bounds__(TH) norm_forward_kernel(const NormArgs a) {
+    constexpr int V = Vec16<T>::N, P = V / 2;
     __shared__ BlockScratch<1> scratch;
+    extern __shared__ uint4 ring[];      // (S, tensors, KV, threads)
     int turn = 0;
-    const int threads = G == 0 ? blockDim.x : G;
-    const int t = G == 0 ? threadIdx.x : threadIdx.x % G;
-    const int64_t first = G == 0 ? blockIdx.x : (int64_t)blockIdx.x * (blockDim.x / G) + threadIdx.x / G;
-    const int64_t step = G == 0 ? gridDim.x : (int64_t)gridDim.x * (blockDim.x / G);
+    const int C = a.C;
+    const RowMap<G, KV, V, RAGGED, TH> map(a);
     const T *x = static_cast<const T *>(a.x), *res = static_cast<const T *>(a.residual);
     const W *w = static_cast<const W *>(a.weight), *b = static_cast<const W *>(a.bias);
-    const int C = a.C;
-    const int64_t extent = a.N * C;
+    const int64_t extent = a.N * C, hop = map.step * C;
     const float inv_C = 1.0f / (float)C;
-    // rows are walked by whole warps: a lane of a group past the last row works on zeros
-    const int64_t warp_first = G == 0 ? first : (int64_t)blockIdx.x * (blockDim.x / G) + (threadIdx.x & ~31) / (G == 0 ? 1 : G);
-    for (int64_t row = first, lead = warp_first; lead < a.N; row += step, lead += step) {
-        const bool valid = row < a.N;
-        const int64_t base = row * C;
-        float s[KV][VEC];
-        bool mine[KV];
-        float sum[1] = {0.0f};
+    const int plane = G == 0 ? blockDim.x : TH;   // a thread's slots are this far apart
+    const int tensors = res ? 2 : 1, tall = tensors * KV * plane;
+    int64_t here = map.start(C), ahead = here;
+    int64_t coming = map.first;          // the row at `ahead`
+    auto fetch = [&](uint4 *to) {
+        const bool there = coming < a.N;
 #pragma unroll
         for (int k = 0; k < KV; ++k) {
-            const int c = (k * threads + t) * VEC;
-            mine[k] = valid && c < C && span_ok(a.err, base + c, VEC, extent);
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) s[k][i] = 0.0f;
-            if (mine[k]) {
-                Raw<T, VEC> r;
-                r.load(x + base + c);
-                r.unpack(s[k]);
-            }
+            map.fetch(to + k * plane, x, ahead, k, there, extent, a.err);
+            if (res) map.fetch(to + (KV + k) * plane, res, ahead, k, there, extent, a.err);
         }
-        if (res) {
+        coming += map.step;
+        ahead += hop;
+        fetch_commit();
+    };
+    uint4 *const begin = ring + threadIdx.x, *slot = begin;
 #pragma unroll
-            for (int k = 0; k < KV; ++k) {
-                const int c = (k * threads + t) * VEC;
-                if (mine[k]) {
-                    Raw<T, VEC> r;
-                    float e[VEC];
-                    r.load(res + base + c);
-                    r.unpack(e);
+    for (int i = 0; i < S; ++i) fetch(begin + i * tall);
+    float2 pw[KV][P], pb[KV][P];
 #pragma unroll
-                    for (int i = 0; i < VEC; ++i) s[k][i] += e[i];
+    for (int k = 0; k < KV; ++k) {
+        const int c = map.channel(k);
+        if (RAGGED) {
+            load_params_masked<W, V>(pw[k], w, c, C, 1.0f);
+            load_params_masked<W, V>(pb[k], b, c, C, 0.0f);
+        } else {
+            load_params<W, V>(pw[k], map.held(k) ? w : nullptr, c, 1.0f);
+            load_params<W, V>(pb[k], map.held(k) ? b : nullptr, c, 0.0f);
+        }
+    }
+    for (int64_t row = map.first, lead = map.lead; lead < a.N; row += map.step, lead += map.step, here += hop) {
+        const bool valid = G == 0 || G == 32 || row < a.N;
+        float2 s[KV][P];
+        float2 acc = both(0.0f);
+        fetch_wait<S - 1>();
+#pragma unroll
+        for (int k = 0; k < KV; ++k) {
+            unpack_pairs<T>(s[k], slot[k * plane]);
+            if (res) {
+                float2 e[P];
+                unpack_pairs<T>(e, slot[(KV + k) * plane]);
+#pragma unroll
+                for (int i = 0; i < P; ++i) s[k][i] = add2(s[k][i], e[i]);
+            }
+            if (a.sum && valid && map.held(k)) map.store(static_cast<T *>(a.sum), here, k, C, s[k]);
+            if (RAGGED && !map.whole(k, C)) {
+#pragma unroll
+                for (int i = 0; i < P; ++i) {
+                    if (!map.has(k, 2 * i, C)) s[k][i].x = 0.0f;
+                    if (!map.has(k, 2 * i + 1, C)) s[k][i].y = 0.0f;
                 }
             }
+#pragma unroll
+            for (int i = 0; i < P; ++i) acc = add2(acc, s[k][i]);
         }
+        float v[1] = {acc.x + acc.y};
+        row_sum<G>(v, &scratch, turn, map.threads, map.index);
+        fetch(slot);
+        slot = slot + tall == begin + S * tall ? begin : slot + tall;
+        const float mean = v[0] * inv_C;
+        acc = both(0.0f);
 #pragma unroll
         for (int k = 0; k < KV; ++k) {
+            const float m = map.held(k) ? -mean : 0.0f;      // a slot without a granule stays zero
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) sum[0] += s[k][i];
-        }
-        row_sum<G>(sum, &scratch, turn);
-        const float mean = sum[0] * inv_C;
-        float sq[1] = {0.0f};
+            for (int i = 0; i < P; ++i) s[k][i] = add2(s[k][i], both(m));
+            if (RAGGED && !map.whole(k, C)) {
 #pragma unroll
-        for (int k = 0; k < KV; ++k) {
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                const float d = mine[k] ? s[k][i] - mean : 0.0f;
-                sq[0] = fmaf(d, d, sq[0]);
+                for (int i = 0; i < P; ++i) {
+                    if (!map.has(k, 2 * i, C)) s[k][i].x = 0.0f;
+                    if (!map.has(k, 2 * i + 1, C)) s[k][i].y = 0.0f;
+                }
             }
+#pragma unroll
+            for (int i = 0; i < P; ++i) acc = fma2(s[k][i], s[k][i], acc);
         }
-        row_sum<G>(sq, &scratch, turn);
-        const float rstd = 1.0f / sqrtf(sq[0] * inv_C + (float)a.eps);
-        if (t == 0 && valid && a.mean && span_ok(a.err, row, 1, a.N)) {
+        v[0] = acc.x + acc.y;
+        row_sum<G>(v, &scratch, turn, map.threads, map.index);
+        const float rstd = rsqrtf(fmaf(v[0], inv_C, (float)a.eps));     // within 2 ulp
+        if (map.t == 0 && valid && a.mean && span_ok(a.err, row, 1, a.N)) {
             static_cast<float *>(a.mean)[row] = mean;
             static_cast<float *>(a.rstd)[row] = rstd;
         }
 #pragma unroll
         for (int k = 0; k < KV; ++k) {
-            const int c = (k * threads + t) * VEC;
-            if (!mine[k]) continue;
-            if (a.sum) Raw<T, VEC>::store(static_cast<T *>(a.sum) + base + c, s[k]);
-            float g[VEC];
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) g[i] = (s[k][i] - mean) * rstd;
-            if (w) {
-                Raw<W, VEC> r;
-                float e[VEC];
-                r.load(w + c);
-                r.unpack(e);
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) g[i] *= e[i];
-            }
-            if (b) {
-                Raw<W, VEC> r;
-                float e[VEC];
-                r.load(b + c);
-                r.unpack(e);
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) g[i] += e[i];
-            }
-            Raw<T, VEC>::store(static_cast<T *>(a.out) + base + c, g);
+            for (int i = 0; i < P; ++i) s[k][i] = fma2(mul2(s[k][i], both(rstd)), pw[k][i], pb[k][i]);
+            if (valid && map.held(k)) map.store(static_cast<T *>(a.out), here, k, C, s[k]);
         }
     }
+    fetch_wait<0>();
 }
 
 // Accumulation type of the general kernels: fp32 for 16- and 32-bit data.
@@ -126,8 +134,9 @@ template <typename A> __device__ __forceinline__ A block_sum(A v, A *scratch) {
     return v;
 }
 
-// Rows of any length, one block each, read three times (the later reads hit
-// the caches): fp64, and rows too long for the registers.
+// Rows of any length and alignment, one block each, read three times (the
+// later reads hit the caches): fp64, rows too long for the registers, pointers
+// off a 16-byte boundary.
 template <typename T, typename W>
 __global__ void __launch_bounds__(512) norm_forward_general_kernel(const NormArgs a) {
     using A = typename Acc<T>::type;
@@ -162,24 +171,34 @@ __global__ void __launch_bounds__(512) norm_forward_general_kernel(const NormArg
     }
 }
 
+template <typename T, typename W, int G, int KV, bool RAGGED, int S, int TH>
+static cudaError_t launch_rows(const NormArgs &a, const NormPlan &p, cudaStream_t stream) {
+    auto kernel = norm_forward_kernel<T, W, G, KV, RAGGED, S, TH>;
+    const size_t smem = (size_t)S * (a.residual ? 2 : 1) * KV * p.threads * 16;
+    if (smem > kDefaultShared) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+    }
+    kernel<<<p.blocks, p.threads, smem, stream>>>(a);
+    return cudaGetLastError();
+}
+
 template <typename T, typename W>
 static cudaError_t launch_forward_t(const NormArgs &a, const NormPlan &p, cudaStream_t stream) {
-#define FWD(g, kv, vec)                                                                            \
-    if (p.G == g && p.KV == kv) {                                                                  \
-        norm_forward_kernel<T, W, g, kv, vec><<<p.blocks, p.threads, 0, stream>>>(a);              \
-        return cudaGetLastError();                                                                 \
-    }
+#define FWD(g, kv, r, s) \
+    if (p.G == g && p.KV == kv && p.ragged == r) return launch_rows<T, W, g, kv, r, s, g == 0 ? 512 : kForwardThreads>(a, p, stream);
     if (p.general) {
         norm_forward_general_kernel<T, W><<<p.blocks, p.threads, 0, stream>>>(a);
         return cudaGetLastError();
     }
-    if (p.vec) {
-        constexpr int V = Vec16<T>::N;
-        FWD(4, 1, V) FWD(8, 1, V) FWD(16, 1, V) FWD(32, 1, V) FWD(32, 2, V)
-        FWD(0, 1, V) FWD(0, 2, V) FWD(0, 4, V)
-    } else {
-        FWD(32, 1, 1) FWD(32, 4, 1) FWD(32, 8, 1) FWD(0, 4, 1) FWD(0, 8, 1)
-    }
+#ifdef NORM_TUNE
+    NORM_TUNE
+#else
+    FWD(2, 2, false, 2) FWD(4, 2, false, 2) FWD(8, 2, false, 2) FWD(16, 2, false, 2) FWD(32, 2, false, 2)
+    FWD(0, 2, false, 2) FWD(0, 4, false, 1)
+    FWD(2, 2, true, 2) FWD(4, 2, true, 2) FWD(8, 2, true, 2) FWD(16, 2, true, 2) FWD(32, 2, true, 2)
+    FWD(0, 2, true, 2) FWD(0, 4, true, 1)
+#endif
 #undef FWD
     return cudaErrorInvalidValue;
 }
