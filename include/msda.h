@@ -424,6 +424,54 @@ MSDA_API msda_status_t msda_layer_norm_backward(
     void *grad_bias, void *workspace, size_t workspace_bytes, const msda_norm_dims_t *dims,
     msda_dtype_t dtype, msda_dtype_t param_dtype, void *stream);
 
+/* The global norm of a list of gradients, and clipping by it.
+ * The list is in HOST memory; grads[i] and outs[i] are DEVICE pointers to
+ * sizes[i] contiguous entries of type dtypes[i] and out_dtypes[i] (values of
+ * msda_dtype_t, given as int32). 0 <= count <= 2^24, 0 <= sizes[i] <= 2^38; an
+ * empty tensor's pointers may be NULL. outs and out_dtypes are read by
+ * msda_clip_grad_norm only: outs[i] is grads[i] (clipped in place, same type)
+ * or memory that overlaps no other tensor of the list; out_dtypes[i] is
+ * dtypes[i], or MSDA_F32 for 16-bit gradients. The arrays are read during the
+ * call and not kept. */
+typedef struct {
+    int64_t count;
+    const void *const *grads;
+    void *const *outs;
+    const int64_t *sizes;
+    const int32_t *dtypes;
+    const int32_t *out_dtypes;
+} msda_grad_list_t;
+
+typedef enum {
+    MSDA_NORM_2 = 0,        /* sqrt of the sum of the squares of all entries */
+    MSDA_NORM_INF = 1       /* the largest absolute value                    */
+} msda_norm_kind_t;
+
+/* Bytes of device workspace the two calls below need for a list of these
+ * sizes, types and addresses. 0 for an invalid list. */
+MSDA_API size_t msda_grad_norm_workspace_bytes(const msda_grad_list_t *list);
+
+/* Writes the norm to `norm`: one float, or one double where the list has an
+ * MSDA_F64 tensor (an empty one counts). Sums are added in fp64 in an order
+ * that the list alone fixes, so the same call gives the same bits; squares
+ * that leave fp32's range are taken in fp64. NaN in any entry gives NaN; an
+ * infinite entry gives an infinite norm. An empty list has norm 0.
+ * workspace: at least msda_grad_norm_workspace_bytes(list) bytes, 16-byte
+ *   aligned, owned by the caller, overwritten.
+ * Errors: MSDA_ERR_NULL, _SHAPE, _DTYPE (types and kind), _ALIGN (element
+ *   size; norm 4 or 8 bytes), _WORKSPACE before any launch; MSDA_ERR_CUDA. */
+MSDA_API msda_status_t msda_grad_norm(const msda_grad_list_t *list, int kind, void *norm,
+                                      void *workspace, size_t workspace_bytes, void *stream);
+
+/* As msda_grad_norm, then outs[i] = grads[i] * min(1, max_norm / (norm + 1e-6)),
+ * rounded once. Nothing is read on the host: the factor is found on the device.
+ * An infinite norm makes the factor 0 (and infinite entries NaN), a NaN norm
+ * makes every entry NaN. Gradients whose norm is within max_norm keep their
+ * bits. max_norm >= 0 (infinity is allowed), else MSDA_ERR_SHAPE. */
+MSDA_API msda_status_t msda_clip_grad_norm(const msda_grad_list_t *list, int kind, double max_norm,
+                                           void *norm, void *workspace, size_t workspace_bytes,
+                                           void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -32,7 +32,8 @@ EXPORTED = ("msda_forward", "msda_backward_workspace_bytes", "msda_backward",
             "msda_debug_corners", "msda_checked_build", "msda_device_check",
             "msda_debug_bounds_self_test", "msda_set_sample_split", "msda_status_string",
             "msda_version", "msda_layer_norm_forward", "msda_layer_norm_backward_workspace_bytes",
-            "msda_layer_norm_backward")
+            "msda_layer_norm_backward", "msda_grad_norm_workspace_bytes", "msda_grad_norm",
+            "msda_clip_grad_norm")
 
 
 class msda_dims_t(ctypes.Structure):
@@ -41,6 +42,12 @@ class msda_dims_t(ctypes.Structure):
 
 class msda_norm_dims_t(ctypes.Structure):
     _fields_ = [("N", ctypes.c_int64), ("C", ctypes.c_int64)]
+
+
+class msda_grad_list_t(ctypes.Structure):
+    _fields_ = [("count", ctypes.c_int64), ("grads", ctypes.c_void_p), ("outs", ctypes.c_void_p),
+                ("sizes", ctypes.c_void_p), ("dtypes", ctypes.c_void_p),
+                ("out_dtypes", ctypes.c_void_p)]
 
 
 class MSDAError(RuntimeError):
@@ -109,6 +116,14 @@ def load(path: str | None = None):
     so.msda_layer_norm_backward.argtypes = [vp] * 11 + [ctypes.c_size_t, norm_dims, ctypes.c_int,
                                                         ctypes.c_int, vp]
     so.msda_layer_norm_backward.restype = ctypes.c_int
+    grad_list = ctypes.POINTER(msda_grad_list_t)
+    so.msda_grad_norm_workspace_bytes.argtypes = [grad_list]
+    so.msda_grad_norm_workspace_bytes.restype = ctypes.c_size_t
+    so.msda_grad_norm.argtypes = [grad_list, ctypes.c_int, vp, vp, ctypes.c_size_t, vp]
+    so.msda_grad_norm.restype = ctypes.c_int
+    so.msda_clip_grad_norm.argtypes = [grad_list, ctypes.c_int, ctypes.c_double, vp, vp,
+                                       ctypes.c_size_t, vp]
+    so.msda_clip_grad_norm.restype = ctypes.c_int
     so.msda_version.argtypes = []
     so.msda_version.restype = ctypes.c_int
     return so
@@ -576,3 +591,160 @@ def layer_norm(x, weight=None, bias=None, residual=None, eps: float = 1e-5, retu
         return LayerNormFunction.apply(x, residual, weight, bias, eps, return_sum)
     out, total, _, _ = msda_layer_norm_forward(x, weight, bias, residual, eps, return_sum, stats=False)
     return (out, total) if return_sum else out
+
+
+# ------------------------------------------------------ gradient norm, clipping
+
+def _dense(t):
+    """Whether t's entries fill one span of memory, each place once."""
+    if t.is_contiguous():
+        return True
+    expected = 1
+    for stride, size in sorted((st, n) for st, n in zip(t.stride(), t.shape) if n != 1):
+        if stride != expected:
+            return False
+        expected *= size
+    return True
+
+
+def _span(t):
+    at = t.data_ptr()
+    return at, at + t.numel() * t.element_size()
+
+
+class GradientBuffers:
+    """A list of gradient tensors, checked once, for msda_grad_norm and
+    msda_clip_grad_norm: what a training loop whose gradients keep their memory (zeroed in
+    place, views of a flat buffer, or captured in a graph) holds across its steps.
+
+    grads: CUDA tensors of one device, of any of the four types, each dense (contiguous, or
+    e.g. channels-last), none sharing memory with another. out: None to clip in place, or as
+    many tensors that receive the clipped gradients, of the same shapes and of the
+    gradients' types, or float32 for 16-bit gradients."""
+
+    def __init__(self, grads, out=None):
+        grads = list(grads)
+        outs = grads if out is None else list(out)
+        if len(outs) != len(grads):
+            raise ValueError(f"{len(outs)} outputs for {len(grads)} gradients")
+        device = grads[0].device if grads else None
+        for g, o in zip(grads, outs):
+            if not g.is_cuda:
+                raise ValueError("libmsda runs on CUDA tensors only (no CPU path)")
+            if g.layout != torch.strided:
+                raise ValueError("a gradient is sparse: give dense gradients")
+            if g.dtype not in _DTYPES:
+                raise ValueError(f"unsupported dtype {g.dtype}")
+            if g.device != device or o.device != device:
+                raise ValueError(f"tensors on {device}, {g.device} and {o.device}: give one device's")
+            if not _dense(g):
+                raise ValueError("a gradient is not dense: libmsda needs its entries in one span")
+            if o is not g:
+                if o.shape != g.shape or (o.stride() != g.stride() and not
+                                          (o.is_contiguous() and g.is_contiguous())):
+                    raise ValueError("an output's shape or strides differ from its gradient's")
+                if o.dtype != g.dtype and not (o.dtype == torch.float32 and
+                                               g.dtype in (torch.bfloat16, torch.float16)):
+                    raise ValueError(f"an output of {o.dtype} for a gradient of {g.dtype}: give the "
+                                     "gradient's type, or float32 for a 16-bit gradient")
+        self.device = device
+        self.in_place = out is None
+        # aliases: what the caller does to its own tensor objects does not reach them
+        self._grads = [g.detach() for g in grads]
+        self._outs = self._grads if out is None else [o.detach() for o in outs]
+        self._all = self._grads if out is None else self._grads + self._outs
+        self._counted = [o for o in self._outs if not o.is_inference()]
+        self.norm_dtype = (torch.float64 if any(g.dtype is torch.float64 for g in grads)
+                           else torch.float32)
+        n = len(grads)
+        self._sizes = (ctypes.c_int64 * n)(*[g.numel() for g in grads])
+        self._dtypes = (ctypes.c_int32 * n)(*[_DTYPES[g.dtype] for g in grads])
+        self._out_dtypes = (ctypes.c_int32 * n)(*[_DTYPES[o.dtype] for o in outs])
+        self._read_addresses()
+
+    def _read_addresses(self):
+        spans = sorted(_span(t) for t in self._all if t.numel())
+        for (_, end), (begin, _) in zip(spans, spans[1:]):
+            if begin < end:
+                raise ValueError("two of the tensors share memory")
+        for t in self._all:
+            held = t.untyped_storage().nbytes() - t.storage_offset() * t.element_size()
+            if held < t.numel() * t.element_size():
+                raise ValueError("a tensor's storage was resized to less than the tensor")
+        self._addresses = list(map(torch.Tensor.data_ptr, self._all))
+        n = len(self._grads)
+        self._at = (ctypes.c_void_p * n)(*self._addresses[:n])
+        self._out_at = self._at if self.in_place else (ctypes.c_void_p * n)(*self._addresses[n:])
+        self._list = msda_grad_list_t(n, *[ctypes.addressof(a) for a in (
+            self._at, self._out_at, self._sizes, self._dtypes, self._out_dtypes)])
+        self._ref = ctypes.byref(self._list)
+        self.workspace_bytes = int(lib().msda_grad_norm_workspace_bytes(self._ref))
+
+    def _prepare(self):
+        if list(map(torch.Tensor.data_ptr, self._all)) != self._addresses:
+            self._read_addresses()
+
+
+def _norm_kind(norm_type):
+    norm_type = float(norm_type)
+    if norm_type == 2.0:
+        return 0
+    if norm_type == float("inf"):
+        return 1
+    raise ValueError(f"norm_type {norm_type}: 2 and inf are supported")
+
+
+def _grad_call(buf, kind, max_norm, stream):
+    buf._prepare()
+    norm = torch.empty((), dtype=buf.norm_dtype, device=buf.device)
+    workspace = torch.empty(buf.workspace_bytes, dtype=torch.uint8, device=buf.device)
+    s = _current_stream(norm.get_device())
+    if max_norm is None:
+        _call("msda_grad_norm", lib().msda_grad_norm(
+            buf._ref, kind, norm.data_ptr(), workspace.data_ptr(), buf.workspace_bytes, s))
+    else:
+        _call("msda_clip_grad_norm", lib().msda_clip_grad_norm(
+            buf._ref, kind, max_norm, norm.data_ptr(), workspace.data_ptr(), buf.workspace_bytes, s))
+        torch._C._increment_version(buf._counted)
+    return norm
+
+
+def _grad_norm(grads, norm_type, max_norm, stream):
+    kind = _norm_kind(norm_type)
+    buf = grads if isinstance(grads, GradientBuffers) else GradientBuffers(grads)
+    if buf.device is None:               # an empty list
+        return torch.zeros(())
+    if stream is not None or torch._C._cuda_getDevice() != buf.device.index:
+        with _on(buf.device, stream):
+            return _grad_call(buf, kind, max_norm, stream)
+    return _grad_call(buf, kind, max_norm, stream)
+
+
+def msda_grad_norm(grads, norm_type: float = 2.0, stream=None):
+    """The norm of all entries of `grads` (GradientBuffers, or a list of tensors): a 0-d
+    float32 tensor on their device (float64 where one of them is). norm_type 2 or inf. See
+    msda_grad_norm in include/msda.h."""
+    return _grad_norm(grads, norm_type, None, stream)
+
+
+def msda_clip_grad_norm(grads, max_norm: float, norm_type: float = 2.0, stream=None):
+    """The norm, as msda_grad_norm; and the gradients times min(1, max_norm / (norm + 1e-6)),
+    in place or in the buffers' outputs. Nothing waits for the device."""
+    return _grad_norm(grads, norm_type, float(max_norm), stream)
+
+
+def clip_grad_norm_(parameters, max_norm: float, norm_type: float = 2.0,
+                    error_if_nonfinite: bool = False):
+    """Clip the gradients of `parameters` (a tensor or an iterable of them; those without a
+    gradient are passed over) to a joint norm of max_norm, in place; returns the norm they
+    had. error_if_nonfinite: raise where that is not finite (waits for the device; the
+    gradients are then left as they were)."""
+    if isinstance(parameters, torch.Tensor):
+        parameters = [parameters]
+    grads = [p.grad for p in parameters if p.grad is not None]
+    buf = GradientBuffers(grads)
+    if error_if_nonfinite:
+        norm = msda_grad_norm(buf, norm_type)
+        if not torch.isfinite(norm):
+            raise RuntimeError(f"the norm of the gradients is {float(norm)}: not clipped")
+    return msda_clip_grad_norm(buf, max_norm, norm_type)

@@ -1,0 +1,567 @@
+// The global norm of a list of gradient tensors, and clipping by it.
+//
+//   norm = sqrt(sum over all entries of g^2), or max |g|
+//   out  = g * min(1, max_norm / (norm + 1e-6))
+//
+// A launch takes a table of up to kLargeTable tensors of one type by value (no
+// copy to the device, nothing to keep alive while a graph replays). The tensors
+// are cut into units of 4 KB; a warp takes a contiguous run of units, so
+// that many small tensors and a few large ones spread over the SMs alike. The
+// first kernel leaves one partial result per block; every block of the second
+// adds them up in the same order (the norm has the same bits in all of them,
+// and from call to call) and scales its units, last to first: those the L2
+// still holds from the first kernel come first.
+#include <float.h>
+
+#include <type_traits>
+
+#include "msda_common.cuh"
+#include "msda_host.h"
+
+namespace msda {
+cudaError_t fault_word_for_launch(unsigned **err);
+
+namespace {
+
+constexpr int kUnitBytes = 4096;         // of the source: eight 16-byte loads per lane
+constexpr int kNormThreads = 256;
+constexpr int kMaxBlocks = 152 * 6;      // of one launch
+constexpr int kSmallTable = 64, kLargeTable = 1024;
+constexpr int64_t kMaxEntries = (int64_t)1 << 38;   // of one tensor: its units fit 2^29
+
+// Tensors of a launch: source, destination, entries, and the units before each.
+template <int N> struct Table {
+    const void *src[N];
+    void *dst[N];
+    int64_t size[N];
+    uint32_t before[N + 1];
+    int count;
+};
+
+struct Run { uint32_t begin, end; };     // a warp's units
+
+template <int N> __device__ __forceinline__ Run warp_run(const Table<N> &t) {
+    const uint32_t units = t.before[t.count], warps = gridDim.x * (kNormThreads / 32);
+    const uint32_t w = blockIdx.x * (kNormThreads / 32) + threadIdx.x / 32;
+    // units / warps each, the first units % warps one more
+    const uint32_t each = units / warps, more = units % warps;
+    const uint32_t begin = w * each + (w < more ? w : more);
+    return Run{begin, begin + each + (w < more ? 1u : 0u)};
+}
+
+// Index of the tensor that unit u lies in.
+template <int N> __device__ __forceinline__ int tensor_of(const Table<N> &t, uint32_t u) {
+    int lo = 0, hi = t.count - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) / 2;
+        if (t.before[mid] <= u) lo = mid;
+        else hi = mid - 1;
+    }
+    return lo;
+}
+
+// A unit's entries [begin, end) of its tensor. The unit boundaries lie on
+// 16-byte boundaries of the source; the first unit takes the entries before its
+// first boundary as well, [0, body).
+template <typename T> struct Unit {
+    int64_t begin, end, body;
+    __device__ __forceinline__ Unit(const T *src, int64_t size, uint32_t at) {
+        constexpr int per = kUnitBytes / sizeof(T);
+        const int64_t head = (16 - (reinterpret_cast<uintptr_t>(src) & 15)) % 16 / sizeof(T);
+        body = head + (int64_t)at * per;
+        begin = at == 0 ? 0 : body;
+        end = body + per < size ? body + per : size;
+        if (body > end) body = end;
+    }
+};
+
+template <typename T> __host__ __device__ uint32_t units_of(const void *src, int64_t size) {
+    constexpr int64_t per = kUnitBytes / sizeof(T);
+    const int64_t head = (16 - (reinterpret_cast<uintptr_t>(src) & 15)) % 16 / sizeof(T);
+    const int64_t body = size > head ? size - head : 0;
+    return size == 0 ? 0u : body == 0 ? 1u : (uint32_t)((body + per - 1) / per);
+}
+
+template <typename T> __device__ __forceinline__ double as_double(T v) {
+    if constexpr (sizeof(T) == 8) return v;
+    else return (double)Elem<T>::to_f(v);
+}
+
+// The larger of two; NaN if either is.
+__device__ __forceinline__ double larger(double a, double b) { return a > b || a != a ? a : b; }
+
+template <bool LARGEST> __device__ __forceinline__ double join(double a, double b) {
+    return LARGEST ? larger(a, b) : a + b;
+}
+
+// One lane's part of a unit. Squares are added in fp32, 32 or 64 of them, and
+// these sums in fp64. Where such a sum is not finite, or so small that squares
+// lost digits (under 1e-36: 64 roundings of subnormals, 2^-150 each, are 2^-24 of
+// it) though not all entries are zero, they are squared and added in fp64 instead.
+template <typename T, bool LARGEST>
+__device__ __forceinline__ double lane_part(const T *src, const Unit<T> &u, int lane) {
+    constexpr int V = 16 / sizeof(T), per = kUnitBytes / 16 / 32;
+    double part = 0.0;
+    // entries before the first and after the last whole vector, at most V - 1 each
+    const int64_t vectors = (u.end - u.body) / V;
+    const int64_t tail = u.body + vectors * V;
+    for (int64_t i = u.begin + lane; i < u.body; i += 32) {
+        const double v = as_double<T>(src[i]);
+        part = LARGEST ? larger(part, fabs(v)) : part + v * v;
+    }
+    if (tail + lane < u.end) {
+        const double v = as_double<T>(src[tail + lane]);
+        part = LARGEST ? larger(part, fabs(v)) : part + v * v;
+    }
+    uint4 raw[per];
+#pragma unroll
+    for (int k = 0; k < per; ++k) {
+        raw[k] = make_uint4(0u, 0u, 0u, 0u);
+        const int64_t at = (int64_t)k * 32 + lane;
+        if (at < vectors) raw[k] = ldg16(src + u.body + at * V);
+    }
+    if constexpr (sizeof(T) == 8) {
+#pragma unroll
+        for (int k = 0; k < per; ++k) {
+            const double a = __hiloint2double(raw[k].y, raw[k].x), b = __hiloint2double(raw[k].w, raw[k].z);
+            part = LARGEST ? larger(larger(part, fabs(a)), fabs(b)) : fma(a, a, fma(b, b, part));
+        }
+    } else if constexpr (LARGEST) {
+        // the bits of |v| order like the values, NaN above infinity
+        uint32_t top = 0u;
+#pragma unroll
+        for (int k = 0; k < per; ++k) {
+            const uint32_t w[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if constexpr (sizeof(T) == 4) top = max(top, w[i] & 0x7fffffffu);
+                else top = __vmaxu2(top, w[i] & 0x7fff7fffu);
+            }
+        }
+        T value;
+        if constexpr (sizeof(T) == 4) value = __uint_as_float(top);
+        else {
+            const unsigned short half = (unsigned short)max(top & 0xffffu, top >> 16);
+            value = *reinterpret_cast<const T *>(&half);
+        }
+        part = larger(part, as_double<T>(value));
+    } else {
+        float sum = 0.0f;
+        uint32_t any = 0u;
+#pragma unroll
+        for (int k = 0; k < per; ++k) {
+            float v[V];
+            unpack16<T>(v, raw[k]);
+#pragma unroll
+            for (int i = 0; i < V; ++i) sum = fmaf(v[i], v[i], sum);
+            any |= raw[k].x | raw[k].y | raw[k].z | raw[k].w;
+        }
+        if (sum >= 1e-36f && sum <= FLT_MAX) part += (double)sum;
+        else if ((any & (sizeof(T) == 4 ? 0x7fffffffu : 0x7fff7fffu)) != 0u) {
+#pragma unroll 1
+            for (int k = 0; k < per; ++k) {
+                const int64_t at = (int64_t)k * 32 + lane;
+                if (at >= vectors) break;
+#pragma unroll 1
+                for (int i = 0; i < V; ++i) {
+                    const double v = as_double<T>(src[u.body + at * V + i]);
+                    part += v * v;
+                }
+            }
+        }
+    }
+    return part;
+}
+
+// Sum (or the largest) over a block, in thread 0 and its warp.
+template <bool LARGEST> __device__ __forceinline__ double block_join(double v, double *scratch) {
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) v = join<LARGEST>(v, __shfl_xor_sync(0xffffffffu, v, off));
+    if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        v = threadIdx.x < blockDim.x / 32 ? scratch[threadIdx.x] : 0.0;
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) v = join<LARGEST>(v, __shfl_xor_sync(0xffffffffu, v, off));
+    }
+    return v;
+}
+
+template <typename T, bool LARGEST, int N>
+__global__ void __launch_bounds__(kNormThreads)
+grad_part_kernel(const __grid_constant__ Table<N> t, double *partial, unsigned *err) {
+    __shared__ double scratch[32];
+    cudaTriggerProgrammaticLaunchCompletion();
+    const Run run = warp_run(t);
+    const int lane = threadIdx.x & 31;
+    double part = 0.0;
+    if (run.begin < run.end) {
+        int i = tensor_of(t, run.begin);
+        for (uint32_t u = run.begin; u < run.end; ++u) {
+            while (u >= t.before[i + 1]) ++i;
+            const T *src = static_cast<const T *>(t.src[i]);
+            const Unit<T> unit(src, t.size[i], u - t.before[i]);
+#ifdef MSDA_CHECKED
+            if (unit.begin < 0 || unit.end > t.size[i] || unit.begin > unit.end || i >= t.count) {
+                if (err) atomicOr(err, 1u);
+                continue;
+            }
+#endif
+            part = join<LARGEST>(part, lane_part<T, LARGEST>(src, unit, lane));
+        }
+    }
+    part = block_join<LARGEST>(part, scratch);
+    if (threadIdx.x == 0) partial[blockIdx.x] = part;
+}
+
+// The norm from the partial results, in every thread of a block.
+template <bool LARGEST> __device__ __forceinline__ double norm_of(const double *partial, int count, double *scratch) {
+    double v = 0.0;
+    for (int i = threadIdx.x; i < count; i += blockDim.x) v = join<LARGEST>(v, partial[i]);
+    v = block_join<LARGEST>(v, scratch);
+    if (threadIdx.x == 0) scratch[0] = LARGEST ? v : sqrt(v);
+    __syncthreads();
+    return scratch[0];
+}
+
+__device__ __forceinline__ void write_norm(double norm, void *to, bool wide) {
+    if (wide) *static_cast<double *>(to) = norm;
+    else *static_cast<float *>(to) = (float)norm;
+}
+
+template <bool LARGEST>
+__global__ void __launch_bounds__(kNormThreads)
+grad_norm_kernel(const double *partial, int count, void *norm, bool wide) {
+    __shared__ double scratch[32];
+    cudaGridDependencySynchronize();
+    const double n = norm_of<LARGEST>(partial, count, scratch);
+    if (threadIdx.x == 0) write_norm(n, norm, wide);
+}
+
+// 32 bytes in one store (the address a multiple of 32).
+__device__ __forceinline__ void store32(float *to, const float *v) {
+    asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(to), "f"(v[0]), "f"(v[1]), "f"(v[2]),
+                 "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+                 : "memory");
+}
+
+template <typename T> __device__ __forceinline__ void put(T *to, float v) { *to = Elem<T>::from_f(v); }
+__device__ __forceinline__ void put(double *to, double v) { *to = v; }
+
+template <typename T, typename U, bool LARGEST, int N>
+__global__ void __launch_bounds__(kNormThreads)
+grad_scale_kernel(const __grid_constant__ Table<N> t, const double *partial, int count, double max_norm,
+                  void *norm, bool wide, unsigned *err) {
+    using A = typename std::conditional<sizeof(T) == 8, double, float>::type;
+    constexpr int V = 16 / sizeof(T), per = kUnitBytes / 16 / 32;
+    __shared__ double scratch[32];
+    cudaGridDependencySynchronize();
+    const double total = norm_of<LARGEST>(partial, count, scratch);
+    if (norm && blockIdx.x == 0 && threadIdx.x == 0) write_norm(total, norm, wide);
+    const double ratio = max_norm / (total + 1e-6);
+    const A factor = (A)(ratio > 1.0 ? 1.0 : ratio);    // NaN stays NaN
+    const Run run = warp_run(t);
+    if (run.begin >= run.end) return;
+    const int lane = threadIdx.x & 31;
+    int i = tensor_of(t, run.end - 1);
+    for (uint32_t u = run.end; u-- > run.begin;) {
+        while (u < t.before[i]) --i;
+        const T *src = static_cast<const T *>(t.src[i]);
+        U *dst = static_cast<U *>(t.dst[i]);
+        if (factor == (A)1 && static_cast<const void *>(src) == static_cast<const void *>(dst)) continue;
+        const Unit<T> unit(src, t.size[i], u - t.before[i]);
+#ifdef MSDA_CHECKED
+        if (unit.begin < 0 || unit.end > t.size[i] || unit.begin > unit.end || i < 0) {
+            if (err) atomicOr(err, 1u);
+            continue;
+        }
+#endif
+        // a source vector's entries go out in one store of 8 to 32 bytes
+        constexpr int out = V * sizeof(U);
+        const bool vec = (reinterpret_cast<uintptr_t>(dst + unit.body) & (out - 1)) == 0;
+        const int64_t vectors = vec ? (unit.end - unit.body) / V : 0;
+        if (vec) {
+            uint4 raw[per];
+#pragma unroll
+            for (int k = 0; k < per; ++k) {
+                const int64_t at = (int64_t)k * 32 + lane;
+                raw[k] = make_uint4(0u, 0u, 0u, 0u);
+                if (at < vectors) raw[k] = *reinterpret_cast<const uint4 *>(src + unit.body + at * V);
+            }
+#pragma unroll
+            for (int k = 0; k < per; ++k) {
+                const int64_t at = (int64_t)k * 32 + lane;
+                if (at >= vectors) continue;
+                U *to = dst + unit.body + at * V;
+                if constexpr (sizeof(T) == 8) {
+                    *reinterpret_cast<double2 *>(to) =
+                        make_double2(__hiloint2double(raw[k].y, raw[k].x) * factor,
+                                     __hiloint2double(raw[k].w, raw[k].z) * factor);
+                } else {
+                    float v[V];
+                    unpack16<T>(v, raw[k]);
+#pragma unroll
+                    for (int j = 0; j < V; ++j) v[j] *= factor;
+                    if constexpr (out == 32) store32(to, v);
+                    else *reinterpret_cast<uint4 *>(to) = pack16<U>(v);
+                }
+            }
+            for (int64_t j = unit.begin + lane; j < unit.body; j += 32) put(dst + j, (A)as_double<T>(src[j]) * factor);
+            for (int64_t j = unit.body + vectors * V + lane; j < unit.end; j += 32)
+                put(dst + j, (A)as_double<T>(src[j]) * factor);
+        } else {
+            // the destination's 16-byte boundaries lie elsewhere: entry by entry, 16 loads ahead
+            for (int64_t j = unit.begin + lane; j < unit.end; j += 32 * 16) {
+                T v[16];
+#pragma unroll
+                for (int k = 0; k < 16; ++k)
+                    if (j + 32 * k < unit.end) v[k] = src[j + 32 * k];
+#pragma unroll
+                for (int k = 0; k < 16; ++k)
+                    if (j + 32 * k < unit.end) put(dst + j + 32 * k, (A)as_double<T>(v[k]) * factor);
+            }
+        }
+    }
+}
+
+// ----------------------------------------------------------------- launches
+
+int bytes_of(int32_t dt) { return dt == MSDA_F64 ? 8 : dt == MSDA_F32 ? 4 : 2; }
+
+// Tensors of a list that share a launch: one type of source and destination.
+bool in_class(const msda_grad_list_t &l, int64_t i, int32_t from, int32_t to) {
+    return l.sizes[i] > 0 && l.dtypes[i] == from && (to < 0 || l.out_dtypes[i] == to);
+}
+
+uint32_t units_for(int32_t dt, const void *src, int64_t size) {
+    switch (dt) {
+        case MSDA_F64: return units_of<double>(src, size);
+        case MSDA_F32: return units_of<float>(src, size);
+        case MSDA_BF16: return units_of<__nv_bfloat16>(src, size);
+        default: return units_of<__half>(src, size);
+    }
+}
+
+// Blocks of a launch over `units`: a warp per unit up to the machine's size,
+// then the count of blocks per SM that leaves the last round of units fullest.
+int blocks_for(uint32_t units) {
+    const uint32_t warps = kNormThreads / 32, sms = 152;
+    if (units <= 2 * sms * warps) return (int)((units + warps - 1) / warps);
+    int best = 0;
+    uint64_t least = ~0ull;
+    for (uint32_t per_sm = 4; per_sm <= 6; ++per_sm) {
+        const uint64_t all = (uint64_t)per_sm * sms * warps, waste = (units + all - 1) / all * all - units;
+        if (waste < least) {
+            least = waste;
+            best = (int)(per_sm * sms);
+        }
+    }
+    return best;
+}
+
+cudaError_t launch(const void *kernel, int blocks, void **args, bool early, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.blockDim = dim3(kNormThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = early ? 1 : 0;
+    return cudaLaunchKernelExC(&cfg, kernel, args);
+}
+
+template <typename T, int N> const void *part_kernel(bool largest) {
+    return largest ? (const void *)grad_part_kernel<T, true, N> : (const void *)grad_part_kernel<T, false, N>;
+}
+template <typename T, typename U, int N> const void *scale_kernel(bool largest) {
+    return largest ? (const void *)grad_scale_kernel<T, U, true, N> : (const void *)grad_scale_kernel<T, U, false, N>;
+}
+template <int N> const void *part_kernel(int32_t dt, bool largest) {
+    switch (dt) {
+        case MSDA_F64: return part_kernel<double, N>(largest);
+        case MSDA_F32: return part_kernel<float, N>(largest);
+        case MSDA_BF16: return part_kernel<__nv_bfloat16, N>(largest);
+        default: return part_kernel<__half, N>(largest);
+    }
+}
+template <int N> const void *scale_kernel(int32_t dt, int32_t to, bool largest) {
+    if (dt == MSDA_F64) return scale_kernel<double, double, N>(largest);
+    if (dt == MSDA_F32) return scale_kernel<float, float, N>(largest);
+    if (dt == MSDA_BF16)
+        return to == MSDA_F32 ? scale_kernel<__nv_bfloat16, float, N>(largest)
+                              : scale_kernel<__nv_bfloat16, __nv_bfloat16, N>(largest);
+    return to == MSDA_F32 ? scale_kernel<__half, float, N>(largest) : scale_kernel<__half, __half, N>(largest);
+}
+
+// Fills tables with the tensors of one class, in the list's order, and hands
+// each to `run(table, units)`. Stops at the first error.
+template <int N, typename F>
+cudaError_t each_table(const msda_grad_list_t &l, int32_t from, int32_t to, F run) {
+    Table<N> t;
+    t.count = 0;
+    t.before[0] = 0;
+    for (int64_t i = 0; i < l.count; ++i) {
+        if (!in_class(l, i, from, to)) continue;
+        const uint32_t units = units_for(from, l.grads[i], l.sizes[i]);
+        if (t.count == N || units > 0x7fffffffu - t.before[t.count]) {
+            const cudaError_t e = run(t);
+            if (e != cudaSuccess) return e;
+            t.count = 0;
+        }
+        t.src[t.count] = l.grads[i];
+        t.dst[t.count] = to < 0 ? nullptr : l.outs[i];
+        t.size[t.count] = l.sizes[i];
+        t.before[t.count + 1] = t.before[t.count] + units;
+        ++t.count;
+    }
+    return t.count ? run(t) : cudaSuccess;
+}
+
+// What one pass over a list finds: per type (msda_dtype_t's values), whether it
+// occurs, with a destination of its own type or fp32, and the launches the first
+// kernel may need.
+constexpr int kTypes = 4;
+struct Summary {
+    int64_t count[kTypes], units[kTypes];
+    bool to_own[kTypes], to_f32[kTypes];
+    bool f64;
+    // a table per kLargeTable tensors, and one more each time that units fill one
+    int64_t launches() const {
+        int64_t n = 0;
+        for (int dt = 0; dt < kTypes; ++dt)
+            if (count[dt]) n += (count[dt] + kLargeTable - 1) / kLargeTable + (units[dt] >> 30);
+        return n;
+    }
+    size_t bytes() const {
+        const int64_t n = launches();
+        return (size_t)(n < 1 ? 1 : n) * kMaxBlocks * sizeof(double);
+    }
+};
+
+msda_status_t check(const msda_grad_list_t *l, bool clip, int kind, Summary *s) {
+    *s = Summary{};
+    if (!l) return MSDA_ERR_NULL;
+    if (l->count < 0 || l->count > (1 << 24)) return MSDA_ERR_SHAPE;
+    if (kind != MSDA_NORM_2 && kind != MSDA_NORM_INF) return MSDA_ERR_DTYPE;
+    if (l->count == 0) return MSDA_OK;
+    if (!l->grads || !l->sizes || !l->dtypes || (clip && (!l->outs || !l->out_dtypes))) return MSDA_ERR_NULL;
+    for (int64_t i = 0; i < l->count; ++i) {
+        if (l->sizes[i] < 0 || l->sizes[i] > kMaxEntries) return MSDA_ERR_SHAPE;
+        const int32_t dt = l->dtypes[i];
+        if (dt < 0 || dt >= kTypes) return MSDA_ERR_DTYPE;
+        s->f64 = s->f64 || dt == MSDA_F64;
+        if (clip) {
+            const int32_t to = l->out_dtypes[i];
+            if (to != dt && !(to == MSDA_F32 && bytes_of(dt) == 2)) return MSDA_ERR_DTYPE;
+            (to == dt ? s->to_own : s->to_f32)[dt] = true;
+        }
+        if (l->sizes[i] == 0) continue;
+        if (!l->grads[i] || (clip && !l->outs[i])) return MSDA_ERR_NULL;
+        if (reinterpret_cast<uintptr_t>(l->grads[i]) % bytes_of(dt)) return MSDA_ERR_ALIGN;
+        if (clip && reinterpret_cast<uintptr_t>(l->outs[i]) % bytes_of(l->out_dtypes[i])) return MSDA_ERR_ALIGN;
+        ++s->count[dt];
+        s->units[dt] += units_for(dt, l->grads[i], l->sizes[i]);
+    }
+    return MSDA_OK;
+}
+
+// First kernel over the whole list; *parts: partial results written.
+template <int N>
+cudaError_t launch_parts(const msda_grad_list_t &l, const Summary &sum, bool largest, double *partial, int *parts,
+                         unsigned *err, cudaStream_t stream) {
+    *parts = 0;
+    for (int32_t dt = 0; dt < kTypes; ++dt) {
+        if (!sum.count[dt]) continue;
+        const cudaError_t e = each_table<N>(l, dt, -1, [&](Table<N> &t) {
+            const int blocks = blocks_for(t.before[t.count]);
+            double *to = partial + *parts;
+            void *args[] = {&t, &to, &err};
+            *parts += blocks;
+            return launch(part_kernel<N>(dt, largest), blocks, args, false, stream);
+        });
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
+template <int N>
+cudaError_t launch_scale(const msda_grad_list_t &l, const Summary &sum, bool largest, const double *partial,
+                         int parts, double max_norm, void *norm, unsigned *err, cudaStream_t stream) {
+    bool first = true, wide = sum.f64;
+    for (int32_t dt = 0; dt < kTypes; ++dt) {
+        for (int own = 0; own < 2; ++own) {
+            if (!sum.count[dt] || !(own ? sum.to_own : sum.to_f32)[dt]) continue;
+            const int32_t to = own ? dt : (int32_t)MSDA_F32;
+            const cudaError_t e = each_table<N>(l, dt, to, [&](Table<N> &t) {
+                void *where = first ? norm : nullptr;
+                void *args[] = {&t, &partial, &parts, &max_norm, &where, &wide, &err};
+                const bool early = first;        // only this one follows the first kernel directly
+                first = false;
+                return launch(scale_kernel<N>(dt, to, largest), blocks_for(t.before[t.count]), args, early, stream);
+            });
+            if (e != cudaSuccess) return e;
+        }
+    }
+    return cudaSuccess;
+}
+
+cudaError_t launch_norm(bool largest, const double *partial, int parts, void *norm, bool wide, cudaStream_t stream) {
+    void *args[] = {&partial, &parts, &norm, &wide};
+    return launch(largest ? (const void *)grad_norm_kernel<true> : (const void *)grad_norm_kernel<false>, 1, args,
+                  true, stream);
+}
+
+template <int N>
+cudaError_t norm_and_scale(const msda_grad_list_t &l, const Summary &sum, bool largest, bool clip, double max_norm,
+                           void *norm, double *partial, cudaStream_t stream) {
+    unsigned *err = nullptr;
+    cudaError_t e = fault_word_for_launch(&err);
+    int parts = 0;
+    if (e == cudaSuccess) e = launch_parts<N>(l, sum, largest, partial, &parts, err, stream);
+    if (e != cudaSuccess) return e;
+    if (!clip || parts == 0) return launch_norm(largest, partial, parts, norm, sum.f64, stream);
+    return launch_scale<N>(l, sum, largest, partial, parts, max_norm, norm, err, stream);
+}
+
+msda_status_t run(const msda_grad_list_t *l, int kind, bool clip, double max_norm, void *norm, void *workspace,
+                  size_t workspace_bytes, void *stream) {
+    Summary sum;
+    const msda_status_t st = check(l, clip, kind, &sum);
+    if (st != MSDA_OK) return st;
+    if (clip && !(max_norm >= 0.0)) return MSDA_ERR_SHAPE;
+    if (!norm) return MSDA_ERR_NULL;
+    if (!workspace || workspace_bytes < sum.bytes()) return MSDA_ERR_WORKSPACE;
+    if (reinterpret_cast<uintptr_t>(workspace) % 16) return MSDA_ERR_ALIGN;
+    if (reinterpret_cast<uintptr_t>(norm) % (sum.f64 ? 8 : 4)) return MSDA_ERR_ALIGN;
+    double *partial = static_cast<double *>(workspace);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const bool largest = kind == MSDA_NORM_INF;
+    const cudaError_t e = l->count <= kSmallTable
+                              ? norm_and_scale<kSmallTable>(*l, sum, largest, clip, max_norm, norm, partial, s)
+                              : norm_and_scale<kLargeTable>(*l, sum, largest, clip, max_norm, norm, partial, s);
+    return e == cudaSuccess ? MSDA_OK : MSDA_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace msda
+
+extern "C" {
+
+size_t msda_grad_norm_workspace_bytes(const msda_grad_list_t *list) {
+    msda::Summary sum;
+    return msda::check(list, false, MSDA_NORM_2, &sum) == MSDA_OK ? sum.bytes() : 0;
+}
+
+msda_status_t msda_grad_norm(const msda_grad_list_t *list, int kind, void *norm, void *workspace,
+                             size_t workspace_bytes, void *stream) {
+    return msda::run(list, kind, false, 0.0, norm, workspace, workspace_bytes, stream);
+}
+
+msda_status_t msda_clip_grad_norm(const msda_grad_list_t *list, int kind, double max_norm, void *norm,
+                                  void *workspace, size_t workspace_bytes, void *stream) {
+    return msda::run(list, kind, true, max_norm, norm, workspace, workspace_bytes, stream);
+}
+
+}  // extern "C"
