@@ -404,6 +404,11 @@ def _norm_dims(numel, C):
     return ctypes.byref(msda_norm_dims_t(numel // C if C else 0, C))
 
 
+@functools.lru_cache(maxsize=256)
+def _norm_workspace(numel, C, dtype):
+    return int(lib().msda_layer_norm_backward_workspace_bytes(_norm_dims(numel, C), dtype))
+
+
 def _param_dtype(x, weight, bias, given=None):
     params = weight if weight is not None else bias
     pdt = params.dtype if params is not None else given if given is not None else x.dtype
@@ -456,7 +461,8 @@ def _norm_forward(x, weight, bias, residual, eps, return_sum, stats, out, pdt):
     total = torch.empty_like(x) if return_sum else None
     mean = rstd = None
     if stats:
-        stats = torch.empty((2, *x.shape[:-1]), dtype=_stats_dtype(x), device=x.device)
+        stats = torch.empty(2 * (x.numel() // x.shape[-1]) if x.shape[-1] else 0,
+                            dtype=_stats_dtype(x), device=x.device)
         mean = stats.data_ptr()
         rstd = mean + stats.numel() // 2 * stats.element_size()
     status = lib().msda_layer_norm_forward(
@@ -477,11 +483,10 @@ def _norm_backward(grad_out, x, mean, rstd, weight, residual, grad_sum, pdt, wan
     need = 0
     if want[1] or want[2]:
         C, device = x.shape[-1], x.device
-        if want[1]:
-            grad_weight = torch.empty(C, dtype=pdt, device=device)
-        if want[2]:
-            grad_bias = torch.empty(C, dtype=pdt, device=device)
-        need = lib().msda_layer_norm_backward_workspace_bytes(dims, dt)
+        grads = [None if not w else torch.empty(C, dtype=pdt, device=device) if weight is None
+                 else torch.empty_like(weight) for w in want[1:]]
+        grad_weight, grad_bias = grads
+        need = _norm_workspace(x.numel(), C, dt)
         workspace = torch.empty(need, dtype=torch.uint8, device=device)
     status = lib().msda_layer_norm_backward(
         grad_out.data_ptr(), _at(grad_sum), x.data_ptr(), _at(residual), _at(weight),
@@ -512,7 +517,10 @@ def msda_layer_norm_forward(x, weight=None, bias=None, residual=None, eps: float
             out, total, both = _norm_forward(*args)
     else:
         out, total, both = _norm_forward(*args)
-    return (out, total, both[0], both[1]) if stats else (out, total, None, None)
+    if not stats:
+        return out, total, None, None
+    mean, rstd = both.view(2, *x.shape[:-1])
+    return out, total, mean, rstd
 
 
 def msda_layer_norm_backward(grad_out, x, mean, rstd, weight=None, residual=None, grad_sum=None,

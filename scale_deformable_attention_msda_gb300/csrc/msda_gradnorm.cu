@@ -25,8 +25,9 @@ namespace {
 
 constexpr int kUnitBytes = 4096;         // of the source: eight 16-byte loads per lane
 constexpr int kNormThreads = 256;
-constexpr int kMaxBlocks = 152 * 6;      // of one launch
-constexpr int kSmallTable = 64, kLargeTable = 1024;
+constexpr int kSMs = 152, kMaxPerSM = 16, kMaxBlocks = kSMs * kMaxPerSM;   // of one launch
+// tensors of a launch: its parameters, the table among them, may fill 32,764 bytes
+constexpr int kSmallTable = 64, kLargeTable = 960;
 constexpr int64_t kMaxEntries = (int64_t)1 << 38;   // of one tensor: its units fit 2^29
 
 // Tensors of a launch: source, destination, entries, and the units before each.
@@ -36,28 +37,31 @@ template <int N> struct Table {
     int64_t size[N];
     uint32_t before[N + 1];
     int count;
+    uint16_t start[kMaxBlocks];          // tensor in which a block's first unit lies
 };
+
+// First unit of warp w of `warps`: units / warps each, the first units % warps
+// one more.
+__host__ __device__ inline uint32_t first_unit(uint32_t units, uint32_t warps, uint32_t w) {
+    const uint32_t each = units / warps, more = units % warps;
+    return w * each + (w < more ? w : more);
+}
+
+static_assert(sizeof(Table<kLargeTable>) <= 32764 - 64, "a launch's parameters");
 
 struct Run { uint32_t begin, end; };     // a warp's units
 
 template <int N> __device__ __forceinline__ Run warp_run(const Table<N> &t) {
     const uint32_t units = t.before[t.count], warps = gridDim.x * (kNormThreads / 32);
     const uint32_t w = blockIdx.x * (kNormThreads / 32) + threadIdx.x / 32;
-    // units / warps each, the first units % warps one more
-    const uint32_t each = units / warps, more = units % warps;
-    const uint32_t begin = w * each + (w < more ? w : more);
-    return Run{begin, begin + each + (w < more ? 1u : 0u)};
+    return Run{first_unit(units, warps, w), first_unit(units, warps, w + 1)};
 }
 
-// Index of the tensor that unit u lies in.
+// Index of the tensor that unit u of the block lies in.
 template <int N> __device__ __forceinline__ int tensor_of(const Table<N> &t, uint32_t u) {
-    int lo = 0, hi = t.count - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) / 2;
-        if (t.before[mid] <= u) lo = mid;
-        else hi = mid - 1;
-    }
-    return lo;
+    int i = t.start[blockIdx.x];
+    while (u >= t.before[i + 1]) ++i;
+    return i;
 }
 
 // A unit's entries [begin, end) of its tensor. The unit boundaries lie on
@@ -240,9 +244,32 @@ grad_norm_kernel(const double *partial, int count, void *norm, bool wide) {
 
 // 32 bytes in one store (the address a multiple of 32).
 __device__ __forceinline__ void store32(float *to, const float *v) {
-    asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(to), "f"(v[0]), "f"(v[1]), "f"(v[2]),
+    asm volatile("st.global.cs.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(to), "f"(v[0]), "f"(v[1]), "f"(v[2]),
                  "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
                  : "memory");
+}
+
+// The 16 bytes that start `bytes` (under 16, a multiple of 2) into a lane's
+// vector and run into the next lane's; lane 31 is followed by lane 0's `next`.
+__device__ __forceinline__ void shift_in(uint4 &own, const uint4 &next, int lane, int bytes) {
+    const uint4 give = lane == 0 ? next : own;
+    uint32_t w[8] = {own.x, own.y, own.z, own.w};
+    const uint32_t g[4] = {give.x, give.y, give.z, give.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[4 + i] = __shfl_sync(0xffffffffu, g[i], (lane + 1) & 31);
+    if (bytes & 8) {
+#pragma unroll
+        for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+    }
+    if (bytes & 4) {
+#pragma unroll
+        for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+    }
+    if (bytes & 2) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+    }
+    own = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 template <typename T> __device__ __forceinline__ void put(T *to, float v) { *to = Elem<T>::from_f(v); }
@@ -264,6 +291,7 @@ grad_scale_kernel(const __grid_constant__ Table<N> t, const double *partial, int
     if (run.begin >= run.end) return;
     const int lane = threadIdx.x & 31;
     int i = tensor_of(t, run.end - 1);
+#pragma unroll 1
     for (uint32_t u = run.end; u-- > run.begin;) {
         while (u < t.before[i]) --i;
         const T *src = static_cast<const T *>(t.src[i]);
@@ -276,49 +304,41 @@ grad_scale_kernel(const __grid_constant__ Table<N> t, const double *partial, int
             continue;
         }
 #endif
-        // a source vector's entries go out in one store of 8 to 32 bytes
+        // A source vector's entries go out in one store of 16 or 32 bytes. Where the
+        // destination's boundaries lie `skew` entries after the source's, a store
+        // takes entries of two source vectors, a lane's own and the next lane's.
         constexpr int out = V * sizeof(U);
-        const bool vec = (reinterpret_cast<uintptr_t>(dst + unit.body) & (out - 1)) == 0;
-        const int64_t vectors = vec ? (unit.end - unit.body) / V : 0;
-        if (vec) {
-            uint4 raw[per];
+        const int skew = (int)((out - (reinterpret_cast<uintptr_t>(dst + unit.body) & (out - 1))) % out / sizeof(U));
+        const int vectors = (int)((unit.end - unit.body) / V);
+        const int whole = skew ? (vectors ? vectors - 1 : 0) : vectors;      // stores
+        const int64_t from = whole ? unit.body + skew : unit.body, to = from + (int64_t)whole * V;
+        uint4 raw[per + 1];
 #pragma unroll
-            for (int k = 0; k < per; ++k) {
-                const int64_t at = (int64_t)k * 32 + lane;
-                raw[k] = make_uint4(0u, 0u, 0u, 0u);
-                if (at < vectors) raw[k] = *reinterpret_cast<const uint4 *>(src + unit.body + at * V);
-            }
+        for (int k = 0; k < per; ++k) {
+            const int at = k * 32 + lane;
+            raw[k] = make_uint4(0u, 0u, 0u, 0u);
+            if (at < vectors) raw[k] = __ldcs(reinterpret_cast<const uint4 *>(src + unit.body + at * V));
+        }
+        raw[per] = make_uint4(0u, 0u, 0u, 0u);
+        for (int64_t j = unit.begin + lane; j < from; j += 32) put(dst + j, (A)as_double<T>(src[j]) * factor);
+        for (int64_t j = to + lane; j < unit.end; j += 32) put(dst + j, (A)as_double<T>(src[j]) * factor);
 #pragma unroll
-            for (int k = 0; k < per; ++k) {
-                const int64_t at = (int64_t)k * 32 + lane;
-                if (at >= vectors) continue;
-                U *to = dst + unit.body + at * V;
-                if constexpr (sizeof(T) == 8) {
-                    *reinterpret_cast<double2 *>(to) =
-                        make_double2(__hiloint2double(raw[k].y, raw[k].x) * factor,
-                                     __hiloint2double(raw[k].w, raw[k].z) * factor);
-                } else {
-                    float v[V];
-                    unpack16<T>(v, raw[k]);
+        for (int k = 0; k < per; ++k) {
+            if (skew) shift_in(raw[k], raw[k + 1], lane, skew * (int)sizeof(T));
+            const int at = k * 32 + lane;
+            if (at >= whole) continue;
+            U *where = dst + from + at * V;
+            if constexpr (sizeof(T) == 8) {
+                __stcs(reinterpret_cast<double2 *>(where),
+                       make_double2(__hiloint2double(raw[k].y, raw[k].x) * factor,
+                                    __hiloint2double(raw[k].w, raw[k].z) * factor));
+            } else {
+                float v[V];
+                unpack16<T>(v, raw[k]);
 #pragma unroll
-                    for (int j = 0; j < V; ++j) v[j] *= factor;
-                    if constexpr (out == 32) store32(to, v);
-                    else *reinterpret_cast<uint4 *>(to) = pack16<U>(v);
-                }
-            }
-            for (int64_t j = unit.begin + lane; j < unit.body; j += 32) put(dst + j, (A)as_double<T>(src[j]) * factor);
-            for (int64_t j = unit.body + vectors * V + lane; j < unit.end; j += 32)
-                put(dst + j, (A)as_double<T>(src[j]) * factor);
-        } else {
-            // the destination's 16-byte boundaries lie elsewhere: entry by entry, 16 loads ahead
-            for (int64_t j = unit.begin + lane; j < unit.end; j += 32 * 16) {
-                T v[16];
-#pragma unroll
-                for (int k = 0; k < 16; ++k)
-                    if (j + 32 * k < unit.end) v[k] = src[j + 32 * k];
-#pragma unroll
-                for (int k = 0; k < 16; ++k)
-                    if (j + 32 * k < unit.end) put(dst + j + 32 * k, (A)as_double<T>(v[k]) * factor);
+                for (int j = 0; j < V; ++j) v[j] *= factor;
+                if constexpr (out == 32) store32(where, v);
+                else __stcs(reinterpret_cast<uint4 *>(where), pack16<U>(v));
             }
         }
     }
@@ -342,18 +362,26 @@ uint32_t units_for(int32_t dt, const void *src, int64_t size) {
     }
 }
 
-// Blocks of a launch over `units`: a warp per unit up to the machine's size,
-// then the count of blocks per SM that leaves the last round of units fullest.
+// Blocks of a launch over `units`: a warp per unit up to two blocks an SM; then
+// so many that a warp has about seven units, 3 to 16 blocks an SM, and of two
+// neighbouring counts the one that leaves the last round of units fuller.
+// Measured at 3, 5, 8, 12 and 16 blocks an SM: the norm of 60 million fp16
+// entries (29,000 units) takes 27.4, 28.5, 32.3, 35.9 and 39.6 us, clipping 300
+// million bf16 into fp32 (146,000 units) 437, 413, 409, 400 and 388 us: few
+// units a warp spend their time on the partial results, many end unevenly.
 int blocks_for(uint32_t units) {
-    const uint32_t warps = kNormThreads / 32, sms = 152;
-    if (units <= 2 * sms * warps) return (int)((units + warps - 1) / warps);
+    const uint32_t warps = kNormThreads / 32;
+    if (units <= 2 * kSMs * warps) return (int)((units + warps - 1) / warps);
+    uint32_t least = units / (kSMs * warps * 7);
+    least = least < 3 ? 3 : least > kMaxPerSM - 1 ? kMaxPerSM - 1 : least;
+    const uint32_t most = least == 3 ? 6 : least + 1;
     int best = 0;
-    uint64_t least = ~0ull;
-    for (uint32_t per_sm = 4; per_sm <= 6; ++per_sm) {
-        const uint64_t all = (uint64_t)per_sm * sms * warps, waste = (units + all - 1) / all * all - units;
-        if (waste < least) {
-            least = waste;
-            best = (int)(per_sm * sms);
+    uint64_t waste = ~0ull;
+    for (uint32_t per_sm = least; per_sm <= most; ++per_sm) {
+        const uint64_t all = (uint64_t)per_sm * kSMs * warps, left = (units + all - 1) / all * all - units;
+        if (left < waste) {
+            waste = left;
+            best = (int)(per_sm * kSMs);
         }
     }
     return best;
@@ -396,10 +424,21 @@ template <int N> const void *scale_kernel(int32_t dt, int32_t to, bool largest) 
 }
 
 // Fills tables with the tensors of one class, in the list's order, and hands
-// each to `run(table, units)`. Stops at the first error.
+// each to `run(table, blocks)`. Stops at the first error.
 template <int N, typename F>
-cudaError_t each_table(const msda_grad_list_t &l, int32_t from, int32_t to, F run) {
+cudaError_t each_table(const msda_grad_list_t &l, int32_t from, int32_t to, F run_blocks) {
     Table<N> t;
+    auto run = [&](Table<N> &t) {
+        const uint32_t units = t.before[t.count], per = kNormThreads / 32;
+        const int blocks = blocks_for(units);
+        int i = 0;
+        for (int b = 0; b < blocks; ++b) {
+            const uint32_t u = first_unit(units, blocks * per, b * per);
+            while (i + 1 < t.count && u >= t.before[i + 1]) ++i;
+            t.start[b] = (uint16_t)i;
+        }
+        return run_blocks(t, blocks);
+    };
     t.count = 0;
     t.before[0] = 0;
     for (int64_t i = 0; i < l.count; ++i) {
@@ -474,8 +513,7 @@ cudaError_t launch_parts(const msda_grad_list_t &l, const Summary &sum, bool lar
     *parts = 0;
     for (int32_t dt = 0; dt < kTypes; ++dt) {
         if (!sum.count[dt]) continue;
-        const cudaError_t e = each_table<N>(l, dt, -1, [&](Table<N> &t) {
-            const int blocks = blocks_for(t.before[t.count]);
+        const cudaError_t e = each_table<N>(l, dt, -1, [&](Table<N> &t, int blocks) {
             double *to = partial + *parts;
             void *args[] = {&t, &to, &err};
             *parts += blocks;
@@ -494,12 +532,12 @@ cudaError_t launch_scale(const msda_grad_list_t &l, const Summary &sum, bool lar
         for (int own = 0; own < 2; ++own) {
             if (!sum.count[dt] || !(own ? sum.to_own : sum.to_f32)[dt]) continue;
             const int32_t to = own ? dt : (int32_t)MSDA_F32;
-            const cudaError_t e = each_table<N>(l, dt, to, [&](Table<N> &t) {
+            const cudaError_t e = each_table<N>(l, dt, to, [&](Table<N> &t, int blocks) {
                 void *where = first ? norm : nullptr;
                 void *args[] = {&t, &partial, &parts, &max_norm, &where, &wide, &err};
                 const bool early = first;        // only this one follows the first kernel directly
                 first = false;
-                return launch(scale_kernel<N>(dt, to, largest), blocks_for(t.before[t.count]), args, early, stream);
+                return launch(scale_kernel<N>(dt, to, largest), blocks, args, early, stream);
             });
             if (e != cudaSuccess) return e;
         }

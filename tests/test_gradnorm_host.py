@@ -78,7 +78,7 @@ def test_workspace(so):
     one = need(Lists(sizes=(5,), dtypes=(0,)))
     assert one > 0 and need(Lists(sizes=(), dtypes=())) == one and need(Lists(sizes=(0,), dtypes=(0,))) == one
     assert need(Lists()) == 2 * one                          # two types with entries
-    assert need(Lists(sizes=[3] * 1025, dtypes=[1] * 1025)) == 2 * one
+    assert need(Lists(sizes=[3] * 961, dtypes=[1] * 961)) == 2 * one
     assert need(Lists(dtypes=(0, 9, 2))) == 0
     assert norm(so, Lists(), size=2 * one - 1) == 5
     assert clip(so, Lists(), size=2 * one - 1) == 5
