@@ -12,6 +12,10 @@ The four projections are ordinary dense matmuls (torch.nn.Linear, i.e.
 cuBLAS); the sampling, the softmax over the L*K logits and their backward run
 in libmsda's fused-softmax kernels. Offsets are in pixels of each level: the
 sampling location of (q, m, l, k) is reference[q, l] + offset / (W_l, H_l).
+
+A detector's encoder or decoder layer ends this sublayer in
+norm(input + sublayer(input)). With norm=True the layer does so itself: the
+residual is added on the way into libmsda's layer norm, forward and backward.
 """
 from __future__ import annotations
 
@@ -23,13 +27,32 @@ from torch import nn
 from . import binding
 
 
+class LayerNorm(nn.Module):
+    """Layer norm over the last dimension, of x + residual where a residual is given
+    (libmsda's kernels; binding.layer_norm). return_sum: (normalised, x + residual), what a
+    pre-norm stack passes on. weight and bias start at one and zero."""
+
+    def __init__(self, dim: int, eps: float = 1e-5, bias: bool = True):
+        super().__init__()
+        self.dim, self.eps = dim, eps
+        self.weight = nn.Parameter(torch.ones(dim))
+        self.bias = nn.Parameter(torch.zeros(dim)) if bias else None
+
+    def forward(self, x, residual=None, return_sum: bool = False):
+        return binding.layer_norm(x, self.weight, self.bias, residual=residual, eps=self.eps,
+                                  return_sum=return_sum)
+
+
 class MultiScaleDeformableAttention(nn.Module):
     """query (B, Q, dim), reference (B, Q, L, 2) or (B, Q, 2) normalised (x, y),
     value (B, S, dim), spatial_shapes (L, 2) int64 (H, W), level_start_index
-    (L,) int64 -> (B, Q, dim). dim = num_heads * head_dim."""
+    (L,) int64 -> (B, Q, dim). dim = num_heads * head_dim. norm=True: the output
+    is LayerNorm(residual + attention), residual (B, Q, dim) the query unless
+    given (a query with its position added is not what the layer adds to)."""
 
     def __init__(self, dim: int = 256, num_heads: int = 8, num_levels: int = 4,
-                 num_points: int = 4, accum: int = binding.MSDA_ACC_FP32_BUFFER):
+                 num_points: int = 4, accum: int = binding.MSDA_ACC_FP32_BUFFER,
+                 norm: bool = False):
         super().__init__()
         if dim % num_heads != 0:
             raise ValueError("dim must be divisible by num_heads")
@@ -41,6 +64,7 @@ class MultiScaleDeformableAttention(nn.Module):
         self.attention_weights = nn.Linear(dim, num_heads * num_levels * num_points)
         self.value_proj = nn.Linear(dim, dim)
         self.output_proj = nn.Linear(dim, dim)
+        self.norm = LayerNorm(dim) if norm else None
         self.reset_parameters()
 
     @torch.no_grad()
@@ -61,7 +85,9 @@ class MultiScaleDeformableAttention(nn.Module):
         nn.init.xavier_uniform_(self.output_proj.weight)
         nn.init.zeros_(self.output_proj.bias)
 
-    def forward(self, query, reference, value, spatial_shapes, level_start_index):
+    def forward(self, query, reference, value, spatial_shapes, level_start_index, residual=None):
+        if residual is not None and self.norm is None:
+            raise ValueError("a residual is added by a layer made with norm=True")
         B, Q, _ = query.shape
         S = value.shape[1]
         M, L, K, D = self.num_heads, self.num_levels, self.num_points, self.head_dim
@@ -74,4 +100,7 @@ class MultiScaleDeformableAttention(nn.Module):
         loc = reference[:, :, None, :, None, :].to(off.dtype) + off / wh[None, None, None, :, None, :]
         out = binding.multi_scale_deformable_attention(v, spatial_shapes, level_start_index, loc,
                                                        logits, accum=self.accum, softmax=True)
-        return self.output_proj(out)
+        out = self.output_proj(out)
+        if self.norm is None:
+            return out
+        return self.norm(out, residual=query if residual is None else residual)
