@@ -1,18 +1,21 @@
-// Layer norm's shared pieces: arguments, how a row is held and fetched, and
+// Layer norm's shared pieces: arguments, how rows are held and fetched, and
 // sums over the threads that hold one row. The kernels are in
-// msda_norm_forward.cu and msda_norm_backward.cu.
+// msda_norm_forward.cu and msda_norm_backward.cu, in three forms:
 //
-// A row of C channels lies in aligned 16-byte granules of V elements. It is
-// held by a group of threads, KV granules each: thread t of g has granules t,
-// t + g, ... of the row. A group is G = 2 to 32 lanes of one warp, or (G = 0)
-// some whole warps of a block. A block holds several groups.
+// rows   Rows that all start on 16-byte boundaries. A row lies in 16-byte
+//        granules of V elements and is held by a group of threads, KV granules
+//        each: thread t of g has granules t, t + g, ... A thread fetches what
+//        it will read itself.
+// tiles  Rows that start anywhere (C not a multiple of V, or a tensor off a
+//        16-byte boundary). Consecutive rows are one span of memory: a block
+//        fetches the granules a few rows touch into shared memory and its
+//        groups read their rows from there element by element, thread t having
+//        channels t, t + g, ..., E of them; the results go back the same way.
+// general  Rows of any length, in loops over memory: fp64, and rows too long
+//        for the registers.
 //
-// Rows that do not start on 16-byte boundaries (RAGGED: C not a multiple of V)
-// are held by the granules they touch: row r starts `phase` = r*C mod V
-// elements into its first one, and the elements of a granule that belong to a
-// neighbour are masked. A thread's rows are a multiple of V apart, so that its
-// phase, and with it its channels, stay the same from row to row. That keeps
-// the weights and the column sums of a thread in its registers.
+// A group is G = 2 to 32 lanes of one warp, or (G = 0) some whole warps of a
+// block; a block holds several groups.
 #pragma once
 
 #include "msda_common.cuh"
@@ -20,9 +23,8 @@
 namespace msda {
 
 constexpr int kSMs = 152;
-// threads of a block whose rows are held by lanes of a warp: the backward's
-// blocks are larger, since each leaves a row of partial sums
-constexpr int kForwardThreads = 128, kBackwardThreads = 256;
+// threads of a block whose groups are lanes of a warp: rows form, tiles form
+constexpr int kGroupThreads = 128, kTileThreads = 256;
 // dynamic shared memory a launch may ask for without raising the kernel's
 // limit: 48 KB less what the kernels declare themselves
 constexpr size_t kDefaultShared = 47 * 1024;
@@ -39,14 +41,16 @@ struct NormArgs {
     int64_t N;
     int C;
     int group;                     // threads of a group of warps (G = 0)
+    // tiles: rows of a group in a tile; tiles under way in shared memory, 2, or 1
+    // where two do not fit
+    int tile_rows, stages;
     unsigned *err;                 // checked build: device word of range faults
 };
 
 // How a problem's rows are held, chosen on the host.
 struct NormPlan {
-    bool general;      // the looping kernels: fp64, rows past the registers, odd pointers
-    bool ragged;
-    int G, KV;
+    enum Form { kRows, kTiles, kGeneral } form;
+    int G, KV;                     // KV: granules (rows) or pairs of channels (tiles) of a thread
     int group, threads, blocks;    // threads of a group and of a block
 };
 
@@ -102,17 +106,6 @@ __device__ __forceinline__ void load_params(float2 *v, const W *w, int c, float 
 #pragma unroll
     for (int i = 0; i < V / per; ++i) unpack_pairs<W>(v + i * per / 2, ldg16(p + i));
 }
-// The same for a masked granule: element by element, `fill` outside [0, C).
-template <typename W, int V>
-__device__ __forceinline__ void load_params_masked(float2 *v, const W *w, int c, int C, float fill) {
-#pragma unroll
-    for (int i = 0; i < V / 2; ++i) {
-        const int a = c + 2 * i, b = a + 1;
-        v[i].x = w && a >= 0 && a < C ? Elem<W>::to_f(w[a]) : fill;
-        v[i].y = w && b >= 0 && b < C ? Elem<W>::to_f(w[b]) : fill;
-    }
-}
-
 // ------------------------------------------------------------- row fetches
 // Asynchronous 16-byte copy of a granule to shared memory; `bytes` < 16 reads
 // only that many and fills the rest with zeros.
@@ -174,48 +167,37 @@ __device__ __forceinline__ void row_sum(float (&v)[R], BlockScratch<R> *scratch,
     }
 }
 
-// The place of a thread among the rows and of its granules in them. TH: threads
-// of a block whose rows are held by lanes of a warp.
-template <int G, int KV, int V, bool RAGGED, int TH> struct RowMap {
+// The place of a thread among the rows. TH: threads of a block whose groups are
+// lanes of a warp.
+template <int G, int TH> struct RowMap {
     int t, threads, index;         // of the group: this thread's place, its threads, its place in the block
+    int rows;                      // of a block at a time: its groups
     int64_t first, step, lead;     // the thread's rows; the first row of its warp
-    int phase, granules;           // granules a row of this phase touches
     __device__ __forceinline__ RowMap(const NormArgs &a) {
-        const int C = a.C;
         threads = G == 0 ? a.group : G;
         index = threadIdx.x / threads;
         t = threadIdx.x - index * threads;
-        const int per_block = G == 0 ? blockDim.x / threads : TH / threads;
-        first = (int64_t)blockIdx.x * per_block + index;
-        lead = G == 0 ? first : (int64_t)blockIdx.x * per_block + (threadIdx.x & ~31) / threads;
-        step = (int64_t)gridDim.x * per_block;
-        phase = RAGGED ? (int)((first & (V - 1)) * (C & (V - 1)) & (V - 1)) : 0;
-        granules = (phase + C + V - 1) / V;
+        rows = (G == 0 ? blockDim.x : TH) / threads;
+        first = (int64_t)blockIdx.x * rows + index;
+        lead = G == 0 ? first : (int64_t)blockIdx.x * rows + (threadIdx.x & ~31) / threads;
+        step = (int64_t)gridDim.x * rows;
     }
-    __device__ __forceinline__ int granule(int k) const { return k * threads + t; }
-    __device__ __forceinline__ bool held(int k) const { return granule(k) < granules; }
-    // the channel of granule k's element 0 (negative in a first granule shared with the row before)
-    __device__ __forceinline__ int channel(int k) const { return granule(k) * V - phase; }
-    // all of granule k's elements belong to the row
-    __device__ __forceinline__ bool whole(int k, int C) const {
-        return !RAGGED || (channel(k) >= 0 && channel(k) + V <= C);
-    }
-    __device__ __forceinline__ bool has(int k, int i, int C) const {
-        return !RAGGED || (channel(k) + i >= 0 && channel(k) + i < C);
-    }
-    // element offset of the thread's first granule in the tensor: a multiple of V
-    __device__ __forceinline__ int64_t start(int C) const { return first * C - phase + (int64_t)t * V; }
-    // A store at element `at` that leaves the neighbours' elements of a shared granule alone.
+};
+
+// The granules of a thread in its row (the rows form).
+template <int G, int V, int TH> struct GranuleMap : RowMap<G, TH> {
+    using RowMap<G, TH>::t;
+    using RowMap<G, TH>::threads;
+    using RowMap<G, TH>::first;
+    int granules;
+    __device__ __forceinline__ GranuleMap(const NormArgs &a) : RowMap<G, TH>(a), granules(a.C / V) {}
+    __device__ __forceinline__ bool held(int k) const { return k * threads + t < granules; }
+    __device__ __forceinline__ int channel(int k) const { return (k * threads + t) * V; }
+    // element offset of the thread's first granule in the tensor
+    __device__ __forceinline__ int64_t start(int C) const { return first * C + (int64_t)t * V; }
     template <typename T>
-    __device__ __forceinline__ void store(T *p, int64_t at, int k, int C, const float2 *v) const {
-        T *to = p + at + k * threads * V;
-        if (whole(k, C)) {
-            *reinterpret_cast<uint4 *>(to) = pack_pairs<T>(v);
-        } else {
-#pragma unroll
-            for (int i = 0; i < V; ++i)
-                if (has(k, i, C)) to[i] = Elem<T>::from_f(i & 1 ? v[i / 2].y : v[i / 2].x);
-        }
+    __device__ __forceinline__ void store(T *p, int64_t at, int k, const float2 *v) const {
+        *reinterpret_cast<uint4 *>(p + at + k * threads * V) = pack_pairs<T>(v);
     }
     // Starts the copy of granule k of the row at element `at` into `to`. Where
     // the thread has no such granule, or the row is past the last (!there), the
@@ -224,11 +206,112 @@ template <int G, int KV, int V, bool RAGGED, int TH> struct RowMap {
     __device__ __forceinline__ void fetch(uint4 *to, const T *p, int64_t at, int k, bool there, int64_t extent,
                                           unsigned *err) const {
         const int64_t off = at + k * threads * V;
-        there = there && held(k);
-        int n = RAGGED && off + V > extent ? (int)(extent - off) : V;
-        if (there && !span_ok(err, off, n, extent)) there = false;
-        fetch16(to, there ? p + off : p, there ? n * (int)sizeof(T) : 0);
+        there = there && held(k) && span_ok(err, off, V, extent);
+        fetch16(to, there ? p + off : p, there ? 16 : 0);
     }
 };
+
+// ------------------------------------------------------------------- tiles
+// Spans of a tensor's elements by the granules they touch: `lead(at)` elements
+// of the first granule come before the span.
+constexpr int kTileE = 16;               // channels of a thread, at most, but for the longest rows (32)
+template <typename T> struct Spans {
+    static constexpr int V = Vec16<T>::N;
+    T *base;
+    int64_t extent;
+    int phase;
+    __device__ __forceinline__ Spans(const void *tensor, int64_t extent)
+        : base(static_cast<T *>(const_cast<void *>(tensor))), extent(extent),
+          phase((int)(reinterpret_cast<uintptr_t>(tensor) / sizeof(T)) & (V - 1)) {}
+    __device__ __forceinline__ int lead(int64_t at) const { return (phase + (int)at) & (V - 1); }
+    // Starts the copies of the granules of n elements from `at` into shared
+    // memory. Elements of them outside the tensor are not read.
+    __device__ __forceinline__ void fetch(uint4 *to, int64_t at, int n, unsigned *err) const {
+        const int l = lead(at), granules = (l + n + V - 1) / V;
+        const int64_t from = at - l;
+        const T *p = base + from;
+        if (from >= 0 && from + granules * V <= extent) {
+            if (!span_ok(err, from, granules * V, extent)) return;
+            for (int i = threadIdx.x; i < granules; i += blockDim.x) fetch16(to + i, p + i * V, 16);
+            return;
+        }
+        for (int i = threadIdx.x; i < granules; i += blockDim.x) {      // the tensor's first or last tile
+            const int64_t off = from + i * V, left = extent - off;
+            const int m = left < V ? (int)left : V;
+            if (off >= 0) {
+                if (span_ok(err, off, m, extent)) fetch16(to + i, p + i * V, m * (int)sizeof(T));
+            } else {
+                for (int k = (int)-off; k < m; ++k) reinterpret_cast<T *>(to + i)[k] = p[i * V + k];
+            }
+        }
+    }
+    // Writes n elements from `at` out of shared memory: whole granules, and
+    // one by one the elements of a first and last that neighbours share.
+    __device__ __forceinline__ void store(const uint4 *from, int64_t at, int n, unsigned *err) const {
+        if (!span_ok(err, at, n, extent)) return;
+        const int l = lead(at), end = l + n, first = l ? 1 : 0, last = end / V;
+        T *p = base + (at - l);
+        const T *e = reinterpret_cast<const T *>(from);
+        for (int i = first + threadIdx.x; i < last; i += blockDim.x) reinterpret_cast<uint4 *>(p)[i] = from[i];
+        const int head = l + (int)threadIdx.x, tail = last * V + (int)threadIdx.x;
+        if (l && head < V && head < end) p[head] = e[head];
+        if (last >= first && tail < end) p[tail] = e[tail];
+    }
+};
+// 16-byte places that any span of n elements fits.
+template <typename T> constexpr __host__ __device__ int tile_places(int64_t n) {
+    return (int)((n + 2 * Vec16<T>::N - 2) / Vec16<T>::N);
+}
+
+// Rows of a group in a tile: up to four, in tiles of up to about 16 KB.
+inline int tile_rows(const NormArgs &a, const NormPlan &p, int bytes) {
+    const int64_t one = (int64_t)(p.threads / p.group) * a.C * bytes;
+    const int64_t n = 16384 / one, share = a.N / ((int64_t)p.blocks * (p.threads / p.group));
+    const int64_t most = share < 4 ? (share < 1 ? 1 : share) : 4;      // as many as leave every block its tile
+    return (int)(n < 1 ? 1 : n < most ? n : most);
+}
+
+// The tiles that fit beside `outs` results: two, or one, of `ins` tensors each.
+constexpr size_t kMostShared = 220 * 1024;
+constexpr int tile_stages(int ins, int outs, size_t bytes) {
+    return (size_t)(2 * ins + outs) * bytes <= kMostShared ? 2 : 1;
+}
+
+// A thread's channels t, t + g, ... as P pairs: pair i is channels t + 2i*g and
+// t + (2i + 1)*g. The group's size is such that all but the last two of six or
+// eight pairs lie in the row, half of sixteen and none of four; only the others
+// look at each channel. There are no branches around pairs: they would keep the
+// shared memory's reads apart.
+template <int P> constexpr int kWholePairs = P == 4 ? 0 : P == 16 ? 8 : P - 2;
+// With sixteen pairs a thread's registers do not hold its weights beside them.
+template <int P> constexpr bool kHoldsWeights = P <= 8;
+template <typename T, bool WHOLE>
+__device__ __forceinline__ float2 load_pair(const T *row, int c, int g, int C) {
+    if constexpr (WHOLE) return make_float2(Elem<T>::to_f(row[c]), Elem<T>::to_f(row[c + g]));
+    return make_float2(c < C ? Elem<T>::to_f(row[c]) : 0.0f, c + g < C ? Elem<T>::to_f(row[c + g]) : 0.0f);
+}
+template <int P, typename T>
+__device__ __forceinline__ void load_pairs(float2 (&v)[P], const T *row, int t, int g, int C) {
+    constexpr int W = kWholePairs<P>;
+#pragma unroll
+    for (int i = 0; i < W; ++i) v[i] = load_pair<T, true>(row, t + 2 * i * g, g, C);
+#pragma unroll
+    for (int i = W; i < P; ++i) v[i] = load_pair<T, false>(row, t + 2 * i * g, g, C);
+}
+template <int P, typename W>
+__device__ __forceinline__ void load_weights(float2 (&v)[P], const W *w, int t, int g, int C, float fill) {
+#pragma unroll
+    for (int i = 0; i < P; ++i) v[i] = both(fill);
+    if (w) load_pairs(v, w, t, g, C);
+}
+template <int P, typename T>
+__device__ __forceinline__ void store_pairs(T *row, int t, int g, int C, const float2 (&v)[P]) {
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+        const int c = t + 2 * i * g;
+        if (i < kWholePairs<P> || c < C) row[c] = Elem<T>::from_f(v[i].x);
+        if (i < kWholePairs<P> || c + g < C) row[c + g] = Elem<T>::from_f(v[i].y);
+    }
+}
 
 }  // namespace msda

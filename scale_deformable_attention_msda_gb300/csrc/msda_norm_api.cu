@@ -29,58 +29,105 @@ msda_status_t check(const msda_norm_dims_t *d, msda_dtype_t dt, msda_dtype_t pdt
     return MSDA_OK;
 }
 
-// How rows of C elements are held (see msda_norm.cuh). `aligned16`: every
-// tensor of rows starts on a 16-byte boundary. Two granules a thread: measured
-// against one, two, three and four on rows of 64 to 8192 channels, they were the
-// fastest or within 3% (one spends more on the row's sums, four leave too few
-// warps); rows past 512 * 2 granules take four.
-NormPlan row_plan(const msda_norm_dims_t &d, msda_dtype_t dt, bool aligned16, int threads) {
+// The longest rows of the tiles form. Forward: 32 channels for each of 512
+// threads, two tensors and two results in a block's shared memory. Backward: 16
+// channels; with 32 its sums leave the registers, and 1,249 rows of 12,001 bf16
+// take 127 us against the general form's 94.
+constexpr int64_t max_tile_columns(msda_dtype_t dt, bool backward) {
+    return backward ? 512 * msda::kTileE : dt == MSDA_F32 ? (int64_t)(msda::kMostShared / (4 * 4)) - 16 : 16384;
+}
+
+// Threads of a group of whole warps with room for `items` at `per` each.
+int warps_for(int64_t items, int per) { return (int)((items + per - 1) / per + 31) / 32 * 32; }
+
+// The rows form for rows of n granules, as measured on rows of 64 to 8192
+// channels at each of 2, 3 and 4 granules a thread. Fewer lanes a row spend less
+// on its sums, and idle lanes cost more than that. Lanes of a warp, up to 128
+// granules: two granules a thread, three where that leaves fewer lanes idle, four
+// past 96 (14,600 x 1024 bf16 forward: 12.2 us, two 15.0; 15,600 x 512 fp32
+// backward 19.7 us, two 21.9). The 16-bit backward, with twice the channels in a
+// granule and sums beside them, stays with two (14,600 x 1024: 21.8 us, four
+// 25.1), but for three just past 64 granules (23,000 x 640: 26.1 us, two 27.5).
+// Groups of warps: four granules, but two of the 16-bit backward's and of 16-bit
+// rows that would leave more than a tenth of the lanes idle (5,990 x 2504 forward:
+// 16.8 us, four 19.4; 3,000 x 5000: 18.1 us, four 14.7), while they hold the row.
+void hold_rows(int64_t n, bool narrow, bool backward, NormPlan *p) {
+    p->form = NormPlan::kRows;
+    int g = 2;
+    while (2 * g < n && g < 32) g *= 2;
+    const bool two = narrow && backward;
+    if (n <= (two ? 80 : 128)) {
+        p->KV = n <= 2 * g ? 2 : n <= 3 * g ? 3 : 4;
+        if (!two && p->KV == 2 && g > 2 && 2 * n <= 3 * g) {
+            g /= 2;
+            p->KV = 3;
+        }
+        p->G = p->group = g;
+        p->threads = msda::kGroupThreads;
+    } else {
+        const bool idle = 10 * n < 9 * 4 * warps_for(n, 4);
+        p->KV = narrow && n <= 1024 && (backward || idle) ? 2 : 4;
+        p->G = 0;
+        p->group = warps_for(n, p->KV);
+        p->threads = p->group >= 256 ? p->group : 256 / p->group * p->group;
+    }
+}
+
+// The tiles form: the fewest threads with at most 16 channels each (32 in the
+// longest rows); more than 8 each but for the shortest.
+void hold_tiles(int64_t C, NormPlan *p) {
+    p->form = NormPlan::kTiles;
+    const int64_t t = (C + msda::kTileE - 1) / msda::kTileE;
+    if (t <= 32) {
+        int g = 2;
+        while (g < t) g *= 2;
+        p->G = p->group = g;
+        p->threads = msda::kTileThreads;
+    } else {
+        p->G = 0;
+        p->group = t < 512 ? warps_for(C, msda::kTileE) : 512;
+        p->threads = p->group >= msda::kTileThreads ? p->group : msda::kTileThreads / p->group * p->group;
+    }
+    p->KV = C <= 8 * p->group ? 4 : C <= 12 * p->group ? 6 : C <= 16 * p->group ? 8 : 16;
+}
+
+// `aligned16`: every tensor of rows starts on a 16-byte boundary.
+NormPlan row_plan(const msda_norm_dims_t &d, msda_dtype_t dt, bool aligned16, bool backward) {
     NormPlan p = {};
     const int V = 16 / elem_bytes(dt);
-    p.ragged = d.C % V != 0;
-    // granules of a row, the most that any phase touches
-    const int64_t n = p.ragged ? (d.C + V - 1 + V - 1) / V : d.C / V;
-    p.KV = n <= 1024 ? 2 : 4;
-    if (dt == MSDA_F64 || !aligned16 || n > 2048) {
-        p.general = true;
-        return p;
-    }
-    if (n <= 64) {
-        p.G = n <= 4 ? 2 : n <= 8 ? 4 : n <= 16 ? 8 : n <= 32 ? 16 : 32;
-        p.group = p.G;
-        p.threads = threads;
+    if (dt != MSDA_F64 && d.C % V == 0 && aligned16 && d.C / V <= 2048) {
+        hold_rows(d.C / V, dt != MSDA_F32, backward, &p);
+    } else if (dt != MSDA_F64 && d.C <= max_tile_columns(dt, backward)) {
+        hold_tiles(d.C, &p);
     } else {
-        p.group = (int)((n + p.KV - 1) / p.KV + 31) / 32 * 32;
-        p.threads = p.group >= threads ? p.group : threads / p.group * p.group;
+        p.form = NormPlan::kGeneral;
+        p.group = p.threads = 512;
     }
     return p;
 }
 
-NormPlan forward_plan(const msda_norm_dims_t &d, msda_dtype_t dt, bool aligned16) {
-    NormPlan p = row_plan(d, dt, aligned16, msda::kForwardThreads);
-    if (p.general) {
-        p.threads = 512;
-        p.blocks = (int)(d.N < (1 << 30) ? d.N : (1 << 30));
-        return p;
-    }
+// Blocks for `per_sm` threads on each SM, or as many as there are rows for.
+int blocks_of(const msda_norm_dims_t &d, const NormPlan &p, int per_sm) {
     const int64_t per_block = p.threads / p.group, want = (d.N + per_block - 1) / per_block;
-    const int64_t cap = msda::kSMs * (1024 / p.threads);
-    p.blocks = (int)(want < cap ? want : cap);
+    const int64_t cap = msda::kSMs * (per_sm > p.threads ? per_sm / p.threads : 1);
+    return (int)(want < 1 ? 1 : want < cap ? want : cap);
+}
+
+// Where a thread has three or four granules of two rows under way, 512 threads of
+// an SM are enough; more of them share fewer rows each, and pay for their start.
+NormPlan forward_plan(const msda_norm_dims_t &d, msda_dtype_t dt, bool aligned16) {
+    NormPlan p = row_plan(d, dt, aligned16, false);
+    if (p.form == NormPlan::kGeneral) p.blocks = (int)(d.N < (1 << 30) ? d.N : (1 << 30));
+    else p.blocks = blocks_of(d, p, p.form == NormPlan::kRows && p.G > 0 && p.KV > 2 ? 512 : 1024);
     return p;
 }
 
 // The backward's blocks walk many rows each, since each leaves a row of
 // partial column sums (general: the count of row chunks).
 NormPlan backward_plan(const msda_norm_dims_t &d, msda_dtype_t dt, bool aligned16) {
-    NormPlan p = row_plan(d, dt, aligned16, msda::kBackwardThreads);
-    if (p.general) {
-        p.threads = 512;
-        p.blocks = (int)(d.N < 1 ? 1 : d.N < 256 ? d.N : 256);
-        return p;
-    }
-    const int64_t per_block = p.threads / p.group, want = (d.N + per_block - 1) / per_block;
-    const int64_t cap = msda::kSMs * (p.threads > 256 ? 1 : 512 / p.threads);
-    p.blocks = (int)(want < 1 ? 1 : want < cap ? want : cap);
+    NormPlan p = row_plan(d, dt, aligned16, true);
+    if (p.form == NormPlan::kGeneral) p.blocks = (int)(d.N < 1 ? 1 : d.N < 256 ? d.N : 256);
+    else p.blocks = blocks_of(d, p, 512);
     return p;
 }
 

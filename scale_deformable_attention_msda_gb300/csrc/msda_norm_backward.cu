@@ -12,9 +12,43 @@
 
 namespace msda {
 
+// Sum over the lanes of a warp that hold the same channels.
+template <int G> __device__ __forceinline__ float2 fold(float2 v) {
+#pragma unroll
+    for (int off = G; off < 32; off <<= 1) {
+        v.x += __shfl_xor_sync(0xffffffffu, v.x, off);
+        v.y += __shfl_xor_sync(0xffffffffu, v.y, off);
+    }
+    return v;
+}
+
+// The block's row of partial sums from those its writers left in shared memory;
+// a block that is the only one writes the gradients.
+template <typename W>
+__device__ __forceinline__ void leave_partials(const NormArgs &a, const float *columns, int writers) {
+    __syncthreads();
+    const int n = 2 * a.C;
+    auto column = [&](int j) {
+        float v = columns[j];
+        for (int i = 1; i < writers; ++i) v += columns[i * n + j];
+        return v;
+    };
+    if (gridDim.x > 1) {
+        float *mine = a.partial + (int64_t)blockIdx.x * n;
+#pragma unroll 4
+        for (int j = threadIdx.x; j < n; j += blockDim.x) mine[j] = column(j);
+        return;
+    }
+    W *gw = static_cast<W *>(a.grad_weight), *gb = static_cast<W *>(a.grad_bias);
+    for (int j = threadIdx.x; j < a.C; j += blockDim.x) {
+        if (gw) gw[j] = Elem<W>::from_f(column(j));
+        if (gb) gb[j] = Elem<W>::from_f(column(a.C + j));
+    }
+}
+
 // S: rows whose copies are under way while one is worked on. A thread copies
 // what it reads itself, so its own wait is all the order the copies need.
-template <typename T, typename W, int G, int KV, bool RAGGED, int S, int TH>
+template <typename T, typename W, int G, int KV, int S, int TH>
 __global__ void __launch_bounds__(TH) norm_backward_kernel(const NormArgs a) {
     constexpr int V = Vec16<T>::N, P = V / 2;
     __shared__ BlockScratch<2> scratch;
@@ -22,7 +56,7 @@ __global__ void __launch_bounds__(TH) norm_backward_kernel(const NormArgs a) {
     int turn = 0;
     cudaTriggerProgrammaticLaunchCompletion();   // the column kernel may be launched; it waits for this one's end
     const int C = a.C;
-    const RowMap<G, KV, V, RAGGED, TH> map(a);
+    const GranuleMap<G, V, TH> map(a);
     const T *x = static_cast<const T *>(a.x), *res = static_cast<const T *>(a.residual);
     const T *dy = static_cast<const T *>(a.grad_out), *ds = static_cast<const T *>(a.grad_sum);
     const W *w = static_cast<const W *>(a.weight);
@@ -56,8 +90,7 @@ __global__ void __launch_bounds__(TH) norm_backward_kernel(const NormArgs a) {
     for (int k = 0; k < KV; ++k) {
 #pragma unroll
         for (int i = 0; i < P; ++i) dw[k][i] = db[k][i] = both(0.0f);
-        if (RAGGED) load_params_masked<W, V>(pw[k], w, map.channel(k), C, 1.0f);
-        else load_params<W, V>(pw[k], map.held(k) ? w : nullptr, map.channel(k), 1.0f);
+        load_params<W, V>(pw[k], map.held(k) ? w : nullptr, map.channel(k), 1.0f);
     }
     float mu = 0.0f, rs = 0.0f;
     if (map.first < a.N) {
@@ -86,13 +119,6 @@ __global__ void __launch_bounds__(TH) norm_backward_kernel(const NormArgs a) {
 #pragma unroll
                 for (int i = 0; i < P; ++i) xh[k][i] = add2(xh[k][i], e[i]);
             }
-            if (RAGGED && !map.whole(k, C)) {      // a neighbour's elements: s = mean, grad_out = 0
-#pragma unroll
-                for (int i = 0; i < P; ++i) {
-                    if (!map.has(k, 2 * i, C)) { xh[k][i].x = m; g[k][i].x = 0.0f; }
-                    if (!map.has(k, 2 * i + 1, C)) { xh[k][i].y = m; g[k][i].y = 0.0f; }
-                }
-            }
 #pragma unroll
             for (int i = 0; i < P; ++i) {
                 xh[k][i] = mul2(add2(xh[k][i], both(-m)), both(r));
@@ -116,7 +142,7 @@ __global__ void __launch_bounds__(TH) norm_backward_kernel(const NormArgs a) {
                     g[k][i] = mul2(fma2(xh[k][i], c2, add2(g[k][i], c1)), both(r));
                     if (ds) g[k][i] = add2(g[k][i], e[i]);
                 }
-                if (valid && map.held(k)) map.store(dx, here, k, C, g[k]);
+                if (valid && map.held(k)) map.store(dx, here, k, g[k]);
             }
         }
         fetch(slot);
@@ -124,59 +150,170 @@ __global__ void __launch_bounds__(TH) norm_backward_kernel(const NormArgs a) {
     }
     fetch_wait<0>();
     if (!a.partial) return;
-    // the block's sums: each group leaves its own in shared memory, or, where
-    // all rows have the same phase, each warp after adding its groups' sums
-    constexpr bool FOLD = !RAGGED && G > 0 && G < 32;
+    // the block's sums: each group of warps leaves its own in shared memory,
+    // and each warp after adding its lanes' groups
+    constexpr bool FOLD = G > 0;
     if constexpr (FOLD) {
 #pragma unroll
         for (int k = 0; k < KV; ++k) {
 #pragma unroll
             for (int i = 0; i < P; ++i) {
-#pragma unroll
-                for (int off = G; off < 32; off <<= 1) {
-                    dw[k][i].x += __shfl_xor_sync(0xffffffffu, dw[k][i].x, off);
-                    dw[k][i].y += __shfl_xor_sync(0xffffffffu, dw[k][i].y, off);
-                    db[k][i].x += __shfl_xor_sync(0xffffffffu, db[k][i].x, off);
-                    db[k][i].y += __shfl_xor_sync(0xffffffffu, db[k][i].y, off);
-                }
+                dw[k][i] = fold<G>(dw[k][i]);
+                db[k][i] = fold<G>(db[k][i]);
             }
         }
     }
     __syncthreads();                     // the ring's space is used again
     float *columns = reinterpret_cast<float *>(ring);
-    const int writer = FOLD ? threadIdx.x >> 5 : map.index;
-    const int writers = FOLD ? blockDim.x >> 5 : blockDim.x / map.threads;
     if (!FOLD || (threadIdx.x & 31) < G) {
-        float *to = columns + writer * 2 * C;
+        float *to = columns + (FOLD ? threadIdx.x >> 5 : map.index) * 2 * C;
 #pragma unroll
         for (int k = 0; k < KV; ++k) {
             if (!map.held(k)) continue;
             const int c = map.channel(k);
-            if constexpr (!RAGGED) {
 #pragma unroll
-                for (int i = 0; i < P / 2; ++i) {
-                    reinterpret_cast<float4 *>(to + c)[i] =
-                        make_float4(dw[k][2 * i].x, dw[k][2 * i].y, dw[k][2 * i + 1].x, dw[k][2 * i + 1].y);
-                    reinterpret_cast<float4 *>(to + C + c)[i] =
-                        make_float4(db[k][2 * i].x, db[k][2 * i].y, db[k][2 * i + 1].x, db[k][2 * i + 1].y);
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    if (!map.has(k, i, C)) continue;
-                    to[c + i] = i & 1 ? dw[k][i / 2].y : dw[k][i / 2].x;
-                    to[C + c + i] = i & 1 ? db[k][i / 2].y : db[k][i / 2].x;
-                }
+            for (int i = 0; i < P / 2; ++i) {
+                reinterpret_cast<float4 *>(to + c)[i] =
+                    make_float4(dw[k][2 * i].x, dw[k][2 * i].y, dw[k][2 * i + 1].x, dw[k][2 * i + 1].y);
+                reinterpret_cast<float4 *>(to + C + c)[i] =
+                    make_float4(db[k][2 * i].x, db[k][2 * i].y, db[k][2 * i + 1].x, db[k][2 * i + 1].y);
             }
         }
     }
-    __syncthreads();
-    float *mine = a.partial + (int64_t)blockIdx.x * 2 * C;
-    for (int j = threadIdx.x; j < 2 * C; j += blockDim.x) {
-        float v = 0.0f;
-        for (int i = 0; i < writers; ++i) v += columns[i * 2 * C + j];
-        mine[j] = v;
+    leave_partials<W>(a, columns, FOLD ? blockDim.x >> 5 : map.rows);
+}
+
+// The tiles form: see msda_norm.cuh.
+template <typename T, typename W, int G, int P>
+__global__ void __launch_bounds__(G == 0 ? 512 : kTileThreads, G == 0 ? 1 : 2)
+norm_backward_tile_kernel(const NormArgs a) {
+    constexpr int TH = kTileThreads;
+    __shared__ BlockScratch<2> scratch;
+    extern __shared__ uint4 ring[];      // stages of (tensors, places), then grad_x; at the end (writers, 2, C) floats
+    int turn = 0;
+    cudaTriggerProgrammaticLaunchCompletion();
+    const int C = a.C;
+    const RowMap<G, TH> map(a);
+    const int g = map.threads, t = map.t;
+    const W *w = static_cast<const W *>(a.weight);
+    const float *mean = static_cast<const float *>(a.mean), *rstd = static_cast<const float *>(a.rstd);
+    const int64_t extent = a.N * C;
+    const float inv_C = 1.0f / (float)C;
+    const int tensors = 2 + (a.residual ? 1 : 0) + (a.grad_sum ? 1 : 0);
+    const int rows = map.rows * a.tile_rows, places = tile_places<T>((int64_t)rows * C);
+    uint4 *const outs = ring + a.stages * tensors * places;
+    const Spans<T> xs(a.x, extent), ys(a.grad_out, extent), rs(a.residual, extent), ds(a.grad_sum, extent),
+        os(a.grad_x, extent);
+    const int ds_at = (tensors - 1) * places;
+    const int64_t step = (int64_t)gridDim.x * rows;
+    auto fetch = [&](int64_t row, int stage) {
+        if (row < a.N) {
+            uint4 *to = ring + stage * tensors * places;
+            const int n = (int)(a.N - row < rows ? a.N - row : rows) * C;
+            xs.fetch(to, row * C, n, a.err);
+            ys.fetch(to + places, row * C, n, a.err);
+            if (a.residual) rs.fetch(to + 2 * places, row * C, n, a.err);
+            if (a.grad_sum) ds.fetch(to + ds_at, row * C, n, a.err);
+        }
+        fetch_commit();
+    };
+    const int64_t begin = (int64_t)blockIdx.x * rows;
+    fetch(begin, 0);
+    if (a.stages == 2) fetch(begin + step, 1);
+    float2 pw[P], dw[P], db[P];
+    load_weights(pw, w, t, g, C, 1.0f);
+#pragma unroll
+    for (int i = 0; i < P; ++i) dw[i] = db[i] = both(0.0f);
+    int stage = 0;
+    for (int64_t tile = begin; tile < a.N; tile += step) {
+        const int64_t at = tile * C;
+        const int there = (int)(a.N - tile < rows ? a.N - tile : rows);
+        float m = 0.0f, r = 0.0f;        // of the group's next row
+        if (map.index < there) {
+            m = __ldg(mean + tile + map.index);
+            r = __ldg(rstd + tile + map.index);
+        }
+        if (a.stages == 2) fetch_wait<1>();
+        else fetch_wait<0>();
+        __syncthreads();
+        const uint4 *in = ring + stage * tensors * places;
+        const T *x0 = reinterpret_cast<const T *>(in) + xs.lead(at);
+        const T *y0 = reinterpret_cast<const T *>(in + places) + ys.lead(at);
+        const T *r0 = reinterpret_cast<const T *>(in + 2 * places) + rs.lead(at);
+        const T *d0 = reinterpret_cast<const T *>(in + ds_at) + ds.lead(at);
+        T *o0 = reinterpret_cast<T *>(outs) + os.lead(at);
+        // groups take the tile's rows in turn; all make the same number of turns
+        for (int lead = 0; lead < there; lead += map.rows) {
+            const int row = lead + map.index, from = row * C;
+            const bool valid = row < there;
+            const float mu = m, rstd_row = r;
+            if (row + map.rows < there) {
+                m = __ldg(mean + tile + row + map.rows);
+                r = __ldg(rstd + tile + row + map.rows);
+            }
+            float2 xh[P], gy[P];
+            float2 v0 = both(0.0f), v1 = both(0.0f);
+            if (valid) {
+                load_pairs(xh, x0 + from, t, g, C);
+                if (a.residual) {
+                    float2 e[P];
+                    load_pairs(e, r0 + from, t, g, C);
+#pragma unroll
+                    for (int i = 0; i < P; ++i) xh[i] = add2(xh[i], e[i]);
+                }
+                load_pairs(gy, y0 + from, t, g, C);
+#pragma unroll
+                for (int i = 0; i < P; ++i) {
+                    xh[i] = mul2(add2(xh[i], both(-mu)), both(rstd_row));
+                    dw[i] = fma2(gy[i], xh[i], dw[i]);       // past the row grad_out is zero
+                    db[i] = add2(db[i], gy[i]);
+                    gy[i] = mul2(gy[i], pw[i]);
+                    v0 = add2(v0, gy[i]);
+                    v1 = fma2(gy[i], xh[i], v1);
+                }
+            }
+            float v[2] = {v0.x + v0.y, v1.x + v1.y};
+            row_sum<G>(v, &scratch, turn, g, map.index);
+            if (valid && a.grad_x) {
+                const float2 c1 = both(-v[0] * inv_C), c2 = both(-v[1] * inv_C);
+#pragma unroll
+                for (int i = 0; i < P; ++i)
+                    gy[i] = mul2(fma2(xh[i], c2, add2(gy[i], c1)), both(rstd_row));
+                if (a.grad_sum) {
+                    load_pairs(xh, d0 + from, t, g, C);
+#pragma unroll
+                    for (int i = 0; i < P; ++i) gy[i] = add2(gy[i], xh[i]);
+                }
+                store_pairs(o0 + from, t, g, C, gy);
+            }
+        }
+        __syncthreads();                 // the results are whole, the inputs used
+        fetch(tile + a.stages * step, stage);
+        stage ^= a.stages - 1;
+        if (a.grad_x) os.store(outs, at, there * C, a.err);
     }
+    fetch_wait<0>();
+    if (!a.partial) return;
+    constexpr bool FOLD = G > 0;
+    if constexpr (FOLD) {
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            dw[i] = fold<G>(dw[i]);
+            db[i] = fold<G>(db[i]);
+        }
+    }
+    __syncthreads();                     // the tiles' space is used again
+    float *columns = reinterpret_cast<float *>(ring);
+    if (!FOLD || (threadIdx.x & 31) < G) {
+        float *to = columns + (FOLD ? threadIdx.x >> 5 : map.index) * 2 * C;
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            const int c = t + 2 * i * g;
+            if (c < C) { to[c] = dw[i].x; to[C + c] = db[i].x; }
+            if (c + g < C) { to[c + g] = dw[i].y; to[C + c + g] = db[i].y; }
+        }
+    }
+    leave_partials<W>(a, columns, FOLD ? blockDim.x >> 5 : map.rows);
 }
 
 // grad_weight and grad_bias from the blocks' partial sums, added in a fixed
@@ -324,13 +461,11 @@ static cudaError_t launch_general(const NormArgs &a, const NormPlan &p, cudaStre
     return e != cudaSuccess ? e : launch_columns<W, A>(a, p.blocks, stream);
 }
 
-template <typename T, typename W, int G, int KV, bool RAGGED, int S, int TH>
-static cudaError_t launch_rows(const NormArgs &a, const NormPlan &p, cudaStream_t stream) {
-    auto kernel = norm_backward_kernel<T, W, G, KV, RAGGED, S, TH>;
-    const int tensors = 2 + (a.residual ? 1 : 0) + (a.grad_sum ? 1 : 0);
-    size_t smem = (size_t)S * tensors * KV * p.threads * 16;
+template <typename W>
+static cudaError_t launch(void (*kernel)(const NormArgs), const NormArgs &a, const NormPlan &p, size_t smem,
+                          cudaStream_t stream) {
     if (a.partial) {
-        const int writers = G > 0 && !RAGGED ? p.threads / 32 : p.threads / p.group;
+        const int writers = p.G > 0 ? p.threads / 32 : p.threads / p.group;
         const size_t columns = (size_t)writers * 2 * a.C * sizeof(float);
         smem = smem > columns ? smem : columns;
     }
@@ -340,23 +475,50 @@ static cudaError_t launch_rows(const NormArgs &a, const NormPlan &p, cudaStream_
     }
     kernel<<<p.blocks, p.threads, smem, stream>>>(a);
     const cudaError_t e = cudaGetLastError();
-    return e != cudaSuccess || !a.partial ? e : launch_columns<W, float>(a, p.blocks, stream);
+    return e != cudaSuccess || !a.partial || p.blocks == 1 ? e : launch_columns<W, float>(a, p.blocks, stream);
+}
+
+template <typename T, typename W, int G, int KV, int S, int TH>
+static cudaError_t launch_rows(const NormArgs &a, const NormPlan &p, cudaStream_t stream) {
+    const int tensors = 2 + (a.residual ? 1 : 0) + (a.grad_sum ? 1 : 0);
+    return launch<W>(norm_backward_kernel<T, W, G, KV, S, TH>, a, p, (size_t)S * tensors * KV * p.threads * 16,
+                     stream);
+}
+
+template <typename T, typename W, int G, int P>
+static cudaError_t launch_tiles(const NormArgs &a, const NormPlan &p, cudaStream_t stream) {
+    const int ins = 2 + (a.residual ? 1 : 0) + (a.grad_sum ? 1 : 0);
+    NormArgs b = a;
+    b.tile_rows = tile_rows(a, p, sizeof(T));
+    const size_t bytes = (size_t)tile_places<T>((int64_t)(p.threads / p.group) * b.tile_rows * a.C) * 16;
+    b.stages = tile_stages(ins, 1, bytes);
+    return launch<W>(norm_backward_tile_kernel<T, W, G, P>, b, p, (b.stages * ins + 1) * bytes, stream);
 }
 
 template <typename T, typename W>
 static cudaError_t launch_backward_t(const NormArgs &a, const NormPlan &p, cudaStream_t stream) {
-#define BWD(g, kv, r, s) \
-    if (p.G == g && p.KV == kv && p.ragged == r) return launch_rows<T, W, g, kv, r, s, g == 0 ? 512 : kBackwardThreads>(a, p, stream);
-    if (p.general) return launch_general<T, W>(a, p, stream);
-#ifdef NORM_TUNE
-    NORM_TUNE
-#else
-    BWD(2, 2, false, 2) BWD(4, 2, false, 2) BWD(8, 2, false, 2) BWD(16, 2, false, 2) BWD(32, 2, false, 2)
-    BWD(0, 2, false, 2) BWD(0, 4, false, 1)
-    BWD(2, 2, true, 2) BWD(4, 2, true, 2) BWD(8, 2, true, 2) BWD(16, 2, true, 2) BWD(32, 2, true, 2)
-    BWD(0, 2, true, 2) BWD(0, 4, true, 1)
-#endif
-#undef BWD
+#define ROWS(g, kv) \
+    if (p.G == g && p.KV == kv) return launch_rows<T, W, g, kv, 2, g == 0 ? 512 : kGroupThreads>(a, p, stream);
+#define TILES(g, pairs) \
+    if (p.G == g && p.KV == pairs) return launch_tiles<T, W, g, pairs>(a, p, stream);
+    if (p.form == NormPlan::kRows) {
+        ROWS(2, 2) ROWS(4, 2) ROWS(8, 2) ROWS(16, 2) ROWS(32, 2) ROWS(32, 3)
+        if constexpr (sizeof(T) == 4) {
+            ROWS(2, 3) ROWS(4, 3) ROWS(8, 3) ROWS(16, 3) ROWS(32, 4)
+            if (p.threads <= 384) { ROWS(0, 4) }
+        } else {
+            ROWS(0, 2)
+        }
+        // the longest rows: one row's copies are what fits
+        if (p.G == 0 && p.KV == 4) return launch_rows<T, W, 0, 4, 1, 512>(a, p, stream);
+    } else if (p.form == NormPlan::kTiles) {
+        TILES(2, 4) TILES(2, 6) TILES(2, 8) TILES(4, 6) TILES(4, 8) TILES(8, 6) TILES(8, 8) TILES(16, 6) TILES(16, 8)
+        TILES(32, 6) TILES(32, 8) TILES(0, 6) TILES(0, 8)
+    } else {
+        return launch_general<T, W>(a, p, stream);
+    }
+#undef ROWS
+#undef TILES
     return cudaErrorInvalidValue;
 }
 

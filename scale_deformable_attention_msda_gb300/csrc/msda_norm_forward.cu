@@ -10,14 +10,14 @@ namespace msda {
 
 // S: rows whose copies are under way while one is worked on. A thread copies
 // what it reads itself, so its own wait is all the order the copies need.
-template <typename T, typename W, int G, int KV, bool RAGGED, int S, int TH>
+template <typename T, typename W, int G, int KV, int S, int TH>
 __global__ void __launch_bounds__(TH) norm_forward_kernel(const NormArgs a) {
     constexpr int V = Vec16<T>::N, P = V / 2;
     __shared__ BlockScratch<1> scratch;
     extern __shared__ uint4 ring[];      // (S, tensors, KV, threads)
     int turn = 0;
     const int C = a.C;
-    const RowMap<G, KV, V, RAGGED, TH> map(a);
+    const GranuleMap<G, V, TH> map(a);
     const T *x = static_cast<const T *>(a.x), *res = static_cast<const T *>(a.residual);
     const W *w = static_cast<const W *>(a.weight), *b = static_cast<const W *>(a.bias);
     const int64_t extent = a.N * C, hop = map.step * C;
@@ -44,13 +44,8 @@ __global__ void __launch_bounds__(TH) norm_forward_kernel(const NormArgs a) {
 #pragma unroll
     for (int k = 0; k < KV; ++k) {
         const int c = map.channel(k);
-        if (RAGGED) {
-            load_params_masked<W, V>(pw[k], w, c, C, 1.0f);
-            load_params_masked<W, V>(pb[k], b, c, C, 0.0f);
-        } else {
-            load_params<W, V>(pw[k], map.held(k) ? w : nullptr, c, 1.0f);
-            load_params<W, V>(pb[k], map.held(k) ? b : nullptr, c, 0.0f);
-        }
+        load_params<W, V>(pw[k], map.held(k) ? w : nullptr, c, 1.0f);
+        load_params<W, V>(pb[k], map.held(k) ? b : nullptr, c, 0.0f);
     }
     for (int64_t row = map.first, lead = map.lead; lead < a.N; row += map.step, lead += map.step, here += hop) {
         const bool valid = G == 0 || G == 32 || row < a.N;
@@ -66,14 +61,7 @@ __global__ void __launch_bounds__(TH) norm_forward_kernel(const NormArgs a) {
 #pragma unroll
                 for (int i = 0; i < P; ++i) s[k][i] = add2(s[k][i], e[i]);
             }
-            if (a.sum && valid && map.held(k)) map.store(static_cast<T *>(a.sum), here, k, C, s[k]);
-            if (RAGGED && !map.whole(k, C)) {
-#pragma unroll
-                for (int i = 0; i < P; ++i) {
-                    if (!map.has(k, 2 * i, C)) s[k][i].x = 0.0f;
-                    if (!map.has(k, 2 * i + 1, C)) s[k][i].y = 0.0f;
-                }
-            }
+            if (a.sum && valid && map.held(k)) map.store(static_cast<T *>(a.sum), here, k, s[k]);
 #pragma unroll
             for (int i = 0; i < P; ++i) acc = add2(acc, s[k][i]);
         }
@@ -88,13 +76,6 @@ __global__ void __launch_bounds__(TH) norm_forward_kernel(const NormArgs a) {
             const float m = map.held(k) ? -mean : 0.0f;      // a slot without a granule stays zero
 #pragma unroll
             for (int i = 0; i < P; ++i) s[k][i] = add2(s[k][i], both(m));
-            if (RAGGED && !map.whole(k, C)) {
-#pragma unroll
-                for (int i = 0; i < P; ++i) {
-                    if (!map.has(k, 2 * i, C)) s[k][i].x = 0.0f;
-                    if (!map.has(k, 2 * i + 1, C)) s[k][i].y = 0.0f;
-                }
-            }
 #pragma unroll
             for (int i = 0; i < P; ++i) acc = fma2(s[k][i], s[k][i], acc);
         }
@@ -109,8 +90,116 @@ __global__ void __launch_bounds__(TH) norm_forward_kernel(const NormArgs a) {
         for (int k = 0; k < KV; ++k) {
 #pragma unroll
             for (int i = 0; i < P; ++i) s[k][i] = fma2(mul2(s[k][i], both(rstd)), pw[k][i], pb[k][i]);
-            if (valid && map.held(k)) map.store(static_cast<T *>(a.out), here, k, C, s[k]);
+            if (valid && map.held(k)) map.store(static_cast<T *>(a.out), here, k, s[k]);
         }
+    }
+    fetch_wait<0>();
+}
+
+// The tiles form: see msda_norm.cuh.
+template <typename T, typename W, int G, int P>
+__global__ void __launch_bounds__(G == 0 ? 512 : kTileThreads, G == 0 ? 1 : 3)
+norm_forward_tile_kernel(const NormArgs a) {
+    constexpr int TH = kTileThreads;
+    __shared__ BlockScratch<1> scratch;
+    extern __shared__ uint4 ring[];      // stages of (tensors, places), then out and sum
+    int turn = 0;
+    const int C = a.C;
+    const RowMap<G, TH> map(a);
+    const int g = map.threads, t = map.t;
+    const W *w = static_cast<const W *>(a.weight), *b = static_cast<const W *>(a.bias);
+    const int64_t extent = a.N * C;
+    const float inv_C = 1.0f / (float)C;
+    const int rows = map.rows * a.tile_rows;
+    const int tensors = a.residual ? 2 : 1, places = tile_places<T>((int64_t)rows * C);
+    uint4 *const outs = ring + a.stages * tensors * places;
+    const Spans<T> xs(a.x, extent), rs(a.residual, extent), os(a.out, extent), ss(a.sum, extent);
+    const int64_t step = (int64_t)gridDim.x * rows;
+    auto fetch = [&](int64_t row, int stage) {
+        if (row < a.N) {
+            uint4 *to = ring + stage * tensors * places;
+            const int n = (int)(a.N - row < rows ? a.N - row : rows) * C;
+            xs.fetch(to, row * C, n, a.err);
+            if (a.residual) rs.fetch(to + places, row * C, n, a.err);
+        }
+        fetch_commit();
+    };
+    const int64_t begin = (int64_t)blockIdx.x * rows;
+    fetch(begin, 0);
+    if (a.stages == 2) fetch(begin + step, 1);
+    constexpr int HELD = kHoldsWeights<P> ? P : 1;
+    float2 pw[HELD], pb[HELD];
+    if constexpr (kHoldsWeights<P>) {
+        load_weights(pw, w, t, g, C, 1.0f);
+        load_weights(pb, b, t, g, C, 0.0f);
+    }
+    int stage = 0;
+    for (int64_t tile = begin; tile < a.N; tile += step) {
+        const int64_t at = tile * C;
+        const int there = (int)(a.N - tile < rows ? a.N - tile : rows);
+        if (a.stages == 2) fetch_wait<1>();
+        else fetch_wait<0>();
+        __syncthreads();
+        const uint4 *in = ring + stage * tensors * places;
+        const T *x0 = reinterpret_cast<const T *>(in) + xs.lead(at);
+        const T *r0 = reinterpret_cast<const T *>(in + places) + rs.lead(at);
+        T *o0 = reinterpret_cast<T *>(outs) + os.lead(at), *s0 = reinterpret_cast<T *>(outs + places) + ss.lead(at);
+        // groups take the tile's rows in turn; all make the same number of turns
+        for (int lead = 0; lead < there; lead += map.rows) {
+            const int row = lead + map.index;
+            const bool valid = row < there;
+            const int from = (valid ? row : 0) * C;      // a group without a row repeats the first, unwritten
+            float2 s[P], acc = both(0.0f);
+            load_pairs(s, x0 + from, t, g, C);
+            if (a.residual) {
+                float2 e[P];
+                load_pairs(e, r0 + from, t, g, C);
+#pragma unroll
+                for (int i = 0; i < P; ++i) s[i] = add2(s[i], e[i]);
+            }
+            if (a.sum && valid) store_pairs(s0 + from, t, g, C, s);
+#pragma unroll
+            for (int i = 0; i < P; ++i) acc = add2(acc, s[i]);
+            float v[1] = {acc.x + acc.y};
+            row_sum<G>(v, &scratch, turn, g, map.index);
+            const float mean = v[0] * inv_C;
+            acc = both(0.0f);
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                const int c = t + 2 * i * g;
+                const bool whole = i < kWholePairs<P>;
+                s[i] = add2(s[i], make_float2(whole || c < C ? -mean : 0.0f, whole || c + g < C ? -mean : 0.0f));
+                acc = fma2(s[i], s[i], acc);
+            }
+            v[0] = acc.x + acc.y;
+            row_sum<G>(v, &scratch, turn, g, map.index);
+            const float rstd = rsqrtf(fmaf(v[0], inv_C, (float)a.eps));
+            if (!valid) continue;
+            if (t == 0 && a.mean && span_ok(a.err, tile + row, 1, a.N)) {
+                static_cast<float *>(a.mean)[tile + row] = mean;
+                static_cast<float *>(a.rstd)[tile + row] = rstd;
+            }
+#pragma unroll
+            for (int i = 0; i < P; ++i) s[i] = mul2(s[i], both(rstd));
+            if constexpr (kHoldsWeights<P>) {
+#pragma unroll
+                for (int i = 0; i < P; ++i) s[i] = fma2(s[i], pw[i], pb[i]);
+            } else {
+                float2 e[P];
+                load_weights(e, w, t, g, C, 1.0f);
+#pragma unroll
+                for (int i = 0; i < P; ++i) s[i] = mul2(s[i], e[i]);
+                load_weights(e, b, t, g, C, 0.0f);
+#pragma unroll
+                for (int i = 0; i < P; ++i) s[i] = add2(s[i], e[i]);
+            }
+            store_pairs(o0 + from, t, g, C, s);
+        }
+        __syncthreads();                 // the outputs are whole, the inputs used
+        fetch(tile + a.stages * step, stage);
+        stage ^= a.stages - 1;
+        os.store(outs, at, there * C, a.err);
+        if (a.sum) ss.store(outs + places, at, there * C, a.err);
     }
     fetch_wait<0>();
 }
@@ -134,9 +223,8 @@ template <typename A> __device__ __forceinline__ A block_sum(A v, A *scratch) {
     return v;
 }
 
-// Rows of any length and alignment, one block each, read three times (the
-// later reads hit the caches): fp64, rows too long for the registers, pointers
-// off a 16-byte boundary.
+// Rows of any length, one block each, read three times (the later reads hit
+// the caches).
 template <typename T, typename W>
 __global__ void __launch_bounds__(512) norm_forward_general_kernel(const NormArgs a) {
     using A = typename Acc<T>::type;
@@ -171,10 +259,9 @@ __global__ void __launch_bounds__(512) norm_forward_general_kernel(const NormArg
     }
 }
 
-template <typename T, typename W, int G, int KV, bool RAGGED, int S, int TH>
-static cudaError_t launch_rows(const NormArgs &a, const NormPlan &p, cudaStream_t stream) {
-    auto kernel = norm_forward_kernel<T, W, G, KV, RAGGED, S, TH>;
-    const size_t smem = (size_t)S * (a.residual ? 2 : 1) * KV * p.threads * 16;
+// A launch with `smem` bytes of dynamic shared memory.
+static cudaError_t launch(void (*kernel)(const NormArgs), const NormArgs &a, const NormPlan &p, size_t smem,
+                          cudaStream_t stream) {
     if (smem > kDefaultShared) {
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
@@ -183,23 +270,48 @@ static cudaError_t launch_rows(const NormArgs &a, const NormPlan &p, cudaStream_
     return cudaGetLastError();
 }
 
+template <typename T, typename W, int G, int KV, int S, int TH>
+static cudaError_t launch_rows(const NormArgs &a, const NormPlan &p, cudaStream_t stream) {
+    return launch(norm_forward_kernel<T, W, G, KV, S, TH>, a, p,
+                  (size_t)S * (a.residual ? 2 : 1) * KV * p.threads * 16, stream);
+}
+
+template <typename T, typename W, int G, int P>
+static cudaError_t launch_tiles(const NormArgs &a, const NormPlan &p, cudaStream_t stream) {
+    const int ins = a.residual ? 2 : 1, outs = a.sum ? 2 : 1;
+    NormArgs b = a;
+    b.tile_rows = tile_rows(a, p, sizeof(T));
+    const size_t bytes = (size_t)tile_places<T>((int64_t)(p.threads / p.group) * b.tile_rows * a.C) * 16;
+    b.stages = tile_stages(ins, outs, bytes);
+    return launch(norm_forward_tile_kernel<T, W, G, P>, b, p, (b.stages * ins + outs) * bytes, stream);
+}
+
 template <typename T, typename W>
 static cudaError_t launch_forward_t(const NormArgs &a, const NormPlan &p, cudaStream_t stream) {
-#define FWD(g, kv, r, s) \
-    if (p.G == g && p.KV == kv && p.ragged == r) return launch_rows<T, W, g, kv, r, s, g == 0 ? 512 : kForwardThreads>(a, p, stream);
-    if (p.general) {
-        norm_forward_general_kernel<T, W><<<p.blocks, p.threads, 0, stream>>>(a);
-        return cudaGetLastError();
+#define ROWS(g, kv) \
+    if (p.G == g && p.KV == kv) return launch_rows<T, W, g, kv, 2, kGroupThreads>(a, p, stream);
+#define TILES(g, pairs) \
+    if (p.G == g && p.KV == pairs) return launch_tiles<T, W, g, pairs>(a, p, stream);
+    if (p.form == NormPlan::kRows) {
+        ROWS(2, 2) ROWS(2, 3) ROWS(4, 2) ROWS(4, 3) ROWS(8, 2) ROWS(8, 3) ROWS(16, 2) ROWS(16, 3)
+        ROWS(32, 2) ROWS(32, 3) ROWS(32, 4)
+        if constexpr (sizeof(T) == 2) {
+            if (p.G == 0 && p.KV == 2) return launch_rows<T, W, 0, 2, 2, 512>(a, p, stream);
+        }
+        // Four granules: two rows under way, or one row of two tensors (4096 x
+        // 4096 fp32 with a residual and the sum: 41.8 us, two 43.1; 8000 x 1000
+        // without: 12.5 us, two 11.4).
+        if (p.G == 0 && p.KV == 4)
+            return a.residual || p.threads > 448 ? launch_rows<T, W, 0, 4, 1, 512>(a, p, stream)
+                                                 : launch_rows<T, W, 0, 4, 2, 512>(a, p, stream);
+    } else if (p.form == NormPlan::kTiles) {
+        TILES(2, 4) TILES(2, 6) TILES(2, 8) TILES(4, 6) TILES(4, 8) TILES(8, 6) TILES(8, 8) TILES(16, 6) TILES(16, 8)
+        TILES(32, 6) TILES(32, 8) TILES(0, 6) TILES(0, 8) TILES(0, 16)
+    } else {
+        return launch(norm_forward_general_kernel<T, W>, a, p, 0, stream);
     }
-#ifdef NORM_TUNE
-    NORM_TUNE
-#else
-    FWD(2, 2, false, 2) FWD(4, 2, false, 2) FWD(8, 2, false, 2) FWD(16, 2, false, 2) FWD(32, 2, false, 2)
-    FWD(0, 2, false, 2) FWD(0, 4, false, 1)
-    FWD(2, 2, true, 2) FWD(4, 2, true, 2) FWD(8, 2, true, 2) FWD(16, 2, true, 2) FWD(32, 2, true, 2)
-    FWD(0, 2, true, 2) FWD(0, 4, true, 1)
-#endif
-#undef FWD
+#undef ROWS
+#undef TILES
     return cudaErrorInvalidValue;
 }
 
@@ -213,8 +325,7 @@ cudaError_t launch_norm_forward(const NormArgs &a, const NormPlan &p, msda_dtype
         case MSDA_F16: return wide ? launch_forward_t<__half, float>(a, p, stream)
                                    : launch_forward_t<__half, __half>(a, p, stream);
         case MSDA_F64:
-            norm_forward_general_kernel<double, double><<<p.blocks, p.threads, 0, stream>>>(a);
-            return cudaGetLastError();
+            return launch(norm_forward_general_kernel<double, double>, a, p, 0, stream);
     }
     return cudaErrorInvalidValue;
 }

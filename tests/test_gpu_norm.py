@@ -54,7 +54,8 @@ def compare(x, w, b, r, dy, ds, total, eps=1e-5):
 # each way of holding a row, its first and last length, and lengths that no vector divides
 SIZES = [(1, 1), (3, 4), (5, 7), (2, 8), (2, 17), (37, 32), (9, 33), (70, 40), (64, 96), (11, 128), (13, 129),
          (7, 160), (33, 255), (600, 256), (19, 264), (5, 512), (4, 520), (3, 1024), (3, 1001),
-         (2, 2049), (2, 4096), (3, 4104), (3, 8192), (2, 8193), (2, 16384), (1, 16392), (2, 32776), (1, 70001)]
+         (2, 2049), (2, 4096), (3, 4104), (5, 6247), (4, 8191), (3, 8192), (2, 8193), (3, 11247), (3, 11249), (3, 12001), (2, 16383), (2, 16384), (1, 16392), (2, 32776),
+         (1, 70001)]
 
 
 @pytest.mark.parametrize("dt,pdt", TYPES, ids=IDS)
@@ -71,9 +72,32 @@ def test_many_rows(N, C, dt, pdt):
 
 
 @pytest.mark.parametrize("dt,pdt", TYPES, ids=IDS)
-@pytest.mark.parametrize("C", [8, 64, 256, 512, 4096])
+@pytest.mark.parametrize("C", [8, 64, 256, 512, 4096, 8192])
 def test_rows_off_a_16_byte_boundary(C, dt, pdt):
     compare(*operands(37, C, dt, pdt, residual=True, offset=1), total=True)
+
+
+@pytest.mark.parametrize("C", [1, 3, 25, 64, 777])
+def test_tensors_off_16_byte_boundaries_by_different_amounts(C):
+    """Every tensor starts at its own place in a 16-byte granule, the output too."""
+    for dt, pdt in ((BF16, F32), (F32, F32)):
+        x, w, b, r, dy, ds = operands(50, C, dt, pdt)
+        want = reference(x, w, b, r, 1e-5, dy, ds)
+
+        def moved(t, by):
+            flat = torch.full((t.numel() + 16,), 9.0, dtype=t.dtype, device="cuda")
+            flat[by:by + t.numel()] = t.flatten()
+            return flat, flat[by:by + t.numel()].view(t.shape)
+
+        (_, x), (_, r), (_, dy), (_, ds), (_, w) = (moved(t, by) for t, by in zip((x, r, dy, ds, w), (1, 2, 3, 5, 1)))
+        flat, out = moved(torch.zeros_like(x), 7)
+        _, s, mean, rstd = binding.msda_layer_norm_forward(x, w, b, r, 1e-5, True, out=out)
+        check("out", out, want["out"])
+        check("sum", s, want["sum"])
+        assert (flat[:7] == 9).all() and (flat[7 + out.numel():] == 9).all()
+        gx, gw, gb = binding.msda_layer_norm_backward(dy, x, mean, rstd, w, r, ds)
+        for name, g in (("grad_x", gx), ("grad_weight", gw), ("grad_bias", gb)):
+            check(name, g, want[name])
 
 
 @pytest.mark.parametrize("dt", [F32, BF16, F16, F64], ids=IDS)
@@ -299,8 +323,8 @@ def test_refusals():
 
 # --------------------------------------------------------- range-checked build
 
-@pytest.mark.parametrize("N,C", [(1, 1), (5, 7), (70, 40), (600, 256), (44446, 256), (9, 777), (19, 4104),
-                                 (2, 16384), (3, 32776)])
+@pytest.mark.parametrize("N,C", [(1, 1), (5, 7), (70, 40), (600, 256), (44446, 256), (9, 777), (1001, 33),
+                                 (19, 4104), (7, 8191), (3, 12001), (2, 16384), (3, 32776)])
 def test_accesses_stay_in_bounds(N, C):
     binding.use_library(build.CHECKED_LIBRARY)
     try:
