@@ -474,20 +474,23 @@ def _norm_forward(x, weight, bias, residual, eps, return_sum, stats, out, pdt):
     return out, total, stats
 
 
-def _norm_backward(grad_out, x, mean, rstd, weight, residual, grad_sum, pdt, want):
+def _norm_made(x, weight, pdt, want):
+    """(grad_weight, grad_bias) to be written, None where not wanted."""
+    return [None if not w else torch.empty(x.shape[-1], dtype=pdt, device=x.device)
+            if weight is None else torch.empty_like(weight) for w in want]
+
+
+def _norm_backward(grad_out, x, mean, rstd, weight, residual, grad_sum, pdt, want, made=None):
     """The launch, on the current device and stream, of operands already checked; mean and
-    rstd are addresses."""
+    rstd are addresses. `made`: grad_weight and grad_bias, if they are there already."""
     dims, dt = _norm_dims(x.numel(), x.shape[-1]), _DTYPES[x.dtype]
     grad_x = torch.empty_like(x) if want[0] else None
     grad_weight = grad_bias = workspace = None
     need = 0
     if want[1] or want[2]:
-        C, device = x.shape[-1], x.device
-        grads = [None if not w else torch.empty(C, dtype=pdt, device=device) if weight is None
-                 else torch.empty_like(weight) for w in want[1:]]
-        grad_weight, grad_bias = grads
-        need = _norm_workspace(x.numel(), C, dt)
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        grad_weight, grad_bias = made or _norm_made(x, weight, pdt, want[1:])
+        need = _norm_workspace(x.numel(), x.shape[-1], dt)
+        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
     status = lib().msda_layer_norm_backward(
         grad_out.data_ptr(), _at(grad_sum), x.data_ptr(), _at(residual), _at(weight),
         mean, rstd, _at(grad_x), _at(grad_weight), _at(grad_bias),
@@ -540,6 +543,30 @@ def msda_layer_norm_backward(grad_out, x, mean, rstd, weight=None, residual=None
     return _norm_backward(*args)
 
 
+def _norm_gradients(ctx, grad_out, grad_sum):
+    """What LayerNormFunction.backward returns. It runs on a thread of the engine's, where
+    every step costs more than on the caller's: the forward has prepared what it could."""
+    need_x, need_res, need_w, need_b, _, _ = ctx.needs_input_grad
+    if grad_sum is not None:
+        grad_sum = grad_sum.contiguous()
+    if grad_out is None:                 # the normalised rows were not used
+        gx = gw = gb = None
+        if need_x or need_res:
+            gx = grad_sum
+    else:
+        x, residual, weight, stats = ctx.saved_tensors
+        mean = stats.data_ptr()
+        args = (grad_out.contiguous(), x, mean, mean + stats.numel() // 2 * stats.element_size(),
+                weight, residual, grad_sum, ctx.param_dtype, (need_x or need_res, need_w, need_b))
+        made, ctx.made = ctx.made, None  # a second backward pass makes its own
+        if _elsewhere(x, None):
+            with _on(x.device, None):
+                gx, gw, gb = _norm_backward(*args, made)
+        else:
+            gx, gw, gb = _norm_backward(*args, made)
+    return gx if need_x else None, gx if need_res else None, gw, gb, None, None
+
+
 class LayerNormFunction(torch.autograd.Function):
     """Autograd wrapper of the two calls above (first derivatives only)."""
 
@@ -555,27 +582,16 @@ class LayerNormFunction(torch.autograd.Function):
             out, total, stats = _norm_forward(*args)
         ctx.save_for_backward(x, residual, weight, stats)
         ctx.set_materialize_grads(False)
+        ctx.made = _norm_made(x, weight, pdt, ctx.needs_input_grad[2:4])
         return (out, total) if return_sum else out
 
     @staticmethod
-    @torch.autograd.function.once_differentiable
     def backward(ctx, grad_out, grad_sum=None):
-        need_x, need_res, need_w, need_b, _, _ = ctx.needs_input_grad
-        if grad_sum is not None:
-            grad_sum = grad_sum.contiguous()
-        if grad_out is None:             # the normalised rows were not used
-            gx, gw, gb = grad_sum, None, None
-        else:
-            x, residual, weight, stats = ctx.saved_tensors
-            mean = stats.data_ptr()
-            args = (grad_out.contiguous(), x, mean, mean + stats.numel() // 2 * stats.element_size(),
-                    weight, residual, grad_sum, ctx.param_dtype, (need_x or need_res, need_w, need_b))
-            if _elsewhere(x, None):
-                with _on(x.device, None):
-                    gx, gw, gb = _norm_backward(*args)
-            else:
-                gx, gw, gb = _norm_backward(*args)
-        return gx if need_x else None, gx if need_res else None, gw, gb, None, None
+        if torch.is_grad_enabled():      # create_graph: second derivatives are an error, if asked for
+            return LayerNormFunction.backward_once(ctx, grad_out, grad_sum)
+        return _norm_gradients(ctx, grad_out, grad_sum)
+
+    backward_once = staticmethod(torch.autograd.function.once_differentiable(_norm_gradients))
 
 
 def layer_norm(x, weight=None, bias=None, residual=None, eps: float = 1e-5, return_sum: bool = False):
@@ -597,7 +613,14 @@ def layer_norm(x, weight=None, bias=None, residual=None, eps: float = 1e-5, retu
         grad = grad or bias.requires_grad
     if grad and torch.is_grad_enabled():
         return LayerNormFunction.apply(x, residual, weight, bias, eps, return_sum)
-    out, total, _, _ = msda_layer_norm_forward(x, weight, bias, residual, eps, return_sum, stats=False)
+    pdt = _param_dtype(x, weight, bias)
+    _norm_operands(x, (("residual", residual),), weight, bias, pdt)
+    args = (x, weight, bias, residual, eps, return_sum, False, None, pdt)
+    if _elsewhere(x, None):
+        with _on(x.device, None):
+            out, total, _ = _norm_forward(*args)
+    else:
+        out, total, _ = _norm_forward(*args)
     return (out, total) if return_sum else out
 
 

@@ -240,6 +240,18 @@ def test_autograd_takes_strides_broadcast_gradients_and_frozen_parameters():
     check("grad_weight", gw, reference(x, w, b, r, 1e-5, dy)["grad_weight"])
 
 
+def test_two_backward_passes_through_one_graph():
+    """The second gradients are tensors of their own."""
+    x, w, b, r, dy, ds = operands(60, 256, F32, F32)
+    leaves = [t.requires_grad_() for t in (x, r, w, b)]
+    out = binding.layer_norm(x, w, b, residual=r)
+    first = torch.autograd.grad(out, leaves, dy, retain_graph=True)
+    kept = [g.clone() for g in first]
+    second = torch.autograd.grad(out, leaves, 2 * dy)
+    for f, k, s in zip(first, kept, second):
+        assert torch.equal(f, k) and torch.equal(s, 2 * k) and f.data_ptr() != s.data_ptr()
+
+
 def test_second_derivatives_are_refused():
     x, w, b, r, dy, ds = operands(4, 8, F64, F64)
     x.requires_grad_()
