@@ -370,8 +370,10 @@ MSDA_API int msda_version(void);
 
 /* N rows of C channels, contiguous. Supported: N >= 0 (zero is a valid empty
  * call), 1 <= C <= 2^20, N*C <= 2^60. Every C and every element alignment is
- * accepted; rows that all start on 16-byte boundaries (C a multiple of
- * 16 / element size, pointers 16-byte aligned) are read in 16-byte vectors. */
+ * accepted. Rows that all start on 16-byte boundaries (C a multiple of
+ * 16 / element size, pointers 16-byte aligned) are the fastest; fp64, rows of
+ * over 8,192 fp32 or 16,384 16-bit channels, and in the backward other rows of
+ * over 8,192 channels, take plain loops. */
 typedef struct {
     int64_t N, C;
 } msda_norm_dims_t;
@@ -411,8 +413,8 @@ MSDA_API size_t msda_layer_norm_backward_workspace_bytes(const msda_norm_dims_t 
  *   grad_weight (C,)   = sum over rows of grad_out * xh, `param_dtype`
  *   grad_bias   (C,)   = sum over rows of grad_out, `param_dtype`
  * All three are OVERWRITTEN; any of them may be NULL. The column sums are held
- * in fp32 (fp64 for MSDA_F64) and added in an order that the sizes alone fix:
- * the same call gives the same bits. N = 0 writes zeros to grad_weight and
+ * in fp32 (fp64 for MSDA_F64) and added in an order that the sizes and the
+ * tensors' alignment fix: the same call gives the same bits. N = 0 writes zeros to grad_weight and
  * grad_bias.
  * workspace: at least msda_layer_norm_backward_workspace_bytes(...) bytes,
  *   16-byte aligned, owned by the caller, overwritten (may be NULL when

@@ -474,23 +474,20 @@ def _norm_forward(x, weight, bias, residual, eps, return_sum, stats, out, pdt):
     return out, total, stats
 
 
-def _norm_made(x, weight, pdt, want):
-    """(grad_weight, grad_bias) to be written, None where not wanted."""
-    return [None if not w else torch.empty(x.shape[-1], dtype=pdt, device=x.device)
-            if weight is None else torch.empty_like(weight) for w in want]
-
-
-def _norm_backward(grad_out, x, mean, rstd, weight, residual, grad_sum, pdt, want, made=None):
+def _norm_backward(grad_out, x, mean, rstd, weight, residual, grad_sum, pdt, want):
     """The launch, on the current device and stream, of operands already checked; mean and
-    rstd are addresses. `made`: grad_weight and grad_bias, if they are there already."""
+    rstd are addresses."""
     dims, dt = _norm_dims(x.numel(), x.shape[-1]), _DTYPES[x.dtype]
     grad_x = torch.empty_like(x) if want[0] else None
     grad_weight = grad_bias = workspace = None
     need = 0
     if want[1] or want[2]:
-        grad_weight, grad_bias = made or _norm_made(x, weight, pdt, want[1:])
-        need = _norm_workspace(x.numel(), x.shape[-1], dt)
-        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+        C, device = x.shape[-1], x.device
+        grad_weight, grad_bias = [
+            None if not w else torch.empty(C, dtype=pdt, device=device) if weight is None
+            else torch.empty_like(weight) for w in want[1:]]
+        need = _norm_workspace(x.numel(), C, dt)
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
     status = lib().msda_layer_norm_backward(
         grad_out.data_ptr(), _at(grad_sum), x.data_ptr(), _at(residual), _at(weight),
         mean, rstd, _at(grad_x), _at(grad_weight), _at(grad_bias),
@@ -544,8 +541,7 @@ def msda_layer_norm_backward(grad_out, x, mean, rstd, weight=None, residual=None
 
 
 def _norm_gradients(ctx, grad_out, grad_sum):
-    """What LayerNormFunction.backward returns. It runs on a thread of the engine's, where
-    every step costs more than on the caller's: the forward has prepared what it could."""
+    """What LayerNormFunction.backward returns."""
     need_x, need_res, need_w, need_b, _, _ = ctx.needs_input_grad
     if grad_sum is not None:
         grad_sum = grad_sum.contiguous()
@@ -558,12 +554,11 @@ def _norm_gradients(ctx, grad_out, grad_sum):
         mean = stats.data_ptr()
         args = (grad_out.contiguous(), x, mean, mean + stats.numel() // 2 * stats.element_size(),
                 weight, residual, grad_sum, ctx.param_dtype, (need_x or need_res, need_w, need_b))
-        made, ctx.made = ctx.made, None  # a second backward pass makes its own
         if _elsewhere(x, None):
             with _on(x.device, None):
-                gx, gw, gb = _norm_backward(*args, made)
+                gx, gw, gb = _norm_backward(*args)
         else:
-            gx, gw, gb = _norm_backward(*args, made)
+            gx, gw, gb = _norm_backward(*args)
     return gx if need_x else None, gx if need_res else None, gw, gb, None, None
 
 
@@ -582,7 +577,6 @@ class LayerNormFunction(torch.autograd.Function):
             out, total, stats = _norm_forward(*args)
         ctx.save_for_backward(x, residual, weight, stats)
         ctx.set_materialize_grads(False)
-        ctx.made = _norm_made(x, weight, pdt, ctx.needs_input_grad[2:4])
         return (out, total) if return_sum else out
 
     @staticmethod
@@ -736,7 +730,7 @@ def _grad_call(buf, kind, max_norm, stream):
     else:
         _call("msda_clip_grad_norm", lib().msda_clip_grad_norm(
             buf._ref, kind, max_norm, norm.data_ptr(), workspace.data_ptr(), buf.workspace_bytes, s))
-        torch._C._increment_version(buf._counted)
+        torch.autograd.graph.increment_version(buf._counted)
     return norm
 
 

@@ -223,7 +223,7 @@ template <typename T> struct Spans {
     __device__ __forceinline__ Spans(const void *tensor, int64_t extent)
         : base(static_cast<T *>(const_cast<void *>(tensor))), extent(extent),
           phase((int)(reinterpret_cast<uintptr_t>(tensor) / sizeof(T)) & (V - 1)) {}
-    __device__ __forceinline__ int lead(int64_t at) const { return (phase + (int)at) & (V - 1); }
+    __device__ __forceinline__ int lead(int64_t at) const { return (int)((unsigned)phase + (unsigned)at) & (V - 1); }
     // Starts the copies of the granules of n elements from `at` into shared
     // memory. Elements of them outside the tensor are not read.
     __device__ __forceinline__ void fetch(uint4 *to, int64_t at, int n, unsigned *err) const {

@@ -95,9 +95,11 @@ void hold_tiles(int64_t C, NormPlan *p) {
 NormPlan row_plan(const msda_norm_dims_t &d, msda_dtype_t dt, bool aligned16, bool backward) {
     NormPlan p = {};
     const int V = 16 / elem_bytes(dt);
-    if (dt != MSDA_F64 && d.C % V == 0 && aligned16 && d.C / V <= 2048) {
+    // no rows: the general form touches nothing of the tensors of rows
+    const bool general = dt == MSDA_F64 || d.N == 0;
+    if (!general && d.C % V == 0 && aligned16 && d.C / V <= 2048) {
         hold_rows(d.C / V, dt != MSDA_F32, backward, &p);
-    } else if (dt != MSDA_F64 && d.C <= max_tile_columns(dt, backward)) {
+    } else if (!general && d.C <= max_tile_columns(dt, backward)) {
         hold_tiles(d.C, &p);
     } else {
         p.form = NormPlan::kGeneral;

@@ -293,6 +293,54 @@ def test_another_stream_and_captured_graphs():
             assert all(torch.equal(p, q) for p, q in zip(o, w))
 
 
+@pytest.mark.parametrize("C", [256, 777])
+def test_graphed_forward_and_backward(C):
+    """Forward and backward captured as two graphs, as a training loop's callables are."""
+    from scale_deformable_attention_msda_gb300.layer import LayerNorm
+    x, w, b, r, dy, ds = operands(300, C, F32, F32)
+    m = LayerNorm(C).cuda()
+    with torch.no_grad():
+        m.weight.copy_(w)
+        m.bias.copy_(b)
+    sample = (torch.randn_like(x, requires_grad=True), torch.randn_like(x, requires_grad=True))
+    graphed = torch.cuda.make_graphed_callables(m, sample)
+    for k in range(3):
+        xs, rs = (x + k).requires_grad_(), r.clone().requires_grad_()
+        m.zero_grad(set_to_none=True)
+        graphed(xs, rs).backward(dy)
+        want = reference(xs, w, b, rs, 1e-5, dy)
+        for name, g in (("grad_x", xs.grad), ("grad_x", rs.grad), ("grad_weight", m.weight.grad),
+                        ("grad_bias", m.bias.grad)):
+            check(name, g, want[name])
+
+
+def test_two_threads_at_once():
+    import threading
+    sets = [operands(600, 256, BF16, F32), operands(900, 777, F16, F16, seed=1)]
+    want = [[t.clone() for t in run(*o, True)] for o in sets]
+    torch.cuda.synchronize()
+    got, errors = [None, None], []
+
+    def work(i):
+        try:
+            st = torch.cuda.Stream()
+            with torch.cuda.stream(st):
+                for _ in range(20):
+                    got[i] = run(*sets[i], True)
+            st.synchronize()
+        except Exception as e:
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
+    for g, w in zip(got, want):
+        assert all(torch.equal(p, q) for p, q in zip(g, w))
+
+
 # ------------------------------------------------------------------- refusals
 
 def test_refusals():
