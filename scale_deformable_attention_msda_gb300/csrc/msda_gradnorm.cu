@@ -11,6 +11,13 @@
 // adds them up in the same order (the norm has the same bits in all of them,
 // and from call to call) and scales its units, last to first: those the L2
 // still holds from the first kernel come first.
+//
+// What bounds it: memory, over two passes of the gradients. 300 million bf16
+// entries into fp32 take 392 us (2.4 GB with the second read, 6.1 TB/s); a
+// detector's 339 fp32 tensors, 163 MB, into another buffer 86 us (31 us and 55 us;
+// the L2 saves 49 of the second read's 163 MB); the largest of 60 million fp16
+// entries 28 us. A layer's ten tensors, 1.4 MB, take 7 us: two launches, each
+// waiting for one round of reads. (GB300, calls in a graph.)
 #include <float.h>
 
 #include <type_traits>

@@ -5,9 +5,20 @@
 //   grad_bias   = sum over the rows of grad_out
 //
 // One pass: while a row is in registers its threads add its part of the column
-// sums to fp32 registers of their own (a thread keeps the same channels for
-// all its rows), and a block leaves one row of partial sums for a second
-// kernel to add up in a fixed order. No atomics: results do not vary.
+// sums to fp32 registers of their own (a thread keeps the same channels for all
+// its rows). A block adds its threads' sums in shared memory and leaves one row of
+// partial sums, and a second kernel, launched while the first runs, adds those in
+// a fixed order. No atomics: results do not vary. A block that is alone writes the
+// gradients itself.
+//
+// What bounds it: memory and issue about evenly. 44,446 rows of 256 bf16 channels
+// with a residual take 18.0 us, the second kernel's 3 us among them (5.1 TB/s of
+// the data alone, 75% of the copy rate; the rows' kernel executes 180 instructions
+// a warp and row); 86,016 x 256 fp32 54.7 us (6.4 TB/s); 8192 x 4096 bf16 with both
+// gradients 55.9 us (6.0 TB/s); 20,011 x 777 fp16, whose rows start anywhere, 38 us.
+// 512 threads of an SM are what 128 registers each allow; with copies that hold no
+// registers they keep about 60 KB on the way. (GB300, calls in a graph, inputs
+// larger than L2.)
 #include "msda_norm.cuh"
 
 namespace msda {
@@ -46,8 +57,9 @@ __device__ __forceinline__ void leave_partials(const NormArgs &a, const float *c
     }
 }
 
-// S: rows whose copies are under way while one is worked on. A thread copies
-// what it reads itself, so its own wait is all the order the copies need.
+// The rows form: see msda_norm.cuh. S: rows whose copies are under way while one
+// is worked on. A thread copies what it reads itself, so its own wait is all the
+// order the copies need.
 template <typename T, typename W, int G, int KV, int S, int TH>
 __global__ void __launch_bounds__(TH) norm_backward_kernel(const NormArgs a) {
     constexpr int V = Vec16<T>::N, P = V / 2;
