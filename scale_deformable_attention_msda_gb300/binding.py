@@ -393,10 +393,9 @@ def _check_like(name, t, shape, dtype, device):
         raise ValueError(f"{name} is not contiguous: libmsda needs contiguous tensors")
 
 
-def _like(t, shape, dtype, device):
-    """The same question as _check_like's, without the answer's wording."""
-    return t is None or (t.dtype is dtype and t.shape == shape and t.device == device and
-                         t.is_contiguous())
+def _unlike(t, shape, dtype, device):
+    """Whether _check_like would raise for t, a tensor."""
+    return not (t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous())
 
 
 @functools.lru_cache(maxsize=256)
@@ -418,9 +417,10 @@ def _param_dtype(x, weight, bias, given=None):
     return pdt
 
 
-def _norm_operands(x, rows, weight, bias, pdt):
-    """Raise unless x is a contiguous CUDA tensor with a channel dimension, `rows` (by name)
-    are like it and weight and bias hold a value of type pdt for each channel."""
+def _norm_operands(x, weight, bias, pdt, **rows):
+    """Raise unless x is a contiguous CUDA tensor with a channel dimension, `rows` (by name;
+    None is passed over) are like it and weight and bias hold a value of type pdt for each
+    channel."""
     if not x.is_cuda:
         raise ValueError("libmsda runs on CUDA tensors only (no CPU path)")
     shape, dtype, device = x.shape, x.dtype, x.device
@@ -430,12 +430,13 @@ def _norm_operands(x, rows, weight, bias, pdt):
         raise ValueError(f"unsupported dtype {dtype}")
     if not x.is_contiguous():
         _check_like("x", x, shape, dtype, device)
-    for name, t in rows:
-        if not _like(t, shape, dtype, device):
+    for name, t in rows.items():
+        if t is not None and _unlike(t, shape, dtype, device):
             _check_like(name, t, shape, dtype, device)
-    for name, t in (("weight", weight), ("bias", bias)):
-        if not _like(t, shape[-1:], pdt, device):
-            _check_like(name, t, shape[-1:], pdt, device)
+    if weight is not None and _unlike(weight, shape[-1:], pdt, device):
+        _check_like("weight", weight, shape[-1:], pdt, device)
+    if bias is not None and _unlike(bias, shape[-1:], pdt, device):
+        _check_like("bias", bias, shape[-1:], pdt, device)
 
 
 def _apart(outs, ins):
@@ -466,8 +467,10 @@ def _norm_forward(x, weight, bias, residual, eps, return_sum, stats, out, pdt):
         mean = stats.data_ptr()
         rstd = mean + stats.numel() // 2 * stats.element_size()
     status = lib().msda_layer_norm_forward(
-        x.data_ptr(), _at(residual), _at(weight), _at(bias), out.data_ptr(), _at(total), mean, rstd,
-        eps, _norm_dims(x.numel(), x.shape[-1]), _DTYPES[x.dtype], _DTYPES[pdt],
+        x.data_ptr(), None if residual is None else residual.data_ptr(),
+        None if weight is None else weight.data_ptr(), None if bias is None else bias.data_ptr(),
+        out.data_ptr(), None if total is None else total.data_ptr(), mean, rstd, eps,
+        _norm_dims(x.numel(), x.shape[-1]), _DTYPES[x.dtype], _DTYPES[pdt],
         _current_stream(x.get_device()))
     if status:
         raise MSDAError(status, "msda_layer_norm_forward")
@@ -508,7 +511,7 @@ def msda_layer_norm_forward(x, weight=None, bias=None, residual=None, eps: float
     None unless return_sum, mean and rstd are None unless stats (the backward needs them).
     See msda_layer_norm_forward in include/msda.h."""
     pdt = _param_dtype(x, weight, bias)
-    _norm_operands(x, (("residual", residual), ("out", out)), weight, bias, pdt)
+    _norm_operands(x, weight, bias, pdt, residual=residual, out=out)
     if out is not None:
         _apart([out], [x, residual, weight, bias])
     args = (x, weight, bias, residual, eps, return_sum, stats, out, pdt)
@@ -529,10 +532,11 @@ def msda_layer_norm_backward(grad_out, x, mean, rstd, weight=None, residual=None
     x and of residual alike. param_dtype: the parameters' type where weight is None. See
     msda_layer_norm_backward in include/msda.h."""
     pdt = _param_dtype(x, weight, None, param_dtype)
-    _norm_operands(x, (("grad_out", grad_out), ("residual", residual), ("grad_sum", grad_sum)),
-                   weight, None, pdt)
-    for name, t in (("mean", mean), ("rstd", rstd)):
-        _check_like(name, t, x.shape[:-1], _stats_dtype(x), x.device)
+    _norm_operands(x, weight, None, pdt, grad_out=grad_out, residual=residual, grad_sum=grad_sum)
+    shape, sdt, device = x.shape[:-1], _stats_dtype(x), x.device
+    if _unlike(mean, shape, sdt, device) or _unlike(rstd, shape, sdt, device):
+        _check_like("mean", mean, shape, sdt, device)
+        _check_like("rstd", rstd, shape, sdt, device)
     args = (grad_out, x, mean.data_ptr(), rstd.data_ptr(), weight, residual, grad_sum, pdt, want)
     if _elsewhere(x, stream):
         with _on(x.device, stream):
@@ -568,7 +572,7 @@ class LayerNormFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, residual, weight, bias, eps, return_sum):
         pdt = ctx.param_dtype = _param_dtype(x, weight, bias)
-        _norm_operands(x, (("residual", residual),), weight, bias, pdt)
+        _norm_operands(x, weight, bias, pdt, residual=residual)
         args = (x, weight, bias, residual, eps, return_sum, True, None, pdt)
         if _elsewhere(x, None):
             with _on(x.device, None):
@@ -608,7 +612,7 @@ def layer_norm(x, weight=None, bias=None, residual=None, eps: float = 1e-5, retu
     if grad and torch.is_grad_enabled():
         return LayerNormFunction.apply(x, residual, weight, bias, eps, return_sum)
     pdt = _param_dtype(x, weight, bias)
-    _norm_operands(x, (("residual", residual),), weight, bias, pdt)
+    _norm_operands(x, weight, bias, pdt, residual=residual)
     args = (x, weight, bias, residual, eps, return_sum, False, None, pdt)
     if _elsewhere(x, None):
         with _on(x.device, None):

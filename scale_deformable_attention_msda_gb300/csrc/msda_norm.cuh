@@ -1,6 +1,6 @@
 // Layer norm's shared pieces: arguments, how rows are held and fetched, and
 // sums over the threads that hold one row. The kernels are in
-// msda_norm_forward.cu and msda_norm_backward.cu, in three forms:
+// msda_norm_forward.cuh and msda_norm_backward.cuh, in three forms:
 //
 // rows   Rows that all start on 16-byte boundaries. A row lies in 16-byte
 //        granules of V elements and is held by a group of threads, KV granules

@@ -3,10 +3,14 @@
 #include "msda_norm.cuh"
 
 namespace msda {
-cudaError_t launch_norm_forward(const NormArgs &a, const NormPlan &p, msda_dtype_t dt,
-                                msda_dtype_t pdt, cudaStream_t stream);
-cudaError_t launch_norm_backward(const NormArgs &a, const NormPlan &p, msda_dtype_t dt,
-                                 msda_dtype_t pdt, cudaStream_t stream);
+cudaError_t launch_norm_forward_f32(const NormArgs &a, const NormPlan &p, cudaStream_t stream);
+cudaError_t launch_norm_forward_f64(const NormArgs &a, const NormPlan &p, cudaStream_t stream);
+cudaError_t launch_norm_forward_bf16(const NormArgs &a, const NormPlan &p, bool wide, cudaStream_t stream);
+cudaError_t launch_norm_forward_f16(const NormArgs &a, const NormPlan &p, bool wide, cudaStream_t stream);
+cudaError_t launch_norm_backward_f32(const NormArgs &a, const NormPlan &p, cudaStream_t stream);
+cudaError_t launch_norm_backward_f64(const NormArgs &a, const NormPlan &p, cudaStream_t stream);
+cudaError_t launch_norm_backward_bf16(const NormArgs &a, const NormPlan &p, bool wide, cudaStream_t stream);
+cudaError_t launch_norm_backward_f16(const NormArgs &a, const NormPlan &p, bool wide, cudaStream_t stream);
 cudaError_t fault_word_for_launch(unsigned **err);
 }  // namespace msda
 
@@ -146,6 +150,28 @@ bool aligned16(const void *const *p, int count) {
     return true;
 }
 
+// Launches of a type checked before.
+cudaError_t launch_forward(const NormArgs &a, const NormPlan &p, msda_dtype_t dt, msda_dtype_t pdt,
+                           cudaStream_t stream) {
+    const bool wide = pdt == MSDA_F32;
+    switch (dt) {
+        case MSDA_F32: return msda::launch_norm_forward_f32(a, p, stream);
+        case MSDA_F64: return msda::launch_norm_forward_f64(a, p, stream);
+        case MSDA_BF16: return msda::launch_norm_forward_bf16(a, p, wide, stream);
+        default: return msda::launch_norm_forward_f16(a, p, wide, stream);
+    }
+}
+cudaError_t launch_backward(const NormArgs &a, const NormPlan &p, msda_dtype_t dt, msda_dtype_t pdt,
+                            cudaStream_t stream) {
+    const bool wide = pdt == MSDA_F32;
+    switch (dt) {
+        case MSDA_F32: return msda::launch_norm_backward_f32(a, p, stream);
+        case MSDA_F64: return msda::launch_norm_backward_f64(a, p, stream);
+        case MSDA_BF16: return msda::launch_norm_backward_bf16(a, p, wide, stream);
+        default: return msda::launch_norm_backward_f16(a, p, wide, stream);
+    }
+}
+
 msda_status_t from_cuda(cudaError_t e) { return e == cudaSuccess ? MSDA_OK : MSDA_ERR_CUDA; }
 
 }  // namespace
@@ -182,8 +208,7 @@ msda_status_t msda_layer_norm_forward(const void *x, const void *residual, const
     a.N = d.N;
     a.C = (int)d.C;
     a.group = p.group;
-    return from_cuda(msda::launch_norm_forward(a, p, dtype, param_dtype,
-                                               static_cast<cudaStream_t>(stream)));
+    return from_cuda(launch_forward(a, p, dtype, param_dtype, static_cast<cudaStream_t>(stream)));
 }
 
 size_t msda_layer_norm_backward_workspace_bytes(const msda_norm_dims_t *dims, msda_dtype_t dtype) {
@@ -230,8 +255,7 @@ msda_status_t msda_layer_norm_backward(const void *grad_out, const void *grad_su
     a.N = d.N;
     a.C = (int)d.C;
     a.group = p.group;
-    return from_cuda(msda::launch_norm_backward(a, p, dtype, param_dtype,
-                                                static_cast<cudaStream_t>(stream)));
+    return from_cuda(launch_backward(a, p, dtype, param_dtype, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

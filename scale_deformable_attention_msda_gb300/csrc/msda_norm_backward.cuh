@@ -13,12 +13,14 @@
 //
 // What bounds it: memory and issue about evenly. 44,446 rows of 256 bf16 channels
 // with a residual take 18.0 us, the second kernel's 3 us among them (5.1 TB/s of
-// the data alone, 75% of the copy rate; the rows' kernel executes 180 instructions
-// a warp and row); 86,016 x 256 fp32 54.7 us (6.4 TB/s); 8192 x 4096 bf16 with both
+// the data alone, 75% of the copy rate; the rows' kernel executes 180 warp
+// instructions a row); 86,016 x 256 fp32 54.7 us (6.4 TB/s); 8192 x 4096 bf16 with both
 // gradients 55.9 us (6.0 TB/s); 20,011 x 777 fp16, whose rows start anywhere, 38 us.
 // 512 threads of an SM are what 128 registers each allow; with copies that hold no
 // registers they keep about 60 KB on the way. (GB300, calls in a graph, inputs
 // larger than L2.)
+#pragma once
+
 #include "msda_norm.cuh"
 
 namespace msda {
@@ -531,20 +533,6 @@ static cudaError_t launch_backward_t(const NormArgs &a, const NormPlan &p, cudaS
     }
 #undef ROWS
 #undef TILES
-    return cudaErrorInvalidValue;
-}
-
-cudaError_t launch_norm_backward(const NormArgs &a, const NormPlan &p, msda_dtype_t dt,
-                                 msda_dtype_t pdt, cudaStream_t stream) {
-    const bool wide = pdt == MSDA_F32;
-    switch (dt) {
-        case MSDA_F32: return launch_backward_t<float, float>(a, p, stream);
-        case MSDA_BF16: return wide ? launch_backward_t<__nv_bfloat16, float>(a, p, stream)
-                                    : launch_backward_t<__nv_bfloat16, __nv_bfloat16>(a, p, stream);
-        case MSDA_F16: return wide ? launch_backward_t<__half, float>(a, p, stream)
-                                   : launch_backward_t<__half, __half>(a, p, stream);
-        case MSDA_F64: return launch_general<double, double>(a, p, stream);
-    }
     return cudaErrorInvalidValue;
 }
 

@@ -11,8 +11,10 @@
 // 86,016 x 256 fp32 41.7 us (6.3 TB/s); 8192 x 4096 bf16 with a residual and the
 // sum 44.6 us (6.0 TB/s). Rows that start anywhere are bound by instructions, an
 // element at a time from shared memory: 20,011 x 777 fp16 take 24.8 us (2.5 TB/s;
-// 380 instructions a warp and row). A few rows are bound by the launch: 300 x 256
+// 761 warp instructions a row). A few rows are bound by the launch: 300 x 256
 // 1.7 us, one row of 8192 3.3 us. (GB300, calls in a graph, inputs larger than L2.)
+#pragma once
+
 #include "msda_norm.cuh"
 
 namespace msda {
@@ -324,21 +326,6 @@ static cudaError_t launch_forward_t(const NormArgs &a, const NormPlan &p, cudaSt
     }
 #undef ROWS
 #undef TILES
-    return cudaErrorInvalidValue;
-}
-
-cudaError_t launch_norm_forward(const NormArgs &a, const NormPlan &p, msda_dtype_t dt,
-                                msda_dtype_t pdt, cudaStream_t stream) {
-    const bool wide = pdt == MSDA_F32;
-    switch (dt) {
-        case MSDA_F32: return launch_forward_t<float, float>(a, p, stream);
-        case MSDA_BF16: return wide ? launch_forward_t<__nv_bfloat16, float>(a, p, stream)
-                                    : launch_forward_t<__nv_bfloat16, __nv_bfloat16>(a, p, stream);
-        case MSDA_F16: return wide ? launch_forward_t<__half, float>(a, p, stream)
-                                   : launch_forward_t<__half, __half>(a, p, stream);
-        case MSDA_F64:
-            return launch(norm_forward_general_kernel<double, double>, a, p, 0, stream);
-    }
     return cudaErrorInvalidValue;
 }
 

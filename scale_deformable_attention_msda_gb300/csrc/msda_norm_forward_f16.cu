@@ -1,0 +1,12 @@
+// Layer norm's forward kernels for fp16 data (a unit of its own, so that the types
+// compile side by side).
+#include "msda_norm_forward.cuh"
+
+namespace msda {
+
+// wide: fp32 parameters.
+cudaError_t launch_norm_forward_f16(const NormArgs &a, const NormPlan &p, bool wide, cudaStream_t stream) {
+    return wide ? launch_forward_t<__half, float>(a, p, stream) : launch_forward_t<__half, __half>(a, p, stream);
+}
+
+}  // namespace msda
