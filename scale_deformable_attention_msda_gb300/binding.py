@@ -361,9 +361,8 @@ def _at(t):
     return None if t is None else t.data_ptr()
 
 
-def _current_stream(index):
-    """Handle of device `index`'s current stream (without building a Stream object)."""
-    return torch._C._cuda_getCurrentRawStream(index)
+# handle of a device's current stream by its index, without building a Stream object
+_current_stream = torch._C._cuda_getCurrentRawStream
 
 
 @contextlib.contextmanager
@@ -393,9 +392,10 @@ def _check_like(name, t, shape, dtype, device):
         raise ValueError(f"{name} is not contiguous: libmsda needs contiguous tensors")
 
 
-def _unlike(t, shape, dtype, device):
-    """Whether _check_like would raise for t, a tensor."""
-    return not (t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous())
+def _unlike(t, shape, dtype, index):
+    """Whether _check_like would raise for t, a tensor, beside one on CUDA device `index`."""
+    return not (t.dtype is dtype and t.get_device() == index and t.shape == shape and
+                t.is_contiguous())
 
 
 @functools.lru_cache(maxsize=256)
@@ -417,26 +417,30 @@ def _param_dtype(x, weight, bias, given=None):
     return pdt
 
 
-def _norm_operands(x, weight, bias, pdt, **rows):
-    """Raise unless x is a contiguous CUDA tensor with a channel dimension, `rows` (by name;
-    None is passed over) are like it and weight and bias hold a value of type pdt for each
-    channel."""
+def _norm_operands(x, weight, bias, pdt, residual, also=()):
+    """Raise unless x is a contiguous CUDA tensor with a channel dimension, the residual and
+    `also` (pairs of name and tensor) are like it or None, and weight and bias hold a value
+    of type pdt for each channel. Returns x's device index."""
+    index, shape, dtype = x.get_device(), x.shape, x.dtype
     if not x.is_cuda:
         raise ValueError("libmsda runs on CUDA tensors only (no CPU path)")
-    shape, dtype, device = x.shape, x.dtype, x.device
     if not shape:
         raise ValueError("x needs a channel dimension")
     if dtype not in _DTYPES:
         raise ValueError(f"unsupported dtype {dtype}")
     if not x.is_contiguous():
-        _check_like("x", x, shape, dtype, device)
-    for name, t in rows.items():
-        if t is not None and _unlike(t, shape, dtype, device):
-            _check_like(name, t, shape, dtype, device)
-    if weight is not None and _unlike(weight, shape[-1:], pdt, device):
-        _check_like("weight", weight, shape[-1:], pdt, device)
-    if bias is not None and _unlike(bias, shape[-1:], pdt, device):
-        _check_like("bias", bias, shape[-1:], pdt, device)
+        _check_like("x", x, shape, dtype, x.device)
+    if residual is not None and _unlike(residual, shape, dtype, index):
+        _check_like("residual", residual, shape, dtype, x.device)
+    for name, t in also:
+        if t is not None and _unlike(t, shape, dtype, index):
+            _check_like(name, t, shape, dtype, x.device)
+    channels = shape[-1:]
+    if weight is not None and _unlike(weight, channels, pdt, index):
+        _check_like("weight", weight, channels, pdt, x.device)
+    if bias is not None and _unlike(bias, channels, pdt, index):
+        _check_like("bias", bias, channels, pdt, x.device)
+    return index
 
 
 def _apart(outs, ins):
@@ -454,7 +458,7 @@ def _stats_dtype(x):
     return torch.float64 if x.dtype is torch.float64 else torch.float32
 
 
-def _norm_forward(x, weight, bias, residual, eps, return_sum, stats, out, pdt):
+def _norm_forward(x, weight, bias, residual, eps, return_sum, stats, out, pdt, index):
     """The launch, on the current device and stream, of operands already checked. `stats`:
     None, or True for (mean, rstd) as one tensor of two halves."""
     if out is None:
@@ -470,8 +474,7 @@ def _norm_forward(x, weight, bias, residual, eps, return_sum, stats, out, pdt):
         x.data_ptr(), None if residual is None else residual.data_ptr(),
         None if weight is None else weight.data_ptr(), None if bias is None else bias.data_ptr(),
         out.data_ptr(), None if total is None else total.data_ptr(), mean, rstd, eps,
-        _norm_dims(x.numel(), x.shape[-1]), _DTYPES[x.dtype], _DTYPES[pdt],
-        _current_stream(x.get_device()))
+        _norm_dims(x.numel(), x.shape[-1]), _DTYPES[x.dtype], _DTYPES[pdt], _current_stream(index))
     if status:
         raise MSDAError(status, "msda_layer_norm_forward")
     return out, total, stats
@@ -500,9 +503,9 @@ def _norm_backward(grad_out, x, mean, rstd, weight, residual, grad_sum, pdt, wan
     return grad_x, grad_weight, grad_bias
 
 
-def _elsewhere(x, stream):
+def _elsewhere(index, stream=None):
     """Whether the launch needs another device or stream than the current ones."""
-    return stream is not None or torch._C._cuda_getDevice() != x.get_device()
+    return stream is not None or torch._C._cuda_getDevice() != index
 
 
 def msda_layer_norm_forward(x, weight=None, bias=None, residual=None, eps: float = 1e-5,
@@ -511,11 +514,11 @@ def msda_layer_norm_forward(x, weight=None, bias=None, residual=None, eps: float
     None unless return_sum, mean and rstd are None unless stats (the backward needs them).
     See msda_layer_norm_forward in include/msda.h."""
     pdt = _param_dtype(x, weight, bias)
-    _norm_operands(x, weight, bias, pdt, residual=residual, out=out)
+    index = _norm_operands(x, weight, bias, pdt, residual, (("out", out),))
     if out is not None:
         _apart([out], [x, residual, weight, bias])
-    args = (x, weight, bias, residual, eps, return_sum, stats, out, pdt)
-    if _elsewhere(x, stream):
+    args = (x, weight, bias, residual, eps, return_sum, stats, out, pdt, index)
+    if _elsewhere(index, stream):
         with _on(x.device, stream):
             out, total, both = _norm_forward(*args)
     else:
@@ -532,13 +535,13 @@ def msda_layer_norm_backward(grad_out, x, mean, rstd, weight=None, residual=None
     x and of residual alike. param_dtype: the parameters' type where weight is None. See
     msda_layer_norm_backward in include/msda.h."""
     pdt = _param_dtype(x, weight, None, param_dtype)
-    _norm_operands(x, weight, None, pdt, grad_out=grad_out, residual=residual, grad_sum=grad_sum)
-    shape, sdt, device = x.shape[:-1], _stats_dtype(x), x.device
-    if _unlike(mean, shape, sdt, device) or _unlike(rstd, shape, sdt, device):
-        _check_like("mean", mean, shape, sdt, device)
-        _check_like("rstd", rstd, shape, sdt, device)
+    index = _norm_operands(x, weight, None, pdt, residual, (("grad_out", grad_out), ("grad_sum", grad_sum)))
+    shape, sdt = x.shape[:-1], _stats_dtype(x)
+    if _unlike(mean, shape, sdt, index) or _unlike(rstd, shape, sdt, index):
+        _check_like("mean", mean, shape, sdt, x.device)
+        _check_like("rstd", rstd, shape, sdt, x.device)
     args = (grad_out, x, mean.data_ptr(), rstd.data_ptr(), weight, residual, grad_sum, pdt, want)
-    if _elsewhere(x, stream):
+    if _elsewhere(index, stream):
         with _on(x.device, stream):
             return _norm_backward(*args)
     return _norm_backward(*args)
@@ -558,7 +561,7 @@ def _norm_gradients(ctx, grad_out, grad_sum):
         mean = stats.data_ptr()
         args = (grad_out.contiguous(), x, mean, mean + stats.numel() // 2 * stats.element_size(),
                 weight, residual, grad_sum, ctx.param_dtype, (need_x or need_res, need_w, need_b))
-        if _elsewhere(x, None):
+        if _elsewhere(x.get_device()):
             with _on(x.device, None):
                 gx, gw, gb = _norm_backward(*args)
         else:
@@ -572,9 +575,9 @@ class LayerNormFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, residual, weight, bias, eps, return_sum):
         pdt = ctx.param_dtype = _param_dtype(x, weight, bias)
-        _norm_operands(x, weight, bias, pdt, residual=residual)
-        args = (x, weight, bias, residual, eps, return_sum, True, None, pdt)
-        if _elsewhere(x, None):
+        index = _norm_operands(x, weight, bias, pdt, residual)
+        args = (x, weight, bias, residual, eps, return_sum, True, None, pdt, index)
+        if _elsewhere(index):
             with _on(x.device, None):
                 out, total, stats = _norm_forward(*args)
         else:
@@ -612,9 +615,9 @@ def layer_norm(x, weight=None, bias=None, residual=None, eps: float = 1e-5, retu
     if grad and torch.is_grad_enabled():
         return LayerNormFunction.apply(x, residual, weight, bias, eps, return_sum)
     pdt = _param_dtype(x, weight, bias)
-    _norm_operands(x, weight, bias, pdt, residual=residual)
-    args = (x, weight, bias, residual, eps, return_sum, False, None, pdt)
-    if _elsewhere(x, None):
+    index = _norm_operands(x, weight, bias, pdt, residual)
+    args = (x, weight, bias, residual, eps, return_sum, False, None, pdt, index)
+    if _elsewhere(index):
         with _on(x.device, None):
             out, total, _ = _norm_forward(*args)
     else:
