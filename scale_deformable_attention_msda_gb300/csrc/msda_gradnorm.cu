@@ -12,12 +12,20 @@
 // and from call to call) and scales its units, last to first: those the L2
 // still holds from the first kernel come first.
 //
+// A list of up to kSmallTable tensors and kSmallUnits units takes one launch of a
+// single cluster instead, whose blocks exchange their partial results through
+// distributed shared memory. A layer's ten tensors take 8.5 us so, 7.0 as two
+// launches in a graph, but a call from the host 15 us instead of 20; past a unit a
+// warp the cluster's 8 SMs are too few (512 units: 12.6 us).
+//
 // What bounds it: memory, over two passes of the gradients. 300 million bf16
-// entries into fp32 take 392 us (2.4 GB with the second read, 6.1 TB/s); a
-// detector's 339 fp32 tensors, 163 MB, into another buffer 86 us (31 us and 55 us;
-// the L2 saves 49 of the second read's 163 MB); the largest of 60 million fp16
-// entries 28 us. A layer's ten tensors, 1.4 MB, take 7 us: two launches, each
-// waiting for one round of reads. (GB300, calls in a graph.)
+// entries into fp32 take 385 us (2.4 GB with the second read, 6.2 TB/s); a
+// detector's 339 fp32 tensors, 163 MB, into another buffer 83 us (the L2 saves 49
+// of the second read's 163 MB), their norm alone 31 us; the largest of 60 million
+// fp16 entries 25 us. fp64 arithmetic is kept to a few additions per block: with
+// fp64 sums in every lane and a square root and a division in every thread, the
+// same calls took 392, 86, 34 and 29 us. (GB300, calls in a graph.)
+#include <cooperative_groups.h>
 #include <float.h>
 
 #include <type_traits>
@@ -35,6 +43,7 @@ constexpr int kNormThreads = 256;
 constexpr int kSMs = 152, kMaxPerSM = 16, kMaxBlocks = kSMs * kMaxPerSM;   // of one launch
 // tensors of a launch: its parameters, the table among them, may fill 32,764 bytes
 constexpr int kSmallTable = 64, kLargeTable = 960;
+constexpr int kSmallBlocks = 8, kSmallThreads = 1024, kSmallUnits = 256;
 constexpr int64_t kMaxEntries = (int64_t)1 << 38;   // of one tensor: its units fit 2^29
 
 // Tensors of a launch: source, destination, entries, and the units before each.
@@ -58,9 +67,9 @@ static_assert(sizeof(Table<kLargeTable>) <= 32764 - 64, "a launch's parameters")
 
 struct Run { uint32_t begin, end; };     // a warp's units
 
-template <int N> __device__ __forceinline__ Run warp_run(const Table<N> &t) {
-    const uint32_t units = t.before[t.count], warps = gridDim.x * (kNormThreads / 32);
-    const uint32_t w = blockIdx.x * (kNormThreads / 32) + threadIdx.x / 32;
+template <int N, int TH = kNormThreads> __device__ __forceinline__ Run warp_run(const Table<N> &t) {
+    const uint32_t units = t.before[t.count], warps = gridDim.x * (TH / 32);
+    const uint32_t w = blockIdx.x * (TH / 32) + threadIdx.x / 32;
     return Run{first_unit(units, warps, w), first_unit(units, warps, w + 1)};
 }
 
@@ -86,6 +95,18 @@ template <typename T> struct Unit {
     }
 };
 
+// Checked build: the unit lies in its tensor, and its tensor in the table.
+template <typename T>
+__device__ __forceinline__ bool unit_ok(const Unit<T> &u, int64_t size, int tensor, int count, unsigned *err) {
+#ifdef MSDA_CHECKED
+    const bool ok = u.begin >= 0 && u.end <= size && u.begin <= u.end && tensor >= 0 && tensor < count;
+    if (!ok && err) atomicOr(err, 1u);
+    return ok;
+#else
+    return true;
+#endif
+}
+
 template <typename T> __host__ __device__ uint32_t units_of(const void *src, int64_t size) {
     constexpr int64_t per = kUnitBytes / sizeof(T);
     const int64_t head = (16 - (reinterpret_cast<uintptr_t>(src) & 15)) % 16 / sizeof(T);
@@ -105,40 +126,65 @@ template <bool LARGEST> __device__ __forceinline__ double join(double a, double 
     return LARGEST ? larger(a, b) : a + b;
 }
 
-// One lane's part of a unit. Squares are added in fp32, 32 or 64 of them, and
-// these sums in fp64. Where such a sum is not finite, or so small that squares
-// lost digits (under 1e-36: 64 roundings of subnormals, 2^-150 each, are 2^-24 of
-// it) though not all entries are zero, they are squared and added in fp64 instead.
-template <typename T, bool LARGEST>
-__device__ __forceinline__ double lane_part(const T *src, const Unit<T> &u, int lane) {
-    constexpr int V = 16 / sizeof(T), per = kUnitBytes / 16 / 32;
-    double part = 0.0;
-    // entries before the first and after the last whole vector, at most V - 1 each
-    const int64_t vectors = (u.end - u.body) / V;
-    const int64_t tail = u.body + vectors * V;
-    for (int64_t i = u.begin + lane; i < u.body; i += 32) {
-        const double v = as_double<T>(src[i]);
-        part = LARGEST ? larger(part, fabs(v)) : part + v * v;
-    }
-    if (tail + lane < u.end) {
-        const double v = as_double<T>(src[tail + lane]);
-        part = LARGEST ? larger(part, fabs(v)) : part + v * v;
-    }
-    uint4 raw[per];
+// A lane's vectors of a unit, zeros where it has none. A whole unit's loads are
+// issued together: where each depends on a test of its own the compiler spreads
+// them out, and the norm of a detector's gradients takes 37.8 us instead of 30.7.
+template <int PER>
+__device__ __forceinline__ void load_unit(uint4 (&raw)[PER], const uint4 *from, int vectors, int lane) {
+    if (vectors == kUnitBytes / 16) {
 #pragma unroll
-    for (int k = 0; k < per; ++k) {
-        raw[k] = make_uint4(0u, 0u, 0u, 0u);
-        const int64_t at = (int64_t)k * 32 + lane;
-        if (at < vectors) raw[k] = ldg16(src + u.body + at * V);
+        for (int k = 0; k < kUnitBytes / 512; ++k) raw[k] = from[k * 32 + lane];
+        return;
     }
+#pragma unroll
+    for (int k = 0; k < kUnitBytes / 512; ++k) {
+        raw[k] = make_uint4(0u, 0u, 0u, 0u);
+        if (k * 32 + lane < vectors) raw[k] = from[k * 32 + lane];
+    }
+}
+
+// One lane's share of its warp's units. Of 16- and 32-bit entries the squares are
+// added in fp32, 34 or 66 of them, and these sums in a pair of fp32 with the error
+// of every addition carried along: fp64 runs at a sixtieth of fp32's rate here.
+// Where a unit's sum is not finite, or would leave that range later (1e30), or is
+// so small that squares lost digits (under 1e-36: 66 roundings of subnormals,
+// 2^-150 each, are 2^-24 of it) though not all entries are zero, the entries are
+// squared and added in fp64 instead. The largest entry is kept as the bits of its
+// absolute value, which order like the values, NaN above infinity.
+struct Share {
+    float hi = 0.0f, lo = 0.0f;
+    double wide = 0.0;
+    uint32_t top = 0u;
+    __device__ __forceinline__ void add(float v) {
+        const float s = hi + v, b = s - hi;
+        lo += (hi - (s - b)) + (v - b);
+        hi = s;
+    }
+};
+
+template <typename T> __device__ __forceinline__ uint32_t abs_bits(T v) {
+    return __float_as_uint(Elem<T>::to_f(v)) & 0x7fffffffu;
+}
+
+template <typename T, bool LARGEST>
+__device__ __forceinline__ void add_unit(Share &share, const T *src, const Unit<T> &u, int lane) {
+    constexpr int V = 16 / sizeof(T), per = kUnitBytes / 16 / 32;
+    const int vectors = (int)((u.end - u.body) / V);
+    uint4 raw[per];
+    load_unit(raw, reinterpret_cast<const uint4 *>(src + u.body), vectors, lane);
+    // before the first and after the last whole vector: at most V - 1 entries each
+    const int64_t head = u.begin + lane, tail = u.body + (int64_t)vectors * V + lane;
+    const bool has_head = head < u.body, has_tail = tail < u.end;
     if constexpr (sizeof(T) == 8) {
+        double a = has_head ? src[head] : 0.0, b = has_tail ? src[tail] : 0.0;
+        share.wide = LARGEST ? larger(larger(share.wide, fabs(a)), fabs(b)) : fma(a, a, fma(b, b, share.wide));
 #pragma unroll
         for (int k = 0; k < per; ++k) {
-            const double a = __hiloint2double(raw[k].y, raw[k].x), b = __hiloint2double(raw[k].w, raw[k].z);
-            part = LARGEST ? larger(larger(part, fabs(a)), fabs(b)) : fma(a, a, fma(b, b, part));
+            a = __hiloint2double(raw[k].y, raw[k].x);
+            b = __hiloint2double(raw[k].w, raw[k].z);
+            share.wide = LARGEST ? larger(larger(share.wide, fabs(a)), fabs(b)) : fma(a, a, fma(b, b, share.wide));
         }
     } else if constexpr (LARGEST) {
-        // the bits of |v| order like the values, NaN above infinity
         uint32_t top = 0u;
 #pragma unroll
         for (int k = 0; k < per; ++k) {
@@ -149,16 +195,17 @@ __device__ __forceinline__ double lane_part(const T *src, const Unit<T> &u, int 
                 else top = __vmaxu2(top, w[i] & 0x7fff7fffu);
             }
         }
-        T value;
-        if constexpr (sizeof(T) == 4) value = __uint_as_float(top);
-        else {
+        if constexpr (sizeof(T) == 2) {
             const unsigned short half = (unsigned short)max(top & 0xffffu, top >> 16);
-            value = *reinterpret_cast<const T *>(&half);
+            top = abs_bits(*reinterpret_cast<const T *>(&half));
         }
-        part = larger(part, as_double<T>(value));
+        if (has_head) top = max(top, abs_bits(src[head]));
+        if (has_tail) top = max(top, abs_bits(src[tail]));
+        share.top = max(share.top, top);
     } else {
-        float sum = 0.0f;
-        uint32_t any = 0u;
+        const float a = has_head ? Elem<T>::to_f(src[head]) : 0.0f, b = has_tail ? Elem<T>::to_f(src[tail]) : 0.0f;
+        float sum = fmaf(a, a, b * b);
+        uint32_t any = __float_as_uint(a) | __float_as_uint(b);
 #pragma unroll
         for (int k = 0; k < per; ++k) {
             float v[V];
@@ -167,27 +214,49 @@ __device__ __forceinline__ double lane_part(const T *src, const Unit<T> &u, int 
             for (int i = 0; i < V; ++i) sum = fmaf(v[i], v[i], sum);
             any |= raw[k].x | raw[k].y | raw[k].z | raw[k].w;
         }
-        if (sum >= 1e-36f && sum <= FLT_MAX) part += (double)sum;
-        else if ((any & (sizeof(T) == 4 ? 0x7fffffffu : 0x7fff7fffu)) != 0u) {
+        if (sum >= 1e-36f && sum <= 1e30f) {
+            share.add(sum);
+        } else if ((any & (sizeof(T) == 4 ? 0x7fffffffu : 0x7fff7fffu)) != 0u) {
+            double wide = (double)a * a + (double)b * b;
 #pragma unroll 1
             for (int k = 0; k < per; ++k) {
-                const int64_t at = (int64_t)k * 32 + lane;
+                const int at = k * 32 + lane;
                 if (at >= vectors) break;
 #pragma unroll 1
                 for (int i = 0; i < V; ++i) {
                     const double v = as_double<T>(src[u.body + at * V + i]);
-                    part += v * v;
+                    wide += v * v;
                 }
             }
+            share.wide += wide;
         }
     }
-    return part;
 }
 
-// Sum (or the largest) over a block, in thread 0 and its warp.
-template <bool LARGEST> __device__ __forceinline__ double block_join(double v, double *scratch) {
+// The shares of a warp's lanes, joined; in lane 0.
+template <typename T, bool LARGEST> __device__ __forceinline__ double warp_join(Share share) {
+    if constexpr (LARGEST && sizeof(T) != 8) {
+        return (double)__uint_as_float(__reduce_max_sync(0xffffffffu, share.top));
+    } else {
+        if (sizeof(T) != 8 && !__any_sync(0xffffffffu, share.wide != 0.0)) {
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) v = join<LARGEST>(v, __shfl_xor_sync(0xffffffffu, v, off));
+            for (int off = 16; off > 0; off >>= 1) {
+                const float hi = __shfl_xor_sync(0xffffffffu, share.hi, off);
+                const float lo = __shfl_xor_sync(0xffffffffu, share.lo, off);
+                share.add(hi);
+                share.lo += lo;
+            }
+            return (threadIdx.x & 31) == 0 ? (double)share.hi + (double)share.lo : 0.0;
+        }
+        double v = sizeof(T) == 8 ? share.wide : share.wide + ((double)share.hi + (double)share.lo);
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) v = join<LARGEST>(v, __shfl_xor_sync(0xffffffffu, v, off));
+        return v;
+    }
+}
+
+// What a block's warps found (each in its lane 0), joined; in thread 0.
+template <bool LARGEST> __device__ __forceinline__ double block_join(double v, double *scratch) {
     if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
     __syncthreads();
     if (threadIdx.x < 32) {
@@ -198,41 +267,60 @@ template <bool LARGEST> __device__ __forceinline__ double block_join(double v, d
     return v;
 }
 
+// A warp's units, joined; in lane 0.
 template <typename T, bool LARGEST, int N>
-__global__ void __launch_bounds__(kNormThreads)
-grad_part_kernel(const __grid_constant__ Table<N> t, double *partial, unsigned *err) {
-    __shared__ double scratch[32];
-    cudaTriggerProgrammaticLaunchCompletion();
-    const Run run = warp_run(t);
+__device__ __forceinline__ double run_part(const Table<N> &t, const Run &run, unsigned *err) {
     const int lane = threadIdx.x & 31;
-    double part = 0.0;
+    Share share;
     if (run.begin < run.end) {
         int i = tensor_of(t, run.begin);
         for (uint32_t u = run.begin; u < run.end; ++u) {
             while (u >= t.before[i + 1]) ++i;
             const T *src = static_cast<const T *>(t.src[i]);
             const Unit<T> unit(src, t.size[i], u - t.before[i]);
-#ifdef MSDA_CHECKED
-            if (unit.begin < 0 || unit.end > t.size[i] || unit.begin > unit.end || i >= t.count) {
-                if (err) atomicOr(err, 1u);
-                continue;
-            }
-#endif
-            part = join<LARGEST>(part, lane_part<T, LARGEST>(src, unit, lane));
+            if (!unit_ok(unit, t.size[i], i, t.count, err)) continue;
+            add_unit<T, LARGEST>(share, src, unit, lane);
         }
     }
-    part = block_join<LARGEST>(part, scratch);
+    return warp_join<T, LARGEST>(share);
+}
+
+template <typename T, bool LARGEST, int N>
+__global__ void __launch_bounds__(kNormThreads)
+grad_part_kernel(const __grid_constant__ Table<N> t, double *partial, unsigned *err) {
+    __shared__ double scratch[32];
+    cudaTriggerProgrammaticLaunchCompletion();
+    const double part = block_join<LARGEST>(run_part<T, LARGEST>(t, warp_run(t), err), scratch);
     if (threadIdx.x == 0) partial[blockIdx.x] = part;
 }
 
-// The norm from the partial results, in every thread of a block.
-template <bool LARGEST> __device__ __forceinline__ double norm_of(const double *partial, int count, double *scratch) {
+// The partial results of all blocks, joined in a fixed order; in the first warp.
+// All threads read, so that the reads wait for each other little, and few add:
+// fp64 is what every block's start waits for.
+template <bool LARGEST>
+__device__ __forceinline__ double join_all(const double *partial, int count, double (&scratch)[kNormThreads]) {
     double v = 0.0;
-    for (int i = threadIdx.x; i < count; i += blockDim.x) v = join<LARGEST>(v, partial[i]);
-    v = block_join<LARGEST>(v, scratch);
-    if (threadIdx.x == 0) scratch[0] = LARGEST ? v : sqrt(v);
+#pragma unroll 4
+    for (int i = threadIdx.x; i < count; i += kNormThreads) v = join<LARGEST>(v, partial[i]);
+    scratch[threadIdx.x] = v;
     __syncthreads();
-    return scratch[0];
+    if (threadIdx.x < 32) {
+        double a = v, b = scratch[threadIdx.x + kNormThreads / 2];
+#pragma unroll
+        for (int i = 32; i < kNormThreads / 2; i += 32) {
+            a = join<LARGEST>(a, scratch[threadIdx.x + i]);
+            b = join<LARGEST>(b, scratch[threadIdx.x + kNormThreads / 2 + i]);
+        }
+        v = join<LARGEST>(a, b);
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) v = join<LARGEST>(v, __shfl_xor_sync(0xffffffffu, v, off));
+    }
+    return v;
+}
+
+// The norm from what all blocks found (`total`), by one thread.
+template <bool LARGEST> __device__ __forceinline__ double norm_of(double total) {
+    return LARGEST ? total : sqrt(total);
 }
 
 __device__ __forceinline__ void write_norm(double norm, void *to, bool wide) {
@@ -243,10 +331,10 @@ __device__ __forceinline__ void write_norm(double norm, void *to, bool wide) {
 template <bool LARGEST>
 __global__ void __launch_bounds__(kNormThreads)
 grad_norm_kernel(const double *partial, int count, void *norm, bool wide) {
-    __shared__ double scratch[32];
+    __shared__ double scratch[kNormThreads];
     cudaGridDependencySynchronize();
-    const double n = norm_of<LARGEST>(partial, count, scratch);
-    if (threadIdx.x == 0) write_norm(n, norm, wide);
+    const double total = join_all<LARGEST>(partial, count, scratch);
+    if (threadIdx.x == 0) write_norm(norm_of<LARGEST>(total), norm, wide);
 }
 
 // 32 bytes in one store (the address a multiple of 32).
@@ -282,19 +370,18 @@ __device__ __forceinline__ void shift_in(uint4 &own, const uint4 &next, int lane
 template <typename T> __device__ __forceinline__ void put(T *to, float v) { *to = Elem<T>::from_f(v); }
 __device__ __forceinline__ void put(double *to, double v) { *to = v; }
 
-template <typename T, typename U, bool LARGEST, int N>
-__global__ void __launch_bounds__(kNormThreads)
-grad_scale_kernel(const __grid_constant__ Table<N> t, const double *partial, int count, double max_norm,
-                  void *norm, bool wide, unsigned *err) {
-    using A = typename std::conditional<sizeof(T) == 8, double, float>::type;
+// min(1, max_norm / (norm + 1e-6)); NaN stays NaN.
+template <typename T> using Factor = typename std::conditional<sizeof(T) == 8, double, float>::type;
+template <typename T> __device__ __forceinline__ Factor<T> factor_of(double max_norm, double norm) {
+    const double ratio = max_norm / (norm + 1e-6);
+    return (Factor<T>)(ratio > 1.0 ? 1.0 : ratio);
+}
+
+// A warp's units, last to first, times the factor.
+template <typename T, typename U, int N>
+__device__ __forceinline__ void run_scale(const Table<N> &t, const Run &run, Factor<T> factor, unsigned *err) {
+    using A = Factor<T>;
     constexpr int V = 16 / sizeof(T), per = kUnitBytes / 16 / 32;
-    __shared__ double scratch[32];
-    cudaGridDependencySynchronize();
-    const double total = norm_of<LARGEST>(partial, count, scratch);
-    if (norm && blockIdx.x == 0 && threadIdx.x == 0) write_norm(total, norm, wide);
-    const double ratio = max_norm / (total + 1e-6);
-    const A factor = (A)(ratio > 1.0 ? 1.0 : ratio);    // NaN stays NaN
-    const Run run = warp_run(t);
     if (run.begin >= run.end) return;
     const int lane = threadIdx.x & 31;
     int i = tensor_of(t, run.end - 1);
@@ -305,12 +392,7 @@ grad_scale_kernel(const __grid_constant__ Table<N> t, const double *partial, int
         U *dst = static_cast<U *>(t.dst[i]);
         if (factor == (A)1 && static_cast<const void *>(src) == static_cast<const void *>(dst)) continue;
         const Unit<T> unit(src, t.size[i], u - t.before[i]);
-#ifdef MSDA_CHECKED
-        if (unit.begin < 0 || unit.end > t.size[i] || unit.begin > unit.end || i < 0) {
-            if (err) atomicOr(err, 1u);
-            continue;
-        }
-#endif
+        if (!unit_ok(unit, t.size[i], i, t.count, err)) continue;
         // A source vector's entries go out in one store of 16 or 32 bytes. Where the
         // destination's boundaries lie `skew` entries after the source's, a store
         // takes entries of two source vectors, a lane's own and the next lane's.
@@ -349,6 +431,47 @@ grad_scale_kernel(const __grid_constant__ Table<N> t, const double *partial, int
             }
         }
     }
+}
+
+template <typename T, typename U, bool LARGEST, int N>
+__global__ void __launch_bounds__(kNormThreads)
+grad_scale_kernel(const __grid_constant__ Table<N> t, const double *partial, int count, double max_norm,
+                  void *norm, bool wide, unsigned *err) {
+    __shared__ double scratch[kNormThreads];
+    __shared__ Factor<T> factor;
+    cudaGridDependencySynchronize();
+    const double total = join_all<LARGEST>(partial, count, scratch);
+    if (threadIdx.x == 0) {
+        const double n = norm_of<LARGEST>(total);
+        if (norm && blockIdx.x == 0) write_norm(n, norm, wide);
+        factor = factor_of<T>(max_norm, n);
+    }
+    __syncthreads();
+    run_scale<T, U>(t, warp_run(t), factor, err);
+}
+
+// The whole of a small list in one cluster: the blocks' partial results are read
+// through distributed shared memory, in the same order by all.
+template <typename T, typename U, bool LARGEST>
+__global__ void __cluster_dims__(kSmallBlocks, 1, 1) __launch_bounds__(kSmallThreads)
+grad_small_kernel(const __grid_constant__ Table<kSmallTable> t, bool scale, double max_norm, void *norm, bool wide,
+                  unsigned *err) {
+    __shared__ double scratch[32], mine;
+    __shared__ Factor<T> factor;
+    const auto cluster = cooperative_groups::this_cluster();
+    const Run run = warp_run<kSmallTable, kSmallThreads>(t);
+    const double part = block_join<LARGEST>(run_part<T, LARGEST>(t, run, err), scratch);
+    if (threadIdx.x == 0) mine = part;
+    cluster.sync();
+    if (threadIdx.x == 0) {
+        double total = 0.0;
+        for (int b = 0; b < kSmallBlocks; ++b) total = join<LARGEST>(total, *cluster.map_shared_rank(&mine, b));
+        const double n = norm_of<LARGEST>(total);
+        if (blockIdx.x == 0) write_norm(n, norm, wide);
+        factor = factor_of<T>(max_norm, n);
+    }
+    cluster.sync();                      // no block leaves while another reads its part
+    if (scale) run_scale<T, U>(t, run, factor, err);
 }
 
 // ----------------------------------------------------------------- launches
@@ -430,39 +553,50 @@ template <int N> const void *scale_kernel(int32_t dt, int32_t to, bool largest) 
     return to == MSDA_F32 ? scale_kernel<__half, float, N>(largest) : scale_kernel<__half, __half, N>(largest);
 }
 
-// Fills tables with the tensors of one class, in the list's order, and hands
-// each to `run(table, blocks)`. Stops at the first error.
-template <int N, typename F>
-cudaError_t each_table(const msda_grad_list_t &l, int32_t from, int32_t to, F run_blocks) {
-    Table<N> t;
-    auto run = [&](Table<N> &t) {
-        const uint32_t units = t.before[t.count], per = kNormThreads / 32;
-        const int blocks = blocks_for(units);
-        int i = 0;
-        for (int b = 0; b < blocks; ++b) {
-            const uint32_t u = first_unit(units, blocks * per, b * per);
-            while (i + 1 < t.count && u >= t.before[i + 1]) ++i;
-            t.start[b] = (uint16_t)i;
-        }
-        return run_blocks(t, blocks);
-    };
-    t.count = 0;
-    t.before[0] = 0;
-    for (int64_t i = 0; i < l.count; ++i) {
+// Adds the tensors of one class to a table, in the list's order from tensor i,
+// until it is full; returns the tensor to go on from.
+template <int N>
+int64_t fill(const msda_grad_list_t &l, int32_t from, int32_t to, int64_t i, Table<N> *t) {
+    t->count = 0;
+    t->before[0] = 0;
+    for (; i < l.count; ++i) {
         if (!in_class(l, i, from, to)) continue;
         const uint32_t units = units_for(from, l.grads[i], l.sizes[i]);
-        if (t.count == N || units > 0x7fffffffu - t.before[t.count]) {
-            const cudaError_t e = run(t);
-            if (e != cudaSuccess) return e;
-            t.count = 0;
-        }
-        t.src[t.count] = l.grads[i];
-        t.dst[t.count] = to < 0 ? nullptr : l.outs[i];
-        t.size[t.count] = l.sizes[i];
-        t.before[t.count + 1] = t.before[t.count] + units;
-        ++t.count;
+        if (t->count == N || units > 0x7fffffffu - t->before[t->count]) break;
+        t->src[t->count] = l.grads[i];
+        t->dst[t->count] = to < 0 ? nullptr : l.outs[i];
+        t->size[t->count] = l.sizes[i];
+        t->before[t->count + 1] = t->before[t->count] + units;
+        ++t->count;
     }
-    return t.count ? run(t) : cudaSuccess;
+    return i;
+}
+
+// The tensors in which the first units of the blocks, of `per` warps, lie.
+template <int N> void set_starts(Table<N> &t, int blocks, uint32_t per) {
+    const uint32_t units = t.before[t.count];
+    int i = 0;
+    for (int b = 0; b < blocks; ++b) {
+        const uint32_t u = first_unit(units, blocks * per, b * per);
+        while (i + 1 < t.count && u >= t.before[i + 1]) ++i;
+        t.start[b] = (uint16_t)i;
+    }
+}
+
+// Hands the tensors of one class to `run(table, blocks)`, a table at a time.
+// Stops at the first error.
+template <int N, typename F>
+cudaError_t each_table(const msda_grad_list_t &l, int32_t from, int32_t to, F run) {
+    Table<N> t;
+    for (int64_t i = 0; i < l.count;) {
+        i = fill<N>(l, from, to, i, &t);
+        if (!t.count) break;
+        const int blocks = blocks_for(t.before[t.count]);
+        set_starts(t, blocks, kNormThreads / 32);
+        const cudaError_t e = run(t, blocks);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
 }
 
 // What one pass over a list finds: per type (msda_dtype_t's values), whether it
@@ -552,6 +686,45 @@ cudaError_t launch_scale(const msda_grad_list_t &l, const Summary &sum, bool lar
     return cudaSuccess;
 }
 
+template <typename T, typename U> const void *small_kernel(bool largest) {
+    return largest ? (const void *)grad_small_kernel<T, U, true> : (const void *)grad_small_kernel<T, U, false>;
+}
+const void *small_kernel(int32_t dt, int32_t to, bool largest) {
+    if (dt == MSDA_F64) return small_kernel<double, double>(largest);
+    if (dt == MSDA_F32) return small_kernel<float, float>(largest);
+    if (dt == MSDA_BF16)
+        return to == MSDA_F32 ? small_kernel<__nv_bfloat16, float>(largest)
+                              : small_kernel<__nv_bfloat16, __nv_bfloat16>(largest);
+    return to == MSDA_F32 ? small_kernel<__half, float>(largest) : small_kernel<__half, __half>(largest);
+}
+
+// Whether one cluster takes the list: its tensors fit the small table, are of one
+// type of source and destination, and few units.
+bool is_small(const msda_grad_list_t &l, const Summary &sum, bool clip, int32_t *from, int32_t *to) {
+    int classes = 0;
+    for (int32_t dt = 0; dt < kTypes; ++dt) {
+        if (!sum.count[dt]) continue;
+        if (sum.units[dt] > kSmallUnits || (clip && sum.to_own[dt] && sum.to_f32[dt])) return false;
+        ++classes;
+        *from = dt;
+        *to = clip && sum.to_f32[dt] ? (int32_t)MSDA_F32 : dt;
+    }
+    return l.count <= kSmallTable && classes == 1;
+}
+
+cudaError_t launch_small(const msda_grad_list_t &l, const Summary &sum, bool largest, bool clip, double max_norm,
+                         void *norm, int32_t from, int32_t to, cudaStream_t stream) {
+    unsigned *err = nullptr;
+    const cudaError_t e = fault_word_for_launch(&err);
+    if (e != cudaSuccess) return e;
+    Table<kSmallTable> t;
+    fill<kSmallTable>(l, from, clip ? to : -1, 0, &t);
+    set_starts(t, kSmallBlocks, kSmallThreads / 32);
+    bool wide = sum.f64;
+    void *args[] = {&t, &clip, &max_norm, &norm, &wide, &err};
+    return cudaLaunchKernel(small_kernel(from, to, largest), dim3(kSmallBlocks), dim3(kSmallThreads), args, 0, stream);
+}
+
 cudaError_t launch_norm(bool largest, const double *partial, int parts, void *norm, bool wide, cudaStream_t stream) {
     void *args[] = {&partial, &parts, &norm, &wide};
     return launch(largest ? (const void *)grad_norm_kernel<true> : (const void *)grad_norm_kernel<false>, 1, args,
@@ -583,6 +756,10 @@ msda_status_t run(const msda_grad_list_t *l, int kind, bool clip, double max_nor
     double *partial = static_cast<double *>(workspace);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool largest = kind == MSDA_NORM_INF;
+    int32_t from, to;
+    if (is_small(*l, sum, clip, &from, &to))
+        return launch_small(*l, sum, largest, clip, max_norm, norm, from, to, s) == cudaSuccess ? MSDA_OK
+                                                                                               : MSDA_ERR_CUDA;
     const cudaError_t e = l->count <= kSmallTable
                               ? norm_and_scale<kSmallTable>(*l, sum, largest, clip, max_norm, norm, partial, s)
                               : norm_and_scale<kLargeTable>(*l, sum, largest, clip, max_norm, norm, partial, s);

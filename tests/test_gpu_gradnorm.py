@@ -1,10 +1,10 @@
 """The global gradient norm and clipping against float64.
 
 Bounds. u32 = 2^-24, u64 = 2^-53, h half a step of the stored type. Norm: a lane
-adds up to 64 squares in fp32, each product and sum rounded once with fma, so
-its sum is off by at most 64 u32 relative; the sums of those are in fp64; the
-square root halves the relative error, and one rounding to fp32 is added: 32 u32
-+ u32. fp64: n u64 at most for n entries. Largest entry: exact. Clipped entry: the
+adds up to 66 squares in fp32, each product and sum rounded once with fma, so
+its sum is off by at most 66 u32 relative; the sums of those are in fp64, or in
+pairs of fp32 whose errors (n u32^2) do not show; the square root halves the
+relative error, and one rounding to fp32 is added: 33 u32 + u32. fp64: n u64 at most for n entries. Largest entry: exact. Clipped entry: the
 norm's error, the factor rounded to fp32, the product and one rounding to the
 stored type: 33 u32 + 2 u32 + h relative, and half the smallest number of a type.
 """
@@ -73,7 +73,7 @@ def check_clipped(before, after, max_norm, norm):
 
 
 # one entry, around a vector, a lane row, a unit of 4 KB, many units; empty ones among them
-SIZES = [[1], [0, 1, 0], [7, 8, 9], [511, 512, 513], [1023, 1024, 1025, 2047, 2048, 2049, 4097], [100003],
+SIZES = [[1], [0, 1, 0], [7, 8, 9], [262144], [262145], [131072], [131073, 0, 4], [511, 512, 513], [1023, 1024, 1025, 2047, 2048, 2049, 4097], [100003],
          [3, 0, 70000, 5, 1, 1, 33, 256, 65536], [1] * 70, [17] * 1500, [2_000_003, 19]]
 
 
@@ -148,8 +148,8 @@ def test_zeros():
 @pytest.mark.parametrize("kind", [2.0, math.inf])
 @pytest.mark.parametrize("at", [0, 3000, 4999])
 def test_entries_that_are_not_finite(dt, kind, at):
-    for value in (float("inf"), float("-inf"), float("nan")):
-        grads = grads_of([5000, 70], dt)
+    for value, more in [(v, m) for v in (float("inf"), float("-inf"), float("nan")) for m in (70, 3_000_001)]:
+        grads = grads_of([5000, more], dt)
         grads[0][at] = value
         norm = binding.msda_clip_grad_norm(grads, 0.1, kind)
         if value != value:
