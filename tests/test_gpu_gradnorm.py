@@ -95,9 +95,10 @@ def test_norm_and_clip_in_place(sizes, dt, kind):
 @pytest.mark.parametrize("dt,out", [(F32, F32), (BF16, BF16), (BF16, F32), (F16, F16), (F16, F32), (F64, F64)],
                          ids=IDS)
 @pytest.mark.parametrize("offset", [0, 1, 3, 5])
-def test_out_of_place_into_a_flat_buffer(dt, out, offset):
+@pytest.mark.parametrize("more", [[], [1_500_001, 3, 600_000]], ids=["one launch", "two"])
+def test_out_of_place_into_a_flat_buffer(dt, out, offset, more):
     """Ragged sizes, so the flat buffer's parts start anywhere; the source too."""
-    sizes = [9, 4096, 31, 1, 100001, 8, 2048, 77]
+    sizes = [9, 4096, 31, 1, 100001, 8, 2048, 77] + more
     grads = grads_of(sizes, dt, offset=offset)
     kept = [g.clone() for g in grads]
     flat = torch.full((sum(sizes) + 2,), 7.0, device="cuda", dtype=out)
@@ -128,11 +129,12 @@ def test_more_tensors_than_one_table_holds():
 @pytest.mark.parametrize("size", [1e-30, 1e-22, 1e-19, 1e17, 1e19, 1e30])
 def test_squares_past_fp32s_range(dt, size):
     """Entries whose squares (or their sum) overflow or vanish in fp32."""
-    grads = grads_of([5000, 17, 1], dt, scale=size)
-    norm = binding.msda_grad_norm(grads)
-    check_norm(norm, grads, 2.0)
-    mixed = grads_of([5000], dt, scale=size) + grads_of([5000], dt, seed=1, scale=1.0)
-    check_norm(binding.msda_grad_norm(mixed), mixed, 2.0)
+    for n in (5000, 2_000_003):
+        grads = grads_of([n, 17, 1], dt, scale=size)
+        norm = binding.msda_grad_norm(grads)
+        check_norm(norm, grads, 2.0)
+        mixed = grads_of([n], dt, scale=size) + grads_of([n], dt, seed=1, scale=1.0)
+        check_norm(binding.msda_grad_norm(mixed), mixed, 2.0)
 
 
 def test_zeros():
@@ -234,7 +236,7 @@ def test_autograd_sees_the_change_in_place():
 
 
 def test_another_stream_and_captured_graphs():
-    a, b = grads_of([5000, 70001, 3], BF16), grads_of([300] * 100, F32, seed=2)
+    a, b = grads_of([5000, 3_000_001, 3], BF16), grads_of([300] * 20, F32, seed=2)
     oa = [torch.empty(g.shape, device="cuda") for g in a]
     ob = [torch.empty_like(g) for g in b]
     A, B = binding.GradientBuffers(a, out=oa), binding.GradientBuffers(b, out=ob)

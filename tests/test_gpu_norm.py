@@ -240,6 +240,19 @@ def test_autograd_takes_strides_broadcast_gradients_and_frozen_parameters():
     check("grad_weight", gw, reference(x, w, b, r, 1e-5, dy)["grad_weight"])
 
 
+def test_the_same_tensor_as_both_summands():
+    x, w, b, r, dy, ds = operands(60, 256, F32, F32)
+    x.requires_grad_()
+    out, s = binding.layer_norm(x, w, b, residual=x, return_sum=True)
+    g, = torch.autograd.grad([out, s], [x], [dy, ds])
+    want, bound = reference(x, w, b, x, 1e-5, dy, ds)["grad_x"]
+    check("grad_x", g, (2 * want, 2 * bound))
+    leaf = x.detach().clone().requires_grad_()
+    binding.layer_norm(leaf, w, b, residual=leaf).backward(dy)
+    want, bound = reference(x, w, b, x, 1e-5, dy)["grad_x"]
+    check("grad_x", leaf.grad, (2 * want, 2 * bound))
+
+
 def test_two_backward_passes_through_one_graph():
     """The second gradients are tensors of their own."""
     x, w, b, r, dy, ds = operands(60, 256, F32, F32)
