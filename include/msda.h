@@ -371,9 +371,9 @@ MSDA_API int msda_version(void);
 /* N rows of C channels, contiguous. Supported: N >= 0 (zero is a valid empty
  * call), 1 <= C <= 2^20, N*C <= 2^60. Every C and every element alignment is
  * accepted. Rows that all start on 16-byte boundaries (C a multiple of
- * 16 / element size, pointers 16-byte aligned) are the fastest; fp64, rows of
- * over 8,192 fp32 or 16,384 16-bit channels, and in the backward other rows of
- * over 8,192 channels, take plain loops. */
+ * 16 / element size, pointers 16-byte aligned) are the fastest; fp64 and the
+ * longest rows (over 13,312 fp32 or 16,384 16-bit channels; over 8,192 in the
+ * backward where rows start anywhere) take plain loops. */
 typedef struct {
     int64_t N, C;
 } msda_norm_dims_t;

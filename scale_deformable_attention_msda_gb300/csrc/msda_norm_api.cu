@@ -70,7 +70,7 @@ void hold_rows(int64_t n, bool narrow, bool backward, NormPlan *p) {
         p->threads = msda::kGroupThreads;
     } else {
         const bool idle = 10 * n < 9 * 4 * warps_for(n, 4);
-        p->KV = narrow && n <= 1024 && (backward || idle) ? 2 : 4;
+        p->KV = narrow && n <= 1024 && (backward || idle) ? 2 : n <= 2048 ? 4 : 8;
         p->G = 0;
         p->group = warps_for(n, p->KV);
         p->threads = p->group >= 256 ? p->group : 256 / p->group * p->group;
@@ -101,7 +101,10 @@ NormPlan row_plan(const msda_norm_dims_t &d, msda_dtype_t dt, bool aligned16, bo
     const int V = 16 / elem_bytes(dt);
     // no rows: the general form touches nothing of the tensors of rows
     const bool general = dt == MSDA_F64 || d.N == 0;
-    if (!general && d.C % V == 0 && aligned16 && d.C / V <= 2048) {
+    // eight granules of fp32 are four of 16 bits; the backward's 416 threads are
+    // what the copies of four tensors leave of a block's shared memory
+    const int64_t most = dt != MSDA_F32 ? 2048 : backward ? 8 * 416 : 8 * 512;
+    if (!general && d.C % V == 0 && aligned16 && d.C / V <= most) {
         hold_rows(d.C / V, dt != MSDA_F32, backward, &p);
     } else if (!general && d.C <= max_tile_columns(dt, backward)) {
         hold_tiles(d.C, &p);

@@ -520,6 +520,7 @@ static cudaError_t launch_backward_t(const NormArgs &a, const NormPlan &p, cudaS
         if constexpr (sizeof(T) == 4) {
             ROWS(2, 3) ROWS(4, 3) ROWS(8, 3) ROWS(16, 3) ROWS(32, 4)
             if (p.threads <= 384) { ROWS(0, 4) }
+            if (p.G == 0 && p.KV == 8) return launch_rows<T, W, 0, 8, 1, 512>(a, p, stream);
         } else {
             ROWS(0, 2)
         }

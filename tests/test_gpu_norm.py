@@ -54,7 +54,7 @@ def compare(x, w, b, r, dy, ds, total, eps=1e-5):
 # each way of holding a row, its first and last length, and lengths that no vector divides
 SIZES = [(1, 1), (3, 4), (5, 7), (2, 8), (2, 17), (37, 32), (9, 33), (70, 40), (64, 96), (11, 128), (13, 129),
          (7, 160), (33, 255), (600, 256), (19, 264), (5, 512), (4, 520), (3, 1024), (3, 1001),
-         (2, 2049), (2, 4096), (3, 4104), (5, 6247), (4, 8191), (3, 8192), (2, 8193), (3, 11247), (3, 11249), (3, 12001), (2, 16383), (2, 16384), (1, 16392), (2, 32776),
+         (2, 2049), (2, 4096), (3, 4104), (5, 6247), (4, 8191), (3, 8192), (2, 8193), (5, 8196), (3, 11247), (3, 11249), (3, 13312), (3, 13316), (3, 14063), (3, 14065), (3, 12001), (2, 16383), (2, 16384), (1, 16392), (2, 32776),
          (1, 70001)]
 
 
@@ -397,7 +397,7 @@ def test_refusals():
 # --------------------------------------------------------- range-checked build
 
 @pytest.mark.parametrize("N,C", [(1, 1), (5, 7), (70, 40), (600, 256), (44446, 256), (9, 777), (1001, 33),
-                                 (19, 4104), (7, 8191), (3, 12001), (2, 16384), (3, 32776)])
+                                 (19, 4104), (7, 8191), (3, 12001), (3, 13312), (2, 16384), (3, 32776)])
 def test_accesses_stay_in_bounds(N, C):
     binding.use_library(build.CHECKED_LIBRARY)
     try:
