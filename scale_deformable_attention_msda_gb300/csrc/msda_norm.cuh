@@ -28,6 +28,9 @@ constexpr int kGroupThreads = 128, kTileThreads = 256;
 // dynamic shared memory a launch may ask for without raising the kernel's
 // limit: 48 KB less what the kernels declare themselves
 constexpr size_t kDefaultShared = 47 * 1024;
+// the limit it is raised to, always the same: two host threads that launch one
+// kernel with different sizes must not lower each other's
+constexpr int kRaisedShared = 226 * 1024;
 
 struct NormArgs {
     const void *x, *residual;      // (N, C); residual NULL: none

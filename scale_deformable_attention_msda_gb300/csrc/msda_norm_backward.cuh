@@ -484,7 +484,7 @@ static cudaError_t launch(void (*kernel)(const NormArgs), const NormArgs &a, con
         smem = smem > columns ? smem : columns;
     }
     if (smem > kDefaultShared) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRaisedShared);
         if (e != cudaSuccess) return e;
     }
     kernel<<<p.blocks, p.threads, smem, stream>>>(a);

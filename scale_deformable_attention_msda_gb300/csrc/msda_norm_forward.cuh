@@ -277,7 +277,7 @@ __global__ void __launch_bounds__(512) norm_forward_general_kernel(const NormArg
 static cudaError_t launch(void (*kernel)(const NormArgs), const NormArgs &a, const NormPlan &p, size_t smem,
                           cudaStream_t stream) {
     if (smem > kDefaultShared) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRaisedShared);
         if (e != cudaSuccess) return e;
     }
     kernel<<<p.blocks, p.threads, smem, stream>>>(a);

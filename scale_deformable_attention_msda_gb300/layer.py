@@ -86,7 +86,8 @@ class MultiScaleDeformableAttention(nn.Module):
         nn.init.zeros_(self.output_proj.bias)
 
     def forward(self, query, reference, value, spatial_shapes, level_start_index, residual=None):
-        if residual is not None and self.norm is None:
+        norm = getattr(self, "norm", None)         # a layer pickled before it could have one
+        if residual is not None and norm is None:
             raise ValueError("a residual is added by a layer made with norm=True")
         B, Q, _ = query.shape
         S = value.shape[1]
@@ -101,6 +102,6 @@ class MultiScaleDeformableAttention(nn.Module):
         out = binding.multi_scale_deformable_attention(v, spatial_shapes, level_start_index, loc,
                                                        logits, accum=self.accum, softmax=True)
         out = self.output_proj(out)
-        if self.norm is None:
+        if norm is None:
             return out
-        return self.norm(out, residual=query if residual is None else residual)
+        return norm(out, residual=query if residual is None else residual)
