@@ -266,18 +266,21 @@ template <typename T> constexpr __host__ __device__ int tile_places(int64_t n) {
     return (int)((n + 2 * Vec16<T>::N - 2) / Vec16<T>::N);
 }
 
-// Rows of a group in a tile: up to four, in tiles of up to about 16 KB.
-inline int tile_rows(const NormArgs &a, const NormPlan &p, int bytes) {
-    const int64_t one = (int64_t)(p.threads / p.group) * a.C * bytes;
-    const int64_t n = 16384 / one, share = a.N / ((int64_t)p.blocks * (p.threads / p.group));
-    const int64_t most = share < 4 ? (share < 1 ? 1 : share) : 4;      // as many as leave every block its tile
-    return (int)(n < 1 ? 1 : n < most ? n : most);
-}
-
 // The tiles that fit beside `outs` results: two, or one, of `ins` tensors each.
 constexpr size_t kMostShared = 220 * 1024;
 constexpr int tile_stages(int ins, int outs, size_t bytes) {
     return (size_t)(2 * ins + outs) * bytes <= kMostShared ? 2 : 1;
+}
+
+// Rows of a group in a tile: up to four, in tiles of up to about 16 KB, or of 32
+// KB where a block has an SM to itself and two tiles fit; and as many as leave
+// every block its tile.
+inline int tile_rows(const NormArgs &a, const NormPlan &p, int ins, int outs, int bytes) {
+    const int64_t one = (int64_t)(p.threads / p.group) * a.C * bytes;
+    const int64_t room = p.threads > 256 && tile_stages(ins, outs, 33 * 1024) == 2 ? 32 * 1024 : 16 * 1024;
+    const int64_t n = room / one, share = a.N / ((int64_t)p.blocks * (p.threads / p.group));
+    const int64_t most = share < 4 ? (share < 1 ? 1 : share) : 4;
+    return (int)(n < 1 ? 1 : n < most ? n : most);
 }
 
 // A thread's channels t, t + g, ... as P pairs: pair i is channels t + 2i*g and

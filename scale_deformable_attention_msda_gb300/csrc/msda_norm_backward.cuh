@@ -503,7 +503,7 @@ template <typename T, typename W, int G, int P>
 static cudaError_t launch_tiles(const NormArgs &a, const NormPlan &p, cudaStream_t stream) {
     const int ins = 2 + (a.residual ? 1 : 0) + (a.grad_sum ? 1 : 0);
     NormArgs b = a;
-    b.tile_rows = tile_rows(a, p, sizeof(T));
+    b.tile_rows = tile_rows(a, p, ins, 1, sizeof(T));
     const size_t bytes = (size_t)tile_places<T>((int64_t)(p.threads / p.group) * b.tile_rows * a.C) * 16;
     b.stages = tile_stages(ins, 1, bytes);
     return launch<W>(norm_backward_tile_kernel<T, W, G, P>, b, p, (b.stages * ins + 1) * bytes, stream);

@@ -294,7 +294,7 @@ template <typename T, typename W, int G, int P>
 static cudaError_t launch_tiles(const NormArgs &a, const NormPlan &p, cudaStream_t stream) {
     const int ins = a.residual ? 2 : 1, outs = a.sum ? 2 : 1;
     NormArgs b = a;
-    b.tile_rows = tile_rows(a, p, sizeof(T));
+    b.tile_rows = tile_rows(a, p, ins, outs, sizeof(T));
     const size_t bytes = (size_t)tile_places<T>((int64_t)(p.threads / p.group) * b.tile_rows * a.C) * 16;
     b.stages = tile_stages(ins, outs, bytes);
     return launch(norm_forward_tile_kernel<T, W, G, P>, b, p, (b.stages * ins + outs) * bytes, stream);
