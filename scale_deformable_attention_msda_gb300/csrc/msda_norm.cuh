@@ -272,13 +272,17 @@ constexpr int tile_stages(int ins, int outs, size_t bytes) {
     return (size_t)(2 * ins + outs) * bytes <= kMostShared ? 2 : 1;
 }
 
-// Rows of a group in a tile: up to four, in tiles of up to about 16 KB, or of 32
-// KB where a block has an SM to itself and two tiles fit; and as many as leave
-// every block its tile.
+// Rows of a group in a tile: up to four, in tiles of up to 16 KB, or of 32 KB where
+// a block has an SM to itself and two tiles fit (3,661 x 4097 bf16 backward: 58 us
+// with 16 KB, 49 so); two at least, while the blocks an SM can hold keep their
+// tiles (31,128 x 257 fp32 forward: 20.1 us with one, 16.8 so); and as many as
+// leave every block its tile. More rows a tile share its copies' and barriers' cost.
 inline int tile_rows(const NormArgs &a, const NormPlan &p, int ins, int outs, int bytes) {
     const int64_t one = (int64_t)(p.threads / p.group) * a.C * bytes;
-    const int64_t room = p.threads > 256 && tile_stages(ins, outs, 33 * 1024) == 2 ? 32 * 1024 : 16 * 1024;
-    const int64_t n = room / one, share = a.N / ((int64_t)p.blocks * (p.threads / p.group));
+    const int64_t resident = p.threads > 256 ? 1 : 512 / p.threads;
+    int64_t n = (p.threads > 256 && tile_stages(ins, outs, 33 * 1024) == 2 ? 32 * 1024 : 16 * 1024) / one;
+    if (n < 2 && resident * (2 * ins + outs) * (2 * one + 32) <= (int64_t)kMostShared) n = 2;
+    const int64_t share = a.N / ((int64_t)p.blocks * (p.threads / p.group));
     const int64_t most = share < 4 ? (share < 1 ? 1 : share) : 4;
     return (int)(n < 1 ? 1 : n < most ? n : most);
 }
