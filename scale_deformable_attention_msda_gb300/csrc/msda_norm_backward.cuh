@@ -65,7 +65,7 @@ __device__ __forceinline__ void leave_partials(const NormArgs &a, const float *c
 template <typename T, typename W, int G, int KV, int S, int TH>
 __global__ void __launch_bounds__(TH) norm_backward_kernel(const NormArgs a) {
     constexpr int V = Vec16<T>::N, P = V / 2;
-    __shared__ BlockScratch<2> scratch;
+    __shared__ BlockScratch scratch;
     extern __shared__ uint4 ring[];      // (S, tensors, KV, threads); at the end (warps, 2, C) floats
     int turn = 0;
     cudaTriggerProgrammaticLaunchCompletion();   // the column kernel may be launched; it waits for this one's end
@@ -202,7 +202,7 @@ template <typename T, typename W, int G, int P>
 __global__ void __launch_bounds__(G == 0 ? 512 : kTileThreads, G == 0 ? 1 : 2)
 norm_backward_tile_kernel(const NormArgs a) {
     constexpr int TH = kTileThreads;
-    __shared__ BlockScratch<2> scratch;
+    __shared__ BlockScratch scratch;
     extern __shared__ uint4 ring[];      // stages of (tensors, places), then grad_x; at the end (writers, 2, C) floats
     int turn = 0;
     cudaTriggerProgrammaticLaunchCompletion();

@@ -2,7 +2,8 @@
 // channels of each row of s = x + residual, mean and biased variance per row.
 //
 // A row is read once and stays in registers: its mean, then the sum of squared
-// distances from that mean (no difference of large sums), then the output. All
+// distances from that mean (no difference of large sums), a correction of the mean
+// by what the distances add up to (fix_mean in msda_norm.cuh), then the output. All
 // arithmetic in fp32; s is not rounded before it is normalised, and out is rounded
 // once.
 //
@@ -23,11 +24,14 @@ namespace msda {
 // is worked on. A thread copies what it reads itself, so its own wait is all the
 // order the copies need, and the copies hold no registers: with plain loads the
 // same rows took 18.3 us instead of 11.2. Sums run on packed pairs of fp32, which
-// take 10% fewer instructions than scalar ones.
+// take 10% fewer instructions than scalar ones. The bounds keep the blocks on an SM
+// that the kernels had before their means were corrected: 4 with three or four
+// granules, 5 or 6 with two.
 template <typename T, typename W, int G, int KV, int S, int TH>
-__global__ void __launch_bounds__(TH) norm_forward_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(TH, G == 0 ? 1 : KV > 2 ? 4 : sizeof(T) == 4 ? 6 : 5)
+norm_forward_kernel(const NormArgs a) {
     constexpr int V = Vec16<T>::N, P = V / 2;
-    __shared__ BlockScratch<1> scratch;
+    __shared__ BlockScratch scratch;
     extern __shared__ uint4 ring[];      // (S, tensors, KV, threads)
     int turn = 0;
     const int C = a.C;
@@ -84,6 +88,7 @@ __global__ void __launch_bounds__(TH) norm_forward_kernel(const NormArgs a) {
         fetch(slot);
         slot = slot + tall == begin + S * tall ? begin : slot + tall;
         const float mean = v[0] * inv_C;
+        float2 off = both(0.0f);
         acc = both(0.0f);
 #pragma unroll
         for (int k = 0; k < KV; ++k) {
@@ -92,18 +97,22 @@ __global__ void __launch_bounds__(TH) norm_forward_kernel(const NormArgs a) {
             for (int i = 0; i < P; ++i) s[k][i] = add2(s[k][i], both(m));
 #pragma unroll
             for (int i = 0; i < P; ++i) acc = fma2(s[k][i], s[k][i], acc);
+#pragma unroll
+            for (int i = 0; i < P; ++i) off = add2(off, s[k][i]);
         }
-        v[0] = acc.x + acc.y;
-        row_sum<G>(v, &scratch, turn, map.threads, map.index);
-        const float rstd = rsqrtf(fmaf(v[0], inv_C, (float)a.eps));     // within 2 ulp
+        float u[2] = {off.x + off.y, acc.x + acc.y};
+        row_sum<G>(u, &scratch, turn, map.threads, map.index);
+        const MeanFix f = fix_mean(u[0], u[1], (float)C, inv_C);
+        const float rstd = row_rstd(f.squares, inv_C, (float)a.eps);
         if (map.t == 0 && valid && a.mean && span_ok(a.err, row, 1, a.N)) {
-            static_cast<float *>(a.mean)[row] = mean;
+            static_cast<float *>(a.mean)[row] = mean + f.shift;
             static_cast<float *>(a.rstd)[row] = rstd;
         }
 #pragma unroll
         for (int k = 0; k < KV; ++k) {
 #pragma unroll
-            for (int i = 0; i < P; ++i) s[k][i] = fma2(mul2(s[k][i], both(rstd)), pw[k][i], pb[k][i]);
+            for (int i = 0; i < P; ++i)
+                s[k][i] = fma2(mul2(add2(s[k][i], both(-f.shift)), both(rstd)), pw[k][i], pb[k][i]);
             if (valid && map.held(k)) map.store(static_cast<T *>(a.out), here, k, s[k]);
         }
     }
@@ -115,7 +124,7 @@ template <typename T, typename W, int G, int P>
 __global__ void __launch_bounds__(G == 0 ? 512 : kTileThreads, G == 0 ? 1 : 3)
 norm_forward_tile_kernel(const NormArgs a) {
     constexpr int TH = kTileThreads;
-    __shared__ BlockScratch<1> scratch;
+    __shared__ BlockScratch scratch;
     extern __shared__ uint4 ring[];      // stages of (tensors, places), then out and sum
     int turn = 0;
     const int C = a.C;
@@ -176,7 +185,7 @@ norm_forward_tile_kernel(const NormArgs a) {
             for (int i = 0; i < P; ++i) acc = add2(acc, s[i]);
             float v[1] = {acc.x + acc.y};
             row_sum<G>(v, &scratch, turn, g, map.index);
-            const float mean = v[0] * inv_C;
+            float mean = v[0] * inv_C;
             acc = both(0.0f);
 #pragma unroll
             for (int i = 0; i < P; ++i) {
@@ -187,7 +196,22 @@ norm_forward_tile_kernel(const NormArgs a) {
             }
             v[0] = acc.x + acc.y;
             row_sum<G>(v, &scratch, turn, g, map.index);
-            const float rstd = rsqrtf(fmaf(v[0], inv_C, (float)a.eps));
+            float rstd = row_rstd(v[0], inv_C, (float)a.eps);
+            const bool far = is_far(mean, rstd);
+            if (G == 0 ? far : __any_sync(0xffffffffu, far)) {   // the same for a group's threads
+                acc = both(0.0f);
+#pragma unroll
+                for (int i = 0; i < P; ++i) acc = add2(acc, s[i]);
+                float u[1] = {acc.x + acc.y};
+                row_sum<G>(u, &scratch, turn, g, map.index);
+                if (far) {
+                    const MeanFix f = fix_mean(u[0], v[0], (float)C, inv_C);
+                    rstd = row_rstd(f.squares, inv_C, (float)a.eps);
+                    mean += f.shift;
+#pragma unroll
+                    for (int i = 0; i < P; ++i) s[i] = add2(s[i], both(-f.shift));
+                }
+            }
             if (!valid) continue;
             if (t == 0 && a.mean && span_ok(a.err, tile + row, 1, a.N)) {
                 static_cast<float *>(a.mean)[tile + row] = mean;
@@ -238,7 +262,10 @@ template <typename A> __device__ __forceinline__ A block_sum(A v, A *scratch) {
 }
 
 // Rows of any length, one block each, read three times (the later reads hit
-// the caches).
+// the caches), five times where the row is_far: then the mean is that of the
+// distances from the row's first entry, so that a row of equal entries has exactly
+// that mean, corrected by what the distances from it add up to. (fp64 additions are
+// what 2000 x 1024 fp64 wait for: 201 us; with the correction in every row 294.)
 template <typename T, typename W>
 __global__ void __launch_bounds__(512) norm_forward_general_kernel(const NormArgs a) {
     using A = typename Acc<T>::type;
@@ -248,24 +275,43 @@ __global__ void __launch_bounds__(512) norm_forward_general_kernel(const NormArg
     for (int64_t row = blockIdx.x; row < a.N; row += gridDim.x) {
         const int64_t base = row * a.C;
         if (!span_ok(a.err, base, a.C, a.N * a.C)) continue;
-        A v = 0;
-        for (int c = threadIdx.x; c < a.C; c += blockDim.x)
-            v += to_acc<T>(x[base + c]) + (res ? to_acc<T>(res[base + c]) : (A)0);
-        const A mean = block_sum<A>(v, scratch) / (A)a.C;
+        auto at = [&](int c) { return to_acc<T>(x[base + c]) + (res ? to_acc<T>(res[base + c]) : (A)0); };
+        A v = 0, shift = 0;
+        for (int c = threadIdx.x; c < a.C; c += blockDim.x) v += at(c);
+        A mean = block_sum<A>(v, scratch) / (A)a.C;
         v = 0;
         for (int c = threadIdx.x; c < a.C; c += blockDim.x) {
-            const A d = to_acc<T>(x[base + c]) + (res ? to_acc<T>(res[base + c]) : (A)0) - mean;
+            const A d = at(c) - mean;
             v += d * d;
         }
-        const A rstd = (A)1 / sqrt(block_sum<A>(v, scratch) / (A)a.C + (A)a.eps);
+        v = block_sum<A>(v, scratch) / (A)a.C + (A)a.eps;
+        A rstd = (A)1 / sqrt(v) + (v - v);               // a variance out of range: NaN
+        if (!(fabs(mean) * rstd <= (A)kFar)) {           // the same for all threads
+            const A first = at(0);
+            v = 0;
+            for (int c = threadIdx.x; c < a.C; c += blockDim.x) v += at(c) - first;
+            mean = first + block_sum<A>(v, scratch) / (A)a.C;
+            A off = 0;
+            v = 0;
+            for (int c = threadIdx.x; c < a.C; c += blockDim.x) {
+                const A d = at(c) - mean;
+                off += d;
+                v += d * d;
+            }
+            off = block_sum<A>(off, scratch);
+            shift = off / (A)a.C;
+            v = block_sum<A>(v, scratch) - shift * off;
+            v = (v < (A)0 ? (A)0 : v) / (A)a.C + (A)a.eps;
+            rstd = (A)1 / sqrt(v) + (v - v);
+        }
         if (threadIdx.x == 0 && a.mean) {
-            static_cast<A *>(a.mean)[row] = mean;
+            static_cast<A *>(a.mean)[row] = mean + shift;
             static_cast<A *>(a.rstd)[row] = rstd;
         }
         for (int c = threadIdx.x; c < a.C; c += blockDim.x) {
-            const A s = to_acc<T>(x[base + c]) + (res ? to_acc<T>(res[base + c]) : (A)0);
+            const A s = at(c);
             if (a.sum) static_cast<T *>(a.sum)[base + c] = from_acc<T, A>(s);
-            A g = (s - mean) * rstd;
+            A g = (s - mean - shift) * rstd;
             if (w) g *= (A)to_acc<W>(w[c]);
             if (b) g += (A)to_acc<W>(b[c]);
             static_cast<T *>(a.out)[base + c] = from_acc<T, A>(g);
