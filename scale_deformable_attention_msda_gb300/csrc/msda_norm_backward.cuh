@@ -112,10 +112,13 @@ __global__ void __launch_bounds__(TH) norm_backward_kernel(const NormArgs a) {
         rs = __ldg(rstd + map.first);
     }
     for (int64_t row = map.first, lead = map.lead; lead < a.N; row += map.step, lead += map.step, here += hop) {
-        // a row past the last, and a granule the thread does not have, were
-        // filled with zeros: grad_out = 0 there, and nothing is added
+        // A row past the last, and a granule the thread does not have, were
+        // filled with zeros: grad_out = 0 there, and with a mean of zero xh as
+        // well, so that nothing is added. (Of a mean as it is, mean * rstd may
+        // leave fp32's range, and 0 * inf is NaN.)
         const bool valid = G == 0 || G == 32 || row < a.N;
         const float m = mu, r = rs;
+        mu = rs = 0.0f;
         if (row + map.step < a.N) {
             mu = __ldg(mean + row + map.step);
             rs = __ldg(rstd + row + map.step);
@@ -133,9 +136,10 @@ __global__ void __launch_bounds__(TH) norm_backward_kernel(const NormArgs a) {
 #pragma unroll
                 for (int i = 0; i < P; ++i) xh[k][i] = add2(xh[k][i], e[i]);
             }
+            const float from = map.held(k) ? -m : 0.0f;
 #pragma unroll
             for (int i = 0; i < P; ++i) {
-                xh[k][i] = mul2(add2(xh[k][i], both(-m)), both(r));
+                xh[k][i] = mul2(add2(xh[k][i], both(from)), both(r));
                 dw[k][i] = fma2(g[k][i], xh[k][i], dw[k][i]);
                 db[k][i] = add2(db[k][i], g[k][i]);
                 g[k][i] = mul2(g[k][i], pw[k][i]);
@@ -278,8 +282,12 @@ norm_backward_tile_kernel(const NormArgs a) {
                 load_pairs(gy, y0 + from, t, g, C);
 #pragma unroll
                 for (int i = 0; i < P; ++i) {
-                    xh[i] = mul2(add2(xh[i], both(-mu)), both(rstd_row));
-                    dw[i] = fma2(gy[i], xh[i], dw[i]);       // past the row grad_out is zero
+                    // past the row grad_out is zero, and xh too
+                    const int c = t + 2 * i * g;
+                    const bool whole = i < kWholePairs<P>;
+                    const float2 from = make_float2(whole || c < C ? -mu : 0.0f, whole || c + g < C ? -mu : 0.0f);
+                    xh[i] = mul2(add2(xh[i], from), both(rstd_row));
+                    dw[i] = fma2(gy[i], xh[i], dw[i]);
                     db[i] = add2(db[i], gy[i]);
                     gy[i] = mul2(gy[i], pw[i]);
                     v0 = add2(v0, gy[i]);
