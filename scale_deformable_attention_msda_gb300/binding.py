@@ -15,6 +15,7 @@ import os
 import threading
 
 import torch
+from torch.autograd import forward_ad
 
 from . import build as _build
 
@@ -595,6 +596,13 @@ class LayerNormFunction(torch.autograd.Function):
     backward_once = staticmethod(torch.autograd.function.once_differentiable(_norm_gradients))
 
 
+def _through_autograd():
+    """Whether torch must see an operation although no gradient is wanted: inside a
+    forward-mode level, whose tangents a launch on addresses would drop (the autograd
+    function has no jvp and says so)."""
+    return forward_ad._current_level >= 0
+
+
 def layer_norm(x, weight=None, bias=None, residual=None, eps: float = 1e-5, return_sum: bool = False):
     """Differentiable layer norm over x's last dimension, of x + residual where a residual is
     given (same shape as x; the sum is not rounded before it is normalised). weight and bias
@@ -612,7 +620,7 @@ def layer_norm(x, weight=None, bias=None, residual=None, eps: float = 1e-5, retu
     if bias is not None:
         bias = bias.contiguous()
         grad = grad or bias.requires_grad
-    if grad and torch.is_grad_enabled():
+    if (grad and torch.is_grad_enabled()) or _through_autograd():
         return LayerNormFunction.apply(x, residual, weight, bias, eps, return_sum)
     pdt = _param_dtype(x, weight, bias)
     index = _norm_operands(x, weight, bias, pdt, residual)
