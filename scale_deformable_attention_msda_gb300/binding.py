@@ -597,10 +597,11 @@ class LayerNormFunction(torch.autograd.Function):
 
 
 def _through_autograd():
-    """Whether torch must see an operation although no gradient is wanted: inside a
-    forward-mode level, whose tangents a launch on addresses would drop (the autograd
-    function has no jvp and says so)."""
-    return forward_ad._current_level >= 0
+    """Whether torch must see an operation although no gradient is wanted: while
+    torch.jit.trace runs, whose record of a launch on addresses would be the output's
+    allocation alone, and inside a forward-mode level, whose tangents it would drop (the
+    autograd function has no jvp and says so)."""
+    return torch._C._get_tracing_state() is not None or forward_ad._current_level >= 0
 
 
 def layer_norm(x, weight=None, bias=None, residual=None, eps: float = 1e-5, return_sum: bool = False):

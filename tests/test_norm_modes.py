@@ -59,3 +59,16 @@ def test_forward_mode_is_refused(launches, grad):
         # what carries no tangent is computed as ever
         plain = torch.randn(3, 8)
         assert torch.allclose(binding.layer_norm(plain), torch.nn.functional.layer_norm(plain, (8,)), atol=1e-5)
+
+
+@pytest.mark.parametrize("grad", [False, True])
+def test_a_trace_calls_the_operator(launches, grad):
+    x = torch.randn(3, 8)
+    with torch.set_grad_enabled(grad):
+        traced = torch.jit.trace(lambda t: binding.layer_norm(t) * 2, (x.clone().requires_grad_(grad),), check_trace=False)
+        for _ in range(3):
+            other = torch.randn(3, 8)
+            before = len(launches)
+            got = traced(other)
+            assert len(launches) == before + 1
+            assert torch.allclose(got, 2 * torch.nn.functional.layer_norm(other, (8,)), atol=1e-5)
