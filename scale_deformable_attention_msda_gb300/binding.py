@@ -409,6 +409,28 @@ def _norm_workspace(numel, C, dtype):
     return int(lib().msda_layer_norm_backward_workspace_bytes(_norm_dims(numel, C), dtype))
 
 
+_PROXY = torch._C._TorchDispatchModeKey.PROXY
+
+
+def _refuse_recording(name):
+    """Raise while torch records operations by dispatch (make_fx): a launch on addresses is
+    not among them, and its record would return the output's allocation."""
+    if torch._C._len_torch_dispatch_stack() and torch._C._get_dispatch_mode(_PROXY) is not None:
+        raise RuntimeError(f"{name} cannot be recorded: it launches on addresses, which torch does not see")
+
+
+def _refuse_modes(name, tensors):
+    """As _refuse_recording, for a call that has no autograd function either: while
+    torch.jit.trace runs, and of tensors that carry a forward-mode tangent."""
+    _refuse_recording(name)
+    if torch._C._get_tracing_state() is not None:
+        raise RuntimeError(f"{name} cannot be recorded: it launches on addresses, which torch does not see")
+    if forward_ad._current_level >= 0:
+        for t in tensors:
+            if t is not None and forward_ad.unpack_dual(t).tangent is not None:
+                raise RuntimeError(f"{name} has no forward-mode derivative: a tangent would be dropped")
+
+
 def _param_dtype(x, weight, bias, given=None):
     params = weight if weight is not None else bias
     pdt = params.dtype if params is not None else given if given is not None else x.dtype
@@ -514,6 +536,7 @@ def msda_layer_norm_forward(x, weight=None, bias=None, residual=None, eps: float
     """(out, sum, mean, rstd) of the rows of x + residual over x's last dimension; sum is
     None unless return_sum, mean and rstd are None unless stats (the backward needs them).
     See msda_layer_norm_forward in include/msda.h."""
+    _refuse_modes("msda_layer_norm_forward", (x, weight, bias, residual))
     pdt = _param_dtype(x, weight, bias)
     index = _norm_operands(x, weight, bias, pdt, residual, (("out", out),))
     if out is not None:
@@ -535,6 +558,7 @@ def msda_layer_norm_backward(grad_out, x, mean, rstd, weight=None, residual=None
     """(grad_x, grad_weight, grad_bias), None where `want` says so; grad_x is the gradient of
     x and of residual alike. param_dtype: the parameters' type where weight is None. See
     msda_layer_norm_backward in include/msda.h."""
+    _refuse_modes("msda_layer_norm_backward", (grad_out, x, mean, rstd, weight, residual, grad_sum))
     pdt = _param_dtype(x, weight, None, param_dtype)
     index = _norm_operands(x, weight, None, pdt, residual, (("grad_out", grad_out), ("grad_sum", grad_sum)))
     shape, sdt = x.shape[:-1], _stats_dtype(x)
@@ -550,6 +574,7 @@ def msda_layer_norm_backward(grad_out, x, mean, rstd, weight=None, residual=None
 
 def _norm_gradients(ctx, grad_out, grad_sum):
     """What LayerNormFunction.backward returns."""
+    _refuse_recording("layer_norm's backward")
     need_x, need_res, need_w, need_b, _, _ = ctx.needs_input_grad
     if grad_sum is not None:
         grad_sum = grad_sum.contiguous()
@@ -610,6 +635,7 @@ def layer_norm(x, weight=None, bias=None, residual=None, eps: float = 1e-5, retu
     (C,) of x's type, or float32 with 16-bit x. return_sum: (normalised, x + residual)."""
     if return_sum and residual is None:
         raise ValueError("return_sum needs a residual")
+    _refuse_recording("layer_norm")
     x = x.contiguous()
     grad = x.requires_grad
     if residual is not None:
@@ -752,7 +778,14 @@ def _grad_call(buf, kind, max_norm, stream):
 
 def _grad_norm(grads, norm_type, max_norm, stream):
     kind = _norm_kind(norm_type)
-    buf = grads if isinstance(grads, GradientBuffers) else GradientBuffers(grads)
+    name = "msda_grad_norm" if max_norm is None else "msda_clip_grad_norm"
+    if isinstance(grads, GradientBuffers):
+        _refuse_modes(name, ())          # aliases without tangents
+        buf = grads
+    else:
+        grads = list(grads)
+        _refuse_modes(name, grads)
+        buf = GradientBuffers(grads)
     if buf.device is None:               # an empty list
         return torch.zeros(())
     if stream is not None or torch._C._cuda_getDevice() != buf.device.index:

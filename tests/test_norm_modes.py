@@ -72,3 +72,35 @@ def test_a_trace_calls_the_operator(launches, grad):
             got = traced(other)
             assert len(launches) == before + 1
             assert torch.allclose(got, 2 * torch.nn.functional.layer_norm(other, (8,)), atol=1e-5)
+
+
+def test_recording_by_dispatch_is_refused(launches):
+    from torch.fx.experimental.proxy_tensor import make_fx
+    x = torch.randn(3, 8)
+    with pytest.raises(RuntimeError, match="record"):
+        make_fx(lambda t: binding.layer_norm(t))(x)
+    leaf = x.clone().requires_grad_()
+    with pytest.raises(RuntimeError, match="record"):
+        make_fx(lambda t: binding.layer_norm(t))(leaf)
+
+
+CALLS = {
+    "msda_layer_norm_forward": lambda t: binding.msda_layer_norm_forward(t)[0],
+    "msda_layer_norm_backward": lambda t: binding.msda_layer_norm_backward(t, t, t[:, 0], t[:, 0])[0],
+    "msda_grad_norm": lambda t: binding.msda_grad_norm([t]),
+    "msda_clip_grad_norm": lambda t: binding.msda_clip_grad_norm([t], 1.0),
+}
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_calls_on_addresses_refuse_to_be_recorded(name):
+    """They have no node that a trace or a tangent could pass through."""
+    from torch.fx.experimental.proxy_tensor import make_fx
+    x = torch.randn(3, 8)
+    with pytest.raises(RuntimeError, match="record"):
+        torch.jit.trace(CALLS[name], (x,), check_trace=False)
+    with pytest.raises(RuntimeError, match="record"):
+        make_fx(CALLS[name])(x)
+    with fwAD.dual_level():
+        with pytest.raises(RuntimeError, match="forward"):
+            CALLS[name](fwAD.make_dual(x, torch.ones(3, 8)))
