@@ -488,16 +488,17 @@ def _norm_forward(x, weight, bias, residual, eps, return_sum, stats, out, pdt, i
         out = torch.empty_like(x)
     total = torch.empty_like(x) if return_sum else None
     mean = rstd = None
+    numel, C = int(x.numel()), int(x.shape[-1])      # a trace makes tensors of sizes
     if stats:
-        stats = torch.empty(2 * (x.numel() // x.shape[-1]) if x.shape[-1] else 0,
-                            dtype=_stats_dtype(x), device=x.device)
+        rows = numel // C if C else 0
+        stats = torch.empty(2 * rows, dtype=_stats_dtype(x), device=x.device)
         mean = stats.data_ptr()
-        rstd = mean + stats.numel() // 2 * stats.element_size()
+        rstd = mean + rows * stats.element_size()
     status = lib().msda_layer_norm_forward(
         x.data_ptr(), None if residual is None else residual.data_ptr(),
         None if weight is None else weight.data_ptr(), None if bias is None else bias.data_ptr(),
         out.data_ptr(), None if total is None else total.data_ptr(), mean, rstd, eps,
-        _norm_dims(x.numel(), x.shape[-1]), _DTYPES[x.dtype], _DTYPES[pdt], _current_stream(index))
+        _norm_dims(numel, C), _DTYPES[x.dtype], _DTYPES[pdt], _current_stream(index))
     if status:
         raise MSDAError(status, "msda_layer_norm_forward")
     return out, total, stats
