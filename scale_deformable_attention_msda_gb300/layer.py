@@ -30,7 +30,9 @@ from . import binding
 class LayerNorm(nn.Module):
     """Layer norm over the last dimension, of x + residual where a residual is given
     (libmsda's kernels; binding.layer_norm). return_sum: (normalised, x + residual), what a
-    pre-norm stack passes on. weight and bias start at one and zero."""
+    pre-norm stack passes on. weight and bias start at one and zero. Under autocast x and a
+    residual of another type (a projection's 16-bit output beside a float32 stream) are both
+    taken in the type that holds both."""
 
     def __init__(self, dim: int, eps: float = 1e-5, bias: bool = True):
         super().__init__()
@@ -39,7 +41,12 @@ class LayerNorm(nn.Module):
         self.bias = nn.Parameter(torch.zeros(dim)) if bias else None
 
     def forward(self, x, residual=None, return_sum: bool = False):
-        return binding.layer_norm(x, self.weight, self.bias, residual=residual, eps=self.eps,
+        weight, bias = self.weight, self.bias
+        if residual is not None and residual.dtype != x.dtype and torch.is_autocast_enabled("cuda"):
+            dtype = torch.promote_types(x.dtype, residual.dtype)
+            x, residual = x.to(dtype), residual.to(dtype)
+            weight, bias = weight.to(dtype), None if bias is None else bias.to(dtype)
+        return binding.layer_norm(x, weight, bias, residual=residual, eps=self.eps,
                                   return_sum=return_sum)
 
 
