@@ -542,12 +542,15 @@ def msda_layer_norm_forward(x, weight=None, bias=None, residual=None, eps: float
     index = _norm_operands(x, weight, bias, pdt, residual, (("out", out),))
     if out is not None:
         _apart([out], [x, residual, weight, bias])
+    given = out
     args = (x, weight, bias, residual, eps, return_sum, stats, out, pdt, index)
     if _elsewhere(index, stream):
         with _on(x.device, stream):
             out, total, both = _norm_forward(*args)
     else:
         out, total, both = _norm_forward(*args)
+    if given is not None and not out.is_inference():
+        torch.autograd.graph.increment_version(out)
     if not stats:
         return out, total, None, None
     mean, rstd = both.view(2, *x.shape[:-1])

@@ -54,3 +54,18 @@ def test_a_tangent_is_refused():
             with torch.set_grad_enabled(grad), pytest.raises(NotImplementedError, match="jvp"):
                 m(fwAD.make_dual(x, torch.ones_like(x)))
         check("out", m(x), reference(x, m.weight, m.bias)["out"])
+
+
+def test_an_output_given_by_the_caller_advances_its_version():
+    """A tensor saved for a backward pass cannot be overwritten unnoticed."""
+    x = torch.randn(3, 8, device="cuda")
+    leaf = torch.ones(3, 8, device="cuda", requires_grad=True)
+    out = torch.ones(3, 8, device="cuda")
+    y = (leaf * out).sum()               # saves out
+    binding.msda_layer_norm_forward(x, out=out)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.backward()
+    with torch.inference_mode():         # such tensors have no version
+        out = torch.empty(3, 8, device="cuda")
+        binding.msda_layer_norm_forward(x, out=out)
+    check("out", out, reference(x, None, None)["out"])
