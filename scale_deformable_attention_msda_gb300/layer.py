@@ -72,6 +72,7 @@ class MultiScaleDeformableAttention(nn.Module):
         self.value_proj = nn.Linear(dim, dim)
         self.output_proj = nn.Linear(dim, dim)
         self.norm = LayerNorm(dim) if norm else None
+        self.ends_in_norm = norm         # a subclass may have a norm of its own under that name
         self.reset_parameters()
 
     @torch.no_grad()
@@ -93,7 +94,10 @@ class MultiScaleDeformableAttention(nn.Module):
         nn.init.zeros_(self.output_proj.bias)
 
     def forward(self, query, reference, value, spatial_shapes, level_start_index, residual=None):
-        norm = getattr(self, "norm", None)         # a layer pickled before it could have one
+        norm = getattr(self, "norm", None)
+        # layers pickled before the mark: those with a norm of this module's were made with it
+        if not getattr(self, "ends_in_norm", isinstance(norm, LayerNorm)):
+            norm = None
         if residual is not None and norm is None:
             raise ValueError("a residual is added by a layer made with norm=True")
         B, Q, _ = query.shape
