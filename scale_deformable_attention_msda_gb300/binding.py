@@ -738,21 +738,33 @@ class GradientBuffers:
         for (_, end), (begin, _) in zip(spans, spans[1:]):
             if begin < end:
                 raise ValueError("two of the tensors share memory")
+        storages = {}
         for t in self._all:
-            held = t.untyped_storage().nbytes() - t.storage_offset() * t.element_size()
+            storage = t.untyped_storage()
+            storages[storage._cdata] = storage
+            held = storage.nbytes() - t.storage_offset() * t.element_size()
             if held < t.numel() * t.element_size():
                 raise ValueError("a tensor's storage was resized to less than the tensor")
-        self._addresses = list(map(torch.Tensor.data_ptr, self._all))
+        self._storages = list(storages.values())
+        self._memory = self._read_memory()
+        addresses = list(map(torch.Tensor.data_ptr, self._all))
         n = len(self._grads)
-        self._at = (ctypes.c_void_p * n)(*self._addresses[:n])
-        self._out_at = self._at if self.in_place else (ctypes.c_void_p * n)(*self._addresses[n:])
+        self._at = (ctypes.c_void_p * n)(*addresses[:n])
+        self._out_at = self._at if self.in_place else (ctypes.c_void_p * n)(*addresses[n:])
         self._list = msda_grad_list_t(n, *[ctypes.addressof(a) for a in (
             self._at, self._out_at, self._sizes, self._dtypes, self._out_dtypes)])
         self._ref = ctypes.byref(self._list)
         self.workspace_bytes = int(lib().msda_grad_norm_workspace_bytes(self._ref))
 
+    def _read_memory(self):
+        """Where the tensors' storages lie and how large they are. The aliases change in
+        nothing else, and a storage freed and made anew may have its address again, and be
+        smaller."""
+        return (list(map(torch.UntypedStorage.data_ptr, self._storages)),
+                list(map(torch.UntypedStorage.nbytes, self._storages)))
+
     def _prepare(self):
-        if list(map(torch.Tensor.data_ptr, self._all)) != self._addresses:
+        if self._read_memory() != self._memory:
             self._read_addresses()
 
 
