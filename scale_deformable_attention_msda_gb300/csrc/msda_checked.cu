@@ -8,7 +8,12 @@
 // extent of the tensor it belongs to (in_tensor in msda_common.cuh); the
 // workspace passes (zero, convert, the fp16 workspace's prepare and finish)
 // each walk a flat range [0, n) of the buffer they are launched over, bounded
-// by their loop conditions. An access that would leave its tensor is
+// by their loop conditions. The layer norm's kernels check their reads and writes
+// of the rows, the statistics, the parameters and the partial sums in global
+// memory the same way (span_ok in msda_norm.cuh), the clipping's each unit against
+// its tensor and each vector and entry they scale (msda_gradnorm.cu); what those
+// keep in shared memory and the order of their blocks' partial results are not
+// checked. An access that would leave its tensor is
 // skipped and sets bit 0 of one device word per context; the host reads and
 // clears that word after a synchronisation. Nothing traps, so a fault found
 // this way leaves the context usable.

@@ -95,6 +95,17 @@ template <typename T> struct Unit {
     }
 };
 
+// Checked build: entries [at, at + n) lie in a tensor of `size`.
+__device__ __forceinline__ bool entries_ok(int64_t at, int64_t n, int64_t size, unsigned *err) {
+#ifdef MSDA_CHECKED
+    const bool ok = at >= 0 && at <= size - n;
+    if (!ok && err) atomicOr(err, 1u);
+    return ok;
+#else
+    return true;
+#endif
+}
+
 // Checked build: the unit lies in its tensor, and its tensor in the table.
 template <typename T>
 __device__ __forceinline__ bool unit_ok(const Unit<T> &u, int64_t size, int tensor, int count, unsigned *err) {
@@ -418,16 +429,18 @@ __device__ __forceinline__ void run_scale(const Table<N> &t, const Run &run, Fac
         for (int k = 0; k < per; ++k) {
             const int at = k * 32 + lane;
             raw[k] = make_uint4(0u, 0u, 0u, 0u);
-            if (at < vectors) raw[k] = __ldcs(reinterpret_cast<const uint4 *>(src + unit.body + at * V));
+            if (at < vectors && entries_ok(unit.body + at * V, V, t.size[i], err)) raw[k] = __ldcs(reinterpret_cast<const uint4 *>(src + unit.body + at * V));
         }
         raw[per] = make_uint4(0u, 0u, 0u, 0u);
-        for (int64_t j = unit.begin + lane; j < from; j += 32) put(dst + j, factor((A)as_double<T>(src[j])));
-        for (int64_t j = to + lane; j < unit.end; j += 32) put(dst + j, factor((A)as_double<T>(src[j])));
+        for (int64_t j = unit.begin + lane; j < from; j += 32)
+            if (entries_ok(j, 1, t.size[i], err)) put(dst + j, factor((A)as_double<T>(src[j])));
+        for (int64_t j = to + lane; j < unit.end; j += 32)
+            if (entries_ok(j, 1, t.size[i], err)) put(dst + j, factor((A)as_double<T>(src[j])));
 #pragma unroll
         for (int k = 0; k < per; ++k) {
             if (skew) shift_in(raw[k], raw[k + 1], lane, skew * (int)sizeof(T));
             const int at = k * 32 + lane;
-            if (at >= whole) continue;
+            if (at >= whole || !entries_ok(from + at * V, V, t.size[i], err)) continue;
             U *where = dst + from + at * V;
             if constexpr (sizeof(T) == 8) {
                 __stcs(reinterpret_cast<double2 *>(where),

@@ -48,6 +48,9 @@ struct NormArgs {
     // where two do not fit
     int tile_rows, stages;
     unsigned *err;                 // checked build: device word of range faults
+    // sums that the workspace has room for (last: between the pointers it cost the
+    // backward of 8192 x 1024 bf16 2%)
+    int64_t partials;
 };
 
 // How a problem's rows are held, chosen on the host.
@@ -96,10 +99,10 @@ template <typename T> __device__ __forceinline__ uint4 pack_pairs(const float2 *
     return pack16<T>(f);
 }
 
-// V parameters of type W at w as fp32 pairs; `fill` where w is NULL.
+// Parameters c to c + V of type W, of C at w, as fp32 pairs; `fill` where w is NULL.
 template <typename W, int V>
-__device__ __forceinline__ void load_params(float2 *v, const W *w, int c, float fill) {
-    if (!w) {
+__device__ __forceinline__ void load_params(float2 *v, const W *w, int c, float fill, int C, unsigned *err) {
+    if (!w || !span_ok(err, c, V, C)) {
 #pragma unroll
         for (int i = 0; i < V / 2; ++i) v[i] = both(fill);
         return;
@@ -227,8 +230,10 @@ template <int G, int V, int TH> struct GranuleMap : RowMap<G, TH> {
     // element offset of the thread's first granule in the tensor
     __device__ __forceinline__ int64_t start(int C) const { return first * C + (int64_t)t * V; }
     template <typename T>
-    __device__ __forceinline__ void store(T *p, int64_t at, int k, const float2 *v) const {
-        *reinterpret_cast<uint4 *>(p + at + k * threads * V) = pack_pairs<T>(v);
+    __device__ __forceinline__ void store(T *p, int64_t at, int k, const float2 *v, int64_t extent,
+                                          unsigned *err) const {
+        if (span_ok(err, at + k * threads * V, V, extent))
+            *reinterpret_cast<uint4 *>(p + at + k * threads * V) = pack_pairs<T>(v);
     }
     // Starts the copy of granule k of the row at element `at` into `to`. Where
     // the thread has no such granule, or the row is past the last (!there), the
@@ -336,11 +341,16 @@ __device__ __forceinline__ void load_pairs(float2 (&v)[P], const T *row, int t, 
 #pragma unroll
     for (int i = W; i < P; ++i) v[i] = load_pair<T, false>(row, t + 2 * i * g, g, C);
 }
+// Checked build: the pairs taken to lie in the row do.
+template <int P> __device__ __forceinline__ bool pairs_ok(unsigned *err, int t, int g, int C) {
+    return kWholePairs<P> == 0 || span_ok(err, t + (2 * kWholePairs<P> - 1) * g, 1, C);
+}
 template <int P, typename W>
-__device__ __forceinline__ void load_weights(float2 (&v)[P], const W *w, int t, int g, int C, float fill) {
+__device__ __forceinline__ void load_weights(float2 (&v)[P], const W *w, int t, int g, int C, float fill,
+                                             unsigned *err) {
 #pragma unroll
     for (int i = 0; i < P; ++i) v[i] = both(fill);
-    if (w) load_pairs(v, w, t, g, C);
+    if (w && pairs_ok<P>(err, t, g, C)) load_pairs(v, w, t, g, C);
 }
 template <int P, typename T>
 __device__ __forceinline__ void store_pairs(T *row, int t, int g, int C, const float2 (&v)[P]) {

@@ -255,6 +255,7 @@ msda_status_t msda_layer_norm_backward(const void *grad_out, const void *grad_su
     a.grad_weight = grad_weight;
     a.grad_bias = grad_bias;
     a.partial = columns ? static_cast<float *>(workspace) : nullptr;
+    a.partials = (int64_t)(workspace_bytes / (dtype == MSDA_F64 ? 8 : 4));
     a.N = d.N;
     a.C = (int)d.C;
     a.group = p.group;

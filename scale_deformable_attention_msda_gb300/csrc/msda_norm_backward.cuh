@@ -47,6 +47,7 @@ __device__ __forceinline__ void leave_partials(const NormArgs &a, const float *c
         return v;
     };
     if (gridDim.x > 1) {
+        if (!span_ok(a.err, (int64_t)blockIdx.x * n, n, a.partials)) return;
         float *mine = a.partial + (int64_t)blockIdx.x * n;
 #pragma unroll 4
         for (int j = threadIdx.x; j < n; j += blockDim.x) mine[j] = column(j);
@@ -104,10 +105,10 @@ __global__ void __launch_bounds__(TH) norm_backward_kernel(const NormArgs a) {
     for (int k = 0; k < KV; ++k) {
 #pragma unroll
         for (int i = 0; i < P; ++i) dw[k][i] = db[k][i] = both(0.0f);
-        load_params<W, V>(pw[k], map.held(k) ? w : nullptr, map.channel(k), 1.0f);
+        load_params<W, V>(pw[k], map.held(k) ? w : nullptr, map.channel(k), 1.0f, C, a.err);
     }
     float mu = 0.0f, rs = 0.0f;
-    if (map.first < a.N) {
+    if (map.first < a.N && span_ok(a.err, map.first, 1, a.N)) {
         mu = __ldg(mean + map.first);
         rs = __ldg(rstd + map.first);
     }
@@ -119,7 +120,7 @@ __global__ void __launch_bounds__(TH) norm_backward_kernel(const NormArgs a) {
         const bool valid = G == 0 || G == 32 || row < a.N;
         const float m = mu, r = rs;
         mu = rs = 0.0f;
-        if (row + map.step < a.N) {
+        if (row + map.step < a.N && span_ok(a.err, row + map.step, 1, a.N)) {
             mu = __ldg(mean + row + map.step);
             rs = __ldg(rstd + row + map.step);
         }
@@ -160,7 +161,7 @@ __global__ void __launch_bounds__(TH) norm_backward_kernel(const NormArgs a) {
                     g[k][i] = mul2(fma2(xh[k][i], c2, add2(g[k][i], c1)), both(r));
                     if (ds) g[k][i] = add2(g[k][i], e[i]);
                 }
-                if (valid && map.held(k)) map.store(dx, here, k, g[k]);
+                if (valid && map.held(k)) map.store(dx, here, k, g[k], extent, a.err);
             }
         }
         fetch(slot);
@@ -224,6 +225,7 @@ norm_backward_tile_kernel(const NormArgs a) {
         os(a.grad_x, extent);
     const int ds_at = (tensors - 1) * places;
     const int64_t step = (int64_t)gridDim.x * rows;
+    (void)pairs_ok<P>(a.err, t, g, C);
     auto fetch = [&](int64_t row, int stage) {
         if (row < a.N) {
             uint4 *to = ring + stage * tensors * places;
@@ -239,7 +241,7 @@ norm_backward_tile_kernel(const NormArgs a) {
     fetch(begin, 0);
     if (a.stages == 2) fetch(begin + step, 1);
     float2 pw[P], dw[P], db[P];
-    load_weights(pw, w, t, g, C, 1.0f);
+    load_weights(pw, w, t, g, C, 1.0f, a.err);
 #pragma unroll
     for (int i = 0; i < P; ++i) dw[i] = db[i] = both(0.0f);
     int stage = 0;
@@ -247,7 +249,7 @@ norm_backward_tile_kernel(const NormArgs a) {
         const int64_t at = tile * C;
         const int there = (int)(a.N - tile < rows ? a.N - tile : rows);
         float m = 0.0f, r = 0.0f;        // of the group's next row
-        if (map.index < there) {
+        if (map.index < there && span_ok(a.err, tile + map.index, 1, a.N)) {
             m = __ldg(mean + tile + map.index);
             r = __ldg(rstd + tile + map.index);
         }
@@ -265,7 +267,7 @@ norm_backward_tile_kernel(const NormArgs a) {
             const int row = lead + map.index, from = row * C;
             const bool valid = row < there;
             const float mu = m, rstd_row = r;
-            if (row + map.rows < there) {
+            if (row + map.rows < there && span_ok(a.err, tile + row + map.rows, 1, a.N)) {
                 m = __ldg(mean + tile + row + map.rows);
                 r = __ldg(rstd + tile + row + map.rows);
             }
@@ -343,8 +345,8 @@ norm_backward_tile_kernel(const NormArgs a) {
 // (threads / TW)th row of partials each. TW = 8 (one 32-byte sector) spreads
 // few channels over more SMs; the rows' reads are what it waits for.
 template <typename W, typename A, int TW>
-__global__ void __launch_bounds__(1024) norm_columns_kernel(const A *partial, int rows, int C,
-                                                            W *grad_weight, W *grad_bias) {
+__global__ void __launch_bounds__(1024) norm_columns_kernel(const A *partial, int64_t partials, int rows, int C,
+                                                            W *grad_weight, W *grad_bias, unsigned *err) {
     __shared__ A part[32][TW];
     cudaGridDependencySynchronize();
     const int tx = threadIdx.x % TW, ty = threadIdx.x / TW, step = blockDim.x / TW;
@@ -352,7 +354,7 @@ __global__ void __launch_bounds__(1024) norm_columns_kernel(const A *partial, in
     const bool mine = j < 2 * (int64_t)C;
     const int64_t c = j < C ? j : j - C;
     A v = 0;
-    if (mine) {
+    if (mine && span_ok(err, (int64_t)(rows - 1) * 2 * C + j, 1, partials)) {
 #pragma unroll 8
         for (int r = ty; r < rows; r += step) v += partial[r * 2 * (int64_t)C + j];
     }
@@ -441,6 +443,7 @@ __global__ void __launch_bounds__(128) norm_backward_columns_general_kernel(cons
         dw += g * ((s - m) * r);
         db += g;
     }
+    if (!span_ok(a.err, (int64_t)blockIdx.y * 2 * a.C + c, a.C + 1, a.partials)) return;
     A *mine = reinterpret_cast<A *>(a.partial) + (int64_t)blockIdx.y * 2 * a.C;
     mine[c] = dw;
     mine[a.C + c] = db;
@@ -463,8 +466,8 @@ static cudaError_t launch_columns(const NormArgs &a, int rows, cudaStream_t stre
     cfg.attrs = &early;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, narrow ? norm_columns_kernel<W, A, 8> : norm_columns_kernel<W, A, 32>,
-                              reinterpret_cast<const A *>(a.partial), rows, a.C,
-                              static_cast<W *>(a.grad_weight), static_cast<W *>(a.grad_bias));
+                              reinterpret_cast<const A *>(a.partial), a.partials, rows, a.C,
+                              static_cast<W *>(a.grad_weight), static_cast<W *>(a.grad_bias), a.err);
 }
 
 template <typename T, typename W>

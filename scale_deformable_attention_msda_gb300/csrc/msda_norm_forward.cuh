@@ -62,8 +62,8 @@ norm_forward_kernel(const NormArgs a) {
 #pragma unroll
     for (int k = 0; k < KV; ++k) {
         const int c = map.channel(k);
-        load_params<W, V>(pw[k], map.held(k) ? w : nullptr, c, 1.0f);
-        load_params<W, V>(pb[k], map.held(k) ? b : nullptr, c, 0.0f);
+        load_params<W, V>(pw[k], map.held(k) ? w : nullptr, c, 1.0f, C, a.err);
+        load_params<W, V>(pb[k], map.held(k) ? b : nullptr, c, 0.0f, C, a.err);
     }
     for (int64_t row = map.first, lead = map.lead; lead < a.N; row += map.step, lead += map.step, here += hop) {
         const bool valid = G == 0 || G == 32 || row < a.N;
@@ -79,7 +79,7 @@ norm_forward_kernel(const NormArgs a) {
 #pragma unroll
                 for (int i = 0; i < P; ++i) s[k][i] = add2(s[k][i], e[i]);
             }
-            if (a.sum && valid && map.held(k)) map.store(static_cast<T *>(a.sum), here, k, s[k]);
+            if (a.sum && valid && map.held(k)) map.store(static_cast<T *>(a.sum), here, k, s[k], extent, a.err);
 #pragma unroll
             for (int i = 0; i < P; ++i) acc = add2(acc, s[k][i]);
         }
@@ -113,7 +113,7 @@ norm_forward_kernel(const NormArgs a) {
 #pragma unroll
             for (int i = 0; i < P; ++i)
                 s[k][i] = fma2(mul2(add2(s[k][i], both(-f.shift)), both(rstd)), pw[k][i], pb[k][i]);
-            if (valid && map.held(k)) map.store(static_cast<T *>(a.out), here, k, s[k]);
+            if (valid && map.held(k)) map.store(static_cast<T *>(a.out), here, k, s[k], extent, a.err);
         }
     }
     fetch_wait<0>();
@@ -138,6 +138,7 @@ norm_forward_tile_kernel(const NormArgs a) {
     uint4 *const outs = ring + a.stages * tensors * places;
     const Spans<T> xs(a.x, extent), rs(a.residual, extent), os(a.out, extent), ss(a.sum, extent);
     const int64_t step = (int64_t)gridDim.x * rows;
+    (void)pairs_ok<P>(a.err, t, g, C);
     auto fetch = [&](int64_t row, int stage) {
         if (row < a.N) {
             uint4 *to = ring + stage * tensors * places;
@@ -153,8 +154,8 @@ norm_forward_tile_kernel(const NormArgs a) {
     constexpr int HELD = kHoldsWeights<P> ? P : 1;
     float2 pw[HELD], pb[HELD];
     if constexpr (kHoldsWeights<P>) {
-        load_weights(pw, w, t, g, C, 1.0f);
-        load_weights(pb, b, t, g, C, 0.0f);
+        load_weights(pw, w, t, g, C, 1.0f, a.err);
+        load_weights(pb, b, t, g, C, 0.0f, a.err);
     }
     int stage = 0;
     for (int64_t tile = begin; tile < a.N; tile += step) {
@@ -224,10 +225,10 @@ norm_forward_tile_kernel(const NormArgs a) {
                 for (int i = 0; i < P; ++i) s[i] = fma2(s[i], pw[i], pb[i]);
             } else {
                 float2 e[P];
-                load_weights(e, w, t, g, C, 1.0f);
+                load_weights(e, w, t, g, C, 1.0f, a.err);
 #pragma unroll
                 for (int i = 0; i < P; ++i) s[i] = mul2(s[i], e[i]);
-                load_weights(e, b, t, g, C, 0.0f);
+                load_weights(e, b, t, g, C, 0.0f, a.err);
 #pragma unroll
                 for (int i = 0; i < P; ++i) s[i] = add2(s[i], e[i]);
             }
