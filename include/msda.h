@@ -321,8 +321,9 @@ MSDA_API msda_status_t msda_debug_corners(const int64_t *spatial_shapes,
  * that would leave its tensor is skipped -- a load yields zeros, a store or
  * add does nothing -- and a per-context fault word is set; nothing traps. The
  * workspace passes (zero, convert, the fp16 workspace's prepare and finish)
- * walk a flat range of the buffer they are given, bounded by their loops. It is a debugging stand-in for
- * a memory checker, much slower than libmsda.so. The normal library exports
+ * walk a flat range of the buffer they are given, bounded by their loops. Layer
+ * norm's kernels are checked alike, clipping's by tensor, vector and entry. It
+ * is a debugging stand-in for a memory checker, much slower than libmsda.so. The normal library exports
  * the same three entry points and never sets the word.
  * msda_checked_build: 1 in libmsda_checked.so, 0 in libmsda.so.
  * msda_device_check: synchronizes `stream`, then reads and clears the fault
@@ -371,9 +372,10 @@ MSDA_API int msda_version(void);
 /* N rows of C channels, contiguous. Supported: N >= 0 (zero is a valid empty
  * call), 1 <= C <= 2^20, N*C <= 2^60. Every C and every element alignment is
  * accepted. Rows that all start on 16-byte boundaries (C a multiple of
- * 16 / element size, pointers 16-byte aligned) are the fastest; fp64 and the
- * longest rows (over 13,312 fp32 or 16,384 16-bit channels; over 8,192 in the
- * backward where rows start anywhere) take plain loops. */
+ * 16 / element size, pointers 16-byte aligned) are the fastest. fp64 and the
+ * longest rows take plain loops: over 16,384 channels, but over 13,312 fp32
+ * channels in the backward; of rows that start anywhere over 14,064 fp32 or
+ * 16,384 16-bit channels, and over 8,192 in the backward. */
 typedef struct {
     int64_t N, C;
 } msda_norm_dims_t;
@@ -388,10 +390,13 @@ typedef struct {
  *   sum               (N, C) `dtype`: receives s, rounded; NULL: not wanted
  *   mean, rstd        (N,) float (double for MSDA_F64): what the backward
  *                     needs; both NULL or neither
- * param_dtype: `dtype`, or MSDA_F32 with 16-bit data. eps >= 0; a row of
- * equal entries with eps = 0 gives NaN. A row with a non-finite entry, or
- * whose squared distances from the mean leave fp32's range, gives non-finite
- * results in that row alone. Outputs must not overlap inputs.
+ * param_dtype: `dtype`, or MSDA_F32 with 16-bit data. eps >= 0, rounded to
+ * fp32 but for MSDA_F64; a row of equal entries with eps = 0 gives NaN. A row
+ * with a non-finite entry, or whose sum or squared distances from the mean
+ * leave the range of fp32 (fp64), gives non-finite results in that row alone.
+ * The roundings of a row's mean do not show where it is large beside the
+ * spread, but in `mean`, which is rounded to its type and which the backward
+ * takes its distances from. Outputs must not overlap inputs.
  * Alignment: element size. Errors: MSDA_ERR_NULL, _SHAPE (also eps < 0 or
  * NaN), _DTYPE, _ALIGN before any launch; MSDA_ERR_CUDA. */
 MSDA_API msda_status_t msda_layer_norm_forward(const void *x, const void *residual,
@@ -454,10 +459,15 @@ typedef enum {
 MSDA_API size_t msda_grad_norm_workspace_bytes(const msda_grad_list_t *list);
 
 /* Writes the norm to `norm`: one float, or one double where the list has an
- * MSDA_F64 tensor (an empty one counts). Sums are added in fp64 in an order
- * that the list alone fixes, so the same call gives the same bits; squares
- * that leave fp32's range are taken in fp64. NaN in any entry gives NaN; an
- * infinite entry gives an infinite norm. An empty list has norm 0.
+ * MSDA_F64 tensor (an empty one counts). Squares of 16- and 32-bit entries are
+ * added in fp32, at most 66 at a time, and these sums in pairs of fp32 that
+ * carry their errors, or in fp64: the norm is within 33 * 2^-24 of its value
+ * before it is rounded, for the share that such tensors have in a double too.
+ * Squares that leave fp32's range, and all of MSDA_F64 entries, are taken and
+ * added in fp64 (entries over 1e154 give infinity). The order is fixed by the
+ * list, its sizes and its alignment: the same call gives the same bits. NaN in
+ * any entry gives NaN; an infinite entry, or a norm past its type's largest
+ * number, gives infinity. An empty list has norm 0. MSDA_NORM_INF is exact.
  * workspace: at least msda_grad_norm_workspace_bytes(list) bytes, 16-byte
  *   aligned, owned by the caller, overwritten.
  * Errors: MSDA_ERR_NULL, _SHAPE, _DTYPE (types and kind), _ALIGN (element
@@ -465,11 +475,16 @@ MSDA_API size_t msda_grad_norm_workspace_bytes(const msda_grad_list_t *list);
 MSDA_API msda_status_t msda_grad_norm(const msda_grad_list_t *list, int kind, void *norm,
                                       void *workspace, size_t workspace_bytes, void *stream);
 
-/* As msda_grad_norm, then outs[i] = grads[i] * min(1, max_norm / (norm + 1e-6)),
- * rounded once. Nothing is read on the host: the factor is found on the device.
- * An infinite norm makes the factor 0 (and infinite entries NaN), a NaN norm
- * makes every entry NaN. Gradients whose norm is within max_norm keep their
- * bits. max_norm >= 0 (infinity is allowed), else MSDA_ERR_SHAPE. */
+/* As msda_grad_norm, then outs[i] = grads[i] * min(1, max_norm / (norm + 1e-6)).
+ * The factor is rounded to fp32 (fp64 for MSDA_F64), its product with an entry
+ * to the output's type. Nothing is read on the host: the factor is found on the
+ * device, from the norm as it was before it was rounded to `norm`'s type.
+ * An infinite entry makes the factor 0 (and infinite entries NaN; all entries
+ * where max_norm is infinite too), a NaN norm makes every entry NaN. Gradients
+ * with norm + 1e-6 <= max_norm keep their bits; a norm between max_norm - 1e-6
+ * and max_norm is scaled down a little, so that a max_norm near 1e-6 or below
+ * shrinks smaller gradients as well. max_norm >= 0 (infinity is allowed), else
+ * MSDA_ERR_SHAPE. */
 MSDA_API msda_status_t msda_clip_grad_norm(const msda_grad_list_t *list, int kind, double max_norm,
                                            void *norm, void *workspace, size_t workspace_bytes,
                                            void *stream);

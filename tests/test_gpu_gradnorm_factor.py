@@ -63,3 +63,45 @@ def test_factors_that_are_ordinary_change_no_bit():
     # the factor from the norm's fp64 value, which the returned float is a rounding of
     steps = [near, torch.nextafter(near, near * 0), torch.nextafter(near, near * 2)]
     assert any(torch.equal(out, g * f.cuda()) for f in steps)
+
+
+def clipped(value, max_norm, kind=2.0, dt=F64):
+    g = torch.tensor([value], device="cuda", dtype=dt)
+    binding.msda_clip_grad_norm([g], max_norm, kind)
+    return g
+
+
+def test_a_norm_just_under_the_limit():
+    """The factor is max_norm / (norm + 1e-6): within 1e-6 of the limit it is below one."""
+    for dt in (F32, F64):
+        for value, max_norm in ((1.0 - 2e-6, 1.0), (0.5, 0.5 + 2e-6), (0.0, 1e-7), (3.0, math.inf)):
+            assert torch.equal(clipped(value, max_norm, dt=dt), torch.tensor([value], device="cuda", dtype=dt))
+        for value, max_norm in ((1.0 - 5e-7, 1.0), (0.5, 0.5), (5e-8, 1e-7)):
+            held = torch.tensor([value], dtype=dt).double()
+            want = held * (max_norm / (held + 1e-6))
+            got = clipped(value, max_norm, dt=dt).double().cpu()
+            assert got < held
+            # one entry: its square and the root in fp64 or fp32, the factor, the product
+            assert (got - want).abs() <= 6 * HALF[dt] * want
+
+
+def test_what_the_header_says_of_infinities():
+    assert clipped(math.inf, math.inf).isnan() and clipped(math.inf, 1.0).isnan()
+    g = torch.tensor([math.inf, 2.0], device="cuda")
+    binding.msda_clip_grad_norm([g], 1.0)
+    assert g[0].isnan() and g[1] == 0
+    # the float is past its range, the norm that makes the factor is not
+    g = torch.full((100,), 3e38, device="cuda")
+    assert binding.msda_clip_grad_norm([g], 1.0) == math.inf
+    assert ((g.double() - 0.1).abs() <= 40 * 2.0 ** -24 * 0.1).all()
+    assert binding.msda_grad_norm([torch.full((2,), 1e160, device="cuda", dtype=F64)]) == math.inf
+
+
+def test_a_double_norm_of_fp32_entries():
+    """Its fp32 share is within the bound of fp32 lists."""
+    gen = torch.Generator(device="cuda").manual_seed(9)
+    g = torch.randn(1_000_003, device="cuda", generator=gen)
+    d = torch.full((1,), 1e-3, device="cuda", dtype=F64)
+    norm = binding.msda_grad_norm([g, d])
+    want = (g.double().square().sum() + 1e-6).sqrt()
+    assert norm.dtype == F64 and abs(norm - want) <= (33 * 2.0 ** -24) * want
