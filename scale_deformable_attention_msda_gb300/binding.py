@@ -732,21 +732,17 @@ class GradientBuffers:
         self._dtypes = (ctypes.c_int32 * n)(*[_DTYPES[g.dtype] for g in grads])
         self._out_dtypes = (ctypes.c_int32 * n)(*[_DTYPES[o.dtype] for o in outs])
         self._read_addresses()
+        self._watch()
 
     def _read_addresses(self):
         spans = sorted(_span(t) for t in self._all if t.numel())
         for (_, end), (begin, _) in zip(spans, spans[1:]):
             if begin < end:
                 raise ValueError("two of the tensors share memory")
-        storages = {}
         for t in self._all:
-            storage = t.untyped_storage()
-            storages[storage._cdata] = storage
-            held = storage.nbytes() - t.storage_offset() * t.element_size()
+            held = t.untyped_storage().nbytes() - t.storage_offset() * t.element_size()
             if held < t.numel() * t.element_size():
                 raise ValueError("a tensor's storage was resized to less than the tensor")
-        self._storages = list(storages.values())
-        self._memory = self._read_memory()
         addresses = list(map(torch.Tensor.data_ptr, self._all))
         n = len(self._grads)
         self._at = (ctypes.c_void_p * n)(*addresses[:n])
@@ -756,6 +752,11 @@ class GradientBuffers:
         self._ref = ctypes.byref(self._list)
         self.workspace_bytes = int(lib().msda_grad_norm_workspace_bytes(self._ref))
 
+    def _watch(self):
+        storages = [t.untyped_storage() for t in self._all]
+        self._storages = list({s._cdata: s for s in storages}.values())
+        self._memory = self._read_memory()
+
     def _read_memory(self):
         """Where the tensors' storages lie and how large they are. The aliases change in
         nothing else, and a storage freed and made anew may have its address again, and be
@@ -764,8 +765,20 @@ class GradientBuffers:
                 list(map(torch.UntypedStorage.nbytes, self._storages)))
 
     def _prepare(self):
-        if self._read_memory() != self._memory:
+        memory = self._read_memory()
+        if memory != self._memory:
             self._read_addresses()
+            self._memory = memory
+
+
+class _OneCall(GradientBuffers):
+    """A list given to a call: read by that call alone."""
+
+    def _watch(self):
+        pass
+
+    def _prepare(self):
+        pass
 
 
 def _norm_kind(norm_type):
@@ -801,7 +814,7 @@ def _grad_norm(grads, norm_type, max_norm, stream):
     else:
         grads = list(grads)
         _refuse_modes(name, grads)
-        buf = GradientBuffers(grads)
+        buf = _OneCall(grads)
     if buf.device is None:               # an empty list
         return torch.zeros(())
     if stream is not None or torch._C._cuda_getDevice() != buf.device.index:
@@ -832,7 +845,8 @@ def clip_grad_norm_(parameters, max_norm: float, norm_type: float = 2.0,
     if isinstance(parameters, torch.Tensor):
         parameters = [parameters]
     grads = [p.grad for p in parameters if p.grad is not None]
-    buf = GradientBuffers(grads)
+    _refuse_modes("clip_grad_norm_", grads)
+    buf = _OneCall(grads)
     if error_if_nonfinite:
         norm = msda_grad_norm(buf, norm_type)
         if not torch.isfinite(norm):

@@ -89,7 +89,17 @@ CALLS = {
     "msda_layer_norm_backward": lambda t: binding.msda_layer_norm_backward(t, t, t[:, 0], t[:, 0])[0],
     "msda_grad_norm": lambda t: binding.msda_grad_norm([t]),
     "msda_clip_grad_norm": lambda t: binding.msda_clip_grad_norm([t], 1.0),
+    "clip_grad_norm_": lambda t: binding.clip_grad_norm_(Holder(t), 1.0),
 }
+
+
+class Holder(list):
+    """A parameter whose gradient is t, in a list."""
+
+    def __init__(self, t):
+        p = torch.nn.Parameter(torch.zeros(3, 8))
+        p.grad = t
+        super().__init__([p])
 
 
 @pytest.mark.parametrize("name", CALLS)
