@@ -172,11 +172,8 @@ __device__ __forceinline__ void row_sum(float (&v)[R], BlockScratch *scratch, in
     }
 }
 
-// 1 / sqrt of a row's variance and eps, within 2 ulp; NaN where that left fp32's range.
-__device__ __forceinline__ float row_rstd(float squares, float inv_C, float eps) {
-    const float v = fmaf(squares, inv_C, eps);
-    return rsqrtf(v) + (v - v);
-}
+// 1 / sqrt of a row's variance and eps, within 2 ulp; NaN where those left fp32's range.
+__device__ __forceinline__ float row_rstd(float v) { return rsqrtf(v) + (v - v); }
 
 // A row's mean is off by the roundings of its sum, up to 28 of them, and rstd
 // multiplies these: a row of 10000.1 throughout would come out as -0.3. The distances
@@ -184,8 +181,7 @@ __device__ __forceinline__ float row_rstd(float squares, float inv_C, float eps)
 // remainder, so that an exact one comes out exact: in a row of equal entries every
 // distance is the same multiple j <= 28 of one step, the sums of j and j^2 over up to
 // 16,384 channels are exact below 2^24, and the shift is that distance and the sum of
-// the squares about the corrected mean 0. Costs 1 to 4% of the rows form's time (44,446
-// x 256 bf16 12.9 us, 13.3).
+// the squares about the corrected mean 0.
 struct MeanFix { float shift, squares; };
 __device__ __forceinline__ MeanFix fix_mean(float sum, float squares, float C, float inv_C) {
     float shift = sum * inv_C;
@@ -194,12 +190,20 @@ __device__ __forceinline__ MeanFix fix_mean(float sum, float squares, float C, f
     return {shift, squares < 0.0f ? 0.0f : squares};     // NaN stays
 }
 
-// The tiles and general forms, which issue or add what they wait for, do it only for
-// rows whose mean is more than kFar / rstd (20,011 x 777 fp16 25.8 us without, 26.5 so,
-// 28.4 for every row); in others the mean's roundings are at most 28 * 2^-24 * kFar of
-// a normalised row.
+// Where that is not done for every row (kFixAll), it is for rows whose mean is more than
+// kFar / rstd; in others the mean's roundings are at most 28 * 2^-24 * kFar of a
+// normalised row. v: the variance and eps. (Zeros, infinities and NaN are far.)
 constexpr float kFar = 2.0f;
-__device__ __forceinline__ bool is_far(float mean, float rstd) { return !(fabsf(mean) * rstd <= kFar); }
+template <typename A> __device__ __forceinline__ bool is_far(A mean, A v) {
+    return !(mean * mean < (A)(kFar * kFar) * v);
+}
+
+// Rows form: groups of warps, which wait for their sums anyway, and fp32 rows fix every
+// mean (86,016 x 256 fp32 40.8 us, 42.6 the other way; 8192 x 4096 bf16 45.0 us, 49.5),
+// lanes with 16-bit rows those of far rows (44,446 x 256 bf16 11.7 us, 12.0; without any
+// fix 11.3). The tiles and general forms, which issue or add what they wait for, the far
+// ones (20,011 x 777 fp16 26.1 us, 28.4; without 25.3).
+template <typename T, int G> constexpr bool kFixAll = G == 0 || sizeof(T) == 4;
 
 // The place of a thread among the rows. TH: threads of a block whose groups are
 // lanes of a warp.

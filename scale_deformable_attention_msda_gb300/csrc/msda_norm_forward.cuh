@@ -88,6 +88,7 @@ norm_forward_kernel(const NormArgs a) {
         fetch(slot);
         slot = slot + tall == begin + S * tall ? begin : slot + tall;
         const float mean = v[0] * inv_C;
+        float shift = 0.0f, squares;
         float2 off = both(0.0f);
         acc = both(0.0f);
 #pragma unroll
@@ -97,22 +98,45 @@ norm_forward_kernel(const NormArgs a) {
             for (int i = 0; i < P; ++i) s[k][i] = add2(s[k][i], both(m));
 #pragma unroll
             for (int i = 0; i < P; ++i) acc = fma2(s[k][i], s[k][i], acc);
+            if constexpr (kFixAll<T, G>) {
 #pragma unroll
-            for (int i = 0; i < P; ++i) off = add2(off, s[k][i]);
+                for (int i = 0; i < P; ++i) off = add2(off, s[k][i]);
+            }
         }
-        float u[2] = {off.x + off.y, acc.x + acc.y};
-        row_sum<G>(u, &scratch, turn, map.threads, map.index);
-        const MeanFix f = fix_mean(u[0], u[1], (float)C, inv_C);
-        const float rstd = row_rstd(f.squares, inv_C, (float)a.eps);
+        if constexpr (kFixAll<T, G>) {
+            float u[2] = {off.x + off.y, acc.x + acc.y};
+            row_sum<G>(u, &scratch, turn, map.threads, map.index);
+            const MeanFix f = fix_mean(u[0], u[1], (float)C, inv_C);
+            shift = f.shift;
+            squares = f.squares;
+        } else {
+            v[0] = acc.x + acc.y;
+            row_sum<G>(v, &scratch, turn, map.threads, map.index);
+            squares = v[0];
+            const bool far = is_far(mean, fmaf(squares, inv_C, (float)a.eps));
+            if (__any_sync(0xffffffffu, far)) {      // the same for a group's lanes
+#pragma unroll
+                for (int k = 0; k < KV; ++k) {
+#pragma unroll
+                    for (int i = 0; i < P; ++i) off = add2(off, s[k][i]);
+                }
+                float u[1] = {off.x + off.y};
+                row_sum<G>(u, &scratch, turn, map.threads, map.index);
+                const MeanFix f = fix_mean(u[0], squares, (float)C, inv_C);
+                shift = far ? f.shift : 0.0f;
+                squares = far ? f.squares : squares;
+            }
+        }
+        const float rstd = row_rstd(fmaf(squares, inv_C, (float)a.eps));
         if (map.t == 0 && valid && a.mean && span_ok(a.err, row, 1, a.N)) {
-            static_cast<float *>(a.mean)[row] = mean + f.shift;
+            static_cast<float *>(a.mean)[row] = mean + shift;
             static_cast<float *>(a.rstd)[row] = rstd;
         }
 #pragma unroll
         for (int k = 0; k < KV; ++k) {
 #pragma unroll
             for (int i = 0; i < P; ++i)
-                s[k][i] = fma2(mul2(add2(s[k][i], both(-f.shift)), both(rstd)), pw[k][i], pb[k][i]);
+                s[k][i] = fma2(mul2(add2(s[k][i], both(-shift)), both(rstd)), pw[k][i], pb[k][i]);
             if (valid && map.held(k)) map.store(static_cast<T *>(a.out), here, k, s[k], extent, a.err);
         }
     }
@@ -197,8 +221,8 @@ norm_forward_tile_kernel(const NormArgs a) {
             }
             v[0] = acc.x + acc.y;
             row_sum<G>(v, &scratch, turn, g, map.index);
-            float rstd = row_rstd(v[0], inv_C, (float)a.eps);
-            const bool far = is_far(mean, rstd);
+            float squares = v[0];
+            const bool far = is_far(mean, fmaf(squares, inv_C, (float)a.eps));
             if (G == 0 ? far : __any_sync(0xffffffffu, far)) {   // the same for a group's threads
                 acc = both(0.0f);
 #pragma unroll
@@ -206,14 +230,15 @@ norm_forward_tile_kernel(const NormArgs a) {
                 float u[1] = {acc.x + acc.y};
                 row_sum<G>(u, &scratch, turn, g, map.index);
                 if (far) {
-                    const MeanFix f = fix_mean(u[0], v[0], (float)C, inv_C);
-                    rstd = row_rstd(f.squares, inv_C, (float)a.eps);
+                    const MeanFix f = fix_mean(u[0], squares, (float)C, inv_C);
+                    squares = f.squares;
                     mean += f.shift;
 #pragma unroll
                     for (int i = 0; i < P; ++i) s[i] = add2(s[i], both(-f.shift));
                 }
             }
             if (!valid) continue;
+            const float rstd = row_rstd(fmaf(squares, inv_C, (float)a.eps));
             if (t == 0 && a.mean && span_ok(a.err, tile + row, 1, a.N)) {
                 static_cast<float *>(a.mean)[tile + row] = mean;
                 static_cast<float *>(a.rstd)[tile + row] = rstd;
@@ -287,7 +312,7 @@ __global__ void __launch_bounds__(512) norm_forward_general_kernel(const NormArg
         }
         v = block_sum<A>(v, scratch) / (A)a.C + (A)a.eps;
         A rstd = (A)1 / sqrt(v) + (v - v);               // a variance out of range: NaN
-        if (!(fabs(mean) * rstd <= (A)kFar)) {           // the same for all threads
+        if (is_far(mean, v)) {                           // the same for all threads
             const A first = at(0);
             v = 0;
             for (int c = threadIdx.x; c < a.C; c += blockDim.x) v += at(c) - first;

@@ -133,3 +133,12 @@ def test_rows_that_leave_the_arithmetics_range(C, dt, size):
     out = binding.layer_norm(x, w, b)
     keep = torch.arange(20, device="cuda") != 7
     assert torch.equal(out[keep], clean[keep]) and not out[7].isfinite().any()
+
+
+@pytest.mark.parametrize("dt", [F32, BF16, F64], ids=IDS)
+@pytest.mark.parametrize("C", COLUMNS)
+def test_equal_rows_without_eps(C, dt):
+    """NaN whatever the entry's size, where squares of the mean or the distances vanish too."""
+    values = torch.tensor([0.0, 1e-38, 1e-30, 1.1e-22, 1e-10, -3.3, 1e10, 1.7e19, 3e34], device="cuda", dtype=F64).to(dt)
+    x = values[:, None].expand(-1, C).contiguous()
+    assert binding.layer_norm(x, eps=0.0).isnan().all()
