@@ -172,8 +172,11 @@ __device__ __forceinline__ void row_sum(float (&v)[R], BlockScratch *scratch, in
     }
 }
 
-// 1 / sqrt of a row's variance and eps, within 2 ulp; NaN where those left fp32's range.
-__device__ __forceinline__ float row_rstd(float v) { return rsqrtf(v) + (v - v); }
+// 1 / sqrt of a row's variance and eps, within 2 ulp; NaN where the squares left fp32's
+// range (eps may: rstd is 0 then).
+__device__ __forceinline__ float row_rstd(float squares, float inv_C, float eps) {
+    return rsqrtf(fmaf(squares, inv_C, eps)) + (squares - squares);
+}
 
 // A row's mean is off by the roundings of its sum, up to 28 of them, and rstd
 // multiplies these: a row of 10000.1 throughout would come out as -0.3. The distances
@@ -200,7 +203,7 @@ template <typename A> __device__ __forceinline__ bool is_far(A mean, A v) {
 
 // Rows form: groups of warps, which wait for their sums anyway, and fp32 rows fix every
 // mean (86,016 x 256 fp32 40.8 us, 42.6 the other way; 8192 x 4096 bf16 45.0 us, 49.5),
-// lanes with 16-bit rows those of far rows (44,446 x 256 bf16 11.7 us, 12.0; without any
+// lanes with 16-bit rows those of far rows (44,446 x 256 bf16 11.8 us, 12.0; without any
 // fix 11.3). The tiles and general forms, which issue or add what they wait for, the far
 // ones (20,011 x 777 fp16 26.1 us, 28.4; without 25.3).
 template <typename T, int G> constexpr bool kFixAll = G == 0 || sizeof(T) == 4;

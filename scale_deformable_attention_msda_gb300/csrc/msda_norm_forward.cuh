@@ -127,7 +127,7 @@ norm_forward_kernel(const NormArgs a) {
                 squares = far ? f.squares : squares;
             }
         }
-        const float rstd = row_rstd(fmaf(squares, inv_C, (float)a.eps));
+        const float rstd = row_rstd(squares, inv_C, (float)a.eps);
         if (map.t == 0 && valid && a.mean && span_ok(a.err, row, 1, a.N)) {
             static_cast<float *>(a.mean)[row] = mean + shift;
             static_cast<float *>(a.rstd)[row] = rstd;
@@ -238,7 +238,7 @@ norm_forward_tile_kernel(const NormArgs a) {
                 }
             }
             if (!valid) continue;
-            const float rstd = row_rstd(fmaf(squares, inv_C, (float)a.eps));
+            const float rstd = row_rstd(squares, inv_C, (float)a.eps);
             if (t == 0 && a.mean && span_ok(a.err, tile + row, 1, a.N)) {
                 static_cast<float *>(a.mean)[tile + row] = mean;
                 static_cast<float *>(a.rstd)[tile + row] = rstd;
@@ -310,8 +310,8 @@ __global__ void __launch_bounds__(512) norm_forward_general_kernel(const NormArg
             const A d = at(c) - mean;
             v += d * d;
         }
-        v = block_sum<A>(v, scratch) / (A)a.C + (A)a.eps;
-        A rstd = (A)1 / sqrt(v) + (v - v);               // a variance out of range: NaN
+        A squares = block_sum<A>(v, scratch);
+        v = squares / (A)a.C + (A)a.eps;
         if (is_far(mean, v)) {                           // the same for all threads
             const A first = at(0);
             v = 0;
@@ -326,10 +326,11 @@ __global__ void __launch_bounds__(512) norm_forward_general_kernel(const NormArg
             }
             off = block_sum<A>(off, scratch);
             shift = off / (A)a.C;
-            v = block_sum<A>(v, scratch) - shift * off;
-            v = (v < (A)0 ? (A)0 : v) / (A)a.C + (A)a.eps;
-            rstd = (A)1 / sqrt(v) + (v - v);
+            squares = block_sum<A>(v, scratch) - shift * off;
+            squares = squares < (A)0 ? (A)0 : squares;
+            v = squares / (A)a.C + (A)a.eps;
         }
+        const A rstd = (A)1 / sqrt(v) + (squares - squares);     // squares out of range: NaN
         if (threadIdx.x == 0 && a.mean) {
             static_cast<A *>(a.mean)[row] = mean + shift;
             static_cast<A *>(a.rstd)[row] = rstd;

@@ -142,3 +142,15 @@ def test_equal_rows_without_eps(C, dt):
     values = torch.tensor([0.0, 1e-38, 1e-30, 1.1e-22, 1e-10, -3.3, 1e10, 1.7e19, 3e34], device="cuda", dtype=F64).to(dt)
     x = values[:, None].expand(-1, C).contiguous()
     assert binding.layer_norm(x, eps=0.0).isnan().all()
+
+
+@pytest.mark.parametrize("dt", [F32, BF16, F64], ids=IDS)
+@pytest.mark.parametrize("C", [256, 333, 4096, 12001, 32776])
+def test_an_eps_past_the_arithmetics_range(C, dt):
+    """rstd is zero then, not NaN: the output is the bias."""
+    w, b = parameters(C, dt)
+    x = torch.randn(5, C, device="cuda").to(dt) + 3
+    for eps in (1e39, float("inf")):
+        if eps == 1e39 and dt == F64:
+            continue                     # in range: rstd is 3e-20
+        assert torch.equal(binding.layer_norm(x, w, b, eps=eps), b.expand_as(x))
