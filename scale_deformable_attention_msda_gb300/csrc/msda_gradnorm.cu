@@ -14,15 +14,15 @@
 //
 // A list of up to kSmallTable tensors and kSmallUnits units takes one launch of a
 // single cluster instead, whose blocks exchange their partial results through
-// distributed shared memory. A layer's ten tensors take 8.5 us so, 7.0 as two
+// distributed shared memory. A layer's ten tensors take 8.8 us so, 7.0 as two
 // launches in a graph, but a call from the host 15 us instead of 20; past a unit a
 // warp the cluster's 8 SMs are too few (512 units: 12.6 us).
 //
 // What bounds it: memory, over two passes of the gradients. 300 million bf16
-// entries into fp32 take 385 us (2.4 GB with the second read, 6.2 TB/s); a
+// entries into fp32 take 386 us (2.4 GB with the second read, 6.2 TB/s); a
 // detector's 339 fp32 tensors, 163 MB, into another buffer 83 us (the L2 saves 49
 // of the second read's 163 MB), their norm alone 31 us; the largest of 60 million
-// fp16 entries 25 us. fp64 arithmetic is kept to a few additions per block: with
+// fp16 entries 24 us. fp64 arithmetic is kept to a few additions per block: with
 // fp64 sums in every lane and a square root and a division in every thread, the
 // same calls took 392, 86, 34 and 29 us. (GB300, calls in a graph.)
 #include <cooperative_groups.h>

@@ -12,11 +12,12 @@
 // gradients itself.
 //
 // What bounds it: memory and issue about evenly. 44,446 rows of 256 bf16 channels
-// with a residual take 18.0 us, the second kernel's 3 us among them (5.1 TB/s of
-// the data alone, 75% of the copy rate; the rows' kernel executes 180 warp
+// with a residual take 18.2 us, the second kernel's 3 us among them (5.0 TB/s of
+// the data alone, 74% of the copy rate; the rows' kernel executes 181 warp
 // instructions a row); 86,016 x 256 fp32 54.7 us (6.4 TB/s); 8192 x 4096 bf16 with both
-// gradients 55.9 us (6.0 TB/s); 20,011 x 777 fp16, whose rows start anywhere, 38 us.
-// 512 threads of an SM are what 128 registers each allow; with copies that hold no
+// gradients 56.5 us (5.9 TB/s); 20,011 x 777 fp16, whose rows start anywhere, 38 us.
+// The longest rows, 32 channels a thread, are bound by spills: 666 x 12,000 fp32 43.9
+// us (2.2 TB/s; 1.1 million spill requests). 512 threads of an SM are what 128 registers each allow; with copies that hold no
 // registers they keep about 60 KB on the way. (GB300, calls in a graph, inputs
 // larger than L2.)
 #pragma once

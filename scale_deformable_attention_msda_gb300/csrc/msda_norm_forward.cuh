@@ -8,12 +8,14 @@
 // once.
 //
 // What bounds it: memory, where rows start on 16-byte boundaries. 44,446 rows of
-// 256 bf16 channels with a residual take 11.2 us (6.1 TB/s, 90% of the copy rate);
-// 86,016 x 256 fp32 41.7 us (6.3 TB/s); 8192 x 4096 bf16 with a residual and the
+// 256 bf16 channels with a residual take 11.7 us (5.8 TB/s, 86% of the copy rate);
+// 86,016 x 256 fp32 40.9 us (6.5 TB/s); 8192 x 4096 bf16 with a residual and the
 // sum 44.6 us (6.0 TB/s). Rows that start anywhere are bound by instructions, an
-// element at a time from shared memory: 20,011 x 777 fp16 take 24.8 us (2.5 TB/s;
-// 761 warp instructions a row). A few rows are bound by the launch: 300 x 256
-// 1.7 us, one row of 8192 3.3 us. (GB300, calls in a graph, inputs larger than L2.)
+// element at a time from shared memory: 20,011 x 777 fp16 take 26.0 us (2.4 TB/s;
+// 801 warp instructions a row). A few rows are bound by the launch: 300 x 256
+// 1.8 us, one row of 8192 3.3 us. (GB300, calls in a graph, inputs larger than L2.
+// Pairs of figures below that compare two forms or sizes were measured before means
+// were corrected, which added up to 5%.)
 #pragma once
 
 #include "msda_norm.cuh"
