@@ -154,3 +154,29 @@ def test_an_eps_past_the_arithmetics_range(C, dt):
         if eps == 1e39 and dt == F64:
             continue                     # in range: rstd is 3e-20
         assert torch.equal(binding.layer_norm(x, w, b, eps=eps), b.expand_as(x))
+
+
+# lengths for each number of lanes and warps that hold a row, and of places that each has
+LENGTHS = [8, 16, 20, 24, 32, 40, 48, 64, 72, 100, 128, 160, 192, 257, 264, 384, 512, 513, 640, 768, 1000, 1024, 1025,
+           1536, 2048, 2504, 4104, 5000, 6000, 8000, 10000, 13312]
+
+
+@pytest.mark.parametrize("dt", [F32, BF16, F16], ids=IDS)
+@pytest.mark.parametrize("C", LENGTHS)
+def test_far_and_near_rows_side_by_side(C, dt):
+    """Rows far from zero, equal rows and ordinary ones in turn: each as if it were alone, to
+    the bit, and within the bounds."""
+    gen = torch.Generator(device="cuda").manual_seed(C)
+    N = 203
+    k = torch.randint(0, 65, (N, C), device="cuda", generator=gen).double()
+    offset, step = {F32: (10000.0, 2.0 ** -6), BF16: (256.0, 2.0), F16: (1024.0, 1.0)}[dt]
+    x = torch.randn(N, C, device="cuda", generator=gen).to(dt)
+    x[1::3] = (offset + k[1::3] * step).to(dt)
+    x[2::7] = 300.0
+    w, b = parameters(C, F32)
+    out, _, mean, rstd = binding.msda_layer_norm_forward(x, w, b)
+    check("out", out, reference(x, w, b, 1e-5, torch.zeros_like(x))["out"])
+    for i in range(0, 21):
+        one = binding.msda_layer_norm_forward(x[i:i + 1], w, b)
+        if x[i:i + 1].data_ptr() % 16 == 0 or C * dt.itemsize % 16:      # the same form of the kernels
+            assert torch.equal(one[0][0], out[i]) and torch.equal(one[2][0], mean[i]) and torch.equal(one[3][0], rstd[i])
