@@ -194,9 +194,10 @@ __device__ __forceinline__ MeanFix fix_mean(float sum, float squares, float C, f
 }
 
 // Where that is not done for every row (kFixAll), it is for rows whose mean is more than
-// kFar / rstd; in others the mean's roundings are at most 28 * 2^-24 * kFar of a
-// normalised row (C / 512 + 26 roundings in the general form). v: the variance and
-// eps. (Zeros, infinities and NaN are far.)
+// kFar / rstd; in others, whose entries' mean size is within (1 + kFar) / rstd, the
+// mean's roundings are at most 28 * 2^-24 * (1 + kFar) of a normalised row (C / 512 + 26
+// roundings in the general form). v: the variance and eps. (Zeros, infinities and NaN
+// are far.)
 constexpr float kFar = 2.0f;
 template <typename A> __device__ __forceinline__ bool is_far(A mean, A v) {
     return !(mean * mean < (A)(kFar * kFar) * v);
