@@ -489,6 +489,104 @@ MSDA_API msda_status_t msda_clip_grad_norm(const msda_grad_list_t *list, int kin
                                            void *norm, void *workspace, size_t workspace_bytes,
                                            void *stream);
 
+/* ---------------------------------------------------------------------------
+ * The rest of a detector's decoder layer: dense attention (of the queries among
+ * themselves, or of mask queries over a feature map), and dropout. */
+
+/* Q queries of M heads over S keys of N heads, D channels a head. M is a
+ * multiple of N: query head m reads key head m / (M / N). Supported:
+ * B, Q, S >= 0 (zero is valid), Q and S <= 2^30, 1 <= N <= M <= 65,536,
+ * 8 <= D <= 128 in multiples of 8, and less than 2^31 tiles of 64 x M rows.
+ * Strides in elements of a batch entry, a position and a head of q, k and v,
+ * whose channels are contiguous: multiples of 16 bytes, positive and below
+ * 2^36; the stride of a dimension of length one is not read. mask_stride, in
+ * bytes, of a batch entry, a head, a query and a key of the mask (0 repeats);
+ * not read without a mask. */
+typedef struct {
+    int64_t B, Q, S, M, N, D;
+    int64_t q_stride[3], k_stride[3], v_stride[3];
+    int64_t mask_stride[4];
+} msda_attention_dims_t;
+
+/* Bytes of device workspace the two calls below need. 0 for invalid dims or
+ * dtype (and where none is needed). with_mask: whether a mask is given. */
+MSDA_API size_t msda_attention_forward_workspace_bytes(const msda_attention_dims_t *dims,
+                                                       msda_dtype_t dtype, int with_mask);
+MSDA_API size_t msda_attention_backward_workspace_bytes(const msda_attention_dims_t *dims,
+                                                        msda_dtype_t dtype, int with_mask);
+
+/* Attention, forward. For each batch entry, query i and head m, over keys j:
+ *   s_j = scale * sum_d(q_i * k_j) where mask allows the pair, else -infinity
+ *   lse = log(sum_j(exp(s_j))),   out_i = sum_j(exp(s_j - lse) * v_j)
+ *   q              (B, Q, M, D) `dtype` at its strides
+ *   k, v           (B, S, N, D) `dtype` at their strides
+ *   mask           bytes, at their strides over (B, M, Q, S): zero means that the
+ *                  query may not attend the key; NULL: every pair is allowed
+ *   out            (B, Q, M, D) `dtype`, contiguous
+ *   lse            (B, M, Q) float, contiguous: what the backward needs; may be NULL
+ * A query with no key (all masked, or S = 0) gives zeros and lse = -infinity.
+ * What lies in masked places, NaN and infinity among it, does not show in the
+ * results. `dtype` is MSDA_F32, MSDA_BF16 or MSDA_F16. Sums, maxima and out's
+ * accumulation are held in fp32; for 16-bit data the probabilities are rounded
+ * to `dtype` as an operand of the second product. scale >= 0 and finite.
+ * workspace: at least msda_attention_forward_workspace_bytes(...) bytes,
+ *   16-byte aligned, owned by the caller, overwritten.
+ * q, k, v and out 16-byte aligned, lse 4. Outputs must not overlap inputs.
+ * The same call gives the same bits. Errors: MSDA_ERR_NULL, _SHAPE, _DTYPE,
+ * _ALIGN, _WORKSPACE before any launch; MSDA_ERR_CUDA. */
+MSDA_API msda_status_t msda_attention_forward(const void *q, const void *k, const void *v,
+                                              const void *mask, void *out, void *lse, double scale,
+                                              void *workspace, size_t workspace_bytes,
+                                              const msda_attention_dims_t *dims,
+                                              msda_dtype_t dtype, void *stream);
+
+/* Attention, backward. grad_out (B, Q, M, D), contiguous, is the gradient of
+ * out; q, k, v, mask, out and lse as the forward had and wrote them. The
+ * probabilities p are computed again from lse. With
+ * ds_ij = p_ij * (sum_d(grad_out_i * v_j) - sum_d(grad_out_i * out_i)):
+ *   grad_q (B, Q, M, D) = scale * sum_j(ds_ij * k_j)
+ *   grad_k (B, S, N, D) = scale * sum_i(ds_ij * q_i)
+ *   grad_v (B, S, N, D) = sum_i(p_ij * grad_out_i),
+ * the latter two summed over the query heads that share the key head too. All
+ * three are contiguous and OVERWRITTEN; grad_q may be NULL, and grad_k and
+ * grad_v both. A pair that the mask forbids has no part in any sum, so a query
+ * with no key gets zeros. Sums are held in fp32 and added in an order that the
+ * sizes fix: the same call gives the same bits. For 16-bit data p and ds are
+ * rounded to `dtype` as operands of the products that follow (fp16: scaled by
+ * powers of two that keep them in range). Errors and workspace as the forward. */
+MSDA_API msda_status_t msda_attention_backward(const void *grad_out, const void *q, const void *k,
+                                               const void *v, const void *mask, const void *out,
+                                               const void *lse, void *grad_q, void *grad_k,
+                                               void *grad_v, double scale, void *workspace,
+                                               size_t workspace_bytes,
+                                               const msda_attention_dims_t *dims,
+                                               msda_dtype_t dtype, void *stream);
+
+/* Dropout of n entries: out[e] = residual[e] + (kept(e) ? x[e] * f : 0), the
+ * sum rounded once (residual NULL: none). With t = round(p * 65536), f =
+ * 65536 / (65536 - t) in fp32, and kept(e) says that 16 random bits are >= t,
+ * so that out's expectation is exact for the p of t. The bits are those of
+ * Philox4x32-10 (Salmon et al., "Parallel random numbers: as easy as 1, 2, 3",
+ * SC 2011) with counter[0] as its key and (e / 8, counter[1]) as its counter,
+ * 64 bits each, low word first: entry e has half e % 2 (0: low) of word
+ * (e % 8) / 2. Nothing is stored: the gradient of x is the same call on the
+ * gradient of out, without a residual, with the same p and counter.
+ *   x, residual, out  n entries of `dtype` (MSDA_F32, _BF16, _F16 or _F64),
+ *                     contiguous; out may be x or residual
+ *   counter           2 int64 on the device, (seed, number of the draw), read only
+ * 0 <= p <= 1, else MSDA_ERR_SHAPE; p = 1 drops everything. 0 <= n <= 2^60.
+ * A dropped entry of x has no part in out, NaN and infinity among it.
+ * Alignment: element size. Errors: MSDA_ERR_NULL, _SHAPE, _DTYPE, _ALIGN before
+ * any launch; MSDA_ERR_CUDA. */
+MSDA_API msda_status_t msda_dropout(const void *x, const void *residual, void *out, int64_t n,
+                                    double p, const int64_t *counter, msda_dtype_t dtype,
+                                    void *stream);
+
+/* The next draw of a generator: drawn = state (2 int64 each, on the device),
+ * and state[1] is advanced by one. Calls on several streams with one state get
+ * different numbers. MSDA_ERR_NULL, _ALIGN (8 bytes); MSDA_ERR_CUDA. */
+MSDA_API msda_status_t msda_dropout_next(int64_t *state, int64_t *drawn, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

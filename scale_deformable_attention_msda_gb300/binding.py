@@ -34,7 +34,9 @@ EXPORTED = ("msda_forward", "msda_backward_workspace_bytes", "msda_backward",
             "msda_debug_bounds_self_test", "msda_set_sample_split", "msda_status_string",
             "msda_version", "msda_layer_norm_forward", "msda_layer_norm_backward_workspace_bytes",
             "msda_layer_norm_backward", "msda_grad_norm_workspace_bytes", "msda_grad_norm",
-            "msda_clip_grad_norm")
+            "msda_clip_grad_norm", "msda_attention_forward_workspace_bytes",
+            "msda_attention_backward_workspace_bytes", "msda_attention_forward",
+            "msda_attention_backward", "msda_dropout", "msda_dropout_next")
 
 
 class msda_dims_t(ctypes.Structure):
@@ -49,6 +51,12 @@ class msda_grad_list_t(ctypes.Structure):
     _fields_ = [("count", ctypes.c_int64), ("grads", ctypes.c_void_p), ("outs", ctypes.c_void_p),
                 ("sizes", ctypes.c_void_p), ("dtypes", ctypes.c_void_p),
                 ("out_dtypes", ctypes.c_void_p)]
+
+
+class msda_attention_dims_t(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int64) for n in ("B", "Q", "S", "M", "N", "D")] +
+                [(n, ctypes.c_int64 * 3) for n in ("q_stride", "k_stride", "v_stride")] +
+                [("mask_stride", ctypes.c_int64 * 4)])
 
 
 class MSDAError(RuntimeError):
@@ -125,6 +133,20 @@ def load(path: str | None = None):
     so.msda_clip_grad_norm.argtypes = [grad_list, ctypes.c_int, ctypes.c_double, vp, vp,
                                        ctypes.c_size_t, vp]
     so.msda_clip_grad_norm.restype = ctypes.c_int
+    attention_dims = ctypes.POINTER(msda_attention_dims_t)
+    for name in ("msda_attention_forward_workspace_bytes", "msda_attention_backward_workspace_bytes"):
+        getattr(so, name).argtypes = [attention_dims, ctypes.c_int, ctypes.c_int]
+        getattr(so, name).restype = ctypes.c_size_t
+    so.msda_attention_forward.argtypes = [vp] * 6 + [ctypes.c_double, vp, ctypes.c_size_t,
+                                                     attention_dims, ctypes.c_int, vp]
+    so.msda_attention_forward.restype = ctypes.c_int
+    so.msda_attention_backward.argtypes = [vp] * 10 + [ctypes.c_double, vp, ctypes.c_size_t,
+                                                       attention_dims, ctypes.c_int, vp]
+    so.msda_attention_backward.restype = ctypes.c_int
+    so.msda_dropout.argtypes = [vp, vp, vp, ctypes.c_int64, ctypes.c_double, vp, ctypes.c_int, vp]
+    so.msda_dropout.restype = ctypes.c_int
+    so.msda_dropout_next.argtypes = [vp, vp, vp]
+    so.msda_dropout_next.restype = ctypes.c_int
     so.msda_version.argtypes = []
     so.msda_version.restype = ctypes.c_int
     return so
@@ -852,3 +874,335 @@ def clip_grad_norm_(parameters, max_norm: float, norm_type: float = 2.0,
         if not torch.isfinite(norm):
             raise RuntimeError(f"the norm of the gradients is {float(norm)}: not clipped")
     return msda_clip_grad_norm(buf, max_norm, norm_type)
+
+
+# ------------------------------------------------------------------ attention
+
+_ATTENTION_DTYPES = (torch.float32, torch.bfloat16, torch.float16)
+
+
+class _AttentionPlan:
+    """The dims of one set of shapes and strides, and what they need of a workspace."""
+
+    def __init__(self, sizes, q, k, v, mask, dtype):
+        self.dims = msda_attention_dims_t(*sizes, (ctypes.c_int64 * 3)(*q), (ctypes.c_int64 * 3)(*k),
+                                          (ctypes.c_int64 * 3)(*v),
+                                          (ctypes.c_int64 * 4)(*(mask or (0, 0, 0, 0))))
+        self.ref = ctypes.byref(self.dims)
+        self.forward_bytes = int(lib().msda_attention_forward_workspace_bytes(
+            self.ref, dtype, mask is not None))
+        self.backward_bytes = int(lib().msda_attention_backward_workspace_bytes(
+            self.ref, dtype, mask is not None))
+
+
+_attention_plan = functools.lru_cache(maxsize=256)(_AttentionPlan)
+
+
+def _heads_ready(t):
+    """t, or a copy of it that the kernels can read: channels contiguous, 16-byte boundaries."""
+    e = t.element_size()
+    strides = t.stride()
+    if strides[3] == 1 and t.data_ptr() % 16 == 0:
+        for stride, size in zip(strides[:3], t.shape):
+            if size > 1 and (stride <= 0 or stride * e % 16):
+                break
+        else:
+            return t
+    return t.clone(memory_format=torch.contiguous_format)
+
+
+def _attention_operands(q, k, v, mask, scale):
+    """Raise unless q, k, v and the mask fit each other; returns (scale, the mask expanded)."""
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        if not t.is_cuda:
+            raise ValueError("libmsda runs on CUDA tensors only (no CPU path)")
+        if t.dim() != 4:
+            raise ValueError(f"{name} needs four dimensions (batch, position, head, channel), "
+                             f"has shape {tuple(t.shape)}")
+        if t.dtype != q.dtype:
+            raise ValueError(f"{name} is {t.dtype}, q is {q.dtype}")
+        if t.device != q.device:
+            raise ValueError(f"{name} is on {t.device}, q is on {q.device}")
+    if q.dtype not in _ATTENTION_DTYPES:
+        raise ValueError(f"unsupported dtype {q.dtype}: float32, bfloat16 and float16 are supported")
+    B, Q, M, D = q.shape
+    S, N = k.shape[1], k.shape[2]
+    if k.shape[0] != B or k.shape[3] != D or v.shape != k.shape:
+        raise ValueError(f"q {tuple(q.shape)}, k {tuple(k.shape)} and v {tuple(v.shape)} do not fit")
+    if N < 1 or M < N or M % N:
+        raise ValueError(f"{M} query heads for {N} key heads: give a multiple")
+    if not 8 <= D <= 128 or D % 8:
+        raise ValueError(f"{D} channels a head: multiples of 8 from 8 to 128 are supported")
+    scale = D ** -0.5 if scale is None else float(scale)
+    if not 0.0 <= scale <= 3e38:
+        raise ValueError(f"scale {scale}: give a finite number, not below zero")
+    if mask is not None:
+        if mask.dtype is not torch.bool:
+            raise ValueError(f"the mask is {mask.dtype}: give torch.bool, true where a query may attend")
+        if mask.device != q.device:
+            raise ValueError(f"the mask is on {mask.device}, q is on {q.device}")
+        try:
+            mask = mask.expand(B, M, Q, S)
+        except RuntimeError:
+            raise ValueError(f"a mask of shape {tuple(mask.shape)} does not broadcast to "
+                             f"{(B, M, Q, S)}") from None
+    return scale, mask
+
+
+def _plan_of(q, k, v, mask):
+    B, Q, M, D = q.shape
+    _, S, N, _ = k.shape
+    strides = None
+    if mask is not None:
+        strides = tuple(st if n > 1 else 0 for st, n in zip(mask.stride(), mask.shape))
+    return _attention_plan((B, Q, S, M, N, D), q.stride()[:3], k.stride()[:3], v.stride()[:3],
+                           strides, _DTYPES[q.dtype])
+
+
+def _workspace(need, device):
+    return torch.empty(need, dtype=torch.uint8, device=device) if need else None
+
+
+def _attend(q, k, v, mask, scale, lse, out):
+    """The launch, on the current device and stream, of operands already checked."""
+    B, Q, M, D = q.shape
+    plan = _plan_of(q, k, v, mask)
+    if out is None:
+        out = torch.empty((B, Q, M * D), dtype=q.dtype, device=q.device)
+    lse = torch.empty((B, M, Q), dtype=torch.float32, device=q.device) if lse else None
+    workspace = _workspace(plan.forward_bytes, q.device)
+    status = lib().msda_attention_forward(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), _at(mask), out.data_ptr(), _at(lse), scale,
+        _at(workspace), plan.forward_bytes, plan.ref, _DTYPES[q.dtype],
+        _current_stream(q.get_device()))
+    if status:
+        raise MSDAError(status, "msda_attention_forward")
+    return out, lse
+
+
+def _attend_backward(grad_out, q, k, v, out, lse, mask, scale, want):
+    """The launch, on the current device and stream, of operands already checked."""
+    plan = _plan_of(q, k, v, mask)
+    gq = torch.empty(q.shape, dtype=q.dtype, device=q.device) if want[0] else None
+    gk = gv = None
+    if want[1] or want[2]:
+        gk, gv = [torch.empty(k.shape, dtype=q.dtype, device=q.device) for _ in range(2)]
+    workspace = _workspace(plan.backward_bytes, q.device)
+    status = lib().msda_attention_backward(
+        grad_out.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), _at(mask), out.data_ptr(),
+        lse.data_ptr(), _at(gq), _at(gk), _at(gv), scale, _at(workspace), plan.backward_bytes,
+        plan.ref, _DTYPES[q.dtype], _current_stream(q.get_device()))
+    if status:
+        raise MSDAError(status, "msda_attention_backward")
+    return gq, gk if want[1] else None, gv if want[2] else None
+
+
+def msda_attention_forward(q, k, v, mask=None, scale=None, lse: bool = True, out=None, stream=None):
+    """(out (B, Q, M*D), lse (B, M, Q)) of q (B, Q, M, D) over k, v (B, S, N, D); lse is None
+    unless `lse` (the backward needs it). mask: bool, broadcasts to (B, M, Q, S), true where a
+    query may attend. scale: D ** -0.5 unless given. See msda_attention_forward in
+    include/msda.h."""
+    _refuse_modes("msda_attention_forward", (q, k, v))
+    scale, mask = _attention_operands(q, k, v, mask, scale)
+    if out is not None:
+        _check_like("out", out, (q.shape[0], q.shape[1], q.shape[2] * q.shape[3]), q.dtype, q.device)
+    given = out
+    with _on(q.device, stream):
+        q, k, v = _heads_ready(q), _heads_ready(k), _heads_ready(v)
+        if out is not None:
+            _apart([out], [q, k, v, mask])
+        out, stats = _attend(q, k, v, mask, scale, lse, out)
+    if given is not None and not out.is_inference():
+        torch.autograd.graph.increment_version(out)
+    return out, stats
+
+
+def msda_attention_backward(grad_out, q, k, v, out, lse, mask=None, scale=None,
+                            want=(True, True, True), stream=None):
+    """(grad_q, grad_k, grad_v) of q's, k's and v's shapes, contiguous, None where `want` says
+    so; out and lse are the forward's. See msda_attention_backward in include/msda.h."""
+    _refuse_modes("msda_attention_backward", (grad_out, q, k, v, out, lse))
+    scale, mask = _attention_operands(q, k, v, mask, scale)
+    B, Q, M, D = q.shape
+    for name, t in (("grad_out", grad_out), ("out", out)):
+        _check_like(name, t, (B, Q, M * D), q.dtype, q.device)
+    _check_like("lse", lse, (B, M, Q), torch.float32, q.device)
+    with _on(q.device, stream):
+        return _attend_backward(_at16(grad_out), _heads_ready(q), _heads_ready(k), _heads_ready(v),
+                                _at16(out), lse, mask, scale, want)
+
+
+def _at16(t):
+    """t, contiguous, or a copy that starts on a 16-byte boundary."""
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
+def _attention_gradients(ctx, grad_out):
+    """What AttentionFunction.backward returns."""
+    _refuse_recording("attention's backward")
+    q, k, v, mask, out, lse = ctx.saved_tensors
+    args = (_at16(grad_out.contiguous()), q, k, v, out, lse, mask, ctx.scale,
+            ctx.needs_input_grad[:3])
+    if _elsewhere(q.get_device()):
+        with _on(q.device, None):
+            grads = _attend_backward(*args)
+    else:
+        grads = _attend_backward(*args)
+    return (*grads, None, None)
+
+
+class AttentionFunction(torch.autograd.Function):
+    """Autograd wrapper of the two calls above (first derivatives only)."""
+
+    @staticmethod
+    def forward(ctx, q, k, v, mask, scale):
+        ctx.scale, mask = _attention_operands(q, k, v, mask, scale)
+        with _on(q.device, None):
+            q, k, v = _heads_ready(q), _heads_ready(k), _heads_ready(v)
+            out, lse = _attend(q, k, v, mask, ctx.scale, True, None)
+        ctx.save_for_backward(q, k, v, mask, out, lse)
+        return out
+
+    @staticmethod
+    def backward(ctx, grad_out):
+        if torch.is_grad_enabled():      # create_graph: second derivatives are an error, if asked for
+            return AttentionFunction.backward_once(ctx, grad_out)
+        return _attention_gradients(ctx, grad_out)
+
+    backward_once = staticmethod(torch.autograd.function.once_differentiable(_attention_gradients))
+
+
+def attention(q, k, v, mask=None, scale=None):
+    """Differentiable attention: q (B, Q, M, D) over k, v (B, S, N, D) -> (B, Q, M*D), query
+    head m reading key head m / (M / N). mask: bool, broadcasts to (B, M, Q, S), true where a
+    query may attend; a query with no key gets zeros. scale: D ** -0.5 unless given. D is a
+    multiple of 8 up to 128; float32, bfloat16 or float16."""
+    _refuse_recording("attention")
+    if (torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad)
+            or _through_autograd()):
+        return AttentionFunction.apply(q, k, v, mask, scale)
+    scale, mask = _attention_operands(q, k, v, mask, scale)
+    if _elsewhere(q.get_device()):
+        with _on(q.device, None):
+            return _attend(_heads_ready(q), _heads_ready(k), _heads_ready(v), mask, scale, False, None)[0]
+    return _attend(_heads_ready(q), _heads_ready(k), _heads_ready(v), mask, scale, False, None)[0]
+
+
+# -------------------------------------------------------------------- dropout
+
+def _drop_operands(x, p, counter, residual):
+    if not x.is_cuda:
+        raise ValueError("libmsda runs on CUDA tensors only (no CPU path)")
+    if x.dtype not in _DTYPES:
+        raise ValueError(f"unsupported dtype {x.dtype}")
+    if not 0.0 <= p <= 1.0:
+        raise ValueError(f"a probability of {p}: give one from 0 to 1")
+    _check_like("x", x, x.shape, x.dtype, x.device)
+    _check_like("residual", residual, x.shape, x.dtype, x.device)
+    _check_like("counter", counter, (2,), torch.int64, x.device)
+
+
+def _drop(x, p, counter, residual, out):
+    """The launch, on the current device and stream, of operands already checked."""
+    if out is None:
+        out = torch.empty_like(x)
+    status = lib().msda_dropout(x.data_ptr(), _at(residual), out.data_ptr(), int(x.numel()), p,
+                                counter.data_ptr(), _DTYPES[x.dtype], _current_stream(x.get_device()))
+    if status:
+        raise MSDAError(status, "msda_dropout")
+    return out
+
+
+def msda_dropout(x, p, counter, residual=None, out=None, stream=None):
+    """residual + x with each entry kept with probability 1 - p and scaled by 1 / (1 - p), in
+    steps of 2^-16. counter: two int64 on x's device, the generator's seed and the draw's
+    number. out may be x or residual. See msda_dropout in include/msda.h."""
+    _refuse_modes("msda_dropout", (x, residual))
+    p = float(p)
+    _drop_operands(x, p, counter, residual)
+    given = out
+    if out is not None:
+        _check_like("out", out, x.shape, x.dtype, x.device)
+        _apart([out], [t for t in (x, residual) if t is not None and t.data_ptr() != out.data_ptr()] + [counter])
+    if _elsewhere(x.get_device(), stream):
+        with _on(x.device, stream):
+            out = _drop(x, p, counter, residual, out)
+    else:
+        out = _drop(x, p, counter, residual, out)
+    if given is not None and not out.is_inference():
+        torch.autograd.graph.increment_version(out)
+    return out
+
+
+def dropout_next(state, stream=None):
+    """The generator's next draw: a new tensor of `state`'s seed and number (two int64 on the
+    device), whose number is then advanced by one, on the device (a captured call draws anew
+    each time it is replayed)."""
+    _refuse_modes("dropout_next", ())
+    if not state.is_cuda:
+        raise ValueError("libmsda runs on CUDA tensors only (no CPU path)")
+    _check_like("state", state, (2,), torch.int64, state.device)
+    with _on(state.device, stream):
+        drawn = torch.empty_like(state)
+        _call("msda_dropout_next", lib().msda_dropout_next(
+            state.data_ptr(), drawn.data_ptr(), _current_stream(state.get_device())))
+    if not state.is_inference():
+        torch.autograd.graph.increment_version(state)
+    return drawn
+
+
+def _drop_gradient(ctx, grad_out):
+    """What DropoutFunction.backward returns."""
+    _refuse_recording("dropout's backward")
+    counter, = ctx.saved_tensors
+    gx = None
+    if ctx.needs_input_grad[0]:
+        grad = grad_out.contiguous()
+        if _elsewhere(grad.get_device()):
+            with _on(grad.device, None):
+                gx = _drop(grad, ctx.p, counter, None, None)
+        else:
+            gx = _drop(grad, ctx.p, counter, None, None)
+    return gx, grad_out if ctx.needs_input_grad[1] else None, None, None
+
+
+class DropoutFunction(torch.autograd.Function):
+    """Autograd wrapper: the backward draws the same mask again (first derivatives only)."""
+
+    @staticmethod
+    def forward(ctx, x, residual, p, counter):
+        _drop_operands(x, p, counter, residual)
+        ctx.p = p
+        ctx.save_for_backward(counter)
+        if _elsewhere(x.get_device()):
+            with _on(x.device, None):
+                return _drop(x, p, counter, residual, None)
+        return _drop(x, p, counter, residual, None)
+
+    @staticmethod
+    def backward(ctx, grad_out):
+        if torch.is_grad_enabled():      # create_graph: second derivatives are an error, if asked for
+            return DropoutFunction.backward_once(ctx, grad_out)
+        return _drop_gradient(ctx, grad_out)
+
+    backward_once = staticmethod(torch.autograd.function.once_differentiable(_drop_gradient))
+
+
+def dropout(x, p, counter, residual=None):
+    """Differentiable dropout, and the residual stream it is added to: residual + x with each
+    entry kept with probability 1 - p and scaled by 1 / (1 - p). counter: two int64 on x's
+    device, the seed and the draw's number (dropout_next gives one); the same counter draws
+    the same mask, and the mask is not stored."""
+    _refuse_recording("dropout")
+    p = float(p)
+    x = x.contiguous()
+    if residual is not None:
+        residual = residual.contiguous()
+    if (torch.is_grad_enabled() and (x.requires_grad or residual is not None and residual.requires_grad)
+            or _through_autograd()):
+        return DropoutFunction.apply(x, residual, p, counter)
+    _drop_operands(x, p, counter, residual)
+    if _elsewhere(x.get_device()):
+        with _on(x.device, None):
+            return _drop(x, p, counter, residual, None)
+    return _drop(x, p, counter, residual, None)
