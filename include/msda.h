@@ -523,6 +523,8 @@ MSDA_API size_t msda_attention_backward_workspace_bytes(const msda_attention_dim
  *   mask           bytes, at their strides over (B, M, Q, S): zero means that the
  *                  query may not attend the key; NULL: every pair is allowed
  *   out            (B, Q, M, D) `dtype`, contiguous
+ *   rest           as out, receives what out's rounding left, itself rounded; NULL:
+ *                  not wanted. With it the backward knows out to twice its digits
  *   lse            (B, M, Q) float, contiguous: what the backward needs; may be NULL
  * A query with no key (all masked, or S = 0) gives zeros and lse = -infinity.
  * What lies in masked places, NaN and infinity among it, does not show in the
@@ -531,19 +533,21 @@ MSDA_API size_t msda_attention_backward_workspace_bytes(const msda_attention_dim
  * to `dtype` as an operand of the second product. scale >= 0 and finite.
  * workspace: at least msda_attention_forward_workspace_bytes(...) bytes,
  *   16-byte aligned, owned by the caller, overwritten.
- * q, k, v and out 16-byte aligned, lse 4. Outputs must not overlap inputs.
+ * q, k, v, out and rest 16-byte aligned, lse 4. Outputs must not overlap inputs.
  * The same call gives the same bits. Errors: MSDA_ERR_NULL, _SHAPE, _DTYPE,
  * _ALIGN, _WORKSPACE before any launch; MSDA_ERR_CUDA. */
 MSDA_API msda_status_t msda_attention_forward(const void *q, const void *k, const void *v,
-                                              const void *mask, void *out, void *lse, double scale,
-                                              void *workspace, size_t workspace_bytes,
+                                              const void *mask, void *out, void *rest, void *lse,
+                                              double scale, void *workspace, size_t workspace_bytes,
                                               const msda_attention_dims_t *dims,
                                               msda_dtype_t dtype, void *stream);
 
 /* Attention, backward. grad_out (B, Q, M, D), contiguous, is the gradient of
- * out; q, k, v, mask, out and lse as the forward had and wrote them. The
+ * out; q, k, v, mask, out, rest and lse as the forward had and wrote them. The
  * probabilities p are computed again from lse. With
- * ds_ij = p_ij * (sum_d(grad_out_i * v_j) - sum_d(grad_out_i * out_i)):
+ * ds_ij = p_ij * (sum_d(grad_out_i * v_j) - sum_d(grad_out_i * (out_i + rest_i)))
+ * (rest NULL: zeros; where a query attends almost only one key the two sums
+ * nearly cancel, and out's rounding shows in ds):
  *   grad_q (B, Q, M, D) = scale * sum_j(ds_ij * k_j)
  *   grad_k (B, S, N, D) = scale * sum_i(ds_ij * q_i)
  *   grad_v (B, S, N, D) = sum_i(p_ij * grad_out_i),
@@ -556,8 +560,8 @@ MSDA_API msda_status_t msda_attention_forward(const void *q, const void *k, cons
  * powers of two that keep them in range). Errors and workspace as the forward. */
 MSDA_API msda_status_t msda_attention_backward(const void *grad_out, const void *q, const void *k,
                                                const void *v, const void *mask, const void *out,
-                                               const void *lse, void *grad_q, void *grad_k,
-                                               void *grad_v, double scale, void *workspace,
+                                               const void *rest, const void *lse, void *grad_q,
+                                               void *grad_k, void *grad_v, double scale, void *workspace,
                                                size_t workspace_bytes,
                                                const msda_attention_dims_t *dims,
                                                msda_dtype_t dtype, void *stream);

@@ -137,10 +137,10 @@ def load(path: str | None = None):
     for name in ("msda_attention_forward_workspace_bytes", "msda_attention_backward_workspace_bytes"):
         getattr(so, name).argtypes = [attention_dims, ctypes.c_int, ctypes.c_int]
         getattr(so, name).restype = ctypes.c_size_t
-    so.msda_attention_forward.argtypes = [vp] * 6 + [ctypes.c_double, vp, ctypes.c_size_t,
+    so.msda_attention_forward.argtypes = [vp] * 7 + [ctypes.c_double, vp, ctypes.c_size_t,
                                                      attention_dims, ctypes.c_int, vp]
     so.msda_attention_forward.restype = ctypes.c_int
-    so.msda_attention_backward.argtypes = [vp] * 10 + [ctypes.c_double, vp, ctypes.c_size_t,
+    so.msda_attention_backward.argtypes = [vp] * 11 + [ctypes.c_double, vp, ctypes.c_size_t,
                                                        attention_dims, ctypes.c_int, vp]
     so.msda_attention_backward.restype = ctypes.c_int
     so.msda_dropout.argtypes = [vp, vp, vp, ctypes.c_int64, ctypes.c_double, vp, ctypes.c_int, vp]
@@ -963,24 +963,26 @@ def _workspace(need, device):
     return torch.empty(need, dtype=torch.uint8, device=device) if need else None
 
 
-def _attend(q, k, v, mask, scale, lse, out):
-    """The launch, on the current device and stream, of operands already checked."""
+def _attend(q, k, v, mask, scale, lse, rest, out):
+    """The launch, on the current device and stream, of operands already checked. rest: also
+    what out's rounding left (16-bit types)."""
     B, Q, M, D = q.shape
     plan = _plan_of(q, k, v, mask)
     if out is None:
         out = torch.empty((B, Q, M * D), dtype=q.dtype, device=q.device)
     lse = torch.empty((B, M, Q), dtype=torch.float32, device=q.device) if lse else None
+    rest = torch.empty_like(out) if rest and q.dtype is not torch.float32 else None
     workspace = _workspace(plan.forward_bytes, q.device)
     status = lib().msda_attention_forward(
-        q.data_ptr(), k.data_ptr(), v.data_ptr(), _at(mask), out.data_ptr(), _at(lse), scale,
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), _at(mask), out.data_ptr(), _at(rest), _at(lse), scale,
         _at(workspace), plan.forward_bytes, plan.ref, _DTYPES[q.dtype],
         _current_stream(q.get_device()))
     if status:
         raise MSDAError(status, "msda_attention_forward")
-    return out, lse
+    return out, lse, rest
 
 
-def _attend_backward(grad_out, q, k, v, out, lse, mask, scale, want):
+def _attend_backward(grad_out, q, k, v, out, rest, lse, mask, scale, want):
     """The launch, on the current device and stream, of operands already checked."""
     plan = _plan_of(q, k, v, mask)
     gq = torch.empty(q.shape, dtype=q.dtype, device=q.device) if want[0] else None
@@ -990,16 +992,18 @@ def _attend_backward(grad_out, q, k, v, out, lse, mask, scale, want):
     workspace = _workspace(plan.backward_bytes, q.device)
     status = lib().msda_attention_backward(
         grad_out.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), _at(mask), out.data_ptr(),
-        lse.data_ptr(), _at(gq), _at(gk), _at(gv), scale, _at(workspace), plan.backward_bytes,
+        _at(rest), lse.data_ptr(), _at(gq), _at(gk), _at(gv), scale, _at(workspace), plan.backward_bytes,
         plan.ref, _DTYPES[q.dtype], _current_stream(q.get_device()))
     if status:
         raise MSDAError(status, "msda_attention_backward")
     return gq, gk if want[1] else None, gv if want[2] else None
 
 
-def msda_attention_forward(q, k, v, mask=None, scale=None, lse: bool = True, out=None, stream=None):
+def msda_attention_forward(q, k, v, mask=None, scale=None, lse: bool = True, out=None, stream=None,
+                           rest: bool = False):
     """(out (B, Q, M*D), lse (B, M, Q)) of q (B, Q, M, D) over k, v (B, S, N, D); lse is None
-    unless `lse` (the backward needs it). mask: bool, broadcasts to (B, M, Q, S), true where a
+    unless `lse` (the backward needs it). rest: a third tensor, what out's rounding to 16 bits
+    left (None for float32), for gradients as good as from an out of twice the digits. mask: bool, broadcasts to (B, M, Q, S), true where a
     query may attend. scale: D ** -0.5 unless given. See msda_attention_forward in
     include/msda.h."""
     _refuse_modes("msda_attention_forward", (q, k, v))
@@ -1011,25 +1015,26 @@ def msda_attention_forward(q, k, v, mask=None, scale=None, lse: bool = True, out
         q, k, v = _heads_ready(q), _heads_ready(k), _heads_ready(v)
         if out is not None:
             _apart([out], [q, k, v, mask])
-        out, stats = _attend(q, k, v, mask, scale, lse, out)
+        out, stats, left = _attend(q, k, v, mask, scale, lse, rest, out)
     if given is not None and not out.is_inference():
         torch.autograd.graph.increment_version(out)
-    return out, stats
+    return (out, stats, left) if rest else (out, stats)
 
 
 def msda_attention_backward(grad_out, q, k, v, out, lse, mask=None, scale=None,
-                            want=(True, True, True), stream=None):
+                            want=(True, True, True), stream=None, rest=None):
     """(grad_q, grad_k, grad_v) of q's, k's and v's shapes, contiguous, None where `want` says
-    so; out and lse are the forward's. See msda_attention_backward in include/msda.h."""
-    _refuse_modes("msda_attention_backward", (grad_out, q, k, v, out, lse))
+    so; out, lse and rest (if it was asked for) are the forward's. See msda_attention_backward in include/msda.h."""
+    _refuse_modes("msda_attention_backward", (grad_out, q, k, v, out, lse, rest))
     scale, mask = _attention_operands(q, k, v, mask, scale)
     B, Q, M, D = q.shape
-    for name, t in (("grad_out", grad_out), ("out", out)):
+    for name, t in (("grad_out", grad_out), ("out", out), ("rest", rest)):
         _check_like(name, t, (B, Q, M * D), q.dtype, q.device)
     _check_like("lse", lse, (B, M, Q), torch.float32, q.device)
     with _on(q.device, stream):
         return _attend_backward(_at16(grad_out), _heads_ready(q), _heads_ready(k), _heads_ready(v),
-                                _at16(out), lse, mask, scale, want)
+                                _at16(out), None if rest is None else _at16(rest), lse, mask, scale,
+                                want)
 
 
 def _at16(t):
@@ -1040,8 +1045,8 @@ def _at16(t):
 def _attention_gradients(ctx, grad_out):
     """What AttentionFunction.backward returns."""
     _refuse_recording("attention's backward")
-    q, k, v, mask, out, lse = ctx.saved_tensors
-    args = (_at16(grad_out.contiguous()), q, k, v, out, lse, mask, ctx.scale,
+    q, k, v, mask, out, lse, rest = ctx.saved_tensors
+    args = (_at16(grad_out.contiguous()), q, k, v, out, rest, lse, mask, ctx.scale,
             ctx.needs_input_grad[:3])
     if _elsewhere(q.get_device()):
         with _on(q.device, None):
@@ -1059,8 +1064,8 @@ class AttentionFunction(torch.autograd.Function):
         ctx.scale, mask = _attention_operands(q, k, v, mask, scale)
         with _on(q.device, None):
             q, k, v = _heads_ready(q), _heads_ready(k), _heads_ready(v)
-            out, lse = _attend(q, k, v, mask, ctx.scale, True, None)
-        ctx.save_for_backward(q, k, v, mask, out, lse)
+            out, lse, rest = _attend(q, k, v, mask, ctx.scale, True, True, None)
+        ctx.save_for_backward(q, k, v, mask, out, lse, rest)
         return out
 
     @staticmethod
@@ -1084,8 +1089,8 @@ def attention(q, k, v, mask=None, scale=None):
     scale, mask = _attention_operands(q, k, v, mask, scale)
     if _elsewhere(q.get_device()):
         with _on(q.device, None):
-            return _attend(_heads_ready(q), _heads_ready(k), _heads_ready(v), mask, scale, False, None)[0]
-    return _attend(_heads_ready(q), _heads_ready(k), _heads_ready(v), mask, scale, False, None)[0]
+            return _attend(_heads_ready(q), _heads_ready(k), _heads_ready(v), mask, scale, False, False, None)[0]
+    return _attend(_heads_ready(q), _heads_ready(k), _heads_ready(v), mask, scale, False, False, None)[0]
 
 
 # -------------------------------------------------------------------- dropout

@@ -48,6 +48,7 @@ struct AttnBits {
 struct AttnArgs {
     AttnTensor q, k, v, o, go;         // o, go: out and its gradient (backward)
     void *out, *gq, *gk, *gv;
+    void *rest;                        // what out's rounding left, of out's type and shape; NULL: none
     float *lse;                        // (B, M, Q); forward: may be NULL
     float *delta;                      // (B, M, Q)
     // fp16 backward: partial maxima of |dO_i|^2 and |v_j|^2 (norms each, see
@@ -236,6 +237,13 @@ __device__ __noinline__ void attn_exact_row(const AttnArgs &a, const AttnRows &w
     }
 }
 
+// A value of the output, and what its rounding left.
+template <typename T> __device__ __forceinline__ void attn_put(void *out, void *rest, int64_t at, float v) {
+    const T rounded = Elem<T>::from_f(v);
+    static_cast<T *>(out)[at] = rounded;
+    if (rest) static_cast<T *>(rest)[at] = Elem<T>::from_f(v - Elem<T>::to_f(rounded));
+}
+
 // One result of a row: a value of the output, or of this split's part. which: 0,
 // or 1 for the second of a key's gradients; f: what the sum is multiplied by.
 template <typename T, int MODE>
@@ -249,7 +257,7 @@ __device__ __forceinline__ void attn_store(const AttnArgs &a, const AttnRows &w,
         return;
     }
     void *to = MODE == kForward ? a.out : MODE == kGradQ ? a.gq : which ? a.gk : a.gv;
-    static_cast<T *>(to)[row * a.D + d] = Elem<T>::from_f(sum * f);
+    attn_put<T>(to, MODE == kForward ? a.rest : nullptr, row * a.D + d, sum * f);
 }
 
 }  // namespace msda

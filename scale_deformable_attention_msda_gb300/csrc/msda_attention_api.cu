@@ -81,8 +81,12 @@ ModePlan plan_mode(const msda_attention_dims_t &d, AttnMode mode, int R, int C, 
     return p;
 }
 
+int tile_rows(msda_dtype_t dt) { return dt == MSDA_F32 ? 64 : 128; }
+
 ModePlan plan_for(const msda_attention_dims_t &d, msda_dtype_t dt, AttnMode mode) {
-    return plan_mode(d, mode, 64, 64, kSMs, 4);
+    if (dt == MSDA_F32) return plan_mode(d, mode, 64, 64, kSMs, 4);
+    const int columns = msda::tc_columns(mode, (int)d.D), blocks = msda::tc_blocks(mode, (int)d.D);
+    return plan_mode(d, mode, 128, columns, kSMs * blocks, 4);
 }
 
 // The workspace, each piece on a 256-byte boundary.
@@ -169,7 +173,7 @@ cudaError_t pack_mask(AttnArgs &a, const msda_attention_dims_t &d, const Layout 
 cudaError_t launch_mode(AttnArgs a, const msda_attention_dims_t &d, msda_dtype_t dt, AttnMode mode, char *part,
                         cudaStream_t stream) {
     const ModePlan p = plan_for(d, dt, mode);
-    a.pack = mode == msda::kGradKV ? 1 : pack_of(d, 64);
+    a.pack = mode == msda::kGradKV ? 1 : pack_of(d, tile_rows(dt));
     a.splits = p.splits;
     a.part = reinterpret_cast<float *>(part);
     a.part_rows = mode == msda::kGradKV ? d.B * d.S * d.N : d.B * d.Q * d.M;
@@ -198,7 +202,7 @@ size_t msda_attention_backward_workspace_bytes(const msda_attention_dims_t *dims
 }
 
 msda_status_t msda_attention_forward(const void *q, const void *k, const void *v, const void *mask, void *out,
-                                     void *lse, double scale, void *workspace, size_t workspace_bytes,
+                                     void *rest, void *lse, double scale, void *workspace, size_t workspace_bytes,
                                      const msda_attention_dims_t *dims, msda_dtype_t dtype, void *stream) {
     const msda_status_t st = check(dims, dtype, mask != nullptr);
     if (st != MSDA_OK) return st;
@@ -206,7 +210,8 @@ msda_status_t msda_attention_forward(const void *q, const void *k, const void *v
     const msda_attention_dims_t &d = *dims;
     if (d.B == 0 || d.Q == 0) return MSDA_OK;
     if (!q || !out || (d.S > 0 && (!k || !v))) return MSDA_ERR_NULL;
-    if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) || !aligned(lse, 4))
+    if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) || !aligned(rest, 16) ||
+        !aligned(lse, 4))
         return MSDA_ERR_ALIGN;
     const bool masked = mask && d.S > 0;
     const Layout w = layout_of(d, dtype, masked, false);
@@ -214,8 +219,9 @@ msda_status_t msda_attention_forward(const void *q, const void *k, const void *v
     if (w.bytes && !aligned(workspace, 16)) return MSDA_ERR_ALIGN;
     AttnArgs a = common_args(d, q, k, v, scale);
     a.out = out;
+    a.rest = rest;
     a.lse = static_cast<float *>(lse);
-    if (msda::fault_word_for_launch(&a.err) != cudaSuccess) return MSDA_ERR_CUDA;
+    if (msda::fault_word(&a.err) != cudaSuccess) return MSDA_ERR_CUDA;
     char *ws = static_cast<char *>(workspace);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e = masked ? pack_mask(a, d, w, mask, ws, false, s) : cudaSuccess;
@@ -224,8 +230,8 @@ msda_status_t msda_attention_forward(const void *q, const void *k, const void *v
 }
 
 msda_status_t msda_attention_backward(const void *grad_out, const void *q, const void *k, const void *v,
-                                      const void *mask, const void *out, const void *lse, void *grad_q, void *grad_k,
-                                      void *grad_v, double scale, void *workspace, size_t workspace_bytes,
+                                      const void *mask, const void *out, const void *rest, const void *lse,
+                                      void *grad_q, void *grad_k, void *grad_v, double scale, void *workspace, size_t workspace_bytes,
                                       const msda_attention_dims_t *dims, msda_dtype_t dtype, void *stream) {
     const msda_status_t st = check(dims, dtype, mask != nullptr);
     if (st != MSDA_OK) return st;
@@ -237,7 +243,7 @@ msda_status_t msda_attention_backward(const void *grad_out, const void *q, const
     if (d.Q > 0 && (!grad_out || !q || !out || !lse)) return MSDA_ERR_NULL;
     if (d.S > 0 && (!k || !v)) return MSDA_ERR_NULL;
     if (!aligned(grad_out, 16) || !aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) ||
-        !aligned(lse, 4) || !aligned(grad_q, 16) || !aligned(grad_k, 16) || !aligned(grad_v, 16))
+        !aligned(rest, 16) || !aligned(lse, 4) || !aligned(grad_q, 16) || !aligned(grad_k, 16) || !aligned(grad_v, 16))
         return MSDA_ERR_ALIGN;
     const bool masked = mask && d.S > 0 && d.Q > 0;
     const Layout w = layout_of(d, dtype, masked, true);
@@ -247,10 +253,11 @@ msda_status_t msda_attention_backward(const void *grad_out, const void *q, const
     a.go = dense(grad_out, d.Q, d.M, d.D);
     a.o = dense(out, d.Q, d.M, d.D);
     a.lse = static_cast<float *>(const_cast<void *>(lse));
+    a.rest = const_cast<void *>(rest);
     a.gq = grad_q;
     a.gk = grad_k;
     a.gv = grad_v;
-    if (msda::fault_word_for_launch(&a.err) != cudaSuccess) return MSDA_ERR_CUDA;
+    if (msda::fault_word(&a.err) != cudaSuccess) return MSDA_ERR_CUDA;
     char *ws = static_cast<char *>(workspace);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     a.delta = reinterpret_cast<float *>(ws + w.delta);

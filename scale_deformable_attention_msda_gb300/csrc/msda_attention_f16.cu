@@ -1,7 +1,7 @@
-#include "msda_attention_simple.cuh"
+#include "msda_attention_tc.cuh"
 
 namespace msda {
 cudaError_t launch_attention_f16(int mode, const AttnArgs &a, int64_t blocks, cudaStream_t stream) {
-    return launch_simple<__half>(mode, a, blocks, stream);
+    return launch_tc<__half>(mode, a, blocks, stream);
 }
 }  // namespace msda

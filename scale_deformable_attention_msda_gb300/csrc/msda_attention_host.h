@@ -11,6 +11,10 @@ cudaError_t launch_attention_f32(int mode, const AttnArgs &a, int64_t blocks, cu
 cudaError_t launch_attention_bf16(int mode, const AttnArgs &a, int64_t blocks, cudaStream_t stream);
 cudaError_t launch_attention_f16(int mode, const AttnArgs &a, int64_t blocks, cudaStream_t stream);
 
+// The 16-bit kernels' columns of a tile, and their blocks of an SM.
+constexpr int tc_columns(int mode, int D) { return mode == kForward && D <= 64 ? 128 : 64; }
+constexpr int tc_blocks(int mode, int D) { return mode != kForward && D > 64 ? 1 : 2; }
+
 // What the mask is made of before it is packed: bytes at strides.
 struct AttnMaskSource {
     const uint8_t *p;
@@ -19,7 +23,6 @@ struct AttnMaskSource {
 };
 cudaError_t launch_attention_pack(const AttnMaskSource &m, uint32_t *by_query, int words_q, uint32_t *by_key,
                                   int words_k, uint8_t *classes, int granules, cudaStream_t stream);
-cudaError_t fault_word_for_launch(unsigned **err);
 cudaError_t launch_attention_delta(const AttnArgs &a, msda_dtype_t dt, cudaStream_t stream);
 cudaError_t launch_attention_join(int mode, const AttnArgs &a, msda_dtype_t dt, cudaStream_t stream);
 

@@ -85,6 +85,12 @@ __global__ void __launch_bounds__(kDeltaThreads) attn_delta_kernel(const AttnArg
             float x[V], y[V];
             unpack16<T>(x, ldg16(static_cast<const T *>(a.go.p) + r * a.D + d));
             unpack16<T>(y, ldg16(static_cast<const T *>(a.o.p) + r * a.D + d));
+            if (a.rest) {
+                float z[V];
+                unpack16<T>(z, ldg16(static_cast<const T *>(a.rest) + r * a.D + d));
+#pragma unroll
+                for (int i = 0; i < V; ++i) y[i] += z[i];
+            }
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 dot = fmaf(x[i], y[i], dot);
@@ -168,11 +174,9 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const AttnArgs a, int mo
             acc = make_float4(fmaf(f, v.x, acc.x), fmaf(f, v.y, acc.y), fmaf(f, v.z, acc.z), fmaf(f, v.w, acc.w));
         }
         const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
-        T *to = static_cast<T *>(a.out) + row * a.D + d;
-        to[0] = Elem<T>::from_f(acc.x * f);
-        to[1] = Elem<T>::from_f(acc.y * f);
-        to[2] = Elem<T>::from_f(acc.z * f);
-        to[3] = Elem<T>::from_f(acc.w * f);
+        const float v[4] = {acc.x * f, acc.y * f, acc.z * f, acc.w * f};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) attn_put<T>(a.out, a.rest, row * a.D + d + k, v[k]);
         if (a.lse && d == 0) {
             const int m = (int)(row % a.M);
             const int64_t bq = row / a.M;

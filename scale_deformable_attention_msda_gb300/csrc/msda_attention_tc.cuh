@@ -1,0 +1,585 @@
+// Attention of 16-bit data on the tensor cores.
+//
+// A block holds 128 rows (queries, or keys in kGradKV) and walks tiles of BN
+// columns, in the three modes of msda_attention.cuh. One warp fetches tiles with
+// TMA, one lane of another issues every MMA, and NWG groups of four warps each
+// take every NWG-th column tile: each of their 128 threads has one whole row of
+// the scores, which it reads from tensor memory, so that a row's maximum and sum
+// need no exchange between threads. The weights go back to tensor memory in 16
+// bits, as the left operand of the second product; nothing of the scores touches
+// shared memory. The same tile in shared memory serves as the right operand of
+// both products, read along its rows for the scores and across them for the
+// second product.
+//
+//            scores                  second product
+// kForward   S = Q K'                O += P V
+// kGradQ     S = Q K', dP = dO V'    dQ += dS K
+// kGradKV    S = K Q', dP = V dO'    dV += P dO, dK += dS Q
+#pragma once
+
+#include <cudaTypedefs.h>
+
+#include "msda_attention_host.h"
+#include "msda_host.h"
+#include "msda_tcgen05.cuh"
+
+namespace msda {
+
+constexpr int kTcRows = 128;
+
+// DP: channels in shared memory. BN: columns of a tile. NWG: groups of warps.
+// ALIAS: the weights lie in the scores' columns of tensor memory, so that the next
+// scores wait for the second product. STAGES: tiles in shared memory. BLOCKS: of
+// an SM, by tensor memory (512 columns) and shared memory.
+template <int MODE, int DP> struct TcConfig;
+template <> struct TcConfig<kForward, 32> { static constexpr int BN = 128, NWG = 1, STAGES = 3, BLOCKS = 2; static constexpr bool ALIAS = false; };
+template <> struct TcConfig<kForward, 64> { static constexpr int BN = 128, NWG = 1, STAGES = 2, BLOCKS = 2; static constexpr bool ALIAS = false; };
+template <> struct TcConfig<kForward, 128> { static constexpr int BN = 64, NWG = 1, STAGES = 2, BLOCKS = 2; static constexpr bool ALIAS = false; };
+template <> struct TcConfig<kGradQ, 32> { static constexpr int BN = 64, NWG = 1, STAGES = 3, BLOCKS = 2; static constexpr bool ALIAS = false; };
+template <> struct TcConfig<kGradQ, 64> { static constexpr int BN = 64, NWG = 1, STAGES = 3, BLOCKS = 2; static constexpr bool ALIAS = false; };
+template <> struct TcConfig<kGradQ, 128> { static constexpr int BN = 64, NWG = 2, STAGES = 3, BLOCKS = 1; static constexpr bool ALIAS = true; };
+template <> struct TcConfig<kGradKV, 32> { static constexpr int BN = 64, NWG = 1, STAGES = 3, BLOCKS = 2; static constexpr bool ALIAS = false; };
+template <> struct TcConfig<kGradKV, 64> { static constexpr int BN = 64, NWG = 1, STAGES = 3, BLOCKS = 2; static constexpr bool ALIAS = true; };
+template <> struct TcConfig<kGradKV, 128> { static constexpr int BN = 64, NWG = 2, STAGES = 3, BLOCKS = 1; static constexpr bool ALIAS = true; };
+
+template <int MODE, int DP> struct Tc : TcConfig<MODE, DP> {
+    using C = TcConfig<MODE, DP>;
+    static constexpr int BN = C::BN, NWG = C::NWG, STAGES = C::STAGES;
+    static constexpr bool ALIAS = C::ALIAS, BACK = MODE != kForward;
+    static constexpr int PITCH = DP == 32 ? 64 : 128, PANELS = DP == 128 ? 2 : 1, PANEL = DP == 128 ? 64 : DP;
+    static constexpr int ROW_BYTES = kTcRows * PITCH * PANELS, COL_BYTES = BN * PITCH * PANELS;
+    static constexpr int THREADS = NWG * 128 + 64;
+    // tensor memory: for each group scores (and dP), then weights unless ALIAS; then
+    // the accumulators (forward: one a group)
+    static constexpr int GROUP = BN * (BACK ? 2 : 1) + (ALIAS ? 0 : BN / 2 * (MODE == kGradKV ? 2 : 1));
+    static constexpr int ACC = NWG * GROUP, ACCS = MODE == kForward ? NWG : MODE == kGradKV ? 2 : 1;
+    static constexpr int USED = ACC + ACCS * DP, COLS = USED <= 128 ? 128 : USED <= 256 ? 256 : 512;
+    static_assert(BN == tc_columns(MODE, DP) && C::BLOCKS == tc_blocks(MODE, DP), "what the host plans with");
+    static_assert(MODE != kForward || NWG == 1, "one maximum and sum a row");
+    static_assert(USED <= 512 && COLS * C::BLOCKS <= 512, "tensor memory");
+    static constexpr int TILES = (BACK ? 2 : 1) * ROW_BYTES + STAGES * 2 * COL_BYTES;
+    static constexpr int NEEDED = 1024 + TILES + 4 * (2 * NWG * 2 * BN + 4 * kTcRows) + 512;
+    // as much as keeps one block more off the SM, which would only wait for its tensor memory
+    static constexpr int LIMIT = 228 * 1024 / (C::BLOCKS + 1);
+    static constexpr int SHARED = NEEDED > LIMIT ? NEEDED : LIMIT;
+    static_assert(SHARED <= 227 * 1024 && (SHARED + 1024) * C::BLOCKS <= 228 * 1024, "shared memory");
+};
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+template <typename T> __device__ __forceinline__ uint32_t pack2(float lo, float hi);
+template <> __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+template <> __device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// fp16 holds what lies between 2^-24 and 65504. The forward's weights, at most 2^8
+// (see the maximum below), are scaled by 2^7; the backward's probabilities by 2^14.
+// ds is at most 2 |dO_i| |v_j| p: it is scaled by the power of two r that takes the
+// largest of these bounds to 2 at most, and so, with p's 2^14, below 2^15 + 2^-10.
+template <typename T> struct TcScale { static constexpr float forward = 0.0f, backward = 0.0f; };
+template <> struct TcScale<__half> { static constexpr float forward = 7.0f, backward = 14.0f; };
+
+__device__ __forceinline__ float tc_most(const float *part, int n) {
+    float v = 0.0f;
+    for (int i = threadIdx.x & 31; i < n; i += 32) v = fmaxf(v, part[i]);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
+    return v;
+}
+__device__ __forceinline__ float tc_ds_scale(const AttnArgs &a) {
+    const float bound = 2.01f * sqrtf(tc_most(a.norm_do, a.norms)) * sqrtf(tc_most(a.norm_v, a.norms));
+    if (bound == 0.0f) return 1.0f;
+    int e;
+    frexpf(bound, &e);                 // bound < 2^e
+    return ldexpf(1.0f, min(1 - e, 100));
+}
+
+// 32 channels of a row: of the output, or of this split's part (scaled by g), and of
+// the output's rounding error.
+template <typename T, int MODE>
+__device__ __forceinline__ void tc_store(const AttnArgs &a, int64_t row, int split, int which, int d0, const float *v,
+                                         float f, float g) {
+    if (a.splits > 1) {
+        float *to = a.part + ((int64_t)(which * a.splits + split) * a.part_rows + row) * a.D;
+#pragma unroll
+        for (int i = 0; i < 32; i += 4)
+            if (d0 + i < a.D)
+                *reinterpret_cast<float4 *>(to + d0 + i) = make_float4(v[i] * g, v[i + 1] * g, v[i + 2] * g, v[i + 3] * g);
+        return;
+    }
+    T *to = static_cast<T *>(MODE == kForward ? a.out : MODE == kGradQ ? a.gq : which ? a.gk : a.gv) + row * a.D;
+#pragma unroll
+    for (int i = 0; i < 32; i += 8) {
+        if (d0 + i >= a.D) break;
+        float x[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[k] = v[i + k] * f;
+        const uint4 packed = pack16<T>(x);
+        *reinterpret_cast<uint4 *>(to + d0 + i) = packed;
+        if (MODE == kForward && a.rest) {
+            float y[8];
+            unpack16<T>(y, packed);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) x[k] -= y[k];
+            *reinterpret_cast<uint4 *>(static_cast<T *>(a.rest) + row * a.D + d0 + i) = pack16<T>(x);
+        }
+    }
+}
+
+struct TcMaps {
+    CUtensorMap a1, a2, x1, x2;        // rows: one or two; columns: two
+};
+
+template <typename T, int MODE, int DP>
+__global__ void __launch_bounds__(Tc<MODE, DP>::THREADS, Tc<MODE, DP>::BLOCKS)
+attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
+    using K = Tc<MODE, DP>;
+    constexpr int BN = K::BN, NWG = K::NWG, STAGES = K::STAGES;
+    constexpr bool BF16 = sizeof(T) == 2 && TcScale<T>::forward == 0.0f, BACK = K::BACK;
+    extern __shared__ unsigned char raw[];
+    unsigned char *base = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+    unsigned char *tile_a1 = base, *tile_a2 = base + K::ROW_BYTES, *tile_x = base + (BACK ? 2 : 1) * K::ROW_BYTES;
+    float *colstat = reinterpret_cast<float *>(base + K::TILES);          // [NWG][2][2][BN]: lse2, delta of columns
+    float *rowstat = colstat + NWG * 2 * 2 * BN;                          // [4][128]
+    uint64_t *bars = reinterpret_cast<uint64_t *>(rowstat + 4 * kTcRows);
+    uint64_t *a_full = bars, *full = bars + 1, *empty = full + STAGES, *s_full = empty + STAGES, *ready = s_full + NWG,
+             *done = ready + NWG, *last = done + NWG;
+    uint32_t *slot = reinterpret_cast<uint32_t *>(last + 1);
+    volatile uint32_t *dead = slot + 1;
+
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    const int split = blockIdx.x % a.splits;
+    const AttnRows w = attn_rows<MODE, kTcRows>(a, blockIdx.x / a.splits);
+    const int64_t tiles = attn_column_tiles<MODE, BN>(a);
+    const int64_t j0 = tiles * split / a.splits, j1 = tiles * (split + 1) / a.splits;
+
+    if (warp == NWG * 4) {
+        tmem_alloc<K::COLS>(slot);
+    } else if (warp == NWG * 4 + 1 && lane == 0) {
+        bar_init(a_full, 1);
+        for (int i = 0; i < STAGES; ++i) {
+            bar_init(full + i, 1);
+            bar_init(empty + i, 1);
+        }
+        for (int i = 0; i < NWG; ++i) {
+            bar_init(s_full + i, 1);
+            bar_init(ready + i, 128);
+            bar_init(done + i, 1);
+        }
+        bar_init(last, 1);
+        bar_init_done();
+        *dead = 0u;
+    }
+    tmem_before_sync();
+    __syncthreads();
+    tmem_after_sync();
+    const uint32_t tmem = *slot;
+
+    int pos, head, cls;
+    // the next column tile with a pair in it, from j on
+    auto next = [&](int64_t j) {
+        for (; j < j1; ++j) {
+            attn_columns<MODE, BN>(a, w, j, &pos, &head);
+            cls = attn_class<MODE, BN>(a, w, pos, head);
+            if (cls) break;
+        }
+        return j;
+    };
+
+    if (warp == NWG * 4 + 1) {
+        // ------------------------------------------------ fetching
+        if (lane == 0) {
+            int it = 0;
+            int64_t j = next(j0);
+            if (j < j1) {
+                bar_expect(a_full, (BACK ? 2 : 1) * (K::PITCH * K::PANELS) * (kTcRows / w.pack * w.pack));
+                for (int p = 0; p < K::PANELS; ++p) {
+                    tma_load(tile_a1 + p * kTcRows * K::PITCH, &maps.a1, 64 * p, w.head, w.pos, w.b, a_full);
+                    if (BACK) tma_load(tile_a2 + p * kTcRows * K::PITCH, &maps.a2, 64 * p, w.head, w.pos, w.b, a_full);
+                }
+            }
+            for (; j < j1; j = next(j + 1), ++it) {
+                const int st = it % STAGES;
+                if (it >= STAGES && !bar_wait(empty + st, (it / STAGES - 1) & 1, dead, a.err)) break;
+                bar_expect(full + st, 2 * K::COL_BYTES);
+                unsigned char *x1 = tile_x + st * 2 * K::COL_BYTES, *x2 = x1 + K::COL_BYTES;
+                for (int p = 0; p < K::PANELS; ++p) {
+                    tma_load(x1 + p * BN * K::PITCH, &maps.x1, 64 * p, head, pos, w.b, full + st);
+                    tma_load(x2 + p * BN * K::PITCH, &maps.x2, 64 * p, head, pos, w.b, full + st);
+                }
+            }
+            if (*dead) {               // copies under way end before the block does
+                uint32_t off = 0u;
+                for (int i = it < STAGES ? 0 : it - STAGES; i < it; ++i) bar_wait(full + i % STAGES, (i / STAGES) & 1, &off, nullptr);
+                if (it > 0) bar_wait(a_full, 0, &off, nullptr);
+            }
+        }
+        __syncwarp();
+    } else if (warp == NWG * 4) {
+        // ------------------------------------------------ MMAs
+        if (lane == 0) {
+            const int steps = (a.D + 15) / 16;
+            const uint32_t a1 = shared_at(tile_a1), a2 = shared_at(tile_a2), x0 = shared_at(tile_x);
+            constexpr uint32_t id_s = mma_desc<BF16, BN, false>(), id_o = mma_desc<BF16, DP, true>();
+            constexpr int per = K::PITCH / 32;      // steps of 16 channels in a panel
+            auto scores = [&](int it) {
+                const int g = it % NWG, st = it % STAGES;
+                const uint32_t x1 = x0 + st * 2 * K::COL_BYTES, x2 = x1 + K::COL_BYTES, d = tmem + g * K::GROUP;
+                for (int k = 0; k < steps; ++k) {
+                    const uint32_t ra = k / per * (kTcRows * K::PITCH) + k % per * 32, rx = k / per * (BN * K::PITCH) + k % per * 32;
+                    mma_shared(d, tile_desc<K::PITCH>(a1 + ra, 16), tile_desc<K::PITCH>(x1 + rx, 16), id_s, k > 0);
+                    if (BACK) mma_shared(d + BN, tile_desc<K::PITCH>(a2 + ra, 16), tile_desc<K::PITCH>(x2 + rx, 16), id_s, k > 0);
+                }
+                mma_commit(s_full + g);
+            };
+            auto second = [&](int it) {
+                const int g = it % NWG, st = it % STAGES;
+                const uint32_t x1 = x0 + st * 2 * K::COL_BYTES, x2 = x1 + K::COL_BYTES;
+                const uint32_t s = tmem + g * K::GROUP, acc = tmem + K::ACC + (MODE == kForward ? g * DP : 0);
+                // weights: P, then dS
+                const uint32_t p = s + (K::ALIAS ? 0 : BN * (BACK ? 2 : 1));
+                const uint32_t ds = MODE == kGradQ ? p : K::ALIAS ? s + BN : p + BN / 2;
+                const bool add = MODE == kForward ? it >= NWG : it > 0;
+                for (int k = 0; k < BN / 16; ++k) {
+                    const uint32_t rx = k * 16 * K::PITCH;
+                    if (MODE != kGradQ) mma_tmem(acc, p + 8 * k, tile_desc<K::PITCH>(x2 + rx, BN * K::PITCH), id_o, add || k > 0);
+                    if (BACK) mma_tmem(acc + (MODE == kGradKV ? DP : 0), ds + 8 * k, tile_desc<K::PITCH>(x1 + rx, BN * K::PITCH), id_o, add || k > 0);
+                }
+                mma_commit(empty + st);
+                mma_commit(done + g);      // last: the block ends after it has arrived
+            };
+            int count = 0, it = 0;
+            int64_t j = next(j0);
+            bool ok = j >= j1 || bar_wait(a_full, 0, dead, a.err);
+            for (; ok && j < j1 && count < NWG; j = next(j + 1), ++count) {
+                ok = bar_wait(full + count % STAGES, (count / STAGES) & 1, dead, a.err);
+                tmem_after_sync();
+                if (ok) scores(count);
+            }
+            for (; ok && it < count; ++it) {
+                const int g = it % NWG, phase = (it / NWG) & 1;
+                ok = bar_wait(ready + g, phase, dead, a.err);
+                tmem_after_sync();
+                if (!ok) break;
+                if (K::ALIAS) second(it);
+                if (j < j1) {
+                    ok = (!K::ALIAS || bar_wait(done + g, phase, dead, a.err)) &&
+                         bar_wait(full + count % STAGES, (count / STAGES) & 1, dead, a.err);
+                    tmem_after_sync();
+                    if (ok) scores(count);
+                    j = next(j + 1);
+                    ++count;
+                }
+                if (!K::ALIAS) second(it);
+            }
+            if (!ok) {                 // MMAs under way end before the block does
+                uint32_t off = 0u;
+                mma_commit(last);
+                bar_wait(last, 0, &off, nullptr);
+            }
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------ one row a thread
+        const int g = warp / 4, r = threadIdx.x % 128;
+        const bool valid = w.valid(r);
+        const bool any_valid = w.valid(r & ~31);           // of this warp's rows
+        const uint32_t mine = tmem + ((uint32_t)(r & ~31) << 16) + g * K::GROUP;
+        const uint32_t at_p = mine + (K::ALIAS ? 0 : BN * (BACK ? 2 : 1));
+        const uint32_t at_ds = MODE == kGradQ ? at_p : K::ALIAS ? mine + BN : at_p + BN / 2;
+        const uint32_t at_acc = tmem + ((uint32_t)(r & ~31) << 16) + K::ACC + (MODE == kForward ? g * DP : 0);
+        const int rpos = w.row_pos(valid ? r : 0), rhead = w.row_head(valid ? r : 0);
+        const int64_t stat = ((int64_t)w.b * a.M + rhead) * a.Q + rpos;
+        const float c = a.c;
+        float ds_scale = 1.0f;
+        if (BACK && a.norm_do) ds_scale = tc_ds_scale(a);
+        constexpr float up = BACK ? TcScale<T>::backward : TcScale<T>::forward;
+        float top = -INFINITY, sum = 0.0f, lse2 = INFINITY, delta = 0.0f;
+        if (MODE == kGradQ && valid) {
+            lse2 = attn_lse2(a.lse[stat]) - up;
+            delta = a.delta[stat] * ds_scale;
+        }
+        const uint32_t *words = MODE == kGradKV ? nullptr : attn_word_row<MODE>(a, w.b, rhead, rpos);
+
+        // after a wait that ran out (ok false) the loop goes on without work: the group's
+        // barriers need all its threads
+        int it = 0;                    // over all groups' tiles
+        bool ok = true;
+        for (int64_t j = next(j0); j < j1; j = next(j + 1), ++it) {
+            if (it % NWG != g) continue;
+            const int phase = (it / NWG) & 1;
+            if (MODE == kGradKV) words = attn_word_row<MODE>(a, w.b, head, rpos);
+            uint32_t bits[BN / 32];
+#pragma unroll
+            for (int i = 0; i < BN / 32; ++i) bits[i] = cls == 2 ? 0xffffffffu : attn_word<MODE>(a, words, pos + 32 * i);
+            float *cs = colstat + (g * 2 + phase) * 2 * BN;
+            if (MODE == kGradKV) {
+                if (r < BN) {
+                    const int at = pos + r;
+                    const int64_t k = ((int64_t)w.b * a.M + head) * a.Q + at;
+                    cs[r] = at < a.Q ? attn_lse2(a.lse[k]) - up : INFINITY;
+                    cs[BN + r] = at < a.Q ? a.delta[k] * ds_scale : 0.0f;
+                }
+                asm volatile("bar.sync %0, 128;" ::"r"(1 + g) : "memory");
+            }
+            ok = ok && bar_wait_warp(s_full + g, phase, dead, a.err);
+            if (!ok) continue;
+            tmem_after_sync();
+            if (MODE == kForward && any_valid) {
+                float most = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < BN / 32; ++i) {
+                    uint32_t s[32];
+                    tmem_load32(s, mine + 32 * i);
+                    tmem_wait_load32(s);
+                    if (cls == 2) {
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) most = fmaxf(most, __uint_as_float(s[k]));
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) most = fmaxf(most, (bits[i] >> k) & 1u ? __uint_as_float(s[k]) : -INFINITY);
+                    }
+                }
+                // The weights are relative to `top`, which follows the maximum only when that has
+                // grown by more than 2^8: then what was summed is scaled down.
+                const bool grow = top == -INFINITY ? most > -INFINITY : (most - top) * c > 8.0f;
+                if (__any_sync(0xffffffffu, grow)) {
+                    const float f = !grow ? 1.0f : top == -INFINITY ? 0.0f : ex2((top - most) * c);
+                    if (grow) top = most;
+                    sum *= f;
+                    if (it >= NWG) {
+                        if (!K::ALIAS) ok = bar_wait_warp(done + g, phase ^ 1, dead, a.err);
+                        tmem_after_sync();
+#pragma unroll
+                        for (int i = 0; i < DP / 32; ++i) {
+                            uint32_t o[32];
+                            tmem_load32(o, at_acc + 32 * i);
+                            tmem_wait_load32(o);
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                            tmem_store32(at_acc + 32 * i, o);
+                        }
+                    }
+                }
+            }
+            if (!K::ALIAS && it >= NWG) {      // the weights' columns are free
+                ok = ok && bar_wait_warp(done + g, phase ^ 1, dead, a.err);
+                tmem_after_sync();
+            }
+            if (!ok) continue;
+            const float ref = top == -INFINITY ? -up : top * c - up;
+            if (any_valid) {
+#pragma unroll
+                for (int i = 0; i < BN / 32; ++i) {
+                    uint32_t s[32], out[16];
+                    tmem_load32(s, mine + 32 * i);
+                    if (MODE == kForward) {
+                        tmem_wait_load32(s);
+#pragma unroll
+                        for (int k = 0; k < 32; k += 2) {
+                            float x = fmaf(__uint_as_float(s[k]), c, -ref), y = fmaf(__uint_as_float(s[k + 1]), c, -ref);
+                            if (cls != 2) {
+                                x = (bits[i] >> k) & 1u ? x : -INFINITY;
+                                y = (bits[i] >> (k + 1)) & 1u ? y : -INFINITY;
+                            }
+                            const float p = ex2(x), q = ex2(y);
+                            sum += p + q;
+                            out[k / 2] = pack2<T>(p, q);
+                        }
+                        tmem_store16(at_p + 16 * i, out);
+                    } else {
+                        uint32_t dp[32], out2[16];
+                        tmem_load32(dp, mine + BN + 32 * i);
+                        tmem_wait_load32(s);
+                        tmem_wait_load32(dp);
+#pragma unroll
+                        for (int k = 0; k < 32; k += 2) {
+                            float l0 = lse2, l1 = lse2, e0 = delta, e1 = delta;
+                            if (MODE == kGradKV) {
+                                const float2 l = *reinterpret_cast<const float2 *>(cs + 32 * i + k);
+                                const float2 e = *reinterpret_cast<const float2 *>(cs + BN + 32 * i + k);
+                                l0 = l.x; l1 = l.y; e0 = e.x; e1 = e.y;
+                            }
+                            float p = ex2(fmaf(__uint_as_float(s[k]), c, -l0)), q = ex2(fmaf(__uint_as_float(s[k + 1]), c, -l1));
+                            float t = __uint_as_float(dp[k]), u = __uint_as_float(dp[k + 1]);
+                            t = p * (BF16 ? t - e0 : fmaf(t, ds_scale, -e0));
+                            u = q * (BF16 ? u - e1 : fmaf(u, ds_scale, -e1));
+                            if (cls != 2) {
+                                const bool on0 = (bits[i] >> k) & 1u, on1 = (bits[i] >> (k + 1)) & 1u;
+                                p = on0 ? p : 0.0f;
+                                q = on1 ? q : 0.0f;
+                                t = on0 ? t : 0.0f;
+                                u = on1 ? u : 0.0f;
+                            }
+                            out[k / 2] = pack2<T>(p, q);
+                            out2[k / 2] = pack2<T>(t, u);
+                        }
+                        if (MODE == kGradKV) tmem_store16(at_p + 16 * i, out);
+                        tmem_store16(at_ds + 16 * i, out2);
+                    }
+                }
+                tmem_wait_store();
+            }
+            tmem_before_sync();
+            bar_arrive(ready + g);
+        }
+
+        // ------------------------------------------------ results
+        const int count = it;          // column tiles of this block; this group's last is its number it
+        const int own = (count - g + NWG - 1) / NWG;       // tiles of this group
+        if (ok && own > 0) ok = bar_wait_warp(done + g, (own - 1) & 1, dead, a.err);
+        tmem_after_sync();
+        if (NWG > 1) {
+            tmem_before_sync();
+            asm volatile("bar.sync 7, %0;" ::"n"(NWG * 128) : "memory");
+            tmem_after_sync();
+        }
+        // the first group has the first results of the rows, the second the others (kGradKV)
+        const bool here = any_valid && __all_sync(0xffffffffu, ok && !*dead) && (g == 0 || MODE == kGradKV);
+        if (here) {
+            constexpr int RESULTS = MODE == kGradKV ? 2 : 1;
+            const uint32_t acc0 = tmem + ((uint32_t)(r & ~31) << 16) + K::ACC;
+            const int64_t row = MODE == kGradKV ? ((int64_t)w.b * a.S + rpos) * a.N + rhead : ((int64_t)w.b * a.Q + rpos) * a.M + rhead;
+            const float ref = top == -INFINITY ? -up : top * c - up;
+            const float down = BACK ? ex2(-up) : 1.0f;     // of P; of dS also 1 / ds_scale
+            const float down_ds = down / ds_scale;
+            if (MODE == kForward && valid) {
+                if (a.splits > 1) {
+                    float *ml = a.part + (int64_t)a.splits * a.part_rows * a.D + 2 * ((int64_t)split * a.part_rows + row);
+                    ml[0] = sum == 0.0f ? -INFINITY : ref;
+                    ml[1] = sum;
+                } else if (a.lse) {
+                    a.lse[stat] = sum == 0.0f ? -INFINITY : (ref + log2f(sum)) * kLn2;
+                }
+            }
+            const float over = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+            for (int which = 0; which < RESULTS; ++which) {
+                if (NWG > 1 && MODE == kGradKV && which != g) continue;
+                const float g_ = MODE == kForward ? 1.0f : MODE == kGradQ || which ? down_ds : down;
+                const float f = MODE == kForward ? over : g_ * (MODE == kGradQ || which ? a.scale : 1.0f);
+                bool finite = true;
+                if (a.classes && count > 0) {
+#pragma unroll
+                    for (int i = 0; i < DP / 32; ++i) {
+                        uint32_t o[32];
+                        tmem_load32(o, acc0 + which * DP + 32 * i);
+                        tmem_wait_load32(o);
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) finite = finite && isfinite(__uint_as_float(o[k]));
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < DP / 32; ++i) {
+                    uint32_t o[32];
+                    float v[32];
+                    if (count > 0) {
+                        tmem_load32(o, acc0 + which * DP + 32 * i);
+                        tmem_wait_load32(o);
+                    }
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) v[k] = count > 0 ? __uint_as_float(o[k]) : 0.0f;
+                    if (valid && finite) tc_store<T, MODE>(a, row, split, which, 32 * i, v, f, g_);
+                }
+                uint32_t bad = __ballot_sync(0xffffffffu, valid && !finite);
+                while (bad) {
+                    const int from = __ffs(bad) - 1;
+                    bad &= bad - 1;
+                    float e1[4], e2[4];
+                    const float m2 = __shfl_sync(0xffffffffu, ref, from), o = __shfl_sync(0xffffffffu, over, from);
+                    attn_exact_row<T, MODE, BN>(a, w, (r & ~31) + from, j0, j1, m2, e1, e2);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int d = lane + 32 * i;
+                        if (d < a.D)
+                            attn_store<T, MODE>(a, w, (r & ~31) + from, split, which, d, MODE == kGradQ || which ? e2[i] : e1[i],
+                                                MODE == kForward ? o : MODE == kGradQ || which ? a.scale : 1.0f);
+                    }
+                }
+            }
+        }
+        tmem_before_sync();
+    }
+    __syncthreads();
+    if (warp == NWG * 4) {
+        tmem_after_sync();
+        tmem_free<K::COLS>(tmem);
+    }
+}
+
+// ------------------------------------------------------------------ launch
+
+// A map of boxes of `heads` heads and `positions` positions.
+template <int MODE, int DP>
+cudaError_t tc_map(CUtensorMap *map, const AttnTensor &t, const AttnArgs &a, int len, int heads, int box_heads, int box_positions,
+                   bool bf16) {
+    using K = Tc<MODE, DP>;
+    const cuuint64_t dense = (cuuint64_t)a.D * 2;
+    const cuuint64_t dims[4] = {(cuuint64_t)a.D, (cuuint64_t)heads, (cuuint64_t)len, (cuuint64_t)a.B};
+    const cuuint64_t strides[3] = {heads > 1 ? (cuuint64_t)t.head * 2 : dense, len > 1 ? (cuuint64_t)t.pos * 2 : dense,
+                                   a.B > 1 ? (cuuint64_t)t.batch * 2 : dense};
+    const cuuint32_t box[4] = {(cuuint32_t)K::PANEL, (cuuint32_t)box_heads, (cuuint32_t)box_positions, 1};
+    const cuuint32_t ones[4] = {1, 1, 1, 1};
+    const PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
+    if (!encode) return cudaErrorNotSupported;
+    const CUresult r = encode(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+                              const_cast<void *>(t.p), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              K::PITCH == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+template <typename T, int MODE, int DP>
+cudaError_t launch_tc_d(const AttnArgs &a, int64_t blocks, cudaStream_t stream) {
+    using K = Tc<MODE, DP>;
+    constexpr bool bf16 = TcScale<T>::forward == 0.0f;
+    TcMaps maps;
+    cudaError_t e;
+    // no columns: the maps are of what is there, and nothing is fetched
+    const bool none = MODE == kGradKV ? a.Q == 0 : a.S == 0;
+    if (MODE == kGradKV) {
+        const AttnTensor &x1 = none ? a.k : a.q, &x2 = none ? a.v : a.go;
+        const int len = none ? a.S : a.Q, heads = none ? a.N : a.M;
+        if ((e = tc_map<MODE, DP>(&maps.a1, a.k, a, a.S, a.N, 1, kTcRows, bf16)) != cudaSuccess ||
+            (e = tc_map<MODE, DP>(&maps.a2, a.v, a, a.S, a.N, 1, kTcRows, bf16)) != cudaSuccess ||
+            (e = tc_map<MODE, DP>(&maps.x1, x1, a, len, heads, 1, K::BN, bf16)) != cudaSuccess ||
+            (e = tc_map<MODE, DP>(&maps.x2, x2, a, len, heads, 1, K::BN, bf16)) != cudaSuccess)
+            return e;
+    } else {
+        const AttnTensor &x1 = none ? a.q : a.k, &x2 = none ? a.q : a.v;
+        const int len = none ? a.Q : a.S, heads = none ? a.M : a.N;
+        if ((e = tc_map<MODE, DP>(&maps.a1, a.q, a, a.Q, a.M, a.pack, kTcRows / a.pack, bf16)) != cudaSuccess ||
+            (e = tc_map<MODE, DP>(&maps.x1, x1, a, len, heads, 1, K::BN, bf16)) != cudaSuccess ||
+            (e = tc_map<MODE, DP>(&maps.x2, x2, a, len, heads, 1, K::BN, bf16)) != cudaSuccess)
+            return e;
+        maps.a2 = maps.a1;
+        if (MODE == kGradQ && (e = tc_map<MODE, DP>(&maps.a2, a.go, a, a.Q, a.M, a.pack, kTcRows / a.pack, bf16)) != cudaSuccess) return e;
+    }
+    auto *kernel = attn_tc_kernel<T, MODE, DP>;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, K::SHARED);
+    if (e != cudaSuccess) return e;
+    kernel<<<(unsigned)blocks, K::THREADS, K::SHARED, stream>>>(a, maps);
+    return cudaGetLastError();
+}
+template <typename T, int MODE>
+cudaError_t launch_tc_mode(const AttnArgs &a, int64_t blocks, cudaStream_t stream) {
+    return a.D <= 32 ? launch_tc_d<T, MODE, 32>(a, blocks, stream)
+         : a.D <= 64 ? launch_tc_d<T, MODE, 64>(a, blocks, stream)
+                     : launch_tc_d<T, MODE, 128>(a, blocks, stream);
+}
+template <typename T>
+cudaError_t launch_tc(int mode, const AttnArgs &a, int64_t blocks, cudaStream_t stream) {
+    return mode == kForward ? launch_tc_mode<T, kForward>(a, blocks, stream)
+         : mode == kGradQ   ? launch_tc_mode<T, kGradQ>(a, blocks, stream)
+                            : launch_tc_mode<T, kGradKV>(a, blocks, stream);
+}
+
+}  // namespace msda

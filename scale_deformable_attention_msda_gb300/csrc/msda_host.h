@@ -1,6 +1,7 @@
 // Host-side helpers shared by the entry points (no device code).
 #pragma once
 
+#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -20,5 +21,9 @@ cudaError_t symbol_address(const void *symbol, void **out);
 // of the range-checked build record an access outside a tensor;
 // msda_device_check reads and clears it.
 cudaError_t fault_word(unsigned **out);
+
+// The driver's encoder of tensor maps (the library does not link libcuda); NULL if
+// it has none.
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 
 }  // namespace msda

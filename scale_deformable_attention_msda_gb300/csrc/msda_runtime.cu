@@ -28,6 +28,7 @@ F driver_entry(const char *name) {
 struct DriverApi {
     PFN_cuCtxGetCurrent_v4000 ctx_get_current = nullptr;
     PFN_cuCtxGetId_v12000 ctx_get_id = nullptr;
+    PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
 };
 
 const DriverApi &driver() {
@@ -36,6 +37,7 @@ const DriverApi &driver() {
     std::call_once(once, [] {
         api.ctx_get_current = driver_entry<PFN_cuCtxGetCurrent_v4000>("cuCtxGetCurrent");
         api.ctx_get_id = driver_entry<PFN_cuCtxGetId_v12000>("cuCtxGetId");
+        api.encode = driver_entry<PFN_cuTensorMapEncodeTiled_v12000>("cuTensorMapEncodeTiled");
     });
     return api;
 }
@@ -97,6 +99,8 @@ cudaError_t symbol_address(const void *symbol, void **out) {
     if (g_used < kCacheSlots) g_cache[g_used++] = CachedAddress{symbol, dev, now, p};
     return cudaSuccess;
 }
+
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() { return driver().encode; }
 
 cudaError_t fault_word(unsigned **out) {
     void *p = nullptr;
