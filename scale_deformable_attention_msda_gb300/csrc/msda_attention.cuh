@@ -30,6 +30,9 @@ enum AttnMode { kForward = 0, kGradQ = 1, kGradKV = 2 };
 constexpr int kAttnMaxD = 128;
 constexpr int kAttnGranule = 64;       // queries and keys of one class of the mask
 constexpr float kLog2e = 1.4426950408889634f;
+// fp16 holds what lies between 2^-24 and 65504: the backward's probabilities are scaled
+// by 2^14, the forward's weights, at most 2^8, by 2^7.
+constexpr float kHalfUp = 14.0f, kHalfWeightUp = 7.0f;
 constexpr float kLn2 = 0.6931471805599453f;
 
 // A tensor of positions and heads: strides in elements.
@@ -50,7 +53,11 @@ struct AttnArgs {
     void *out, *gq, *gk, *gv;
     void *rest;                        // what out's rounding left, of out's type and shape; NULL: none
     float *lse;                        // (B, M, Q); forward: may be NULL
-    float *delta;                      // (B, M, Q)
+    // backward: (B, M, stat_row / 2, 4), for two queries each -lse in the exponent's
+    // units, plus `up`, and -delta; past the last query -infinity and 0
+    float *stat;
+    int stat_row;                      // queries in a row of stat: Q up to a multiple of 64
+    float up;                          // fp16 backward: its probabilities are scaled by 2^up
     // fp16 backward: partial maxima of |dO_i|^2 and |v_j|^2 (norms each, see
     // attn_delta_kernel); NULL for other types
     float *norm_do, *norm_v;
@@ -172,6 +179,11 @@ __device__ __forceinline__ float attn_lse2(float lse) {
     return lse == -INFINITY ? INFINITY : lse == INFINITY ? __int_as_float(0x7fffffff) : lse * kLog2e;
 }
 
+// A query's pair of stat.
+__device__ __forceinline__ float *attn_stat(const AttnArgs &a, int b, int head, int pos) {
+    return a.stat + ((int64_t)b * a.M + head) * a.stat_row * 2 + (pos >> 1) * 4 + (pos & 1);
+}
+
 // What lies in a masked place may be anything. Its score and its weight are
 // replaced, but a product of the weight 0 with NaN or infinity is NaN, so a row
 // whose sums are not finite is computed again from its allowed pairs alone: by
@@ -186,8 +198,12 @@ __device__ __noinline__ void attn_exact_row(const AttnArgs &a, const AttnRows &w
     const T *a1 = MODE == kGradKV ? attn_at<T>(a.k, w.b, pos, head) : attn_at<T>(a.q, w.b, pos, head);
     const T *a2 = MODE == kGradKV ? attn_at<T>(a.v, w.b, pos, head)
                                   : MODE == kGradQ ? attn_at<T>(a.go, w.b, pos, head) : nullptr;
-    const int64_t stat = ((int64_t)w.b * a.M + head) * a.Q + pos;
-    float lse2 = MODE == kGradQ ? attn_lse2(a.lse[stat]) : m2, delta = MODE == kGradQ ? a.delta[stat] : 0.0f;
+    float lse2 = m2, delta = 0.0f;
+    if (MODE == kGradQ) {
+        const float *st = attn_stat(a, w.b, head, pos);
+        lse2 = a.up - st[0];
+        delta = -st[2];
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc1[i] = acc2[i] = 0.0f;
     for (int64_t j = j0; j < j1; ++j) {
@@ -210,9 +226,9 @@ __device__ __noinline__ void attn_exact_row(const AttnArgs &a, const AttnRows &w
                     if (MODE != kForward) dp = fmaf(Elem<T>::to_f(a2[d]), Elem<T>::to_f(x2[d]), dp);
                 }
                 if (MODE == kGradKV) {
-                    const int64_t cs = ((int64_t)w.b * a.M + chead) * a.Q + at;
-                    lse2 = attn_lse2(a.lse[cs]);
-                    delta = a.delta[cs];
+                    const float *st = attn_stat(a, w.b, chead, at);
+                    lse2 = a.up - st[0];
+                    delta = -st[2];
                 }
                 if (MODE != kForward) on = lse2 != INFINITY;
                 p = on ? exp2f(fmaf(s, a.c, -lse2)) : 0.0f;

@@ -91,7 +91,7 @@ ModePlan plan_for(const msda_attention_dims_t &d, msda_dtype_t dt, AttnMode mode
 
 // The workspace, each piece on a 256-byte boundary.
 struct Layout {
-    size_t bits_q, bits_k, classes, delta, norms, part[3], bytes;
+    size_t bits_q, bits_k, classes, stat, norms, part[3], bytes;
     int mb, mm, mq, words_q, words_k, granules;    // the mask's own extents (1 where it repeats)
 };
 
@@ -117,7 +117,7 @@ Layout layout_of(const msda_attention_dims_t &d, msda_dtype_t dt, bool mask, boo
         if (backward) w.bits_k = take(maps * d.S * w.words_k * 4);
     }
     if (backward) {
-        w.delta = take((size_t)d.B * d.M * d.Q * 4);
+        w.stat = take((size_t)d.B * d.M * ceil_div(d.Q, 64) * 64 * 8);
         if (dt == MSDA_F16) w.norms = take(2 * kDeltaBlocks * 4);
         w.part[1] = take(plan_for(d, dt, msda::kGradQ).part);
         w.part[2] = take(plan_for(d, dt, msda::kGradKV).part);
@@ -146,7 +146,8 @@ AttnArgs common_args(const msda_attention_dims_t &d, const void *q, const void *
     a.D = (int)d.D;
     a.G = (int)(d.M / d.N);
     a.scale = (float)scale;
-    a.c = (float)(scale * 1.4426950408889634);
+    // above zero, so that a masked score, -infinity, stays so
+    a.c = (float)(scale * 1.4426950408889634 > 1e-37 ? scale * 1.4426950408889634 : 1e-37);
     return a;
 }
 
@@ -260,7 +261,9 @@ msda_status_t msda_attention_backward(const void *grad_out, const void *q, const
     if (msda::fault_word(&a.err) != cudaSuccess) return MSDA_ERR_CUDA;
     char *ws = static_cast<char *>(workspace);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    a.delta = reinterpret_cast<float *>(ws + w.delta);
+    a.stat = reinterpret_cast<float *>(ws + w.stat);
+    a.stat_row = (int)(ceil_div(d.Q, 64) * 64);
+    a.up = dtype == MSDA_F16 ? msda::kHalfUp : 0.0f;
     const int64_t rows = d.B * d.Q * d.M;
     a.norms = (int)(rows < 1 ? 1 : rows < kDeltaBlocks ? rows : kDeltaBlocks);
     if (dtype == MSDA_F16) {

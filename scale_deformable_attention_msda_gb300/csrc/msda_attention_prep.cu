@@ -68,26 +68,28 @@ __global__ void __launch_bounds__(256) attn_pack_kernel(const AttnMaskSource m, 
 
 constexpr int kDeltaThreads = 512, kDeltaBlocks = 304;
 
-// delta = sum over channels of dO out for each query and head, L lanes a row of
-// 16 bytes each. fp16 (norm_do given): also the largest finite |dO_i|^2 and
-// |v_j|^2 of what this block has seen.
+// The queries' stat: the row sums delta = sum over channels of dO out, L lanes a row
+// of 16 bytes each, beside the forward's lse. fp16 (norm_do given): also the largest
+// finite |dO_i|^2 and |v_j|^2 of what this block has seen.
 template <typename T, int L>
 __global__ void __launch_bounds__(kDeltaThreads) attn_delta_kernel(const AttnArgs a) {
     constexpr int V = 16 / sizeof(T), per = kDeltaThreads / L;
     const int lane = threadIdx.x % L, d = lane * V;
-    const int64_t rows = (int64_t)a.B * a.Q * a.M;
+    const int64_t rows = (int64_t)a.B * a.stat_row * a.M;
     float most_do = 0.0f, most_v = 0.0f;
     for (int64_t r0 = (int64_t)blockIdx.x * per; r0 < rows; r0 += (int64_t)gridDim.x * per) {
-        const int64_t r = r0 + threadIdx.x / L;
-        const bool valid = r < rows;
+        const int64_t r = r0 + threadIdx.x / L, bq = r / a.M;
+        const int m = (int)(r % a.M), b = (int)(bq / a.stat_row), q = (int)(bq % a.stat_row);
+        const bool valid = r < rows && q < a.Q;
         float dot = 0.0f, square = 0.0f;
         if (valid && d < a.D) {
+            const int64_t at = (((int64_t)b * a.Q + q) * a.M + m) * a.D + d;
             float x[V], y[V];
-            unpack16<T>(x, ldg16(static_cast<const T *>(a.go.p) + r * a.D + d));
-            unpack16<T>(y, ldg16(static_cast<const T *>(a.o.p) + r * a.D + d));
+            unpack16<T>(x, ldg16(static_cast<const T *>(a.go.p) + at));
+            unpack16<T>(y, ldg16(static_cast<const T *>(a.o.p) + at));
             if (a.rest) {
                 float z[V];
-                unpack16<T>(z, ldg16(static_cast<const T *>(a.rest) + r * a.D + d));
+                unpack16<T>(z, ldg16(static_cast<const T *>(a.rest) + at));
 #pragma unroll
                 for (int i = 0; i < V; ++i) y[i] += z[i];
             }
@@ -103,10 +105,10 @@ __global__ void __launch_bounds__(kDeltaThreads) attn_delta_kernel(const AttnArg
             square += __shfl_xor_sync(0xffffffffu, square, off);
         }
         if (isfinite(square)) most_do = fmaxf(most_do, square);
-        if (valid && lane == 0) {
-            const int m = (int)(r % a.M);
-            const int64_t bq = r / a.M;
-            a.delta[(bq / a.Q * a.M + m) * a.Q + bq % a.Q] = dot;
+        if (r < rows && lane == 0) {
+            float *to = attn_stat(a, b, m, q);
+            to[0] = valid ? a.up - attn_lse2(a.lse[((int64_t)b * a.M + m) * a.Q + q]) : -INFINITY;
+            to[2] = valid ? -dot : 0.0f;
         }
     }
     if (!a.norm_do) return;

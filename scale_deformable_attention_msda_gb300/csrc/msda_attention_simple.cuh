@@ -115,9 +115,9 @@ __global__ void __launch_bounds__(kSimpleThreads) attn_simple_kernel(const AttnA
         if (MODE != kGradKV && w.valid(r)) {
             words[i] = attn_word_row<MODE>(a, w.b, w.row_head(r), w.row_pos(r));
             if (MODE == kGradQ) {
-                const int64_t at = ((int64_t)w.b * a.M + w.row_head(r)) * a.Q + w.row_pos(r);
-                lse2[i] = attn_lse2(a.lse[at]);
-                delta[i] = a.delta[at];
+                const float *st = attn_stat(a, w.b, w.row_head(r), w.row_pos(r));
+                lse2[i] = -st[0];
+                delta[i] = -st[2];
             }
         }
 #pragma unroll
@@ -137,10 +137,9 @@ __global__ void __launch_bounds__(kSimpleThreads) attn_simple_kernel(const AttnA
         simple_load<T, DP>(sh.x2, a.D, column_of(MODE == kGradKV ? a.go : a.v));
         if (MODE == kGradKV) {
             if (threadIdx.x < C) {
-                const int at = pos + threadIdx.x;
-                const int64_t s = ((int64_t)w.b * a.M + head) * a.Q + at;
-                sh.lse2[threadIdx.x] = at < len ? attn_lse2(a.lse[s]) : INFINITY;
-                sh.delta[threadIdx.x] = at < len ? a.delta[s] : 0.0f;
+                const float *st = attn_stat(a, w.b, head, pos + threadIdx.x);
+                sh.lse2[threadIdx.x] = -st[0];
+                sh.delta[threadIdx.x] = -st[2];
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i)

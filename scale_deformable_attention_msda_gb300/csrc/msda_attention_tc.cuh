@@ -17,6 +17,7 @@
 // kGradKV    S = K Q', dP = V dO'    dV += P dO, dK += dS Q
 #pragma once
 
+#include <stdio.h>
 #include <cudaTypedefs.h>
 
 #include "msda_attention_host.h"
@@ -37,9 +38,9 @@ template <> struct TcConfig<kForward, 64> { static constexpr int BN = 128, NWG =
 template <> struct TcConfig<kForward, 128> { static constexpr int BN = 64, NWG = 1, STAGES = 2, BLOCKS = 2; static constexpr bool ALIAS = false; };
 template <> struct TcConfig<kGradQ, 32> { static constexpr int BN = 64, NWG = 1, STAGES = 3, BLOCKS = 2; static constexpr bool ALIAS = false; };
 template <> struct TcConfig<kGradQ, 64> { static constexpr int BN = 64, NWG = 1, STAGES = 3, BLOCKS = 2; static constexpr bool ALIAS = false; };
-template <> struct TcConfig<kGradQ, 128> { static constexpr int BN = 64, NWG = 2, STAGES = 3, BLOCKS = 1; static constexpr bool ALIAS = true; };
+template <> struct TcConfig<kGradQ, 128> { static constexpr int BN = 64, NWG = 2, STAGES = 4, BLOCKS = 1; static constexpr bool ALIAS = false; };
 template <> struct TcConfig<kGradKV, 32> { static constexpr int BN = 64, NWG = 1, STAGES = 3, BLOCKS = 2; static constexpr bool ALIAS = false; };
-template <> struct TcConfig<kGradKV, 64> { static constexpr int BN = 64, NWG = 1, STAGES = 3, BLOCKS = 2; static constexpr bool ALIAS = true; };
+template <> struct TcConfig<kGradKV, 64> { static constexpr int BN = 64, NWG = 2, STAGES = 4, BLOCKS = 1; static constexpr bool ALIAS = false; };
 template <> struct TcConfig<kGradKV, 128> { static constexpr int BN = 64, NWG = 2, STAGES = 3, BLOCKS = 1; static constexpr bool ALIAS = true; };
 
 template <int MODE, int DP> struct Tc : TcConfig<MODE, DP> {
@@ -55,10 +56,12 @@ template <int MODE, int DP> struct Tc : TcConfig<MODE, DP> {
     static constexpr int ACC = NWG * GROUP, ACCS = MODE == kForward ? NWG : MODE == kGradKV ? 2 : 1;
     static constexpr int USED = ACC + ACCS * DP, COLS = USED <= 128 ? 128 : USED <= 256 ? 256 : 512;
     static_assert(BN == tc_columns(MODE, DP) && C::BLOCKS == tc_blocks(MODE, DP), "what the host plans with");
+    static_assert(NWG <= STAGES, "an end for each group");
     static_assert(MODE != kForward || NWG == 1, "one maximum and sum a row");
     static_assert(USED <= 512 && COLS * C::BLOCKS <= 512, "tensor memory");
     static constexpr int TILES = (BACK ? 2 : 1) * ROW_BYTES + STAGES * 2 * COL_BYTES;
-    static constexpr int NEEDED = 1024 + TILES + 4 * (2 * NWG * 2 * BN + 4 * kTcRows) + 512;
+    static constexpr int STAT_BYTES = MODE == kGradKV ? 8 * BN : 0;    // of a column tile
+    static constexpr int NEEDED = 1024 + TILES + STAGES * STAT_BYTES + 1024;
     // as much as keeps one block more off the SM, which would only wait for its tensor memory
     static constexpr int LIMIT = 228 * 1024 / (C::BLOCKS + 1);
     static constexpr int SHARED = NEEDED > LIMIT ? NEEDED : LIMIT;
@@ -80,12 +83,10 @@ template <> __device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-// fp16 holds what lies between 2^-24 and 65504. The forward's weights, at most 2^8
-// (see the maximum below), are scaled by 2^7; the backward's probabilities by 2^14.
-// ds is at most 2 |dO_i| |v_j| p: it is scaled by the power of two r that takes the
-// largest of these bounds to 2 at most, and so, with p's 2^14, below 2^15 + 2^-10.
+// ds is at most 2 |dO_i| |v_j| p: for fp16 it is scaled by the power of two r that takes
+// the largest of these bounds to 2 at most, and so, with p's 2^14, below 2^15 + 2^-10.
 template <typename T> struct TcScale { static constexpr float forward = 0.0f, backward = 0.0f; };
-template <> struct TcScale<__half> { static constexpr float forward = 7.0f, backward = 14.0f; };
+template <> struct TcScale<__half> { static constexpr float forward = kHalfWeightUp, backward = kHalfUp; };
 
 __device__ __forceinline__ float tc_most(const float *part, int n) {
     float v = 0.0f;
@@ -134,6 +135,20 @@ __device__ __forceinline__ void tc_store(const AttnArgs &a, int64_t row, int spl
     }
 }
 
+#ifdef V_CLOCK
+#define VCLKDEF long long ck[8] = {}, ck0 = clock64(); const long long ckb = ck0;
+#define VCLK(i) { const long long n_ = clock64(); ck[i] += n_ - ck0; ck0 = n_; }
+#define VCLKPRINT if (threadIdx.x == 0 && (blockIdx.x == 0 || blockIdx.x == 200)) printf("mode %d DP %d it %d total %lld : loop %lld s_full %lld ld %lld max %lld done %lld exp %lld st %lld\n", MODE, DP, own, (clock64() - ckb) / (own ? own : 1), ck[0] / (own ? own : 1), ck[1] / (own ? own : 1), ck[2] / (own ? own : 1), ck[3] / (own ? own : 1), ck[4] / (own ? own : 1), ck[5] / (own ? own : 1), ck[6] / (own ? own : 1));
+#else
+#define VCLKDEF
+#define VCLK(i)
+#define VCLKPRINT
+#endif
+// What the fetching lane tells the others of a column tile; cls 0: there is none more.
+struct TcTile {
+    int pos, head, cls;
+};
+
 struct TcMaps {
     CUtensorMap a1, a2, x1, x2;        // rows: one or two; columns: two
 };
@@ -143,16 +158,17 @@ __global__ void __launch_bounds__(Tc<MODE, DP>::THREADS, Tc<MODE, DP>::BLOCKS)
 attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
     using K = Tc<MODE, DP>;
     constexpr int BN = K::BN, NWG = K::NWG, STAGES = K::STAGES;
-    constexpr bool BF16 = sizeof(T) == 2 && TcScale<T>::forward == 0.0f, BACK = K::BACK;
+    constexpr bool BF16 = TcScale<T>::forward == 0.0f, BACK = K::BACK;
     extern __shared__ unsigned char raw[];
     unsigned char *base = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
     unsigned char *tile_a1 = base, *tile_a2 = base + K::ROW_BYTES, *tile_x = base + (BACK ? 2 : 1) * K::ROW_BYTES;
-    float *colstat = reinterpret_cast<float *>(base + K::TILES);          // [NWG][2][2][BN]: lse2, delta of columns
-    float *rowstat = colstat + NWG * 2 * 2 * BN;                          // [4][128]
-    uint64_t *bars = reinterpret_cast<uint64_t *>(rowstat + 4 * kTcRows);
-    uint64_t *a_full = bars, *full = bars + 1, *empty = full + STAGES, *s_full = empty + STAGES, *ready = s_full + NWG,
-             *done = ready + NWG, *last = done + NWG;
-    uint32_t *slot = reinterpret_cast<uint32_t *>(last + 1);
+    unsigned char *tile_stat = base + K::TILES;                           // stat of a tile's columns
+    uint64_t *bars = reinterpret_cast<uint64_t *>(tile_stat + STAGES * K::STAT_BYTES);
+    uint64_t *a_full = bars, *full = bars + 1, *empty = full + STAGES, *s_full = empty + STAGES, *s_free = s_full + NWG,
+             *ready = s_free + NWG, *done = ready + NWG, *last = done + NWG;
+    TcTile *info = reinterpret_cast<TcTile *>(last + 1);                  // [STAGES]
+    int *total = reinterpret_cast<int *>(info + STAGES);
+    uint32_t *slot = reinterpret_cast<uint32_t *>(total + 1);
     volatile uint32_t *dead = slot + 1;
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
@@ -171,50 +187,62 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
         }
         for (int i = 0; i < NWG; ++i) {
             bar_init(s_full + i, 1);
+            bar_init(s_free + i, 128);
             bar_init(ready + i, 128);
             bar_init(done + i, 1);
         }
         bar_init(last, 1);
         bar_init_done();
         *dead = 0u;
+        *total = 0;
     }
     tmem_before_sync();
     __syncthreads();
     tmem_after_sync();
     const uint32_t tmem = *slot;
 
-    int pos, head, cls;
-    // the next column tile with a pair in it, from j on
-    auto next = [&](int64_t j) {
-        for (; j < j1; ++j) {
-            attn_columns<MODE, BN>(a, w, j, &pos, &head);
-            cls = attn_class<MODE, BN>(a, w, pos, head);
-            if (cls) break;
-        }
-        return j;
-    };
-
     if (warp == NWG * 4 + 1) {
         // ------------------------------------------------ fetching
         if (lane == 0) {
-            int it = 0;
-            int64_t j = next(j0);
-            if (j < j1) {
-                bar_expect(a_full, (BACK ? 2 : 1) * (K::PITCH * K::PANELS) * (kTcRows / w.pack * w.pack));
-                for (int p = 0; p < K::PANELS; ++p) {
-                    tma_load(tile_a1 + p * kTcRows * K::PITCH, &maps.a1, 64 * p, w.head, w.pos, w.b, a_full);
-                    if (BACK) tma_load(tile_a2 + p * kTcRows * K::PITCH, &maps.a2, 64 * p, w.head, w.pos, w.b, a_full);
+            int it = 0, pos = 0, head = 0;
+            if (j0 < j1) attn_columns<MODE, BN>(a, w, j0, &pos, &head);
+            bool ok = true;
+            for (int64_t j = j0; j < j1 && ok; ++j) {
+                const int cls = attn_class<MODE, BN>(a, w, pos, head);
+                if (cls) {
+                    if (it == 0) {
+                        bar_expect(a_full, (BACK ? 2 : 1) * (K::PITCH * K::PANELS) * (kTcRows / w.pack * w.pack));
+                        for (int p = 0; p < K::PANELS; ++p) {
+                            tma_load(tile_a1 + p * kTcRows * K::PITCH, &maps.a1, 64 * p, w.head, w.pos, w.b, a_full);
+                            if (BACK) tma_load(tile_a2 + p * kTcRows * K::PITCH, &maps.a2, 64 * p, w.head, w.pos, w.b, a_full);
+                        }
+                    }
+                    const int st = it % STAGES;
+                    ok = it < STAGES || bar_wait(empty + st, (it / STAGES - 1) & 1, dead, a.err);
+                    if (!ok) break;
+                    info[st] = {pos, head, cls};
+                    bar_expect(full + st, 2 * K::COL_BYTES + K::STAT_BYTES);
+                    unsigned char *x1 = tile_x + st * 2 * K::COL_BYTES, *x2 = x1 + K::COL_BYTES;
+                    for (int p = 0; p < K::PANELS; ++p) {
+                        tma_load(x1 + p * BN * K::PITCH, &maps.x1, 64 * p, head, pos, w.b, full + st);
+                        tma_load(x2 + p * BN * K::PITCH, &maps.x2, 64 * p, head, pos, w.b, full + st);
+                    }
+                    if (MODE == kGradKV) bulk_load(tile_stat + st * K::STAT_BYTES, attn_stat(a, w.b, head, pos), K::STAT_BYTES, full + st);
+                    ++it;
+                }
+                pos += BN;
+                if (MODE == kGradKV && pos >= a.Q) {
+                    pos = 0;
+                    ++head;
                 }
             }
-            for (; j < j1; j = next(j + 1), ++it) {
-                const int st = it % STAGES;
-                if (it >= STAGES && !bar_wait(empty + st, (it / STAGES - 1) & 1, dead, a.err)) break;
-                bar_expect(full + st, 2 * K::COL_BYTES);
-                unsigned char *x1 = tile_x + st * 2 * K::COL_BYTES, *x2 = x1 + K::COL_BYTES;
-                for (int p = 0; p < K::PANELS; ++p) {
-                    tma_load(x1 + p * BN * K::PITCH, &maps.x1, 64 * p, head, pos, w.b, full + st);
-                    tma_load(x2 + p * BN * K::PITCH, &maps.x2, 64 * p, head, pos, w.b, full + st);
-                }
+            *total = it;
+            for (int i = it; ok && i < it + NWG; ++i) {    // each group finds an end
+                const int st = i % STAGES;
+                ok = i < STAGES || bar_wait(empty + st, (i / STAGES - 1) & 1, dead, a.err);
+                if (!ok) break;
+                info[st].cls = 0;
+                bar_arrive(full + st);
             }
             if (*dead) {               // copies under way end before the block does
                 uint32_t off = 0u;
@@ -227,58 +255,71 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
         // ------------------------------------------------ MMAs
         if (lane == 0) {
             const int steps = (a.D + 15) / 16;
-            const uint32_t a1 = shared_at(tile_a1), a2 = shared_at(tile_a2), x0 = shared_at(tile_x);
-            constexpr uint32_t id_s = mma_desc<BF16, BN, false>(), id_o = mma_desc<BF16, DP, true>();
+            const uint32_t a1 = desc_low(shared_at(tile_a1), 16), a2 = desc_low(shared_at(tile_a2), 16);
+            const uint32_t along = desc_low(shared_at(tile_x), 16), across = desc_low(shared_at(tile_x), BN * K::PITCH);
+            constexpr uint32_t id_s = mma_desc<BF16, BN, false>(), id_o = mma_desc<BF16, DP, true>(), high = desc_high<K::PITCH>();
             constexpr int per = K::PITCH / 32;      // steps of 16 channels in a panel
             auto scores = [&](int it) {
-                const int g = it % NWG, st = it % STAGES;
-                const uint32_t x1 = x0 + st * 2 * K::COL_BYTES, x2 = x1 + K::COL_BYTES, d = tmem + g * K::GROUP;
-                for (int k = 0; k < steps; ++k) {
-                    const uint32_t ra = k / per * (kTcRows * K::PITCH) + k % per * 32, rx = k / per * (BN * K::PITCH) + k % per * 32;
-                    mma_shared(d, tile_desc<K::PITCH>(a1 + ra, 16), tile_desc<K::PITCH>(x1 + rx, 16), id_s, k > 0);
-                    if (BACK) mma_shared(d + BN, tile_desc<K::PITCH>(a2 + ra, 16), tile_desc<K::PITCH>(x2 + rx, 16), id_s, k > 0);
+                const int g = it % NWG;
+                const uint32_t x1 = along + it % STAGES * desc_step(2 * K::COL_BYTES), x2 = x1 + desc_step(K::COL_BYTES);
+                const uint32_t d = tmem + g * K::GROUP;
+#pragma unroll
+                for (int k = 0; k < DP / 16; ++k) {
+                    if (k >= steps) break;
+                    const uint32_t ra = desc_step(k / per * (kTcRows * K::PITCH) + k % per * 32), rx = desc_step(k / per * (BN * K::PITCH) + k % per * 32);
+                    mma_shared<id_s, high>(d, a1 + ra, x1 + rx, k > 0);
+                    if (BACK) mma_shared<id_s, high>(d + BN, a2 + ra, x2 + rx, k > 0);
                 }
                 mma_commit(s_full + g);
             };
             auto second = [&](int it) {
                 const int g = it % NWG, st = it % STAGES;
-                const uint32_t x1 = x0 + st * 2 * K::COL_BYTES, x2 = x1 + K::COL_BYTES;
+                const uint32_t x1 = across + st * desc_step(2 * K::COL_BYTES), x2 = x1 + desc_step(K::COL_BYTES);
                 const uint32_t s = tmem + g * K::GROUP, acc = tmem + K::ACC + (MODE == kForward ? g * DP : 0);
                 // weights: P, then dS
                 const uint32_t p = s + (K::ALIAS ? 0 : BN * (BACK ? 2 : 1));
                 const uint32_t ds = MODE == kGradQ ? p : K::ALIAS ? s + BN : p + BN / 2;
                 const bool add = MODE == kForward ? it >= NWG : it > 0;
+#pragma unroll
                 for (int k = 0; k < BN / 16; ++k) {
-                    const uint32_t rx = k * 16 * K::PITCH;
-                    if (MODE != kGradQ) mma_tmem(acc, p + 8 * k, tile_desc<K::PITCH>(x2 + rx, BN * K::PITCH), id_o, add || k > 0);
-                    if (BACK) mma_tmem(acc + (MODE == kGradKV ? DP : 0), ds + 8 * k, tile_desc<K::PITCH>(x1 + rx, BN * K::PITCH), id_o, add || k > 0);
+                    const uint32_t rx = desc_step(k * 16 * K::PITCH);
+                    if (MODE != kGradQ) mma_tmem<id_o, high>(acc, p + 8 * k, x2 + rx, add || k > 0);
+                    if (BACK) mma_tmem<id_o, high>(acc + (MODE == kGradKV ? DP : 0), ds + 8 * k, x1 + rx, add || k > 0);
                 }
                 mma_commit(empty + st);
                 mma_commit(done + g);      // last: the block ends after it has arrived
             };
-            int count = 0, it = 0;
-            int64_t j = next(j0);
-            bool ok = j >= j1 || bar_wait(a_full, 0, dead, a.err);
-            for (; ok && j < j1 && count < NWG; j = next(j + 1), ++count) {
+            int count = 0;
+            bool ok = true, more = true;
+            // the next tile's scores, if there is one
+            auto issue = [&]() {
                 ok = bar_wait(full + count % STAGES, (count / STAGES) & 1, dead, a.err);
+                more = ok && info[count % STAGES].cls != 0;
+                if (more && count == 0) more = ok = bar_wait(a_full, 0, dead, a.err);
                 tmem_after_sync();
-                if (ok) scores(count);
-            }
-            for (; ok && it < count; ++it) {
+                if (more) scores(count++);
+            };
+            for (int i = 0; i < NWG && more; ++i) issue();
+            // The next scores of a group go as soon as it has read its last ones (ALIAS: as
+            // soon as these, which became weights, are used).
+            for (int it = 0; ok && it < count; ++it) {
                 const int g = it % NWG, phase = (it / NWG) & 1;
-                ok = bar_wait(ready + g, phase, dead, a.err);
-                tmem_after_sync();
-                if (!ok) break;
-                if (K::ALIAS) second(it);
-                if (j < j1) {
-                    ok = (!K::ALIAS || bar_wait(done + g, phase, dead, a.err)) &&
-                         bar_wait(full + count % STAGES, (count / STAGES) & 1, dead, a.err);
+                if (K::ALIAS) {
+                    ok = bar_wait(ready + g, phase, dead, a.err);
                     tmem_after_sync();
-                    if (ok) scores(count);
-                    j = next(j + 1);
-                    ++count;
+                    if (!ok) break;
+                    second(it);
                 }
-                if (!K::ALIAS) second(it);
+                if (more) {
+                    ok = bar_wait((K::ALIAS ? done : s_free) + g, phase, dead, a.err);
+                    if (!ok) break;
+                    issue();
+                }
+                if (!K::ALIAS) {
+                    ok = ok && bar_wait(ready + g, phase, dead, a.err);
+                    tmem_after_sync();
+                    if (ok) second(it);
+                }
             }
             if (!ok) {                 // MMAs under way end before the block does
                 uint32_t off = 0u;
@@ -297,57 +338,74 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
         const uint32_t at_ds = MODE == kGradQ ? at_p : K::ALIAS ? mine + BN : at_p + BN / 2;
         const uint32_t at_acc = tmem + ((uint32_t)(r & ~31) << 16) + K::ACC + (MODE == kForward ? g * DP : 0);
         const int rpos = w.row_pos(valid ? r : 0), rhead = w.row_head(valid ? r : 0);
-        const int64_t stat = ((int64_t)w.b * a.M + rhead) * a.Q + rpos;
         const float c = a.c;
         float ds_scale = 1.0f;
         if (BACK && a.norm_do) ds_scale = tc_ds_scale(a);
-        constexpr float up = BACK ? TcScale<T>::backward : TcScale<T>::forward;
-        float top = -INFINITY, sum = 0.0f, lse2 = INFINITY, delta = 0.0f;
+        constexpr float up = TcScale<T>::forward;
+        float top = -INFINITY, sum = 0.0f, lse2 = 0.0f, delta = 0.0f;    // backward: negative, as in stat
         if (MODE == kGradQ && valid) {
-            lse2 = attn_lse2(a.lse[stat]) - up;
-            delta = a.delta[stat] * ds_scale;
+            const float *st = attn_stat(a, w.b, rhead, rpos);
+            lse2 = st[0];
+            delta = st[2];
         }
         const uint32_t *words = MODE == kGradKV ? nullptr : attn_word_row<MODE>(a, w.b, rhead, rpos);
 
-        // after a wait that ran out (ok false) the loop goes on without work: the group's
-        // barriers need all its threads
-        int it = 0;                    // over all groups' tiles
+        // after a wait that ran out (ok false) the group's threads go on to their results'
+        // barriers
+        VCLKDEF
+        int own = 0;                   // tiles of this group
         bool ok = true;
-        for (int64_t j = next(j0); j < j1; j = next(j + 1), ++it) {
-            if (it % NWG != g) continue;
-            const int phase = (it / NWG) & 1;
-            if (MODE == kGradKV) words = attn_word_row<MODE>(a, w.b, head, rpos);
+        for (int it = g;; it += NWG, ++own) {
+            const int st = it % STAGES, phase = (it / NWG) & 1;
+            ok = bar_wait_warp(full + st, (it / STAGES) & 1, dead, a.err);
+            if (!ok) break;
+            const TcTile tile = info[st];
+            const int cls = tile.cls;
+            if (!cls) break;
             uint32_t bits[BN / 32];
+            if (cls != 2) {
+                if (MODE == kGradKV) words = attn_word_row<MODE>(a, w.b, tile.head, rpos);
 #pragma unroll
-            for (int i = 0; i < BN / 32; ++i) bits[i] = cls == 2 ? 0xffffffffu : attn_word<MODE>(a, words, pos + 32 * i);
-            float *cs = colstat + (g * 2 + phase) * 2 * BN;
-            if (MODE == kGradKV) {
-                if (r < BN) {
-                    const int at = pos + r;
-                    const int64_t k = ((int64_t)w.b * a.M + head) * a.Q + at;
-                    cs[r] = at < a.Q ? attn_lse2(a.lse[k]) - up : INFINITY;
-                    cs[BN + r] = at < a.Q ? a.delta[k] * ds_scale : 0.0f;
-                }
-                asm volatile("bar.sync %0, 128;" ::"r"(1 + g) : "memory");
+                for (int i = 0; i < BN / 32; ++i) bits[i] = attn_word<MODE>(a, words, tile.pos + 32 * i);
             }
-            ok = ok && bar_wait_warp(s_full + g, phase, dead, a.err);
-            if (!ok) continue;
+            const unsigned char *cs = tile_stat + st * K::STAT_BYTES;
+            VCLK(0);
+            ok = bar_wait_warp(s_full + g, phase, dead, a.err);
+            if (!ok) break;
             tmem_after_sync();
-            if (MODE == kForward && any_valid) {
-                float most = -INFINITY;
+            VCLK(1);
+            // forward: the row's scores, all at once for their maximum
+            uint32_t v[BACK ? 1 : BN];
+            if (!BACK) {
+                if (any_valid) {
 #pragma unroll
-                for (int i = 0; i < BN / 32; ++i) {
-                    uint32_t s[32];
-                    tmem_load32(s, mine + 32 * i);
-                    tmem_wait_load32(s);
-                    if (cls == 2) {
+                    for (int i = 0; i < BN; i += 32) tmem_load32(v + i, mine + i);
+                    tmem_wait_load();
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) most = fmaxf(most, __uint_as_float(s[k]));
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) most = fmaxf(most, (bits[i] >> k) & 1u ? __uint_as_float(s[k]) : -INFINITY);
-                    }
+                    for (int i = 0; i < BN; ++i) asm volatile("" : "+r"(v[i]));
                 }
+                VCLK(2);
+                if (!K::ALIAS) {
+                    tmem_before_sync();
+                    bar_arrive(s_free + g);
+                }
+                if (cls != 2) {
+#pragma unroll
+                    for (int k = 0; k < BN; ++k)
+                        if (!((bits[k / 32] >> (k % 32)) & 1u)) v[k] = 0xff800000u;
+                }
+            }
+            if (MODE == kForward && any_valid) {
+                float most4[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    most4[i] = __uint_as_float(v[i]);
+#pragma unroll
+                    for (int k = i + 4; k < BN; k += 8)
+                        most4[i] = k + 4 < BN ? fmaxf(fmaxf(most4[i], __uint_as_float(v[k])), __uint_as_float(v[k + 4]))
+                                              : fmaxf(most4[i], __uint_as_float(v[k]));
+                }
+                const float most = fmaxf(fmaxf(most4[0], most4[1]), fmaxf(most4[2], most4[3]));
                 // The weights are relative to `top`, which follows the maximum only when that has
                 // grown by more than 2^8: then what was summed is scaled down.
                 const bool grow = top == -INFINITY ? most > -INFINITY : (most - top) * c > 8.0f;
@@ -356,88 +414,101 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
                     if (grow) top = most;
                     sum *= f;
                     if (it >= NWG) {
-                        if (!K::ALIAS) ok = bar_wait_warp(done + g, phase ^ 1, dead, a.err);
+                        if (!K::ALIAS) ok = bar_wait_warp(done + g, phase ^ 1, dead, a.err);   // again below
                         tmem_after_sync();
+#pragma unroll 1
+                        for (int i = 0; i < DP; i += 16) {
+                            uint32_t o[16];
+                            tmem_load16(o, at_acc + i);
+                            tmem_wait_load();
 #pragma unroll
-                        for (int i = 0; i < DP / 32; ++i) {
-                            uint32_t o[32];
-                            tmem_load32(o, at_acc + 32 * i);
-                            tmem_wait_load32(o);
-#pragma unroll
-                            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-                            tmem_store32(at_acc + 32 * i, o);
+                            for (int k = 0; k < 16; ++k) {
+                                asm volatile("" : "+r"(o[k]));
+                                o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                            }
+                            tmem_store16(at_acc + i, o);
                         }
                     }
                 }
             }
+            VCLK(3);
             if (!K::ALIAS && it >= NWG) {      // the weights' columns are free
                 ok = ok && bar_wait_warp(done + g, phase ^ 1, dead, a.err);
                 tmem_after_sync();
             }
-            if (!ok) continue;
-            const float ref = top == -INFINITY ? -up : top * c - up;
+            if (!ok) break;
+            VCLK(4);
+            if (BACK && !K::ALIAS && !any_valid) bar_arrive(s_free + g);
             if (any_valid) {
+                if (MODE == kForward) {
+                    const float ref = top == -INFINITY ? -up : top * c - up;
+                    const float2 c2 = make_float2(c, c), ref2 = make_float2(-ref, -ref);
+                    float2 sums[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
-                for (int i = 0; i < BN / 32; ++i) {
-                    uint32_t s[32], out[16];
-                    tmem_load32(s, mine + 32 * i);
-                    if (MODE == kForward) {
-                        tmem_wait_load32(s);
+                    for (int i = 0; i < BN; i += 32) {
+                        uint32_t out[16];
 #pragma unroll
                         for (int k = 0; k < 32; k += 2) {
-                            float x = fmaf(__uint_as_float(s[k]), c, -ref), y = fmaf(__uint_as_float(s[k + 1]), c, -ref);
-                            if (cls != 2) {
-                                x = (bits[i] >> k) & 1u ? x : -INFINITY;
-                                y = (bits[i] >> (k + 1)) & 1u ? y : -INFINITY;
-                            }
-                            const float p = ex2(x), q = ex2(y);
-                            sum += p + q;
-                            out[k / 2] = pack2<T>(p, q);
+                            const float2 x = __ffma2_rn(make_float2(__uint_as_float(v[i + k]), __uint_as_float(v[i + k + 1])), c2, ref2);
+                            const float2 p = make_float2(ex2(x.x), ex2(x.y));
+                            sums[k / 2 % 2] = __fadd2_rn(sums[k / 2 % 2], p);
+                            out[k / 2] = pack2<T>(p.x, p.y);
                         }
-                        tmem_store16(at_p + 16 * i, out);
-                    } else {
-                        uint32_t dp[32], out2[16];
-                        tmem_load32(dp, mine + BN + 32 * i);
-                        tmem_wait_load32(s);
-                        tmem_wait_load32(dp);
+                        tmem_store16(at_p + i / 2, out);
+                    }
+                    sum += (sums[0].x + sums[1].x) + (sums[0].y + sums[1].y);
+                } else {
+                    const float2 c2 = make_float2(c, c), one = make_float2(ds_scale, ds_scale);
+                    float2 l2 = make_float2(lse2, lse2), e2 = make_float2(delta, delta);
+#pragma unroll
+                    for (int i = 0; i < BN; i += 32) {
+                        uint32_t sc[32], dp[32], out[16], out2[16];
+                        tmem_load32(sc, mine + i);
+                        tmem_load32(dp, mine + BN + i);
+                        tmem_wait_load();
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) asm volatile("" : "+r"(sc[k]), "+r"(dp[k]));
+                        if (!K::ALIAS && i == BN - 32) {
+                            tmem_before_sync();
+                            bar_arrive(s_free + g);
+                        }
+                        if (cls != 2) {    // p, and with it ds unless dP is not finite, will be 0
+#pragma unroll
+                            for (int k = 0; k < 32; ++k)
+                                if (!((bits[i / 32] >> k) & 1u)) sc[k] = 0xff800000u;
+                        }
 #pragma unroll
                         for (int k = 0; k < 32; k += 2) {
-                            float l0 = lse2, l1 = lse2, e0 = delta, e1 = delta;
                             if (MODE == kGradKV) {
-                                const float2 l = *reinterpret_cast<const float2 *>(cs + 32 * i + k);
-                                const float2 e = *reinterpret_cast<const float2 *>(cs + BN + 32 * i + k);
-                                l0 = l.x; l1 = l.y; e0 = e.x; e1 = e.y;
+                                const float4 two = *reinterpret_cast<const float4 *>(cs + 8 * (i + k));
+                                l2 = make_float2(two.x, two.y);
+                                e2 = make_float2(two.z, two.w);
                             }
-                            float p = ex2(fmaf(__uint_as_float(s[k]), c, -l0)), q = ex2(fmaf(__uint_as_float(s[k + 1]), c, -l1));
-                            float t = __uint_as_float(dp[k]), u = __uint_as_float(dp[k + 1]);
-                            t = p * (BF16 ? t - e0 : fmaf(t, ds_scale, -e0));
-                            u = q * (BF16 ? u - e1 : fmaf(u, ds_scale, -e1));
-                            if (cls != 2) {
-                                const bool on0 = (bits[i] >> k) & 1u, on1 = (bits[i] >> (k + 1)) & 1u;
-                                p = on0 ? p : 0.0f;
-                                q = on1 ? q : 0.0f;
-                                t = on0 ? t : 0.0f;
-                                u = on1 ? u : 0.0f;
-                            }
-                            out[k / 2] = pack2<T>(p, q);
-                            out2[k / 2] = pack2<T>(t, u);
+                            const float2 x = __ffma2_rn(make_float2(__uint_as_float(sc[k]), __uint_as_float(sc[k + 1])), c2, l2);
+                            const float2 p = make_float2(ex2(x.x), ex2(x.y));
+                            float2 d = __fmul2_rn(p, __fadd2_rn(make_float2(__uint_as_float(dp[k]), __uint_as_float(dp[k + 1])), e2));
+                            if (!BF16) d = __fmul2_rn(d, one);
+                            out[k / 2] = pack2<T>(p.x, p.y);
+                            out2[k / 2] = pack2<T>(d.x, d.y);
                         }
-                        if (MODE == kGradKV) tmem_store16(at_p + 16 * i, out);
-                        tmem_store16(at_ds + 16 * i, out2);
+                        if (MODE == kGradKV) tmem_store16(at_p + i / 2, out);
+                        tmem_store16(at_ds + i / 2, out2);
                     }
                 }
+                VCLK(5);
                 tmem_wait_store();
             }
             tmem_before_sync();
             bar_arrive(ready + g);
+            VCLK(6);
         }
 
+        VCLKPRINT
         // ------------------------------------------------ results
-        const int count = it;          // column tiles of this block; this group's last is its number it
-        const int own = (count - g + NWG - 1) / NWG;       // tiles of this group
         if (ok && own > 0) ok = bar_wait_warp(done + g, (own - 1) & 1, dead, a.err);
         tmem_after_sync();
-        if (NWG > 1) {
+        const int count = *total;      // column tiles of the block
+        if (NWG > 1) {                 // the other groups' are done too
             tmem_before_sync();
             asm volatile("bar.sync 7, %0;" ::"n"(NWG * 128) : "memory");
             tmem_after_sync();
@@ -449,7 +520,7 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
             const uint32_t acc0 = tmem + ((uint32_t)(r & ~31) << 16) + K::ACC;
             const int64_t row = MODE == kGradKV ? ((int64_t)w.b * a.S + rpos) * a.N + rhead : ((int64_t)w.b * a.Q + rpos) * a.M + rhead;
             const float ref = top == -INFINITY ? -up : top * c - up;
-            const float down = BACK ? ex2(-up) : 1.0f;     // of P; of dS also 1 / ds_scale
+            const float down = BACK ? ex2(-TcScale<T>::backward) : 1.0f;   // of P; of dS also 1 / ds_scale
             const float down_ds = down / ds_scale;
             if (MODE == kForward && valid) {
                 if (a.splits > 1) {
@@ -457,7 +528,7 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
                     ml[0] = sum == 0.0f ? -INFINITY : ref;
                     ml[1] = sum;
                 } else if (a.lse) {
-                    a.lse[stat] = sum == 0.0f ? -INFINITY : (ref + log2f(sum)) * kLn2;
+                    a.lse[((int64_t)w.b * a.M + rhead) * a.Q + rpos] = sum == 0.0f ? -INFINITY : (ref + log2f(sum)) * kLn2;
                 }
             }
             const float over = sum == 0.0f ? 0.0f : 1.0f / sum;

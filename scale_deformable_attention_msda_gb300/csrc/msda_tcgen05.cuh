@@ -45,12 +45,12 @@ __device__ __forceinline__ bool bar_try(uint64_t *bar, uint32_t parity) {
 __device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity, volatile uint32_t *dead, unsigned *err) {
     if (bar_try(bar, parity)) return true;
     unsigned long long start = 0;
-    for (uint32_t i = 0;; ++i) {
+    for (uint32_t i = 1;; ++i) {
         if (bar_try(bar, parity)) return true;
-        if (i & 15u) continue;
+        if (i & 63u) continue;         // the timer is slow to read
         if (*dead) return false;
         const unsigned long long now = nanoseconds();
-        if (i == 0) start = now;
+        if (start == 0) start = now;
         else if (now - start > kWaitNs) break;
     }
     *dead = 1u;
@@ -67,6 +67,12 @@ __device__ __forceinline__ bool bar_wait_warp(uint64_t *bar, uint32_t parity, vo
 __device__ __forceinline__ void tma_load(void *to, const CUtensorMap *map, int x, int y, int z, int w, uint64_t *bar) {
     asm volatile("cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
                  ::"r"(shared_at(to)), "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(shared_at(bar))
+                 : "memory");
+}
+// `bytes`, a multiple of 16, from and to 16-byte boundaries.
+__device__ __forceinline__ void bulk_load(void *to, const void *from, uint32_t bytes, uint64_t *bar) {
+    asm volatile("cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                 ::"r"(shared_at(to)), "l"(from), "r"(bytes), "r"(shared_at(bar))
                  : "memory");
 }
 __device__ __forceinline__ void tma_prefetch_map(const CUtensorMap *map) {
@@ -97,7 +103,7 @@ __device__ __forceinline__ void tmem_wait_load32(uint32_t (&v)[32]) {
 }
 
 // 32 columns of the calling warp's 32 lanes: one lane's row to each thread.
-__device__ __forceinline__ void tmem_load32(uint32_t (&v)[32], uint32_t at) {
+__device__ __forceinline__ void tmem_load32(uint32_t *v, uint32_t at) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
         "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
@@ -105,6 +111,13 @@ __device__ __forceinline__ void tmem_load32(uint32_t (&v)[32], uint32_t at) {
           "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]),
           "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]),
           "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+        : "r"(at));
+}
+__device__ __forceinline__ void tmem_load16(uint32_t *v, uint32_t at) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
         : "r"(at));
 }
 __device__ __forceinline__ void tmem_store32(uint32_t at, const uint32_t (&v)[32]) {
@@ -134,12 +147,16 @@ __device__ __forceinline__ void tmem_store16(uint32_t at, const uint32_t (&v)[16
 // descriptor's stride is that of a group of 8 rows. Read across them (MN-major:
 // the contraction runs over the rows), it is the same stride between 8 steps of
 // the contraction, and the leading stride is that of a panel.
-template <int PITCH>
-__device__ __forceinline__ uint64_t tile_desc(uint32_t at, uint32_t panel_bytes) {
+//
+// The descriptor's two words: the low one has the address and the leading stride, and
+// a step along the tile adds to it (offset / 16); the high one is constant.
+__device__ __forceinline__ constexpr uint32_t desc_step(uint32_t bytes) { return bytes >> 4; }
+__device__ __forceinline__ uint32_t desc_low(uint32_t at, uint32_t panel_bytes) {
+    return ((at & 0x3ffffu) >> 4) | ((panel_bytes >> 4) << 16);
+}
+template <int PITCH> __device__ __forceinline__ constexpr uint32_t desc_high() {
     static_assert(PITCH == 64 || PITCH == 128, "the tile's swizzle");
-    constexpr uint64_t layout = PITCH == 128 ? 2 : 4;
-    return (uint64_t)((at & 0x3ffffu) >> 4) | ((uint64_t)(panel_bytes >> 4) << 16) | ((uint64_t)(8 * PITCH >> 4) << 32) |
-           ((uint64_t)1 << 46) | (layout << 61);
+    return (uint32_t)(8 * PITCH >> 4) | (1u << 14) | ((PITCH == 128 ? 2u : 4u) << 29);
 }
 // fp32 accumulators of 16-bit operands (bf16, or fp16), 128 rows by N columns.
 template <bool BF16, int N, bool B_ACROSS>
@@ -147,16 +164,21 @@ __device__ __forceinline__ constexpr uint32_t mma_desc() {
     return (1u << 4) | ((BF16 ? 1u : 0u) << 7) | ((BF16 ? 1u : 0u) << 10) | ((B_ACROSS ? 1u : 0u) << 16) |
            ((uint32_t)(N / 8) << 17) | ((uint32_t)(128 / 16) << 24);
 }
-__device__ __forceinline__ void mma_shared(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-                 ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+// d (+)= a b' of descriptors with the same high word; idesc and high are constants.
+template <uint32_t IDESC, uint32_t HIGH>
+__device__ __forceinline__ void mma_shared(uint32_t d, uint32_t a, uint32_t b, bool add) {
+    asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.u32 p, %3, 0;\n\t"
+                 "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, p;\n\t}"
+                 ::"r"(d), "r"(a), "r"(b), "r"((uint32_t)add), "n"(IDESC), "n"(HIGH)
                  : "memory");
 }
-__device__ __forceinline__ void mma_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-                 ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+template <uint32_t IDESC, uint32_t HIGH>
+__device__ __forceinline__ void mma_tmem(uint32_t d, uint32_t a, uint32_t b, bool add) {
+    asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 db;\n\tsetp.ne.u32 p, %3, 0;\n\t"
+                 "mov.b64 db, {%2, %5};\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n\t}"
+                 ::"r"(d), "r"(a), "r"(b), "r"((uint32_t)add), "n"(IDESC), "n"(HIGH)
                  : "memory");
 }
 // Arrives at `bar` when every MMA issued before has finished.
