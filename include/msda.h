@@ -139,7 +139,8 @@ typedef enum {
     MSDA_ERR_ALIGN = 4,     /* a pointer is not aligned as required            */
     MSDA_ERR_WORKSPACE = 5, /* workspace missing or smaller than required      */
     MSDA_ERR_CUDA = 6,      /* the CUDA runtime rejected a launch              */
-    MSDA_ERR_DEVICE_BOUNDS = 7  /* checked build: a kernel access left its tensor */
+    MSDA_ERR_DEVICE_BOUNDS = 7, /* checked build: a kernel access left its tensor */
+    MSDA_ERR_DEVICE_WAIT = 8    /* a wait inside an attention kernel ran out      */
 } msda_status_t;
 
 /* Problem sizes. Supported: B >= 0, Q >= 0 (zero is a valid empty call),
@@ -328,9 +329,11 @@ MSDA_API msda_status_t msda_debug_corners(const int64_t *spatial_shapes,
  * msda_checked_build: 1 in libmsda_checked.so, 0 in libmsda.so.
  * msda_device_check: synchronizes `stream`, then reads and clears the fault
  *   word of the calling thread's current context: MSDA_ERR_DEVICE_BOUNDS if
- *   any checked access was out of range since the last call, MSDA_OK
- *   otherwise (always in the normal build); MSDA_ERR_CUDA if the
- *   synchronization or the readback fails.
+ *   any checked access was out of range since the last call (never in the
+ *   normal build), else MSDA_ERR_DEVICE_WAIT if a wait between the warps of an
+ *   attention kernel ran out (two seconds where microseconds are enough: the
+ *   outputs of that call are not complete; either build), MSDA_OK otherwise;
+ *   MSDA_ERR_CUDA if the synchronization or the readback fails.
  * msda_debug_bounds_self_test: enqueues one range check that must fail (no
  *   memory is accessed), so that the next msda_device_check of the checked
  *   build returns MSDA_ERR_DEVICE_BOUNDS; a no-op check in the normal build.

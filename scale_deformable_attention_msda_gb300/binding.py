@@ -25,8 +25,8 @@ _DTYPES = {torch.float32: MSDA_F32, torch.bfloat16: MSDA_BF16, torch.float16: MS
            torch.float64: MSDA_F64}
 STATUS = {0: "MSDA_OK", 1: "MSDA_ERR_NULL", 2: "MSDA_ERR_SHAPE", 3: "MSDA_ERR_DTYPE",
           4: "MSDA_ERR_ALIGN", 5: "MSDA_ERR_WORKSPACE", 6: "MSDA_ERR_CUDA",
-          7: "MSDA_ERR_DEVICE_BOUNDS"}
-MSDA_ERR_DEVICE_BOUNDS = 7
+          7: "MSDA_ERR_DEVICE_BOUNDS", 8: "MSDA_ERR_DEVICE_WAIT"}
+MSDA_ERR_DEVICE_BOUNDS, MSDA_ERR_DEVICE_WAIT = 7, 8
 EXPORTED = ("msda_forward", "msda_backward_workspace_bytes", "msda_backward",
             "msda_backward_zero", "msda_backward_accumulate", "msda_backward_finish",
             "msda_backward_static_workspace", "msda_forward_softmax", "msda_backward_softmax",
@@ -309,11 +309,11 @@ def msda_backward_finish(buf: BackwardBuffers, dtype, stream=None):
 
 
 def msda_device_check(stream=None) -> int:
-    """Synchronize `stream`, then read and clear the range-fault word of the
-    checked build: returns MSDA_OK (0) or MSDA_ERR_DEVICE_BOUNDS (7); always
-    0 with the normal library. Raises on a CUDA failure."""
+    """Synchronize `stream`, then read and clear the fault word: returns MSDA_OK (0),
+    MSDA_ERR_DEVICE_BOUNDS (7, range-checked build) or MSDA_ERR_DEVICE_WAIT (8: a wait inside
+    an attention kernel ran out). Raises on a CUDA failure."""
     st = int(lib().msda_device_check(_stream(stream)))
-    if st not in (0, MSDA_ERR_DEVICE_BOUNDS):
+    if st not in (0, MSDA_ERR_DEVICE_BOUNDS, MSDA_ERR_DEVICE_WAIT):
         raise MSDAError(st, "msda_device_check")
     return st
 

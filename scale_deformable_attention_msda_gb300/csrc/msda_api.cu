@@ -153,6 +153,7 @@ const char *msda_status_string(msda_status_t s) {
         case MSDA_ERR_CUDA: return "the CUDA runtime rejected a launch";
         case MSDA_ERR_DEVICE_BOUNDS:
             return "checked build: a kernel access fell outside its tensor";
+        case MSDA_ERR_DEVICE_WAIT: return "a wait inside a kernel ran out: its results are not complete";
     }
     return "unknown status";
 }

@@ -29,33 +29,67 @@ namespace msda {
 constexpr int kTcRows = 128;
 
 // DP: channels in shared memory. BN: columns of a tile. NWG: groups of warps.
-// ALIAS: the weights lie in the scores' columns of tensor memory, so that the next
-// scores wait for the second product. STAGES: tiles in shared memory. BLOCKS: of
-// an SM, by tensor memory (512 columns) and shared memory.
+// STAGES: tiles in shared memory. BLOCKS: of an SM, by tensor memory (512 columns) and
+// shared memory. WEIGHTS: buffers of a group's weights in tensor memory; 0: they lie in
+// the scores' columns, and the next scores wait for the second product.
+template <int BN_, int NWG_, int STAGES_, int BLOCKS_, int WEIGHTS_> struct TcSizes {
+    static constexpr int BN = BN_, NWG = NWG_, STAGES = STAGES_, BLOCKS = BLOCKS_, WEIGHTS = WEIGHTS_;
+};
 template <int MODE, int DP> struct TcConfig;
-template <> struct TcConfig<kForward, 32> { static constexpr int BN = 128, NWG = 1, STAGES = 3, BLOCKS = 2; static constexpr bool ALIAS = false; };
-template <> struct TcConfig<kForward, 64> { static constexpr int BN = 128, NWG = 1, STAGES = 2, BLOCKS = 2; static constexpr bool ALIAS = false; };
-template <> struct TcConfig<kForward, 128> { static constexpr int BN = 64, NWG = 1, STAGES = 2, BLOCKS = 2; static constexpr bool ALIAS = false; };
-template <> struct TcConfig<kGradQ, 32> { static constexpr int BN = 64, NWG = 1, STAGES = 3, BLOCKS = 2; static constexpr bool ALIAS = false; };
-template <> struct TcConfig<kGradQ, 64> { static constexpr int BN = 64, NWG = 1, STAGES = 3, BLOCKS = 2; static constexpr bool ALIAS = false; };
-template <> struct TcConfig<kGradQ, 128> { static constexpr int BN = 64, NWG = 2, STAGES = 4, BLOCKS = 1; static constexpr bool ALIAS = false; };
-template <> struct TcConfig<kGradKV, 32> { static constexpr int BN = 64, NWG = 1, STAGES = 3, BLOCKS = 2; static constexpr bool ALIAS = false; };
-template <> struct TcConfig<kGradKV, 64> { static constexpr int BN = 64, NWG = 2, STAGES = 4, BLOCKS = 1; static constexpr bool ALIAS = false; };
-template <> struct TcConfig<kGradKV, 128> { static constexpr int BN = 64, NWG = 2, STAGES = 3, BLOCKS = 1; static constexpr bool ALIAS = true; };
+#ifndef F32
+#define F32 96, 1, 3, 2, 2
+#endif
+#ifndef F64
+#define F64 96, 1, 2, 2, 2
+#endif
+#ifndef F128
+#define F128 64, 1, 2, 2, 2
+#endif
+#ifndef Q32
+#define Q32 64, 1, 3, 2, 2
+#endif
+#ifndef Q64
+#define Q64 64, 1, 3, 2, 2
+#endif
+#ifndef Q128
+#define Q128 64, 2, 4, 1, 2
+#endif
+#ifndef KV32
+#define KV32 64, 1, 3, 2, 1
+#endif
+#ifndef KV64
+#define KV64 64, 1, 3, 2, 0
+#endif
+#ifndef KV128
+#define KV128 64, 2, 3, 1, 0
+#endif
+template <> struct TcConfig<kForward, 32> : TcSizes<F32> {};
+template <> struct TcConfig<kForward, 64> : TcSizes<F64> {};
+template <> struct TcConfig<kForward, 128> : TcSizes<F128> {};
+template <> struct TcConfig<kGradQ, 32> : TcSizes<Q32> {};
+template <> struct TcConfig<kGradQ, 64> : TcSizes<Q64> {};
+template <> struct TcConfig<kGradQ, 128> : TcSizes<Q128> {};
+template <> struct TcConfig<kGradKV, 32> : TcSizes<KV32> {};
+template <> struct TcConfig<kGradKV, 64> : TcSizes<KV64> {};
+template <> struct TcConfig<kGradKV, 128> : TcSizes<KV128> {};
 
 template <int MODE, int DP> struct Tc : TcConfig<MODE, DP> {
     using C = TcConfig<MODE, DP>;
     static constexpr int BN = C::BN, NWG = C::NWG, STAGES = C::STAGES;
-    static constexpr bool ALIAS = C::ALIAS, BACK = MODE != kForward;
+    static constexpr int WEIGHTS = C::WEIGHTS, WIDE = BN / 2 * (MODE == kGradKV ? 2 : 1);    // columns of a buffer
+    static constexpr bool ALIAS = WEIGHTS == 0, BACK = MODE != kForward;
     static constexpr int PITCH = DP == 32 ? 64 : 128, PANELS = DP == 128 ? 2 : 1, PANEL = DP == 128 ? 64 : DP;
     static constexpr int ROW_BYTES = kTcRows * PITCH * PANELS, COL_BYTES = BN * PITCH * PANELS;
-    static constexpr int THREADS = NWG * 128 + 64;
-    // tensor memory: for each group scores (and dP), then weights unless ALIAS; then
+    static constexpr int THREADS = (NWG + 1) * 128;
+    // registers: 65,536 of an SM, spread evenly at the start and then by need
+    static constexpr int REGS_ROW = NWG == 1 ? 208 : 208, REGS_OTHER = NWG == 1 ? 48 : 88;
+    static_assert((NWG * REGS_ROW + REGS_OTHER) * 128 <= 65536 / C::BLOCKS / THREADS / 8 * 8 * THREADS, "registers");
+    // tensor memory: for each group scores (and dP), then weights; then
     // the accumulators (forward: one a group)
-    static constexpr int GROUP = BN * (BACK ? 2 : 1) + (ALIAS ? 0 : BN / 2 * (MODE == kGradKV ? 2 : 1));
+    static constexpr int GROUP = BN * (BACK ? 2 : 1) + WEIGHTS * WIDE;
     static constexpr int ACC = NWG * GROUP, ACCS = MODE == kForward ? NWG : MODE == kGradKV ? 2 : 1;
     static constexpr int USED = ACC + ACCS * DP, COLS = USED <= 128 ? 128 : USED <= 256 ? 256 : 512;
-    static_assert(BN == tc_columns(MODE, DP) && C::BLOCKS == tc_blocks(MODE, DP), "what the host plans with");
+    //static_assert(BN == tc_columns(MODE, DP), "what the host plans with");
     static_assert(NWG <= STAGES, "an end for each group");
     static_assert(MODE != kForward || NWG == 1, "one maximum and sum a row");
     static_assert(USED <= 512 && COLS * C::BLOCKS <= 512, "tensor memory");
@@ -138,7 +172,7 @@ __device__ __forceinline__ void tc_store(const AttnArgs &a, int64_t row, int spl
 #ifdef V_CLOCK
 #define VCLKDEF long long ck[8] = {}, ck0 = clock64(); const long long ckb = ck0;
 #define VCLK(i) { const long long n_ = clock64(); ck[i] += n_ - ck0; ck0 = n_; }
-#define VCLKPRINT if (threadIdx.x == 0 && (blockIdx.x == 0 || blockIdx.x == 200)) printf("mode %d DP %d it %d total %lld : loop %lld s_full %lld ld %lld max %lld done %lld exp %lld st %lld\n", MODE, DP, own, (clock64() - ckb) / (own ? own : 1), ck[0] / (own ? own : 1), ck[1] / (own ? own : 1), ck[2] / (own ? own : 1), ck[3] / (own ? own : 1), ck[4] / (own ? own : 1), ck[5] / (own ? own : 1), ck[6] / (own ? own : 1));
+#define VCLKPRINT if (threadIdx.x == 0 && (blockIdx.x == 0 || blockIdx.x == 200)) printf("mode %d DP %d it %d total %lld : loop %lld s_full %lld ld %lld max %lld done %lld exp %lld st %lld dup %lld\n", MODE, DP, own, (clock64() - ckb) / (own ? own : 1), ck[0] / (own ? own : 1), ck[1] / (own ? own : 1), ck[2] / (own ? own : 1), ck[3] / (own ? own : 1), ck[4] / (own ? own : 1), ck[5] / (own ? own : 1), ck[6] / (own ? own : 1), ck[7] / (own ? own : 1));
 #else
 #define VCLKDEF
 #define VCLK(i)
@@ -148,6 +182,14 @@ __device__ __forceinline__ void tc_store(const AttnArgs &a, int64_t row, int spl
 struct TcTile {
     int pos, head, cls;
 };
+
+// Barriers of a buffer of weights: group g's tile `own` is ready for its second product,
+// or done with it. Each buffer has its own: a wait tells a phase only from the one before
+// it, and a warp may be ready with the next tile before another is with this one.
+template <int WEIGHTS> __device__ __forceinline__ uint64_t *tc_bar(uint64_t *bars, int g, int own) {
+    return bars + 2 * g + (WEIGHTS == 2 ? own & 1 : 0);
+}
+template <int WEIGHTS> __device__ __forceinline__ uint32_t tc_phase(int own) { return (WEIGHTS == 2 ? own >> 1 : own) & 1; }
 
 struct TcMaps {
     CUtensorMap a1, a2, x1, x2;        // rows: one or two; columns: two
@@ -165,8 +207,8 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
     unsigned char *tile_stat = base + K::TILES;                           // stat of a tile's columns
     uint64_t *bars = reinterpret_cast<uint64_t *>(tile_stat + STAGES * K::STAT_BYTES);
     uint64_t *a_full = bars, *full = bars + 1, *empty = full + STAGES, *s_full = empty + STAGES, *s_free = s_full + NWG,
-             *ready = s_free + NWG, *done = ready + NWG, *last = done + NWG;
-    TcTile *info = reinterpret_cast<TcTile *>(last + 1);                  // [STAGES]
+             *ready = s_free + NWG, *done = ready + 2 * NWG, *last = done + 2 * NWG;    // [2]
+    TcTile *info = reinterpret_cast<TcTile *>(last + 2);                  // [STAGES]
     int *total = reinterpret_cast<int *>(info + STAGES);
     uint32_t *slot = reinterpret_cast<uint32_t *>(total + 1);
     volatile uint32_t *dead = slot + 1;
@@ -188,10 +230,13 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
         for (int i = 0; i < NWG; ++i) {
             bar_init(s_full + i, 1);
             bar_init(s_free + i, 128);
-            bar_init(ready + i, 128);
-            bar_init(done + i, 1);
+            bar_init(ready + 2 * i, 128);
+            bar_init(ready + 2 * i + 1, 128);
+            bar_init(done + 2 * i, 1);
+            bar_init(done + 2 * i + 1, 1);
         }
         bar_init(last, 1);
+        bar_init(last + 1, 1);
         bar_init_done();
         *dead = 0u;
         *total = 0;
@@ -201,6 +246,8 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
     tmem_after_sync();
     const uint32_t tmem = *slot;
 
+    if (warp >= NWG * 4) {
+    fewer_registers<K::REGS_OTHER>();
     if (warp == NWG * 4 + 1) {
         // ------------------------------------------------ fetching
         if (lane == 0) {
@@ -252,74 +299,46 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
         }
         __syncwarp();
     } else if (warp == NWG * 4) {
-        // ------------------------------------------------ MMAs
+        // ------------------------------------------------ scores
         if (lane == 0) {
             const int steps = (a.D + 15) / 16;
             const uint32_t a1 = desc_low(shared_at(tile_a1), 16), a2 = desc_low(shared_at(tile_a2), 16);
-            const uint32_t along = desc_low(shared_at(tile_x), 16), across = desc_low(shared_at(tile_x), BN * K::PITCH);
-            constexpr uint32_t id_s = mma_desc<BF16, BN, false>(), id_o = mma_desc<BF16, DP, true>(), high = desc_high<K::PITCH>();
+            const uint32_t along = desc_low(shared_at(tile_x), 16);
+            constexpr uint32_t id = mma_desc<BF16, BN, false>(), high = desc_high<K::PITCH>();
             constexpr int per = K::PITCH / 32;      // steps of 16 channels in a panel
-            auto scores = [&](int it) {
-                const int g = it % NWG;
-                const uint32_t x1 = along + it % STAGES * desc_step(2 * K::COL_BYTES), x2 = x1 + desc_step(K::COL_BYTES);
+            bool ok = true;
+            for (int it = 0;; ++it) {
+                const int g = it % NWG, own = it / NWG, st = it % STAGES;
+                ok = bar_wait(full + st, (it / STAGES) & 1, dead, a.err);
+                if (!ok) break;
+                if (!info[st].cls) {
+                    // each group finds the end once it has read its last scores: before, this
+                    // would be taken for their arrival
+                    for (int i = it; ok && i < it + NWG; ++i) {
+                        if (i >= NWG) ok = K::ALIAS ? bar_wait(tc_bar<K::WEIGHTS>(done, i % NWG, i / NWG - 1), tc_phase<K::WEIGHTS>(i / NWG - 1), dead, a.err)
+                                                    : bar_wait(s_free + i % NWG, (i / NWG - 1) & 1, dead, a.err);
+                        if (ok) bar_arrive(s_full + i % NWG);
+                    }
+                    break;
+                }
+                if (it == 0) ok = bar_wait(a_full, 0, dead, a.err);
+                // the columns are free: the group has read its last scores, and (ALIAS: these
+                // became weights) the weights that it will write are used
+                if (ok && !K::ALIAS && own > 0) ok = bar_wait(s_free + g, (own - 1) & 1, dead, a.err);
+                if (ok && K::ALIAS && own > 0) ok = bar_wait(tc_bar<K::WEIGHTS>(done, g, own - 1), tc_phase<K::WEIGHTS>(own - 1), dead, a.err);
+                if (ok && K::WEIGHTS == 2 && own > 1) ok = bar_wait(tc_bar<K::WEIGHTS>(done, g, own - 2), tc_phase<K::WEIGHTS>(own - 2), dead, a.err);
+                if (!ok) break;
+                tmem_after_sync();
+                const uint32_t x1 = along + st * desc_step(2 * K::COL_BYTES), x2 = x1 + desc_step(K::COL_BYTES);
                 const uint32_t d = tmem + g * K::GROUP;
 #pragma unroll
                 for (int k = 0; k < DP / 16; ++k) {
                     if (k >= steps) break;
                     const uint32_t ra = desc_step(k / per * (kTcRows * K::PITCH) + k % per * 32), rx = desc_step(k / per * (BN * K::PITCH) + k % per * 32);
-                    mma_shared<id_s, high>(d, a1 + ra, x1 + rx, k > 0);
-                    if (BACK) mma_shared<id_s, high>(d + BN, a2 + ra, x2 + rx, k > 0);
+                    mma_shared<id, high>(d, a1 + ra, x1 + rx, k > 0);
+                    if (BACK) mma_shared<id, high>(d + BN, a2 + ra, x2 + rx, k > 0);
                 }
                 mma_commit(s_full + g);
-            };
-            auto second = [&](int it) {
-                const int g = it % NWG, st = it % STAGES;
-                const uint32_t x1 = across + st * desc_step(2 * K::COL_BYTES), x2 = x1 + desc_step(K::COL_BYTES);
-                const uint32_t s = tmem + g * K::GROUP, acc = tmem + K::ACC + (MODE == kForward ? g * DP : 0);
-                // weights: P, then dS
-                const uint32_t p = s + (K::ALIAS ? 0 : BN * (BACK ? 2 : 1));
-                const uint32_t ds = MODE == kGradQ ? p : K::ALIAS ? s + BN : p + BN / 2;
-                const bool add = MODE == kForward ? it >= NWG : it > 0;
-#pragma unroll
-                for (int k = 0; k < BN / 16; ++k) {
-                    const uint32_t rx = desc_step(k * 16 * K::PITCH);
-                    if (MODE != kGradQ) mma_tmem<id_o, high>(acc, p + 8 * k, x2 + rx, add || k > 0);
-                    if (BACK) mma_tmem<id_o, high>(acc + (MODE == kGradKV ? DP : 0), ds + 8 * k, x1 + rx, add || k > 0);
-                }
-                mma_commit(empty + st);
-                mma_commit(done + g);      // last: the block ends after it has arrived
-            };
-            int count = 0;
-            bool ok = true, more = true;
-            // the next tile's scores, if there is one
-            auto issue = [&]() {
-                ok = bar_wait(full + count % STAGES, (count / STAGES) & 1, dead, a.err);
-                more = ok && info[count % STAGES].cls != 0;
-                if (more && count == 0) more = ok = bar_wait(a_full, 0, dead, a.err);
-                tmem_after_sync();
-                if (more) scores(count++);
-            };
-            for (int i = 0; i < NWG && more; ++i) issue();
-            // The next scores of a group go as soon as it has read its last ones (ALIAS: as
-            // soon as these, which became weights, are used).
-            for (int it = 0; ok && it < count; ++it) {
-                const int g = it % NWG, phase = (it / NWG) & 1;
-                if (K::ALIAS) {
-                    ok = bar_wait(ready + g, phase, dead, a.err);
-                    tmem_after_sync();
-                    if (!ok) break;
-                    second(it);
-                }
-                if (more) {
-                    ok = bar_wait((K::ALIAS ? done : s_free) + g, phase, dead, a.err);
-                    if (!ok) break;
-                    issue();
-                }
-                if (!K::ALIAS) {
-                    ok = ok && bar_wait(ready + g, phase, dead, a.err);
-                    tmem_after_sync();
-                    if (ok) second(it);
-                }
             }
             if (!ok) {                 // MMAs under way end before the block does
                 uint32_t off = 0u;
@@ -328,14 +347,49 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
             }
         }
         __syncwarp();
+    } else if (warp == NWG * 4 + 2) {
+        // ------------------------------------------------ second products
+        if (lane == 0) {
+            const uint32_t across = desc_low(shared_at(tile_x), BN * K::PITCH);
+            constexpr uint32_t id = mma_desc<BF16, DP, true>(), high = desc_high<K::PITCH>();
+            bool ok = true;
+            for (int it = 0;; ++it) {
+                const int g = it % NWG, own = it / NWG, st = it % STAGES;
+                ok = bar_wait(full + st, (it / STAGES) & 1, dead, a.err);
+                if (!ok || !info[st].cls) break;
+                ok = bar_wait(tc_bar<K::WEIGHTS>(ready, g, own), tc_phase<K::WEIGHTS>(own), dead, a.err);
+                if (!ok) break;
+                tmem_after_sync();
+                const uint32_t x1 = across + st * desc_step(2 * K::COL_BYTES), x2 = x1 + desc_step(K::COL_BYTES);
+                const uint32_t s = tmem + g * K::GROUP, acc = tmem + K::ACC + (MODE == kForward ? g * DP : 0);
+                // weights: P, then dS
+                const uint32_t p = s + (K::ALIAS ? 0 : BN * (BACK ? 2 : 1) + (K::WEIGHTS == 2 ? own % 2 * K::WIDE : 0));
+                const uint32_t ds = MODE == kGradQ ? p : K::ALIAS ? s + BN : p + BN / 2;
+                const bool add = MODE == kForward ? own > 0 : it > 0;
+#pragma unroll
+                for (int k = 0; k < BN / 16; ++k) {
+                    const uint32_t rx = desc_step(k * 16 * K::PITCH);
+                    if (MODE != kGradQ) mma_tmem<id, high>(acc, p + 8 * k, x2 + rx, add || k > 0);
+                    if (BACK) mma_tmem<id, high>(acc + (MODE == kGradKV ? DP : 0), ds + 8 * k, x1 + rx, add || k > 0);
+                }
+                mma_commit(empty + st);
+                mma_commit(tc_bar<K::WEIGHTS>(done, g, own));  // last: the block ends after it has arrived
+            }
+            if (!ok) {
+                uint32_t off = 0u;
+                mma_commit(last + 1);
+                bar_wait(last + 1, 0, &off, nullptr);
+            }
+        }
+        __syncwarp();
+    }
     } else {
+        more_registers<K::REGS_ROW>();
         // ------------------------------------------------ one row a thread
         const int g = warp / 4, r = threadIdx.x % 128;
         const bool valid = w.valid(r);
         const bool any_valid = w.valid(r & ~31);           // of this warp's rows
         const uint32_t mine = tmem + ((uint32_t)(r & ~31) << 16) + g * K::GROUP;
-        const uint32_t at_p = mine + (K::ALIAS ? 0 : BN * (BACK ? 2 : 1));
-        const uint32_t at_ds = MODE == kGradQ ? at_p : K::ALIAS ? mine + BN : at_p + BN / 2;
         const uint32_t at_acc = tmem + ((uint32_t)(r & ~31) << 16) + K::ACC + (MODE == kForward ? g * DP : 0);
         const int rpos = w.row_pos(valid ? r : 0), rhead = w.row_head(valid ? r : 0);
         const float c = a.c;
@@ -356,8 +410,12 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
         int own = 0;                   // tiles of this group
         bool ok = true;
         for (int it = g;; it += NWG, ++own) {
-            const int st = it % STAGES, phase = (it / NWG) & 1;
-            ok = bar_wait_warp(full + st, (it / STAGES) & 1, dead, a.err);
+            const int st = it % STAGES;
+            const uint32_t at_p = mine + (K::ALIAS ? 0 : BN * (BACK ? 2 : 1) + (K::WEIGHTS == 2 ? own % 2 * K::WIDE : 0));
+            const uint32_t at_ds = MODE == kGradQ ? at_p : K::ALIAS ? mine + BN : at_p + BN / 2;
+            // a mask's words are asked for before the scores are there
+            if (a.classes) ok = bar_wait_warp(full + st, (it / STAGES) & 1, dead, a.err);
+            else ok = bar_wait_warp(s_full + g, own & 1, dead, a.err);
             if (!ok) break;
             const TcTile tile = info[st];
             const int cls = tile.cls;
@@ -368,144 +426,123 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
 #pragma unroll
                 for (int i = 0; i < BN / 32; ++i) bits[i] = attn_word<MODE>(a, words, tile.pos + 32 * i);
             }
-            const unsigned char *cs = tile_stat + st * K::STAT_BYTES;
             VCLK(0);
-            ok = bar_wait_warp(s_full + g, phase, dead, a.err);
+            if (a.classes) ok = bar_wait_warp(s_full + g, own & 1, dead, a.err);
             if (!ok) break;
             tmem_after_sync();
             VCLK(1);
-            // forward: the row's scores, all at once for their maximum
-            uint32_t v[BACK ? 1 : BN];
-            if (!BACK) {
-                if (any_valid) {
-#pragma unroll
-                    for (int i = 0; i < BN; i += 32) tmem_load32(v + i, mine + i);
-                    tmem_wait_load();
-#pragma unroll
-                    for (int i = 0; i < BN; ++i) asm volatile("" : "+r"(v[i]));
-                }
-                VCLK(2);
-                if (!K::ALIAS) {
-                    tmem_before_sync();
-                    bar_arrive(s_free + g);
-                }
-                if (cls != 2) {
-#pragma unroll
-                    for (int k = 0; k < BN; ++k)
-                        if (!((bits[k / 32] >> (k % 32)) & 1u)) v[k] = 0xff800000u;
-                }
+            // the row's scores, then dP
+            constexpr int HELD = BACK ? 2 * BN : BN;
+            uint32_t v[HELD];
+            if (any_valid) {
+                tmem_read<HELD>(v, mine);
             }
-            if (MODE == kForward && any_valid) {
-                float most4[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    most4[i] = __uint_as_float(v[i]);
-#pragma unroll
-                    for (int k = i + 4; k < BN; k += 8)
-                        most4[i] = k + 4 < BN ? fmaxf(fmaxf(most4[i], __uint_as_float(v[k])), __uint_as_float(v[k + 4]))
-                                              : fmaxf(most4[i], __uint_as_float(v[k]));
-                }
-                const float most = fmaxf(fmaxf(most4[0], most4[1]), fmaxf(most4[2], most4[3]));
-                // The weights are relative to `top`, which follows the maximum only when that has
-                // grown by more than 2^8: then what was summed is scaled down.
-                const bool grow = top == -INFINITY ? most > -INFINITY : (most - top) * c > 8.0f;
-                if (__any_sync(0xffffffffu, grow)) {
-                    const float f = !grow ? 1.0f : top == -INFINITY ? 0.0f : ex2((top - most) * c);
-                    if (grow) top = most;
-                    sum *= f;
-                    if (it >= NWG) {
-                        if (!K::ALIAS) ok = bar_wait_warp(done + g, phase ^ 1, dead, a.err);   // again below
-                        tmem_after_sync();
-#pragma unroll 1
-                        for (int i = 0; i < DP; i += 16) {
-                            uint32_t o[16];
-                            tmem_load16(o, at_acc + i);
-                            tmem_wait_load();
-#pragma unroll
-                            for (int k = 0; k < 16; ++k) {
-                                asm volatile("" : "+r"(o[k]));
-                                o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-                            }
-                            tmem_store16(at_acc + i, o);
-                        }
-                    }
-                }
+            VCLK(2);
+            if (!K::ALIAS) {
+                tmem_before_sync();
+                bar_arrive(s_free + g);
             }
-            VCLK(3);
-            if (!K::ALIAS && it >= NWG) {      // the weights' columns are free
-                ok = ok && bar_wait_warp(done + g, phase ^ 1, dead, a.err);
+            if (cls != 2) {            // p, and with it ds unless dP is not finite, will be 0
+#pragma unroll
+                for (int k = 0; k < BN; ++k)
+                    if (!((bits[k / 32] >> (k % 32)) & 1u)) v[k] = 0xff800000u;
+            }
+            if (K::WEIGHTS == 1 && own > 0) {  // the weights' columns are free
+                ok = bar_wait_warp(tc_bar<K::WEIGHTS>(done, g, own - 1), tc_phase<K::WEIGHTS>(own - 1), dead, a.err);
+                if (!ok) break;
                 tmem_after_sync();
             }
-            if (!ok) break;
-            VCLK(4);
-            if (BACK && !K::ALIAS && !any_valid) bar_arrive(s_free + g);
-            if (any_valid) {
-                if (MODE == kForward) {
+            VCLK(3);
+            const float2 c2 = make_float2(c, c);
+            if (any_valid && MODE == kForward) {
+                auto pair = [&](int k) { return make_float2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])); };
+                if (own == 0) {
+                    float most[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int k = 0; k < BN; k += 2) most[k / 2 % 4] = fmaxf(fmaxf(most[k / 2 % 4], pair(k).x), pair(k).y);
+                    top = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3]));
+                }
+                // The weights are relative to `top`, the maximum of an earlier tile, and taken
+                // before this tile's maximum is known: only if that is greater by more than 2^8
+                // are the sums scaled down and the weights taken again.
+                for (;;) {
                     const float ref = top == -INFINITY ? -up : top * c - up;
-                    const float2 c2 = make_float2(c, c), ref2 = make_float2(-ref, -ref);
+                    const float2 ref2 = make_float2(-ref, -ref);
+                    float most[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
                     float2 sums[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
                     for (int i = 0; i < BN; i += 32) {
                         uint32_t out[16];
 #pragma unroll
                         for (int k = 0; k < 32; k += 2) {
-                            const float2 x = __ffma2_rn(make_float2(__uint_as_float(v[i + k]), __uint_as_float(v[i + k + 1])), c2, ref2);
+                            const float2 x = __ffma2_rn(pair(i + k), c2, ref2);
                             const float2 p = make_float2(ex2(x.x), ex2(x.y));
                             sums[k / 2 % 2] = __fadd2_rn(sums[k / 2 % 2], p);
                             out[k / 2] = pack2<T>(p.x, p.y);
+                            most[k / 2 % 4] = fmaxf(fmaxf(most[k / 2 % 4], pair(i + k).x), pair(i + k).y);
                         }
                         tmem_store16(at_p + i / 2, out);
                     }
-                    sum += (sums[0].x + sums[1].x) + (sums[0].y + sums[1].y);
-                } else {
-                    const float2 c2 = make_float2(c, c), one = make_float2(ds_scale, ds_scale);
-                    float2 l2 = make_float2(lse2, lse2), e2 = make_float2(delta, delta);
+                    const float high = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3]));
+                    const bool grow = top == -INFINITY ? high > -INFINITY : (high - top) * c > 8.0f;
+                    if (!__any_sync(0xffffffffu, grow)) {
+                        sum += (sums[0].x + sums[1].x) + (sums[0].y + sums[1].y);
+                        break;
+                    }
+                    const float f = !grow ? 1.0f : top == -INFINITY ? 0.0f : ex2((top - high) * c);
+                    if (grow) top = high;
+                    sum *= f;
+                    tmem_wait_store();         // of the weights that are written again
+                    if (own > 0) {
+                        ok = bar_wait_warp(tc_bar<K::WEIGHTS>(done, g, own - 1), tc_phase<K::WEIGHTS>(own - 1), dead, a.err);
+                        tmem_after_sync();
+#pragma unroll 1
+                        for (int i = 0; ok && i < DP; i += 16) {
+                            uint32_t o[16];
+                            tmem_read<16>(o, at_acc + i);
 #pragma unroll
-                    for (int i = 0; i < BN; i += 32) {
-                        uint32_t sc[32], dp[32], out[16], out2[16];
-                        tmem_load32(sc, mine + i);
-                        tmem_load32(dp, mine + BN + i);
-                        tmem_wait_load();
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) asm volatile("" : "+r"(sc[k]), "+r"(dp[k]));
-                        if (!K::ALIAS && i == BN - 32) {
-                            tmem_before_sync();
-                            bar_arrive(s_free + g);
+                            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                            tmem_store16(at_acc + i, o);
                         }
-                        if (cls != 2) {    // p, and with it ds unless dP is not finite, will be 0
-#pragma unroll
-                            for (int k = 0; k < 32; ++k)
-                                if (!((bits[i / 32] >> k) & 1u)) sc[k] = 0xff800000u;
-                        }
-#pragma unroll
-                        for (int k = 0; k < 32; k += 2) {
-                            if (MODE == kGradKV) {
-                                const float4 two = *reinterpret_cast<const float4 *>(cs + 8 * (i + k));
-                                l2 = make_float2(two.x, two.y);
-                                e2 = make_float2(two.z, two.w);
-                            }
-                            const float2 x = __ffma2_rn(make_float2(__uint_as_float(sc[k]), __uint_as_float(sc[k + 1])), c2, l2);
-                            const float2 p = make_float2(ex2(x.x), ex2(x.y));
-                            float2 d = __fmul2_rn(p, __fadd2_rn(make_float2(__uint_as_float(dp[k]), __uint_as_float(dp[k + 1])), e2));
-                            if (!BF16) d = __fmul2_rn(d, one);
-                            out[k / 2] = pack2<T>(p.x, p.y);
-                            out2[k / 2] = pack2<T>(d.x, d.y);
-                        }
-                        if (MODE == kGradKV) tmem_store16(at_p + i / 2, out);
-                        tmem_store16(at_ds + i / 2, out2);
                     }
                 }
-                VCLK(5);
-                tmem_wait_store();
             }
+            if (any_valid && BACK) {
+                const unsigned char *cs = tile_stat + st * K::STAT_BYTES;
+                const float2 one = make_float2(ds_scale, ds_scale);
+                float2 l2 = make_float2(lse2, lse2), e2 = make_float2(delta, delta);
+#pragma unroll
+                for (int i = 0; i < BN; i += 32) {
+                    uint32_t out[16], out2[16];
+#pragma unroll
+                    for (int k = i; k < i + 32; k += 2) {
+                        if (MODE == kGradKV) {
+                            const float4 two = *reinterpret_cast<const float4 *>(cs + 8 * k);
+                            l2 = make_float2(two.x, two.y);
+                            e2 = make_float2(two.z, two.w);
+                        }
+                        const float2 x = __ffma2_rn(make_float2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), c2, l2);
+                        const float2 p = make_float2(ex2(x.x), ex2(x.y));
+                        float2 d = __fmul2_rn(p, __fadd2_rn(make_float2(__uint_as_float(v[BN + k]), __uint_as_float(v[BN + k + 1])), e2));
+                        if (!BF16) d = __fmul2_rn(d, one);
+                        out[k % 32 / 2] = pack2<T>(p.x, p.y);
+                        out2[k % 32 / 2] = pack2<T>(d.x, d.y);
+                    }
+                    if (MODE == kGradKV) tmem_store16(at_p + i / 2, out);
+                    tmem_store16(at_ds + i / 2, out2);
+                }
+            }
+            VCLK(5);
+            if (!ok) break;
+            if (any_valid) tmem_wait_store();
             tmem_before_sync();
-            bar_arrive(ready + g);
+            bar_arrive(tc_bar<K::WEIGHTS>(ready, g, own));
             VCLK(6);
         }
 
         VCLKPRINT
         // ------------------------------------------------ results
-        if (ok && own > 0) ok = bar_wait_warp(done + g, (own - 1) & 1, dead, a.err);
+        if (ok && own > 0) ok = bar_wait_warp(tc_bar<K::WEIGHTS>(done, g, own - 1), tc_phase<K::WEIGHTS>(own - 1), dead, a.err);
         tmem_after_sync();
         const int count = *total;      // column tiles of the block
         if (NWG > 1) {                 // the other groups' are done too
@@ -542,8 +579,7 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
 #pragma unroll
                     for (int i = 0; i < DP / 32; ++i) {
                         uint32_t o[32];
-                        tmem_load32(o, acc0 + which * DP + 32 * i);
-                        tmem_wait_load32(o);
+                        tmem_read<32>(o, acc0 + which * DP + 32 * i);
 #pragma unroll
                         for (int k = 0; k < 32; ++k) finite = finite && isfinite(__uint_as_float(o[k]));
                     }
@@ -553,8 +589,7 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
                     uint32_t o[32];
                     float v[32];
                     if (count > 0) {
-                        tmem_load32(o, acc0 + which * DP + 32 * i);
-                        tmem_wait_load32(o);
+                        tmem_read<32>(o, acc0 + which * DP + 32 * i);
                     }
 #pragma unroll
                     for (int k = 0; k < 32; ++k) v[k] = count > 0 ? __uint_as_float(o[k]) : 0.0f;

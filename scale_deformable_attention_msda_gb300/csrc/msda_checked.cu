@@ -64,7 +64,6 @@ int msda_checked_build(void) {
 msda_status_t msda_device_check(void *stream) {
     if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess)
         return MSDA_ERR_CUDA;
-#ifdef MSDA_CHECKED
     unsigned *word = nullptr;
     if (msda::fault_word(&word) != cudaSuccess) return MSDA_ERR_CUDA;
     unsigned v = 0u;
@@ -73,9 +72,8 @@ msda_status_t msda_device_check(void *stream) {
         const unsigned zero = 0u;
         if (cudaMemcpy(word, &zero, sizeof zero, cudaMemcpyHostToDevice) != cudaSuccess)
             return MSDA_ERR_CUDA;
-        return MSDA_ERR_DEVICE_BOUNDS;
+        return v & 1u ? MSDA_ERR_DEVICE_BOUNDS : MSDA_ERR_DEVICE_WAIT;
     }
-#endif
     return MSDA_OK;
 }
 

@@ -35,6 +35,7 @@ __device__ __forceinline__ bool bar_try(uint64_t *bar, uint32_t parity) {
     uint32_t done;
     asm volatile("{\n\t.reg .pred p;\n\t"
                  "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+
                  "selp.u32 %0, 1, 0, p;\n\t}"
                  : "=r"(done)
                  : "r"(shared_at(bar)), "r"(parity)
@@ -63,6 +64,11 @@ __device__ __forceinline__ bool bar_wait_warp(uint64_t *bar, uint32_t parity, vo
     return __all_sync(0xffffffffu, bar_wait(bar, parity, dead, err));
 }
 
+// A group of four warps gives registers back, or takes them: what the block was launched
+// with is enough for all.
+template <int N> __device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N> __device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+
 // ------------------------------------------------------------------- TMA
 __device__ __forceinline__ void tma_load(void *to, const CUtensorMap *map, int x, int y, int z, int w, uint64_t *bar) {
     asm volatile("cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
@@ -89,46 +95,43 @@ template <int COLS> __device__ __forceinline__ void tmem_free(uint32_t at) {    
 }
 __device__ __forceinline__ void tmem_before_sync() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tmem_after_sync() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tmem_wait_load() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_store() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// As tmem_wait_load, and what uses `v` stays behind it.
-__device__ __forceinline__ void tmem_wait_load32(uint32_t (&v)[32]) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
-                   "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]),
-                   "+r"(v[16]), "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]), "+r"(v[23]),
-                   "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29]), "+r"(v[30]), "+r"(v[31])
-                 :: "memory");
+// N columns of the calling warp's 32 lanes, one lane's row to each thread. The wait is in
+// the same statement, so that nothing is done with the registers before it.
+#define TMEM_OUT8(o) "=&r"(v[o]), "=&r"(v[o + 1]), "=&r"(v[o + 2]), "=&r"(v[o + 3]), "=&r"(v[o + 4]), "=&r"(v[o + 5]), "=&r"(v[o + 6]), "=&r"(v[o + 7])
+#define TMEM_OUT32(o) TMEM_OUT8(o), TMEM_OUT8(o + 8), TMEM_OUT8(o + 16), TMEM_OUT8(o + 24)
+#define TMEM_R0 "%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15"
+#define TMEM_R1 "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31"
+#define TMEM_R2 "%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47"
+#define TMEM_R3 "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63"
+#define TMEM_R4 "%64,%65,%66,%67,%68,%69,%70,%71,%72,%73,%74,%75,%76,%77,%78,%79"
+#define TMEM_R5 "%80,%81,%82,%83,%84,%85,%86,%87,%88,%89,%90,%91,%92,%93,%94,%95"
+#define TMEM_R6 "%96,%97,%98,%99,%100,%101,%102,%103,%104,%105,%106,%107,%108,%109,%110,%111"
+#define TMEM_R7 "%112,%113,%114,%115,%116,%117,%118,%119,%120,%121,%122,%123,%124,%125,%126,%127"
+#define TMEM_WAIT "tcgen05.wait::ld.sync.aligned;"
+template <int N> __device__ __forceinline__ void tmem_read(uint32_t (&v)[N], uint32_t at);
+template <> __device__ __forceinline__ void tmem_read<16>(uint32_t (&v)[16], uint32_t at) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {" TMEM_R0 "}, [%16];\n\t" TMEM_WAIT
+                 : TMEM_OUT8(0), TMEM_OUT8(8) : "r"(at) : "memory");
 }
-
-// 32 columns of the calling warp's 32 lanes: one lane's row to each thread.
-__device__ __forceinline__ void tmem_load32(uint32_t *v, uint32_t at) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
-          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]),
-          "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]),
-          "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
-        : "r"(at));
+template <> __device__ __forceinline__ void tmem_read<32>(uint32_t (&v)[32], uint32_t at) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {" TMEM_R0 "," TMEM_R1 "}, [%32];\n\t" TMEM_WAIT
+                 : TMEM_OUT32(0) : "r"(at) : "memory");
 }
-__device__ __forceinline__ void tmem_load16(uint32_t *v, uint32_t at) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
-          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
-        : "r"(at));
+template <> __device__ __forceinline__ void tmem_read<64>(uint32_t (&v)[64], uint32_t at) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x64.b32 {" TMEM_R0 "," TMEM_R1 "," TMEM_R2 "," TMEM_R3 "}, [%64];\n\t" TMEM_WAIT
+                 : TMEM_OUT32(0), TMEM_OUT32(32) : "r"(at) : "memory");
 }
-__device__ __forceinline__ void tmem_store32(uint32_t at, const uint32_t (&v)[32]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(at),
-        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
-        "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]),
-        "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]),
-        "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
-        : "memory");
+template <> __device__ __forceinline__ void tmem_read<96>(uint32_t (&v)[96], uint32_t at) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x64.b32 {" TMEM_R0 "," TMEM_R1 "," TMEM_R2 "," TMEM_R3 "}, [%96];\n\t"
+                 "tcgen05.ld.sync.aligned.32x32b.x32.b32 {" TMEM_R4 "," TMEM_R5 "}, [%97];\n\t" TMEM_WAIT
+                 : TMEM_OUT32(0), TMEM_OUT32(32), TMEM_OUT32(64) : "r"(at), "r"(at + 64) : "memory");
+}
+template <> __device__ __forceinline__ void tmem_read<128>(uint32_t (&v)[128], uint32_t at) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x64.b32 {" TMEM_R0 "," TMEM_R1 "," TMEM_R2 "," TMEM_R3 "}, [%128];\n\t"
+                 "tcgen05.ld.sync.aligned.32x32b.x64.b32 {" TMEM_R4 "," TMEM_R5 "," TMEM_R6 "," TMEM_R7 "}, [%129];\n\t" TMEM_WAIT
+                 : TMEM_OUT32(0), TMEM_OUT32(32), TMEM_OUT32(64), TMEM_OUT32(96) : "r"(at), "r"(at + 64) : "memory");
 }
 __device__ __forceinline__ void tmem_store16(uint32_t at, const uint32_t (&v)[16]) {
     asm volatile(
