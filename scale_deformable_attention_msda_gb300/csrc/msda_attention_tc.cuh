@@ -37,10 +37,10 @@ template <int BN_, int NWG_, int STAGES_, int BLOCKS_, int WEIGHTS_> struct TcSi
 };
 template <int MODE, int DP> struct TcConfig;
 #ifndef F32
-#define F32 96, 1, 3, 2, 2
+#define F32 128, 1, 3, 2, 1
 #endif
 #ifndef F64
-#define F64 96, 1, 2, 2, 2
+#define F64 128, 1, 2, 2, 1
 #endif
 #ifndef F128
 #define F128 64, 1, 2, 2, 2
@@ -105,6 +105,11 @@ template <int MODE, int DP> struct Tc : TcConfig<MODE, DP> {
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float y;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
     return y;
 }
 template <typename T> __device__ __forceinline__ uint32_t pack2(float lo, float hi);
@@ -173,7 +178,9 @@ __device__ __forceinline__ void tc_store(const AttnArgs &a, int64_t row, int spl
 #define VCLKDEF long long ck[8] = {}, ck0 = clock64(); const long long ckb = ck0;
 #define VCLK(i) { const long long n_ = clock64(); ck[i] += n_ - ck0; ck0 = n_; }
 #define VCLKPRINT if (threadIdx.x == 0 && (blockIdx.x == 0 || blockIdx.x == 200)) printf("mode %d DP %d it %d total %lld : loop %lld s_full %lld ld %lld max %lld done %lld exp %lld st %lld dup %lld\n", MODE, DP, own, (clock64() - ckb) / (own ? own : 1), ck[0] / (own ? own : 1), ck[1] / (own ? own : 1), ck[2] / (own ? own : 1), ck[3] / (own ? own : 1), ck[4] / (own ? own : 1), ck[5] / (own ? own : 1), ck[6] / (own ? own : 1), ck[7] / (own ? own : 1));
+#define VCLKP2(n, c) if (threadIdx.x % 32 == 0) if (blockIdx.x == 0 || blockIdx.x == 200) printf("mode %d DP %d %s it %d total %lld : loop %lld full %lld free %lld done %lld issue %lld lat %lld\n", MODE, DP, n, c, (clock64() - ckb) / c, ck[0] / c, ck[1] / c, ck[2] / c, ck[3] / c, ck[4] / c, ck[5] / c);
 #else
+#define VCLKP2(n, c) ;
 #define VCLKDEF
 #define VCLK(i)
 #define VCLKPRINT
@@ -213,7 +220,7 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
     uint32_t *slot = reinterpret_cast<uint32_t *>(total + 1);
     volatile uint32_t *dead = slot + 1;
 
-    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x & 31;
     const int split = blockIdx.x % a.splits;
     const AttnRows w = attn_rows<MODE, kTcRows>(a, blockIdx.x / a.splits);
     const int64_t tiles = attn_column_tiles<MODE, BN>(a);
@@ -250,7 +257,7 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
     fewer_registers<K::REGS_OTHER>();
     if (warp == NWG * 4 + 1) {
         // ------------------------------------------------ fetching
-        if (lane == 0) {
+        {
             int it = 0, pos = 0, head = 0;
             if (j0 < j1) attn_columns<MODE, BN>(a, w, j0, &pos, &head);
             bool ok = true;
@@ -265,9 +272,10 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
                         }
                     }
                     const int st = it % STAGES;
-                    ok = it < STAGES || bar_wait(empty + st, (it / STAGES - 1) & 1, dead, a.err);
+                    ok = it < STAGES || bar_wait_warp(empty + st, (it / STAGES - 1) & 1, dead, a.err);
                     if (!ok) break;
-                    info[st] = {pos, head, cls};
+                    if (lane == 0) info[st] = {pos, head, cls};
+                    __syncwarp();
                     bar_expect(full + st, 2 * K::COL_BYTES + K::STAT_BYTES);
                     unsigned char *x1 = tile_x + st * 2 * K::COL_BYTES, *x2 = x1 + K::COL_BYTES;
                     for (int p = 0; p < K::PANELS; ++p) {
@@ -283,51 +291,58 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
                     ++head;
                 }
             }
-            *total = it;
+            if (lane == 0) *total = it;
             for (int i = it; ok && i < it + NWG; ++i) {    // each group finds an end
                 const int st = i % STAGES;
-                ok = i < STAGES || bar_wait(empty + st, (i / STAGES - 1) & 1, dead, a.err);
+                ok = i < STAGES || bar_wait_warp(empty + st, (i / STAGES - 1) & 1, dead, a.err);
                 if (!ok) break;
-                info[st].cls = 0;
-                bar_arrive(full + st);
+                if (lane == 0) info[st].cls = 0;
+                __syncwarp();
+                bar_arrive_one(full + st);
             }
             if (*dead) {               // copies under way end before the block does
                 uint32_t off = 0u;
-                for (int i = it < STAGES ? 0 : it - STAGES; i < it; ++i) bar_wait(full + i % STAGES, (i / STAGES) & 1, &off, nullptr);
-                if (it > 0) bar_wait(a_full, 0, &off, nullptr);
+                for (int i = it < STAGES ? 0 : it - STAGES; i < it; ++i) bar_wait_warp(full + i % STAGES, (i / STAGES) & 1, &off, nullptr);
+                if (it > 0) bar_wait_warp(a_full, 0, &off, nullptr);
             }
         }
         __syncwarp();
     } else if (warp == NWG * 4) {
         // ------------------------------------------------ scores
-        if (lane == 0) {
+        {
             const int steps = (a.D + 15) / 16;
             const uint32_t a1 = desc_low(shared_at(tile_a1), 16), a2 = desc_low(shared_at(tile_a2), 16);
             const uint32_t along = desc_low(shared_at(tile_x), 16);
             constexpr uint32_t id = mma_desc<BF16, BN, false>(), high = desc_high<K::PITCH>();
             constexpr int per = K::PITCH / 32;      // steps of 16 channels in a panel
             bool ok = true;
+            VCLKDEF
             for (int it = 0;; ++it) {
                 const int g = it % NWG, own = it / NWG, st = it % STAGES;
-                ok = bar_wait(full + st, (it / STAGES) & 1, dead, a.err);
+                VCLK(0);
+                ok = bar_wait_warp(full + st, (it / STAGES) & 1, dead, a.err);
+                VCLK(1);
                 if (!ok) break;
                 if (!info[st].cls) {
+                    VCLKP2("scores", it)
                     // each group finds the end once it has read its last scores: before, this
                     // would be taken for their arrival
                     for (int i = it; ok && i < it + NWG; ++i) {
-                        if (i >= NWG) ok = K::ALIAS ? bar_wait(tc_bar<K::WEIGHTS>(done, i % NWG, i / NWG - 1), tc_phase<K::WEIGHTS>(i / NWG - 1), dead, a.err)
-                                                    : bar_wait(s_free + i % NWG, (i / NWG - 1) & 1, dead, a.err);
-                        if (ok) bar_arrive(s_full + i % NWG);
+                        if (i >= NWG) ok = K::ALIAS ? bar_wait_warp(tc_bar<K::WEIGHTS>(done, i % NWG, i / NWG - 1), tc_phase<K::WEIGHTS>(i / NWG - 1), dead, a.err)
+                                                    : bar_wait_warp(s_free + i % NWG, (i / NWG - 1) & 1, dead, a.err);
+                        if (ok) bar_arrive_one(s_full + i % NWG);
                     }
                     break;
                 }
-                if (it == 0) ok = bar_wait(a_full, 0, dead, a.err);
+                if (it == 0) ok = bar_wait_warp(a_full, 0, dead, a.err);
                 // the columns are free: the group has read its last scores, and (ALIAS: these
                 // became weights) the weights that it will write are used
-                if (ok && !K::ALIAS && own > 0) ok = bar_wait(s_free + g, (own - 1) & 1, dead, a.err);
-                if (ok && K::ALIAS && own > 0) ok = bar_wait(tc_bar<K::WEIGHTS>(done, g, own - 1), tc_phase<K::WEIGHTS>(own - 1), dead, a.err);
-                if (ok && K::WEIGHTS == 2 && own > 1) ok = bar_wait(tc_bar<K::WEIGHTS>(done, g, own - 2), tc_phase<K::WEIGHTS>(own - 2), dead, a.err);
+                if (ok && !K::ALIAS && own > 0) ok = bar_wait_warp(s_free + g, (own - 1) & 1, dead, a.err);
+                if (ok && K::ALIAS && own > 0) ok = bar_wait_warp(tc_bar<K::WEIGHTS>(done, g, own - 1), tc_phase<K::WEIGHTS>(own - 1), dead, a.err);
+                VCLK(2);
+                if (ok && K::WEIGHTS == 2 && own > 1) ok = bar_wait_warp(tc_bar<K::WEIGHTS>(done, g, own - 2), tc_phase<K::WEIGHTS>(own - 2), dead, a.err);
                 if (!ok) break;
+                VCLK(3);
                 tmem_after_sync();
                 const uint32_t x1 = along + st * desc_step(2 * K::COL_BYTES), x2 = x1 + desc_step(K::COL_BYTES);
                 const uint32_t d = tmem + g * K::GROUP;
@@ -339,26 +354,36 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
                     if (BACK) mma_shared<id, high>(d + BN, a2 + ra, x2 + rx, k > 0);
                 }
                 mma_commit(s_full + g);
+                VCLK(4);
+#ifdef V_LAT
+                bar_wait_warp(s_full + g, own & 1, dead, a.err);
+                VCLK(5);
+#endif
             }
             if (!ok) {                 // MMAs under way end before the block does
                 uint32_t off = 0u;
                 mma_commit(last);
-                bar_wait(last, 0, &off, nullptr);
+                bar_wait_warp(last, 0, &off, nullptr);
             }
         }
         __syncwarp();
     } else if (warp == NWG * 4 + 2) {
         // ------------------------------------------------ second products
-        if (lane == 0) {
+        {
             const uint32_t across = desc_low(shared_at(tile_x), BN * K::PITCH);
             constexpr uint32_t id = mma_desc<BF16, DP, true>(), high = desc_high<K::PITCH>();
             bool ok = true;
+            VCLKDEF
             for (int it = 0;; ++it) {
                 const int g = it % NWG, own = it / NWG, st = it % STAGES;
-                ok = bar_wait(full + st, (it / STAGES) & 1, dead, a.err);
+                VCLK(0);
+                ok = bar_wait_warp(full + st, (it / STAGES) & 1, dead, a.err);
+                VCLK(1);
+                if (!info[st].cls) VCLKP2("second", it)
                 if (!ok || !info[st].cls) break;
-                ok = bar_wait(tc_bar<K::WEIGHTS>(ready, g, own), tc_phase<K::WEIGHTS>(own), dead, a.err);
+                ok = bar_wait_warp(tc_bar<K::WEIGHTS>(ready, g, own), tc_phase<K::WEIGHTS>(own), dead, a.err);
                 if (!ok) break;
+                VCLK(2);
                 tmem_after_sync();
                 const uint32_t x1 = across + st * desc_step(2 * K::COL_BYTES), x2 = x1 + desc_step(K::COL_BYTES);
                 const uint32_t s = tmem + g * K::GROUP, acc = tmem + K::ACC + (MODE == kForward ? g * DP : 0);
@@ -374,11 +399,12 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
                 }
                 mma_commit(empty + st);
                 mma_commit(tc_bar<K::WEIGHTS>(done, g, own));  // last: the block ends after it has arrived
+                VCLK(4);
             }
             if (!ok) {
                 uint32_t off = 0u;
                 mma_commit(last + 1);
-                bar_wait(last + 1, 0, &off, nullptr);
+                bar_wait_warp(last + 1, 0, &off, nullptr);
             }
         }
         __syncwarp();
@@ -456,43 +482,17 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
             const float2 c2 = make_float2(c, c);
             if (any_valid && MODE == kForward) {
                 auto pair = [&](int k) { return make_float2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])); };
-                if (own == 0) {
-                    float most[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                float most[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                    for (int k = 0; k < BN; k += 2) most[k / 2 % 4] = fmaxf(fmaxf(most[k / 2 % 4], pair(k).x), pair(k).y);
-                    top = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3]));
-                }
-                // The weights are relative to `top`, the maximum of an earlier tile, and taken
-                // before this tile's maximum is known: only if that is greater by more than 2^8
-                // are the sums scaled down and the weights taken again.
-                for (;;) {
-                    const float ref = top == -INFINITY ? -up : top * c - up;
-                    const float2 ref2 = make_float2(-ref, -ref);
-                    float most[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                    float2 sums[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-#pragma unroll
-                    for (int i = 0; i < BN; i += 32) {
-                        uint32_t out[16];
-#pragma unroll
-                        for (int k = 0; k < 32; k += 2) {
-                            const float2 x = __ffma2_rn(pair(i + k), c2, ref2);
-                            const float2 p = make_float2(ex2(x.x), ex2(x.y));
-                            sums[k / 2 % 2] = __fadd2_rn(sums[k / 2 % 2], p);
-                            out[k / 2] = pack2<T>(p.x, p.y);
-                            most[k / 2 % 4] = fmaxf(fmaxf(most[k / 2 % 4], pair(i + k).x), pair(i + k).y);
-                        }
-                        tmem_store16(at_p + i / 2, out);
-                    }
-                    const float high = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3]));
-                    const bool grow = top == -INFINITY ? high > -INFINITY : (high - top) * c > 8.0f;
-                    if (!__any_sync(0xffffffffu, grow)) {
-                        sum += (sums[0].x + sums[1].x) + (sums[0].y + sums[1].y);
-                        break;
-                    }
+                for (int k = 0; k < BN; k += 2) most[k / 2 % 4] = max3(most[k / 2 % 4], pair(k).x, pair(k).y);
+                const float high = max3(fmaxf(most[0], most[1]), most[2], most[3]);
+                // The weights are relative to `top`, which follows the maximum only when that has
+                // grown by more than 2^8: then what was summed is scaled down.
+                const bool grow = top == -INFINITY ? high > -INFINITY : (high - top) * c > 8.0f;
+                if (__any_sync(0xffffffffu, grow)) {
                     const float f = !grow ? 1.0f : top == -INFINITY ? 0.0f : ex2((top - high) * c);
                     if (grow) top = high;
                     sum *= f;
-                    tmem_wait_store();         // of the weights that are written again
                     if (own > 0) {
                         ok = bar_wait_warp(tc_bar<K::WEIGHTS>(done, g, own - 1), tc_phase<K::WEIGHTS>(own - 1), dead, a.err);
                         tmem_after_sync();
@@ -506,6 +506,23 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
                         }
                     }
                 }
+                VCLK(4);
+                const float ref = top == -INFINITY ? -up : top * c - up;
+                const float2 ref2 = make_float2(-ref, -ref);
+                float2 sums[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+#pragma unroll
+                for (int i = 0; i < BN; i += 32) {
+                    uint32_t out[16];
+#pragma unroll
+                    for (int k = 0; k < 32; k += 2) {
+                        const float2 x = __ffma2_rn(pair(i + k), c2, ref2);
+                        const float2 p = make_float2(ex2(x.x), ex2(x.y));
+                        sums[k / 2 % 2] = __fadd2_rn(sums[k / 2 % 2], p);
+                        out[k / 2] = pack2<T>(p.x, p.y);
+                    }
+                    tmem_store16(at_p + i / 2, out);
+                }
+                sum += (sums[0].x + sums[1].x) + (sums[0].y + sums[1].y);
             }
             if (any_valid && BACK) {
                 const unsigned char *cs = tile_stat + st * K::STAT_BYTES;

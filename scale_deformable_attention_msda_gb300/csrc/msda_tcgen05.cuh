@@ -21,6 +21,15 @@ __device__ __forceinline__ unsigned long long nanoseconds() {
     asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
     return t;
 }
+// One lane of a whole warp issues the instruction, always the same one. The warp's
+// code around it stays uniform, and with it descriptors and addresses, which these
+// instructions take from uniform registers: issued from a branch of one lane, an MMA
+// costs 70 cycles instead of 45.
+#define ELECT(instruction) "{\n\t.reg .pred one;\n\telect.sync _|one, 0xffffffff;\n\t@one " instruction "\n\t}"
+
+__device__ __forceinline__ void bar_arrive_one(uint64_t *bar) {
+    asm volatile(ELECT("mbarrier.arrive.shared::cta.b64 _, [%0];") ::"r"(shared_at(bar)) : "memory");
+}
 __device__ __forceinline__ void bar_init(uint64_t *bar, uint32_t count) {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(shared_at(bar)), "r"(count) : "memory");
 }
@@ -29,7 +38,7 @@ __device__ __forceinline__ void bar_arrive(uint64_t *bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(shared_at(bar)) : "memory");
 }
 __device__ __forceinline__ void bar_expect(uint64_t *bar, uint32_t bytes) {
-    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(shared_at(bar)), "r"(bytes) : "memory");
+    asm volatile(ELECT("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;") ::"r"(shared_at(bar)), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ bool bar_try(uint64_t *bar, uint32_t parity) {
     uint32_t done;
@@ -71,13 +80,13 @@ template <int N> __device__ __forceinline__ void more_registers() { asm volatile
 
 // ------------------------------------------------------------------- TMA
 __device__ __forceinline__ void tma_load(void *to, const CUtensorMap *map, int x, int y, int z, int w, uint64_t *bar) {
-    asm volatile("cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
+    asm volatile(ELECT("cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];")
                  ::"r"(shared_at(to)), "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(shared_at(bar))
                  : "memory");
 }
 // `bytes`, a multiple of 16, from and to 16-byte boundaries.
 __device__ __forceinline__ void bulk_load(void *to, const void *from, uint32_t bytes, uint64_t *bar) {
-    asm volatile("cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+    asm volatile(ELECT("cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];")
                  ::"r"(shared_at(to)), "l"(from), "r"(bytes), "r"(shared_at(bar))
                  : "memory");
 }
@@ -170,23 +179,23 @@ __device__ __forceinline__ constexpr uint32_t mma_desc() {
 // d (+)= a b' of descriptors with the same high word; idesc and high are constants.
 template <uint32_t IDESC, uint32_t HIGH>
 __device__ __forceinline__ void mma_shared(uint32_t d, uint32_t a, uint32_t b, bool add) {
-    asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.u32 p, %3, 0;\n\t"
+    asm volatile("{\n\t.reg .pred p, one;\n\t.reg .b64 da, db;\n\telect.sync _|one, 0xffffffff;\n\tsetp.ne.u32 p, %3, 0;\n\t"
                  "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, p;\n\t}"
+                 "@one tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, p;\n\t}"
                  ::"r"(d), "r"(a), "r"(b), "r"((uint32_t)add), "n"(IDESC), "n"(HIGH)
                  : "memory");
 }
 template <uint32_t IDESC, uint32_t HIGH>
 __device__ __forceinline__ void mma_tmem(uint32_t d, uint32_t a, uint32_t b, bool add) {
-    asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 db;\n\tsetp.ne.u32 p, %3, 0;\n\t"
+    asm volatile("{\n\t.reg .pred p, one;\n\t.reg .b64 db;\n\telect.sync _|one, 0xffffffff;\n\tsetp.ne.u32 p, %3, 0;\n\t"
                  "mov.b64 db, {%2, %5};\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n\t}"
+                 "@one tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n\t}"
                  ::"r"(d), "r"(a), "r"(b), "r"((uint32_t)add), "n"(IDESC), "n"(HIGH)
                  : "memory");
 }
 // Arrives at `bar` when every MMA issued before has finished.
 __device__ __forceinline__ void mma_commit(uint64_t *bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(shared_at(bar)) : "memory");
+    asm volatile(ELECT("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];") ::"r"(shared_at(bar)) : "memory");
 }
 
 }  // namespace msda
