@@ -56,7 +56,8 @@ struct AttnArgs {
     // backward: (B, M, stat_row / 2, 4), for two queries each -lse in the exponent's
     // units, plus `up`, and -delta; past the last query -infinity and 0
     float *stat;
-    int stat_row;                      // queries in a row of stat: Q up to a multiple of 64
+    int stat_row;                      // queries in a row of stat: Q up to a multiple of 128, the
+                                       // longest tile's
     float up;                          // fp16 backward: its probabilities are scaled by 2^up
     // fp16 backward: partial maxima of |dO_i|^2 and |v_j|^2 (norms each, see
     // attn_delta_kernel); NULL for other types
@@ -161,7 +162,7 @@ __device__ __forceinline__ int attn_class(const AttnArgs &a, const AttnRows &w, 
 // Bits of columns pos + 32 i to pos + 32 i + 31 of one row (pos a multiple of 32).
 template <int MODE>
 __device__ __forceinline__ uint32_t attn_word(const AttnArgs &a, const uint32_t *row, int at) {
-    if (MODE == kGradKV) return row ? row[(int64_t)(at >> 5) * a.by_key.word] : 0xffffffffu;
+    if (MODE == kGradKV) return !row ? 0xffffffffu : at < a.Q ? row[(int64_t)(at >> 5) * a.by_key.word] : 0u;
     if (row) return at < a.S ? row[at >> 5] : 0u;
     const int left = a.S - at;
     return left >= 32 ? 0xffffffffu : left <= 0 ? 0u : (1u << left) - 1u;

@@ -117,7 +117,7 @@ Layout layout_of(const msda_attention_dims_t &d, msda_dtype_t dt, bool mask, boo
         if (backward) w.bits_k = take(maps * d.S * w.words_k * 4);
     }
     if (backward) {
-        w.stat = take((size_t)d.B * d.M * ceil_div(d.Q, 64) * 64 * 8);
+        w.stat = take((size_t)d.B * d.M * ceil_div(d.Q, 128) * 128 * 8);
         if (dt == MSDA_F16) w.norms = take(2 * kDeltaBlocks * 4);
         w.part[1] = take(plan_for(d, dt, msda::kGradQ).part);
         w.part[2] = take(plan_for(d, dt, msda::kGradKV).part);
@@ -262,7 +262,7 @@ msda_status_t msda_attention_backward(const void *grad_out, const void *q, const
     char *ws = static_cast<char *>(workspace);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     a.stat = reinterpret_cast<float *>(ws + w.stat);
-    a.stat_row = (int)(ceil_div(d.Q, 64) * 64);
+    a.stat_row = (int)(ceil_div(d.Q, 128) * 128);
     a.up = dtype == MSDA_F16 ? msda::kHalfUp : 0.0f;
     const int64_t rows = d.B * d.Q * d.M;
     a.norms = (int)(rows < 1 ? 1 : rows < kDeltaBlocks ? rows : kDeltaBlocks);

@@ -12,8 +12,8 @@ cudaError_t launch_attention_bf16(int mode, const AttnArgs &a, int64_t blocks, c
 cudaError_t launch_attention_f16(int mode, const AttnArgs &a, int64_t blocks, cudaStream_t stream);
 
 // The 16-bit kernels' columns of a tile, and their blocks of an SM.
-constexpr int tc_columns(int mode, int D) { return mode == kForward && D <= 64 ? 96 : 64; }
-constexpr int tc_blocks(int mode, int D) { return mode != kForward && D > 64 ? 1 : 2; }
+constexpr int tc_columns(int mode, int D) { return mode == kForward && D > 64 ? 64 : 128; }
+constexpr int tc_blocks(int mode, int D) { return mode != kForward ? 1 : 2; }
 
 // What the mask is made of before it is packed: bytes at strides.
 struct AttnMaskSource {

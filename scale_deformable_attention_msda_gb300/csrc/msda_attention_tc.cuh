@@ -28,40 +28,41 @@ namespace msda {
 
 constexpr int kTcRows = 128;
 
-// DP: channels in shared memory. BN: columns of a tile. NWG: groups of warps.
-// STAGES: tiles in shared memory. BLOCKS: of an SM, by tensor memory (512 columns) and
-// shared memory. WEIGHTS: buffers of a group's weights in tensor memory; 0: they lie in
-// the scores' columns, and the next scores wait for the second product.
-template <int BN_, int NWG_, int STAGES_, int BLOCKS_, int WEIGHTS_> struct TcSizes {
-    static constexpr int BN = BN_, NWG = NWG_, STAGES = STAGES_, BLOCKS = BLOCKS_, WEIGHTS = WEIGHTS_;
+// DP: channels in shared memory. BN: columns of a tile. PARTS: groups of four warps that
+// share each row, a part of the columns each. STAGES, EARLY: tiles in shared memory of the
+// two column operands. BLOCKS: of an SM, by tensor memory (512 columns) and shared memory.
+// WEIGHTS: buffers of weights in tensor memory; 0: they lie in the scores' columns, and the
+// next scores wait for the second product.
+template <int BN_, int PARTS_, int STAGES_, int EARLY_, int BLOCKS_, int WEIGHTS_> struct TcSizes {
+    static constexpr int BN = BN_, PARTS = PARTS_, STAGES = STAGES_, EARLY = EARLY_, BLOCKS = BLOCKS_, WEIGHTS = WEIGHTS_;
 };
 template <int MODE, int DP> struct TcConfig;
 #ifndef F32
-#define F32 128, 1, 3, 2, 1
+#define F32 128, 1, 3, 3, 2, 1
 #endif
 #ifndef F64
-#define F64 128, 1, 2, 2, 1
+#define F64 128, 1, 2, 2, 2, 1
 #endif
 #ifndef F128
-#define F128 64, 1, 2, 2, 2
+#define F128 64, 1, 2, 2, 2, 2
 #endif
 #ifndef Q32
-#define Q32 64, 1, 3, 2, 2
+#define Q32 128, 2, 4, 4, 1, 2
 #endif
 #ifndef Q64
-#define Q64 64, 1, 3, 2, 2
+#define Q64 128, 2, 3, 3, 1, 2
 #endif
 #ifndef Q128
-#define Q128 64, 2, 4, 1, 2
+#define Q128 128, 2, 2, 2, 1, 2
 #endif
 #ifndef KV32
-#define KV32 64, 1, 3, 2, 1
+#define KV32 128, 2, 4, 4, 1, 1
 #endif
 #ifndef KV64
-#define KV64 64, 1, 3, 2, 0
+#define KV64 128, 2, 3, 3, 1, 1
 #endif
 #ifndef KV128
-#define KV128 64, 2, 3, 1, 0
+#define KV128 128, 2, 2, 2, 1, 0
 #endif
 template <> struct TcConfig<kForward, 32> : TcSizes<F32> {};
 template <> struct TcConfig<kForward, 64> : TcSizes<F64> {};
@@ -75,26 +76,25 @@ template <> struct TcConfig<kGradKV, 128> : TcSizes<KV128> {};
 
 template <int MODE, int DP> struct Tc : TcConfig<MODE, DP> {
     using C = TcConfig<MODE, DP>;
-    static constexpr int BN = C::BN, NWG = C::NWG, STAGES = C::STAGES;
-    static constexpr int WEIGHTS = C::WEIGHTS, WIDE = BN / 2 * (MODE == kGradKV ? 2 : 1);    // columns of a buffer
+    static constexpr int BN = C::BN, PARTS = C::PARTS, STAGES = C::STAGES, EARLY = C::EARLY, WEIGHTS = C::WEIGHTS;
     static constexpr bool ALIAS = WEIGHTS == 0, BACK = MODE != kForward;
     static constexpr int PITCH = DP == 32 ? 64 : 128, PANELS = DP == 128 ? 2 : 1, PANEL = DP == 128 ? 64 : DP;
     static constexpr int ROW_BYTES = kTcRows * PITCH * PANELS, COL_BYTES = BN * PITCH * PANELS;
-    static constexpr int THREADS = (NWG + 1) * 128;
+    static constexpr int ROW_THREADS = PARTS * 128, THREADS = ROW_THREADS + 128, PART = BN / PARTS;
     // registers: 65,536 of an SM, spread evenly at the start and then by need
-    static constexpr int REGS_ROW = NWG == 1 ? 208 : 208, REGS_OTHER = NWG == 1 ? 48 : 88;
-    static_assert((NWG * REGS_ROW + REGS_OTHER) * 128 <= 65536 / C::BLOCKS / THREADS / 8 * 8 * THREADS, "registers");
-    // tensor memory: for each group scores (and dP), then weights; then
-    // the accumulators (forward: one a group)
-    static constexpr int GROUP = BN * (BACK ? 2 : 1) + WEIGHTS * WIDE;
-    static constexpr int ACC = NWG * GROUP, ACCS = MODE == kForward ? NWG : MODE == kGradKV ? 2 : 1;
-    static constexpr int USED = ACC + ACCS * DP, COLS = USED <= 128 ? 128 : USED <= 256 ? 256 : 512;
-    //static_assert(BN == tc_columns(MODE, DP), "what the host plans with");
-    static_assert(NWG <= STAGES, "an end for each group");
-    static_assert(MODE != kForward || NWG == 1, "one maximum and sum a row");
+    static constexpr int REGS_ROW = PARTS == 1 ? 208 : 208, REGS_OTHER = PARTS == 1 ? 48 : 88;
+    static_assert((PARTS * REGS_ROW + REGS_OTHER) * 128 <= 65536 / C::BLOCKS / THREADS / 8 * 8 * THREADS, "registers");
+    // tensor memory: scores (and dP), weights, accumulators
+    static constexpr int SCORES = BN * (BACK ? 2 : 1), WIDE = BN / 2 * (MODE == kGradKV ? 2 : 1);
+    static constexpr int ACC = SCORES + WEIGHTS * WIDE, RESULTS = MODE == kGradKV ? 2 : 1;
+    static constexpr int USED = ACC + RESULTS * DP, COLS = USED <= 128 ? 128 : USED <= 256 ? 256 : 512;
+    static_assert(BN == tc_columns(MODE, DP) && C::BLOCKS == tc_blocks(MODE, DP), "what the host plans with");
+    static_assert(MODE != kForward || PARTS == 1, "one maximum and sum a row");
     static_assert(USED <= 512 && COLS * C::BLOCKS <= 512, "tensor memory");
-    static constexpr int TILES = (BACK ? 2 : 1) * ROW_BYTES + STAGES * 2 * COL_BYTES;
+    static constexpr int TILES = (BACK ? 2 : 1) * ROW_BYTES + (STAGES + EARLY) * COL_BYTES;
     static constexpr int STAT_BYTES = MODE == kGradKV ? 8 * BN : 0;    // of a column tile
+    static constexpr int INFO = 8;
+    static_assert(STAGES + 1 <= INFO, "announcements are read before they are written over");
     static constexpr int NEEDED = 1024 + TILES + STAGES * STAT_BYTES + 1024;
     // as much as keeps one block more off the SM, which would only wait for its tensor memory
     static constexpr int LIMIT = 228 * 1024 / (C::BLOCKS + 1);
@@ -177,7 +177,7 @@ __device__ __forceinline__ void tc_store(const AttnArgs &a, int64_t row, int spl
 #ifdef V_CLOCK
 #define VCLKDEF long long ck[8] = {}, ck0 = clock64(); const long long ckb = ck0;
 #define VCLK(i) { const long long n_ = clock64(); ck[i] += n_ - ck0; ck0 = n_; }
-#define VCLKPRINT if (threadIdx.x == 0 && (blockIdx.x == 0 || blockIdx.x == 200)) printf("mode %d DP %d it %d total %lld : loop %lld s_full %lld ld %lld max %lld done %lld exp %lld st %lld dup %lld\n", MODE, DP, own, (clock64() - ckb) / (own ? own : 1), ck[0] / (own ? own : 1), ck[1] / (own ? own : 1), ck[2] / (own ? own : 1), ck[3] / (own ? own : 1), ck[4] / (own ? own : 1), ck[5] / (own ? own : 1), ck[6] / (own ? own : 1), ck[7] / (own ? own : 1));
+#define VCLKPRINT if (threadIdx.x == 0 && (blockIdx.x == 0 || blockIdx.x == 200)) printf("mode %d DP %d it %d total %lld : loop %lld s_full %lld ld %lld max %lld done %lld exp %lld st %lld dup %lld\n", MODE, DP, it, (clock64() - ckb) / (it ? it : 1), ck[0] / (it ? it : 1), ck[1] / (it ? it : 1), ck[2] / (it ? it : 1), ck[3] / (it ? it : 1), ck[4] / (it ? it : 1), ck[5] / (it ? it : 1), ck[6] / (it ? it : 1), ck[7] / (it ? it : 1));
 #define VCLKP2(n, c) if (threadIdx.x % 32 == 0) if (blockIdx.x == 0 || blockIdx.x == 200) printf("mode %d DP %d %s it %d total %lld : loop %lld full %lld free %lld done %lld issue %lld lat %lld\n", MODE, DP, n, c, (clock64() - ckb) / c, ck[0] / c, ck[1] / c, ck[2] / c, ck[3] / c, ck[4] / c, ck[5] / c);
 #else
 #define VCLKP2(n, c) ;
@@ -190,13 +190,13 @@ struct TcTile {
     int pos, head, cls;
 };
 
-// Barriers of a buffer of weights: group g's tile `own` is ready for its second product,
-// or done with it. Each buffer has its own: a wait tells a phase only from the one before
+// Barriers of a buffer of weights: column tile `it` is ready for its second product, or
+// done with it. Each buffer has its own: a wait tells a phase only from the one before
 // it, and a warp may be ready with the next tile before another is with this one.
-template <int WEIGHTS> __device__ __forceinline__ uint64_t *tc_bar(uint64_t *bars, int g, int own) {
-    return bars + 2 * g + (WEIGHTS == 2 ? own & 1 : 0);
+template <int WEIGHTS> __device__ __forceinline__ uint64_t *tc_bar(uint64_t *bars, int it) {
+    return bars + (WEIGHTS == 2 ? it & 1 : 0);
 }
-template <int WEIGHTS> __device__ __forceinline__ uint32_t tc_phase(int own) { return (WEIGHTS == 2 ? own >> 1 : own) & 1; }
+template <int WEIGHTS> __device__ __forceinline__ uint32_t tc_phase(int it) { return (WEIGHTS == 2 ? it >> 1 : it) & 1; }
 
 struct TcMaps {
     CUtensorMap a1, a2, x1, x2;        // rows: one or two; columns: two
@@ -206,18 +206,21 @@ template <typename T, int MODE, int DP>
 __global__ void __launch_bounds__(Tc<MODE, DP>::THREADS, Tc<MODE, DP>::BLOCKS)
 attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
     using K = Tc<MODE, DP>;
-    constexpr int BN = K::BN, NWG = K::NWG, STAGES = K::STAGES;
+    constexpr int BN = K::BN, STAGES = K::STAGES, EARLY = K::EARLY, INFO = K::INFO, HELPER = K::PARTS * 4;
     constexpr bool BF16 = TcScale<T>::forward == 0.0f, BACK = K::BACK;
+    // Which operand's tile is only used for the scores, and free after them: forward's k,
+    // the x1, and dq's v, the x2. The other one's stays for the second product.
+    constexpr bool FIRST_EARLY = MODE == kForward;
     extern __shared__ unsigned char raw[];
     unsigned char *base = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
-    unsigned char *tile_a1 = base, *tile_a2 = base + K::ROW_BYTES, *tile_x = base + (BACK ? 2 : 1) * K::ROW_BYTES;
+    unsigned char *tile_a1 = base, *tile_a2 = base + K::ROW_BYTES, *tile_late = base + (BACK ? 2 : 1) * K::ROW_BYTES;
+    unsigned char *tile_early = tile_late + STAGES * K::COL_BYTES;
     unsigned char *tile_stat = base + K::TILES;                           // stat of a tile's columns
     uint64_t *bars = reinterpret_cast<uint64_t *>(tile_stat + STAGES * K::STAT_BYTES);
-    uint64_t *a_full = bars, *full = bars + 1, *empty = full + STAGES, *s_full = empty + STAGES, *s_free = s_full + NWG,
-             *ready = s_free + NWG, *done = ready + 2 * NWG, *last = done + 2 * NWG;    // [2]
-    TcTile *info = reinterpret_cast<TcTile *>(last + 2);                  // [STAGES]
-    int *total = reinterpret_cast<int *>(info + STAGES);
-    uint32_t *slot = reinterpret_cast<uint32_t *>(total + 1);
+    uint64_t *a_full = bars, *full = bars + 1, *empty = full + STAGES, *full_early = empty + STAGES, *empty_early = full_early + EARLY;
+    uint64_t *s_full = empty_early + EARLY, *s_free = s_full + 1, *ready = s_free + 1, *done = ready + 2, *last = done + 2;
+    TcTile *info = reinterpret_cast<TcTile *>(last + 2);                  // [INFO]
+    uint32_t *slot = reinterpret_cast<uint32_t *>(info + INFO);
     volatile uint32_t *dead = slot + 1;
 
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x & 31;
@@ -226,38 +229,37 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
     const int64_t tiles = attn_column_tiles<MODE, BN>(a);
     const int64_t j0 = tiles * split / a.splits, j1 = tiles * (split + 1) / a.splits;
 
-    if (warp == NWG * 4) {
+    if (warp == HELPER) {
         tmem_alloc<K::COLS>(slot);
-    } else if (warp == NWG * 4 + 1 && lane == 0) {
+    } else if (warp == HELPER + 1 && lane == 0) {
         bar_init(a_full, 1);
         for (int i = 0; i < STAGES; ++i) {
             bar_init(full + i, 1);
             bar_init(empty + i, 1);
         }
-        for (int i = 0; i < NWG; ++i) {
-            bar_init(s_full + i, 1);
-            bar_init(s_free + i, 128);
-            bar_init(ready + 2 * i, 128);
-            bar_init(ready + 2 * i + 1, 128);
-            bar_init(done + 2 * i, 1);
-            bar_init(done + 2 * i + 1, 1);
+        for (int i = 0; i < EARLY; ++i) {
+            bar_init(full_early + i, 1);
+            bar_init(empty_early + i, 1);
         }
-        bar_init(last, 1);
-        bar_init(last + 1, 1);
+        bar_init(s_full, 1);
+        bar_init(s_free, K::ROW_THREADS);
+        for (int i = 0; i < 2; ++i) {
+            bar_init(ready + i, K::ROW_THREADS);
+            bar_init(done + i, 1);
+            bar_init(last + i, 1);
+        }
         bar_init_done();
         *dead = 0u;
-        *total = 0;
     }
     tmem_before_sync();
     __syncthreads();
     tmem_after_sync();
     const uint32_t tmem = *slot;
 
-    if (warp >= NWG * 4) {
-    fewer_registers<K::REGS_OTHER>();
-    if (warp == NWG * 4 + 1) {
-        // ------------------------------------------------ fetching
-        {
+    if (warp >= HELPER) {
+        fewer_registers<K::REGS_OTHER>();
+        if (warp == HELPER + 1) {
+            // -------------------------------------------- fetching
             int it = 0, pos = 0, head = 0;
             if (j0 < j1) attn_columns<MODE, BN>(a, w, j0, &pos, &head);
             bool ok = true;
@@ -271,17 +273,19 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
                             if (BACK) tma_load(tile_a2 + p * kTcRows * K::PITCH, &maps.a2, 64 * p, w.head, w.pos, w.b, a_full);
                         }
                     }
-                    const int st = it % STAGES;
+                    const int st = it % STAGES, se = it % EARLY;
+                    ok = it < EARLY || bar_wait_warp(empty_early + se, (it / EARLY - 1) & 1, dead, a.err);
+                    if (!ok) break;
+                    if (lane == 0) info[it % INFO] = {pos, head, cls};
+                    __syncwarp();
+                    bar_expect(full_early + se, K::COL_BYTES);
+                    for (int p = 0; p < K::PANELS; ++p)
+                        tma_load(tile_early + se * K::COL_BYTES + p * BN * K::PITCH, FIRST_EARLY ? &maps.x1 : &maps.x2, 64 * p, head, pos, w.b, full_early + se);
                     ok = it < STAGES || bar_wait_warp(empty + st, (it / STAGES - 1) & 1, dead, a.err);
                     if (!ok) break;
-                    if (lane == 0) info[st] = {pos, head, cls};
-                    __syncwarp();
-                    bar_expect(full + st, 2 * K::COL_BYTES + K::STAT_BYTES);
-                    unsigned char *x1 = tile_x + st * 2 * K::COL_BYTES, *x2 = x1 + K::COL_BYTES;
-                    for (int p = 0; p < K::PANELS; ++p) {
-                        tma_load(x1 + p * BN * K::PITCH, &maps.x1, 64 * p, head, pos, w.b, full + st);
-                        tma_load(x2 + p * BN * K::PITCH, &maps.x2, 64 * p, head, pos, w.b, full + st);
-                    }
+                    bar_expect(full + st, K::COL_BYTES + K::STAT_BYTES);
+                    for (int p = 0; p < K::PANELS; ++p)
+                        tma_load(tile_late + st * K::COL_BYTES + p * BN * K::PITCH, FIRST_EARLY ? &maps.x2 : &maps.x1, 64 * p, head, pos, w.b, full + st);
                     if (MODE == kGradKV) bulk_load(tile_stat + st * K::STAT_BYTES, attn_stat(a, w.b, head, pos), K::STAT_BYTES, full + st);
                     ++it;
                 }
@@ -291,132 +295,123 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
                     ++head;
                 }
             }
-            if (lane == 0) *total = it;
-            for (int i = it; ok && i < it + NWG; ++i) {    // each group finds an end
-                const int st = i % STAGES;
-                ok = i < STAGES || bar_wait_warp(empty + st, (i / STAGES - 1) & 1, dead, a.err);
-                if (!ok) break;
-                if (lane == 0) info[st].cls = 0;
-                __syncwarp();
-                bar_arrive_one(full + st);
+            if (ok) {                  // the end, for all
+                ok = it < EARLY || bar_wait_warp(empty_early + it % EARLY, (it / EARLY - 1) & 1, dead, a.err);
+                ok = ok && (it < STAGES || bar_wait_warp(empty + it % STAGES, (it / STAGES - 1) & 1, dead, a.err));
+                if (ok) {
+                    if (lane == 0) info[it % INFO].cls = 0;
+                    __syncwarp();
+                    bar_arrive_one(full_early + it % EARLY);
+                    bar_arrive_one(full + it % STAGES);
+                }
             }
             if (*dead) {               // copies under way end before the block does
                 uint32_t off = 0u;
-                for (int i = it < STAGES ? 0 : it - STAGES; i < it; ++i) bar_wait_warp(full + i % STAGES, (i / STAGES) & 1, &off, nullptr);
-                if (it > 0) bar_wait_warp(a_full, 0, &off, nullptr);
+                if (it > 0) bar_wait(a_full, 0, &off, nullptr);
+                for (int i = it < EARLY ? 0 : it - EARLY; i < it; ++i) bar_wait(full_early + i % EARLY, (i / EARLY) & 1, &off, nullptr);
+                for (int i = it < STAGES ? 0 : it - STAGES; i < it; ++i) bar_wait(full + i % STAGES, (i / STAGES) & 1, &off, nullptr);
             }
-        }
-        __syncwarp();
-    } else if (warp == NWG * 4) {
-        // ------------------------------------------------ scores
-        {
+        } else if (warp == HELPER) {
+            // -------------------------------------------- scores
             const int steps = (a.D + 15) / 16;
             const uint32_t a1 = desc_low(shared_at(tile_a1), 16), a2 = desc_low(shared_at(tile_a2), 16);
-            const uint32_t along = desc_low(shared_at(tile_x), 16);
+            const uint32_t late = desc_low(shared_at(tile_late), 16), early = desc_low(shared_at(tile_early), 16);
             constexpr uint32_t id = mma_desc<BF16, BN, false>(), high = desc_high<K::PITCH>();
             constexpr int per = K::PITCH / 32;      // steps of 16 channels in a panel
             bool ok = true;
             VCLKDEF
             for (int it = 0;; ++it) {
-                const int g = it % NWG, own = it / NWG, st = it % STAGES;
+                const int st = it % STAGES, se = it % EARLY;
                 VCLK(0);
-                ok = bar_wait_warp(full + st, (it / STAGES) & 1, dead, a.err);
+                ok = bar_wait_warp(full_early + se, (it / EARLY) & 1, dead, a.err);
                 VCLK(1);
                 if (!ok) break;
-                if (!info[st].cls) {
-                    VCLKP2("scores", it)
-                    // each group finds the end once it has read its last scores: before, this
-                    // would be taken for their arrival
-                    for (int i = it; ok && i < it + NWG; ++i) {
-                        if (i >= NWG) ok = K::ALIAS ? bar_wait_warp(tc_bar<K::WEIGHTS>(done, i % NWG, i / NWG - 1), tc_phase<K::WEIGHTS>(i / NWG - 1), dead, a.err)
-                                                    : bar_wait_warp(s_free + i % NWG, (i / NWG - 1) & 1, dead, a.err);
-                        if (ok) bar_arrive_one(s_full + i % NWG);
-                    }
-                    break;
-                }
-                if (it == 0) ok = bar_wait_warp(a_full, 0, dead, a.err);
-                // the columns are free: the group has read its last scores, and (ALIAS: these
-                // became weights) the weights that it will write are used
-                if (ok && !K::ALIAS && own > 0) ok = bar_wait_warp(s_free + g, (own - 1) & 1, dead, a.err);
-                if (ok && K::ALIAS && own > 0) ok = bar_wait_warp(tc_bar<K::WEIGHTS>(done, g, own - 1), tc_phase<K::WEIGHTS>(own - 1), dead, a.err);
+                const bool end = info[it % INFO].cls == 0;
+                if (!end && BACK) ok = bar_wait_warp(full + st, (it / STAGES) & 1, dead, a.err);
+                if (!end && it == 0) ok = ok && bar_wait_warp(a_full, 0, dead, a.err);
+                // the columns are free: the last scores are read, and (ALIAS: these became
+                // weights) the weights that will be written over are used
+                if (ok && !K::ALIAS && it > 0) ok = bar_wait_warp(s_free, (it - 1) & 1, dead, a.err);
+                if (ok && K::ALIAS && it > 0) ok = bar_wait_warp(tc_bar<K::WEIGHTS>(done, it - 1), tc_phase<K::WEIGHTS>(it - 1), dead, a.err);
                 VCLK(2);
-                if (ok && K::WEIGHTS == 2 && own > 1) ok = bar_wait_warp(tc_bar<K::WEIGHTS>(done, g, own - 2), tc_phase<K::WEIGHTS>(own - 2), dead, a.err);
+                if (ok && K::WEIGHTS == 2 && it > 1) ok = bar_wait_warp(tc_bar<K::WEIGHTS>(done, it - 2), tc_phase<K::WEIGHTS>(it - 2), dead, a.err);
                 if (!ok) break;
                 VCLK(3);
+                if (end) {             // not before: it would be taken for the last scores' arrival
+                    VCLKP2("scores", it)
+                    bar_arrive_one(s_full);
+                    break;
+                }
                 tmem_after_sync();
-                const uint32_t x1 = along + st * desc_step(2 * K::COL_BYTES), x2 = x1 + desc_step(K::COL_BYTES);
-                const uint32_t d = tmem + g * K::GROUP;
+                const uint32_t x_late = late + st * desc_step(K::COL_BYTES), x_early = early + se * desc_step(K::COL_BYTES);
+                const uint32_t x1 = FIRST_EARLY ? x_early : x_late, x2 = FIRST_EARLY ? x_late : x_early;
 #pragma unroll
                 for (int k = 0; k < DP / 16; ++k) {
                     if (k >= steps) break;
                     const uint32_t ra = desc_step(k / per * (kTcRows * K::PITCH) + k % per * 32), rx = desc_step(k / per * (BN * K::PITCH) + k % per * 32);
-                    mma_shared<id, high>(d, a1 + ra, x1 + rx, k > 0);
-                    if (BACK) mma_shared<id, high>(d + BN, a2 + ra, x2 + rx, k > 0);
+                    mma_shared<id, high>(tmem, a1 + ra, x1 + rx, k > 0);
+                    if (BACK) mma_shared<id, high>(tmem + BN, a2 + ra, x2 + rx, k > 0);
                 }
-                mma_commit(s_full + g);
+                if (MODE != kGradKV) mma_commit(empty_early + se);
+                mma_commit(s_full);
                 VCLK(4);
-#ifdef V_LAT
-                bar_wait_warp(s_full + g, own & 1, dead, a.err);
-                VCLK(5);
-#endif
             }
             if (!ok) {                 // MMAs under way end before the block does
                 uint32_t off = 0u;
                 mma_commit(last);
-                bar_wait_warp(last, 0, &off, nullptr);
+                bar_wait(last, 0, &off, nullptr);
             }
-        }
-        __syncwarp();
-    } else if (warp == NWG * 4 + 2) {
-        // ------------------------------------------------ second products
-        {
-            const uint32_t across = desc_low(shared_at(tile_x), BN * K::PITCH);
+        } else if (warp == HELPER + 2) {
+            // -------------------------------------------- second products
+            const uint32_t late = desc_low(shared_at(tile_late), BN * K::PITCH), early = desc_low(shared_at(tile_early), BN * K::PITCH);
             constexpr uint32_t id = mma_desc<BF16, DP, true>(), high = desc_high<K::PITCH>();
+            constexpr int PART_STEPS = K::PART / 16;
             bool ok = true;
             VCLKDEF
             for (int it = 0;; ++it) {
-                const int g = it % NWG, own = it / NWG, st = it % STAGES;
+                const int st = it % STAGES, se = it % EARLY;
                 VCLK(0);
                 ok = bar_wait_warp(full + st, (it / STAGES) & 1, dead, a.err);
                 VCLK(1);
-                if (!info[st].cls) VCLKP2("second", it)
-                if (!ok || !info[st].cls) break;
-                ok = bar_wait_warp(tc_bar<K::WEIGHTS>(ready, g, own), tc_phase<K::WEIGHTS>(own), dead, a.err);
+                if (!info[it % INFO].cls) VCLKP2("second", it)
+                if (!ok || !info[it % INFO].cls) break;
+                if (MODE == kGradKV) ok = bar_wait_warp(full_early + se, (it / EARLY) & 1, dead, a.err);
+                ok = ok && bar_wait_warp(tc_bar<K::WEIGHTS>(ready, it), tc_phase<K::WEIGHTS>(it), dead, a.err);
                 if (!ok) break;
                 VCLK(2);
                 tmem_after_sync();
-                const uint32_t x1 = across + st * desc_step(2 * K::COL_BYTES), x2 = x1 + desc_step(K::COL_BYTES);
-                const uint32_t s = tmem + g * K::GROUP, acc = tmem + K::ACC + (MODE == kForward ? g * DP : 0);
-                // weights: P, then dS
-                const uint32_t p = s + (K::ALIAS ? 0 : BN * (BACK ? 2 : 1) + (K::WEIGHTS == 2 ? own % 2 * K::WIDE : 0));
-                const uint32_t ds = MODE == kGradQ ? p : K::ALIAS ? s + BN : p + BN / 2;
-                const bool add = MODE == kForward ? own > 0 : it > 0;
+                const uint32_t x_late = late + st * desc_step(K::COL_BYTES), x_early = early + se * desc_step(K::COL_BYTES);
+                // weights: P, then dS; over the scores each part's in the part's own columns
+                const uint32_t p = tmem + (K::ALIAS ? 0 : K::SCORES + (K::WEIGHTS == 2 ? it % 2 * K::WIDE : 0));
+                const uint32_t ds = MODE == kGradQ ? p : K::ALIAS ? p + BN : p + BN / 2, acc = tmem + K::ACC;
 #pragma unroll
                 for (int k = 0; k < BN / 16; ++k) {
                     const uint32_t rx = desc_step(k * 16 * K::PITCH);
-                    if (MODE != kGradQ) mma_tmem<id, high>(acc, p + 8 * k, x2 + rx, add || k > 0);
-                    if (BACK) mma_tmem<id, high>(acc + (MODE == kGradKV ? DP : 0), ds + 8 * k, x1 + rx, add || k > 0);
+                    const uint32_t at = K::ALIAS ? k / PART_STEPS * K::PART + k % PART_STEPS * 8 : 8 * k;
+                    if (MODE == kForward) mma_tmem<id, high>(acc, p + at, x_late + rx, it > 0 || k > 0);
+                    if (MODE == kGradKV) mma_tmem<id, high>(acc, p + at, x_early + rx, it > 0 || k > 0);
+                    if (BACK) mma_tmem<id, high>(acc + (MODE == kGradKV ? DP : 0), ds + at, x_late + rx, it > 0 || k > 0);
                 }
+                if (MODE == kGradKV) mma_commit(empty_early + se);
                 mma_commit(empty + st);
-                mma_commit(tc_bar<K::WEIGHTS>(done, g, own));  // last: the block ends after it has arrived
+                mma_commit(tc_bar<K::WEIGHTS>(done, it));  // last: the block ends after it has arrived
                 VCLK(4);
             }
             if (!ok) {
                 uint32_t off = 0u;
                 mma_commit(last + 1);
-                bar_wait_warp(last + 1, 0, &off, nullptr);
+                bar_wait(last + 1, 0, &off, nullptr);
             }
         }
         __syncwarp();
-    }
     } else {
         more_registers<K::REGS_ROW>();
         // ------------------------------------------------ one row a thread
-        const int g = warp / 4, r = threadIdx.x % 128;
+        const int part = warp / 4, r = threadIdx.x % 128;  // columns PART part on of each tile
         const bool valid = w.valid(r);
         const bool any_valid = w.valid(r & ~31);           // of this warp's rows
-        const uint32_t mine = tmem + ((uint32_t)(r & ~31) << 16) + g * K::GROUP;
-        const uint32_t at_acc = tmem + ((uint32_t)(r & ~31) << 16) + K::ACC + (MODE == kForward ? g * DP : 0);
+        const uint32_t mine = tmem + ((uint32_t)(r & ~31) << 16), at_acc = mine + K::ACC;
+        constexpr int PART = K::PART;
         const int rpos = w.row_pos(valid ? r : 0), rhead = w.row_head(valid ? r : 0);
         const float c = a.c;
         float ds_scale = 1.0f;
@@ -433,48 +428,48 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
         // after a wait that ran out (ok false) the group's threads go on to their results'
         // barriers
         VCLKDEF
-        int own = 0;                   // tiles of this group
         bool ok = true;
-        for (int it = g;; it += NWG, ++own) {
+        int it = 0;
+        for (;; ++it) {
             const int st = it % STAGES;
-            const uint32_t at_p = mine + (K::ALIAS ? 0 : BN * (BACK ? 2 : 1) + (K::WEIGHTS == 2 ? own % 2 * K::WIDE : 0));
-            const uint32_t at_ds = MODE == kGradQ ? at_p : K::ALIAS ? mine + BN : at_p + BN / 2;
+            const uint32_t at_p = mine + (K::ALIAS ? PART * part : K::SCORES + (K::WEIGHTS == 2 ? it % 2 * K::WIDE : 0) + PART / 2 * part);
+            const uint32_t at_ds = MODE == kGradQ ? at_p : K::ALIAS ? at_p + BN : at_p + BN / 2;
             // a mask's words are asked for before the scores are there
+            // (their tile's barrier moves on only after this tile's second product)
             if (a.classes) ok = bar_wait_warp(full + st, (it / STAGES) & 1, dead, a.err);
-            else ok = bar_wait_warp(s_full + g, own & 1, dead, a.err);
+            else ok = bar_wait_warp(s_full, it & 1, dead, a.err);
             if (!ok) break;
-            const TcTile tile = info[st];
+            const TcTile tile = info[it % INFO];
             const int cls = tile.cls;
             if (!cls) break;
-            uint32_t bits[BN / 32];
+            uint32_t bits[PART / 32];
             if (cls != 2) {
                 if (MODE == kGradKV) words = attn_word_row<MODE>(a, w.b, tile.head, rpos);
 #pragma unroll
-                for (int i = 0; i < BN / 32; ++i) bits[i] = attn_word<MODE>(a, words, tile.pos + 32 * i);
+                for (int i = 0; i < PART / 32; ++i) bits[i] = attn_word<MODE>(a, words, tile.pos + PART * part + 32 * i);
             }
             VCLK(0);
-            if (a.classes) ok = bar_wait_warp(s_full + g, own & 1, dead, a.err);
+            if (a.classes) ok = bar_wait_warp(s_full, it & 1, dead, a.err);
             if (!ok) break;
             tmem_after_sync();
             VCLK(1);
-            // the row's scores, then dP
-            constexpr int HELD = BACK ? 2 * BN : BN;
-            uint32_t v[HELD];
+            uint32_t v[PART], dp[BACK ? PART : 1];         // the row's scores, and dP
             if (any_valid) {
-                tmem_read<HELD>(v, mine);
+                if constexpr (BACK) tmem_read_two<PART>(v, dp, mine + PART * part, mine + BN + PART * part);
+                else tmem_read<PART>(v, mine);
             }
             VCLK(2);
             if (!K::ALIAS) {
                 tmem_before_sync();
-                bar_arrive(s_free + g);
+                bar_arrive(s_free);
             }
             if (cls != 2) {            // p, and with it ds unless dP is not finite, will be 0
 #pragma unroll
-                for (int k = 0; k < BN; ++k)
+                for (int k = 0; k < PART; ++k)
                     if (!((bits[k / 32] >> (k % 32)) & 1u)) v[k] = 0xff800000u;
             }
-            if (K::WEIGHTS == 1 && own > 0) {  // the weights' columns are free
-                ok = bar_wait_warp(tc_bar<K::WEIGHTS>(done, g, own - 1), tc_phase<K::WEIGHTS>(own - 1), dead, a.err);
+            if (K::WEIGHTS == 1 && it > 0) {   // the weights' columns are free
+                ok = bar_wait_warp(tc_bar<K::WEIGHTS>(done, it - 1), tc_phase<K::WEIGHTS>(it - 1), dead, a.err);
                 if (!ok) break;
                 tmem_after_sync();
             }
@@ -493,8 +488,8 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
                     const float f = !grow ? 1.0f : top == -INFINITY ? 0.0f : ex2((top - high) * c);
                     if (grow) top = high;
                     sum *= f;
-                    if (own > 0) {
-                        ok = bar_wait_warp(tc_bar<K::WEIGHTS>(done, g, own - 1), tc_phase<K::WEIGHTS>(own - 1), dead, a.err);
+                    if (it > 0) {
+                        ok = bar_wait_warp(tc_bar<K::WEIGHTS>(done, it - 1), tc_phase<K::WEIGHTS>(it - 1), dead, a.err);
                         tmem_after_sync();
 #pragma unroll 1
                         for (int i = 0; ok && i < DP; i += 16) {
@@ -525,11 +520,11 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
                 sum += (sums[0].x + sums[1].x) + (sums[0].y + sums[1].y);
             }
             if (any_valid && BACK) {
-                const unsigned char *cs = tile_stat + st * K::STAT_BYTES;
+                const unsigned char *cs = tile_stat + st * K::STAT_BYTES + 8 * PART * part;
                 const float2 one = make_float2(ds_scale, ds_scale);
                 float2 l2 = make_float2(lse2, lse2), e2 = make_float2(delta, delta);
 #pragma unroll
-                for (int i = 0; i < BN; i += 32) {
+                for (int i = 0; i < PART; i += 32) {
                     uint32_t out[16], out2[16];
 #pragma unroll
                     for (int k = i; k < i + 32; k += 2) {
@@ -540,7 +535,7 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
                         }
                         const float2 x = __ffma2_rn(make_float2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), c2, l2);
                         const float2 p = make_float2(ex2(x.x), ex2(x.y));
-                        float2 d = __fmul2_rn(p, __fadd2_rn(make_float2(__uint_as_float(v[BN + k]), __uint_as_float(v[BN + k + 1])), e2));
+                        float2 d = __fmul2_rn(p, __fadd2_rn(make_float2(__uint_as_float(dp[k]), __uint_as_float(dp[k + 1])), e2));
                         if (!BF16) d = __fmul2_rn(d, one);
                         out[k % 32 / 2] = pack2<T>(p.x, p.y);
                         out2[k % 32 / 2] = pack2<T>(d.x, d.y);
@@ -553,25 +548,16 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
             if (!ok) break;
             if (any_valid) tmem_wait_store();
             tmem_before_sync();
-            bar_arrive(tc_bar<K::WEIGHTS>(ready, g, own));
+            bar_arrive(tc_bar<K::WEIGHTS>(ready, it));
             VCLK(6);
         }
 
         VCLKPRINT
         // ------------------------------------------------ results
-        if (ok && own > 0) ok = bar_wait_warp(tc_bar<K::WEIGHTS>(done, g, own - 1), tc_phase<K::WEIGHTS>(own - 1), dead, a.err);
+        if (ok && it > 0) ok = bar_wait_warp(tc_bar<K::WEIGHTS>(done, it - 1), tc_phase<K::WEIGHTS>(it - 1), dead, a.err);
         tmem_after_sync();
-        const int count = *total;      // column tiles of the block
-        if (NWG > 1) {                 // the other groups' are done too
-            tmem_before_sync();
-            asm volatile("bar.sync 7, %0;" ::"n"(NWG * 128) : "memory");
-            tmem_after_sync();
-        }
-        // the first group has the first results of the rows, the second the others (kGradKV)
-        const bool here = any_valid && __all_sync(0xffffffffu, ok && !*dead) && (g == 0 || MODE == kGradKV);
-        if (here) {
-            constexpr int RESULTS = MODE == kGradKV ? 2 : 1;
-            const uint32_t acc0 = tmem + ((uint32_t)(r & ~31) << 16) + K::ACC;
+        const int count = it;          // column tiles of the block
+        if (any_valid && __all_sync(0xffffffffu, ok && !*dead)) {
             const int64_t row = MODE == kGradKV ? ((int64_t)w.b * a.S + rpos) * a.N + rhead : ((int64_t)w.b * a.Q + rpos) * a.M + rhead;
             const float ref = top == -INFINITY ? -up : top * c - up;
             const float down = BACK ? ex2(-TcScale<T>::backward) : 1.0f;   // of P; of dS also 1 / ds_scale
@@ -587,26 +573,30 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
             }
             const float over = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
-            for (int which = 0; which < RESULTS; ++which) {
-                if (NWG > 1 && MODE == kGradKV && which != g) continue;
+            for (int which = 0; which < K::RESULTS; ++which) {
+                // of two groups one has each of a key's gradients, or half of dq's channels
+                if (K::PARTS > 1 && MODE == kGradKV && which != part) continue;
+                constexpr int CHUNKS = MODE == kGradQ && K::PARTS > 1 && DP >= 64 ? DP / 32 / K::PARTS : DP / 32;
+                const int c0 = CHUNKS * 32 < DP ? part * CHUNKS : 0;
+                if (MODE == kGradQ && CHUNKS * 32 == DP && part > 0) continue;
                 const float g_ = MODE == kForward ? 1.0f : MODE == kGradQ || which ? down_ds : down;
                 const float f = MODE == kForward ? over : g_ * (MODE == kGradQ || which ? a.scale : 1.0f);
                 bool finite = true;
                 if (a.classes && count > 0) {
 #pragma unroll
-                    for (int i = 0; i < DP / 32; ++i) {
+                    for (int i = c0; i < c0 + CHUNKS; ++i) {
                         uint32_t o[32];
-                        tmem_read<32>(o, acc0 + which * DP + 32 * i);
+                        tmem_read<32>(o, at_acc + which * DP + 32 * i);
 #pragma unroll
                         for (int k = 0; k < 32; ++k) finite = finite && isfinite(__uint_as_float(o[k]));
                     }
                 }
 #pragma unroll
-                for (int i = 0; i < DP / 32; ++i) {
+                for (int i = c0; i < c0 + CHUNKS; ++i) {
                     uint32_t o[32];
                     float v[32];
                     if (count > 0) {
-                        tmem_read<32>(o, acc0 + which * DP + 32 * i);
+                        tmem_read<32>(o, at_acc + which * DP + 32 * i);
                     }
 #pragma unroll
                     for (int k = 0; k < 32; ++k) v[k] = count > 0 ? __uint_as_float(o[k]) : 0.0f;
@@ -622,7 +612,7 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int d = lane + 32 * i;
-                        if (d < a.D)
+                        if (d < a.D && d / 32 >= c0 && d / 32 < c0 + CHUNKS)
                             attn_store<T, MODE>(a, w, (r & ~31) + from, split, which, d, MODE == kGradQ || which ? e2[i] : e1[i],
                                                 MODE == kForward ? o : MODE == kGradQ || which ? a.scale : 1.0f);
                     }
@@ -632,7 +622,7 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
         tmem_before_sync();
     }
     __syncthreads();
-    if (warp == NWG * 4) {
+    if (warp == HELPER) {
         tmem_after_sync();
         tmem_free<K::COLS>(tmem);
     }

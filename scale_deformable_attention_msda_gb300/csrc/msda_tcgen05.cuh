@@ -132,15 +132,24 @@ template <> __device__ __forceinline__ void tmem_read<64>(uint32_t (&v)[64], uin
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x64.b32 {" TMEM_R0 "," TMEM_R1 "," TMEM_R2 "," TMEM_R3 "}, [%64];\n\t" TMEM_WAIT
                  : TMEM_OUT32(0), TMEM_OUT32(32) : "r"(at) : "memory");
 }
-template <> __device__ __forceinline__ void tmem_read<96>(uint32_t (&v)[96], uint32_t at) {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x64.b32 {" TMEM_R0 "," TMEM_R1 "," TMEM_R2 "," TMEM_R3 "}, [%96];\n\t"
-                 "tcgen05.ld.sync.aligned.32x32b.x32.b32 {" TMEM_R4 "," TMEM_R5 "}, [%97];\n\t" TMEM_WAIT
-                 : TMEM_OUT32(0), TMEM_OUT32(32), TMEM_OUT32(64) : "r"(at), "r"(at + 64) : "memory");
-}
 template <> __device__ __forceinline__ void tmem_read<128>(uint32_t (&v)[128], uint32_t at) {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x64.b32 {" TMEM_R0 "," TMEM_R1 "," TMEM_R2 "," TMEM_R3 "}, [%128];\n\t"
                  "tcgen05.ld.sync.aligned.32x32b.x64.b32 {" TMEM_R4 "," TMEM_R5 "," TMEM_R6 "," TMEM_R7 "}, [%129];\n\t" TMEM_WAIT
                  : TMEM_OUT32(0), TMEM_OUT32(32), TMEM_OUT32(64), TMEM_OUT32(96) : "r"(at), "r"(at + 64) : "memory");
+}
+// Two ranges of N columns each.
+template <int N> __device__ __forceinline__ void tmem_read_two(uint32_t (&v)[N], uint32_t (&w)[N], uint32_t at, uint32_t at2);
+#define TMEM_OUT8W(o) "=&r"(w[o]), "=&r"(w[o + 1]), "=&r"(w[o + 2]), "=&r"(w[o + 3]), "=&r"(w[o + 4]), "=&r"(w[o + 5]), "=&r"(w[o + 6]), "=&r"(w[o + 7])
+#define TMEM_OUT32W(o) TMEM_OUT8W(o), TMEM_OUT8W(o + 8), TMEM_OUT8W(o + 16), TMEM_OUT8W(o + 24)
+template <> __device__ __forceinline__ void tmem_read_two<64>(uint32_t (&v)[64], uint32_t (&w)[64], uint32_t at, uint32_t at2) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x64.b32 {" TMEM_R0 "," TMEM_R1 "," TMEM_R2 "," TMEM_R3 "}, [%128];\n\t"
+                 "tcgen05.ld.sync.aligned.32x32b.x64.b32 {" TMEM_R4 "," TMEM_R5 "," TMEM_R6 "," TMEM_R7 "}, [%129];\n\t" TMEM_WAIT
+                 : TMEM_OUT32(0), TMEM_OUT32(32), TMEM_OUT32W(0), TMEM_OUT32W(32) : "r"(at), "r"(at2) : "memory");
+}
+template <> __device__ __forceinline__ void tmem_read_two<32>(uint32_t (&v)[32], uint32_t (&w)[32], uint32_t at, uint32_t at2) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {" TMEM_R0 "," TMEM_R1 "}, [%64];\n\t"
+                 "tcgen05.ld.sync.aligned.32x32b.x32.b32 {" TMEM_R2 "," TMEM_R3 "}, [%65];\n\t" TMEM_WAIT
+                 : TMEM_OUT32(0), TMEM_OUT32W(0) : "r"(at), "r"(at2) : "memory");
 }
 __device__ __forceinline__ void tmem_store16(uint32_t at, const uint32_t (&v)[16]) {
     asm volatile(
