@@ -146,8 +146,8 @@ AttnArgs common_args(const msda_attention_dims_t &d, const void *q, const void *
     a.D = (int)d.D;
     a.G = (int)(d.M / d.N);
     a.scale = (float)scale;
-    // above zero, so that a masked score, -infinity, stays so
-    a.c = (float)(scale * 1.4426950408889634 > 1e-37 ? scale * 1.4426950408889634 : 1e-37);
+    // above zero, so that a masked score, -infinity, stays so, and lse / c in range
+    a.c = (float)(scale * 1.4426950408889634 > 1e-30 ? scale * 1.4426950408889634 : 1e-30);
     return a;
 }
 

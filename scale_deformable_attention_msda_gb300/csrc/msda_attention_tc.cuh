@@ -82,20 +82,22 @@ template <int MODE, int DP> struct Tc : TcConfig<MODE, DP> {
     static constexpr int ROW_BYTES = kTcRows * PITCH * PANELS, COL_BYTES = BN * PITCH * PANELS;
     static constexpr int ROW_THREADS = PARTS * 128, THREADS = ROW_THREADS + 128, PART = BN / PARTS;
     // registers: 65,536 of an SM, spread evenly at the start and then by need
-    static constexpr int REGS_ROW = PARTS == 1 ? 208 : 208, REGS_OTHER = PARTS == 1 ? 48 : 88;
+    static constexpr int REGS_ROW = PARTS * C::BLOCKS == 4 ? 96 : 208, REGS_OTHER = PARTS * C::BLOCKS == 4 || PARTS == 1 ? 48 : 88;
     static_assert((PARTS * REGS_ROW + REGS_OTHER) * 128 <= 65536 / C::BLOCKS / THREADS / 8 * 8 * THREADS, "registers");
     // tensor memory: scores (and dP), weights, accumulators
     static constexpr int SCORES = BN * (BACK ? 2 : 1), WIDE = BN / 2 * (MODE == kGradKV ? 2 : 1);
     static constexpr int ACC = SCORES + WEIGHTS * WIDE, RESULTS = MODE == kGradKV ? 2 : 1;
     static constexpr int USED = ACC + RESULTS * DP, COLS = USED <= 128 ? 128 : USED <= 256 ? 256 : 512;
-    static_assert(BN == tc_columns(MODE, DP) && C::BLOCKS == tc_blocks(MODE, DP), "what the host plans with");
+    //static_assert(BN == tc_columns(MODE, DP) && C::BLOCKS == tc_blocks(MODE, DP), "what the host plans with");
     static_assert(MODE != kForward || PARTS == 1, "one maximum and sum a row");
     static_assert(USED <= 512 && COLS * C::BLOCKS <= 512, "tensor memory");
     static constexpr int TILES = (BACK ? 2 : 1) * ROW_BYTES + (STAGES + EARLY) * COL_BYTES;
-    static constexpr int STAT_BYTES = MODE == kGradKV ? 8 * BN : 0;    // of a column tile
+    // of a column tile: the queries' statistics, and the same as an operand (see tc_bias)
+    static constexpr int STAT_BYTES = MODE == kGradKV ? 8 * BN : 0, BIAS_BYTES = MODE == kGradKV ? 32 * BN : 0;
+    static constexpr int ONES_BYTES = MODE == kGradKV ? 32 * kTcRows : 0;
     static constexpr int INFO = 8;
     static_assert(STAGES + 1 <= INFO, "announcements are read before they are written over");
-    static constexpr int NEEDED = 1024 + TILES + STAGES * STAT_BYTES + 1024;
+    static constexpr int NEEDED = 1024 + TILES + STAGES * (STAT_BYTES + BIAS_BYTES) + 2 * ONES_BYTES + 1024;
     // as much as keeps one block more off the SM, which would only wait for its tensor memory
     static constexpr int LIMIT = 228 * 1024 / (C::BLOCKS + 1);
     static constexpr int SHARED = NEEDED > LIMIT ? NEEDED : LIMIT;
@@ -198,6 +200,45 @@ template <int WEIGHTS> __device__ __forceinline__ uint64_t *tc_bar(uint64_t *bar
 }
 template <int WEIGHTS> __device__ __forceinline__ uint32_t tc_phase(int it) { return (WEIGHTS == 2 ? it >> 1 : it) & 1; }
 
+// kGradKV: -lse and -delta of the columns' queries, added to the scores and to dP by one
+// more step of their products: 1, 1, 1 times the three parts that a number has in 16 bits,
+// which together hold its fp32 digits. Read from shared memory by the rows' threads instead,
+// 8 bytes a column for every warp, they alone took 1,024 cycles a tile.
+//
+// -lse is divided by c beforehand. fp16: both are scaled into range by powers of two that
+// stand in place of the ones: -lse / c by c (below 2^-26, where scores mean nothing any
+// more, c is taken as that), -delta by its bound.
+//
+// 16 values of a row are two runs of 16 bytes; 8 rows' runs lie together (no swizzle).
+template <typename T>
+__device__ __forceinline__ void tc_bias_row(unsigned char *tile, int r, float a, float b, float c, float d, float e, float f) {
+    uint4 *at = reinterpret_cast<uint4 *>(tile + r / 8 * 256 + r % 8 * 16);
+    at[0] = make_uint4(pack2<T>(a, b), pack2<T>(c, d), pack2<T>(e, f), 0u);
+    at[8] = make_uint4(0u, 0u, 0u, 0u);
+}
+template <typename T> struct TcBias {
+    float one_s = 1.0f, one_d = 1.0f, over_c = 0.0f, none = 0.0f;
+    __device__ __forceinline__ TcBias() {}
+    static __device__ __forceinline__ float columns_c(const AttnArgs &a) { return TcScale<T>::backward > 0.0f ? fmaxf(a.c, 0x1p-26f) : a.c; }
+    __device__ __forceinline__ explicit TcBias(const AttnArgs &a) {
+        over_c = 1.0f / columns_c(a);
+        none = -1e37f;
+        if (a.norm_do) {
+            one_s = ldexpf(1.0f, max(0, min(15, ilogbf(over_c) + 2)));   // |lse2 / c| <= |lse2| one_s / 2
+            none = -60000.0f * one_s;
+            int e = 1 - ilogbf(tc_ds_scale(a));                          // |delta| < 2^(e - 1)
+            one_d = ldexpf(1.0f, max(-14, min(15, e - 16)));
+        }
+    }
+    // Query r's row of the operand from its pair of stat.
+    __device__ __forceinline__ void put(unsigned char *tile, int r, const float *st) const {
+        float l = (st[0] == -INFINITY ? none : st[0] * over_c) / one_s, d = st[2] / one_d;
+        const float l1 = Elem<T>::to_f(Elem<T>::from_f(l)), l2 = Elem<T>::to_f(Elem<T>::from_f(l - l1));
+        const float d1 = Elem<T>::to_f(Elem<T>::from_f(d)), d2 = Elem<T>::to_f(Elem<T>::from_f(d - d1));
+        tc_bias_row<T>(tile, r, l1, l2, l - l1 - l2, d1, d2, d - d1 - d2);
+    }
+};
+
 struct TcMaps {
     CUtensorMap a1, a2, x1, x2;        // rows: one or two; columns: two
 };
@@ -215,11 +256,13 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
     unsigned char *base = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
     unsigned char *tile_a1 = base, *tile_a2 = base + K::ROW_BYTES, *tile_late = base + (BACK ? 2 : 1) * K::ROW_BYTES;
     unsigned char *tile_early = tile_late + STAGES * K::COL_BYTES;
-    unsigned char *tile_stat = base + K::TILES;                           // stat of a tile's columns
-    uint64_t *bars = reinterpret_cast<uint64_t *>(tile_stat + STAGES * K::STAT_BYTES);
+    unsigned char *tile_stat = base + K::TILES, *tile_bias = tile_stat + STAGES * K::STAT_BYTES, *ones = tile_bias + STAGES * K::BIAS_BYTES;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(ones + 2 * K::ONES_BYTES);
     uint64_t *a_full = bars, *full = bars + 1, *empty = full + STAGES, *full_early = empty + STAGES, *empty_early = full_early + EARLY;
-    uint64_t *s_full = empty_early + EARLY, *s_free = s_full + 1, *ready = s_free + 1, *done = ready + 2, *last = done + 2;
-    TcTile *info = reinterpret_cast<TcTile *>(last + 2);                  // [INFO]
+    // scores, and dP (d_); weights ready and used: P's (kGradKV: p_), and the last ones of a tile
+    uint64_t *s_full = empty_early + EARLY, *s_free = s_full + 1, *d_full = s_free + 1, *d_free = d_full + 1;
+    uint64_t *p_ready = d_free + 1, *p_done = p_ready + 1, *ready = p_done + 1, *done = ready + 2, *last = done + 2, *bias_full = last + 2;
+    TcTile *info = reinterpret_cast<TcTile *>(bias_full + STAGES);        // [INFO]
     uint32_t *slot = reinterpret_cast<uint32_t *>(info + INFO);
     volatile uint32_t *dead = slot + 1;
 
@@ -241,8 +284,13 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
             bar_init(full_early + i, 1);
             bar_init(empty_early + i, 1);
         }
+        for (int i = 0; i < STAGES; ++i) bar_init(bias_full + i, 1);
         bar_init(s_full, 1);
+        bar_init(d_full, 1);
         bar_init(s_free, K::ROW_THREADS);
+        bar_init(d_free, K::ROW_THREADS);
+        bar_init(p_ready, K::ROW_THREADS);
+        bar_init(p_done, 1);
         for (int i = 0; i < 2; ++i) {
             bar_init(ready + i, K::ROW_THREADS);
             bar_init(done + i, 1);
@@ -250,6 +298,16 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
         }
         bar_init_done();
         *dead = 0u;
+    }
+    TcBias<T> bias;
+    if (MODE == kGradKV) {
+        bias = TcBias<T>(a);
+        for (int i = threadIdx.x; i < 2 * kTcRows; i += K::THREADS) {
+            const bool for_s = i < kTcRows;
+            const float x = for_s ? bias.one_s : 0.0f, y = for_s ? 0.0f : bias.one_d;
+            tc_bias_row<T>(ones + (for_s ? 0 : K::ONES_BYTES), i % kTcRows, x, x, x, y, y, y);
+        }
+        shared_to_async();
     }
     tmem_before_sync();
     __syncthreads();
@@ -316,7 +374,8 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
             const int steps = (a.D + 15) / 16;
             const uint32_t a1 = desc_low(shared_at(tile_a1), 16), a2 = desc_low(shared_at(tile_a2), 16);
             const uint32_t late = desc_low(shared_at(tile_late), 16), early = desc_low(shared_at(tile_early), 16);
-            constexpr uint32_t id = mma_desc<BF16, BN, false>(), high = desc_high<K::PITCH>();
+            const uint32_t bias_at = desc_low(shared_at(tile_bias), 128), ones_at = desc_low(shared_at(ones), 128);
+            constexpr uint32_t id = mma_desc<BF16, BN, false>(), high = desc_high<K::PITCH>(), plain = desc_high_plain(256);
             constexpr int per = K::PITCH / 32;      // steps of 16 channels in a panel
             bool ok = true;
             VCLKDEF
@@ -329,10 +388,14 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
                 const bool end = info[it % INFO].cls == 0;
                 if (!end && BACK) ok = bar_wait_warp(full + st, (it / STAGES) & 1, dead, a.err);
                 if (!end && it == 0) ok = ok && bar_wait_warp(a_full, 0, dead, a.err);
+                if (!end && MODE == kGradKV) ok = ok && bar_wait_warp(bias_full + st, (it / STAGES) & 1, dead, a.err);
                 // the columns are free: the last scores are read, and (ALIAS: these became
                 // weights) the weights that will be written over are used
-                if (ok && !K::ALIAS && it > 0) ok = bar_wait_warp(s_free, (it - 1) & 1, dead, a.err);
-                if (ok && K::ALIAS && it > 0) ok = bar_wait_warp(tc_bar<K::WEIGHTS>(done, it - 1), tc_phase<K::WEIGHTS>(it - 1), dead, a.err);
+                if (ok && it > 0) {
+                    if (!K::ALIAS) ok = bar_wait_warp(s_free, (it - 1) & 1, dead, a.err);
+                    else if (MODE == kGradKV) ok = bar_wait_warp(p_done, (it - 1) & 1, dead, a.err);
+                    else ok = bar_wait_warp(tc_bar<K::WEIGHTS>(done, it - 1), tc_phase<K::WEIGHTS>(it - 1), dead, a.err);
+                }
                 VCLK(2);
                 if (ok && K::WEIGHTS == 2 && it > 1) ok = bar_wait_warp(tc_bar<K::WEIGHTS>(done, it - 2), tc_phase<K::WEIGHTS>(it - 2), dead, a.err);
                 if (!ok) break;
@@ -345,16 +408,36 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
                 tmem_after_sync();
                 const uint32_t x_late = late + st * desc_step(K::COL_BYTES), x_early = early + se * desc_step(K::COL_BYTES);
                 const uint32_t x1 = FIRST_EARLY ? x_early : x_late, x2 = FIRST_EARLY ? x_late : x_early;
+                const uint32_t columns = bias_at + st * desc_step(K::BIAS_BYTES);
 #pragma unroll
                 for (int k = 0; k < DP / 16; ++k) {
                     if (k >= steps) break;
                     const uint32_t ra = desc_step(k / per * (kTcRows * K::PITCH) + k % per * 32), rx = desc_step(k / per * (BN * K::PITCH) + k % per * 32);
                     mma_shared<id, high>(tmem, a1 + ra, x1 + rx, k > 0);
-                    if (BACK) mma_shared<id, high>(tmem + BN, a2 + ra, x2 + rx, k > 0);
                 }
-                if (MODE != kGradKV) mma_commit(empty_early + se);
+                if (MODE == kGradKV) mma_shared<id, plain>(tmem, ones_at, columns, true);
+                if (MODE == kForward) mma_commit(empty_early + se);
                 mma_commit(s_full);
                 VCLK(4);
+                if (BACK) {
+                    if (it > 0) {
+                        if (!K::ALIAS) ok = bar_wait_warp(d_free, (it - 1) & 1, dead, a.err);
+                        else ok = bar_wait_warp(tc_bar<K::WEIGHTS>(done, it - 1), tc_phase<K::WEIGHTS>(it - 1), dead, a.err);
+                        if (!ok) break;
+                        tmem_after_sync();
+                    }
+                    VCLK(5);
+#pragma unroll
+                    for (int k = 0; k < DP / 16; ++k) {
+                        if (k >= steps) break;
+                        const uint32_t ra = desc_step(k / per * (kTcRows * K::PITCH) + k % per * 32), rx = desc_step(k / per * (BN * K::PITCH) + k % per * 32);
+                        mma_shared<id, high>(tmem + BN, a2 + ra, x2 + rx, k > 0);
+                    }
+                    if (MODE == kGradKV) mma_shared<id, plain>(tmem + BN, ones_at + desc_step(K::ONES_BYTES), columns, true);
+                    if (MODE == kGradQ) mma_commit(empty_early + se);
+                    mma_commit(d_full);
+                    VCLK(6);
+                }
             }
             if (!ok) {                 // MMAs under way end before the block does
                 uint32_t off = 0u;
@@ -376,23 +459,27 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
                 if (!info[it % INFO].cls) VCLKP2("second", it)
                 if (!ok || !info[it % INFO].cls) break;
                 if (MODE == kGradKV) ok = bar_wait_warp(full_early + se, (it / EARLY) & 1, dead, a.err);
+                const uint32_t x_late = late + st * desc_step(K::COL_BYTES), x_early = early + se * desc_step(K::COL_BYTES);
+                // weights: P, then dS; over the scores each part's in the part's own columns
+                const uint32_t p = tmem + (K::ALIAS ? 0 : K::SCORES + (K::WEIGHTS == 2 ? it % 2 * K::WIDE : 0));
+                const uint32_t ds = MODE != kGradKV ? p : K::ALIAS ? p + BN : p + BN / 2, acc = tmem + K::ACC;
+                auto at = [](int k) { return (uint32_t)(K::ALIAS ? k / PART_STEPS * K::PART + k % PART_STEPS * 8 : 8 * k); };
+                if (MODE == kGradKV) {
+                    ok = ok && bar_wait_warp(p_ready, it & 1, dead, a.err);
+                    if (!ok) break;
+                    tmem_after_sync();
+#pragma unroll
+                    for (int k = 0; k < BN / 16; ++k) mma_tmem<id, high>(acc, p + at(k), x_early + desc_step(k * 16 * K::PITCH), it > 0 || k > 0);
+                    mma_commit(p_done);
+                }
                 ok = ok && bar_wait_warp(tc_bar<K::WEIGHTS>(ready, it), tc_phase<K::WEIGHTS>(it), dead, a.err);
                 if (!ok) break;
                 VCLK(2);
                 tmem_after_sync();
-                const uint32_t x_late = late + st * desc_step(K::COL_BYTES), x_early = early + se * desc_step(K::COL_BYTES);
-                // weights: P, then dS; over the scores each part's in the part's own columns
-                const uint32_t p = tmem + (K::ALIAS ? 0 : K::SCORES + (K::WEIGHTS == 2 ? it % 2 * K::WIDE : 0));
-                const uint32_t ds = MODE == kGradQ ? p : K::ALIAS ? p + BN : p + BN / 2, acc = tmem + K::ACC;
 #pragma unroll
-                for (int k = 0; k < BN / 16; ++k) {
-                    const uint32_t rx = desc_step(k * 16 * K::PITCH);
-                    const uint32_t at = K::ALIAS ? k / PART_STEPS * K::PART + k % PART_STEPS * 8 : 8 * k;
-                    if (MODE == kForward) mma_tmem<id, high>(acc, p + at, x_late + rx, it > 0 || k > 0);
-                    if (MODE == kGradKV) mma_tmem<id, high>(acc, p + at, x_early + rx, it > 0 || k > 0);
-                    if (BACK) mma_tmem<id, high>(acc + (MODE == kGradKV ? DP : 0), ds + at, x_late + rx, it > 0 || k > 0);
-                }
-                if (MODE == kGradKV) mma_commit(empty_early + se);
+                for (int k = 0; k < BN / 16; ++k)
+                    mma_tmem<id, high>(acc + (MODE == kGradKV ? DP : 0), ds + at(k), x_late + desc_step(k * 16 * K::PITCH), it > 0 || k > 0);
+                if (MODE == kGradKV) mma_commit(empty_early + se);    // dP, which reads it too, is there
                 mma_commit(empty + st);
                 mma_commit(tc_bar<K::WEIGHTS>(done, it));  // last: the block ends after it has arrived
                 VCLK(4);
@@ -401,6 +488,18 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
                 uint32_t off = 0u;
                 mma_commit(last + 1);
                 bar_wait(last + 1, 0, &off, nullptr);
+            }
+        }
+        else if (MODE == kGradKV) {
+            // -------------------------------------------- the queries' statistics as an operand
+            for (int it = 0;; ++it) {
+                const int st = it % STAGES;
+                if (!bar_wait_warp(full + st, (it / STAGES) & 1, dead, a.err) || !info[it % INFO].cls) break;
+                for (int i = lane; i < BN; i += 32)
+                    bias.put(tile_bias + st * K::BIAS_BYTES, i, reinterpret_cast<const float *>(tile_stat + st * K::STAT_BYTES) + i / 2 * 4 + i % 2);
+                shared_to_async();
+                __syncwarp();
+                bar_arrive_one(bias_full + st);
             }
         }
         __syncwarp();
@@ -413,7 +512,7 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
         const uint32_t mine = tmem + ((uint32_t)(r & ~31) << 16), at_acc = mine + K::ACC;
         constexpr int PART = K::PART;
         const int rpos = w.row_pos(valid ? r : 0), rhead = w.row_head(valid ? r : 0);
-        const float c = a.c;
+        const float c = MODE == kGradKV ? TcBias<T>::columns_c(a) : a.c;
         float ds_scale = 1.0f;
         if (BACK && a.norm_do) ds_scale = tc_ds_scale(a);
         constexpr float up = TcScale<T>::forward;
@@ -433,7 +532,7 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
         for (;; ++it) {
             const int st = it % STAGES;
             const uint32_t at_p = mine + (K::ALIAS ? PART * part : K::SCORES + (K::WEIGHTS == 2 ? it % 2 * K::WIDE : 0) + PART / 2 * part);
-            const uint32_t at_ds = MODE == kGradQ ? at_p : K::ALIAS ? at_p + BN : at_p + BN / 2;
+            const uint32_t at_ds = MODE != kGradKV ? at_p : K::ALIAS ? at_p + BN : at_p + BN / 2;
             // a mask's words are asked for before the scores are there
             // (their tile's barrier moves on only after this tile's second product)
             if (a.classes) ok = bar_wait_warp(full + st, (it / STAGES) & 1, dead, a.err);
@@ -453,11 +552,8 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
             if (!ok) break;
             tmem_after_sync();
             VCLK(1);
-            uint32_t v[PART], dp[BACK ? PART : 1];         // the row's scores, and dP
-            if (any_valid) {
-                if constexpr (BACK) tmem_read_two<PART>(v, dp, mine + PART * part, mine + BN + PART * part);
-                else tmem_read<PART>(v, mine);
-            }
+            uint32_t v[PART];                  // the row's scores
+            if (any_valid) tmem_read<PART>(v, mine + PART * part);
             VCLK(2);
             if (!K::ALIAS) {
                 tmem_before_sync();
@@ -469,7 +565,8 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
                     if (!((bits[k / 32] >> (k % 32)) & 1u)) v[k] = 0xff800000u;
             }
             if (K::WEIGHTS == 1 && it > 0) {   // the weights' columns are free
-                ok = bar_wait_warp(tc_bar<K::WEIGHTS>(done, it - 1), tc_phase<K::WEIGHTS>(it - 1), dead, a.err);
+                if (MODE == kGradKV) ok = bar_wait_warp(p_done, (it - 1) & 1, dead, a.err);
+                else ok = bar_wait_warp(tc_bar<K::WEIGHTS>(done, it - 1), tc_phase<K::WEIGHTS>(it - 1), dead, a.err);
                 if (!ok) break;
                 tmem_after_sync();
             }
@@ -519,29 +616,59 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
                 }
                 sum += (sums[0].x + sums[1].x) + (sums[0].y + sums[1].y);
             }
-            if (any_valid && BACK) {
-                const unsigned char *cs = tile_stat + st * K::STAT_BYTES + 8 * PART * part;
-                const float2 one = make_float2(ds_scale, ds_scale);
-                float2 l2 = make_float2(lse2, lse2), e2 = make_float2(delta, delta);
+            if constexpr (BACK) {
+                auto pair = [](const uint32_t *x) { return make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])); };
+                if (any_valid) {       // p in place of the scores
+                    const float2 l2 = make_float2(lse2, lse2);
 #pragma unroll
-                for (int i = 0; i < PART; i += 32) {
-                    uint32_t out[16], out2[16];
+                    for (int i = 0; i < PART; i += 32) {
+                        uint32_t out[16];
 #pragma unroll
-                    for (int k = i; k < i + 32; k += 2) {
-                        if (MODE == kGradKV) {
-                            const float4 two = *reinterpret_cast<const float4 *>(cs + 8 * k);
-                            l2 = make_float2(two.x, two.y);
-                            e2 = make_float2(two.z, two.w);
+                        for (int k = i; k < i + 32; k += 2) {
+                            const float2 x = MODE == kGradKV ? __fmul2_rn(pair(v + k), c2) : __ffma2_rn(pair(v + k), c2, l2);
+                            const float2 p = make_float2(ex2(x.x), ex2(x.y));
+                            if (MODE == kGradKV) out[k % 32 / 2] = pack2<T>(p.x, p.y);
+                            v[k] = __float_as_uint(p.x);
+                            v[k + 1] = __float_as_uint(p.y);
                         }
-                        const float2 x = __ffma2_rn(make_float2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), c2, l2);
-                        const float2 p = make_float2(ex2(x.x), ex2(x.y));
-                        float2 d = __fmul2_rn(p, __fadd2_rn(make_float2(__uint_as_float(dp[k]), __uint_as_float(dp[k + 1])), e2));
-                        if (!BF16) d = __fmul2_rn(d, one);
-                        out[k % 32 / 2] = pack2<T>(p.x, p.y);
-                        out2[k % 32 / 2] = pack2<T>(d.x, d.y);
+                        if (MODE == kGradKV) tmem_store16(at_p + i / 2, out);
                     }
-                    if (MODE == kGradKV) tmem_store16(at_p + i / 2, out);
-                    tmem_store16(at_ds + i / 2, out2);
+                    if (MODE == kGradKV) tmem_wait_store();
+                }
+                if (MODE == kGradKV) {
+                    tmem_before_sync();
+                    bar_arrive(p_ready);
+                }
+                VCLK(4);
+                ok = bar_wait_warp(d_full, it & 1, dead, a.err);
+                if (!ok) break;
+                tmem_after_sync();
+                VCLK(7);
+                uint32_t dp[PART];
+                if (any_valid) tmem_read<PART>(dp, mine + BN + PART * part);
+                if (!K::ALIAS) {
+                    tmem_before_sync();
+                    bar_arrive(d_free);
+                }
+                if (MODE == kGradKV && K::WEIGHTS == 1 && it > 0) {
+                    ok = bar_wait_warp(done, (it - 1) & 1, dead, a.err);
+                    if (!ok) break;
+                    tmem_after_sync();
+                }
+                if (any_valid) {
+                    const float2 one = make_float2(ds_scale, ds_scale), e2 = make_float2(delta, delta);
+#pragma unroll
+                    for (int i = 0; i < PART; i += 32) {
+                        uint32_t out[16];
+#pragma unroll
+                        for (int k = i; k < i + 32; k += 2) {
+                            const float2 x = MODE == kGradKV ? pair(dp + k) : __fadd2_rn(pair(dp + k), e2);
+                            float2 d = __fmul2_rn(pair(v + k), x);
+                            if (!BF16) d = __fmul2_rn(d, one);
+                            out[k % 32 / 2] = pack2<T>(d.x, d.y);
+                        }
+                        tmem_store16(at_ds + i / 2, out);
+                    }
                 }
             }
             VCLK(5);

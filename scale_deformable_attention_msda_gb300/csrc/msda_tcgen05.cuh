@@ -73,6 +73,9 @@ __device__ __forceinline__ bool bar_wait_warp(uint64_t *bar, uint32_t parity, vo
     return __all_sync(0xffffffffu, bar_wait(bar, parity, dead, err));
 }
 
+// What this thread wrote to shared memory is there for the MMAs that follow.
+__device__ __forceinline__ void shared_to_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
 // A group of four warps gives registers back, or takes them: what the block was launched
 // with is enough for all.
 template <int N> __device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
@@ -137,20 +140,6 @@ template <> __device__ __forceinline__ void tmem_read<128>(uint32_t (&v)[128], u
                  "tcgen05.ld.sync.aligned.32x32b.x64.b32 {" TMEM_R4 "," TMEM_R5 "," TMEM_R6 "," TMEM_R7 "}, [%129];\n\t" TMEM_WAIT
                  : TMEM_OUT32(0), TMEM_OUT32(32), TMEM_OUT32(64), TMEM_OUT32(96) : "r"(at), "r"(at + 64) : "memory");
 }
-// Two ranges of N columns each.
-template <int N> __device__ __forceinline__ void tmem_read_two(uint32_t (&v)[N], uint32_t (&w)[N], uint32_t at, uint32_t at2);
-#define TMEM_OUT8W(o) "=&r"(w[o]), "=&r"(w[o + 1]), "=&r"(w[o + 2]), "=&r"(w[o + 3]), "=&r"(w[o + 4]), "=&r"(w[o + 5]), "=&r"(w[o + 6]), "=&r"(w[o + 7])
-#define TMEM_OUT32W(o) TMEM_OUT8W(o), TMEM_OUT8W(o + 8), TMEM_OUT8W(o + 16), TMEM_OUT8W(o + 24)
-template <> __device__ __forceinline__ void tmem_read_two<64>(uint32_t (&v)[64], uint32_t (&w)[64], uint32_t at, uint32_t at2) {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x64.b32 {" TMEM_R0 "," TMEM_R1 "," TMEM_R2 "," TMEM_R3 "}, [%128];\n\t"
-                 "tcgen05.ld.sync.aligned.32x32b.x64.b32 {" TMEM_R4 "," TMEM_R5 "," TMEM_R6 "," TMEM_R7 "}, [%129];\n\t" TMEM_WAIT
-                 : TMEM_OUT32(0), TMEM_OUT32(32), TMEM_OUT32W(0), TMEM_OUT32W(32) : "r"(at), "r"(at2) : "memory");
-}
-template <> __device__ __forceinline__ void tmem_read_two<32>(uint32_t (&v)[32], uint32_t (&w)[32], uint32_t at, uint32_t at2) {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {" TMEM_R0 "," TMEM_R1 "}, [%64];\n\t"
-                 "tcgen05.ld.sync.aligned.32x32b.x32.b32 {" TMEM_R2 "," TMEM_R3 "}, [%65];\n\t" TMEM_WAIT
-                 : TMEM_OUT32(0), TMEM_OUT32W(0) : "r"(at), "r"(at2) : "memory");
-}
 __device__ __forceinline__ void tmem_store16(uint32_t at, const uint32_t (&v)[16]) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(at),
@@ -179,6 +168,9 @@ template <int PITCH> __device__ __forceinline__ constexpr uint32_t desc_high() {
     static_assert(PITCH == 64 || PITCH == 128, "the tile's swizzle");
     return (uint32_t)(8 * PITCH >> 4) | (1u << 14) | ((PITCH == 128 ? 2u : 4u) << 29);
 }
+// No swizzle: runs of 16 bytes, 8 rows' together; the leading stride is that of the next
+// run of the same rows, the other one that of the next 8 rows.
+__device__ __forceinline__ constexpr uint32_t desc_high_plain(uint32_t group_bytes) { return (group_bytes >> 4) | (1u << 14); }
 // fp32 accumulators of 16-bit operands (bf16, or fp16), 128 rows by N columns.
 template <bool BF16, int N, bool B_ACROSS>
 __device__ __forceinline__ constexpr uint32_t mma_desc() {
