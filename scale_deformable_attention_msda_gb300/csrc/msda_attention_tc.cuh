@@ -77,7 +77,8 @@ template <> struct TcConfig<kGradKV, 128> : TcSizes<KV128> {};
 template <int MODE, int DP> struct Tc : TcConfig<MODE, DP> {
     using C = TcConfig<MODE, DP>;
     static constexpr int BN = C::BN, PARTS = C::PARTS, STAGES = C::STAGES, EARLY = C::EARLY, WEIGHTS = C::WEIGHTS;
-    static constexpr bool ALIAS = WEIGHTS == 0, BACK = MODE != kForward;
+    // SPLIT: P is released, and its product issued, before dP is waited for
+    static constexpr bool ALIAS = WEIGHTS == 0, BACK = MODE != kForward, SPLIT = MODE == kGradKV && ALIAS;
     static constexpr int PITCH = DP == 32 ? 64 : 128, PANELS = DP == 128 ? 2 : 1, PANEL = DP == 128 ? 64 : DP;
     static constexpr int ROW_BYTES = kTcRows * PITCH * PANELS, COL_BYTES = BN * PITCH * PANELS;
     static constexpr int ROW_THREADS = PARTS * 128, THREADS = ROW_THREADS + 128, PART = BN / PARTS;
@@ -176,11 +177,17 @@ __device__ __forceinline__ void tc_store(const AttnArgs &a, int64_t row, int spl
     }
 }
 
-#ifdef V_CLOCK
+#ifdef V_TRACE
+#define VCLKDEF long long ck0 = 0; (void)ck0;
+__device__ long long g_tr[3][4][8];
+#define VCLK(i) if (blockIdx.x == 100 && threadIdx.x % 32 == 0 && it >= 12 && it < 16 && (threadIdx.x < 32 || threadIdx.x >= 256)) g_tr[threadIdx.x < 32 ? 0 : threadIdx.x / 32 == 8 ? 1 : 2][it - 12][i] = clock64();
+#define VCLKPRINT if (blockIdx.x == 100 && threadIdx.x == 0) for (int q = 0; q < 96; ++q) printf("m%d D%d r%d it%d e%d t%lld\n", MODE, DP, q / 32, q / 8 % 4, q % 8, g_tr[q / 32][q / 8 % 4][q % 8]);
+#define VCLKP2(n, c) ;
+#elif defined(V_CLOCK)
 #define VCLKDEF long long ck[8] = {}, ck0 = clock64(); const long long ckb = ck0;
 #define VCLK(i) { const long long n_ = clock64(); ck[i] += n_ - ck0; ck0 = n_; }
 #define VCLKPRINT if (threadIdx.x == 0 && (blockIdx.x == 0 || blockIdx.x == 200)) printf("mode %d DP %d it %d total %lld : loop %lld s_full %lld ld %lld max %lld done %lld exp %lld st %lld dup %lld\n", MODE, DP, it, (clock64() - ckb) / (it ? it : 1), ck[0] / (it ? it : 1), ck[1] / (it ? it : 1), ck[2] / (it ? it : 1), ck[3] / (it ? it : 1), ck[4] / (it ? it : 1), ck[5] / (it ? it : 1), ck[6] / (it ? it : 1), ck[7] / (it ? it : 1));
-#define VCLKP2(n, c) if (threadIdx.x % 32 == 0) if (blockIdx.x == 0 || blockIdx.x == 200) printf("mode %d DP %d %s it %d total %lld : loop %lld full %lld free %lld done %lld issue %lld lat %lld\n", MODE, DP, n, c, (clock64() - ckb) / c, ck[0] / c, ck[1] / c, ck[2] / c, ck[3] / c, ck[4] / c, ck[5] / c);
+#define VCLKP2(n, c) if (threadIdx.x % 32 == 0) if (blockIdx.x == 0 || blockIdx.x == 200) printf("mode %d DP %d %s it %d total %lld : loop %lld full %lld free %lld done %lld issue %lld lat %lld issue2 %lld\n", MODE, DP, n, c, (clock64() - ckb) / c, ck[0] / c, ck[1] / c, ck[2] / c, ck[3] / c, ck[4] / c, ck[5] / c, ck[6] / c);
 #else
 #define VCLKP2(n, c) ;
 #define VCLKDEF
@@ -287,12 +294,12 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
         for (int i = 0; i < STAGES; ++i) bar_init(bias_full + i, 1);
         bar_init(s_full, 1);
         bar_init(d_full, 1);
-        bar_init(s_free, K::ROW_THREADS);
-        bar_init(d_free, K::ROW_THREADS);
-        bar_init(p_ready, K::ROW_THREADS);
+        bar_init(s_free, K::ROW_THREADS / 32);
+        bar_init(d_free, K::ROW_THREADS / 32);
+        bar_init(p_ready, K::ROW_THREADS / 32);
         bar_init(p_done, 1);
         for (int i = 0; i < 2; ++i) {
-            bar_init(ready + i, K::ROW_THREADS);
+            bar_init(ready + i, K::ROW_THREADS / 32);
             bar_init(done + i, 1);
             bar_init(last + i, 1);
         }
@@ -382,23 +389,24 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
             for (int it = 0;; ++it) {
                 const int st = it % STAGES, se = it % EARLY;
                 VCLK(0);
-                ok = bar_wait_warp(full_early + se, (it / EARLY) & 1, dead, a.err);
+                // the columns are free: the last scores are read, and (ALIAS: these became
+                // weights) the weights that will be written over are used
+                const Phase none = {nullptr, 0}, used = {tc_bar<K::WEIGHTS>(done, it - 1), tc_phase<K::WEIGHTS>(it - 1)};
+                const Phase free = it == 0 ? none : !K::ALIAS ? Phase{s_free, (uint32_t)(it - 1) & 1} : MODE == kGradKV ? Phase{p_done, (uint32_t)(it - 1) & 1} : used;
+                const Phase older = K::WEIGHTS == 2 && it > 1 ? Phase{tc_bar<K::WEIGHTS>(done, it - 2), tc_phase<K::WEIGHTS>(it - 2)} : none;
+                ok = bar_wait_all(dead, a.err, Phase{full_early + se, (uint32_t)(it / EARLY) & 1});
                 VCLK(1);
                 if (!ok) break;
                 const bool end = info[it % INFO].cls == 0;
-                if (!end && BACK) ok = bar_wait_warp(full + st, (it / STAGES) & 1, dead, a.err);
-                if (!end && it == 0) ok = ok && bar_wait_warp(a_full, 0, dead, a.err);
-                if (!end && MODE == kGradKV) ok = ok && bar_wait_warp(bias_full + st, (it / STAGES) & 1, dead, a.err);
-                // the columns are free: the last scores are read, and (ALIAS: these became
-                // weights) the weights that will be written over are used
-                if (ok && it > 0) {
-                    if (!K::ALIAS) ok = bar_wait_warp(s_free, (it - 1) & 1, dead, a.err);
-                    else if (MODE == kGradKV) ok = bar_wait_warp(p_done, (it - 1) & 1, dead, a.err);
-                    else ok = bar_wait_warp(tc_bar<K::WEIGHTS>(done, it - 1), tc_phase<K::WEIGHTS>(it - 1), dead, a.err);
+                if (!end && (BACK || it == 0)) {       // (a block without a tile has fetched nothing)
+                    ok = bar_wait_all(dead, a.err, it == 0 ? Phase{a_full, 0} : none, BACK ? Phase{full + st, (uint32_t)(it / STAGES) & 1} : none,
+                                      MODE == kGradKV ? Phase{bias_full + st, (uint32_t)(it / STAGES) & 1} : none);
+                    if (!ok) break;
                 }
                 VCLK(2);
-                if (ok && K::WEIGHTS == 2 && it > 1) ok = bar_wait_warp(tc_bar<K::WEIGHTS>(done, it - 2), tc_phase<K::WEIGHTS>(it - 2), dead, a.err);
+                ok = bar_wait_all(dead, a.err, free, older);
                 if (!ok) break;
+                VCLK(2);
                 VCLK(3);
                 if (end) {             // not before: it would be taken for the last scores' arrival
                     VCLKP2("scores", it)
@@ -417,12 +425,11 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
                 }
                 if (MODE == kGradKV) mma_shared<id, plain>(tmem, ones_at, columns, true);
                 if (MODE == kForward) mma_commit(empty_early + se);
-                mma_commit(s_full);
+                if (!BACK || K::SPLIT) mma_commit(s_full);
                 VCLK(4);
                 if (BACK) {
                     if (it > 0) {
-                        if (!K::ALIAS) ok = bar_wait_warp(d_free, (it - 1) & 1, dead, a.err);
-                        else ok = bar_wait_warp(tc_bar<K::WEIGHTS>(done, it - 1), tc_phase<K::WEIGHTS>(it - 1), dead, a.err);
+                        ok = K::ALIAS ? bar_wait_all(dead, a.err, used) : !K::SPLIT || bar_wait_all(dead, a.err, Phase{d_free, (uint32_t)(it - 1) & 1});
                         if (!ok) break;
                         tmem_after_sync();
                     }
@@ -435,8 +442,12 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
                     }
                     if (MODE == kGradKV) mma_shared<id, plain>(tmem + BN, ones_at + desc_step(K::ONES_BYTES), columns, true);
                     if (MODE == kGradQ) mma_commit(empty_early + se);
-                    mma_commit(d_full);
+                    mma_commit(K::SPLIT ? d_full : s_full);
                     VCLK(6);
+#ifdef V_LAT2
+                    bar_wait_all(dead, a.err, Phase{K::SPLIT ? d_full : s_full, (uint32_t)it & 1});
+                    VCLK(5);
+#endif
                 }
             }
             if (!ok) {                 // MMAs under way end before the block does
@@ -454,35 +465,40 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
             for (int it = 0;; ++it) {
                 const int st = it % STAGES, se = it % EARLY;
                 VCLK(0);
-                ok = bar_wait_warp(full + st, (it / STAGES) & 1, dead, a.err);
+                ok = bar_wait_all(dead, a.err, Phase{full + st, (uint32_t)(it / STAGES) & 1}, Phase{MODE == kGradKV ? full_early + se : nullptr, (uint32_t)(it / EARLY) & 1});
                 VCLK(1);
                 if (!info[it % INFO].cls) VCLKP2("second", it)
                 if (!ok || !info[it % INFO].cls) break;
-                if (MODE == kGradKV) ok = bar_wait_warp(full_early + se, (it / EARLY) & 1, dead, a.err);
                 const uint32_t x_late = late + st * desc_step(K::COL_BYTES), x_early = early + se * desc_step(K::COL_BYTES);
                 // weights: P, then dS; over the scores each part's in the part's own columns
                 const uint32_t p = tmem + (K::ALIAS ? 0 : K::SCORES + (K::WEIGHTS == 2 ? it % 2 * K::WIDE : 0));
                 const uint32_t ds = MODE != kGradKV ? p : K::ALIAS ? p + BN : p + BN / 2, acc = tmem + K::ACC;
                 auto at = [](int k) { return (uint32_t)(K::ALIAS ? k / PART_STEPS * K::PART + k % PART_STEPS * 8 : 8 * k); };
-                if (MODE == kGradKV) {
-                    ok = ok && bar_wait_warp(p_ready, it & 1, dead, a.err);
+                if (K::SPLIT) {
+                    ok = bar_wait_all(dead, a.err, Phase{p_ready, (uint32_t)it & 1});
                     if (!ok) break;
                     tmem_after_sync();
 #pragma unroll
                     for (int k = 0; k < BN / 16; ++k) mma_tmem<id, high>(acc, p + at(k), x_early + desc_step(k * 16 * K::PITCH), it > 0 || k > 0);
                     mma_commit(p_done);
                 }
-                ok = ok && bar_wait_warp(tc_bar<K::WEIGHTS>(ready, it), tc_phase<K::WEIGHTS>(it), dead, a.err);
+                ok = bar_wait_all(dead, a.err, Phase{tc_bar<K::WEIGHTS>(ready, it), tc_phase<K::WEIGHTS>(it)});
                 if (!ok) break;
                 VCLK(2);
                 tmem_after_sync();
 #pragma unroll
-                for (int k = 0; k < BN / 16; ++k)
+                for (int k = 0; k < BN / 16; ++k) {
+                    if (MODE == kGradKV && !K::SPLIT) mma_tmem<id, high>(acc, p + at(k), x_early + desc_step(k * 16 * K::PITCH), it > 0 || k > 0);
                     mma_tmem<id, high>(acc + (MODE == kGradKV ? DP : 0), ds + at(k), x_late + desc_step(k * 16 * K::PITCH), it > 0 || k > 0);
+                }
                 if (MODE == kGradKV) mma_commit(empty_early + se);    // dP, which reads it too, is there
                 mma_commit(empty + st);
                 mma_commit(tc_bar<K::WEIGHTS>(done, it));  // last: the block ends after it has arrived
                 VCLK(4);
+#ifdef V_LAT2
+                bar_wait_all(dead, a.err, Phase{tc_bar<K::WEIGHTS>(done, it), tc_phase<K::WEIGHTS>(it)});
+                VCLK(5);
+#endif
             }
             if (!ok) {
                 uint32_t off = 0u;
@@ -552,31 +568,30 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
             if (!ok) break;
             tmem_after_sync();
             VCLK(1);
-            uint32_t v[PART];                  // the row's scores
-            if (any_valid) tmem_read<PART>(v, mine + PART * part);
+            // the row's scores, and dP beside them unless it comes later
+            uint32_t v[PART], dp[BACK ? PART : 1];
+            if (any_valid) {
+                if constexpr (BACK && !K::SPLIT) tmem_read_two<PART>(v, dp, mine + PART * part, mine + BN + PART * part);
+                else tmem_read<PART>(v, mine + PART * part);
+            }
             VCLK(2);
             if (!K::ALIAS) {
                 tmem_before_sync();
-                bar_arrive(s_free);
+                bar_arrive_warp(s_free);
             }
             if (cls != 2) {            // p, and with it ds unless dP is not finite, will be 0
 #pragma unroll
                 for (int k = 0; k < PART; ++k)
                     if (!((bits[k / 32] >> (k % 32)) & 1u)) v[k] = 0xff800000u;
             }
-            if (K::WEIGHTS == 1 && it > 0) {   // the weights' columns are free
-                if (MODE == kGradKV) ok = bar_wait_warp(p_done, (it - 1) & 1, dead, a.err);
-                else ok = bar_wait_warp(tc_bar<K::WEIGHTS>(done, it - 1), tc_phase<K::WEIGHTS>(it - 1), dead, a.err);
-                if (!ok) break;
-                tmem_after_sync();
-            }
             VCLK(3);
             const float2 c2 = make_float2(c, c);
+            auto pair = [](const uint32_t *x) { return make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])); };
+            uint32_t out[MODE == kGradKV ? PART / 2 : 1], out2[BACK ? PART / 2 : 1];     // weights: P, dS
             if (any_valid && MODE == kForward) {
-                auto pair = [&](int k) { return make_float2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])); };
                 float most[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int k = 0; k < BN; k += 2) most[k / 2 % 4] = max3(most[k / 2 % 4], pair(k).x, pair(k).y);
+                for (int k = 0; k < PART; k += 2) most[k / 2 % 4] = max3(most[k / 2 % 4], pair(v + k).x, pair(v + k).y);
                 const float high = max3(fmaxf(most[0], most[1]), most[2], most[3]);
                 // The weights are relative to `top`, which follows the maximum only when that has
                 // grown by more than 2^8: then what was summed is scaled down.
@@ -598,84 +613,90 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
                         }
                     }
                 }
-                VCLK(4);
                 const float ref = top == -INFINITY ? -up : top * c - up;
                 const float2 ref2 = make_float2(-ref, -ref);
                 float2 sums[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+                if (K::WEIGHTS == 1 && it > 0) {   // the weights' columns are free
+                    ok = ok && bar_wait_warp(tc_bar<K::WEIGHTS>(done, it - 1), tc_phase<K::WEIGHTS>(it - 1), dead, a.err);
+                    tmem_after_sync();
+                }
 #pragma unroll
-                for (int i = 0; i < BN; i += 32) {
-                    uint32_t out[16];
+                for (int i = 0; i < PART; i += 32) {
+                    uint32_t w[16];
 #pragma unroll
                     for (int k = 0; k < 32; k += 2) {
-                        const float2 x = __ffma2_rn(pair(i + k), c2, ref2);
+                        const float2 x = __ffma2_rn(pair(v + i + k), c2, ref2);
                         const float2 p = make_float2(ex2(x.x), ex2(x.y));
                         sums[k / 2 % 2] = __fadd2_rn(sums[k / 2 % 2], p);
-                        out[k / 2] = pack2<T>(p.x, p.y);
+                        w[k / 2] = pack2<T>(p.x, p.y);
                     }
-                    tmem_store16(at_p + i / 2, out);
+                    tmem_store16(at_p + i / 2, w);
                 }
                 sum += (sums[0].x + sums[1].x) + (sums[0].y + sums[1].y);
             }
             if constexpr (BACK) {
-                auto pair = [](const uint32_t *x) { return make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])); };
-                if (any_valid) {       // p in place of the scores
-                    const float2 l2 = make_float2(lse2, lse2);
+                const float2 l2 = make_float2(lse2, lse2), e2 = make_float2(delta, delta), one = make_float2(ds_scale, ds_scale);
+                auto probability = [&](int k) {
+                    const float2 x = MODE == kGradKV ? __fmul2_rn(pair(v + k), c2) : __ffma2_rn(pair(v + k), c2, l2);
+                    return make_float2(ex2(x.x), ex2(x.y));
+                };
+                auto slope = [&](float2 p, int k) {
+                    const float2 d = __fmul2_rn(p, MODE == kGradKV ? pair(dp + k) : __fadd2_rn(pair(dp + k), e2));
+                    return BF16 ? d : __fmul2_rn(d, one);
+                };
+                if constexpr (K::SPLIT) {
+                    if (any_valid) {   // p in place of the scores
 #pragma unroll
-                    for (int i = 0; i < PART; i += 32) {
-                        uint32_t out[16];
-#pragma unroll
-                        for (int k = i; k < i + 32; k += 2) {
-                            const float2 x = MODE == kGradKV ? __fmul2_rn(pair(v + k), c2) : __ffma2_rn(pair(v + k), c2, l2);
-                            const float2 p = make_float2(ex2(x.x), ex2(x.y));
-                            if (MODE == kGradKV) out[k % 32 / 2] = pack2<T>(p.x, p.y);
+                        for (int k = 0; k < PART; k += 2) {
+                            const float2 p = probability(k);
+                            out[k / 2] = pack2<T>(p.x, p.y);
                             v[k] = __float_as_uint(p.x);
                             v[k + 1] = __float_as_uint(p.y);
                         }
-                        if (MODE == kGradKV) tmem_store16(at_p + i / 2, out);
+                        tmem_store<PART / 2>(at_p, out);
+                        tmem_wait_store();
                     }
-                    if (MODE == kGradKV) tmem_wait_store();
-                }
-                if (MODE == kGradKV) {
                     tmem_before_sync();
-                    bar_arrive(p_ready);
-                }
-                VCLK(4);
-                ok = bar_wait_warp(d_full, it & 1, dead, a.err);
-                if (!ok) break;
-                tmem_after_sync();
-                VCLK(7);
-                uint32_t dp[PART];
-                if (any_valid) tmem_read<PART>(dp, mine + BN + PART * part);
-                if (!K::ALIAS) {
-                    tmem_before_sync();
-                    bar_arrive(d_free);
-                }
-                if (MODE == kGradKV && K::WEIGHTS == 1 && it > 0) {
-                    ok = bar_wait_warp(done, (it - 1) & 1, dead, a.err);
+                    bar_arrive_warp(p_ready);
+                    VCLK(4);
+                    ok = bar_wait_warp(d_full, it & 1, dead, a.err);
                     if (!ok) break;
                     tmem_after_sync();
-                }
-                if (any_valid) {
-                    const float2 one = make_float2(ds_scale, ds_scale), e2 = make_float2(delta, delta);
+                    VCLK(7);
+                    if (any_valid) {
+                        tmem_read<PART>(dp, mine + BN + PART * part);
 #pragma unroll
-                    for (int i = 0; i < PART; i += 32) {
-                        uint32_t out[16];
-#pragma unroll
-                        for (int k = i; k < i + 32; k += 2) {
-                            const float2 x = MODE == kGradKV ? pair(dp + k) : __fadd2_rn(pair(dp + k), e2);
-                            float2 d = __fmul2_rn(pair(v + k), x);
-                            if (!BF16) d = __fmul2_rn(d, one);
-                            out[k % 32 / 2] = pack2<T>(d.x, d.y);
+                        for (int k = 0; k < PART; k += 2) {
+                            const float2 d = slope(pair(v + k), k);
+                            out2[k / 2] = pack2<T>(d.x, d.y);
                         }
-                        tmem_store16(at_ds + i / 2, out);
+                    }
+                } else if (any_valid) {
+#pragma unroll
+                    for (int k = 0; k < PART; k += 2) {
+                        const float2 p = probability(k), d = slope(p, k);
+                        if (MODE == kGradKV) out[k / 2] = pack2<T>(p.x, p.y);
+                        out2[k / 2] = pack2<T>(d.x, d.y);
                     }
                 }
+            }
+            VCLK(4);
+            // the weights' columns are free (forward's rows have waited)
+            if (K::WEIGHTS == 1 && it > 0 && (BACK || !any_valid)) {
+                ok = ok && bar_wait_warp(tc_bar<K::WEIGHTS>(done, it - 1), tc_phase<K::WEIGHTS>(it - 1), dead, a.err);
+                tmem_after_sync();
+            }
+            if (!ok) break;
+            VCLK(7);
+            if (any_valid) {
+                if constexpr (MODE == kGradKV && !K::SPLIT) tmem_store<PART / 2>(at_p, out);
+                if constexpr (BACK) tmem_store<PART / 2>(at_ds, out2);
             }
             VCLK(5);
             if (!ok) break;
             if (any_valid) tmem_wait_store();
             tmem_before_sync();
-            bar_arrive(tc_bar<K::WEIGHTS>(ready, it));
+            bar_arrive_warp(tc_bar<K::WEIGHTS>(ready, it));
             VCLK(6);
         }
 

@@ -30,13 +30,16 @@ __device__ __forceinline__ unsigned long long nanoseconds() {
 __device__ __forceinline__ void bar_arrive_one(uint64_t *bar) {
     asm volatile(ELECT("mbarrier.arrive.shared::cta.b64 _, [%0];") ::"r"(shared_at(bar)) : "memory");
 }
+// One arrival for a whole warp, all of whose lanes have come so far: 32 arrivals at one
+// address are taken one after another.
+__device__ __forceinline__ void bar_arrive_warp(uint64_t *bar) {
+    __syncwarp();
+    bar_arrive_one(bar);
+}
 __device__ __forceinline__ void bar_init(uint64_t *bar, uint32_t count) {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(shared_at(bar)), "r"(count) : "memory");
 }
 __device__ __forceinline__ void bar_init_done() { asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory"); }
-__device__ __forceinline__ void bar_arrive(uint64_t *bar) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(shared_at(bar)) : "memory");
-}
 __device__ __forceinline__ void bar_expect(uint64_t *bar, uint32_t bytes) {
     asm volatile(ELECT("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;") ::"r"(shared_at(bar)), "r"(bytes) : "memory");
 }
@@ -71,6 +74,22 @@ __device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity, volatil
 // The same for a whole warp: the lanes agree.
 __device__ __forceinline__ bool bar_wait_warp(uint64_t *bar, uint32_t parity, volatile uint32_t *dead, unsigned *err) {
     return __all_sync(0xffffffffu, bar_wait(bar, parity, dead, err));
+}
+// A barrier and the parity of the phase waited for; NULL: nothing.
+struct Phase {
+    uint64_t *bar;
+    uint32_t parity;
+};
+// Waits for all of them. A look at a barrier takes 100 cycles until it is acted on: these
+// look at all before they act.
+template <class... P>
+__device__ __forceinline__ bool bar_wait_all(volatile uint32_t *dead, unsigned *err, P... phases) {
+    bool now = true;
+    ((now = (!phases.bar || bar_try(phases.bar, phases.parity)) && now), ...);
+    if (__all_sync(0xffffffffu, now)) return true;
+    bool ok = true;
+    ((ok = ok && (!phases.bar || bar_wait(phases.bar, phases.parity, dead, err))), ...);
+    return __all_sync(0xffffffffu, ok);
 }
 
 // What this thread wrote to shared memory is there for the MMAs that follow.
@@ -146,6 +165,30 @@ __device__ __forceinline__ void tmem_store16(uint32_t at, const uint32_t (&v)[16
         "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
         "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
         : "memory");
+}
+// Two ranges of N columns each.
+template <int N> __device__ __forceinline__ void tmem_read_two(uint32_t (&v)[N], uint32_t (&w)[N], uint32_t at, uint32_t at2);
+#define TMEM_OUT8W(o) "=&r"(w[o]), "=&r"(w[o + 1]), "=&r"(w[o + 2]), "=&r"(w[o + 3]), "=&r"(w[o + 4]), "=&r"(w[o + 5]), "=&r"(w[o + 6]), "=&r"(w[o + 7])
+#define TMEM_OUT32W(o) TMEM_OUT8W(o), TMEM_OUT8W(o + 8), TMEM_OUT8W(o + 16), TMEM_OUT8W(o + 24)
+template <> __device__ __forceinline__ void tmem_read_two<64>(uint32_t (&v)[64], uint32_t (&w)[64], uint32_t at, uint32_t at2) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x64.b32 {" TMEM_R0 "," TMEM_R1 "," TMEM_R2 "," TMEM_R3 "}, [%128];\n\t"
+                 "tcgen05.ld.sync.aligned.32x32b.x64.b32 {" TMEM_R4 "," TMEM_R5 "," TMEM_R6 "," TMEM_R7 "}, [%129];\n\t" TMEM_WAIT
+                 : TMEM_OUT32(0), TMEM_OUT32(32), TMEM_OUT32W(0), TMEM_OUT32W(32) : "r"(at), "r"(at2) : "memory");
+}
+template <> __device__ __forceinline__ void tmem_read_two<32>(uint32_t (&v)[32], uint32_t (&w)[32], uint32_t at, uint32_t at2) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {" TMEM_R0 "," TMEM_R1 "}, [%64];\n\t"
+                 "tcgen05.ld.sync.aligned.32x32b.x32.b32 {" TMEM_R2 "," TMEM_R3 "}, [%65];\n\t" TMEM_WAIT
+                 : TMEM_OUT32(0), TMEM_OUT32W(0) : "r"(at), "r"(at2) : "memory");
+}
+template <int N> __device__ __forceinline__ void tmem_store(uint32_t at, const uint32_t (&v)[N]);
+#define TMEM_IN8(o) "r"(v[o]), "r"(v[o + 1]), "r"(v[o + 2]), "r"(v[o + 3]), "r"(v[o + 4]), "r"(v[o + 5]), "r"(v[o + 6]), "r"(v[o + 7])
+#define TMEM_IN32(o) TMEM_IN8(o), TMEM_IN8(o + 8), TMEM_IN8(o + 16), TMEM_IN8(o + 24)
+template <> __device__ __forceinline__ void tmem_store<32>(uint32_t at, const uint32_t (&v)[32]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {" TMEM_R0 "," TMEM_R1 "};" ::TMEM_IN32(0), "r"(at) : "memory");
+}
+template <> __device__ __forceinline__ void tmem_store<16>(uint32_t at, const uint32_t (&v)[16]) { tmem_store16(at, v); }
+template <> __device__ __forceinline__ void tmem_store<64>(uint32_t at, const uint32_t (&v)[64]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x64.b32 [%64], {" TMEM_R0 "," TMEM_R1 "," TMEM_R2 "," TMEM_R3 "};" ::TMEM_IN32(0), TMEM_IN32(32), "r"(at) : "memory");
 }
 
 // ------------------------------------------------------------------- MMA
