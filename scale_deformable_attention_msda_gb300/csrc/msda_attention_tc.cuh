@@ -83,7 +83,7 @@ template <int MODE, int DP> struct Tc : TcConfig<MODE, DP> {
     static constexpr int ROW_BYTES = kTcRows * PITCH * PANELS, COL_BYTES = BN * PITCH * PANELS;
     static constexpr int ROW_THREADS = PARTS * 128, THREADS = ROW_THREADS + 128, PART = BN / PARTS;
     // registers: 65,536 of an SM, spread evenly at the start and then by need
-    static constexpr int REGS_ROW = PARTS * C::BLOCKS == 4 ? 96 : 208, REGS_OTHER = PARTS * C::BLOCKS == 4 || PARTS == 1 ? 48 : 88;
+    static constexpr int REGS_ROW = PARTS == 4 ? 104 : PARTS * C::BLOCKS == 4 ? 96 : 208, REGS_OTHER = PARTS == 4 ? 64 : PARTS * C::BLOCKS == 4 || PARTS == 1 ? 48 : 88;
     static_assert((PARTS * REGS_ROW + REGS_OTHER) * 128 <= 65536 / C::BLOCKS / THREADS / 8 * 8 * THREADS, "registers");
     // tensor memory: scores (and dP), weights, accumulators
     static constexpr int SCORES = BN * (BACK ? 2 : 1), WIDE = BN / 2 * (MODE == kGradKV ? 2 : 1);
@@ -580,6 +580,7 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
                 bar_arrive_warp(s_free);
             }
             if (cls != 2) {            // p, and with it ds unless dP is not finite, will be 0
+                asm volatile("");      // a branch, not a select for each score
 #pragma unroll
                 for (int k = 0; k < PART; ++k)
                     if (!((bits[k / 32] >> (k % 32)) & 1u)) v[k] = 0xff800000u;
@@ -720,49 +721,36 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
                 }
             }
             const float over = sum == 0.0f ? 0.0f : 1.0f / sum;
+            // 32 channels of a result at a time, shared among the groups
+#pragma unroll 1
+            for (int q = part; q < K::RESULTS * (DP / 32); q += K::PARTS) {
+                const int which = q / (DP / 32), d0 = q % (DP / 32) * 32;
+                const float g = MODE == kForward ? 1.0f : MODE == kGradQ || which ? down_ds : down;
+                const float f = MODE == kForward ? over : g * (MODE == kGradQ || which ? a.scale : 1.0f);
+                uint32_t o[32];
+                float v[32];
+                if (count > 0) tmem_read<32>(o, at_acc + 32 * q);
 #pragma unroll
-            for (int which = 0; which < K::RESULTS; ++which) {
-                // of two groups one has each of a key's gradients, or half of dq's channels
-                if (K::PARTS > 1 && MODE == kGradKV && which != part) continue;
-                constexpr int CHUNKS = MODE == kGradQ && K::PARTS > 1 && DP >= 64 ? DP / 32 / K::PARTS : DP / 32;
-                const int c0 = CHUNKS * 32 < DP ? part * CHUNKS : 0;
-                if (MODE == kGradQ && CHUNKS * 32 == DP && part > 0) continue;
-                const float g_ = MODE == kForward ? 1.0f : MODE == kGradQ || which ? down_ds : down;
-                const float f = MODE == kForward ? over : g_ * (MODE == kGradQ || which ? a.scale : 1.0f);
+                for (int k = 0; k < 32; ++k) v[k] = count > 0 ? __uint_as_float(o[k]) : 0.0f;
                 bool finite = true;
-                if (a.classes && count > 0) {
+                if (a.classes) {
 #pragma unroll
-                    for (int i = c0; i < c0 + CHUNKS; ++i) {
-                        uint32_t o[32];
-                        tmem_read<32>(o, at_acc + which * DP + 32 * i);
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) finite = finite && isfinite(__uint_as_float(o[k]));
-                    }
+                    for (int k = 0; k < 32; ++k) finite = finite && isfinite(v[k]);
                 }
-#pragma unroll
-                for (int i = c0; i < c0 + CHUNKS; ++i) {
-                    uint32_t o[32];
-                    float v[32];
-                    if (count > 0) {
-                        tmem_read<32>(o, at_acc + which * DP + 32 * i);
-                    }
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) v[k] = count > 0 ? __uint_as_float(o[k]) : 0.0f;
-                    if (valid && finite) tc_store<T, MODE>(a, row, split, which, 32 * i, v, f, g_);
-                }
+                if (valid && finite) tc_store<T, MODE>(a, row, split, which, d0, v, f, g);
                 uint32_t bad = __ballot_sync(0xffffffffu, valid && !finite);
                 while (bad) {
                     const int from = __ffs(bad) - 1;
                     bad &= bad - 1;
                     float e1[4], e2[4];
-                    const float m2 = __shfl_sync(0xffffffffu, ref, from), o = __shfl_sync(0xffffffffu, over, from);
+                    const float m2 = __shfl_sync(0xffffffffu, ref, from), over_from = __shfl_sync(0xffffffffu, over, from);
                     attn_exact_row<T, MODE, BN>(a, w, (r & ~31) + from, j0, j1, m2, e1, e2);
+                    const bool of_ds = MODE == kGradQ || which;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const int d = lane + 32 * i;
-                        if (d < a.D && d / 32 >= c0 && d / 32 < c0 + CHUNKS)
-                            attn_store<T, MODE>(a, w, (r & ~31) + from, split, which, d, MODE == kGradQ || which ? e2[i] : e1[i],
-                                                MODE == kForward ? o : MODE == kGradQ || which ? a.scale : 1.0f);
+                        if (32 * i != d0 || d0 + lane >= a.D) continue;
+                        attn_store<T, MODE>(a, w, (r & ~31) + from, split, which, d0 + lane, of_ds ? e2[i] : e1[i],
+                                            MODE == kForward ? over_from : of_ds ? a.scale : 1.0f);
                     }
                 }
             }
