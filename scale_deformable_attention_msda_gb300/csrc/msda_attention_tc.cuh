@@ -17,7 +17,6 @@
 // kGradKV    S = K Q', dP = V dO'    dV += P dO, dK += dS Q
 #pragma once
 
-#include <stdio.h>
 #include <cudaTypedefs.h>
 
 #include "msda_attention_host.h"
@@ -177,23 +176,6 @@ __device__ __forceinline__ void tc_store(const AttnArgs &a, int64_t row, int spl
     }
 }
 
-#ifdef V_TRACE
-#define VCLKDEF long long ck0 = 0; (void)ck0;
-__device__ long long g_tr[3][4][8];
-#define VCLK(i) if (blockIdx.x == 100 && threadIdx.x % 32 == 0 && it >= 12 && it < 16 && (threadIdx.x < 32 || threadIdx.x >= 256)) g_tr[threadIdx.x < 32 ? 0 : threadIdx.x / 32 == 8 ? 1 : 2][it - 12][i] = clock64();
-#define VCLKPRINT if (blockIdx.x == 100 && threadIdx.x == 0) for (int q = 0; q < 96; ++q) printf("m%d D%d r%d it%d e%d t%lld\n", MODE, DP, q / 32, q / 8 % 4, q % 8, g_tr[q / 32][q / 8 % 4][q % 8]);
-#define VCLKP2(n, c) ;
-#elif defined(V_CLOCK)
-#define VCLKDEF long long ck[8] = {}, ck0 = clock64(); const long long ckb = ck0;
-#define VCLK(i) { const long long n_ = clock64(); ck[i] += n_ - ck0; ck0 = n_; }
-#define VCLKPRINT if (threadIdx.x == 0 && (blockIdx.x == 0 || blockIdx.x == 200)) printf("mode %d DP %d it %d total %lld : loop %lld s_full %lld ld %lld max %lld done %lld exp %lld st %lld dup %lld\n", MODE, DP, it, (clock64() - ckb) / (it ? it : 1), ck[0] / (it ? it : 1), ck[1] / (it ? it : 1), ck[2] / (it ? it : 1), ck[3] / (it ? it : 1), ck[4] / (it ? it : 1), ck[5] / (it ? it : 1), ck[6] / (it ? it : 1), ck[7] / (it ? it : 1));
-#define VCLKP2(n, c) if (threadIdx.x % 32 == 0) if (blockIdx.x == 0 || blockIdx.x == 200) printf("mode %d DP %d %s it %d total %lld : loop %lld full %lld free %lld done %lld issue %lld lat %lld issue2 %lld\n", MODE, DP, n, c, (clock64() - ckb) / c, ck[0] / c, ck[1] / c, ck[2] / c, ck[3] / c, ck[4] / c, ck[5] / c, ck[6] / c);
-#else
-#define VCLKP2(n, c) ;
-#define VCLKDEF
-#define VCLK(i)
-#define VCLKPRINT
-#endif
 // What the fetching lane tells the others of a column tile; cls 0: there is none more.
 struct TcTile {
     int pos, head, cls;
@@ -326,6 +308,8 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
         if (warp == HELPER + 1) {
             // -------------------------------------------- fetching
             int it = 0, pos = 0, head = 0;
+            Ring<STAGES> st;
+            Ring<EARLY> se;
             if (j0 < j1) attn_columns<MODE, BN>(a, w, j0, &pos, &head);
             bool ok = true;
             for (int64_t j = j0; j < j1 && ok; ++j) {
@@ -338,21 +322,22 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
                             if (BACK) tma_load(tile_a2 + p * kTcRows * K::PITCH, &maps.a2, 64 * p, w.head, w.pos, w.b, a_full);
                         }
                     }
-                    const int st = it % STAGES, se = it % EARLY;
-                    ok = it < EARLY || bar_wait_warp(empty_early + se, (it / EARLY - 1) & 1, dead, a.err);
+                    ok = bar_wait(empty_early + se.at, se.phase ^ 1u, dead, a.err);
                     if (!ok) break;
                     if (lane == 0) info[it % INFO] = {pos, head, cls};
                     __syncwarp();
-                    bar_expect(full_early + se, K::COL_BYTES);
+                    bar_expect(full_early + se.at, K::COL_BYTES);
                     for (int p = 0; p < K::PANELS; ++p)
-                        tma_load(tile_early + se * K::COL_BYTES + p * BN * K::PITCH, FIRST_EARLY ? &maps.x1 : &maps.x2, 64 * p, head, pos, w.b, full_early + se);
-                    ok = it < STAGES || bar_wait_warp(empty + st, (it / STAGES - 1) & 1, dead, a.err);
+                        tma_load(tile_early + se.at * K::COL_BYTES + p * BN * K::PITCH, FIRST_EARLY ? &maps.x1 : &maps.x2, 64 * p, head, pos, w.b, full_early + se.at);
+                    ok = bar_wait(empty + st.at, st.phase ^ 1u, dead, a.err);
                     if (!ok) break;
-                    bar_expect(full + st, K::COL_BYTES + K::STAT_BYTES);
+                    bar_expect(full + st.at, K::COL_BYTES + K::STAT_BYTES);
                     for (int p = 0; p < K::PANELS; ++p)
-                        tma_load(tile_late + st * K::COL_BYTES + p * BN * K::PITCH, FIRST_EARLY ? &maps.x2 : &maps.x1, 64 * p, head, pos, w.b, full + st);
-                    if (MODE == kGradKV) bulk_load(tile_stat + st * K::STAT_BYTES, attn_stat(a, w.b, head, pos), K::STAT_BYTES, full + st);
+                        tma_load(tile_late + st.at * K::COL_BYTES + p * BN * K::PITCH, FIRST_EARLY ? &maps.x2 : &maps.x1, 64 * p, head, pos, w.b, full + st.at);
+                    if (MODE == kGradKV) bulk_load(tile_stat + st.at * K::STAT_BYTES, attn_stat(a, w.b, head, pos), K::STAT_BYTES, full + st.at);
                     ++it;
+                    st.next();
+                    se.next();
                 }
                 pos += BN;
                 if (MODE == kGradKV && pos >= a.Q) {
@@ -360,15 +345,12 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
                     ++head;
                 }
             }
-            if (ok) {                  // the end, for all
-                ok = it < EARLY || bar_wait_warp(empty_early + it % EARLY, (it / EARLY - 1) & 1, dead, a.err);
-                ok = ok && (it < STAGES || bar_wait_warp(empty + it % STAGES, (it / STAGES - 1) & 1, dead, a.err));
-                if (ok) {
-                    if (lane == 0) info[it % INFO].cls = 0;
-                    __syncwarp();
-                    bar_arrive_one(full_early + it % EARLY);
-                    bar_arrive_one(full + it % STAGES);
-                }
+            // the end, for all
+            if (ok && bar_wait_all(dead, a.err, Phase{empty_early + se.at, se.phase ^ 1u}, Phase{empty + st.at, st.phase ^ 1u})) {
+                if (lane == 0) info[it % INFO].cls = 0;
+                __syncwarp();
+                bar_arrive_one(full_early + se.at);
+                bar_arrive_one(full + st.at);
             }
             if (*dead) {               // copies under way end before the block does
                 uint32_t off = 0u;
@@ -384,71 +366,57 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
             const uint32_t bias_at = desc_low(shared_at(tile_bias), 128), ones_at = desc_low(shared_at(ones), 128);
             constexpr uint32_t id = mma_desc<BF16, BN, false>(), high = desc_high<K::PITCH>(), plain = desc_high_plain(256);
             constexpr int per = K::PITCH / 32;      // steps of 16 channels in a panel
-            bool ok = true;
-            VCLKDEF
-            for (int it = 0;; ++it) {
-                const int st = it % STAGES, se = it % EARLY;
-                VCLK(0);
-                // the columns are free: the last scores are read, and (ALIAS: these became
-                // weights) the weights that will be written over are used
-                const Phase none = {nullptr, 0}, used = {tc_bar<K::WEIGHTS>(done, it - 1), tc_phase<K::WEIGHTS>(it - 1)};
-                const Phase free = it == 0 ? none : !K::ALIAS ? Phase{s_free, (uint32_t)(it - 1) & 1} : MODE == kGradKV ? Phase{p_done, (uint32_t)(it - 1) & 1} : used;
-                const Phase older = K::WEIGHTS == 2 && it > 1 ? Phase{tc_bar<K::WEIGHTS>(done, it - 2), tc_phase<K::WEIGHTS>(it - 2)} : none;
-                ok = bar_wait_all(dead, a.err, Phase{full_early + se, (uint32_t)(it / EARLY) & 1});
-                VCLK(1);
-                if (!ok) break;
-                const bool end = info[it % INFO].cls == 0;
-                if (!end && (BACK || it == 0)) {       // (a block without a tile has fetched nothing)
-                    ok = bar_wait_all(dead, a.err, it == 0 ? Phase{a_full, 0} : none, BACK ? Phase{full + st, (uint32_t)(it / STAGES) & 1} : none,
-                                      MODE == kGradKV ? Phase{bias_full + st, (uint32_t)(it / STAGES) & 1} : none);
-                    if (!ok) break;
-                }
-                VCLK(2);
-                ok = bar_wait_all(dead, a.err, free, older);
-                if (!ok) break;
-                VCLK(2);
-                VCLK(3);
-                if (end) {             // not before: it would be taken for the last scores' arrival
-                    VCLKP2("scores", it)
-                    bar_arrive_one(s_full);
-                    break;
-                }
-                tmem_after_sync();
-                const uint32_t x_late = late + st * desc_step(K::COL_BYTES), x_early = early + se * desc_step(K::COL_BYTES);
-                const uint32_t x1 = FIRST_EARLY ? x_early : x_late, x2 = FIRST_EARLY ? x_late : x_early;
-                const uint32_t columns = bias_at + st * desc_step(K::BIAS_BYTES);
+            // the products of a row tile and a column tile
+            auto product = [&](uint32_t d, uint32_t rows, uint32_t columns) {
 #pragma unroll
                 for (int k = 0; k < DP / 16; ++k) {
                     if (k >= steps) break;
-                    const uint32_t ra = desc_step(k / per * (kTcRows * K::PITCH) + k % per * 32), rx = desc_step(k / per * (BN * K::PITCH) + k % per * 32);
-                    mma_shared<id, high>(tmem, a1 + ra, x1 + rx, k > 0);
+                    mma_shared<id, high>(d, rows + desc_step(k / per * (kTcRows * K::PITCH) + k % per * 32),
+                                         columns + desc_step(k / per * (BN * K::PITCH) + k % per * 32), k > 0);
                 }
+            };
+            bool ok = true;
+            Ring<STAGES> st;
+            Ring<EARLY> se;
+            for (int it = 0;; ++it) {
+                // The tiles are there; and the columns are free: the last scores are read, and
+                // (ALIAS: these became weights) the weights that will be written over are used.
+                const uint32_t last_phase = (it & 1) ^ 1u;
+                const Phase tile = {full_early + se.at, se.phase}, tile2 = {BACK ? full + st.at : full_early + se.at, BACK ? st.phase : se.phase};
+                const Phase tile3 = MODE == kGradKV ? Phase{bias_full + st.at, st.phase} : tile;
+                const Phase free = K::SPLIT ? Phase{p_done, last_phase} : K::ALIAS ? Phase{done, last_phase} : Phase{s_free, last_phase};
+                const Phase used = K::WEIGHTS == 2 ? Phase{done + (it & 1), ((it >> 1) & 1) ^ 1u} : free;
+                ok = MODE == kGradKV ? bar_wait_all(dead, a.err, tile, tile2) && (info[it % INFO].cls == 0 || bar_wait(tile3.bar, tile3.parity, dead, a.err))
+                   : BACK ? bar_wait_all(dead, a.err, tile, tile2) : bar_wait(tile.bar, tile.parity, dead, a.err);
+                if (!ok) break;
+                const bool end = info[it % INFO].cls == 0;
+                if (it == 0 && !end && !bar_wait(a_full, 0, dead, a.err)) break;
+                ok = K::WEIGHTS == 2 ? bar_wait_all(dead, a.err, free, used) : bar_wait(free.bar, free.parity, dead, a.err);
+                if (!ok) break;
+                tmem_after_sync();
+                if (end) {             // not before: it would be taken for the last scores' arrival
+                    bar_arrive_one(s_full);
+                    break;
+                }
+                const uint32_t x_late = late + st.at * desc_step(K::COL_BYTES), x_early = early + se.at * desc_step(K::COL_BYTES);
+                const uint32_t columns = bias_at + st.at * desc_step(K::BIAS_BYTES);
+                product(tmem, a1, FIRST_EARLY ? x_early : x_late);
                 if (MODE == kGradKV) mma_shared<id, plain>(tmem, ones_at, columns, true);
-                if (MODE == kForward) mma_commit(empty_early + se);
+                if (MODE == kForward) mma_commit(empty_early + se.at);
                 if (!BACK || K::SPLIT) mma_commit(s_full);
-                VCLK(4);
                 if (BACK) {
-                    if (it > 0) {
-                        ok = K::ALIAS ? bar_wait_all(dead, a.err, used) : !K::SPLIT || bar_wait_all(dead, a.err, Phase{d_free, (uint32_t)(it - 1) & 1});
+                    if (K::SPLIT) {
+                        ok = bar_wait(done, last_phase, dead, a.err);
                         if (!ok) break;
                         tmem_after_sync();
                     }
-                    VCLK(5);
-#pragma unroll
-                    for (int k = 0; k < DP / 16; ++k) {
-                        if (k >= steps) break;
-                        const uint32_t ra = desc_step(k / per * (kTcRows * K::PITCH) + k % per * 32), rx = desc_step(k / per * (BN * K::PITCH) + k % per * 32);
-                        mma_shared<id, high>(tmem + BN, a2 + ra, x2 + rx, k > 0);
-                    }
+                    product(tmem + BN, a2, x_early);
                     if (MODE == kGradKV) mma_shared<id, plain>(tmem + BN, ones_at + desc_step(K::ONES_BYTES), columns, true);
-                    if (MODE == kGradQ) mma_commit(empty_early + se);
+                    if (MODE == kGradQ) mma_commit(empty_early + se.at);
                     mma_commit(K::SPLIT ? d_full : s_full);
-                    VCLK(6);
-#ifdef V_LAT2
-                    bar_wait_all(dead, a.err, Phase{K::SPLIT ? d_full : s_full, (uint32_t)it & 1});
-                    VCLK(5);
-#endif
                 }
+                st.next();
+                se.next();
             }
             if (!ok) {                 // MMAs under way end before the block does
                 uint32_t off = 0u;
@@ -460,62 +428,55 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
             const uint32_t late = desc_low(shared_at(tile_late), BN * K::PITCH), early = desc_low(shared_at(tile_early), BN * K::PITCH);
             constexpr uint32_t id = mma_desc<BF16, DP, true>(), high = desc_high<K::PITCH>();
             constexpr int PART_STEPS = K::PART / 16;
+            auto product = [&](uint32_t d, uint32_t weights, uint32_t columns, bool add) {
+#pragma unroll
+                for (int k = 0; k < BN / 16; ++k)      // over the scores each part's weights are in its own columns
+                    mma_tmem<id, high>(d, weights + (K::ALIAS ? k / PART_STEPS * K::PART + k % PART_STEPS * 8 : 8 * k), columns + desc_step(k * 16 * K::PITCH), add || k > 0);
+            };
             bool ok = true;
-            VCLKDEF
+            Ring<STAGES> st;
+            Ring<EARLY> se;
             for (int it = 0;; ++it) {
-                const int st = it % STAGES, se = it % EARLY;
-                VCLK(0);
-                ok = bar_wait_all(dead, a.err, Phase{full + st, (uint32_t)(it / STAGES) & 1}, Phase{MODE == kGradKV ? full_early + se : nullptr, (uint32_t)(it / EARLY) & 1});
-                VCLK(1);
-                if (!info[it % INFO].cls) VCLKP2("second", it)
+                ok = MODE == kGradKV ? bar_wait_all(dead, a.err, Phase{full + st.at, st.phase}, Phase{full_early + se.at, se.phase})
+                                     : bar_wait(full + st.at, st.phase, dead, a.err);
                 if (!ok || !info[it % INFO].cls) break;
-                const uint32_t x_late = late + st * desc_step(K::COL_BYTES), x_early = early + se * desc_step(K::COL_BYTES);
-                // weights: P, then dS; over the scores each part's in the part's own columns
-                const uint32_t p = tmem + (K::ALIAS ? 0 : K::SCORES + (K::WEIGHTS == 2 ? it % 2 * K::WIDE : 0));
-                const uint32_t ds = MODE != kGradKV ? p : K::ALIAS ? p + BN : p + BN / 2, acc = tmem + K::ACC;
-                auto at = [](int k) { return (uint32_t)(K::ALIAS ? k / PART_STEPS * K::PART + k % PART_STEPS * 8 : 8 * k); };
+                const uint32_t x_late = late + st.at * desc_step(K::COL_BYTES), x_early = early + se.at * desc_step(K::COL_BYTES), acc = tmem + K::ACC;
+                // weights: P, then dS
+                const uint32_t p = tmem + (K::ALIAS ? 0 : K::SCORES + (K::WEIGHTS == 2 ? (it & 1) * K::WIDE : 0));
+                const uint32_t ds = MODE != kGradKV ? p : K::ALIAS ? p + BN : p + BN / 2;
                 if (K::SPLIT) {
-                    ok = bar_wait_all(dead, a.err, Phase{p_ready, (uint32_t)it & 1});
+                    ok = bar_wait(p_ready, it & 1, dead, a.err);
                     if (!ok) break;
                     tmem_after_sync();
-#pragma unroll
-                    for (int k = 0; k < BN / 16; ++k) mma_tmem<id, high>(acc, p + at(k), x_early + desc_step(k * 16 * K::PITCH), it > 0 || k > 0);
+                    product(acc, p, x_early, it > 0);
                     mma_commit(p_done);
                 }
-                ok = bar_wait_all(dead, a.err, Phase{tc_bar<K::WEIGHTS>(ready, it), tc_phase<K::WEIGHTS>(it)});
+                ok = bar_wait(tc_bar<K::WEIGHTS>(ready, it), tc_phase<K::WEIGHTS>(it), dead, a.err);
                 if (!ok) break;
-                VCLK(2);
                 tmem_after_sync();
-#pragma unroll
-                for (int k = 0; k < BN / 16; ++k) {
-                    if (MODE == kGradKV && !K::SPLIT) mma_tmem<id, high>(acc, p + at(k), x_early + desc_step(k * 16 * K::PITCH), it > 0 || k > 0);
-                    mma_tmem<id, high>(acc + (MODE == kGradKV ? DP : 0), ds + at(k), x_late + desc_step(k * 16 * K::PITCH), it > 0 || k > 0);
-                }
-                if (MODE == kGradKV) mma_commit(empty_early + se);    // dP, which reads it too, is there
-                mma_commit(empty + st);
+                if (MODE == kGradKV && !K::SPLIT) product(acc, p, x_early, it > 0);
+                product(acc + (MODE == kGradKV ? DP : 0), ds, x_late, it > 0);
+                if (MODE == kGradKV) mma_commit(empty_early + se.at);    // dP, which reads it too, is there
+                mma_commit(empty + st.at);
                 mma_commit(tc_bar<K::WEIGHTS>(done, it));  // last: the block ends after it has arrived
-                VCLK(4);
-#ifdef V_LAT2
-                bar_wait_all(dead, a.err, Phase{tc_bar<K::WEIGHTS>(done, it), tc_phase<K::WEIGHTS>(it)});
-                VCLK(5);
-#endif
+                st.next();
+                se.next();
             }
             if (!ok) {
                 uint32_t off = 0u;
                 mma_commit(last + 1);
                 bar_wait(last + 1, 0, &off, nullptr);
             }
-        }
-        else if (MODE == kGradKV) {
+        } else if (MODE == kGradKV) {
             // -------------------------------------------- the queries' statistics as an operand
-            for (int it = 0;; ++it) {
-                const int st = it % STAGES;
-                if (!bar_wait_warp(full + st, (it / STAGES) & 1, dead, a.err) || !info[it % INFO].cls) break;
+            Ring<STAGES> st;
+            for (int it = 0;; ++it, st.next()) {
+                if (!bar_wait(full + st.at, st.phase, dead, a.err) || !info[it % INFO].cls) break;
                 for (int i = lane; i < BN; i += 32)
-                    bias.put(tile_bias + st * K::BIAS_BYTES, i, reinterpret_cast<const float *>(tile_stat + st * K::STAT_BYTES) + i / 2 * 4 + i % 2);
+                    bias.put(tile_bias + st.at * K::BIAS_BYTES, i, reinterpret_cast<const float *>(tile_stat + st.at * K::STAT_BYTES) + i / 2 * 4 + i % 2);
                 shared_to_async();
                 __syncwarp();
-                bar_arrive_one(bias_full + st);
+                bar_arrive_one(bias_full + st.at);
             }
         }
         __syncwarp();
@@ -542,17 +503,16 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
 
         // after a wait that ran out (ok false) the group's threads go on to their results'
         // barriers
-        VCLKDEF
         bool ok = true;
         int it = 0;
-        for (;; ++it) {
-            const int st = it % STAGES;
+        Ring<STAGES> st;
+        for (;; ++it, st.next()) {
             const uint32_t at_p = mine + (K::ALIAS ? PART * part : K::SCORES + (K::WEIGHTS == 2 ? it % 2 * K::WIDE : 0) + PART / 2 * part);
             const uint32_t at_ds = MODE != kGradKV ? at_p : K::ALIAS ? at_p + BN : at_p + BN / 2;
             // a mask's words are asked for before the scores are there
             // (their tile's barrier moves on only after this tile's second product)
-            if (a.classes) ok = bar_wait_warp(full + st, (it / STAGES) & 1, dead, a.err);
-            else ok = bar_wait_warp(s_full, it & 1, dead, a.err);
+            if (a.classes) ok = bar_wait(full + st.at, st.phase, dead, a.err);
+            else ok = bar_wait(s_full, it & 1, dead, a.err);
             if (!ok) break;
             const TcTile tile = info[it % INFO];
             const int cls = tile.cls;
@@ -563,18 +523,15 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
 #pragma unroll
                 for (int i = 0; i < PART / 32; ++i) bits[i] = attn_word<MODE>(a, words, tile.pos + PART * part + 32 * i);
             }
-            VCLK(0);
-            if (a.classes) ok = bar_wait_warp(s_full, it & 1, dead, a.err);
+            if (a.classes) ok = bar_wait(s_full, it & 1, dead, a.err);
             if (!ok) break;
             tmem_after_sync();
-            VCLK(1);
             // the row's scores, and dP beside them unless it comes later
             uint32_t v[PART], dp[BACK ? PART : 1];
             if (any_valid) {
                 if constexpr (BACK && !K::SPLIT) tmem_read_two<PART>(v, dp, mine + PART * part, mine + BN + PART * part);
                 else tmem_read<PART>(v, mine + PART * part);
             }
-            VCLK(2);
             if (!K::ALIAS) {
                 tmem_before_sync();
                 bar_arrive_warp(s_free);
@@ -585,7 +542,6 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
                 for (int k = 0; k < PART; ++k)
                     if (!((bits[k / 32] >> (k % 32)) & 1u)) v[k] = 0xff800000u;
             }
-            VCLK(3);
             const float2 c2 = make_float2(c, c);
             auto pair = [](const uint32_t *x) { return make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])); };
             uint32_t out[MODE == kGradKV ? PART / 2 : 1], out2[BACK ? PART / 2 : 1];     // weights: P, dS
@@ -602,7 +558,7 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
                     if (grow) top = high;
                     sum *= f;
                     if (it > 0) {
-                        ok = bar_wait_warp(tc_bar<K::WEIGHTS>(done, it - 1), tc_phase<K::WEIGHTS>(it - 1), dead, a.err);
+                        ok = bar_wait(tc_bar<K::WEIGHTS>(done, it - 1), tc_phase<K::WEIGHTS>(it - 1), dead, a.err);
                         tmem_after_sync();
 #pragma unroll 1
                         for (int i = 0; ok && i < DP; i += 16) {
@@ -618,7 +574,7 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
                 const float2 ref2 = make_float2(-ref, -ref);
                 float2 sums[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
                 if (K::WEIGHTS == 1 && it > 0) {   // the weights' columns are free
-                    ok = ok && bar_wait_warp(tc_bar<K::WEIGHTS>(done, it - 1), tc_phase<K::WEIGHTS>(it - 1), dead, a.err);
+                    ok = ok && bar_wait(tc_bar<K::WEIGHTS>(done, it - 1), tc_phase<K::WEIGHTS>(it - 1), dead, a.err);
                     tmem_after_sync();
                 }
 #pragma unroll
@@ -659,11 +615,9 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
                     }
                     tmem_before_sync();
                     bar_arrive_warp(p_ready);
-                    VCLK(4);
-                    ok = bar_wait_warp(d_full, it & 1, dead, a.err);
+                    ok = bar_wait(d_full, it & 1, dead, a.err);
                     if (!ok) break;
                     tmem_after_sync();
-                    VCLK(7);
                     if (any_valid) {
                         tmem_read<PART>(dp, mine + BN + PART * part);
 #pragma unroll
@@ -681,29 +635,24 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
                     }
                 }
             }
-            VCLK(4);
             // the weights' columns are free (forward's rows have waited)
             if (K::WEIGHTS == 1 && it > 0 && (BACK || !any_valid)) {
-                ok = ok && bar_wait_warp(tc_bar<K::WEIGHTS>(done, it - 1), tc_phase<K::WEIGHTS>(it - 1), dead, a.err);
+                ok = ok && bar_wait(tc_bar<K::WEIGHTS>(done, it - 1), tc_phase<K::WEIGHTS>(it - 1), dead, a.err);
                 tmem_after_sync();
             }
             if (!ok) break;
-            VCLK(7);
             if (any_valid) {
                 if constexpr (MODE == kGradKV && !K::SPLIT) tmem_store<PART / 2>(at_p, out);
                 if constexpr (BACK) tmem_store<PART / 2>(at_ds, out2);
             }
-            VCLK(5);
             if (!ok) break;
             if (any_valid) tmem_wait_store();
             tmem_before_sync();
             bar_arrive_warp(tc_bar<K::WEIGHTS>(ready, it));
-            VCLK(6);
         }
 
-        VCLKPRINT
         // ------------------------------------------------ results
-        if (ok && it > 0) ok = bar_wait_warp(tc_bar<K::WEIGHTS>(done, it - 1), tc_phase<K::WEIGHTS>(it - 1), dead, a.err);
+        if (ok && it > 0) ok = bar_wait(tc_bar<K::WEIGHTS>(done, it - 1), tc_phase<K::WEIGHTS>(it - 1), dead, a.err);
         tmem_after_sync();
         const int count = it;          // column tiles of the block
         if (any_valid && __all_sync(0xffffffffu, ok && !*dead)) {

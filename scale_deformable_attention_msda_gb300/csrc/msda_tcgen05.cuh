@@ -54,9 +54,9 @@ __device__ __forceinline__ bool bar_try(uint64_t *bar, uint32_t parity) {
                  : "memory");
     return done != 0;
 }
-// False when the wait ran out, here or in another wait of the block.
-__device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity, volatile uint32_t *dead, unsigned *err) {
-    if (bar_try(bar, parity)) return true;
+// The rest of a wait whose first look found the phase not there. False when it ran out,
+// here or in another wait of the block.
+__device__ __forceinline__ bool bar_wait_more(uint64_t *bar, uint32_t parity, volatile uint32_t *dead, unsigned *err) {
     unsigned long long start = 0;
     for (uint32_t i = 1;; ++i) {
         if (bar_try(bar, parity)) return true;
@@ -70,27 +70,38 @@ __device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity, volatil
     if (err) atomicOr(err, 2u);
     return false;
 }
-
-// The same for a whole warp: the lanes agree.
-__device__ __forceinline__ bool bar_wait_warp(uint64_t *bar, uint32_t parity, volatile uint32_t *dead, unsigned *err) {
-    return __all_sync(0xffffffffu, bar_wait(bar, parity, dead, err));
+// For a whole warp, whose lanes agree. A barrier's phase of the other parity than the one
+// under way counts as there: so does, before the first, that of parity 1.
+__device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity, volatile uint32_t *dead, unsigned *err) {
+    if (__all_sync(0xffffffffu, bar_try(bar, parity))) return true;
+    return __all_sync(0xffffffffu, bar_wait_more(bar, parity, dead, err));
 }
-// A barrier and the parity of the phase waited for; NULL: nothing.
+// A barrier and the parity of the phase waited for.
 struct Phase {
     uint64_t *bar;
     uint32_t parity;
 };
-// Waits for all of them. A look at a barrier takes 100 cycles until it is acted on: these
-// look at all before they act.
+// Waits for all of them, and looks at all before it acts on one.
 template <class... P>
 __device__ __forceinline__ bool bar_wait_all(volatile uint32_t *dead, unsigned *err, P... phases) {
     bool now = true;
-    ((now = (!phases.bar || bar_try(phases.bar, phases.parity)) && now), ...);
+    ((now = bar_try(phases.bar, phases.parity) && now), ...);
     if (__all_sync(0xffffffffu, now)) return true;
     bool ok = true;
-    ((ok = ok && (!phases.bar || bar_wait(phases.bar, phases.parity, dead, err))), ...);
+    ((ok = ok && bar_wait_more(phases.bar, phases.parity, dead, err)), ...);
     return __all_sync(0xffffffffu, ok);
 }
+// Place and phase in a ring of N.
+template <int N> struct Ring {
+    int at = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void next() {
+        if (++at == N) {
+            at = 0;
+            phase ^= 1u;
+        }
+    }
+};
 
 // What this thread wrote to shared memory is there for the MMAs that follow.
 __device__ __forceinline__ void shared_to_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
