@@ -13,7 +13,7 @@ using msda::AttnMode;
 constexpr int kSMs = 152;
 constexpr int64_t kMaxPositions = (int64_t)1 << 30, kMaxHeads = 65536, kMaxStride = (int64_t)1 << 36;
 constexpr int64_t kMaxTiles = ((int64_t)1 << 31) - 1;
-constexpr int kDeltaBlocks = 304;
+constexpr int kDeltaBlocks = 608;
 
 int elem_bytes(msda_dtype_t dt) { return dt == MSDA_F32 ? 4 : 2; }
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -84,8 +84,9 @@ ModePlan plan_mode(const msda_attention_dims_t &d, AttnMode mode, int R, int C, 
 int tile_rows(msda_dtype_t dt) { return dt == MSDA_F32 ? 64 : 128; }
 
 ModePlan plan_for(const msda_attention_dims_t &d, msda_dtype_t dt, AttnMode mode) {
-    if (dt == MSDA_F32) return plan_mode(d, mode, 64, 64, kSMs, 4);
-    const int columns = msda::tc_columns(mode, (int)d.D), blocks = msda::tc_blocks(mode, (int)d.D);
+    if (dt == MSDA_F32) return plan_mode(d, mode, 64, 64, kSMs * (d.D <= 32 ? 3 : d.D <= 64 ? 2 : 1), 1);
+    const bool is_short = msda::tc_short(mode, d.D, d.Q, d.M / d.N);
+    const int columns = msda::tc_columns(mode, d.D, is_short), blocks = msda::tc_blocks(mode, d.D, is_short);
     return plan_mode(d, mode, 128, columns, kSMs * blocks, 4);
 }
 
@@ -264,8 +265,10 @@ msda_status_t msda_attention_backward(const void *grad_out, const void *q, const
     a.stat = reinterpret_cast<float *>(ws + w.stat);
     a.stat_row = (int)(ceil_div(d.Q, 128) * 128);
     a.up = dtype == MSDA_F16 ? msda::kHalfUp : 0.0f;
-    const int64_t rows = d.B * d.Q * d.M;
-    a.norms = (int)(rows < 1 ? 1 : rows < kDeltaBlocks ? rows : kDeltaBlocks);
+    // a block of 256 threads has 64 rows at once at the least
+    const int64_t rows = d.B * a.stat_row * d.M, keys = dtype == MSDA_F16 ? d.B * d.S * d.N : 0;
+    const int64_t delta_blocks = ceil_div(rows > keys ? rows : keys, 64);
+    a.norms = (int)(delta_blocks < 1 ? 1 : delta_blocks < kDeltaBlocks ? delta_blocks : kDeltaBlocks);
     if (dtype == MSDA_F16) {
         a.norm_do = reinterpret_cast<float *>(ws + w.norms);
         a.norm_v = a.norm_do + kDeltaBlocks;

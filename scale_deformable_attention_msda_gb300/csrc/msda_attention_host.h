@@ -11,9 +11,14 @@ cudaError_t launch_attention_f32(int mode, const AttnArgs &a, int64_t blocks, cu
 cudaError_t launch_attention_bf16(int mode, const AttnArgs &a, int64_t blocks, cudaStream_t stream);
 cudaError_t launch_attention_f16(int mode, const AttnArgs &a, int64_t blocks, cudaStream_t stream);
 
+// Whether a key tile's few queries are walked by small blocks, two an SM, one starting
+// while the other ends, rather than by one an SM with tiles of 128 columns. 100 queries of
+// 32 heads over 4,096 keys, fp16, D 32, the whole backward: 73 us, 94 with large blocks; 300
+// queries 22.5 us, 20.4; 512 queries, D 64, 36.7 us, 25.8.
+constexpr bool tc_short(int mode, int64_t D, int64_t Q, int64_t G) { return mode == kGradKV && D <= 64 && G * ((Q + 63) / 64 * 64) <= 256; }
 // The 16-bit kernels' columns of a tile, and their blocks of an SM.
-constexpr int tc_columns(int mode, int D) { return mode == kForward && D > 64 ? 64 : 128; }
-constexpr int tc_blocks(int mode, int D) { return mode != kForward ? 1 : 2; }
+constexpr int tc_columns(int mode, int64_t D, bool is_short) { return is_short || (mode == kForward && D > 64) ? 64 : 128; }
+constexpr int tc_blocks(int mode, int64_t D, bool is_short) { return is_short || mode == kForward ? 2 : 1; }
 
 // What the mask is made of before it is packed: bytes at strides.
 struct AttnMaskSource {

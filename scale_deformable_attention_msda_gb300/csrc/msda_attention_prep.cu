@@ -25,13 +25,17 @@ __global__ void __launch_bounds__(256) attn_pack_kernel(const AttnMaskSource m, 
     const int64_t bh = t / tq;
     const int b = (int)(bh / m.M), h = (int)(bh % m.M);
     const uint8_t *from = m.p + b * m.batch + h * m.head;
-#pragma unroll 8
-    for (int i = 0; i < kPackQ * (kPackK / 32) / 8; ++i) {
-        const int r = warp + 8 * (i / (kPackK / 32)), c = i % (kPackK / 32);
-        const int q = q0 + r, k = k0 + 32 * c + lane;
-        const bool on = q < m.Q && k < m.S && from[q * m.query + k * m.key] != 0;
-        const uint32_t bits = __ballot_sync(0xffffffffu, on);
-        if (lane == c) word[r][c] = bits;
+    constexpr int kWords = kPackQ * (kPackK / 32) / 8;     // of a warp; all its loads are under way at once
+    uint8_t byte[kWords];
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+        const int q = q0 + warp + 8 * (i / (kPackK / 32)), k = k0 + 32 * (i % (kPackK / 32)) + lane;
+        byte[i] = q < m.Q && k < m.S ? from[q * m.query + k * m.key] : 0;
+    }
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+        const uint32_t bits = __ballot_sync(0xffffffffu, byte[i] != 0);
+        if (lane == i % (kPackK / 32)) word[warp + 8 * (i / (kPackK / 32))][i % (kPackK / 32)] = bits;
     }
     __syncthreads();
     const int rows = min(kPackQ, m.Q - q0);
@@ -66,66 +70,81 @@ __global__ void __launch_bounds__(256) attn_pack_kernel(const AttnMaskSource m, 
     }
 }
 
-constexpr int kDeltaThreads = 512, kDeltaBlocks = 304;
+constexpr int kDeltaThreads = 256;
 
 // The queries' stat: the row sums delta = sum over channels of dO out, L lanes a row
 // of 16 bytes each, beside the forward's lse. fp16 (norm_do given): also the largest
 // finite |dO_i|^2 and |v_j|^2 of what this block has seen.
 template <typename T, int L>
 __global__ void __launch_bounds__(kDeltaThreads) attn_delta_kernel(const AttnArgs a) {
-    constexpr int V = 16 / sizeof(T), per = kDeltaThreads / L;
+    constexpr int V = 16 / sizeof(T), per = kDeltaThreads / L, AT_ONCE = 4;
     const int lane = threadIdx.x % L, d = lane * V;
-    const int64_t rows = (int64_t)a.B * a.stat_row * a.M;
+    const int64_t rows = (int64_t)a.B * a.stat_row * a.M, step = (int64_t)gridDim.x * per;
     float most_do = 0.0f, most_v = 0.0f;
-    for (int64_t r0 = (int64_t)blockIdx.x * per; r0 < rows; r0 += (int64_t)gridDim.x * per) {
-        const int64_t r = r0 + threadIdx.x / L, bq = r / a.M;
-        const int m = (int)(r % a.M), b = (int)(bq / a.stat_row), q = (int)(bq % a.stat_row);
-        const bool valid = r < rows && q < a.Q;
-        float dot = 0.0f, square = 0.0f;
-        if (valid && d < a.D) {
-            const int64_t at = (((int64_t)b * a.Q + q) * a.M + m) * a.D + d;
-            float x[V], y[V];
-            unpack16<T>(x, ldg16(static_cast<const T *>(a.go.p) + at));
-            unpack16<T>(y, ldg16(static_cast<const T *>(a.o.p) + at));
-            if (a.rest) {
-                float z[V];
-                unpack16<T>(z, ldg16(static_cast<const T *>(a.rest) + at));
+    for (int64_t r0 = (int64_t)blockIdx.x * per + threadIdx.x / L; r0 - threadIdx.x / L < rows; r0 += AT_ONCE * step) {
+        uint4 x[AT_ONCE], y[AT_ONCE], z[AT_ONCE];
+        float *to[AT_ONCE];
+        float lse[AT_ONCE];
 #pragma unroll
-                for (int i = 0; i < V; ++i) y[i] += z[i];
-            }
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                dot = fmaf(x[i], y[i], dot);
-                square = fmaf(x[i], x[i], square);
+        for (int i = 0; i < AT_ONCE; ++i) {
+            const int64_t r = r0 + i * step, bq = r / a.M;
+            const int m = (int)(r - bq * a.M), b = (int)(bq / a.stat_row), q = (int)(bq - (int64_t)b * a.stat_row);
+            to[i] = r < rows ? attn_stat(a, b, m, q) : nullptr;
+            x[i] = y[i] = z[i] = make_uint4(0u, 0u, 0u, 0u);
+            lse[i] = -INFINITY;
+            if (r < rows && q < a.Q) {
+                if (lane == 0) lse[i] = a.lse[((int64_t)b * a.M + m) * a.Q + q];
+                const int64_t at = (((int64_t)b * a.Q + q) * a.M + m) * a.D + d;
+                if (d < a.D) {
+                    x[i] = ldg16(static_cast<const T *>(a.go.p) + at);
+                    y[i] = ldg16(static_cast<const T *>(a.o.p) + at);
+                    if (a.rest) z[i] = ldg16(static_cast<const T *>(a.rest) + at);
+                }
             }
         }
 #pragma unroll
-        for (int off = L / 2; off > 0; off >>= 1) {
-            dot += __shfl_xor_sync(0xffffffffu, dot, off);
-            square += __shfl_xor_sync(0xffffffffu, square, off);
-        }
-        if (isfinite(square)) most_do = fmaxf(most_do, square);
-        if (r < rows && lane == 0) {
-            float *to = attn_stat(a, b, m, q);
-            to[0] = valid ? a.up - attn_lse2(a.lse[((int64_t)b * a.M + m) * a.Q + q]) : -INFINITY;
-            to[2] = valid ? -dot : 0.0f;
+        for (int i = 0; i < AT_ONCE; ++i) {
+            float fx[V], fy[V], fz[V], dot = 0.0f, square = 0.0f;
+            unpack16<T>(fx, x[i]);
+            unpack16<T>(fy, y[i]);
+            unpack16<T>(fz, z[i]);
+#pragma unroll
+            for (int k = 0; k < V; ++k) {
+                dot = fmaf(fx[k], fy[k] + fz[k], dot);
+                square = fmaf(fx[k], fx[k], square);
+            }
+#pragma unroll
+            for (int off = L / 2; off > 0; off >>= 1) {
+                dot += __shfl_xor_sync(0xffffffffu, dot, off);
+                square += __shfl_xor_sync(0xffffffffu, square, off);
+            }
+            if (isfinite(square)) most_do = fmaxf(most_do, square);
+            if (to[i] && lane == 0) {  // past the last query: -infinity and 0
+                to[i][0] = a.up - attn_lse2(lse[i]);
+                to[i][2] = -dot;
+            }
         }
     }
     if (!a.norm_do) return;
     const int64_t keys = (int64_t)a.B * a.S * a.N;
-    for (int64_t r0 = (int64_t)blockIdx.x * per; r0 < keys; r0 += (int64_t)gridDim.x * per) {
-        const int64_t r = r0 + threadIdx.x / L;
-        float square = 0.0f;
-        if (r < keys && d < a.D) {
-            const int64_t bs = r / a.N;
-            float x[V];
-            unpack16<T>(x, ldg16(attn_at<T>(a.v, (int)(bs / a.S), (int)(bs % a.S), (int)(r % a.N)) + d));
+    for (int64_t r0 = (int64_t)blockIdx.x * per + threadIdx.x / L; r0 - threadIdx.x / L < keys; r0 += AT_ONCE * step) {
+        uint4 x[AT_ONCE];
 #pragma unroll
-            for (int i = 0; i < V; ++i) square = fmaf(x[i], x[i], square);
+        for (int i = 0; i < AT_ONCE; ++i) {
+            const int64_t r = r0 + i * step, bs = r / a.N;
+            const int b = (int)(bs / a.S);
+            x[i] = r < keys && d < a.D ? ldg16(attn_at<T>(a.v, b, (int)(bs - (int64_t)b * a.S), (int)(r - bs * a.N)) + d) : make_uint4(0u, 0u, 0u, 0u);
         }
 #pragma unroll
-        for (int off = L / 2; off > 0; off >>= 1) square += __shfl_xor_sync(0xffffffffu, square, off);
-        if (isfinite(square)) most_v = fmaxf(most_v, square);
+        for (int i = 0; i < AT_ONCE; ++i) {
+            float fx[V], square = 0.0f;
+            unpack16<T>(fx, x[i]);
+#pragma unroll
+            for (int k = 0; k < V; ++k) square = fmaf(fx[k], fx[k], square);
+#pragma unroll
+            for (int off = L / 2; off > 0; off >>= 1) square += __shfl_xor_sync(0xffffffffu, square, off);
+            if (isfinite(square)) most_v = fmaxf(most_v, square);
+        }
     }
     __shared__ float part[2][kDeltaThreads / 32];
 #pragma unroll
@@ -154,51 +173,76 @@ template <typename T> cudaError_t launch_delta(const AttnArgs &a, cudaStream_t s
     return cudaGetLastError();
 }
 
-// Sums of the splits, four channels a thread. Forward: each split's sums are
-// relative to its own maximum, and its weight is exp2 of the distance.
-template <typename T>
+// Sums of the splits: a warp a row, four channels a lane, and where that leaves lanes the
+// splits in turn over groups of LD of them, so that all loads are under way together.
+// Forward: each split's sums are relative to its own maximum, and its weight is exp2 of
+// the distance. At most 64 splits.
+template <typename T, int LD>
 __global__ void __launch_bounds__(128) attn_join_kernel(const AttnArgs a, int mode) {
-    const int per = a.D / 4;
-    const int64_t i = (int64_t)blockIdx.x * 128 + threadIdx.x, row = i / per;
-    const int d = (int)(i % per) * 4;
+    constexpr int GROUPS = 32 / LD;
+    const int lane = threadIdx.x & 31, group = lane / LD, d = lane % LD * 4;
+    const int64_t row = (int64_t)blockIdx.x * 4 + threadIdx.x / 32, step = a.part_rows * a.D;
     if (row >= a.part_rows) return;
-    const int64_t step = a.part_rows * a.D;
-    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float weight[2] = {1.0f, 1.0f}, base = 0.0f, sum = 1.0f;       // of splits lane, lane + 32
     if (mode == kForward) {
-        const float *ml = a.part + a.splits * step + 2 * row;
-        float top = -INFINITY, sum = 0.0f;
-        for (int s = 0; s < a.splits; ++s) top = fmaxf(top, ml[2 * s * a.part_rows]);
-        const float base = top == -INFINITY ? 0.0f : top;
-        for (int s = 0; s < a.splits; ++s) {
-            const float f = exp2f(ml[2 * s * a.part_rows] - base);
-            const float4 v = *reinterpret_cast<const float4 *>(a.part + s * step + row * a.D + d);
-            sum = fmaf(f, ml[2 * s * a.part_rows + 1], sum);
-            acc = make_float4(fmaf(f, v.x, acc.x), fmaf(f, v.y, acc.y), fmaf(f, v.z, acc.z), fmaf(f, v.w, acc.w));
-        }
-        const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
-        const float v[4] = {acc.x * f, acc.y * f, acc.z * f, acc.w * f};
+        const float2 *ml = reinterpret_cast<const float2 *>(a.part + a.splits * step) + row;
+        float2 mine[2];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) attn_put<T>(a.out, a.rest, row * a.D + d + k, v[k]);
-        if (a.lse && d == 0) {
-            const int m = (int)(row % a.M);
-            const int64_t bq = row / a.M;
-            a.lse[(bq / a.Q * a.M + m) * a.Q + bq % a.Q] = sum == 0.0f ? -INFINITY : (base + log2f(sum)) * kLn2;
+        for (int i = 0; i < 2; ++i)
+            mine[i] = lane + 32 * i < a.splits ? ml[(lane + 32 * i) * a.part_rows] : make_float2(-INFINITY, 0.0f);
+        float top = fmaxf(mine[0].x, mine[1].x);
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+        base = top == -INFINITY ? 0.0f : top;
+        sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            weight[i] = exp2f(mine[i].x - base);
+            sum = fmaf(weight[i], mine[i].y, sum);
         }
-        return;
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
     }
     for (int which = 0; which < (mode == kGradKV ? 2 : 1); ++which) {
-        acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        for (int s = 0; s < a.splits; ++s) {
-            const float4 v = *reinterpret_cast<const float4 *>(a.part + (which * a.splits + s) * step + row * a.D + d);
-            acc = make_float4(acc.x + v.x, acc.y + v.y, acc.z + v.z, acc.w + v.w);
+        const float *from = a.part + which * a.splits * step + row * a.D + d;
+        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+        for (int s0 = 0; s0 < a.splits; s0 += GROUPS) {
+            const int s = s0 + group;
+            const float lo = __shfl_sync(0xffffffffu, weight[0], s & 31), hi = __shfl_sync(0xffffffffu, weight[1], s & 31);
+            if (s < a.splits && d < a.D) {
+                const float4 v = *reinterpret_cast<const float4 *>(from + s * step);
+                const float f = s < 32 ? lo : hi;
+                acc = make_float4(fmaf(f, v.x, acc.x), fmaf(f, v.y, acc.y), fmaf(f, v.z, acc.z), fmaf(f, v.w, acc.w));
+            }
         }
-        const float f = mode == kGradQ || which ? a.scale : 1.0f;
-        T *to = static_cast<T *>(mode == kGradQ ? a.gq : which ? a.gk : a.gv) + row * a.D + d;
-        to[0] = Elem<T>::from_f(acc.x * f);
-        to[1] = Elem<T>::from_f(acc.y * f);
-        to[2] = Elem<T>::from_f(acc.z * f);
-        to[3] = Elem<T>::from_f(acc.w * f);
+#pragma unroll
+        for (int off = LD; off < 32; off <<= 1) {
+            acc.x += __shfl_xor_sync(0xffffffffu, acc.x, off);
+            acc.y += __shfl_xor_sync(0xffffffffu, acc.y, off);
+            acc.z += __shfl_xor_sync(0xffffffffu, acc.z, off);
+            acc.w += __shfl_xor_sync(0xffffffffu, acc.w, off);
+        }
+        if (group > 0 || d >= a.D) continue;
+        const float f = mode == kForward ? (sum == 0.0f ? 0.0f : 1.0f / sum) : mode == kGradQ || which ? a.scale : 1.0f;
+        void *to = mode == kForward ? a.out : mode == kGradQ ? a.gq : which ? a.gk : a.gv;
+        const float v[4] = {acc.x * f, acc.y * f, acc.z * f, acc.w * f};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) attn_put<T>(to, mode == kForward ? a.rest : nullptr, row * a.D + d + k, v[k]);
     }
+    if (mode == kForward && a.lse && lane == 0) {
+        const int m = (int)(row % a.M);
+        const int64_t bq = row / a.M;
+        a.lse[(bq / a.Q * a.M + m) * a.Q + bq % a.Q] = sum == 0.0f ? -INFINITY : (base + log2f(sum)) * kLn2;
+    }
+}
+
+template <typename T> void launch_join(int mode, const AttnArgs &a, cudaStream_t stream) {
+    const unsigned blocks = (unsigned)((a.part_rows + 3) / 4);
+    if (a.D <= 16) attn_join_kernel<T, 4><<<blocks, 128, 0, stream>>>(a, mode);
+    else if (a.D <= 32) attn_join_kernel<T, 8><<<blocks, 128, 0, stream>>>(a, mode);
+    else if (a.D <= 64) attn_join_kernel<T, 16><<<blocks, 128, 0, stream>>>(a, mode);
+    else attn_join_kernel<T, 32><<<blocks, 128, 0, stream>>>(a, mode);
 }
 
 }  // namespace
@@ -216,10 +260,9 @@ cudaError_t launch_attention_delta(const AttnArgs &a, msda_dtype_t dt, cudaStrea
 }
 
 cudaError_t launch_attention_join(int mode, const AttnArgs &a, msda_dtype_t dt, cudaStream_t stream) {
-    const unsigned blocks = (unsigned)((a.part_rows * (a.D / 4) + 127) / 128);
-    if (dt == MSDA_F32) attn_join_kernel<float><<<blocks, 128, 0, stream>>>(a, mode);
-    else if (dt == MSDA_BF16) attn_join_kernel<__nv_bfloat16><<<blocks, 128, 0, stream>>>(a, mode);
-    else attn_join_kernel<__half><<<blocks, 128, 0, stream>>>(a, mode);
+    if (dt == MSDA_F32) launch_join<float>(mode, a, stream);
+    else if (dt == MSDA_BF16) launch_join<__nv_bfloat16>(mode, a, stream);
+    else launch_join<__half>(mode, a, stream);
     return cudaGetLastError();
 }
 

@@ -35,46 +35,21 @@ constexpr int kTcRows = 128;
 template <int BN_, int PARTS_, int STAGES_, int EARLY_, int BLOCKS_, int WEIGHTS_> struct TcSizes {
     static constexpr int BN = BN_, PARTS = PARTS_, STAGES = STAGES_, EARLY = EARLY_, BLOCKS = BLOCKS_, WEIGHTS = WEIGHTS_;
 };
-template <int MODE, int DP> struct TcConfig;
-#ifndef F32
-#define F32 128, 1, 3, 3, 2, 1
-#endif
-#ifndef F64
-#define F64 128, 1, 2, 2, 2, 1
-#endif
-#ifndef F128
-#define F128 64, 1, 2, 2, 2, 2
-#endif
-#ifndef Q32
-#define Q32 128, 2, 4, 4, 1, 2
-#endif
-#ifndef Q64
-#define Q64 128, 2, 3, 3, 1, 2
-#endif
-#ifndef Q128
-#define Q128 128, 2, 2, 2, 1, 2
-#endif
-#ifndef KV32
-#define KV32 128, 2, 4, 4, 1, 1
-#endif
-#ifndef KV64
-#define KV64 128, 2, 3, 3, 1, 1
-#endif
-#ifndef KV128
-#define KV128 128, 2, 2, 2, 1, 0
-#endif
-template <> struct TcConfig<kForward, 32> : TcSizes<F32> {};
-template <> struct TcConfig<kForward, 64> : TcSizes<F64> {};
-template <> struct TcConfig<kForward, 128> : TcSizes<F128> {};
-template <> struct TcConfig<kGradQ, 32> : TcSizes<Q32> {};
-template <> struct TcConfig<kGradQ, 64> : TcSizes<Q64> {};
-template <> struct TcConfig<kGradQ, 128> : TcSizes<Q128> {};
-template <> struct TcConfig<kGradKV, 32> : TcSizes<KV32> {};
-template <> struct TcConfig<kGradKV, 64> : TcSizes<KV64> {};
-template <> struct TcConfig<kGradKV, 128> : TcSizes<KV128> {};
+template <int MODE, int DP, bool SHORT> struct TcConfig;
+template <> struct TcConfig<kForward, 32, false> : TcSizes<128, 1, 3, 3, 2, 1> {};
+template <> struct TcConfig<kForward, 64, false> : TcSizes<128, 1, 2, 2, 2, 1> {};
+template <> struct TcConfig<kForward, 128, false> : TcSizes<64, 1, 2, 2, 2, 2> {};
+template <> struct TcConfig<kGradQ, 32, false> : TcSizes<128, 2, 4, 4, 1, 2> {};
+template <> struct TcConfig<kGradQ, 64, false> : TcSizes<128, 2, 3, 3, 1, 2> {};
+template <> struct TcConfig<kGradQ, 128, false> : TcSizes<128, 2, 2, 2, 1, 2> {};
+template <> struct TcConfig<kGradKV, 32, false> : TcSizes<128, 2, 4, 4, 1, 1> {};
+template <> struct TcConfig<kGradKV, 64, false> : TcSizes<128, 2, 3, 3, 1, 1> {};
+template <> struct TcConfig<kGradKV, 32, true> : TcSizes<64, 1, 2, 2, 2, 1> {};
+template <> struct TcConfig<kGradKV, 64, true> : TcSizes<64, 1, 2, 2, 2, 0> {};
+template <> struct TcConfig<kGradKV, 128, false> : TcSizes<128, 2, 2, 2, 1, 0> {};
 
-template <int MODE, int DP> struct Tc : TcConfig<MODE, DP> {
-    using C = TcConfig<MODE, DP>;
+template <int MODE, int DP, bool SHORT> struct Tc : TcConfig<MODE, DP, SHORT> {
+    using C = TcConfig<MODE, DP, SHORT>;
     static constexpr int BN = C::BN, PARTS = C::PARTS, STAGES = C::STAGES, EARLY = C::EARLY, WEIGHTS = C::WEIGHTS;
     // SPLIT: P is released, and its product issued, before dP is waited for
     static constexpr bool ALIAS = WEIGHTS == 0, BACK = MODE != kForward, SPLIT = MODE == kGradKV && ALIAS;
@@ -88,7 +63,7 @@ template <int MODE, int DP> struct Tc : TcConfig<MODE, DP> {
     static constexpr int SCORES = BN * (BACK ? 2 : 1), WIDE = BN / 2 * (MODE == kGradKV ? 2 : 1);
     static constexpr int ACC = SCORES + WEIGHTS * WIDE, RESULTS = MODE == kGradKV ? 2 : 1;
     static constexpr int USED = ACC + RESULTS * DP, COLS = USED <= 128 ? 128 : USED <= 256 ? 256 : 512;
-    //static_assert(BN == tc_columns(MODE, DP) && C::BLOCKS == tc_blocks(MODE, DP), "what the host plans with");
+    static_assert(BN == tc_columns(MODE, DP, SHORT) && C::BLOCKS == tc_blocks(MODE, DP, SHORT), "what the host plans with");
     static_assert(MODE != kForward || PARTS == 1, "one maximum and sum a row");
     static_assert(USED <= 512 && COLS * C::BLOCKS <= 512, "tensor memory");
     static constexpr int TILES = (BACK ? 2 : 1) * ROW_BYTES + (STAGES + EARLY) * COL_BYTES;
@@ -232,10 +207,10 @@ struct TcMaps {
     CUtensorMap a1, a2, x1, x2;        // rows: one or two; columns: two
 };
 
-template <typename T, int MODE, int DP>
-__global__ void __launch_bounds__(Tc<MODE, DP>::THREADS, Tc<MODE, DP>::BLOCKS)
+template <typename T, int MODE, int DP, bool SHORT>
+__global__ void __launch_bounds__(Tc<MODE, DP, SHORT>::THREADS, Tc<MODE, DP, SHORT>::BLOCKS)
 attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
-    using K = Tc<MODE, DP>;
+    using K = Tc<MODE, DP, SHORT>;
     constexpr int BN = K::BN, STAGES = K::STAGES, EARLY = K::EARLY, INFO = K::INFO, HELPER = K::PARTS * 4;
     constexpr bool BF16 = TcScale<T>::forward == 0.0f, BACK = K::BACK;
     // Which operand's tile is only used for the scores, and free after them: forward's k,
@@ -276,12 +251,12 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
         for (int i = 0; i < STAGES; ++i) bar_init(bias_full + i, 1);
         bar_init(s_full, 1);
         bar_init(d_full, 1);
-        bar_init(s_free, K::ROW_THREADS / 32);
-        bar_init(d_free, K::ROW_THREADS / 32);
-        bar_init(p_ready, K::ROW_THREADS / 32);
+        bar_init(s_free, K::ROW_THREADS);
+        bar_init(d_free, K::ROW_THREADS);
+        bar_init(p_ready, K::ROW_THREADS);
         bar_init(p_done, 1);
         for (int i = 0; i < 2; ++i) {
-            bar_init(ready + i, K::ROW_THREADS / 32);
+            bar_init(ready + i, K::ROW_THREADS);
             bar_init(done + i, 1);
             bar_init(last + i, 1);
         }
@@ -307,14 +282,21 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
         fewer_registers<K::REGS_OTHER>();
         if (warp == HELPER + 1) {
             // -------------------------------------------- fetching
-            int it = 0, pos = 0, head = 0;
+            // Each lane finds the class of one of the next 32 column tiles.
+            int it = 0;
             Ring<STAGES> st;
             Ring<EARLY> se;
-            if (j0 < j1) attn_columns<MODE, BN>(a, w, j0, &pos, &head);
             bool ok = true;
-            for (int64_t j = j0; j < j1 && ok; ++j) {
-                const int cls = attn_class<MODE, BN>(a, w, pos, head);
-                if (cls) {
+            for (int64_t j = j0; j < j1 && ok; j += 32) {
+                int its_pos = 0, its_head = 0, its_cls = 0;
+                if (j + lane < j1) {
+                    attn_columns<MODE, BN>(a, w, j + lane, &its_pos, &its_head);
+                    its_cls = attn_class<MODE, BN>(a, w, its_pos, its_head);
+                }
+                for (uint32_t left = __ballot_sync(0xffffffffu, its_cls != 0); left && ok; left &= left - 1) {
+                    const int from = __ffs(left) - 1;
+                    const int pos = __shfl_sync(0xffffffffu, its_pos, from), head = __shfl_sync(0xffffffffu, its_head, from);
+                    const int cls = __shfl_sync(0xffffffffu, its_cls, from);
                     if (it == 0) {
                         bar_expect(a_full, (BACK ? 2 : 1) * (K::PITCH * K::PANELS) * (kTcRows / w.pack * w.pack));
                         for (int p = 0; p < K::PANELS; ++p) {
@@ -338,11 +320,6 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
                     ++it;
                     st.next();
                     se.next();
-                }
-                pos += BN;
-                if (MODE == kGradKV && pos >= a.Q) {
-                    pos = 0;
-                    ++head;
                 }
             }
             // the end, for all
@@ -509,10 +486,9 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
         for (;; ++it, st.next()) {
             const uint32_t at_p = mine + (K::ALIAS ? PART * part : K::SCORES + (K::WEIGHTS == 2 ? it % 2 * K::WIDE : 0) + PART / 2 * part);
             const uint32_t at_ds = MODE != kGradKV ? at_p : K::ALIAS ? at_p + BN : at_p + BN / 2;
-            // a mask's words are asked for before the scores are there
-            // (their tile's barrier moves on only after this tile's second product)
-            if (a.classes) ok = bar_wait(full + st.at, st.phase, dead, a.err);
-            else ok = bar_wait(s_full, it & 1, dead, a.err);
+            // a mask's words are asked for before the scores are there (their tile's barrier moves
+            // on only after this tile's second product)
+            ok = a.classes ? bar_wait(full + st.at, st.phase, dead, a.err) : bar_wait(s_full, it & 1, dead, a.err);
             if (!ok) break;
             const TcTile tile = info[it % INFO];
             const int cls = tile.cls;
@@ -534,7 +510,7 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
             }
             if (!K::ALIAS) {
                 tmem_before_sync();
-                bar_arrive_warp(s_free);
+                bar_arrive(s_free);
             }
             if (cls != 2) {            // p, and with it ds unless dP is not finite, will be 0
                 asm volatile("");      // a branch, not a select for each score
@@ -614,7 +590,7 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
                         tmem_wait_store();
                     }
                     tmem_before_sync();
-                    bar_arrive_warp(p_ready);
+                    bar_arrive(p_ready);
                     ok = bar_wait(d_full, it & 1, dead, a.err);
                     if (!ok) break;
                     tmem_after_sync();
@@ -648,7 +624,7 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
             if (!ok) break;
             if (any_valid) tmem_wait_store();
             tmem_before_sync();
-            bar_arrive_warp(tc_bar<K::WEIGHTS>(ready, it));
+            bar_arrive(tc_bar<K::WEIGHTS>(ready, it));
         }
 
         // ------------------------------------------------ results
@@ -716,10 +692,10 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
 // ------------------------------------------------------------------ launch
 
 // A map of boxes of `heads` heads and `positions` positions.
-template <int MODE, int DP>
+template <int MODE, int DP, bool SHORT>
 cudaError_t tc_map(CUtensorMap *map, const AttnTensor &t, const AttnArgs &a, int len, int heads, int box_heads, int box_positions,
                    bool bf16) {
-    using K = Tc<MODE, DP>;
+    using K = Tc<MODE, DP, SHORT>;
     const cuuint64_t dense = (cuuint64_t)a.D * 2;
     const cuuint64_t dims[4] = {(cuuint64_t)a.D, (cuuint64_t)heads, (cuuint64_t)len, (cuuint64_t)a.B};
     const cuuint64_t strides[3] = {heads > 1 ? (cuuint64_t)t.head * 2 : dense, len > 1 ? (cuuint64_t)t.pos * 2 : dense,
@@ -735,9 +711,9 @@ cudaError_t tc_map(CUtensorMap *map, const AttnTensor &t, const AttnArgs &a, int
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <typename T, int MODE, int DP>
+template <typename T, int MODE, int DP, bool SHORT = false>
 cudaError_t launch_tc_d(const AttnArgs &a, int64_t blocks, cudaStream_t stream) {
-    using K = Tc<MODE, DP>;
+    using K = Tc<MODE, DP, SHORT>;
     constexpr bool bf16 = TcScale<T>::forward == 0.0f;
     TcMaps maps;
     cudaError_t e;
@@ -746,22 +722,22 @@ cudaError_t launch_tc_d(const AttnArgs &a, int64_t blocks, cudaStream_t stream) 
     if (MODE == kGradKV) {
         const AttnTensor &x1 = none ? a.k : a.q, &x2 = none ? a.v : a.go;
         const int len = none ? a.S : a.Q, heads = none ? a.N : a.M;
-        if ((e = tc_map<MODE, DP>(&maps.a1, a.k, a, a.S, a.N, 1, kTcRows, bf16)) != cudaSuccess ||
-            (e = tc_map<MODE, DP>(&maps.a2, a.v, a, a.S, a.N, 1, kTcRows, bf16)) != cudaSuccess ||
-            (e = tc_map<MODE, DP>(&maps.x1, x1, a, len, heads, 1, K::BN, bf16)) != cudaSuccess ||
-            (e = tc_map<MODE, DP>(&maps.x2, x2, a, len, heads, 1, K::BN, bf16)) != cudaSuccess)
+        if ((e = tc_map<MODE, DP, SHORT>(&maps.a1, a.k, a, a.S, a.N, 1, kTcRows, bf16)) != cudaSuccess ||
+            (e = tc_map<MODE, DP, SHORT>(&maps.a2, a.v, a, a.S, a.N, 1, kTcRows, bf16)) != cudaSuccess ||
+            (e = tc_map<MODE, DP, SHORT>(&maps.x1, x1, a, len, heads, 1, K::BN, bf16)) != cudaSuccess ||
+            (e = tc_map<MODE, DP, SHORT>(&maps.x2, x2, a, len, heads, 1, K::BN, bf16)) != cudaSuccess)
             return e;
     } else {
         const AttnTensor &x1 = none ? a.q : a.k, &x2 = none ? a.q : a.v;
         const int len = none ? a.Q : a.S, heads = none ? a.M : a.N;
-        if ((e = tc_map<MODE, DP>(&maps.a1, a.q, a, a.Q, a.M, a.pack, kTcRows / a.pack, bf16)) != cudaSuccess ||
-            (e = tc_map<MODE, DP>(&maps.x1, x1, a, len, heads, 1, K::BN, bf16)) != cudaSuccess ||
-            (e = tc_map<MODE, DP>(&maps.x2, x2, a, len, heads, 1, K::BN, bf16)) != cudaSuccess)
+        if ((e = tc_map<MODE, DP, SHORT>(&maps.a1, a.q, a, a.Q, a.M, a.pack, kTcRows / a.pack, bf16)) != cudaSuccess ||
+            (e = tc_map<MODE, DP, SHORT>(&maps.x1, x1, a, len, heads, 1, K::BN, bf16)) != cudaSuccess ||
+            (e = tc_map<MODE, DP, SHORT>(&maps.x2, x2, a, len, heads, 1, K::BN, bf16)) != cudaSuccess)
             return e;
         maps.a2 = maps.a1;
-        if (MODE == kGradQ && (e = tc_map<MODE, DP>(&maps.a2, a.go, a, a.Q, a.M, a.pack, kTcRows / a.pack, bf16)) != cudaSuccess) return e;
+        if (MODE == kGradQ && (e = tc_map<MODE, DP, SHORT>(&maps.a2, a.go, a, a.Q, a.M, a.pack, kTcRows / a.pack, bf16)) != cudaSuccess) return e;
     }
-    auto *kernel = attn_tc_kernel<T, MODE, DP>;
+    auto *kernel = attn_tc_kernel<T, MODE, DP, SHORT>;
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, K::SHARED);
     if (e != cudaSuccess) return e;
     kernel<<<(unsigned)blocks, K::THREADS, K::SHARED, stream>>>(a, maps);
@@ -769,6 +745,9 @@ cudaError_t launch_tc_d(const AttnArgs &a, int64_t blocks, cudaStream_t stream) 
 }
 template <typename T, int MODE>
 cudaError_t launch_tc_mode(const AttnArgs &a, int64_t blocks, cudaStream_t stream) {
+    if constexpr (MODE == kGradKV)
+        if (tc_short(MODE, a.D, a.Q, a.G))
+            return a.D <= 32 ? launch_tc_d<T, MODE, 32, true>(a, blocks, stream) : launch_tc_d<T, MODE, 64, true>(a, blocks, stream);
     return a.D <= 32 ? launch_tc_d<T, MODE, 32>(a, blocks, stream)
          : a.D <= 64 ? launch_tc_d<T, MODE, 64>(a, blocks, stream)
                      : launch_tc_d<T, MODE, 128>(a, blocks, stream);

@@ -57,48 +57,76 @@ template <> __device__ __forceinline__ double widen<double>(double v) { return v
 template <typename T> __device__ __forceinline__ T narrow(typename Wide<T>::type v) { return Elem<T>::from_f(v); }
 template <> __device__ __forceinline__ double narrow<double>(double v) { return v; }
 
-// Eight entries a thread and turn: one call of the generator. VEC: all tensors
-// start on 16-byte boundaries.
+// 16 bytes that are read once, asked for where this stands: before the generator's rounds.
+__device__ __forceinline__ uint4 fetch(const void *p) {
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+
+template <typename T> union Eight {
+    static constexpr int P = 8 * sizeof(T) / 16;
+    uint4 raw[P];
+    T v[8];
+    __device__ Eight() {}
+};
+
+// The eight entries of one call of the generator.
+template <typename T, bool RES>
+__device__ __forceinline__ void drop_eight(Eight<T> &in, const Eight<T> &add, const DropArgs &a, int64_t seed, int64_t number, int64_t i) {
+    using W = typename Wide<T>::type;
+    const W factor = (W)a.factor;
+    const Philox r(seed, number, i);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const W kept = r.half(j) >= a.threshold ? widen<T>(in.v[j]) * factor : (W)0;
+        in.v[j] = narrow<T>(RES ? kept + widen<T>(add.v[j]) : kept);
+    }
+}
+
+// VEC: all tensors start on 16-byte boundaries, and a thread has 32 bytes of each under
+// way. The last entries, and all without VEC, go one by one.
+template <typename T, bool VEC> constexpr int kAtOnce = VEC && sizeof(T) == 2 ? 2 : 1;
 template <typename T, bool VEC, bool RES>
 __global__ void __launch_bounds__(kThreads) dropout_kernel(const DropArgs a) {
-    using W = typename Wide<T>::type;
+    constexpr int AT_ONCE = kAtOnce<T, VEC>, P = Eight<T>::P;
     const T *x = static_cast<const T *>(a.x), *res = static_cast<const T *>(a.residual);
     T *out = static_cast<T *>(a.out);
-    const int64_t seed = a.counter[0], number = a.counter[1], blocks = (a.n + 7) / 8;
-    const W factor = (W)a.factor;
-    for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < blocks; i += (int64_t)gridDim.x * kThreads) {
-        constexpr int P = 8 * sizeof(T) / 16;
-        union Eight { uint4 raw[P]; T v[8]; __device__ Eight() {} } in, add;
-        const int64_t at = 8 * i;
-        const int many = a.n - at < 8 ? (int)(a.n - at) : 8;
-        const bool whole = VEC && many == 8;
-        if (whole) {
+    const int64_t seed = a.counter[0], number = a.counter[1], whole = VEC ? a.n / 8 : 0, blocks = (a.n + 7) / 8;
+    const int64_t step = (int64_t)gridDim.x * kThreads, first = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    for (int64_t i = first; i < blocks; i += AT_ONCE * step) {
+        Eight<T> in[AT_ONCE], add[AT_ONCE];
+#pragma unroll
+        for (int u = 0; u < AT_ONCE; ++u) {
+            const int64_t at = i + u * step;
+            if (at >= whole) continue;
 #pragma unroll
             for (int j = 0; j < P; ++j) {
-                in.raw[j] = reinterpret_cast<const uint4 *>(x + at)[j];
-                if (RES) add.raw[j] = reinterpret_cast<const uint4 *>(res + at)[j];
+                in[u].raw[j] = fetch(reinterpret_cast<const uint4 *>(x + 8 * at) + j);
+                if (RES) add[u].raw[j] = fetch(reinterpret_cast<const uint4 *>(res + 8 * at) + j);
             }
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (j < many) {
-                    in.v[j] = x[at + j];
-                    if (RES) add.v[j] = res[at + j];
-                }
         }
-        const Philox r(seed, number, i);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const W kept = r.half(j) >= a.threshold ? widen<T>(in.v[j]) * factor : (W)0;
-            in.v[j] = narrow<T>(RES ? kept + widen<T>(add.v[j]) : kept);
-        }
-        if (whole) {
+        for (int u = 0; u < AT_ONCE; ++u) {
+            const int64_t at = i + u * step;
+            if (at < whole) {
+                drop_eight<T, RES>(in[u], add[u], a, seed, number, at);
 #pragma unroll
-            for (int j = 0; j < P; ++j) reinterpret_cast<uint4 *>(out + at)[j] = in.raw[j];
-        } else {
+                for (int j = 0; j < P; ++j) reinterpret_cast<uint4 *>(out + 8 * at)[j] = in[u].raw[j];
+            } else if (at < blocks) {
+                const int many = a.n - 8 * at < 8 ? (int)(a.n - 8 * at) : 8;
+                Eight<T> one, other;
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (j < many) out[at + j] = in.v[j];
+                for (int j = 0; j < 8; ++j)
+                    if (j < many) {
+                        one.v[j] = x[8 * at + j];
+                        if (RES) other.v[j] = res[8 * at + j];
+                    }
+                drop_eight<T, RES>(one, other, a, seed, number, at);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (j < many) out[8 * at + j] = one.v[j];
+            }
         }
     }
 }
@@ -109,10 +137,10 @@ __global__ void dropout_next_kernel(int64_t *state, int64_t *drawn) {
 }
 
 template <typename T> cudaError_t launch(const DropArgs &a, cudaStream_t stream) {
-    const int64_t want = ((a.n + 7) / 8 + kThreads - 1) / kThreads, cap = (int64_t)1 << 30;
-    const unsigned blocks = (unsigned)(want < cap ? want : cap);
     const bool vec = ((reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.residual) |
                        reinterpret_cast<uintptr_t>(a.out)) % 16) == 0;
+    const int64_t per = (int64_t)kThreads * (vec ? kAtOnce<T, true> : 1), want = ((a.n + 7) / 8 + per - 1) / per, cap = (int64_t)1 << 30;
+    const unsigned blocks = (unsigned)(want < cap ? want : cap);
     if (vec && a.residual) dropout_kernel<T, true, true><<<blocks, kThreads, 0, stream>>>(a);
     else if (vec) dropout_kernel<T, true, false><<<blocks, kThreads, 0, stream>>>(a);
     else if (a.residual) dropout_kernel<T, false, true><<<blocks, kThreads, 0, stream>>>(a);

@@ -30,11 +30,8 @@ __device__ __forceinline__ unsigned long long nanoseconds() {
 __device__ __forceinline__ void bar_arrive_one(uint64_t *bar) {
     asm volatile(ELECT("mbarrier.arrive.shared::cta.b64 _, [%0];") ::"r"(shared_at(bar)) : "memory");
 }
-// One arrival for a whole warp, all of whose lanes have come so far: 32 arrivals at one
-// address are taken one after another.
-__device__ __forceinline__ void bar_arrive_warp(uint64_t *bar) {
-    __syncwarp();
-    bar_arrive_one(bar);
+__device__ __forceinline__ void bar_arrive(uint64_t *bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(shared_at(bar)) : "memory");
 }
 __device__ __forceinline__ void bar_init(uint64_t *bar, uint32_t count) {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(shared_at(bar)), "r"(count) : "memory");
