@@ -881,38 +881,8 @@ def clip_grad_norm_(parameters, max_norm: float, norm_type: float = 2.0,
 _ATTENTION_DTYPES = (torch.float32, torch.bfloat16, torch.float16)
 
 
-class _AttentionPlan:
-    """The dims of one set of shapes and strides, and what they need of a workspace."""
-
-    def __init__(self, sizes, q, k, v, mask, dtype):
-        self.dims = msda_attention_dims_t(*sizes, (ctypes.c_int64 * 3)(*q), (ctypes.c_int64 * 3)(*k),
-                                          (ctypes.c_int64 * 3)(*v),
-                                          (ctypes.c_int64 * 4)(*(mask or (0, 0, 0, 0))))
-        self.ref = ctypes.byref(self.dims)
-        self.forward_bytes = int(lib().msda_attention_forward_workspace_bytes(
-            self.ref, dtype, mask is not None))
-        self.backward_bytes = int(lib().msda_attention_backward_workspace_bytes(
-            self.ref, dtype, mask is not None))
-
-
-_attention_plan = functools.lru_cache(maxsize=256)(_AttentionPlan)
-
-
-def _heads_ready(t):
-    """t, or a copy of it that the kernels can read: channels contiguous, 16-byte boundaries."""
-    e = t.element_size()
-    strides = t.stride()
-    if strides[3] == 1 and t.data_ptr() % 16 == 0:
-        for stride, size in zip(strides[:3], t.shape):
-            if size > 1 and (stride <= 0 or stride * e % 16):
-                break
-        else:
-            return t
-    return t.clone(memory_format=torch.contiguous_format)
-
-
-def _attention_operands(q, k, v, mask, scale):
-    """Raise unless q, k, v and the mask fit each other; returns (scale, the mask expanded)."""
+def _attention_check(q, k, v, mask):
+    """Raise unless the shapes, types and strides of q, k, v and the mask fit each other."""
     for name, t in (("q", q), ("k", k), ("v", v)):
         if not t.is_cuda:
             raise ValueError("libmsda runs on CUDA tensors only (no CPU path)")
@@ -921,8 +891,6 @@ def _attention_operands(q, k, v, mask, scale):
                              f"has shape {tuple(t.shape)}")
         if t.dtype != q.dtype:
             raise ValueError(f"{name} is {t.dtype}, q is {q.dtype}")
-        if t.device != q.device:
-            raise ValueError(f"{name} is on {t.device}, q is on {q.device}")
     if q.dtype not in _ATTENTION_DTYPES:
         raise ValueError(f"unsupported dtype {q.dtype}: float32, bfloat16 and float16 are supported")
     B, Q, M, D = q.shape
@@ -933,70 +901,135 @@ def _attention_operands(q, k, v, mask, scale):
         raise ValueError(f"{M} query heads for {N} key heads: give a multiple")
     if not 8 <= D <= 128 or D % 8:
         raise ValueError(f"{D} channels a head: multiples of 8 from 8 to 128 are supported")
-    scale = D ** -0.5 if scale is None else float(scale)
-    if not 0.0 <= scale <= 3e38:
-        raise ValueError(f"scale {scale}: give a finite number, not below zero")
     if mask is not None:
         if mask.dtype is not torch.bool:
             raise ValueError(f"the mask is {mask.dtype}: give torch.bool, true where a query may attend")
-        if mask.device != q.device:
-            raise ValueError(f"the mask is on {mask.device}, q is on {q.device}")
         try:
-            mask = mask.expand(B, M, Q, S)
+            mask.expand(B, M, Q, S)
         except RuntimeError:
             raise ValueError(f"a mask of shape {tuple(mask.shape)} does not broadcast to "
                              f"{(B, M, Q, S)}") from None
-    return scale, mask
+
+
+class _AttentionPlan:
+    """What one set of shapes, strides and types needs: the C dims, the workspaces' bytes,
+    and which of q, k and v have to be copied first (channels not contiguous, or rows not on
+    16-byte boundaries)."""
+
+    def __init__(self, q, k, v, mask):
+        _attention_check(q, k, v, mask)
+        B, Q, M, D = q.shape
+        S, N = k.shape[1], k.shape[2]
+        e = q.element_size()
+        self.copies = [t.stride(3) != 1 or any(n > 1 and (st <= 0 or st * e % 16)
+                                               for st, n in zip(t.stride()[:3], t.shape))
+                       for t in (q, k, v)]
+        self.copy = any(self.copies)
+        self.dtype = _DTYPES[q.dtype]
+        self.out_shape, self.stats_shape = (B, Q, M * D), (B, M, Q)
+        self.default_scale = D ** -0.5
+        strides = [(ctypes.c_int64 * 3)(*t.stride()[:3]) for t in (q, k, v)]
+        mask_strides = (0, 0, 0, 0)
+        if mask is not None:
+            mask_strides = [st if n > 1 else 0
+                            for st, n in zip(mask.expand(B, M, Q, S).stride(), (B, M, Q, S))]
+        self.dims = msda_attention_dims_t(B, Q, S, M, N, D, *strides, (ctypes.c_int64 * 4)(*mask_strides))
+        self.ref = ctypes.byref(self.dims)
+        so = lib()
+        self.forward_bytes = int(so.msda_attention_forward_workspace_bytes(
+            self.ref, self.dtype, mask is not None))
+        self.backward_bytes = int(so.msda_attention_backward_workspace_bytes(
+            self.ref, self.dtype, mask is not None))
+
+
+_attention_plans = {}
 
 
 def _plan_of(q, k, v, mask):
-    B, Q, M, D = q.shape
-    _, S, N, _ = k.shape
-    strides = None
-    if mask is not None:
-        strides = tuple(st if n > 1 else 0 for st, n in zip(mask.stride(), mask.shape))
-    return _attention_plan((B, Q, S, M, N, D), q.stride()[:3], k.stride()[:3], v.stride()[:3],
-                           strides, _DTYPES[q.dtype])
+    """(the plan of these operands' shapes, strides and types, their device's index)"""
+    key = (q.shape, k.shape, v.shape, q.stride(), k.stride(), v.stride(), q.dtype, k.dtype, v.dtype,
+           None if mask is None else (mask.shape, mask.stride(), mask.dtype))
+    index = q.get_device()
+    if index < 0 or k.get_device() != index or v.get_device() != index or (
+            mask is not None and mask.get_device() != index):
+        _attention_check(q, k, v, mask)
+        raise ValueError("q, k, v and the mask are on "
+                         f"{[str(t.device) for t in (q, k, v, mask) if t is not None]}: give one device's")
+    plan = _attention_plans.get(key)
+    if plan is None:
+        plan = _AttentionPlan(q, k, v, mask)
+        if len(_attention_plans) >= 256:
+            _attention_plans.clear()
+        _attention_plans[key] = plan
+    return plan, index
 
 
-def _workspace(need, device):
-    return torch.empty(need, dtype=torch.uint8, device=device) if need else None
+def _scale_of(scale, plan):
+    if scale is None:
+        return plan.default_scale
+    scale = float(scale)
+    if not 0.0 <= scale <= 3e38:
+        raise ValueError(f"scale {scale}: give a finite number, not below zero")
+    return scale
 
 
-def _attend(q, k, v, mask, scale, lse, rest, out):
+def _ready(q, k, v, mask, plan):
+    """q, k and v, or copies that the kernels can read, and their plan. On the device and
+    stream of the launch."""
+    copies = plan.copies if plan.copy else (False, False, False)
+    made = [t.clone(memory_format=torch.contiguous_format) if c or t.data_ptr() % 16 else t
+            for t, c in zip((q, k, v), copies)]
+    if made[0] is q and made[1] is k and made[2] is v:
+        return q, k, v, plan
+    return (*made, _plan_of(*made, mask)[0])
+
+
+def _attend(q, k, v, mask, plan, index, scale, lse, rest, out):
     """The launch, on the current device and stream, of operands already checked. rest: also
     what out's rounding left (16-bit types)."""
-    B, Q, M, D = q.shape
-    plan = _plan_of(q, k, v, mask)
+    if plan.copy or (q.data_ptr() | k.data_ptr() | v.data_ptr()) % 16:
+        q, k, v, plan = _ready(q, k, v, mask, plan)
+    device = q.device
     if out is None:
-        out = torch.empty((B, Q, M * D), dtype=q.dtype, device=q.device)
-    lse = torch.empty((B, M, Q), dtype=torch.float32, device=q.device) if lse else None
+        out = torch.empty(plan.out_shape, dtype=q.dtype, device=device)
+    lse = torch.empty(plan.stats_shape, dtype=torch.float32, device=device) if lse else None
     rest = torch.empty_like(out) if rest and q.dtype is not torch.float32 else None
-    workspace = _workspace(plan.forward_bytes, q.device)
+    need = plan.forward_bytes
+    workspace = torch.empty(need, dtype=torch.uint8, device=device) if need else None
     status = lib().msda_attention_forward(
-        q.data_ptr(), k.data_ptr(), v.data_ptr(), _at(mask), out.data_ptr(), _at(rest), _at(lse), scale,
-        _at(workspace), plan.forward_bytes, plan.ref, _DTYPES[q.dtype],
-        _current_stream(q.get_device()))
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), None if mask is None else mask.data_ptr(),
+        out.data_ptr(), None if rest is None else rest.data_ptr(), None if lse is None else lse.data_ptr(),
+        scale, None if workspace is None else workspace.data_ptr(), need, plan.ref, plan.dtype,
+        _current_stream(index))
     if status:
         raise MSDAError(status, "msda_attention_forward")
     return out, lse, rest
 
 
-def _attend_backward(grad_out, q, k, v, out, rest, lse, mask, scale, want):
+def _attend_backward(grad_out, q, k, v, out, rest, lse, mask, plan, index, scale, want):
     """The launch, on the current device and stream, of operands already checked."""
-    plan = _plan_of(q, k, v, mask)
-    gq = torch.empty(q.shape, dtype=q.dtype, device=q.device) if want[0] else None
+    if plan.copy or (q.data_ptr() | k.data_ptr() | v.data_ptr()) % 16:
+        q, k, v, plan = _ready(q, k, v, mask, plan)
+    grad_out, out, rest = _at16(grad_out), _at16(out), None if rest is None else _at16(rest)
+    dtype, device = q.dtype, q.device
+    gq = torch.empty(q.shape, dtype=dtype, device=device) if want[0] else None
     gk = gv = None
     if want[1] or want[2]:
-        gk, gv = [torch.empty(k.shape, dtype=q.dtype, device=q.device) for _ in range(2)]
-    workspace = _workspace(plan.backward_bytes, q.device)
+        gk, gv = [torch.empty(k.shape, dtype=dtype, device=device) for _ in range(2)]
+    need = plan.backward_bytes
+    workspace = torch.empty(need, dtype=torch.uint8, device=device) if need else None
     status = lib().msda_attention_backward(
         grad_out.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), _at(mask), out.data_ptr(),
-        _at(rest), lse.data_ptr(), _at(gq), _at(gk), _at(gv), scale, _at(workspace), plan.backward_bytes,
-        plan.ref, _DTYPES[q.dtype], _current_stream(q.get_device()))
+        _at(rest), lse.data_ptr(), _at(gq), _at(gk), _at(gv), scale, _at(workspace), need, plan.ref,
+        plan.dtype, _current_stream(index))
     if status:
         raise MSDAError(status, "msda_attention_backward")
     return gq, gk if want[1] else None, gv if want[2] else None
+
+
+def _at16(t):
+    """t, contiguous, or a copy that starts on a 16-byte boundary."""
+    return t if t.data_ptr() % 16 == 0 else t.clone()
 
 
 def msda_attention_forward(q, k, v, mask=None, scale=None, lse: bool = True, out=None, stream=None,
@@ -1007,15 +1040,25 @@ def msda_attention_forward(q, k, v, mask=None, scale=None, lse: bool = True, out
     query may attend. scale: D ** -0.5 unless given. See msda_attention_forward in
     include/msda.h."""
     _refuse_modes("msda_attention_forward", (q, k, v))
-    scale, mask = _attention_operands(q, k, v, mask, scale)
+    plan, index = _plan_of(q, k, v, mask)
+    scale = _scale_of(scale, plan)
     if out is not None:
-        _check_like("out", out, (q.shape[0], q.shape[1], q.shape[2] * q.shape[3]), q.dtype, q.device)
+        _check_like("out", out, plan.out_shape, q.dtype, q.device)
+        if out.data_ptr() % 16:
+            raise ValueError("out does not start on a 16-byte boundary")
+        for t in (q, k, v, mask):        # spans of strided tensors
+            if t is not None and t.numel() and out.numel():
+                last = sum((n - 1) * st for n, st in zip(t.shape, t.stride()))
+                if (t.data_ptr() < out.data_ptr() + out.numel() * out.element_size()
+                        and out.data_ptr() < t.data_ptr() + (last + 1) * t.element_size()):
+                    raise ValueError("an output overlaps an input or another output")
     given = out
-    with _on(q.device, stream):
-        q, k, v = _heads_ready(q), _heads_ready(k), _heads_ready(v)
-        if out is not None:
-            _apart([out], [q, k, v, mask])
-        out, stats, left = _attend(q, k, v, mask, scale, lse, rest, out)
+    args = (q, k, v, mask, plan, index, scale, lse, rest, out)
+    if _elsewhere(index, stream):
+        with _on(q.device, stream):
+            out, stats, left = _attend(*args)
+    else:
+        out, stats, left = _attend(*args)
     if given is not None and not out.is_inference():
         torch.autograd.graph.increment_version(out)
     return (out, stats, left) if rest else (out, stats)
@@ -1026,29 +1069,26 @@ def msda_attention_backward(grad_out, q, k, v, out, lse, mask=None, scale=None,
     """(grad_q, grad_k, grad_v) of q's, k's and v's shapes, contiguous, None where `want` says
     so; out, lse and rest (if it was asked for) are the forward's. See msda_attention_backward in include/msda.h."""
     _refuse_modes("msda_attention_backward", (grad_out, q, k, v, out, lse, rest))
-    scale, mask = _attention_operands(q, k, v, mask, scale)
-    B, Q, M, D = q.shape
+    plan, index = _plan_of(q, k, v, mask)
+    scale = _scale_of(scale, plan)
     for name, t in (("grad_out", grad_out), ("out", out), ("rest", rest)):
-        _check_like(name, t, (B, Q, M * D), q.dtype, q.device)
-    _check_like("lse", lse, (B, M, Q), torch.float32, q.device)
-    with _on(q.device, stream):
-        return _attend_backward(_at16(grad_out), _heads_ready(q), _heads_ready(k), _heads_ready(v),
-                                _at16(out), None if rest is None else _at16(rest), lse, mask, scale,
-                                want)
-
-
-def _at16(t):
-    """t, contiguous, or a copy that starts on a 16-byte boundary."""
-    return t if t.data_ptr() % 16 == 0 else t.clone()
+        _check_like(name, t, plan.out_shape, q.dtype, q.device)
+    _check_like("lse", lse, plan.stats_shape, torch.float32, q.device)
+    args = (grad_out, q, k, v, out, rest, lse, mask, plan, index, scale, want)
+    if _elsewhere(index, stream):
+        with _on(q.device, stream):
+            return _attend_backward(*args)
+    return _attend_backward(*args)
 
 
 def _attention_gradients(ctx, grad_out):
     """What AttentionFunction.backward returns."""
     _refuse_recording("attention's backward")
     q, k, v, mask, out, lse, rest = ctx.saved_tensors
-    args = (_at16(grad_out.contiguous()), q, k, v, out, rest, lse, mask, ctx.scale,
+    plan, index = _plan_of(q, k, v, mask)
+    args = (grad_out.contiguous(), q, k, v, out, rest, lse, mask, plan, index, ctx.scale,
             ctx.needs_input_grad[:3])
-    if _elsewhere(q.get_device()):
+    if _elsewhere(index):
         with _on(q.device, None):
             grads = _attend_backward(*args)
     else:
@@ -1061,10 +1101,14 @@ class AttentionFunction(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, q, k, v, mask, scale):
-        ctx.scale, mask = _attention_operands(q, k, v, mask, scale)
-        with _on(q.device, None):
-            q, k, v = _heads_ready(q), _heads_ready(k), _heads_ready(v)
-            out, lse, rest = _attend(q, k, v, mask, ctx.scale, True, True, None)
+        plan, index = _plan_of(q, k, v, mask)
+        ctx.scale = _scale_of(scale, plan)
+        args = (q, k, v, mask, plan, index, ctx.scale, True, True, None)
+        if _elsewhere(index):
+            with _on(q.device, None):
+                out, lse, rest = _attend(*args)
+        else:
+            out, lse, rest = _attend(*args)
         ctx.save_for_backward(q, k, v, mask, out, lse, rest)
         return out
 
@@ -1081,30 +1125,37 @@ def attention(q, k, v, mask=None, scale=None):
     """Differentiable attention: q (B, Q, M, D) over k, v (B, S, N, D) -> (B, Q, M*D), query
     head m reading key head m / (M / N). mask: bool, broadcasts to (B, M, Q, S), true where a
     query may attend; a query with no key gets zeros. scale: D ** -0.5 unless given. D is a
-    multiple of 8 up to 128; float32, bfloat16 or float16."""
+    multiple of 8 up to 128; float32, bfloat16 or float16. q, k and v may be strided, as parts
+    of one projection are."""
     _refuse_recording("attention")
     if (torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad)
             or _through_autograd()):
         return AttentionFunction.apply(q, k, v, mask, scale)
-    scale, mask = _attention_operands(q, k, v, mask, scale)
-    if _elsewhere(q.get_device()):
+    plan, index = _plan_of(q, k, v, mask)
+    args = (q, k, v, mask, plan, index, _scale_of(scale, plan), False, False, None)
+    if _elsewhere(index):
         with _on(q.device, None):
-            return _attend(_heads_ready(q), _heads_ready(k), _heads_ready(v), mask, scale, False, False, None)[0]
-    return _attend(_heads_ready(q), _heads_ready(k), _heads_ready(v), mask, scale, False, False, None)[0]
+            return _attend(*args)[0]
+    return _attend(*args)[0]
 
 
 # -------------------------------------------------------------------- dropout
 
 def _drop_operands(x, p, counter, residual):
-    if not x.is_cuda:
+    index, dtype = x.get_device(), x.dtype
+    if index < 0:
         raise ValueError("libmsda runs on CUDA tensors only (no CPU path)")
-    if x.dtype not in _DTYPES:
-        raise ValueError(f"unsupported dtype {x.dtype}")
+    if dtype not in _DTYPES:
+        raise ValueError(f"unsupported dtype {dtype}")
     if not 0.0 <= p <= 1.0:
         raise ValueError(f"a probability of {p}: give one from 0 to 1")
-    _check_like("x", x, x.shape, x.dtype, x.device)
-    _check_like("residual", residual, x.shape, x.dtype, x.device)
-    _check_like("counter", counter, (2,), torch.int64, x.device)
+    if not x.is_contiguous():
+        _check_like("x", x, x.shape, dtype, x.device)
+    if residual is not None and _unlike(residual, x.shape, dtype, index):
+        _check_like("residual", residual, x.shape, dtype, x.device)
+    if _unlike(counter, (2,), torch.int64, index):
+        _check_like("counter", counter, (2,), torch.int64, x.device)
+    return index
 
 
 def _drop(x, p, counter, residual, out):

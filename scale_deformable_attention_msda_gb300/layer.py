@@ -16,6 +16,10 @@ sampling location of (q, m, l, k) is reference[q, l] + offset / (W_l, H_l).
 A detector's encoder or decoder layer ends this sublayer in
 norm(input + sublayer(input)). With norm=True the layer does so itself: the
 residual is added on the way into libmsda's layer norm, forward and backward.
+With dropout=p the sublayer's output goes through dropout first.
+
+A decoder layer begins with attention of the queries among themselves:
+MultiHeadAttention is that sublayer, in the same form.
 """
 from __future__ import annotations
 
@@ -50,16 +54,91 @@ class LayerNorm(nn.Module):
                                   return_sum=return_sum)
 
 
+class Dropout(nn.Module):
+    """Dropout of libmsda's counter-based generator (binding.dropout), in training; of x, or
+    of x on its way into residual + x. `state`, a buffer, holds the generator's seed, drawn
+    from torch's, and the number of the next draw, and is advanced on the device at each call
+    in training: a captured step draws anew each time it is replayed."""
+
+    def __init__(self, p: float = 0.1):
+        super().__init__()
+        if not 0.0 <= p <= 1.0:
+            raise ValueError("a dropout probability lies between 0 and 1")
+        self.p = p
+        seed = torch.randint(-2 ** 63, 2 ** 63 - 1, (), dtype=torch.int64)
+        self.register_buffer("state", torch.stack([seed, torch.zeros_like(seed)]))
+
+    def extra_repr(self):
+        return f"p={self.p}"
+
+    def forward(self, x, residual=None):
+        if residual is not None and residual.dtype != x.dtype and torch.is_autocast_enabled("cuda"):
+            dtype = torch.promote_types(x.dtype, residual.dtype)
+            x, residual = x.to(dtype), residual.to(dtype)
+        if not self.training or self.p == 0.0:
+            return x if residual is None else residual + x
+        return binding.dropout(x, self.p, binding.dropout_next(self.state), residual=residual)
+
+
+class MultiHeadAttention(nn.Module):
+    """Attention of a detector's decoder: query (B, Q, dim) over key and value (B, S, dim) ->
+    (B, Q, dim), through projections of their own and binding.attention. key: the query unless
+    given; value: the key unless given (a decoder adds the queries' positions to query and key
+    and not to value). mask: bool, broadcasts to (B, num_heads, Q, S), true where a query may
+    attend; a query with no key gets the output projection of zeros. kv_heads: key heads, each
+    shared by num_heads / kv_heads query heads. dropout: of the output. norm=True: the result
+    is LayerNorm(residual + output), residual the query unless given."""
+
+    def __init__(self, dim: int = 256, num_heads: int = 8, kv_heads: int | None = None,
+                 dropout: float = 0.0, norm: bool = False):
+        super().__init__()
+        kv_heads = num_heads if kv_heads is None else kv_heads
+        if dim % num_heads != 0 or num_heads % kv_heads != 0:
+            raise ValueError("dim must be divisible by num_heads, num_heads by kv_heads")
+        self.dim, self.num_heads, self.kv_heads = dim, num_heads, kv_heads
+        self.head_dim = dim // num_heads
+        self.query_proj = nn.Linear(dim, dim)
+        self.key_proj = nn.Linear(dim, kv_heads * self.head_dim)
+        self.value_proj = nn.Linear(dim, kv_heads * self.head_dim)
+        self.output_proj = nn.Linear(dim, dim)
+        self.dropout = Dropout(dropout) if dropout > 0.0 else None
+        self.norm = LayerNorm(dim) if norm else None
+        self.reset_parameters()
+
+    @torch.no_grad()
+    def reset_parameters(self):
+        for proj in (self.query_proj, self.key_proj, self.value_proj, self.output_proj):
+            nn.init.xavier_uniform_(proj.weight)
+            nn.init.zeros_(proj.bias)
+
+    def forward(self, query, key=None, value=None, mask=None, residual=None):
+        if residual is not None and self.norm is None:
+            raise ValueError("a residual is added by a layer made with norm=True")
+        key = query if key is None else key
+        value = key if value is None else value
+        B, Q, _ = query.shape
+        q = self.query_proj(query).view(B, Q, self.num_heads, self.head_dim)
+        k = self.key_proj(key).view(B, key.shape[1], self.kv_heads, self.head_dim)
+        v = self.value_proj(value).view(B, value.shape[1], self.kv_heads, self.head_dim)
+        out = self.output_proj(binding.attention(q, k, v, mask=mask))
+        if self.dropout is not None:
+            out = self.dropout(out)
+        if self.norm is None:
+            return out
+        return self.norm(out, residual=query if residual is None else residual)
+
+
 class MultiScaleDeformableAttention(nn.Module):
     """query (B, Q, dim), reference (B, Q, L, 2) or (B, Q, 2) normalised (x, y),
     value (B, S, dim), spatial_shapes (L, 2) int64 (H, W), level_start_index
     (L,) int64 -> (B, Q, dim). dim = num_heads * head_dim. norm=True: the output
     is LayerNorm(residual + attention), residual (B, Q, dim) the query unless
-    given (a query with its position added is not what the layer adds to)."""
+    given (a query with its position added is not what the layer adds to).
+    dropout: of the output projection's result, in training."""
 
     def __init__(self, dim: int = 256, num_heads: int = 8, num_levels: int = 4,
                  num_points: int = 4, accum: int = binding.MSDA_ACC_FP32_BUFFER,
-                 norm: bool = False):
+                 norm: bool = False, dropout: float = 0.0):
         super().__init__()
         if dim % num_heads != 0:
             raise ValueError("dim must be divisible by num_heads")
@@ -71,6 +150,7 @@ class MultiScaleDeformableAttention(nn.Module):
         self.attention_weights = nn.Linear(dim, num_heads * num_levels * num_points)
         self.value_proj = nn.Linear(dim, dim)
         self.output_proj = nn.Linear(dim, dim)
+        self.output_dropout = Dropout(dropout) if dropout > 0.0 else None
         self.norm = LayerNorm(dim) if norm else None
         self.ends_in_norm = norm         # a subclass may have a norm of its own under that name
         self.reset_parameters()
@@ -113,6 +193,9 @@ class MultiScaleDeformableAttention(nn.Module):
         out = binding.multi_scale_deformable_attention(v, spatial_shapes, level_start_index, loc,
                                                        logits, accum=self.accum, softmax=True)
         out = self.output_proj(out)
+        drop = getattr(self, "output_dropout", None)     # layers pickled before it have none
+        if isinstance(drop, Dropout):
+            out = drop(out)
         if norm is None:
             return out
         return norm(out, residual=query if residual is None else residual)
