@@ -37,6 +37,7 @@ msda_status_t check(const msda_attention_dims_t *d, msda_dtype_t dt, bool mask) 
     const int64_t *strides[3] = {d->q_stride, d->k_stride, d->v_stride};
     for (int t = 0; t < 3; ++t) {
         const int64_t size[3] = {len[0], t ? d->S : d->Q, t ? d->N : d->M};
+        if (size[0] * size[1] == 0) continue;                  // nothing there
         for (int i = 0; i < 3; ++i)
             if (!stride_ok(strides[t][i], size[i], e))
                 return strides[t][i] > 0 && strides[t][i] < kMaxStride ? MSDA_ERR_ALIGN : MSDA_ERR_SHAPE;
