@@ -228,6 +228,7 @@ msda_status_t msda_attention_forward(const void *q, const void *k, const void *v
     char *ws = static_cast<char *>(workspace);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e = masked ? pack_mask(a, d, w, mask, ws, false, s) : cudaSuccess;
+    a.chained = masked;
     if (e == cudaSuccess) e = launch_mode(a, d, dtype, msda::kForward, ws + w.part[0], s);
     return from_cuda(e);
 }
@@ -275,8 +276,11 @@ msda_status_t msda_attention_backward(const void *grad_out, const void *q, const
         a.norm_v = a.norm_do + kDeltaBlocks;
     }
     cudaError_t e = masked ? pack_mask(a, d, w, mask, ws, true, s) : cudaSuccess;
+    a.chained = masked;
     if (e == cudaSuccess) e = msda::launch_attention_delta(a, dtype, s);
+    a.chained = true;
     if (e == cudaSuccess && for_q) e = launch_mode(a, d, dtype, msda::kGradQ, ws + w.part[1], s);
+    a.overlapped = for_q;
     if (e == cudaSuccess && for_kv) e = launch_mode(a, d, dtype, msda::kGradKV, ws + w.part[2], s);
     return from_cuda(e);
 }

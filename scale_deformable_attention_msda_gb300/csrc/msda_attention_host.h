@@ -11,6 +11,23 @@ cudaError_t launch_attention_f32(int mode, const AttnArgs &a, int64_t blocks, cu
 cudaError_t launch_attention_bf16(int mode, const AttnArgs &a, int64_t blocks, cudaStream_t stream);
 cudaError_t launch_attention_f16(int mode, const AttnArgs &a, int64_t blocks, cudaStream_t stream);
 
+// A launch that may start while the kernel before it in the stream ends (chained; see
+// attn_after).
+template <class... P, class... A>
+cudaError_t launch_after(bool chained, void (*kernel)(P...), int64_t blocks, int threads, size_t shared, cudaStream_t stream, const A &...args) {
+    cudaLaunchAttribute attribute = {};
+    attribute.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attribute.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t config = {};
+    config.gridDim = dim3((unsigned)blocks);
+    config.blockDim = dim3((unsigned)threads);
+    config.dynamicSmemBytes = shared;
+    config.stream = stream;
+    config.attrs = &attribute;
+    config.numAttrs = chained ? 1 : 0;
+    return cudaLaunchKernelEx(&config, kernel, P(args)...);
+}
+
 // Whether a key tile's few queries are walked by small blocks, two an SM, one starting
 // while the other ends, rather than by one an SM with tiles of 128 columns. 100 queries of
 // 32 heads over 4,096 keys, fp16, D 32, the whole backward: 73 us, 94 with large blocks; 300

@@ -16,6 +16,7 @@ constexpr int kPackQ = 64, kPackK = 128;
 __global__ void __launch_bounds__(256) attn_pack_kernel(const AttnMaskSource m, uint32_t *by_query, int words_q,
                                                         uint32_t *by_key, int words_k, uint8_t *classes, int granules) {
     __shared__ uint32_t word[kPackQ][kPackK / 32 + 1];
+    attn_after();
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
     const int tk = granules / 2, tq = (m.Q + kPackQ - 1) / kPackQ;
     int64_t t = blockIdx.x;
@@ -78,6 +79,7 @@ constexpr int kDeltaThreads = 256;
 template <typename T, int L>
 __global__ void __launch_bounds__(kDeltaThreads) attn_delta_kernel(const AttnArgs a) {
     constexpr int V = 16 / sizeof(T), per = kDeltaThreads / L, AT_ONCE = 4;
+    attn_after();
     const int lane = threadIdx.x % L, d = lane * V;
     const int64_t rows = (int64_t)a.B * a.stat_row * a.M, step = (int64_t)gridDim.x * per;
     float most_do = 0.0f, most_v = 0.0f;
@@ -166,11 +168,10 @@ __global__ void __launch_bounds__(kDeltaThreads) attn_delta_kernel(const AttnArg
 
 template <typename T> cudaError_t launch_delta(const AttnArgs &a, cudaStream_t stream) {
     const int lanes = a.D * (int)sizeof(T) / 16;
-    if (lanes <= 4) attn_delta_kernel<T, 4><<<a.norms, kDeltaThreads, 0, stream>>>(a);
-    else if (lanes <= 8) attn_delta_kernel<T, 8><<<a.norms, kDeltaThreads, 0, stream>>>(a);
-    else if (lanes <= 16) attn_delta_kernel<T, 16><<<a.norms, kDeltaThreads, 0, stream>>>(a);
-    else attn_delta_kernel<T, 32><<<a.norms, kDeltaThreads, 0, stream>>>(a);
-    return cudaGetLastError();
+    if (lanes <= 4) return launch_after(a.chained, attn_delta_kernel<T, 4>, a.norms, kDeltaThreads, 0, stream, a);
+    if (lanes <= 8) return launch_after(a.chained, attn_delta_kernel<T, 8>, a.norms, kDeltaThreads, 0, stream, a);
+    if (lanes <= 16) return launch_after(a.chained, attn_delta_kernel<T, 16>, a.norms, kDeltaThreads, 0, stream, a);
+    return launch_after(a.chained, attn_delta_kernel<T, 32>, a.norms, kDeltaThreads, 0, stream, a);
 }
 
 // Sums of the splits: a warp a row, four channels a lane, and where that leaves lanes the
@@ -180,6 +181,7 @@ template <typename T> cudaError_t launch_delta(const AttnArgs &a, cudaStream_t s
 template <typename T, int LD>
 __global__ void __launch_bounds__(128) attn_join_kernel(const AttnArgs a, int mode) {
     constexpr int GROUPS = 32 / LD;
+    attn_after();
     const int lane = threadIdx.x & 31, group = lane / LD, d = lane % LD * 4;
     const int64_t row = (int64_t)blockIdx.x * 4 + threadIdx.x / 32, step = a.part_rows * a.D;
     if (row >= a.part_rows) return;
@@ -237,12 +239,12 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const AttnArgs a, int mo
     }
 }
 
-template <typename T> void launch_join(int mode, const AttnArgs &a, cudaStream_t stream) {
-    const unsigned blocks = (unsigned)((a.part_rows + 3) / 4);
-    if (a.D <= 16) attn_join_kernel<T, 4><<<blocks, 128, 0, stream>>>(a, mode);
-    else if (a.D <= 32) attn_join_kernel<T, 8><<<blocks, 128, 0, stream>>>(a, mode);
-    else if (a.D <= 64) attn_join_kernel<T, 16><<<blocks, 128, 0, stream>>>(a, mode);
-    else attn_join_kernel<T, 32><<<blocks, 128, 0, stream>>>(a, mode);
+template <typename T> cudaError_t launch_join(int mode, const AttnArgs &a, cudaStream_t stream) {
+    const int64_t blocks = ((a.part_rows + 3) / 4);
+    if (a.D <= 16) return launch_after(true, attn_join_kernel<T, 4>, blocks, 128, 0, stream, a, mode);
+    if (a.D <= 32) return launch_after(true, attn_join_kernel<T, 8>, blocks, 128, 0, stream, a, mode);
+    if (a.D <= 64) return launch_after(true, attn_join_kernel<T, 16>, blocks, 128, 0, stream, a, mode);
+    return launch_after(true, attn_join_kernel<T, 32>, blocks, 128, 0, stream, a, mode);
 }
 
 }  // namespace
@@ -250,8 +252,7 @@ template <typename T> void launch_join(int mode, const AttnArgs &a, cudaStream_t
 cudaError_t launch_attention_pack(const AttnMaskSource &m, uint32_t *by_query, int words_q, uint32_t *by_key,
                                   int words_k, uint8_t *classes, int granules, cudaStream_t stream) {
     const int64_t blocks = (int64_t)m.B * m.M * ((m.Q + kPackQ - 1) / kPackQ) * (granules / 2);
-    attn_pack_kernel<<<(unsigned)blocks, 256, 0, stream>>>(m, by_query, words_q, by_key, words_k, classes, granules);
-    return cudaGetLastError();
+    return launch_after(false, attn_pack_kernel, blocks, 256, 0, stream, m, by_query, words_q, by_key, words_k, classes, granules);
 }
 
 cudaError_t launch_attention_delta(const AttnArgs &a, msda_dtype_t dt, cudaStream_t stream) {
@@ -260,10 +261,8 @@ cudaError_t launch_attention_delta(const AttnArgs &a, msda_dtype_t dt, cudaStrea
 }
 
 cudaError_t launch_attention_join(int mode, const AttnArgs &a, msda_dtype_t dt, cudaStream_t stream) {
-    if (dt == MSDA_F32) launch_join<float>(mode, a, stream);
-    else if (dt == MSDA_BF16) launch_join<__nv_bfloat16>(mode, a, stream);
-    else launch_join<__half>(mode, a, stream);
-    return cudaGetLastError();
+    return dt == MSDA_F32 ? launch_join<float>(mode, a, stream)
+         : dt == MSDA_BF16 ? launch_join<__nv_bfloat16>(mode, a, stream) : launch_join<__half>(mode, a, stream);
 }
 
 }  // namespace msda

@@ -95,6 +95,8 @@ __global__ void __launch_bounds__(kSimpleThreads) attn_simple_kernel(const AttnA
     const AttnRows w = attn_rows<MODE, R>(a, blockIdx.x / a.splits);
     const int64_t tiles = attn_column_tiles<MODE, C>(a);
     const int64_t j0 = tiles * split / a.splits, j1 = tiles * (split + 1) / a.splits;
+    if (MODE == kGradKV && a.overlapped) attn_let_next();
+    else attn_after();
 
     auto row_of = [&](const AttnTensor &t) {
         return [&, t](int r) { return w.valid(r) ? attn_at<T>(t, w.b, w.row_pos(r), w.row_head(r)) : nullptr; };
@@ -248,6 +250,7 @@ __global__ void __launch_bounds__(kSimpleThreads) attn_simple_kernel(const AttnA
             if (MODE != kForward) attn_store<T, MODE>(a, w, r, split, MODE == kGradKV, d, e2[i], f);
         }
     }
+    if (MODE == kGradKV && a.overlapped) attn_after_all();
 }
 
 template <typename T, int MODE, int DP>
@@ -257,8 +260,7 @@ cudaError_t launch_simple_d(const AttnArgs &a, int64_t blocks, cudaStream_t stre
         const cudaError_t e = cudaFuncSetAttribute(attn_simple_kernel<T, MODE, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e != cudaSuccess) return e;
     }
-    attn_simple_kernel<T, MODE, DP><<<(unsigned)blocks, kSimpleThreads, bytes, stream>>>(a);
-    return cudaGetLastError();
+    return launch_after(a.chained, attn_simple_kernel<T, MODE, DP>, blocks, kSimpleThreads, bytes, stream, a);
 }
 template <typename T, int MODE>
 cudaError_t launch_simple_mode(const AttnArgs &a, int64_t blocks, cudaStream_t stream) {

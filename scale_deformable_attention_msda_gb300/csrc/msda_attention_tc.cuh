@@ -263,6 +263,8 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
         bar_init_done();
         *dead = 0u;
     }
+    if (MODE == kGradKV && a.overlapped) attn_let_next();
+    else attn_after();
     TcBias<T> bias;
     if (MODE == kGradKV) {
         bias = TcBias<T>(a);
@@ -513,10 +515,16 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
                 bar_arrive(s_free);
             }
             if (cls != 2) {            // p, and with it ds unless dP is not finite, will be 0
-                asm volatile("");      // a branch, not a select for each score
 #pragma unroll
                 for (int k = 0; k < PART; ++k)
                     if (!((bits[k / 32] >> (k % 32)) & 1u)) v[k] = 0xff800000u;
+            }
+            // The weights' columns are free. Forward waits here, backward after its arithmetic; waited
+            // for after the maximum, 4096 x 4096 of 64 channels take 195 us, not 174.
+            if (MODE == kForward && K::WEIGHTS == 1 && it > 0) {
+                ok = bar_wait(tc_bar<K::WEIGHTS>(done, it - 1), tc_phase<K::WEIGHTS>(it - 1), dead, a.err);
+                if (!ok) break;
+                tmem_after_sync();
             }
             const float2 c2 = make_float2(c, c);
             auto pair = [](const uint32_t *x) { return make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])); };
@@ -534,6 +542,7 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
                     if (grow) top = high;
                     sum *= f;
                     if (it > 0) {
+                        if (K::WEIGHTS != 1)
                         ok = bar_wait(tc_bar<K::WEIGHTS>(done, it - 1), tc_phase<K::WEIGHTS>(it - 1), dead, a.err);
                         tmem_after_sync();
 #pragma unroll 1
@@ -549,10 +558,6 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
                 const float ref = top == -INFINITY ? -up : top * c - up;
                 const float2 ref2 = make_float2(-ref, -ref);
                 float2 sums[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-                if (K::WEIGHTS == 1 && it > 0) {   // the weights' columns are free
-                    ok = ok && bar_wait(tc_bar<K::WEIGHTS>(done, it - 1), tc_phase<K::WEIGHTS>(it - 1), dead, a.err);
-                    tmem_after_sync();
-                }
 #pragma unroll
                 for (int i = 0; i < PART; i += 32) {
                     uint32_t w[16];
@@ -611,9 +616,8 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
                     }
                 }
             }
-            // the weights' columns are free (forward's rows have waited)
-            if (K::WEIGHTS == 1 && it > 0 && (BACK || !any_valid)) {
-                ok = ok && bar_wait(tc_bar<K::WEIGHTS>(done, it - 1), tc_phase<K::WEIGHTS>(it - 1), dead, a.err);
+            if (BACK && K::WEIGHTS == 1 && it > 0) {
+                ok = bar_wait(tc_bar<K::WEIGHTS>(done, it - 1), tc_phase<K::WEIGHTS>(it - 1), dead, a.err);
                 tmem_after_sync();
             }
             if (!ok) break;
@@ -682,6 +686,7 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
         }
         tmem_before_sync();
     }
+    if (MODE == kGradKV && a.overlapped) attn_after_all();
     __syncthreads();
     if (warp == HELPER) {
         tmem_after_sync();
@@ -740,8 +745,7 @@ cudaError_t launch_tc_d(const AttnArgs &a, int64_t blocks, cudaStream_t stream) 
     auto *kernel = attn_tc_kernel<T, MODE, DP, SHORT>;
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, K::SHARED);
     if (e != cudaSuccess) return e;
-    kernel<<<(unsigned)blocks, K::THREADS, K::SHARED, stream>>>(a, maps);
-    return cudaGetLastError();
+    return launch_after(a.chained, kernel, blocks, K::THREADS, K::SHARED, stream, a, maps);
 }
 template <typename T, int MODE>
 cudaError_t launch_tc_mode(const AttnArgs &a, int64_t blocks, cudaStream_t stream) {
