@@ -85,6 +85,17 @@ ModePlan plan_mode(const msda_attention_dims_t &d, AttnMode mode, int R, int C, 
 int tile_rows(msda_dtype_t dt) { return dt == MSDA_F32 ? 64 : 128; }
 
 ModePlan plan_for(const msda_attention_dims_t &d, msda_dtype_t dt, AttnMode mode) {
+    if (msda::few_rows(mode, dt, d.Q, d.M / d.N)) {
+        // a key head's keys over as many blocks as two an SM leave it, 256 keys or more each
+        ModePlan p = {};
+        p.tiles = d.B * d.N;
+        int64_t s = p.tiles > 0 ? 2 * kSMs / p.tiles : 1;
+        if (s > d.S / 256) s = d.S / 256;
+        p.splits = (int)(s < 1 ? 1 : s > 64 ? 64 : s);
+        p.blocks = p.tiles * p.splits;
+        if (p.splits > 1) p.part = (size_t)p.splits * d.B * d.Q * d.M * (d.D + 2) * 4;
+        return p;
+    }
     if (dt == MSDA_F32) return plan_mode(d, mode, 64, 64, kSMs * (d.D <= 32 ? 3 : d.D <= 64 ? 2 : 1), 1);
     const bool is_short = msda::tc_short(mode, d.D, d.Q, d.M / d.N);
     const int columns = msda::tc_columns(mode, d.D, is_short), blocks = msda::tc_blocks(mode, d.D, is_short);
@@ -180,7 +191,8 @@ cudaError_t launch_mode(AttnArgs a, const msda_attention_dims_t &d, msda_dtype_t
     a.splits = p.splits;
     a.part = reinterpret_cast<float *>(part);
     a.part_rows = mode == msda::kGradKV ? d.B * d.S * d.N : d.B * d.Q * d.M;
-    const cudaError_t e = dt == MSDA_F32  ? msda::launch_attention_f32(mode, a, p.blocks, stream)
+    const cudaError_t e = msda::few_rows(mode, dt, d.Q, a.G) ? msda::launch_attention_few(a, p.blocks, stream)
+                        : dt == MSDA_F32  ? msda::launch_attention_f32(mode, a, p.blocks, stream)
                         : dt == MSDA_BF16 ? msda::launch_attention_bf16(mode, a, p.blocks, stream)
                                           : msda::launch_attention_f16(mode, a, p.blocks, stream);
     if (e != cudaSuccess || p.splits == 1) return e;
