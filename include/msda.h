@@ -323,9 +323,13 @@ MSDA_API msda_status_t msda_debug_corners(const int64_t *spatial_shapes,
  * add does nothing -- and a per-context fault word is set; nothing traps. The
  * workspace passes (zero, convert, the fp16 workspace's prepare and finish)
  * walk a flat range of the buffer they are given, bounded by their loops. Layer
- * norm's kernels are checked alike, clipping's by tensor, vector and entry. It
- * is a debugging stand-in for a memory checker, much slower than libmsda.so. The normal library exports
- * the same three entry points and never sets the word.
+ * norm's kernels are checked alike, clipping's by tensor, vector and entry;
+ * attention's by row: a row read that its tensor does not have is replaced by
+ * the first, one written is skipped (what TMA reads is bounded by its tensor's
+ * map; the workspace is not checked). Dropout walks flat ranges. It is a
+ * debugging stand-in for a memory checker, much slower than libmsda.so. The
+ * normal library exports the same three entry points and sets the word for
+ * waits alone.
  * msda_checked_build: 1 in libmsda_checked.so, 0 in libmsda.so.
  * msda_device_check: synchronizes `stream`, then reads and clears the fault
  *   word of the calling thread's current context: MSDA_ERR_DEVICE_BOUNDS if

@@ -35,10 +35,11 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kHalfUp = 14.0f, kHalfWeightUp = 7.0f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-// A tensor of positions and heads: strides in elements.
+// A tensor of positions and heads: strides in elements, and its extents.
 struct AttnTensor {
     const void *p;
     int64_t batch, pos, head;
+    int len, heads;
 };
 
 // The mask as bits, one word for 32 columns; strides in words, 0 repeats.
@@ -73,7 +74,7 @@ struct AttnArgs {
     int splits;                        // blocks that share a row tile's columns (this mode)
     float *part;                       // splits > 1: (splits, rows, D) sums, then (splits, rows, 2)
                                        // maximum and sum (forward); gradients of keys twice
-    int64_t part_rows;
+    int64_t part_rows;                 // rows of this mode's results
     unsigned *err;                     // device word of range faults and of waits that ran out
     // The kernels of one call follow each other in one stream, each started while the one
     // before it ends (see attn_after). chained: there is one before. overlapped (kGradKV):
@@ -94,7 +95,7 @@ __device__ __forceinline__ void attn_after() {
 __device__ __forceinline__ void attn_let_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void attn_after_all() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
-// Checked build: element `i` of a tensor of `n`; always true in the normal build.
+// Checked build: whether i is one of n; a fault otherwise. Always true in the normal build.
 __device__ __forceinline__ bool attn_ok(const AttnArgs &a, int64_t i, int64_t n) {
 #ifdef MSDA_CHECKED
     if (i >= 0 && i < n) return true;
@@ -105,9 +106,15 @@ __device__ __forceinline__ bool attn_ok(const AttnArgs &a, int64_t i, int64_t n)
 #endif
 }
 
+// A row of a tensor (checked build: its first in place of one that it does not have).
 template <typename T>
-__device__ __forceinline__ const T *attn_at(const AttnTensor &t, int b, int pos, int head) {
-    return static_cast<const T *>(t.p) + b * t.batch + pos * t.pos + head * t.head;
+__device__ __forceinline__ const T *attn_at(const AttnArgs &a, const AttnTensor &t, int b, int pos, int head) {
+    const T *first = static_cast<const T *>(t.p);
+    return attn_ok(a, b, a.B) && attn_ok(a, pos, t.len) && attn_ok(a, head, t.heads) ? first + b * t.batch + pos * t.pos + head * t.head : first;
+}
+__device__ __forceinline__ void attn_put_lse(const AttnArgs &a, int b, int head, int pos, float lse) {
+    const int64_t at = ((int64_t)b * a.M + head) * a.Q + pos;
+    if (attn_ok(a, at, (int64_t)a.B * a.M * a.Q)) a.lse[at] = lse;
 }
 
 // Where a row tile's rows are. FWD and DQ: `pack` heads a position.
@@ -213,9 +220,9 @@ __device__ __noinline__ void attn_exact_row(const AttnArgs &a, const AttnRows &w
                                             float m2, float (&acc1)[4], float (&acc2)[4]) {
     const int lane = threadIdx.x & 31;
     const int pos = w.row_pos(r), head = w.row_head(r);
-    const T *a1 = MODE == kGradKV ? attn_at<T>(a.k, w.b, pos, head) : attn_at<T>(a.q, w.b, pos, head);
-    const T *a2 = MODE == kGradKV ? attn_at<T>(a.v, w.b, pos, head)
-                                  : MODE == kGradQ ? attn_at<T>(a.go, w.b, pos, head) : nullptr;
+    const T *a1 = MODE == kGradKV ? attn_at<T>(a, a.k, w.b, pos, head) : attn_at<T>(a, a.q, w.b, pos, head);
+    const T *a2 = MODE == kGradKV ? attn_at<T>(a, a.v, w.b, pos, head)
+                                  : MODE == kGradQ ? attn_at<T>(a, a.go, w.b, pos, head) : nullptr;
     float lse2 = m2, delta = 0.0f;
     if (MODE == kGradQ) {
         const float *st = attn_stat(a, w.b, head, pos);
@@ -236,8 +243,8 @@ __device__ __noinline__ void attn_exact_row(const AttnArgs &a, const AttnRows &w
             const T *x1 = nullptr, *x2 = nullptr;
             float p = 0.0f, ds = 0.0f;
             if (on) {
-                x1 = MODE == kGradKV ? attn_at<T>(a.q, w.b, at, chead) : attn_at<T>(a.k, w.b, at, chead);
-                x2 = MODE == kGradKV ? attn_at<T>(a.go, w.b, at, chead) : attn_at<T>(a.v, w.b, at, chead);
+                x1 = MODE == kGradKV ? attn_at<T>(a, a.q, w.b, at, chead) : attn_at<T>(a, a.k, w.b, at, chead);
+                x2 = MODE == kGradKV ? attn_at<T>(a, a.go, w.b, at, chead) : attn_at<T>(a, a.v, w.b, at, chead);
                 float s = 0.0f, dp = 0.0f;
                 for (int d = 0; d < a.D; ++d) {
                     s = fmaf(Elem<T>::to_f(a1[d]), Elem<T>::to_f(x1[d]), s);
@@ -272,7 +279,8 @@ __device__ __noinline__ void attn_exact_row(const AttnArgs &a, const AttnRows &w
 }
 
 // A value of the output, and what its rounding left.
-template <typename T> __device__ __forceinline__ void attn_put(void *out, void *rest, int64_t at, float v) {
+template <typename T> __device__ __forceinline__ void attn_put(const AttnArgs &a, void *out, void *rest, int64_t at, float v) {
+    if (!attn_ok(a, at, a.part_rows * a.D)) return;
     const T rounded = Elem<T>::from_f(v);
     static_cast<T *>(out)[at] = rounded;
     if (rest) static_cast<T *>(rest)[at] = Elem<T>::from_f(v - Elem<T>::to_f(rounded));
@@ -291,7 +299,7 @@ __device__ __forceinline__ void attn_store(const AttnArgs &a, const AttnRows &w,
         return;
     }
     void *to = MODE == kForward ? a.out : MODE == kGradQ ? a.gq : which ? a.gk : a.gv;
-    attn_put<T>(to, MODE == kForward ? a.rest : nullptr, row * a.D + d, sum * f);
+    attn_put<T>(a, to, MODE == kForward ? a.rest : nullptr, row * a.D + d, sum * f);
 }
 
 }  // namespace msda

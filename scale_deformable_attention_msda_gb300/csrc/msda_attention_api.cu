@@ -117,7 +117,7 @@ Layout layout_of(const msda_attention_dims_t &d, msda_dtype_t dt, bool mask, boo
         return here;
     };
     if (mask) {
-        // sized for a mask that repeats nowhere: the size query does not depend on strides
+        // a mask that repeats along a dimension is packed once for all of it
         w.mb = d.B > 1 && d.mask_stride[0] == 0 ? 1 : (int)d.B;
         w.mm = d.mask_stride[1] == 0 ? 1 : (int)d.M;
         w.mq = d.mask_stride[2] == 0 ? 1 : (int)d.Q;
@@ -141,16 +141,16 @@ Layout layout_of(const msda_attention_dims_t &d, msda_dtype_t dt, bool mask, boo
     return w;
 }
 
-msda::AttnTensor strided(const void *p, const int64_t *s) { return {p, s[0], s[1], s[2]}; }
+msda::AttnTensor strided(const void *p, const int64_t *s, int64_t len, int64_t heads) { return {p, s[0], s[1], s[2], (int)len, (int)heads}; }
 msda::AttnTensor dense(const void *p, int64_t len, int64_t heads, int64_t D) {
-    return {p, len * heads * D, heads * D, D};
+    return {p, len * heads * D, heads * D, D, (int)len, (int)heads};
 }
 
 AttnArgs common_args(const msda_attention_dims_t &d, const void *q, const void *k, const void *v, double scale) {
     AttnArgs a = {};
-    a.q = strided(q, d.q_stride);
-    a.k = strided(k, d.k_stride);
-    a.v = strided(v, d.v_stride);
+    a.q = strided(q, d.q_stride, d.Q, d.M);
+    a.k = strided(k, d.k_stride, d.S, d.N);
+    a.v = strided(v, d.v_stride, d.S, d.N);
     a.B = (int)d.B;
     a.Q = (int)d.Q;
     a.S = (int)d.S;

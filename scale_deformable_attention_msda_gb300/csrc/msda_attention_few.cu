@@ -56,7 +56,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) attn_few_kernel(const AttnArgs
     for (int r = 0; r < R; ++r) {
         Channels x;
         x.zero();
-        if (w.valid(r) && mine) x.load(attn_at<float>(a.q, w.b, w.row_pos(r), w.row_head(r)) + d);
+        if (w.valid(r) && mine) x.load(attn_at<float>(a, a.q, w.b, w.row_pos(r), w.row_head(r)) + d);
         x.get(q[r]);
         words[r] = w.valid(r) ? attn_word_row<kForward>(a, w.b, w.row_head(r), w.row_pos(r)) : nullptr;
         top[r] = -INFINITY;
@@ -75,8 +75,8 @@ __global__ void __launch_bounds__(kFewThreads, 2) attn_few_kernel(const AttnArgs
             k[u].zero();
             v[u].zero();
             if (key < k1 && mine) {
-                k[u].load(attn_at<float>(a.k, w.b, key, n) + d);
-                v[u].load(attn_at<float>(a.v, w.b, key, n) + d);
+                k[u].load(attn_at<float>(a, a.k, w.b, key, n) + d);
+                v[u].load(attn_at<float>(a, a.v, w.b, key, n) + d);
             }
         }
         uint32_t on = 0u;              // bit r U + u
@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) attn_few_kernel(const AttnArgs
                 ml[0] = all == 0.0f ? -INFINITY : base;
                 ml[1] = all;
             } else if (a.lse) {
-                a.lse[((int64_t)w.b * a.M + w.row_head(r)) * a.Q + w.row_pos(r)] = all == 0.0f ? -INFINITY : (base + log2f(all)) * kLn2;
+                attn_put_lse(a, w.b, w.row_head(r), w.row_pos(r), all == 0.0f ? -INFINITY : (base + log2f(all)) * kLn2);
             }
         }
         attn_store<float, kForward>(a, w, r, split, 0, at, value, all == 0.0f ? 0.0f : 1.0f / all);

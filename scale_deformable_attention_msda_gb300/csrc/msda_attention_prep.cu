@@ -96,9 +96,10 @@ __global__ void __launch_bounds__(kDeltaThreads) attn_delta_kernel(const AttnArg
             lse[i] = -INFINITY;
             if (r < rows && q < a.Q) {
                 if (lane == 0) lse[i] = a.lse[((int64_t)b * a.M + m) * a.Q + q];
-                const int64_t at = (((int64_t)b * a.Q + q) * a.M + m) * a.D + d;
-                if (d < a.D) {
-                    x[i] = ldg16(static_cast<const T *>(a.go.p) + at);
+                if (d < a.D) {         // these three lie alike
+                    const T *go = attn_at<T>(a, a.go, b, q, m) + d;
+                    const int64_t at = go - static_cast<const T *>(a.go.p);
+                    x[i] = ldg16(go);
                     y[i] = ldg16(static_cast<const T *>(a.o.p) + at);
                     if (a.rest) z[i] = ldg16(static_cast<const T *>(a.rest) + at);
                 }
@@ -135,7 +136,7 @@ __global__ void __launch_bounds__(kDeltaThreads) attn_delta_kernel(const AttnArg
         for (int i = 0; i < AT_ONCE; ++i) {
             const int64_t r = r0 + i * step, bs = r / a.N;
             const int b = (int)(bs / a.S);
-            x[i] = r < keys && d < a.D ? ldg16(attn_at<T>(a.v, b, (int)(bs - (int64_t)b * a.S), (int)(r - bs * a.N)) + d) : make_uint4(0u, 0u, 0u, 0u);
+            x[i] = r < keys && d < a.D ? ldg16(attn_at<T>(a, a.v, b, (int)(bs - (int64_t)b * a.S), (int)(r - bs * a.N)) + d) : make_uint4(0u, 0u, 0u, 0u);
         }
 #pragma unroll
         for (int i = 0; i < AT_ONCE; ++i) {
@@ -230,12 +231,12 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const AttnArgs a, int mo
         void *to = mode == kForward ? a.out : mode == kGradQ ? a.gq : which ? a.gk : a.gv;
         const float v[4] = {acc.x * f, acc.y * f, acc.z * f, acc.w * f};
 #pragma unroll
-        for (int k = 0; k < 4; ++k) attn_put<T>(to, mode == kForward ? a.rest : nullptr, row * a.D + d + k, v[k]);
+        for (int k = 0; k < 4; ++k) attn_put<T>(a, to, mode == kForward ? a.rest : nullptr, row * a.D + d + k, v[k]);
     }
     if (mode == kForward && a.lse && lane == 0) {
         const int m = (int)(row % a.M);
         const int64_t bq = row / a.M;
-        a.lse[(bq / a.Q * a.M + m) * a.Q + bq % a.Q] = sum == 0.0f ? -INFINITY : (base + log2f(sum)) * kLn2;
+        attn_put_lse(a, (int)(bq / a.Q), m, (int)(bq % a.Q), sum == 0.0f ? -INFINITY : (base + log2f(sum)) * kLn2);
     }
 }
 

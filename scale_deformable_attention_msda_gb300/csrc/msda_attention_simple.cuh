@@ -19,19 +19,13 @@ template <int DP> struct SimpleShared {
 };
 
 // 64 rows of D channels into shared memory, zeros where `row` gives NULL and past D.
-template <typename T, int DP, class F>
+template <int DP, class F>
 __device__ __forceinline__ void simple_load(float *to, int D, F row) {
     for (int i = threadIdx.x; i < kSimpleTile * (DP / 4); i += kSimpleThreads) {
         const int r = i / (DP / 4), d = i % (DP / 4) * 4;
-        const T *from = row(r);
+        const float *from = row(r);
         float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (from && d < D) {
-            if constexpr (sizeof(T) == 4) {
-                v = __ldg(reinterpret_cast<const float4 *>(from + d));
-            } else {
-                v = make_float4(Elem<T>::to_f(from[d]), Elem<T>::to_f(from[d + 1]), Elem<T>::to_f(from[d + 2]), Elem<T>::to_f(from[d + 3]));
-            }
-        }
+        if (from && d < D) v = __ldg(reinterpret_cast<const float4 *>(from + d));
         *reinterpret_cast<float4 *>(to + r * (DP + 4) + d) = v;
     }
 }
@@ -85,7 +79,7 @@ __device__ __forceinline__ void simple_product(float (&acc)[4][DP / 16], const f
     }
 }
 
-template <typename T, int MODE, int DP>
+template <int MODE, int DP>
 __global__ void __launch_bounds__(kSimpleThreads) attn_simple_kernel(const AttnArgs a) {
     constexpr int R = kSimpleTile, C = kSimpleTile, E = DP / 16, LDP = SimpleShared<DP>::kLdP;
     extern __shared__ __align__(16) unsigned char raw[];
@@ -99,10 +93,10 @@ __global__ void __launch_bounds__(kSimpleThreads) attn_simple_kernel(const AttnA
     else attn_after();
 
     auto row_of = [&](const AttnTensor &t) {
-        return [&, t](int r) { return w.valid(r) ? attn_at<T>(t, w.b, w.row_pos(r), w.row_head(r)) : nullptr; };
+        return [&, t](int r) { return w.valid(r) ? attn_at<float>(a, t, w.b, w.row_pos(r), w.row_head(r)) : nullptr; };
     };
-    simple_load<T, DP>(sh.a1, a.D, row_of(MODE == kGradKV ? a.k : a.q));
-    if (MODE != kForward) simple_load<T, DP>(sh.a2, a.D, row_of(MODE == kGradKV ? a.v : a.go));
+    simple_load<DP>(sh.a1, a.D, row_of(MODE == kGradKV ? a.k : a.q));
+    if (MODE != kForward) simple_load<DP>(sh.a2, a.D, row_of(MODE == kGradKV ? a.v : a.go));
     if (threadIdx.x < R) sh.bad[threadIdx.x] = 0;
 
     float acc1[4][E], acc2[4][E], top[4], sum[4], lse2[4], delta[4];
@@ -133,10 +127,10 @@ __global__ void __launch_bounds__(kSimpleThreads) attn_simple_kernel(const AttnA
         if (!cls) continue;
         __syncthreads();
         auto column_of = [&](const AttnTensor &t) {
-            return [&, t](int c) { return pos + c < len ? attn_at<T>(t, w.b, pos + c, head) : nullptr; };
+            return [&, t](int c) { return pos + c < len ? attn_at<float>(a, t, w.b, pos + c, head) : nullptr; };
         };
-        simple_load<T, DP>(sh.x1, a.D, column_of(MODE == kGradKV ? a.q : a.k));
-        simple_load<T, DP>(sh.x2, a.D, column_of(MODE == kGradKV ? a.go : a.v));
+        simple_load<DP>(sh.x1, a.D, column_of(MODE == kGradKV ? a.q : a.k));
+        simple_load<DP>(sh.x2, a.D, column_of(MODE == kGradKV ? a.go : a.v));
         if (MODE == kGradKV) {
             if (threadIdx.x < C) {
                 const float *st = attn_stat(a, w.b, head, pos + threadIdx.x);
@@ -209,14 +203,13 @@ __global__ void __launch_bounds__(kSimpleThreads) attn_simple_kernel(const AttnA
         if (!w.valid(r)) continue;
         const float m2 = top[i] == -INFINITY ? 0.0f : top[i] * a.c;
         if (MODE == kForward && tx == 0) {
-            const int64_t at = ((int64_t)w.b * a.M + w.row_head(r)) * a.Q + w.row_pos(r);
             const int64_t row = ((int64_t)w.b * a.Q + w.row_pos(r)) * a.M + w.row_head(r);
             if (a.splits > 1) {
                 float *ml = a.part + (int64_t)a.splits * a.part_rows * a.D + 2 * ((int64_t)split * a.part_rows + row);
                 ml[0] = sum[i] == 0.0f ? -INFINITY : m2;
                 ml[1] = sum[i];
             } else if (a.lse) {
-                a.lse[at] = sum[i] == 0.0f ? -INFINITY : (m2 + log2f(sum[i])) * kLn2;
+                attn_put_lse(a, w.b, w.row_head(r), w.row_pos(r), sum[i] == 0.0f ? -INFINITY : (m2 + log2f(sum[i])) * kLn2);
             }
         }
         if (vote && a.classes) {       // not finite, and the mask may be why
@@ -232,47 +225,46 @@ __global__ void __launch_bounds__(kSimpleThreads) attn_simple_kernel(const AttnA
         for (int k = 0; k < E; ++k) {
             const int d = tx * E + k;
             if (d >= a.D) continue;
-            if (MODE != kGradQ) attn_store<T, MODE>(a, w, r, split, 0, d, acc1[i][k], MODE == kForward ? f : 1.0f);
-            if (MODE != kForward) attn_store<T, MODE>(a, w, r, split, MODE == kGradKV, d, acc2[i][k], f);
+            if (MODE != kGradQ) attn_store<float, MODE>(a, w, r, split, 0, d, acc1[i][k], MODE == kForward ? f : 1.0f);
+            if (MODE != kForward) attn_store<float, MODE>(a, w, r, split, MODE == kGradKV, d, acc2[i][k], f);
         }
     }
     __syncthreads();
     for (int r = threadIdx.x / 32; r < R; r += kSimpleThreads / 32) {
         if (!sh.bad[r]) continue;
         float e1[4], e2[4];
-        attn_exact_row<T, MODE, C>(a, w, r, j0, j1, MODE == kForward ? sh.stat[0][r] : 0.0f, e1, e2);
+        attn_exact_row<float, MODE, C>(a, w, r, j0, j1, MODE == kForward ? sh.stat[0][r] : 0.0f, e1, e2);
         const float f = MODE != kForward ? a.scale : sh.stat[1][r] == 0.0f ? 0.0f : 1.0f / sh.stat[1][r];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int d = lane + 32 * i;
             if (d >= a.D) continue;
-            if (MODE != kGradQ) attn_store<T, MODE>(a, w, r, split, 0, d, e1[i], MODE == kForward ? f : 1.0f);
-            if (MODE != kForward) attn_store<T, MODE>(a, w, r, split, MODE == kGradKV, d, e2[i], f);
+            if (MODE != kGradQ) attn_store<float, MODE>(a, w, r, split, 0, d, e1[i], MODE == kForward ? f : 1.0f);
+            if (MODE != kForward) attn_store<float, MODE>(a, w, r, split, MODE == kGradKV, d, e2[i], f);
         }
     }
     if (MODE == kGradKV && a.overlapped) attn_after_all();
 }
 
-template <typename T, int MODE, int DP>
+template <int MODE, int DP>
 cudaError_t launch_simple_d(const AttnArgs &a, int64_t blocks, cudaStream_t stream) {
     constexpr int bytes = (int)sizeof(SimpleShared<DP>);
     if (bytes > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(attn_simple_kernel<T, MODE, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        const cudaError_t e = cudaFuncSetAttribute(attn_simple_kernel<MODE, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e != cudaSuccess) return e;
     }
-    return launch_after(a.chained, attn_simple_kernel<T, MODE, DP>, blocks, kSimpleThreads, bytes, stream, a);
+    return launch_after(a.chained, attn_simple_kernel<MODE, DP>, blocks, kSimpleThreads, bytes, stream, a);
 }
-template <typename T, int MODE>
+template <int MODE>
 cudaError_t launch_simple_mode(const AttnArgs &a, int64_t blocks, cudaStream_t stream) {
-    return a.D <= 32 ? launch_simple_d<T, MODE, 32>(a, blocks, stream)
-         : a.D <= 64 ? launch_simple_d<T, MODE, 64>(a, blocks, stream)
-                     : launch_simple_d<T, MODE, 128>(a, blocks, stream);
+    return a.D <= 32 ? launch_simple_d<MODE, 32>(a, blocks, stream)
+         : a.D <= 64 ? launch_simple_d<MODE, 64>(a, blocks, stream)
+                     : launch_simple_d<MODE, 128>(a, blocks, stream);
 }
-template <typename T>
-cudaError_t launch_simple(int mode, const AttnArgs &a, int64_t blocks, cudaStream_t stream) {
-    return mode == kForward ? launch_simple_mode<T, kForward>(a, blocks, stream)
-         : mode == kGradQ   ? launch_simple_mode<T, kGradQ>(a, blocks, stream)
-                            : launch_simple_mode<T, kGradKV>(a, blocks, stream);
+inline cudaError_t launch_simple(int mode, const AttnArgs &a, int64_t blocks, cudaStream_t stream) {
+    return mode == kForward ? launch_simple_mode<kForward>(a, blocks, stream)
+         : mode == kGradQ   ? launch_simple_mode<kGradQ>(a, blocks, stream)
+                            : launch_simple_mode<kGradKV>(a, blocks, stream);
 }
 
 }  // namespace msda

@@ -1,20 +1,42 @@
 // Attention of 16-bit data on the tensor cores.
 //
 // A block holds 128 rows (queries, or keys in kGradKV) and walks tiles of BN
-// columns, in the three modes of msda_attention.cuh. One warp fetches tiles with
-// TMA, one lane of another issues every MMA, and NWG groups of four warps each
-// take every NWG-th column tile: each of their 128 threads has one whole row of
-// the scores, which it reads from tensor memory, so that a row's maximum and sum
-// need no exchange between threads. The weights go back to tensor memory in 16
-// bits, as the left operand of the second product; nothing of the scores touches
-// shared memory. The same tile in shared memory serves as the right operand of
-// both products, read along its rows for the scores and across them for the
-// second product.
+// columns, in the three modes of msda_attention.cuh:
 //
 //            scores                  second product
 // kForward   S = Q K'                O += P V
 // kGradQ     S = Q K', dP = dO V'    dQ += dS K
 // kGradKV    S = K Q', dP = V dO'    dV += P dO, dK += dS Q
+//
+// One warp fetches tiles with TMA, one issues the scores' MMAs, one those of the
+// second products, and in kGradKV one makes an operand of the queries' statistics
+// (tc_bias_row). The other warps, in groups of four, work on rows: each thread has
+// one row of the scores (PARTS 1), or a half of one (PARTS 2), which it reads from
+// tensor memory, so that a row's maximum and sum need no exchange between threads.
+// The weights go back to tensor memory in 16 bits, as the left operand of the second
+// product; nothing of the scores touches shared memory. The same tile in shared
+// memory serves as the right operand of both products, read along its rows for the
+// scores and across them for the second product.
+//
+// Roundings: the weights (P, dS) to the data's 16 bits, off by 2^-8 of the value at most in
+// bf16 and by 2^-11 in fp16, as the second product's operands have
+// to be; all sums, maxima and statistics are fp32.
+//
+// What bounds it: exponentials and conversions, not the products. Of 4096 x 4096 scores
+// of 32 heads, bf16, D 32 / 64 / 128:
+//   forward     168 / 174 / 242 us, 408 / 790 / 1,130 TFLOP/s; 2^29 exponentials at 16 a
+//               clock and SM take 115 us alone
+//   backward    483 / 531 / 832 us for 5 products' worth, 356 / 647 / 826 TFLOP/s (it
+//               computes 7)
+// Tiles, by what was measured at D 64 unless said otherwise:
+//   forward     two blocks of an SM (one waits for its products while the other takes
+//               exponentials) of 128 columns. 64 or 96 columns: slower, or the registers
+//               spill. D 128: tensor memory leaves 64 columns, and two buffers of weights.
+//   backward    one block with two groups of row warps, a half of each row's columns each:
+//               531 us; four groups 578, and three that take tiles in turn were slower than two.
+//               D 128 in kGradKV: the weights lie over the scores, so P is released, and
+//               its product issued, before dP is waited for.
+//   kGradKV for few queries: see tc_short.
 #pragma once
 
 #include <cudaTypedefs.h>
@@ -56,8 +78,9 @@ template <int MODE, int DP, bool SHORT> struct Tc : TcConfig<MODE, DP, SHORT> {
     static constexpr int PITCH = DP == 32 ? 64 : 128, PANELS = DP == 128 ? 2 : 1, PANEL = DP == 128 ? 64 : DP;
     static constexpr int ROW_BYTES = kTcRows * PITCH * PANELS, COL_BYTES = BN * PITCH * PANELS;
     static constexpr int ROW_THREADS = PARTS * 128, THREADS = ROW_THREADS + 128, PART = BN / PARTS;
-    // registers: 65,536 of an SM, spread evenly at the start and then by need
-    static constexpr int REGS_ROW = PARTS == 4 ? 104 : PARTS * C::BLOCKS == 4 ? 96 : 208, REGS_OTHER = PARTS == 4 ? 64 : PARTS * C::BLOCKS == 4 || PARTS == 1 ? 48 : 88;
+    // registers: 65,536 of an SM, spread evenly at the start and then by need: a row's thread
+    // has its scores of a tile in registers, 128 or (PARTS 2) 64 and as many of dP
+    static constexpr int REGS_ROW = 208, REGS_OTHER = PARTS == 1 ? 48 : 88;
     static_assert((PARTS * REGS_ROW + REGS_OTHER) * 128 <= 65536 / C::BLOCKS / THREADS / 8 * 8 * THREADS, "registers");
     // tensor memory: scores (and dP), weights, accumulators
     static constexpr int SCORES = BN * (BACK ? 2 : 1), WIDE = BN / 2 * (MODE == kGradKV ? 2 : 1);
@@ -124,6 +147,7 @@ __device__ __forceinline__ float tc_ds_scale(const AttnArgs &a) {
 template <typename T, int MODE>
 __device__ __forceinline__ void tc_store(const AttnArgs &a, int64_t row, int split, int which, int d0, const float *v,
                                          float f, float g) {
+    if (!attn_ok(a, row, a.part_rows)) return;
     if (a.splits > 1) {
         float *to = a.part + ((int64_t)(which * a.splits + split) * a.part_rows + row) * a.D;
 #pragma unroll
@@ -542,8 +566,7 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
                     if (grow) top = high;
                     sum *= f;
                     if (it > 0) {
-                        if (K::WEIGHTS != 1)
-                        ok = bar_wait(tc_bar<K::WEIGHTS>(done, it - 1), tc_phase<K::WEIGHTS>(it - 1), dead, a.err);
+                        if (K::WEIGHTS != 1) ok = bar_wait(tc_bar<K::WEIGHTS>(done, it - 1), tc_phase<K::WEIGHTS>(it - 1), dead, a.err);
                         tmem_after_sync();
 #pragma unroll 1
                         for (int i = 0; ok && i < DP; i += 16) {
@@ -624,9 +647,8 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
             if (any_valid) {
                 if constexpr (MODE == kGradKV && !K::SPLIT) tmem_store<PART / 2>(at_p, out);
                 if constexpr (BACK) tmem_store<PART / 2>(at_ds, out2);
+                tmem_wait_store();
             }
-            if (!ok) break;
-            if (any_valid) tmem_wait_store();
             tmem_before_sync();
             bar_arrive(tc_bar<K::WEIGHTS>(ready, it));
         }
@@ -646,7 +668,7 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
                     ml[0] = sum == 0.0f ? -INFINITY : ref;
                     ml[1] = sum;
                 } else if (a.lse) {
-                    a.lse[((int64_t)w.b * a.M + rhead) * a.Q + rpos] = sum == 0.0f ? -INFINITY : (ref + log2f(sum)) * kLn2;
+                    attn_put_lse(a, w.b, rhead, rpos, sum == 0.0f ? -INFINITY : (ref + log2f(sum)) * kLn2);
                 }
             }
             const float over = sum == 0.0f ? 0.0f : 1.0f / sum;

@@ -13,7 +13,10 @@
 // memory the same way (span_ok in msda_norm.cuh), the clipping's each unit against
 // its tensor and each vector and entry they scale (msda_gradnorm.cu); what those
 // keep in shared memory and the order of their blocks' partial results are not
-// checked. An access that would leave its tensor is
+// checked. Attention's threads check the rows of their tensors that they read and
+// write (attn_at, attn_put, tc_store); TMA is bounded by the tensor maps, and the
+// packed mask, the statistics and the splits' parts in the workspace are not checked.
+// Dropout walks flat ranges bounded by its loops. An access that would leave its tensor is
 // skipped and sets bit 0 of one device word per context; the host reads and
 // clears that word after a synchronisation. Nothing traps, so a fault found
 // this way leaves the context usable.

@@ -24,7 +24,6 @@ struct DropArgs {
     int64_t n;
     uint32_t threshold;
     double factor;
-    unsigned *err;
 };
 
 struct Philox {
@@ -164,10 +163,9 @@ msda_status_t msda_dropout(const void *x, const void *residual, void *out, int64
     const uintptr_t e = dtype == MSDA_F64 ? 8 : dtype == MSDA_F32 ? 4 : 2;
     if (!msda::aligned(x, e) || !msda::aligned(residual, e) || !msda::aligned(out, e) || !msda::aligned(counter, 8))
         return MSDA_ERR_ALIGN;
-    msda::DropArgs a = {x, residual, out, counter, n, 0u, 0.0, nullptr};
+    msda::DropArgs a = {x, residual, out, counter, n, 0u, 0.0};
     a.threshold = (uint32_t)nearbyint(p * 65536.0);
     a.factor = a.threshold < 65536u ? 65536.0 / (65536.0 - a.threshold) : 0.0;
-    if (msda::fault_word_for_launch(&a.err) != cudaSuccess) return MSDA_ERR_CUDA;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     const cudaError_t err = dtype == MSDA_F32  ? msda::launch<float>(a, s)
                           : dtype == MSDA_BF16 ? msda::launch<__nv_bfloat16>(a, s)

@@ -23,8 +23,8 @@ __device__ __forceinline__ unsigned long long nanoseconds() {
 }
 // One lane of a whole warp issues the instruction, always the same one. The warp's
 // code around it stays uniform, and with it descriptors and addresses, which these
-// instructions take from uniform registers: issued from a branch of one lane, an MMA
-// costs 70 cycles instead of 45.
+// instructions take from uniform registers: an MMA of 128 x 32 x 16 with its left operand
+// in tensor memory then takes 16 cycles, and 45 to 70 issued from a branch of one lane.
 #define ELECT(instruction) "{\n\t.reg .pred one;\n\telect.sync _|one, 0xffffffff;\n\t@one " instruction "\n\t}"
 
 __device__ __forceinline__ void bar_arrive_one(uint64_t *bar) {
@@ -44,7 +44,6 @@ __device__ __forceinline__ bool bar_try(uint64_t *bar, uint32_t parity) {
     uint32_t done;
     asm volatile("{\n\t.reg .pred p;\n\t"
                  "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-
                  "selp.u32 %0, 1, 0, p;\n\t}"
                  : "=r"(done)
                  : "r"(shared_at(bar)), "r"(parity)
@@ -119,9 +118,6 @@ __device__ __forceinline__ void bulk_load(void *to, const void *from, uint32_t b
     asm volatile(ELECT("cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];")
                  ::"r"(shared_at(to)), "l"(from), "r"(bytes), "r"(shared_at(bar))
                  : "memory");
-}
-__device__ __forceinline__ void tma_prefetch_map(const CUtensorMap *map) {
-    asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
 
 // ---------------------------------------------------------- tensor memory
