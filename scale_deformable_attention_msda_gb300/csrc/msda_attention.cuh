@@ -122,8 +122,9 @@ struct AttnRows {
     int b, head, pos, count;           // first head (of queries, or of keys) and position; positions
     int pack;
     __device__ __forceinline__ bool valid(int r) const { return r < count * pack; }
-    __device__ __forceinline__ int row_pos(int r) const { return pos + r / pack; }
-    __device__ __forceinline__ int row_head(int r) const { return head + r % pack; }
+    // (a division takes 20 instructions)
+    __device__ __forceinline__ int row_pos(int r) const { return pos + (pack == 1 ? r : r / pack); }
+    __device__ __forceinline__ int row_head(int r) const { return head + (pack == 1 ? 0 : r % pack); }
 };
 
 // Row tile number `t` of tiles of R rows.

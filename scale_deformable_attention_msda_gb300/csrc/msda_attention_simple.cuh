@@ -79,6 +79,23 @@ __device__ __forceinline__ void simple_product(float (&acc)[4][DP / 16], const f
     }
 }
 
+// E channels of a row from d on, two at a time (D is a multiple of 8, and of E).
+template <int MODE, int E>
+__device__ __forceinline__ void simple_store(const AttnArgs &a, const AttnRows &w, int r, int split, int which, int d, const float (&v)[E], float f) {
+    const int len = MODE == kGradKV ? a.S : a.Q, heads = MODE == kGradKV ? a.N : a.M;
+    const int64_t row = ((int64_t)w.b * len + w.row_pos(r)) * heads + w.row_head(r);
+    if (!attn_ok(a, row, a.part_rows)) return;
+    const bool parts = a.splits > 1;
+    float *to = parts ? a.part + ((int64_t)(which * a.splits + split) * a.part_rows + row) * a.D
+                      : static_cast<float *>(MODE == kForward ? a.out : MODE == kGradQ ? a.gq : which ? a.gk : a.gv) + row * a.D;
+    if (parts) f = 1.0f;
+#pragma unroll
+    for (int k = 0; k < E; k += 2) {
+        *reinterpret_cast<float2 *>(to + d + k) = make_float2(v[k] * f, v[k + 1] * f);
+        if (MODE == kForward && !parts && a.rest) *reinterpret_cast<float2 *>(static_cast<float *>(a.rest) + row * a.D + d + k) = make_float2(0.0f, 0.0f);
+    }
+}
+
 template <int MODE, int DP>
 __global__ void __launch_bounds__(kSimpleThreads) attn_simple_kernel(const AttnArgs a) {
     constexpr int R = kSimpleTile, C = kSimpleTile, E = DP / 16, LDP = SimpleShared<DP>::kLdP;
@@ -221,13 +238,9 @@ __global__ void __launch_bounds__(kSimpleThreads) attn_simple_kernel(const AttnA
             continue;
         }
         const float f = MODE == kForward ? (sum[i] == 0.0f ? 0.0f : 1.0f / sum[i]) : a.scale;
-#pragma unroll
-        for (int k = 0; k < E; ++k) {
-            const int d = tx * E + k;
-            if (d >= a.D) continue;
-            if (MODE != kGradQ) attn_store<float, MODE>(a, w, r, split, 0, d, acc1[i][k], MODE == kForward ? f : 1.0f);
-            if (MODE != kForward) attn_store<float, MODE>(a, w, r, split, MODE == kGradKV, d, acc2[i][k], f);
-        }
+        if (tx * E >= a.D) continue;
+        if (MODE != kGradQ) simple_store<MODE, E>(a, w, r, split, 0, tx * E, acc1[i], MODE == kForward ? f : 1.0f);
+        if (MODE != kForward) simple_store<MODE, E>(a, w, r, split, MODE == kGradKV, tx * E, acc2[i], f);
     }
     __syncthreads();
     for (int r = threadIdx.x / 32; r < R; r += kSimpleThreads / 32) {
