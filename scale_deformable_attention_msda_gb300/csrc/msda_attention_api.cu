@@ -96,7 +96,7 @@ ModePlan plan_for(const msda_attention_dims_t &d, msda_dtype_t dt, AttnMode mode
         if (p.splits > 1) p.part = (size_t)p.splits * d.B * d.Q * d.M * (d.D + 2) * 4;
         return p;
     }
-    if (dt == MSDA_F32) return plan_mode(d, mode, 64, 64, kSMs * (d.D <= 32 ? 3 : d.D <= 64 ? 2 : 1), 1);
+    if (dt == MSDA_F32) return plan_mode(d, mode, 64, 64, kSMs * msda::simple_blocks(d.D), 1);
     const bool is_short = msda::tc_short(mode, d.D, d.Q, d.M / d.N);
     const int columns = msda::tc_columns(mode, d.D, is_short), blocks = msda::tc_blocks(mode, d.D, is_short);
     return plan_mode(d, mode, 128, columns, kSMs * blocks, 4);

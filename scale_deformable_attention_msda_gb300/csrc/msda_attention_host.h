@@ -37,6 +37,9 @@ constexpr bool tc_short(int mode, int64_t D, int64_t Q, int64_t G) { return mode
 constexpr int tc_columns(int mode, int64_t D, bool is_short) { return is_short || (mode == kForward && D > 64) ? 64 : 128; }
 constexpr int tc_blocks(int mode, int64_t D, bool is_short) { return is_short || mode == kForward ? 2 : 1; }
 
+// The fp32 kernels' blocks of an SM, by registers and shared memory.
+constexpr int simple_blocks(int64_t D) { return D <= 64 ? 2 : 1; }
+
 // The forward in fp32 of at most four rows a key head (see msda_attention_few.cu).
 constexpr bool few_rows(int mode, msda_dtype_t dt, int64_t Q, int64_t G) { return mode == kForward && dt == MSDA_F32 && Q * G <= 4; }
 cudaError_t launch_attention_few(const AttnArgs &a, int64_t blocks, cudaStream_t stream);

@@ -1,5 +1,16 @@
 // Attention in fp32 arithmetic: tiles of 64 rows by 64 columns in shared memory,
-// scores and products with fused multiply-adds, 4 x 4 scores a thread.
+// scores and products with fused multiply-adds, 4 x 4 scores a thread. All of it is
+// fp32; no operand is rounded to fewer bits.
+//
+// What bounds it: the instructions around the multiply-adds (a shared-memory load of 16
+// bytes for every 8 of them, exponentials, addresses) and their latencies: 1024 x 1024 of
+// 16 heads, D 32 / 64 / 128: forward 96 / 150 / 342 us (22 to 29 TFLOP/s of 75), backward
+// 287 / 468 / 1,069. 300 queries of 16 heads, D 32, where a block has one tile or two:
+// 19 and 50 us. 8 x 4 scores and 128 threads, with packed multiply-adds: 114 us forward
+// instead of 101, 617 instead of 467 at D 128. The next tile's loads under way during the
+// arithmetic: no gain at D 32 (95.6 us, 96.4), slower at D 64 (509 us backward, 468). Three
+// blocks of an SM at D 32: 47 us instead of 50 for the 300 queries' backward, but 342
+// instead of 287 for 1024.
 #pragma once
 
 #include "msda_attention.cuh"
@@ -18,17 +29,25 @@ template <int DP> struct SimpleShared {
     int bad[kSimpleTile];
 };
 
-// 64 rows of D channels into shared memory, zeros where `row` gives NULL and past D.
-template <int DP, class F>
-__device__ __forceinline__ void simple_load(float *to, int D, F row) {
-    for (int i = threadIdx.x; i < kSimpleTile * (DP / 4); i += kSimpleThreads) {
-        const int r = i / (DP / 4), d = i % (DP / 4) * 4;
-        const float *from = row(r);
-        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (from && d < D) v = __ldg(reinterpret_cast<const float4 *>(from + d));
-        *reinterpret_cast<float4 *>(to + r * (DP + 4) + d) = v;
+// This thread's share of 64 rows of D channels on their way to shared memory; zeros where
+// `row` gives NULL and past D.
+template <int DP> struct SimpleRows {
+    static constexpr int N = kSimpleTile * (DP / 4) / kSimpleThreads, STEP = kSimpleThreads / (DP / 4);
+    float4 v[N];
+    template <class F> __device__ __forceinline__ void fetch(int D, F row) {
+        const int r = threadIdx.x / (DP / 4), d = threadIdx.x % (DP / 4) * 4;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const float *from = row(r + i * STEP);
+            v[i] = from && d < D ? __ldg(reinterpret_cast<const float4 *>(from + d)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        }
     }
-}
+    __device__ __forceinline__ void put(float *to) const {
+        const int r = threadIdx.x / (DP / 4), d = threadIdx.x % (DP / 4) * 4;
+#pragma unroll
+        for (int i = 0; i < N; ++i) *reinterpret_cast<float4 *>(to + (r + i * STEP) * (DP + 4) + d) = v[i];
+    }
+};
 
 // s[i][j] = row 4 ty + i of a times row tx + 16 j of x.
 template <int DP>
@@ -97,7 +116,7 @@ __device__ __forceinline__ void simple_store(const AttnArgs &a, const AttnRows &
 }
 
 template <int MODE, int DP>
-__global__ void __launch_bounds__(kSimpleThreads) attn_simple_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(kSimpleThreads, simple_blocks(DP)) attn_simple_kernel(const AttnArgs a) {
     constexpr int R = kSimpleTile, C = kSimpleTile, E = DP / 16, LDP = SimpleShared<DP>::kLdP;
     extern __shared__ __align__(16) unsigned char raw[];
     SimpleShared<DP> &sh = *reinterpret_cast<SimpleShared<DP> *>(raw);
@@ -112,8 +131,11 @@ __global__ void __launch_bounds__(kSimpleThreads) attn_simple_kernel(const AttnA
     auto row_of = [&](const AttnTensor &t) {
         return [&, t](int r) { return w.valid(r) ? attn_at<float>(a, t, w.b, w.row_pos(r), w.row_head(r)) : nullptr; };
     };
-    simple_load<DP>(sh.a1, a.D, row_of(MODE == kGradKV ? a.k : a.q));
-    if (MODE != kForward) simple_load<DP>(sh.a2, a.D, row_of(MODE == kGradKV ? a.v : a.go));
+    SimpleRows<DP> x1, x2;
+    x1.fetch(a.D, row_of(MODE == kGradKV ? a.k : a.q));
+    if (MODE != kForward) x2.fetch(a.D, row_of(MODE == kGradKV ? a.v : a.go));
+    x1.put(sh.a1);
+    if (MODE != kForward) x2.put(sh.a2);
     if (threadIdx.x < R) sh.bad[threadIdx.x] = 0;
 
     float acc1[4][E], acc2[4][E], top[4], sum[4], lse2[4], delta[4];
@@ -137,17 +159,20 @@ __global__ void __launch_bounds__(kSimpleThreads) attn_simple_kernel(const AttnA
         for (int k = 0; k < E; ++k) acc1[i][k] = acc2[i][k] = 0.0f;
     }
 
+    const int len = MODE == kGradKV ? a.Q : a.S;
     for (int64_t j = j0; j < j1; ++j) {
         int pos, head;
         attn_columns<MODE, C>(a, w, j, &pos, &head);
-        const int cls = attn_class<MODE, C>(a, w, pos, head), len = MODE == kGradKV ? a.Q : a.S;
+        const int cls = attn_class<MODE, C>(a, w, pos, head);
         if (!cls) continue;
-        __syncthreads();
         auto column_of = [&](const AttnTensor &t) {
             return [&, t](int c) { return pos + c < len ? attn_at<float>(a, t, w.b, pos + c, head) : nullptr; };
         };
-        simple_load<DP>(sh.x1, a.D, column_of(MODE == kGradKV ? a.q : a.k));
-        simple_load<DP>(sh.x2, a.D, column_of(MODE == kGradKV ? a.go : a.v));
+        x1.fetch(a.D, column_of(MODE == kGradKV ? a.q : a.k));
+        x2.fetch(a.D, column_of(MODE == kGradKV ? a.go : a.v));
+        __syncthreads();
+        x1.put(sh.x1);
+        x2.put(sh.x2);
         if (MODE == kGradKV) {
             if (threadIdx.x < C) {
                 const float *st = attn_stat(a, w.b, head, pos + threadIdx.x);

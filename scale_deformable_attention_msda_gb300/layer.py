@@ -58,7 +58,9 @@ class Dropout(nn.Module):
     """Dropout of libmsda's counter-based generator (binding.dropout), in training; of x, or
     of x on its way into residual + x. `state`, a buffer, holds the generator's seed, drawn
     from torch's, and the number of the next draw, and is advanced on the device at each call
-    in training: a captured step draws anew each time it is replayed."""
+    in training: a captured step draws anew each time it is replayed, and so does a forward
+    that is run again for its backward (activation checkpointing), whose gradients would then be
+    of another draw: there use binding.dropout with one counter."""
 
     def __init__(self, p: float = 0.1):
         super().__init__()
