@@ -98,7 +98,8 @@ __device__ __forceinline__ void simple_product(float (&acc)[4][DP / 16], const f
     }
 }
 
-// E channels of a row from d on, two at a time (D is a multiple of 8, and of E).
+// E channels of a row from d on, two at a time (E divides 8, and D is a multiple of 8).
+// The sums are of the output's type: its rounding leaves nothing.
 template <int MODE, int E>
 __device__ __forceinline__ void simple_store(const AttnArgs &a, const AttnRows &w, int r, int split, int which, int d, const float (&v)[E], float f) {
     const int len = MODE == kGradKV ? a.S : a.Q, heads = MODE == kGradKV ? a.N : a.M;
