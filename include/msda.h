@@ -564,7 +564,10 @@ MSDA_API msda_status_t msda_attention_forward(const void *q, const void *k, cons
  * with no key gets zeros. Sums are held in fp32 and added in an order that the
  * sizes fix: the same call gives the same bits. For 16-bit data p and ds are
  * rounded to `dtype` as operands of the products that follow (fp16: scaled by
- * powers of two that keep them in range). Errors and workspace as the forward. */
+ * powers of two that keep them in range). p has the error of its score and lse
+ * as fp32 numbers in its exponent: past scores of about 2^20 the gradients mean
+ * little, and past 2^21 fp16's need not be finite. Errors and workspace as the
+ * forward. */
 MSDA_API msda_status_t msda_attention_backward(const void *grad_out, const void *q, const void *k,
                                                const void *v, const void *mask, const void *out,
                                                const void *rest, const void *lse, void *grad_q,

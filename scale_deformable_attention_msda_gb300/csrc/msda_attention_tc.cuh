@@ -90,7 +90,7 @@ template <int MODE, int DP, bool SHORT> struct Tc : TcConfig<MODE, DP, SHORT> {
     static_assert(MODE != kForward || PARTS == 1, "one maximum and sum a row");
     static_assert(USED <= 512 && COLS * C::BLOCKS <= 512, "tensor memory");
     static constexpr int TILES = (BACK ? 2 : 1) * ROW_BYTES + (STAGES + EARLY) * COL_BYTES;
-    // of a column tile: the queries' statistics, and the same as an operand (see tc_bias)
+    // of a column tile: the queries' statistics, and the same as an operand (see tc_bias_row)
     static constexpr int STAT_BYTES = MODE == kGradKV ? 8 * BN : 0, BIAS_BYTES = MODE == kGradKV ? 32 * BN : 0;
     static constexpr int ONES_BYTES = MODE == kGradKV ? 32 * kTcRows : 0;
     static constexpr int INFO = 8;
@@ -189,43 +189,27 @@ template <int WEIGHTS> __device__ __forceinline__ uint64_t *tc_bar(uint64_t *bar
 template <int WEIGHTS> __device__ __forceinline__ uint32_t tc_phase(int it) { return (WEIGHTS == 2 ? it >> 1 : it) & 1; }
 
 // kGradKV: -lse and -delta of the columns' queries, added to the scores and to dP by one
-// more step of their products: 1, 1, 1 times the three parts that a number has in 16 bits,
+// more step of their products: 1, 1, 1 times the three parts that a number has in bf16,
 // which together hold its fp32 digits. Read from shared memory by the rows' threads instead,
 // 8 bytes a column for every warp, they alone took 1,024 cycles a tile.
 //
-// -lse is divided by c beforehand. fp16: both are scaled into range by powers of two that
-// stand in place of the ones: -lse / c by c (below 2^-26, where scores mean nothing any
-// more, c is taken as that), -delta by its bound.
+// -lse is divided by c beforehand. This step's operands are bf16 for fp16 data too, whose
+// own 16 bits end at 65504: -lse / c is as large as the largest score.
 //
 // 16 values of a row are two runs of 16 bytes; 8 rows' runs lie together (no swizzle).
-template <typename T>
 __device__ __forceinline__ void tc_bias_row(unsigned char *tile, int r, float a, float b, float c, float d, float e, float f) {
     uint4 *at = reinterpret_cast<uint4 *>(tile + r / 8 * 256 + r % 8 * 16);
-    at[0] = make_uint4(pack2<T>(a, b), pack2<T>(c, d), pack2<T>(e, f), 0u);
+    at[0] = make_uint4(pack2<__nv_bfloat16>(a, b), pack2<__nv_bfloat16>(c, d), pack2<__nv_bfloat16>(e, f), 0u);
     at[8] = make_uint4(0u, 0u, 0u, 0u);
 }
-template <typename T> struct TcBias {
-    float one_s = 1.0f, one_d = 1.0f, over_c = 0.0f, none = 0.0f;
-    __device__ __forceinline__ TcBias() {}
-    static __device__ __forceinline__ float columns_c(const AttnArgs &a) { return TcScale<T>::backward > 0.0f ? fmaxf(a.c, 0x1p-26f) : a.c; }
-    __device__ __forceinline__ explicit TcBias(const AttnArgs &a) {
-        over_c = 1.0f / columns_c(a);
-        none = -1e37f;
-        if (a.norm_do) {
-            one_s = ldexpf(1.0f, max(0, min(15, ilogbf(over_c) + 2)));   // |lse2 / c| <= |lse2| one_s / 2
-            none = -60000.0f * one_s;
-            int e = 1 - ilogbf(tc_ds_scale(a));                          // |delta| < 2^(e - 1)
-            one_d = ldexpf(1.0f, max(-14, min(15, e - 16)));
-        }
-    }
-    // Query r's row of the operand from its pair of stat.
-    __device__ __forceinline__ void put(unsigned char *tile, int r, const float *st) const {
-        float l = (st[0] == -INFINITY ? none : st[0] * over_c) / one_s, d = st[2] / one_d;
-        const float l1 = Elem<T>::to_f(Elem<T>::from_f(l)), l2 = Elem<T>::to_f(Elem<T>::from_f(l - l1));
-        const float d1 = Elem<T>::to_f(Elem<T>::from_f(d)), d2 = Elem<T>::to_f(Elem<T>::from_f(d - d1));
-        tc_bias_row<T>(tile, r, l1, l2, l - l1 - l2, d1, d2, d - d1 - d2);
-    }
-};
+__device__ __forceinline__ float tc_bf16(float v) { return __bfloat162float(__float2bfloat16_rn(v)); }
+// Query r's row of the operand from its pair of stat. A query without keys (or past the
+// last) gets a number that leaves no weight at the smallest c, 1e-30.
+__device__ __forceinline__ void tc_bias_put(unsigned char *tile, int r, const float *st, float over_c) {
+    const float l = st[0] == -INFINITY ? -1e37f : st[0] * over_c, d = st[2];
+    const float l1 = tc_bf16(l), l2 = tc_bf16(l - l1), d1 = tc_bf16(d), d2 = tc_bf16(d - d1);
+    tc_bias_row(tile, r, l1, l2, l - l1 - l2, d1, d2, d - d1 - d2);
+}
 
 struct TcMaps {
     CUtensorMap a1, a2, x1, x2;        // rows: one or two; columns: two
@@ -289,13 +273,11 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
     }
     if (MODE == kGradKV && a.overlapped) attn_let_next();
     else attn_after();
-    TcBias<T> bias;
     if (MODE == kGradKV) {
-        bias = TcBias<T>(a);
         for (int i = threadIdx.x; i < 2 * kTcRows; i += K::THREADS) {
             const bool for_s = i < kTcRows;
-            const float x = for_s ? bias.one_s : 0.0f, y = for_s ? 0.0f : bias.one_d;
-            tc_bias_row<T>(ones + (for_s ? 0 : K::ONES_BYTES), i % kTcRows, x, x, x, y, y, y);
+            const float x = for_s ? 1.0f : 0.0f, y = for_s ? 0.0f : 1.0f;
+            tc_bias_row(ones + (for_s ? 0 : K::ONES_BYTES), i % kTcRows, x, x, x, y, y, y);
         }
         shared_to_async();
     }
@@ -367,7 +349,8 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
             const uint32_t a1 = desc_low(shared_at(tile_a1), 16), a2 = desc_low(shared_at(tile_a2), 16);
             const uint32_t late = desc_low(shared_at(tile_late), 16), early = desc_low(shared_at(tile_early), 16);
             const uint32_t bias_at = desc_low(shared_at(tile_bias), 128), ones_at = desc_low(shared_at(ones), 128);
-            constexpr uint32_t id = mma_desc<BF16, BN, false>(), high = desc_high<K::PITCH>(), plain = desc_high_plain(256);
+            constexpr uint32_t id = mma_desc<BF16, BN, false>(), high = desc_high<K::PITCH>();
+            constexpr uint32_t bias_id = mma_desc<true, BN, false>(), plain = desc_high_plain(256);
             constexpr int per = K::PITCH / 32;      // steps of 16 channels in a panel
             // the products of a row tile and a column tile
             auto product = [&](uint32_t d, uint32_t rows, uint32_t columns) {
@@ -404,7 +387,7 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
                 const uint32_t x_late = late + st.at * desc_step(K::COL_BYTES), x_early = early + se.at * desc_step(K::COL_BYTES);
                 const uint32_t columns = bias_at + st.at * desc_step(K::BIAS_BYTES);
                 product(tmem, a1, FIRST_EARLY ? x_early : x_late);
-                if (MODE == kGradKV) mma_shared<id, plain>(tmem, ones_at, columns, true);
+                if (MODE == kGradKV) mma_shared<bias_id, plain>(tmem, ones_at, columns, true);
                 if (MODE == kForward) mma_commit(empty_early + se.at);
                 if (!BACK || K::SPLIT) mma_commit(s_full);
                 if (BACK) {
@@ -414,7 +397,7 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
                         tmem_after_sync();
                     }
                     product(tmem + BN, a2, x_early);
-                    if (MODE == kGradKV) mma_shared<id, plain>(tmem + BN, ones_at + desc_step(K::ONES_BYTES), columns, true);
+                    if (MODE == kGradKV) mma_shared<bias_id, plain>(tmem + BN, ones_at + desc_step(K::ONES_BYTES), columns, true);
                     if (MODE == kGradQ) mma_commit(empty_early + se.at);
                     mma_commit(K::SPLIT ? d_full : s_full);
                 }
@@ -472,11 +455,12 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
             }
         } else if (MODE == kGradKV) {
             // -------------------------------------------- the queries' statistics as an operand
+            const float over_c = 1.0f / a.c;
             Ring<STAGES> st;
             for (int it = 0;; ++it, st.next()) {
                 if (!bar_wait(full + st.at, st.phase, dead, a.err) || !info[it % INFO].cls) break;
                 for (int i = lane; i < BN; i += 32)
-                    bias.put(tile_bias + st.at * K::BIAS_BYTES, i, reinterpret_cast<const float *>(tile_stat + st.at * K::STAT_BYTES) + i / 2 * 4 + i % 2);
+                    tc_bias_put(tile_bias + st.at * K::BIAS_BYTES, i, reinterpret_cast<const float *>(tile_stat + st.at * K::STAT_BYTES) + i / 2 * 4 + i % 2, over_c);
                 shared_to_async();
                 __syncwarp();
                 bar_arrive_one(bias_full + st.at);
@@ -492,7 +476,7 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
         const uint32_t mine = tmem + ((uint32_t)(r & ~31) << 16), at_acc = mine + K::ACC;
         constexpr int PART = K::PART;
         const int rpos = w.row_pos(valid ? r : 0), rhead = w.row_head(valid ? r : 0);
-        const float c = MODE == kGradKV ? TcBias<T>::columns_c(a) : a.c;
+        const float c = a.c;
         float ds_scale = 1.0f;
         if (BACK && a.norm_do) ds_scale = tc_ds_scale(a);
         constexpr float up = TcScale<T>::forward;
