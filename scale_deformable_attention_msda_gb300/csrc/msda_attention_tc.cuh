@@ -91,11 +91,11 @@ template <int MODE, int DP, bool SHORT> struct Tc : TcConfig<MODE, DP, SHORT> {
     static_assert(USED <= 512 && COLS * C::BLOCKS <= 512, "tensor memory");
     static constexpr int TILES = (BACK ? 2 : 1) * ROW_BYTES + (STAGES + EARLY) * COL_BYTES;
     // of a column tile: the queries' statistics, and the same as an operand (see tc_bias_row)
-    static constexpr int STAT_BYTES = MODE == kGradKV ? 8 * BN : 0, BIAS_BYTES = MODE == kGradKV ? 32 * BN : 0;
-    static constexpr int ONES_BYTES = MODE == kGradKV ? 32 * kTcRows : 0;
+    static constexpr int STAT_BYTES = MODE == kGradKV ? 8 * BN : 0, BIAS_BYTES = MODE == kGradKV ? 48 * BN : 0;
+    static constexpr int ONES_BYTES = MODE == kGradKV ? 48 * kTcRows : 0;
     static constexpr int INFO = 8;
     static_assert(STAGES + 1 <= INFO, "announcements are read before they are written over");
-    static constexpr int NEEDED = 1024 + TILES + STAGES * (STAT_BYTES + BIAS_BYTES) + 2 * ONES_BYTES + 1024;
+    static constexpr int NEEDED = 1024 + TILES + STAGES * (STAT_BYTES + BIAS_BYTES) + ONES_BYTES + 1024;
     // as much as keeps one block more off the SM, which would only wait for its tensor memory
     static constexpr int LIMIT = 228 * 1024 / (C::BLOCKS + 1);
     static constexpr int SHARED = NEEDED > LIMIT ? NEEDED : LIMIT;
@@ -196,11 +196,15 @@ template <int WEIGHTS> __device__ __forceinline__ uint32_t tc_phase(int it) { re
 // -lse is divided by c beforehand. This step's operands are bf16 for fp16 data too, whose
 // own 16 bits end at 65504: -lse / c is as large as the largest score.
 //
-// 16 values of a row are two runs of 16 bytes; 8 rows' runs lie together (no swizzle).
+// 16 values of a row are two runs of 16 bytes; 8 rows' runs lie together (no swizzle). The
+// scores' step and dP's share no run but one of zeros between theirs: in one run, a delta
+// that is not finite would make 0 times itself a part of the scores.
+constexpr int kBiasGroup = 3 * 128, kBiasForD = 128;       // bytes of 8 rows; where dP's runs begin
 __device__ __forceinline__ void tc_bias_row(unsigned char *tile, int r, float a, float b, float c, float d, float e, float f) {
-    uint4 *at = reinterpret_cast<uint4 *>(tile + r / 8 * 256 + r % 8 * 16);
-    at[0] = make_uint4(pack2<__nv_bfloat16>(a, b), pack2<__nv_bfloat16>(c, d), pack2<__nv_bfloat16>(e, f), 0u);
+    uint4 *at = reinterpret_cast<uint4 *>(tile + r / 8 * kBiasGroup + r % 8 * 16);
+    at[0] = make_uint4(pack2<__nv_bfloat16>(a, b), pack2<__nv_bfloat16>(c, 0.0f), 0u, 0u);
     at[8] = make_uint4(0u, 0u, 0u, 0u);
+    at[16] = make_uint4(pack2<__nv_bfloat16>(d, e), pack2<__nv_bfloat16>(f, 0.0f), 0u, 0u);
 }
 __device__ __forceinline__ float tc_bf16(float v) { return __bfloat162float(__float2bfloat16_rn(v)); }
 // Query r's row of the operand from its pair of stat. A query without keys (or past the
@@ -229,7 +233,7 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
     unsigned char *tile_a1 = base, *tile_a2 = base + K::ROW_BYTES, *tile_late = base + (BACK ? 2 : 1) * K::ROW_BYTES;
     unsigned char *tile_early = tile_late + STAGES * K::COL_BYTES;
     unsigned char *tile_stat = base + K::TILES, *tile_bias = tile_stat + STAGES * K::STAT_BYTES, *ones = tile_bias + STAGES * K::BIAS_BYTES;
-    uint64_t *bars = reinterpret_cast<uint64_t *>(ones + 2 * K::ONES_BYTES);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(ones + K::ONES_BYTES);
     uint64_t *a_full = bars, *full = bars + 1, *empty = full + STAGES, *full_early = empty + STAGES, *empty_early = full_early + EARLY;
     // scores, and dP (d_); weights ready and used: P's (kGradKV: p_), and the last ones of a tile
     uint64_t *s_full = empty_early + EARLY, *s_free = s_full + 1, *d_full = s_free + 1, *d_free = d_full + 1;
@@ -274,11 +278,7 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
     if (MODE == kGradKV && a.overlapped) attn_let_next();
     else attn_after();
     if (MODE == kGradKV) {
-        for (int i = threadIdx.x; i < 2 * kTcRows; i += K::THREADS) {
-            const bool for_s = i < kTcRows;
-            const float x = for_s ? 1.0f : 0.0f, y = for_s ? 0.0f : 1.0f;
-            tc_bias_row(ones + (for_s ? 0 : K::ONES_BYTES), i % kTcRows, x, x, x, y, y, y);
-        }
+        for (int i = threadIdx.x; i < kTcRows; i += K::THREADS) tc_bias_row(ones, i, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f);
         shared_to_async();
     }
     tmem_before_sync();
@@ -350,7 +350,7 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
             const uint32_t late = desc_low(shared_at(tile_late), 16), early = desc_low(shared_at(tile_early), 16);
             const uint32_t bias_at = desc_low(shared_at(tile_bias), 128), ones_at = desc_low(shared_at(ones), 128);
             constexpr uint32_t id = mma_desc<BF16, BN, false>(), high = desc_high<K::PITCH>();
-            constexpr uint32_t bias_id = mma_desc<true, BN, false>(), plain = desc_high_plain(256);
+            constexpr uint32_t bias_id = mma_desc<true, BN, false>(), plain = desc_high_plain(kBiasGroup);
             constexpr int per = K::PITCH / 32;      // steps of 16 channels in a panel
             // the products of a row tile and a column tile
             auto product = [&](uint32_t d, uint32_t rows, uint32_t columns) {
@@ -397,7 +397,7 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
                         tmem_after_sync();
                     }
                     product(tmem + BN, a2, x_early);
-                    if (MODE == kGradKV) mma_shared<bias_id, plain>(tmem + BN, ones_at + desc_step(K::ONES_BYTES), columns, true);
+                    if (MODE == kGradKV) mma_shared<bias_id, plain>(tmem + BN, ones_at + desc_step(kBiasForD), columns + desc_step(kBiasForD), true);
                     if (MODE == kGradQ) mma_commit(empty_early + se.at);
                     mma_commit(K::SPLIT ? d_full : s_full);
                 }
