@@ -60,8 +60,8 @@ struct AttnArgs {
     int stat_row;                      // queries in a row of stat: Q up to a multiple of 128, the
                                        // longest tile's
     float up;                          // fp16 backward: its probabilities are scaled by 2^up
-    // fp16 backward: partial maxima of |dO_i|^2 and |v_j|^2 (norms each, see
-    // attn_delta_kernel); NULL for other types
+    // fp16 backward: of each batch entry and key head, partial maxima of |dO_i|^2 and
+    // |v_j|^2 (norms each, see attn_delta_kernel); NULL for other types
     float *norm_do, *norm_v;
     int norms;
     AttnBits by_query, by_key;         // rows are queries (columns keys), and the other way

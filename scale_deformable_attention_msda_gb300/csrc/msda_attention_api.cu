@@ -82,6 +82,19 @@ ModePlan plan_mode(const msda_attention_dims_t &d, AttnMode mode, int R, int C, 
     return p;
 }
 
+// Blocks of the pass over the queries' rows. A block of 256 threads has 64 rows at once at
+// the least.
+int64_t delta_blocks(int64_t rows) {
+    const int64_t blocks = ceil_div(rows, 64);
+    return blocks < 1 ? 1 : blocks < kDeltaBlocks ? blocks : kDeltaBlocks;
+}
+// fp16: parts of a batch entry's and key head's rows, of queries and of keys, in that pass.
+int norm_parts(const msda_attention_dims_t &d) {
+    const int64_t queries = ceil_div(d.Q, 128) * 128 * (d.M / d.N), most = kDeltaBlocks / 2 / (d.B * d.N);
+    const int64_t parts = delta_blocks(queries > d.S ? queries : d.S);
+    return (int)(most < 1 ? 1 : parts < most ? parts : most);
+}
+
 int tile_rows(msda_dtype_t dt) { return dt == MSDA_F32 ? 64 : 128; }
 
 ModePlan plan_for(const msda_attention_dims_t &d, msda_dtype_t dt, AttnMode mode) {
@@ -131,7 +144,7 @@ Layout layout_of(const msda_attention_dims_t &d, msda_dtype_t dt, bool mask, boo
     }
     if (backward) {
         w.stat = take((size_t)d.B * d.M * ceil_div(d.Q, 128) * 128 * 8);
-        if (dt == MSDA_F16) w.norms = take(2 * kDeltaBlocks * 4);
+        if (dt == MSDA_F16 && d.B > 0) w.norms = take((size_t)2 * d.B * d.N * norm_parts(d) * 4);
         w.part[1] = take(plan_for(d, dt, msda::kGradQ).part);
         w.part[2] = take(plan_for(d, dt, msda::kGradKV).part);
     } else {
@@ -279,17 +292,16 @@ msda_status_t msda_attention_backward(const void *grad_out, const void *q, const
     a.stat = reinterpret_cast<float *>(ws + w.stat);
     a.stat_row = (int)(ceil_div(d.Q, 128) * 128);
     a.up = dtype == MSDA_F16 ? msda::kHalfUp : 0.0f;
-    // a block of 256 threads has 64 rows at once at the least
-    const int64_t rows = d.B * a.stat_row * d.M, keys = dtype == MSDA_F16 ? d.B * d.S * d.N : 0;
-    const int64_t delta_blocks = ceil_div(rows > keys ? rows : keys, 64);
-    a.norms = (int)(delta_blocks < 1 ? 1 : delta_blocks < kDeltaBlocks ? delta_blocks : kDeltaBlocks);
+    int64_t blocks = delta_blocks(d.B * a.stat_row * d.M);
     if (dtype == MSDA_F16) {
+        a.norms = norm_parts(d);
         a.norm_do = reinterpret_cast<float *>(ws + w.norms);
-        a.norm_v = a.norm_do + kDeltaBlocks;
+        a.norm_v = a.norm_do + d.B * d.N * a.norms;
+        blocks = 2 * d.B * d.N * a.norms < kDeltaBlocks ? 2 * d.B * d.N * a.norms : kDeltaBlocks;
     }
     cudaError_t e = masked ? pack_mask(a, d, w, mask, ws, true, s) : cudaSuccess;
     a.chained = masked;
-    if (e == cudaSuccess) e = msda::launch_attention_delta(a, dtype, s);
+    if (e == cudaSuccess) e = msda::launch_attention_delta(a, blocks, dtype, s);
     a.chained = true;
     if (e == cudaSuccess && for_q) e = launch_mode(a, d, dtype, msda::kGradQ, ws + w.part[1], s);
     a.overlapped = for_q;

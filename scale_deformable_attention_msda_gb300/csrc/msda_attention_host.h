@@ -52,7 +52,7 @@ struct AttnMaskSource {
 };
 cudaError_t launch_attention_pack(const AttnMaskSource &m, uint32_t *by_query, int words_q, uint32_t *by_key,
                                   int words_k, uint8_t *classes, int granules, cudaStream_t stream);
-cudaError_t launch_attention_delta(const AttnArgs &a, msda_dtype_t dt, cudaStream_t stream);
+cudaError_t launch_attention_delta(const AttnArgs &a, int64_t blocks, msda_dtype_t dt, cudaStream_t stream);
 cudaError_t launch_attention_join(int mode, const AttnArgs &a, msda_dtype_t dt, cudaStream_t stream);
 
 }  // namespace msda

@@ -1,5 +1,7 @@
 // Attention's small kernels: the mask packed to bits, the backward's row sums
 // dO out, and the join of split columns.
+#include <type_traits>
+
 #include "msda_attention_host.h"
 
 namespace msda {
@@ -73,106 +75,167 @@ __global__ void __launch_bounds__(256) attn_pack_kernel(const AttnMaskSource m, 
 
 constexpr int kDeltaThreads = 256;
 
-// The queries' stat: the row sums delta = sum over channels of dO out, L lanes a row
-// of 16 bytes each, beside the forward's lse. fp16 (norm_do given): also the largest
-// finite |dO_i|^2 and |v_j|^2 of what this block has seen.
+// Which of the 32 keys from key0 on, a multiple of 32, some query of a key head attends: the
+// class of the granule that they lie in, of 64 queries at a time, and where it is mixed each
+// lane its key's bits. For a whole warp.
+__device__ __forceinline__ uint32_t attn_attended(const AttnArgs &a, int b, int n, int key0) {
+    const int key = key0 + (threadIdx.x & 31);
+    uint32_t some = __ballot_sync(0xffffffffu, key < a.S);
+    if (!a.classes) return some;
+    const uint32_t there = some;
+    some = 0u;
+    for (int h = n * a.G; h < n * a.G + (a.class_head ? a.G : 1); ++h) {
+        const uint8_t *c = a.classes + b * a.class_batch + h * a.class_head + key0 / kAttnGranule;
+        const uint32_t *words = key < a.S ? attn_word_row<kGradKV>(a, b, h, key) : nullptr;
+        for (int q = 0; q < (a.class_row ? a.Q : 1); q += kAttnGranule, c += a.class_row) {
+            const int cls = *c;
+            if (cls == 2) return there;
+            if (cls == 0) continue;
+            const bool any = words && (attn_word<kGradKV>(a, words, q) | attn_word<kGradKV>(a, words, q + 32));
+            some |= __ballot_sync(0xffffffffu, any);
+            if (some == there) return there;
+        }
+    }
+    return some;
+}
+
+// The largest of a block's values.
+__device__ __forceinline__ float attn_block_most(float most) {
+    __shared__ float part[kDeltaThreads / 32];
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, off));
+    __syncthreads();                   // the last call's are read
+    if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = most;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kDeltaThreads / 32; ++i) most = fmaxf(most, part[i]);
+    return most;
+}
+
+// fp16: the largest finite |v_j|^2 of the keys of part p of a batch entry's and key head's,
+// of those that a query attends: what lies in masked places has no part in it.
 template <typename T, int L>
+__device__ __forceinline__ void attn_key_norms(const AttnArgs &a, int64_t slice, int p) {
+    constexpr int V = 16 / sizeof(T), AT_ONCE = 4;
+    const int d = threadIdx.x % L * V, b = (int)(slice / a.N), n = (int)(slice - (int64_t)b * a.N);
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, groups = (a.S + 31) / 32;     // of 32 keys, one a warp
+    const int begin = (int)((int64_t)groups * p / a.norms), end = (int)((int64_t)groups * (p + 1) / a.norms);
+    float most = 0.0f;
+    for (int t = begin + warp; t < end; t += kDeltaThreads / 32) {
+        uint32_t some = 0u;
+#pragma unroll
+        for (int i0 = 0; i0 < L; i0 += AT_ONCE) {
+            uint4 x[AT_ONCE];
+#pragma unroll
+            for (int i = 0; i < AT_ONCE; ++i) {
+                const int key = 32 * t + (i0 + i) * (32 / L) + lane / L;
+                x[i] = key < a.S && d < a.D ? ldg16(attn_at<T>(a, a.v, b, key, n) + d) : make_uint4(0u, 0u, 0u, 0u);
+            }
+            if (i0 == 0) some = attn_attended(a, b, n, 32 * t);
+#pragma unroll
+            for (int i = 0; i < AT_ONCE; ++i) {
+                float fx[V], square = 0.0f;
+                unpack16<T>(fx, x[i]);
+#pragma unroll
+                for (int k = 0; k < V; ++k) square = fmaf(fx[k], fx[k], square);
+#pragma unroll
+                for (int off = L / 2; off > 0; off >>= 1) square += __shfl_xor_sync(0xffffffffu, square, off);
+                const bool on = (some >> ((i0 + i) * (32 / L) + lane / L)) & 1u;
+                if (on && isfinite(square)) most = fmaxf(most, square);
+            }
+        }
+    }
+    most = attn_block_most(most);
+    if (threadIdx.x == 0) a.norm_v[slice * a.norms + p] = most;
+}
+
+// The queries' stat: the row sums delta = sum over channels of dO out, L lanes a row
+// of 16 bytes each, beside the forward's lse. NORMS (fp16): rows by batch entry and key
+// head, in a.norms parts each, and of each part the largest finite |dO_i|^2 of queries that
+// attend a key; and the keys' norms, by other blocks.
+template <typename T, int L, bool NORMS>
 __global__ void __launch_bounds__(kDeltaThreads) attn_delta_kernel(const AttnArgs a) {
     constexpr int V = 16 / sizeof(T), per = kDeltaThreads / L, AT_ONCE = 4;
     attn_after();
-    const int lane = threadIdx.x % L, d = lane * V;
-    const int64_t rows = (int64_t)a.B * a.stat_row * a.M, step = (int64_t)gridDim.x * per;
-    float most_do = 0.0f, most_v = 0.0f;
-    for (int64_t r0 = (int64_t)blockIdx.x * per + threadIdx.x / L; r0 - threadIdx.x / L < rows; r0 += AT_ONCE * step) {
-        uint4 x[AT_ONCE], y[AT_ONCE], z[AT_ONCE];
-        float *to[AT_ONCE];
-        float lse[AT_ONCE];
+    const int lane = threadIdx.x % L, d = lane * V, heads = NORMS ? a.G : a.M;
+    const int64_t step = NORMS ? per : (int64_t)gridDim.x * per;
+    const int64_t parts = NORMS ? (int64_t)a.B * a.N * a.norms : gridDim.x;
+    for (int64_t t = blockIdx.x; t < (NORMS ? 2 * parts : parts); t += gridDim.x) {
+        const int64_t slice = NORMS ? t % parts / a.norms : 0;         // b N + n
+        const int p = NORMS ? (int)(t % parts - slice * a.norms) : 0;
+        if (NORMS && t >= parts) {
+            attn_key_norms<T, L>(a, slice, p);
+            continue;
+        }
+        const int64_t all = NORMS ? (int64_t)a.stat_row * a.G : (int64_t)a.B * a.stat_row * a.M;
+        const int64_t begin = NORMS ? all * p / a.norms : (int64_t)blockIdx.x * per, rows = NORMS ? all * (p + 1) / a.norms : all;
+        float most_do = 0.0f;
+        for (int64_t r0 = begin + threadIdx.x / L; r0 - threadIdx.x / L < rows; r0 += AT_ONCE * step) {
+            uint4 x[AT_ONCE], y[AT_ONCE], z[AT_ONCE];
+            float *to[AT_ONCE];
+            float lse[AT_ONCE];
 #pragma unroll
-        for (int i = 0; i < AT_ONCE; ++i) {
-            const int64_t r = r0 + i * step, bq = r / a.M;
-            const int m = (int)(r - bq * a.M), b = (int)(bq / a.stat_row), q = (int)(bq - (int64_t)b * a.stat_row);
-            to[i] = r < rows ? attn_stat(a, b, m, q) : nullptr;
-            x[i] = y[i] = z[i] = make_uint4(0u, 0u, 0u, 0u);
-            lse[i] = -INFINITY;
-            if (r < rows && q < a.Q) {
-                if (lane == 0) lse[i] = a.lse[((int64_t)b * a.M + m) * a.Q + q];
-                if (d < a.D) {         // these three lie alike
-                    const T *go = attn_at<T>(a, a.go, b, q, m) + d;
-                    const int64_t at = go - static_cast<const T *>(a.go.p);
-                    x[i] = ldg16(go);
-                    y[i] = ldg16(static_cast<const T *>(a.o.p) + at);
-                    if (a.rest) z[i] = ldg16(static_cast<const T *>(a.rest) + at);
+            for (int i = 0; i < AT_ONCE; ++i) {
+                const int64_t r = r0 + i * step, bq = r / heads;
+                int m = (int)(r - bq * heads), b, q;
+                if (NORMS) {
+                    b = (int)(slice / a.N);
+                    q = (int)bq;
+                    m += (int)(slice - (int64_t)b * a.N) * a.G;
+                } else {
+                    b = (int)(bq / a.stat_row);
+                    q = (int)(bq - (int64_t)b * a.stat_row);
+                }
+                to[i] = r < rows ? attn_stat(a, b, m, q) : nullptr;
+                x[i] = y[i] = z[i] = make_uint4(0u, 0u, 0u, 0u);
+                lse[i] = -INFINITY;
+                if (r < rows && q < a.Q) {
+                    if (NORMS || lane == 0) lse[i] = a.lse[((int64_t)b * a.M + m) * a.Q + q];
+                    if (d < a.D) {     // these three lie alike
+                        const T *go = attn_at<T>(a, a.go, b, q, m) + d;
+                        const int64_t at = go - static_cast<const T *>(a.go.p);
+                        x[i] = ldg16(go);
+                        y[i] = ldg16(static_cast<const T *>(a.o.p) + at);
+                        if (a.rest) z[i] = ldg16(static_cast<const T *>(a.rest) + at);
+                    }
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < AT_ONCE; ++i) {
+                float fx[V], fy[V], fz[V], dot = 0.0f, square = 0.0f;
+                unpack16<T>(fx, x[i]);
+                unpack16<T>(fy, y[i]);
+                unpack16<T>(fz, z[i]);
+#pragma unroll
+                for (int k = 0; k < V; ++k) {
+                    dot = fmaf(fx[k], fy[k] + fz[k], dot);
+                    if (NORMS) square = fmaf(fx[k], fx[k], square);
+                }
+#pragma unroll
+                for (int off = L / 2; off > 0; off >>= 1) {
+                    dot += __shfl_xor_sync(0xffffffffu, dot, off);
+                    if (NORMS) square += __shfl_xor_sync(0xffffffffu, square, off);
+                }
+                if (NORMS && isfinite(square) && lse[i] != -INFINITY) most_do = fmaxf(most_do, square);
+                if (to[i] && lane == 0) {      // past the last query: -infinity and 0
+                    to[i][0] = a.up - attn_lse2(lse[i]);
+                    to[i][2] = -dot;
                 }
             }
         }
-#pragma unroll
-        for (int i = 0; i < AT_ONCE; ++i) {
-            float fx[V], fy[V], fz[V], dot = 0.0f, square = 0.0f;
-            unpack16<T>(fx, x[i]);
-            unpack16<T>(fy, y[i]);
-            unpack16<T>(fz, z[i]);
-#pragma unroll
-            for (int k = 0; k < V; ++k) {
-                dot = fmaf(fx[k], fy[k] + fz[k], dot);
-                square = fmaf(fx[k], fx[k], square);
-            }
-#pragma unroll
-            for (int off = L / 2; off > 0; off >>= 1) {
-                dot += __shfl_xor_sync(0xffffffffu, dot, off);
-                square += __shfl_xor_sync(0xffffffffu, square, off);
-            }
-            if (isfinite(square)) most_do = fmaxf(most_do, square);
-            if (to[i] && lane == 0) {  // past the last query: -infinity and 0
-                to[i][0] = a.up - attn_lse2(lse[i]);
-                to[i][2] = -dot;
-            }
-        }
-    }
-    if (!a.norm_do) return;
-    const int64_t keys = (int64_t)a.B * a.S * a.N;
-    for (int64_t r0 = (int64_t)blockIdx.x * per + threadIdx.x / L; r0 - threadIdx.x / L < keys; r0 += AT_ONCE * step) {
-        uint4 x[AT_ONCE];
-#pragma unroll
-        for (int i = 0; i < AT_ONCE; ++i) {
-            const int64_t r = r0 + i * step, bs = r / a.N;
-            const int b = (int)(bs / a.S);
-            x[i] = r < keys && d < a.D ? ldg16(attn_at<T>(a, a.v, b, (int)(bs - (int64_t)b * a.S), (int)(r - bs * a.N)) + d) : make_uint4(0u, 0u, 0u, 0u);
-        }
-#pragma unroll
-        for (int i = 0; i < AT_ONCE; ++i) {
-            float fx[V], square = 0.0f;
-            unpack16<T>(fx, x[i]);
-#pragma unroll
-            for (int k = 0; k < V; ++k) square = fmaf(fx[k], fx[k], square);
-#pragma unroll
-            for (int off = L / 2; off > 0; off >>= 1) square += __shfl_xor_sync(0xffffffffu, square, off);
-            if (isfinite(square)) most_v = fmaxf(most_v, square);
-        }
-    }
-    __shared__ float part[2][kDeltaThreads / 32];
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-        most_do = fmaxf(most_do, __shfl_xor_sync(0xffffffffu, most_do, off));
-        most_v = fmaxf(most_v, __shfl_xor_sync(0xffffffffu, most_v, off));
-    }
-    if (threadIdx.x % 32 == 0) {
-        part[0][threadIdx.x / 32] = most_do;
-        part[1][threadIdx.x / 32] = most_v;
-    }
-    __syncthreads();
-    if (threadIdx.x < 2) {
-        float most = 0.0f;
-        for (int i = 0; i < kDeltaThreads / 32; ++i) most = fmaxf(most, part[threadIdx.x][i]);
-        (threadIdx.x ? a.norm_v : a.norm_do)[blockIdx.x] = most;
+        if (!NORMS) return;
+        most_do = attn_block_most(most_do);
+        if (threadIdx.x == 0) a.norm_do[t] = most_do;
     }
 }
 
-template <typename T> cudaError_t launch_delta(const AttnArgs &a, cudaStream_t stream) {
+template <typename T> cudaError_t launch_delta(const AttnArgs &a, int64_t blocks, cudaStream_t stream) {
+    constexpr bool NORMS = std::is_same<T, __half>::value;
     const int lanes = a.D * (int)sizeof(T) / 16;
-    if (lanes <= 4) return launch_after(a.chained, attn_delta_kernel<T, 4>, a.norms, kDeltaThreads, 0, stream, a);
-    if (lanes <= 8) return launch_after(a.chained, attn_delta_kernel<T, 8>, a.norms, kDeltaThreads, 0, stream, a);
-    if (lanes <= 16) return launch_after(a.chained, attn_delta_kernel<T, 16>, a.norms, kDeltaThreads, 0, stream, a);
-    return launch_after(a.chained, attn_delta_kernel<T, 32>, a.norms, kDeltaThreads, 0, stream, a);
+    if (lanes <= 4) return launch_after(a.chained, attn_delta_kernel<T, 4, NORMS>, blocks, kDeltaThreads, 0, stream, a);
+    if (lanes <= 8) return launch_after(a.chained, attn_delta_kernel<T, 8, NORMS>, blocks, kDeltaThreads, 0, stream, a);
+    if (lanes <= 16) return launch_after(a.chained, attn_delta_kernel<T, 16, NORMS>, blocks, kDeltaThreads, 0, stream, a);
+    return launch_after(a.chained, attn_delta_kernel<T, 32, NORMS>, blocks, kDeltaThreads, 0, stream, a);
 }
 
 // Sums of the splits: a warp a row, four channels a lane, and where that leaves lanes the
@@ -256,9 +319,9 @@ cudaError_t launch_attention_pack(const AttnMaskSource &m, uint32_t *by_query, i
     return launch_after(false, attn_pack_kernel, blocks, 256, 0, stream, m, by_query, words_q, by_key, words_k, classes, granules);
 }
 
-cudaError_t launch_attention_delta(const AttnArgs &a, msda_dtype_t dt, cudaStream_t stream) {
-    return dt == MSDA_F32 ? launch_delta<float>(a, stream)
-         : dt == MSDA_BF16 ? launch_delta<__nv_bfloat16>(a, stream) : launch_delta<__half>(a, stream);
+cudaError_t launch_attention_delta(const AttnArgs &a, int64_t blocks, msda_dtype_t dt, cudaStream_t stream) {
+    return dt == MSDA_F32 ? launch_delta<float>(a, blocks, stream)
+         : dt == MSDA_BF16 ? launch_delta<__nv_bfloat16>(a, blocks, stream) : launch_delta<__half>(a, blocks, stream);
 }
 
 cudaError_t launch_attention_join(int mode, const AttnArgs &a, msda_dtype_t dt, cudaStream_t stream) {

@@ -123,7 +123,10 @@ template <> __device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi
 }
 
 // ds is at most 2 |dO_i| |v_j| p: for fp16 it is scaled by the power of two r that takes
-// the largest of these bounds to 2 at most, and so, with p's 2^14, below 2^15 + 2^-10.
+// the largest of these bounds to 2 at most, and so, with p's 2^14, below 2^15 + 2^-10. The
+// largest v_j is that of the batch entry's and key head's keys that some query attends. The
+// sums of a query's gradient have its dO_i in common; those of the keys' take the largest of
+// the head's queries that attend a key.
 template <typename T> struct TcScale { static constexpr float forward = 0.0f, backward = 0.0f; };
 template <> struct TcScale<__half> { static constexpr float forward = kHalfWeightUp, backward = kHalfUp; };
 
@@ -134,12 +137,25 @@ __device__ __forceinline__ float tc_most(const float *part, int n) {
     for (int off = 16; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
     return v;
 }
-__device__ __forceinline__ float tc_ds_scale(const AttnArgs &a) {
-    const float bound = 2.01f * sqrtf(tc_most(a.norm_do, a.norms)) * sqrtf(tc_most(a.norm_v, a.norms));
-    if (bound == 0.0f) return 1.0f;
+// square: |dO|^2 of the query, kGradQ.
+template <int MODE> __device__ __forceinline__ float tc_ds_scale(const AttnArgs &a, const AttnRows &w, float square) {
+    const int64_t at = ((int64_t)w.b * a.N + (MODE == kGradKV ? w.head : w.head / a.G)) * a.norms;
+    if (MODE == kGradKV) square = tc_most(a.norm_do + at, a.norms);
+    const float bound = 2.01f * sqrtf(square) * sqrtf(tc_most(a.norm_v + at, a.norms));
+    if (bound == 0.0f || !isfinite(bound)) return 1.0f;
     int e;
     frexpf(bound, &e);                 // bound < 2^e
     return ldexpf(1.0f, min(1 - e, 100));
+}
+template <typename T> __device__ __forceinline__ float tc_square(const T *row, int D) {
+    float square = 0.0f;
+    for (int d = 0; d < D; d += 8) {
+        float x[8];
+        unpack16<T>(x, ldg16(row + d));
+#pragma unroll
+        for (int k = 0; k < 8; ++k) square = fmaf(x[k], x[k], square);
+    }
+    return square;
 }
 
 // 32 channels of a row: of the output, or of this split's part (scaled by g), and of
@@ -478,7 +494,7 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
         const int rpos = w.row_pos(valid ? r : 0), rhead = w.row_head(valid ? r : 0);
         const float c = a.c;
         float ds_scale = 1.0f;
-        if (BACK && a.norm_do) ds_scale = tc_ds_scale(a);
+        if (BACK && !BF16) ds_scale = tc_ds_scale<MODE>(a, w, MODE == kGradQ && valid ? tc_square(attn_at<T>(a, a.go, w.b, rpos, rhead), a.D) : 0.0f);
         constexpr float up = TcScale<T>::forward;
         float top = -INFINITY, sum = 0.0f, lse2 = 0.0f, delta = 0.0f;    // backward: negative, as in stat
         if (MODE == kGradQ && valid) {
