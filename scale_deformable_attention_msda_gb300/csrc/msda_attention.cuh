@@ -210,15 +210,91 @@ __device__ __forceinline__ float *attn_stat(const AttnArgs &a, int b, int head, 
     return a.stat + ((int64_t)b * a.M + head) * a.stat_row * 2 + (pos >> 1) * 4 + (pos & 1);
 }
 
-// What lies in a masked place may be anything. Its score and its weight are
-// replaced, but a product of the weight 0 with NaN or infinity is NaN, so a row
-// whose sums are not finite is computed again from its allowed pairs alone: by
-// one warp, column by column, slowly, and only then. The caller's sums have the
-// row's reference maximum `m2` (forward, in the exponent's units). acc1 and acc2:
-// channels lane, lane + 32, ... of p x2 and ds x1.
+// What lies in a masked place may be anything. Its score and its weight are replaced, but
+// a product of the weight 0 with NaN or infinity is NaN. So a row whose sums are not finite
+// is computed again from its allowed pairs alone (attn_exact_row), if a masked pair may be
+// the cause and the allowed ones would not make all of it NaN anyway (attn_spoiled). Where
+// only allowed places hold what is not finite, as in a step whose gradients overflowed, that
+// search is all that such a row costs.
+
+// A number that is finite and whose products with another such, summed over the channels, are.
+constexpr float kAttnTame = 0x1p60f;
+template <typename T> __device__ __forceinline__ void attn_survey(const T *row, int D, bool &tame, bool &finite) {
+    constexpr int V = 16 / sizeof(T);
+    float most = 0.0f;
+    bool number = true;
+    for (int d = 0; d < D; d += V) {
+        float x[V];
+        unpack16<T>(x, ldg16(row + d));
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            most = fmaxf(most, fabsf(x[k]));
+            number = number && x[k] == x[k];
+        }
+    }
+    tame = number && most < kAttnTame;
+    finite = number && most < INFINITY;
+}
+
+// For a whole warp, each lane a row r of its own (below zero: none): whether it has to be
+// computed again. The lanes look at 32 columns at a time, one each, and tell one another.
+// lost: the allowed pairs make all of the row NaN.
+template <typename T, int MODE, int C>
+__device__ __noinline__ bool attn_spoiled(const AttnArgs &a, const AttnRows &w, int r, int64_t j0, int64_t j1, bool lost) {
+    const int lane = threadIdx.x & 31;
+    const int pos = w.row_pos(r < 0 ? 0 : r), head = w.row_head(r < 0 ? 0 : r);
+    bool tame = true, finite = true;   // what of the row goes into its pairs' dP
+    if (MODE != kForward && r >= 0) {
+        attn_survey<T>(MODE == kGradQ ? attn_at<T>(a, a.go, w.b, pos, head) : attn_at<T>(a, a.v, w.b, pos, head), a.D, tame, finite);
+        if (MODE == kGradQ) {
+            const float *st = attn_stat(a, w.b, head, pos);
+            finite = finite && st[0] < INFINITY && isfinite(st[2]);            // st[0] is -infinity without keys
+            tame = tame && finite;
+        }
+    }
+    bool allowed = false, masked = false, cause = false;
+    lost = lost || r < 0;
+    for (int64_t j = j0; j < j1; ++j) {
+        int cpos, chead;
+        attn_columns<MODE, C>(a, w, j, &cpos, &chead);
+        if (!attn_class<MODE, C>(a, w, cpos, chead)) continue;
+        const uint32_t *words = attn_word_row<MODE>(a, w.b, MODE == kGradKV ? chead : head, pos);
+        for (int c0 = 0; c0 < C; c0 += 32) {
+            const int at = cpos + c0 + lane, len = MODE == kGradKV ? a.Q : a.S;
+            if (cpos + c0 >= len) break;
+            bool mild = true, number = true, unused;
+            if (at < len) {
+                attn_survey<T>(MODE == kGradKV ? attn_at<T>(a, a.go, w.b, at, chead) : attn_at<T>(a, a.v, w.b, at, chead), a.D, mild, unused);
+                if (MODE != kForward) {
+                    bool other;
+                    attn_survey<T>(MODE == kGradKV ? attn_at<T>(a, a.q, w.b, at, chead) : attn_at<T>(a, a.k, w.b, at, chead), a.D, other, unused);
+                    mild = mild && other;
+                }
+                if (MODE == kGradKV) {
+                    const float *st = attn_stat(a, w.b, chead, at);
+                    number = st[0] == st[0];
+                    mild = mild && isfinite(st[2]);
+                }
+            }
+            const uint32_t there = __ballot_sync(0xffffffffu, at < len), wild = __ballot_sync(0xffffffffu, !mild), nan = __ballot_sync(0xffffffffu, !number);
+            const uint32_t on = attn_word<MODE>(a, words, cpos + c0) & there, off = ~on & there;
+            allowed = allowed || on;
+            masked = masked || off;
+            cause = cause || (off & wild);
+            lost = lost || (on & nan) || (MODE == kGradQ && !finite && on);
+        }
+        if (__all_sync(0xffffffffu, lost)) return false;
+    }
+    return !lost && (cause || (finite ? !tame && masked : !allowed));
+}
+
+// Row r from its allowed pairs alone: by one warp, column by column, slowly. The caller's
+// sums have the row's reference maximum `m2` (forward, in the exponent's units). acc1 and
+// acc2: channels lane, lane + 32, ... of p x2 and ds x1.
 template <typename T, int MODE, int C>
 __device__ __noinline__ void attn_exact_row(const AttnArgs &a, const AttnRows &w, int r, int64_t j0, int64_t j1,
                                             float m2, float (&acc1)[4], float (&acc2)[4]) {
+    constexpr int V = 16 / sizeof(T);
     const int lane = threadIdx.x & 31;
     const int pos = w.row_pos(r), head = w.row_head(r);
     const T *a1 = MODE == kGradKV ? attn_at<T>(a, a.k, w.b, pos, head) : attn_at<T>(a, a.q, w.b, pos, head);
@@ -247,9 +323,17 @@ __device__ __noinline__ void attn_exact_row(const AttnArgs &a, const AttnRows &w
                 x1 = MODE == kGradKV ? attn_at<T>(a, a.q, w.b, at, chead) : attn_at<T>(a, a.k, w.b, at, chead);
                 x2 = MODE == kGradKV ? attn_at<T>(a, a.go, w.b, at, chead) : attn_at<T>(a, a.v, w.b, at, chead);
                 float s = 0.0f, dp = 0.0f;
-                for (int d = 0; d < a.D; ++d) {
-                    s = fmaf(Elem<T>::to_f(a1[d]), Elem<T>::to_f(x1[d]), s);
-                    if (MODE != kForward) dp = fmaf(Elem<T>::to_f(a2[d]), Elem<T>::to_f(x2[d]), dp);
+                for (int d = 0; d < a.D; d += V) {
+                    float y[V], z[V];
+                    unpack16<T>(y, ldg16(a1 + d));
+                    unpack16<T>(z, ldg16(x1 + d));
+#pragma unroll
+                    for (int k = 0; k < V; ++k) s = fmaf(y[k], z[k], s);
+                    if (MODE == kForward) continue;
+                    unpack16<T>(y, ldg16(a2 + d));
+                    unpack16<T>(z, ldg16(x2 + d));
+#pragma unroll
+                    for (int k = 0; k < V; ++k) dp = fmaf(y[k], z[k], dp);
                 }
                 if (MODE == kGradKV) {
                     const float *st = attn_stat(a, w.b, chead, at);

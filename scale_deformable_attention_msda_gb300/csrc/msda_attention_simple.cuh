@@ -261,7 +261,6 @@ __global__ void __launch_bounds__(kSimpleThreads, simple_blocks(DP)) attn_simple
                 sh.stat[0][r] = m2;
                 sh.stat[1][r] = sum[i];
             }
-            continue;
         }
         const float f = MODE == kForward ? (sum[i] == 0.0f ? 0.0f : 1.0f / sum[i]) : a.scale;
         if (tx * E >= a.D) continue;
@@ -269,8 +268,14 @@ __global__ void __launch_bounds__(kSimpleThreads, simple_blocks(DP)) attn_simple
         if (MODE != kForward) simple_store<MODE, E>(a, w, r, split, MODE == kGradKV, tx * E, acc2[i], f);
     }
     __syncthreads();
-    for (int r = threadIdx.x / 32; r < R; r += kSimpleThreads / 32) {
-        if (!sh.bad[r]) continue;
+    // a warp has every eighth row
+    constexpr int WARPS = kSimpleThreads / 32;
+    const int mine = threadIdx.x / 32 + WARPS * lane;
+    const bool bad = lane < R / WARPS && sh.bad[mine];
+    uint32_t again = __ballot_sync(0xffffffffu, bad);
+    if (again) again = __ballot_sync(0xffffffffu, attn_spoiled<float, MODE, C>(a, w, bad ? mine : -1, j0, j1, MODE == kForward && bad && !isfinite(sh.stat[1][mine])));
+    for (; again; again &= again - 1) {
+        const int r = threadIdx.x / 32 + WARPS * (__ffs(again) - 1);
         float e1[4], e2[4];
         attn_exact_row<float, MODE, C>(a, w, r, j0, j1, MODE == kForward ? sh.stat[0][r] : 0.0f, e1, e2);
         const float f = MODE != kForward ? a.scale : sh.stat[1][r] == 0.0f ? 0.0f : 1.0f / sh.stat[1][r];

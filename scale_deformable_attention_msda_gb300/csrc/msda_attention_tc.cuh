@@ -672,6 +672,7 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
                 }
             }
             const float over = sum == 0.0f ? 0.0f : 1.0f / sum;
+            uint32_t open = 0u;        // of this group's chunks, those that are not finite
             // 32 channels of a result at a time, shared among the groups
 #pragma unroll 1
             for (int q = part; q < K::RESULTS * (DP / 32); q += K::PARTS) {
@@ -683,24 +684,29 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
                 if (count > 0) tmem_read<32>(o, at_acc + 32 * q);
 #pragma unroll
                 for (int k = 0; k < 32; ++k) v[k] = count > 0 ? __uint_as_float(o[k]) : 0.0f;
-                bool finite = true;
                 if (a.classes) {
+                    bool finite = true;
 #pragma unroll
                     for (int k = 0; k < 32; ++k) finite = finite && isfinite(v[k]);
+                    if (valid && !finite) open |= 1u << q;
                 }
-                if (valid && finite) tc_store<T, MODE>(a, row, split, which, d0, v, f, g);
-                uint32_t bad = __ballot_sync(0xffffffffu, valid && !finite);
-                while (bad) {
+                if (valid) tc_store<T, MODE>(a, row, split, which, d0, v, f, g);
+            }
+            if (__any_sync(0xffffffffu, open)) {
+                const bool again = attn_spoiled<T, MODE, BN>(a, w, open ? r : -1, j0, j1, MODE == kForward && !isfinite(sum));
+                for (uint32_t bad = __ballot_sync(0xffffffffu, again); bad; bad &= bad - 1) {
                     const int from = __ffs(bad) - 1;
-                    bad &= bad - 1;
                     float e1[4], e2[4];
                     const float m2 = __shfl_sync(0xffffffffu, ref, from), over_from = __shfl_sync(0xffffffffu, over, from);
+                    const uint32_t chunks = __shfl_sync(0xffffffffu, open, from);
                     attn_exact_row<T, MODE, BN>(a, w, (r & ~31) + from, j0, j1, m2, e1, e2);
-                    const bool of_ds = MODE == kGradQ || which;
+                    __syncwarp();      // in place of what its lane has stored
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        if (32 * i != d0 || d0 + lane >= a.D) continue;
-                        attn_store<T, MODE>(a, w, (r & ~31) + from, split, which, d0 + lane, of_ds ? e2[i] : e1[i],
+                    for (int i = 0; i < K::RESULTS * (DP / 32); ++i) {
+                        const int which = i / (DP / 32), c = i % (DP / 32), at = 32 * c + lane;
+                        if (!((chunks >> i) & 1u) || at >= a.D) continue;
+                        const bool of_ds = MODE == kGradQ || which;
+                        attn_store<T, MODE>(a, w, (r & ~31) + from, split, which, at, of_ds ? e2[c] : e1[c],
                                             MODE == kForward ? over_from : of_ds ? a.scale : 1.0f);
                     }
                 }
