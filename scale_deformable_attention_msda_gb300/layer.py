@@ -23,6 +23,7 @@ MultiHeadAttention is that sublayer, in the same form.
 """
 from __future__ import annotations
 
+import copy
 import math
 
 import torch
@@ -60,15 +61,33 @@ class Dropout(nn.Module):
     from torch's, and the number of the next draw, and is advanced on the device at each call
     in training: a captured step draws anew each time it is replayed, and so does a forward
     that is run again for its backward (activation checkpointing), whose gradients would then be
-    of another draw: there use binding.dropout with one counter."""
+    of another draw: there use binding.dropout with one counter. A copy of the module
+    (copy.deepcopy, of which a decoder's layers are made) has a seed of its own; one that is
+    pickled or loaded continues where the stored one was."""
 
     def __init__(self, p: float = 0.1):
         super().__init__()
         if not 0.0 <= p <= 1.0:
             raise ValueError("a dropout probability lies between 0 and 1")
         self.p = p
+        self.register_buffer("state", self._new_state())
+
+    @staticmethod
+    def _new_state():
         seed = torch.randint(-2 ** 63, 2 ** 63 - 1, (), dtype=torch.int64)
-        self.register_buffer("state", torch.stack([seed, torch.zeros_like(seed)]))
+        return torch.stack([seed, torch.zeros_like(seed)])
+
+    @torch.no_grad()
+    def reseed(self):
+        """Start a generator of another seed, drawn from torch's."""
+        self.state.copy_(self._new_state())
+
+    def __deepcopy__(self, memo):
+        copied = self.__class__.__new__(self.__class__)
+        memo[id(self)] = copied
+        copied.__setstate__(copy.deepcopy(self.__dict__, memo))
+        copied.reseed()
+        return copied
 
     def extra_repr(self):
         return f"p={self.p}"
