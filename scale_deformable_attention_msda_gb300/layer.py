@@ -57,20 +57,25 @@ class LayerNorm(nn.Module):
 
 class Dropout(nn.Module):
     """Dropout of libmsda's counter-based generator (binding.dropout), in training; of x, or
-    of x on its way into residual + x. `state`, a buffer, holds the generator's seed, drawn
+    of x on its way into residual + x. `state` holds the generator's seed, drawn
     from torch's, and the number of the next draw, and is advanced on the device at each call
     in training: a captured step draws anew each time it is replayed, and so does a forward
     that is run again for its backward (activation checkpointing), whose gradients would then be
     of another draw: there use binding.dropout with one counter. A copy of the module
     (copy.deepcopy, of which a decoder's layers are made) has a seed of its own; one that is
-    pickled or loaded continues where the stored one was."""
+    pickled or loaded continues where the stored one was.
+
+    `state` is stored and moved with the module but is not among its buffers, which
+    DistributedDataParallel makes those of rank 0: ranks draw from seeds of their own, if
+    torch's generators were seeded differently on them. Where they were not, or where all
+    ranks loaded one state, call reseed with a seed of the rank's."""
 
     def __init__(self, p: float = 0.1):
         super().__init__()
         if not 0.0 <= p <= 1.0:
             raise ValueError("a dropout probability lies between 0 and 1")
         self.p = p
-        self.register_buffer("state", self._new_state())
+        self.state = self._new_state()
 
     @staticmethod
     def _new_state():
@@ -78,9 +83,43 @@ class Dropout(nn.Module):
         return torch.stack([seed, torch.zeros_like(seed)])
 
     @torch.no_grad()
-    def reseed(self):
-        """Start a generator of another seed, drawn from torch's."""
-        self.state.copy_(self._new_state())
+    def reseed(self, seed=None):
+        """Start a generator of `seed`, 64 bits, drawn from torch's unless given."""
+        if seed is None:
+            self.state.copy_(self._new_state())
+        else:
+            self.state.copy_(torch.tensor([(int(seed) + 2 ** 63) % 2 ** 64 - 2 ** 63, 0]))
+
+    def _apply(self, fn, recurse=True):
+        super()._apply(fn, recurse)
+        self.state = fn(self.state)
+        return self
+
+    def _save_to_state_dict(self, destination, prefix, keep_vars):
+        super()._save_to_state_dict(destination, prefix, keep_vars)
+        destination[prefix + "state"] = self.state
+
+    def _load_from_state_dict(self, state_dict, prefix, local_metadata, strict, missing_keys,
+                              unexpected_keys, error_msgs):
+        key = prefix + "state"
+        super()._load_from_state_dict({k: v for k, v in state_dict.items() if k != key}, prefix, local_metadata,
+                                      strict, missing_keys, unexpected_keys, error_msgs)
+        given = state_dict.get(key)
+        if given is None:
+            if strict:
+                missing_keys.append(key)
+        elif given.shape != (2,) or given.dtype != torch.int64:
+            error_msgs.append(f"{key} is {given.dtype} of shape {tuple(given.shape)}: two int64 are expected")
+        elif local_metadata.get("assign_to_params_buffers", False):
+            self.state = given
+        else:
+            with torch.no_grad():
+                self.state.copy_(given)
+
+    def __setstate__(self, state):
+        super().__setstate__(state)
+        if "state" in self._buffers:             # modules pickled while it was one
+            self.state = self._buffers.pop("state")
 
     def __deepcopy__(self, memo):
         copied = self.__class__.__new__(self.__class__)
