@@ -59,9 +59,10 @@ class Dropout(nn.Module):
     """Dropout of libmsda's counter-based generator (binding.dropout), in training; of x, or
     of x on its way into residual + x. `state` holds the generator's seed, drawn
     from torch's, and the number of the next draw, and is advanced on the device at each call
-    in training: a captured step draws anew each time it is replayed, and so does a forward
-    that is run again for its backward (activation checkpointing), whose gradients would then be
-    of another draw: there use binding.dropout with one counter. A copy of the module
+    in training: a captured step draws anew each time it is replayed. A forward that is run
+    again for its backward (activation checkpointing) has to draw what it drew first: there
+    give the call a `counter` that `next` returned outside of what is run again. Without one
+    the second run is refused. A copy of the module
     (copy.deepcopy, of which a decoder's layers are made) has a seed of its own; one that is
     pickled or loaded continues where the stored one was.
 
@@ -131,13 +132,21 @@ class Dropout(nn.Module):
     def extra_repr(self):
         return f"p={self.p}"
 
-    def forward(self, x, residual=None):
+    def next(self):
+        """The counter of the next draw, two int64 on the state's device, for calls that are to
+        draw the same."""
+        if torch._C._current_graph_task_id() != -1:          # autograd runs a backward pass on this thread
+            raise RuntimeError("dropout in a forward that is run again for its backward would draw another mask: "
+                               "give both runs one counter (Dropout.next)")
+        return binding.dropout_next(self.state)
+
+    def forward(self, x, residual=None, counter=None):
         if residual is not None and residual.dtype != x.dtype and torch.is_autocast_enabled("cuda"):
             dtype = torch.promote_types(x.dtype, residual.dtype)
             x, residual = x.to(dtype), residual.to(dtype)
         if not self.training or self.p == 0.0:
             return x if residual is None else residual + x
-        return binding.dropout(x, self.p, binding.dropout_next(self.state), residual=residual)
+        return binding.dropout(x, self.p, self.next() if counter is None else counter, residual=residual)
 
 
 class MultiHeadAttention(nn.Module):
@@ -146,7 +155,8 @@ class MultiHeadAttention(nn.Module):
     given; value: the key unless given (a decoder adds the queries' positions to query and key
     and not to value). mask: bool, broadcasts to (B, num_heads, Q, S), true where a query may
     attend; a query with no key gets the output projection of zeros. kv_heads: key heads, each
-    shared by num_heads / kv_heads query heads. dropout: of the output. norm=True: the result
+    shared by num_heads / kv_heads query heads. dropout: of the output; counter: its draw's,
+    where the layer's own next one will not do (see Dropout). norm=True: the result
     is LayerNorm(residual + output), residual the query unless given."""
 
     def __init__(self, dim: int = 256, num_heads: int = 8, kv_heads: int | None = None,
@@ -171,9 +181,11 @@ class MultiHeadAttention(nn.Module):
             nn.init.xavier_uniform_(proj.weight)
             nn.init.zeros_(proj.bias)
 
-    def forward(self, query, key=None, value=None, mask=None, residual=None):
+    def forward(self, query, key=None, value=None, mask=None, residual=None, counter=None):
         if residual is not None and self.norm is None:
             raise ValueError("a residual is added by a layer made with norm=True")
+        if counter is not None and self.dropout is None:
+            raise ValueError("a counter is for the draws of a layer made with dropout")
         key = query if key is None else key
         value = key if value is None else value
         B, Q, _ = query.shape
@@ -182,7 +194,7 @@ class MultiHeadAttention(nn.Module):
         v = self.value_proj(value).view(B, value.shape[1], self.kv_heads, self.head_dim)
         out = self.output_proj(binding.attention(q, k, v, mask=mask))
         if self.dropout is not None:
-            out = self.dropout(out)
+            out = self.dropout(out) if counter is None else self.dropout(out, counter=counter)
         if self.norm is None:
             return out
         return self.norm(out, residual=query if residual is None else residual)
@@ -194,7 +206,8 @@ class MultiScaleDeformableAttention(nn.Module):
     (L,) int64 -> (B, Q, dim). dim = num_heads * head_dim. norm=True: the output
     is LayerNorm(residual + attention), residual (B, Q, dim) the query unless
     given (a query with its position added is not what the layer adds to).
-    dropout: of the output projection's result, in training."""
+    dropout: of the output projection's result, in training; counter: its draw's,
+    where the layer's own next one will not do (see Dropout)."""
 
     def __init__(self, dim: int = 256, num_heads: int = 8, num_levels: int = 4,
                  num_points: int = 4, accum: int = binding.MSDA_ACC_FP32_BUFFER,
@@ -233,13 +246,17 @@ class MultiScaleDeformableAttention(nn.Module):
         nn.init.xavier_uniform_(self.output_proj.weight)
         nn.init.zeros_(self.output_proj.bias)
 
-    def forward(self, query, reference, value, spatial_shapes, level_start_index, residual=None):
+    def forward(self, query, reference, value, spatial_shapes, level_start_index, residual=None,
+                counter=None):
         norm = getattr(self, "norm", None)
         # layers pickled before the mark: those with a norm of this module's were made with it
         if not getattr(self, "ends_in_norm", isinstance(norm, LayerNorm)):
             norm = None
         if residual is not None and norm is None:
             raise ValueError("a residual is added by a layer made with norm=True")
+        drop = getattr(self, "output_dropout", None)     # layers pickled before it have none
+        if counter is not None and not isinstance(drop, Dropout):
+            raise ValueError("a counter is for the draws of a layer made with dropout")
         B, Q, _ = query.shape
         S = value.shape[1]
         M, L, K, D = self.num_heads, self.num_levels, self.num_points, self.head_dim
@@ -253,9 +270,8 @@ class MultiScaleDeformableAttention(nn.Module):
         out = binding.multi_scale_deformable_attention(v, spatial_shapes, level_start_index, loc,
                                                        logits, accum=self.accum, softmax=True)
         out = self.output_proj(out)
-        drop = getattr(self, "output_dropout", None)     # layers pickled before it have none
         if isinstance(drop, Dropout):
-            out = drop(out)
+            out = drop(out, counter=counter)
         if norm is None:
             return out
         return norm(out, residual=query if residual is None else residual)
