@@ -42,7 +42,7 @@ def sources() -> list:
 
 
 def _inputs() -> list:
-    return (sources() + glob.glob(os.path.join(CSRC, "*.cuh")) +
+    return (sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) +
             [os.path.join(INCLUDE, "msda.h"), os.path.abspath(__file__)])
 
 
