@@ -163,8 +163,10 @@ class MultiHeadAttention(nn.Module):
                  dropout: float = 0.0, norm: bool = False):
         super().__init__()
         kv_heads = num_heads if kv_heads is None else kv_heads
-        if dim % num_heads != 0 or num_heads % kv_heads != 0:
+        if min(dim, num_heads, kv_heads) < 1 or dim % num_heads != 0 or num_heads % kv_heads != 0:
             raise ValueError("dim must be divisible by num_heads, num_heads by kv_heads")
+        if dim // num_heads % 8 != 0 or dim // num_heads > 128:
+            raise ValueError(f"{dim // num_heads} channels a head: multiples of 8 up to 128 are supported")
         self.dim, self.num_heads, self.kv_heads = dim, num_heads, kv_heads
         self.head_dim = dim // num_heads
         self.query_proj = nn.Linear(dim, dim)
