@@ -537,7 +537,8 @@ MSDA_API size_t msda_attention_backward_workspace_bytes(const msda_attention_dim
  * What lies in masked places, NaN and infinity among it, does not show in the
  * results. `dtype` is MSDA_F32, MSDA_BF16 or MSDA_F16. Sums, maxima and out's
  * accumulation are held in fp32; for 16-bit data the probabilities are rounded
- * to `dtype` as an operand of the second product. scale >= 0 and finite.
+ * to `dtype` as an operand of the second product. 0 <= scale <= 2.3e38; scores past fp32's
+ * range make a query's lse infinite or NaN, and out NaN or its largest score's v.
  * workspace: at least msda_attention_forward_workspace_bytes(...) bytes,
  *   16-byte aligned, owned by the caller, overwritten.
  * q, k, v, out and rest 16-byte aligned, lse 4. Outputs must not overlap inputs.

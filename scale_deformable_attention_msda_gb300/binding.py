@@ -968,8 +968,8 @@ def _scale_of(scale, plan):
     if scale is None:
         return plan.default_scale
     scale = float(scale)
-    if not 0.0 <= scale <= 3e38:
-        raise ValueError(f"scale {scale}: give a finite number, not below zero")
+    if not 0.0 <= scale <= 2.3e38:
+        raise ValueError(f"scale {scale}: give a number from zero to 2.3e38")
     return scale
 
 

@@ -213,7 +213,8 @@ cudaError_t launch_mode(AttnArgs a, const msda_attention_dims_t &d, msda_dtype_t
 }
 
 msda_status_t from_cuda(cudaError_t e) { return e == cudaSuccess ? MSDA_OK : MSDA_ERR_CUDA; }
-bool scale_ok(double s) { return s >= 0.0 && s <= 3.0e38; }
+// times log2(e) an fp32 number
+bool scale_ok(double s) { return s >= 0.0 && s <= 2.3e38; }
 
 }  // namespace
 

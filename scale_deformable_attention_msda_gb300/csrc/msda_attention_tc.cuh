@@ -112,6 +112,12 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
     return y;
 }
+// What a row's weights are relative to, in the exponent's units. NaN where a maximum that is
+// finite overflows by the scale: infinity would make every weight 0, as of a query without keys.
+__device__ __forceinline__ float tc_reference(float top, float c, float up) {
+    const float ref = top == -INFINITY ? -up : fmaf(top, c, -up);
+    return ref == INFINITY ? __int_as_float(0x7fffffff) : ref;
+}
 template <typename T> __device__ __forceinline__ uint32_t pack2(float lo, float hi);
 template <> __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
@@ -578,7 +584,7 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
                         }
                     }
                 }
-                const float ref = top == -INFINITY ? -up : top * c - up;
+                const float ref = tc_reference(top, c, up);
                 const float2 ref2 = make_float2(-ref, -ref);
                 float2 sums[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
@@ -659,7 +665,7 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
         const int count = it;          // column tiles of the block
         if (any_valid && __all_sync(0xffffffffu, ok && !*dead)) {
             const int64_t row = MODE == kGradKV ? ((int64_t)w.b * a.S + rpos) * a.N + rhead : ((int64_t)w.b * a.Q + rpos) * a.M + rhead;
-            const float ref = top == -INFINITY ? -up : top * c - up;
+            const float ref = tc_reference(top, c, up);
             const float down = BACK ? ex2(-TcScale<T>::backward) : 1.0f;   // of P; of dS also 1 / ds_scale
             const float down_ds = down / ds_scale;
             if (MODE == kForward && valid) {
