@@ -77,9 +77,8 @@ struct AttnArgs {
     int64_t part_rows;                 // rows of this mode's results
     unsigned *err;                     // device word of range faults and of waits that ran out
     // The kernels of one call follow each other in one stream, each started while the one
-    // before it ends (see attn_after). chained: there is one before. overlapped (kGradKV):
-    // the one before reads and writes nothing of this one's.
-    bool chained, overlapped;
+    // before it ends (see attn_after). chained: there is one before.
+    bool chained;
 };
 
 // Between kernels of one call: what follows sees all that the kernel before has written,
@@ -89,11 +88,6 @@ __device__ __forceinline__ void attn_after() {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
-// The keys' gradients after the queries': the wait is left to the end, so that blocks run
-// beside the last ones of the kernel before, and all before that one had ended before it
-// let this one start.
-__device__ __forceinline__ void attn_let_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void attn_after_all() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // Checked build: whether i is one of n; a fault otherwise. Always true in the normal build.
 __device__ __forceinline__ bool attn_ok(const AttnArgs &a, int64_t i, int64_t n) {

@@ -197,19 +197,49 @@ cudaError_t pack_mask(AttnArgs &a, const msda_attention_dims_t &d, const Layout 
     return msda::launch_attention_pack(m, by_query, w.words_q, by_key, w.words_k, classes, w.granules, stream);
 }
 
-cudaError_t launch_mode(AttnArgs a, const msda_attention_dims_t &d, msda_dtype_t dt, AttnMode mode, char *part,
-                        cudaStream_t stream) {
+// One mode's share of a call: its arguments and blocks.
+struct Part {
+    AttnMode mode;
+    AttnArgs a;
+    int64_t blocks;
+};
+Part part_of(AttnArgs a, const msda_attention_dims_t &d, msda_dtype_t dt, AttnMode mode, char *part) {
     const ModePlan p = plan_for(d, dt, mode);
     a.pack = mode == msda::kGradKV ? 1 : pack_of(d, tile_rows(dt));
     a.splits = p.splits;
     a.part = reinterpret_cast<float *>(part);
     a.part_rows = mode == msda::kGradKV ? d.B * d.S * d.N : d.B * d.Q * d.M;
-    const cudaError_t e = msda::few_rows(mode, dt, d.Q, a.G) ? msda::launch_attention_few(a, p.blocks, stream)
-                        : dt == MSDA_F32  ? msda::launch_attention_f32(mode, a, p.blocks, stream)
-                        : dt == MSDA_BF16 ? msda::launch_attention_bf16(mode, a, p.blocks, stream)
-                                          : msda::launch_attention_f16(mode, a, p.blocks, stream);
-    if (e != cudaSuccess || p.splits == 1) return e;
-    return msda::launch_attention_join(mode, a, dt, stream);
+    return {mode, a, p.blocks};
+}
+cudaError_t join(const Part &p, msda_dtype_t dt, cudaStream_t stream) {
+    return p.blocks > 0 && p.a.splits > 1 ? msda::launch_attention_join(p.mode, p.a, dt, stream) : cudaSuccess;
+}
+
+cudaError_t launch_forward(const Part &p, msda_dtype_t dt, cudaStream_t stream) {
+    const cudaError_t e = msda::few_rows(p.mode, dt, p.a.Q, p.a.G) ? msda::launch_attention_few(p.a, p.blocks, stream)
+                        : dt == MSDA_F32  ? msda::launch_attention_f32(p.mode, p.a, p.blocks, stream)
+                        : dt == MSDA_BF16 ? msda::launch_attention_bf16(p.a, p.blocks, stream)
+                                          : msda::launch_attention_f16(p.a, p.blocks, stream);
+    return e == cudaSuccess ? join(p, dt, stream) : e;
+}
+// The gradients of the queries, and of keys and values; no blocks: not wanted.
+cudaError_t launch_backward(const Part &q, const Part &kv, msda_dtype_t dt, cudaStream_t stream) {
+    auto back = [&](const Part &p, const Part &r) {      // 16-bit
+        return dt == MSDA_BF16 ? msda::launch_attention_bf16_back(p.a, p.blocks, r.a, r.blocks, stream)
+                               : msda::launch_attention_f16_back(p.a, p.blocks, r.a, r.blocks, stream);
+    };
+    auto one = [&](const Part &p) {
+        if (p.blocks == 0) return cudaSuccess;
+        Part none = p;
+        none.blocks = 0;
+        return dt == MSDA_F32 ? msda::launch_attention_f32(p.mode, p.a, p.blocks, stream)
+             : p.mode == msda::kGradQ ? back(p, none) : back(none, p);
+    };
+    const bool apart = dt == MSDA_F32 || q.blocks == 0 || kv.blocks == 0 || msda::tc_short(kv.mode, kv.a.D, kv.a.Q, kv.a.G);
+    cudaError_t e = apart ? one(q) : back(q, kv);
+    if (e == cudaSuccess) e = join(q, dt, stream);
+    if (e == cudaSuccess && apart) e = one(kv);
+    return e == cudaSuccess ? join(kv, dt, stream) : e;
 }
 
 msda_status_t from_cuda(cudaError_t e) { return e == cudaSuccess ? MSDA_OK : MSDA_ERR_CUDA; }
@@ -255,7 +285,7 @@ msda_status_t msda_attention_forward(const void *q, const void *k, const void *v
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e = masked ? pack_mask(a, d, w, mask, ws, false, s) : cudaSuccess;
     a.chained = masked;
-    if (e == cudaSuccess) e = launch_mode(a, d, dtype, msda::kForward, ws + w.part[0], s);
+    if (e == cudaSuccess) e = launch_forward(part_of(a, d, dtype, msda::kForward, ws + w.part[0]), dtype, s);
     return from_cuda(e);
 }
 
@@ -304,9 +334,10 @@ msda_status_t msda_attention_backward(const void *grad_out, const void *q, const
     a.chained = masked;
     if (e == cudaSuccess) e = msda::launch_attention_delta(a, blocks, dtype, s);
     a.chained = true;
-    if (e == cudaSuccess && for_q) e = launch_mode(a, d, dtype, msda::kGradQ, ws + w.part[1], s);
-    a.overlapped = for_q;
-    if (e == cudaSuccess && for_kv) e = launch_mode(a, d, dtype, msda::kGradKV, ws + w.part[2], s);
+    Part pq = part_of(a, d, dtype, msda::kGradQ, ws + w.part[1]), pkv = part_of(a, d, dtype, msda::kGradKV, ws + w.part[2]);
+    if (!for_q) pq.blocks = 0;
+    if (!for_kv) pkv.blocks = 0;
+    if (e == cudaSuccess) e = launch_backward(pq, pkv, dtype, s);
     return from_cuda(e);
 }
 

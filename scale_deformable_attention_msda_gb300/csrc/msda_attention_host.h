@@ -8,8 +8,10 @@
 namespace msda {
 
 cudaError_t launch_attention_f32(int mode, const AttnArgs &a, int64_t blocks, cudaStream_t stream);
-cudaError_t launch_attention_bf16(int mode, const AttnArgs &a, int64_t blocks, cudaStream_t stream);
-cudaError_t launch_attention_f16(int mode, const AttnArgs &a, int64_t blocks, cudaStream_t stream);
+cudaError_t launch_attention_bf16(const AttnArgs &a, int64_t blocks, cudaStream_t stream);        // forward
+cudaError_t launch_attention_f16(const AttnArgs &a, int64_t blocks, cudaStream_t stream);
+cudaError_t launch_attention_bf16_back(const AttnArgs &q, int64_t q_blocks, const AttnArgs &kv, int64_t kv_blocks, cudaStream_t stream);
+cudaError_t launch_attention_f16_back(const AttnArgs &q, int64_t q_blocks, const AttnArgs &kv, int64_t kv_blocks, cudaStream_t stream);
 
 // A launch that may start while the kernel before it in the stream ends (chained; see
 // attn_after).

@@ -126,8 +126,7 @@ __global__ void __launch_bounds__(kSimpleThreads, simple_blocks(DP)) attn_simple
     const AttnRows w = attn_rows<MODE, R>(a, blockIdx.x / a.splits);
     const int64_t tiles = attn_column_tiles<MODE, C>(a);
     const int64_t j0 = tiles * split / a.splits, j1 = tiles * (split + 1) / a.splits;
-    if (MODE == kGradKV && a.overlapped) attn_let_next();
-    else attn_after();
+    attn_after();
 
     auto row_of = [&](const AttnTensor &t) {
         return [&, t](int r) { return w.valid(r) ? attn_at<float>(a, t, w.b, w.row_pos(r), w.row_head(r)) : nullptr; };
@@ -287,7 +286,6 @@ __global__ void __launch_bounds__(kSimpleThreads, simple_blocks(DP)) attn_simple
             if (MODE != kForward) attn_store<float, MODE>(a, w, r, split, MODE == kGradKV, d, e2[i], f);
         }
     }
-    if (MODE == kGradKV && a.overlapped) attn_after_all();
 }
 
 template <int MODE, int DP>

@@ -241,9 +241,9 @@ struct TcMaps {
     CUtensorMap a1, a2, x1, x2;        // rows: one or two; columns: two
 };
 
+// Block `block` of a mode.
 template <typename T, int MODE, int DP, bool SHORT>
-__global__ void __launch_bounds__(Tc<MODE, DP, SHORT>::THREADS, Tc<MODE, DP, SHORT>::BLOCKS)
-attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
+__device__ __forceinline__ void attn_tc_block(const AttnArgs &a, const TcMaps &maps, int block) {
     using K = Tc<MODE, DP, SHORT>;
     constexpr int BN = K::BN, STAGES = K::STAGES, EARLY = K::EARLY, INFO = K::INFO, HELPER = K::PARTS * 4;
     constexpr bool BF16 = TcScale<T>::forward == 0.0f, BACK = K::BACK;
@@ -265,8 +265,8 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
     volatile uint32_t *dead = slot + 1;
 
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x & 31;
-    const int split = blockIdx.x % a.splits;
-    const AttnRows w = attn_rows<MODE, kTcRows>(a, blockIdx.x / a.splits);
+    const int split = block % a.splits;
+    const AttnRows w = attn_rows<MODE, kTcRows>(a, block / a.splits);
     const int64_t tiles = attn_column_tiles<MODE, BN>(a);
     const int64_t j0 = tiles * split / a.splits, j1 = tiles * (split + 1) / a.splits;
 
@@ -297,8 +297,7 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
         bar_init_done();
         *dead = 0u;
     }
-    if (MODE == kGradKV && a.overlapped) attn_let_next();
-    else attn_after();
+    attn_after();
     if (MODE == kGradKV) {
         for (int i = threadIdx.x; i < kTcRows; i += K::THREADS) tc_bias_row(ones, i, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f);
         shared_to_async();
@@ -720,12 +719,30 @@ attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
         }
         tmem_before_sync();
     }
-    if (MODE == kGradKV && a.overlapped) attn_after_all();
     __syncthreads();
     if (warp == HELPER) {
         tmem_after_sync();
         tmem_free<K::COLS>(tmem);
     }
+}
+
+template <typename T, int MODE, int DP, bool SHORT>
+__global__ void __launch_bounds__(Tc<MODE, DP, SHORT>::THREADS, Tc<MODE, DP, SHORT>::BLOCKS)
+attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ TcMaps maps) {
+    attn_tc_block<T, MODE, DP, SHORT>(a, maps, blockIdx.x);
+}
+
+// Both gradients' blocks in one launch: neither needs the other's results, and the last ones
+// of one kind leave no SM idle. The keys' first (`keys` of them), which take longer: the
+// queries' first is 2 to 6 % slower. One launch after the other: 17.3 us instead of 10.6 for
+// 300 queries and keys of 2 x 8 heads of 32, 511 instead of 507 for 4,096 of 32 heads of 64.
+template <typename T, int DP>
+__global__ void __launch_bounds__(Tc<kGradQ, DP, false>::THREADS, 1)
+attn_tc_back_kernel(const __grid_constant__ AttnArgs q, const __grid_constant__ TcMaps q_maps, int keys,
+                    const __grid_constant__ AttnArgs kv, const __grid_constant__ TcMaps kv_maps) {
+    static_assert((int)Tc<kGradQ, DP, false>::THREADS == (int)Tc<kGradKV, DP, false>::THREADS, "one launch");
+    if ((int)blockIdx.x < keys) attn_tc_block<T, kGradKV, DP, false>(kv, kv_maps, blockIdx.x);
+    else attn_tc_block<T, kGradQ, DP, false>(q, q_maps, blockIdx.x - keys);
 }
 
 // ------------------------------------------------------------------ launch
@@ -750,51 +767,74 @@ cudaError_t tc_map(CUtensorMap *map, const AttnTensor &t, const AttnArgs &a, int
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <typename T, int MODE, int DP, bool SHORT = false>
-cudaError_t launch_tc_d(const AttnArgs &a, int64_t blocks, cudaStream_t stream) {
+// The maps of a mode's tensors. No columns: the maps are of what is there, and nothing is
+// fetched.
+template <typename T, int MODE, int DP, bool SHORT> cudaError_t tc_maps(TcMaps *maps, const AttnArgs &a) {
     using K = Tc<MODE, DP, SHORT>;
     constexpr bool bf16 = TcScale<T>::forward == 0.0f;
-    TcMaps maps;
     cudaError_t e;
-    // no columns: the maps are of what is there, and nothing is fetched
     const bool none = MODE == kGradKV ? a.Q == 0 : a.S == 0;
     if (MODE == kGradKV) {
         const AttnTensor &x1 = none ? a.k : a.q, &x2 = none ? a.v : a.go;
         const int len = none ? a.S : a.Q, heads = none ? a.N : a.M;
-        if ((e = tc_map<MODE, DP, SHORT>(&maps.a1, a.k, a, a.S, a.N, 1, kTcRows, bf16)) != cudaSuccess ||
-            (e = tc_map<MODE, DP, SHORT>(&maps.a2, a.v, a, a.S, a.N, 1, kTcRows, bf16)) != cudaSuccess ||
-            (e = tc_map<MODE, DP, SHORT>(&maps.x1, x1, a, len, heads, 1, K::BN, bf16)) != cudaSuccess ||
-            (e = tc_map<MODE, DP, SHORT>(&maps.x2, x2, a, len, heads, 1, K::BN, bf16)) != cudaSuccess)
+        if ((e = tc_map<MODE, DP, SHORT>(&maps->a1, a.k, a, a.S, a.N, 1, kTcRows, bf16)) != cudaSuccess ||
+            (e = tc_map<MODE, DP, SHORT>(&maps->a2, a.v, a, a.S, a.N, 1, kTcRows, bf16)) != cudaSuccess ||
+            (e = tc_map<MODE, DP, SHORT>(&maps->x1, x1, a, len, heads, 1, K::BN, bf16)) != cudaSuccess)
             return e;
-    } else {
-        const AttnTensor &x1 = none ? a.q : a.k, &x2 = none ? a.q : a.v;
-        const int len = none ? a.Q : a.S, heads = none ? a.M : a.N;
-        if ((e = tc_map<MODE, DP, SHORT>(&maps.a1, a.q, a, a.Q, a.M, a.pack, kTcRows / a.pack, bf16)) != cudaSuccess ||
-            (e = tc_map<MODE, DP, SHORT>(&maps.x1, x1, a, len, heads, 1, K::BN, bf16)) != cudaSuccess ||
-            (e = tc_map<MODE, DP, SHORT>(&maps.x2, x2, a, len, heads, 1, K::BN, bf16)) != cudaSuccess)
-            return e;
-        maps.a2 = maps.a1;
-        if (MODE == kGradQ && (e = tc_map<MODE, DP, SHORT>(&maps.a2, a.go, a, a.Q, a.M, a.pack, kTcRows / a.pack, bf16)) != cudaSuccess) return e;
+        return tc_map<MODE, DP, SHORT>(&maps->x2, x2, a, len, heads, 1, K::BN, bf16);
     }
+    const AttnTensor &x1 = none ? a.q : a.k, &x2 = none ? a.q : a.v;
+    const int len = none ? a.Q : a.S, heads = none ? a.M : a.N;
+    if ((e = tc_map<MODE, DP, SHORT>(&maps->a1, a.q, a, a.Q, a.M, a.pack, kTcRows / a.pack, bf16)) != cudaSuccess ||
+        (e = tc_map<MODE, DP, SHORT>(&maps->x1, x1, a, len, heads, 1, K::BN, bf16)) != cudaSuccess ||
+        (e = tc_map<MODE, DP, SHORT>(&maps->x2, x2, a, len, heads, 1, K::BN, bf16)) != cudaSuccess)
+        return e;
+    maps->a2 = maps->a1;
+    if (MODE != kGradQ) return cudaSuccess;
+    return tc_map<MODE, DP, SHORT>(&maps->a2, a.go, a, a.Q, a.M, a.pack, kTcRows / a.pack, bf16);
+}
+
+template <typename T, int MODE, int DP, bool SHORT>
+cudaError_t launch_tc_d(const AttnArgs &a, int64_t blocks, cudaStream_t stream) {
+    using K = Tc<MODE, DP, SHORT>;
+    TcMaps maps;
+    cudaError_t e = tc_maps<T, MODE, DP, SHORT>(&maps, a);
+    if (e != cudaSuccess) return e;
     auto *kernel = attn_tc_kernel<T, MODE, DP, SHORT>;
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, K::SHARED);
     if (e != cudaSuccess) return e;
     return launch_after(a.chained, kernel, blocks, K::THREADS, K::SHARED, stream, a, maps);
 }
-template <typename T, int MODE>
-cudaError_t launch_tc_mode(const AttnArgs &a, int64_t blocks, cudaStream_t stream) {
-    if constexpr (MODE == kGradKV)
-        if (tc_short(MODE, a.D, a.Q, a.G))
-            return a.D <= 32 ? launch_tc_d<T, MODE, 32, true>(a, blocks, stream) : launch_tc_d<T, MODE, 64, true>(a, blocks, stream);
-    return a.D <= 32 ? launch_tc_d<T, MODE, 32>(a, blocks, stream)
-         : a.D <= 64 ? launch_tc_d<T, MODE, 64>(a, blocks, stream)
-                     : launch_tc_d<T, MODE, 128>(a, blocks, stream);
-}
 template <typename T>
-cudaError_t launch_tc(int mode, const AttnArgs &a, int64_t blocks, cudaStream_t stream) {
-    return mode == kForward ? launch_tc_mode<T, kForward>(a, blocks, stream)
-         : mode == kGradQ   ? launch_tc_mode<T, kGradQ>(a, blocks, stream)
-                            : launch_tc_mode<T, kGradKV>(a, blocks, stream);
+cudaError_t launch_tc(const AttnArgs &a, int64_t blocks, cudaStream_t stream) {
+    return a.D <= 32 ? launch_tc_d<T, kForward, 32, false>(a, blocks, stream)
+         : a.D <= 64 ? launch_tc_d<T, kForward, 64, false>(a, blocks, stream)
+                     : launch_tc_d<T, kForward, 128, false>(a, blocks, stream);
+}
+
+template <typename T, int DP>
+cudaError_t launch_tc_back_d(const AttnArgs &q, int64_t q_blocks, const AttnArgs &kv, int64_t kv_blocks, cudaStream_t stream) {
+    using Q = Tc<kGradQ, DP, false>;
+    using KV = Tc<kGradKV, DP, false>;
+    constexpr int bytes = Q::SHARED > KV::SHARED ? Q::SHARED : KV::SHARED;
+    TcMaps q_maps = {}, kv_maps = {};
+    cudaError_t e = q_blocks > 0 ? tc_maps<T, kGradQ, DP, false>(&q_maps, q) : cudaSuccess;
+    if (e == cudaSuccess && kv_blocks > 0) e = tc_maps<T, kGradKV, DP, false>(&kv_maps, kv);
+    if (e != cudaSuccess) return e;
+    auto *kernel = attn_tc_back_kernel<T, DP>;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    return launch_after(true, kernel, q_blocks + kv_blocks, Q::THREADS, bytes, stream, q, q_maps, (int)kv_blocks, kv, kv_maps);
+}
+// The gradients; no blocks of a kind that is not wanted. The small blocks of few queries have
+// a launch of their own.
+template <typename T>
+cudaError_t launch_tc_back(const AttnArgs &q, int64_t q_blocks, const AttnArgs &kv, int64_t kv_blocks, cudaStream_t stream) {
+    if (q_blocks == 0 && tc_short(kGradKV, kv.D, kv.Q, kv.G))
+        return kv.D <= 32 ? launch_tc_d<T, kGradKV, 32, true>(kv, kv_blocks, stream) : launch_tc_d<T, kGradKV, 64, true>(kv, kv_blocks, stream);
+    return q.D <= 32 ? launch_tc_back_d<T, 32>(q, q_blocks, kv, kv_blocks, stream)
+         : q.D <= 64 ? launch_tc_back_d<T, 64>(q, q_blocks, kv, kv_blocks, stream)
+                     : launch_tc_back_d<T, 128>(q, q_blocks, kv, kv_blocks, stream);
 }
 
 }  // namespace msda
