@@ -13,8 +13,10 @@ __device__ __forceinline__ uint32_t shared_at(const void *p) { return (uint32_t)
 // ------------------------------------------------------------- mbarriers
 // Waits are bounded: one of two seconds (they take microseconds) sets the block's
 // `dead` word, whereupon every other wait of the block gives up too, and bit 1 of
-// the device word.
-constexpr unsigned long long kWaitNs = 2000000000ull;
+// the device word. A pause between two looks at the timer, as of a process whose turn on
+// the GPU was another's, counts as ten milliseconds at most: what ran out is time that the
+// block had.
+constexpr unsigned long long kWaitNs = 2000000000ull, kPauseNs = 10000000ull;
 
 __device__ __forceinline__ unsigned long long nanoseconds() {
     unsigned long long t;
@@ -53,15 +55,17 @@ __device__ __forceinline__ bool bar_try(uint64_t *bar, uint32_t parity) {
 // The rest of a wait whose first look found the phase not there. False when it ran out,
 // here or in another wait of the block.
 __device__ __forceinline__ bool bar_wait_more(uint64_t *bar, uint32_t parity, volatile uint32_t *dead, unsigned *err) {
-    unsigned long long start = 0;
+    unsigned long long last = 0, waited = 0;
     for (uint32_t i = 1;; ++i) {
         if (bar_try(bar, parity)) return true;
         if (i & 63u) continue;         // the timer is slow to read
         if (*dead) return false;
         const unsigned long long now = nanoseconds();
-        if (start == 0) start = now;
-        else if (now - start > kWaitNs) break;
+        if (last != 0) waited += now - last < kPauseNs ? now - last : kPauseNs;
+        last = now;
+        if (waited > kWaitNs) break;
     }
+    if (bar_try(bar, parity)) return true;
     *dead = 1u;
     if (err) atomicOr(err, 2u);
     return false;
