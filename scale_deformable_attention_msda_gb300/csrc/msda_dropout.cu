@@ -12,7 +12,6 @@
 #include "msda_host.h"
 
 namespace msda {
-cudaError_t fault_word_for_launch(unsigned **err);
 namespace {
 
 constexpr int kThreads = 256;

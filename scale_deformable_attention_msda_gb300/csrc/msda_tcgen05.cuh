@@ -183,20 +183,11 @@ template <> __device__ __forceinline__ void tmem_read_two<64>(uint32_t (&v)[64],
                  "tcgen05.ld.sync.aligned.32x32b.x64.b32 {" TMEM_R4 "," TMEM_R5 "," TMEM_R6 "," TMEM_R7 "}, [%129];\n\t" TMEM_WAIT
                  : TMEM_OUT32(0), TMEM_OUT32(32), TMEM_OUT32W(0), TMEM_OUT32W(32) : "r"(at), "r"(at2) : "memory");
 }
-template <> __device__ __forceinline__ void tmem_read_two<32>(uint32_t (&v)[32], uint32_t (&w)[32], uint32_t at, uint32_t at2) {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {" TMEM_R0 "," TMEM_R1 "}, [%64];\n\t"
-                 "tcgen05.ld.sync.aligned.32x32b.x32.b32 {" TMEM_R2 "," TMEM_R3 "}, [%65];\n\t" TMEM_WAIT
-                 : TMEM_OUT32(0), TMEM_OUT32W(0) : "r"(at), "r"(at2) : "memory");
-}
 template <int N> __device__ __forceinline__ void tmem_store(uint32_t at, const uint32_t (&v)[N]);
 #define TMEM_IN8(o) "r"(v[o]), "r"(v[o + 1]), "r"(v[o + 2]), "r"(v[o + 3]), "r"(v[o + 4]), "r"(v[o + 5]), "r"(v[o + 6]), "r"(v[o + 7])
 #define TMEM_IN32(o) TMEM_IN8(o), TMEM_IN8(o + 8), TMEM_IN8(o + 16), TMEM_IN8(o + 24)
 template <> __device__ __forceinline__ void tmem_store<32>(uint32_t at, const uint32_t (&v)[32]) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {" TMEM_R0 "," TMEM_R1 "};" ::TMEM_IN32(0), "r"(at) : "memory");
-}
-template <> __device__ __forceinline__ void tmem_store<16>(uint32_t at, const uint32_t (&v)[16]) { tmem_store16(at, v); }
-template <> __device__ __forceinline__ void tmem_store<64>(uint32_t at, const uint32_t (&v)[64]) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x64.b32 [%64], {" TMEM_R0 "," TMEM_R1 "," TMEM_R2 "," TMEM_R3 "};" ::TMEM_IN32(0), TMEM_IN32(32), "r"(at) : "memory");
 }
 
 // ------------------------------------------------------------------- MMA
