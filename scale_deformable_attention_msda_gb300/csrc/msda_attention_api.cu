@@ -82,8 +82,10 @@ ModePlan plan_mode(const msda_attention_dims_t &d, AttnMode mode, int R, int C, 
     return p;
 }
 
-// Blocks of the pass over the queries' rows. A block of 256 threads has 64 rows at once at
-// the least.
+// Blocks of the pass over the queries' rows: one for 64 rows, of which its 256 threads have 32
+// to 256 under way at once, and four an SM at most. One for each 8 to 64 rows instead, as many
+// as there are threads for: the backward of 600 rows of 4 heads of 128 in fp32 150 us (153),
+// of 2 x 300 of 8 heads of 64 in fp16 15.9 (14.5), of 4 x 512 in bf16 24.5 (22.9).
 int64_t delta_blocks(int64_t rows) {
     const int64_t blocks = ceil_div(rows, 64);
     return blocks < 1 ? 1 : blocks < kDeltaBlocks ? blocks : kDeltaBlocks;
@@ -99,7 +101,8 @@ int tile_rows(msda_dtype_t dt) { return dt == MSDA_F32 ? 64 : 128; }
 
 ModePlan plan_for(const msda_attention_dims_t &d, msda_dtype_t dt, AttnMode mode) {
     if (msda::few_rows(mode, dt, d.Q, d.M / d.N)) {
-        // a key head's keys over as many blocks as two an SM leave it, 256 keys or more each
+        // a key head's keys over as many blocks as two an SM leave it, 256 keys or more for each
+        // (their shares are rounded up to 32 keys, and the last one has what is left)
         ModePlan p = {};
         p.tiles = d.B * d.N;
         int64_t s = p.tiles > 0 ? 2 * kSMs / p.tiles : 1;
