@@ -338,20 +338,35 @@ __device__ __noinline__ void attn_exact_row(const AttnArgs &a, const AttnRows &w
                 p = on ? exp2f(fmaf(s, a.c, -lse2)) : 0.0f;
                 ds = on ? p * (dp - delta) : 0.0f;
             }
-            uint32_t left = __ballot_sync(0xffffffffu, on);
-            while (left) {
-                const int from = __ffs(left) - 1;
-                left &= left - 1;
-                const float pf = __shfl_sync(0xffffffffu, p, from), df = __shfl_sync(0xffffffffu, ds, from);
-                const T *y1 = reinterpret_cast<const T *>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(x1), from));
-                const T *y2 = reinterpret_cast<const T *>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(x2), from));
+            // four allowed columns at a time, their loads under way together
+            const T *rows1 = MODE == kGradKV ? attn_at<T>(a, a.q, w.b, cpos + c0, chead) : attn_at<T>(a, a.k, w.b, cpos + c0, chead);
+            const T *rows2 = MODE == kGradKV ? attn_at<T>(a, a.go, w.b, cpos + c0, chead) : attn_at<T>(a, a.v, w.b, cpos + c0, chead);
+            const int64_t step1 = MODE == kGradKV ? a.q.pos : a.k.pos, step2 = MODE == kGradKV ? a.go.pos : a.v.pos;
+            for (uint32_t left = __ballot_sync(0xffffffffu, on); left;) {
+                constexpr int U = 4;
+                float pf[U], df[U], y1[U][4], y2[U][4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int d = lane + 32 * i;
-                    if (d >= a.D) continue;
-                    if (MODE != kGradQ) acc1[i] = fmaf(pf, Elem<T>::to_f(y2[d]), acc1[i]);
-                    if (MODE != kForward) acc2[i] = fmaf(df, Elem<T>::to_f(y1[d]), acc2[i]);
+                for (int u = 0; u < U; ++u) {
+                    const bool any = left != 0u;       // of the whole warp
+                    const int from = any ? __ffs(left) - 1 : 0;
+                    left &= left - 1;
+                    pf[u] = __shfl_sync(0xffffffffu, any ? p : 0.0f, from);
+                    df[u] = __shfl_sync(0xffffffffu, any ? ds : 0.0f, from);
+                    const T *r1 = rows1 + from * step1 + lane, *r2 = rows2 + from * step2 + lane;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const bool there = any && lane + 32 * i < a.D;
+                        if (MODE != kForward) y1[u][i] = there ? Elem<T>::to_f(r1[32 * i]) : 0.0f;
+                        if (MODE != kGradQ) y2[u][i] = there ? Elem<T>::to_f(r2[32 * i]) : 0.0f;
+                    }
                 }
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if (MODE != kGradQ) acc1[i] = fmaf(pf[u], y2[u][i], acc1[i]);
+                        if (MODE != kForward) acc2[i] = fmaf(df[u], y1[u][i], acc2[i]);
+                    }
             }
         }
     }
