@@ -579,7 +579,7 @@ MSDA_API msda_status_t msda_attention_backward(const void *grad_out, const void 
 
 /* Dropout of n entries: out[e] = residual[e] + (kept(e) ? x[e] * f : 0), the
  * sum rounded once (residual NULL: none). With t = round(p * 65536), f =
- * 65536 / (65536 - t) in fp32, and kept(e) says that 16 random bits are >= t,
+ * 65536 / (65536 - t) in fp32 (MSDA_F64: in fp64), and kept(e) says that 16 random bits are >= t,
  * so that out's expectation is exact for the p of t. The bits are those of
  * Philox4x32-10 (Salmon et al., "Parallel random numbers: as easy as 1, 2, 3",
  * SC 2011) with counter[0] as its key and (e / 8, counter[1]) as its counter,

@@ -238,7 +238,9 @@ cudaError_t launch_backward(const Part &q, const Part &kv, msda_dtype_t dt, cuda
         return dt == MSDA_F32 ? msda::launch_attention_f32(p.mode, p.a, p.blocks, stream)
              : p.mode == msda::kGradQ ? back(p, none) : back(none, p);
     };
-    const bool apart = dt == MSDA_F32 || q.blocks == 0 || kv.blocks == 0 || msda::tc_short(kv.mode, kv.a.D, kv.a.Q, kv.a.G);
+    // two launches also where one grid would not hold both
+    const bool apart = dt == MSDA_F32 || q.blocks == 0 || kv.blocks == 0 || q.blocks + kv.blocks > kMaxTiles ||
+                       msda::tc_short(kv.mode, kv.a.D, kv.a.Q, kv.a.G);
     cudaError_t e = apart ? one(q) : back(q, kv);
     if (e == cudaSuccess) e = join(q, dt, stream);
     if (e == cudaSuccess && apart) e = one(kv);
