@@ -113,7 +113,7 @@ ModePlan plan_for(const msda_attention_dims_t &d, msda_dtype_t dt, AttnMode mode
         return p;
     }
     if (dt == MSDA_F32) return plan_mode(d, mode, 64, 64, kSMs * msda::simple_blocks(d.D), 1);
-    const bool is_short = msda::tc_short(mode, d.D, d.Q, d.M / d.N);
+    const bool is_short = msda::tc_short(mode, d.D, d.Q, d.M / d.N, d.B * d.N * ceil_div(d.S, 128));
     const int columns = msda::tc_columns(mode, d.D, is_short), blocks = msda::tc_blocks(mode, d.D, is_short);
     return plan_mode(d, mode, 128, columns, kSMs * blocks, 4);
 }
@@ -240,7 +240,7 @@ cudaError_t launch_backward(const Part &q, const Part &kv, msda_dtype_t dt, cuda
     };
     // two launches also where one grid would not hold both
     const bool apart = dt == MSDA_F32 || q.blocks == 0 || kv.blocks == 0 || q.blocks + kv.blocks > kMaxTiles ||
-                       msda::tc_short(kv.mode, kv.a.D, kv.a.Q, kv.a.G);
+                       msda::tc_short(kv.a);
     cudaError_t e = apart ? one(q) : back(q, kv);
     if (e == cudaSuccess) e = join(q, dt, stream);
     if (e == cudaSuccess && apart) e = one(kv);

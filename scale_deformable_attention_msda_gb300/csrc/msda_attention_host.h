@@ -30,11 +30,15 @@ cudaError_t launch_after(bool chained, void (*kernel)(P...), int64_t blocks, int
     return cudaLaunchKernelEx(&config, kernel, P(args)...);
 }
 
-// Whether a key tile's few queries are walked by small blocks, two an SM, one starting
-// while the other ends, rather than by one an SM with tiles of 128 columns. 100 queries of
-// 32 heads over 4,096 keys, fp16, D 32, the whole backward: 73 us, 94 with large blocks; 300
-// queries 22.5 us, 20.4; 512 queries, D 64, 36.7 us, 25.8.
-constexpr bool tc_short(int mode, int64_t D, int64_t Q, int64_t G) { return mode == kGradKV && D <= 64 && G * ((Q + 63) / 64 * 64) <= 256; }
+// Whether a key tile's few queries are walked by small blocks, two an SM, one starting while
+// the other ends, in a launch of their own, rather than by one an SM with tiles of 128 columns
+// beside the queries' gradients. The whole backward, 4 x 8 heads of 32, bf16, small blocks and
+// large: 120 queries over 2,400 keys 31.0 us, 38.8, over 1,200 (320 key tiles) 26.7 and 23.2,
+// over 200 16.6 and 9.3; 300 queries over 300 keys 25.8 and 21.4.
+constexpr bool tc_short(int mode, int64_t D, int64_t Q, int64_t G, int64_t key_tiles) {
+    return mode == kGradKV && D <= 64 && G * ((Q + 63) / 64 * 64) <= 256 && key_tiles > 456;
+}
+inline bool tc_short(const AttnArgs &a) { return tc_short(kGradKV, a.D, a.Q, a.G, (int64_t)a.B * a.N * (((int64_t)a.S + 127) / 128)); }
 // The 16-bit kernels' columns of a tile, and their blocks of an SM.
 constexpr int tc_columns(int mode, int64_t D, bool is_short) { return is_short || (mode == kForward && D > 64) ? 64 : 128; }
 constexpr int tc_blocks(int mode, int64_t D, bool is_short) { return is_short || mode == kForward ? 2 : 1; }

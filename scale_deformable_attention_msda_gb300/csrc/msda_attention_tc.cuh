@@ -733,16 +733,19 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ TcMap
 }
 
 // Both gradients' blocks in one launch: neither needs the other's results, and the last ones
-// of one kind leave no SM idle. The keys' first (`keys` of them), which take longer: the
-// queries' first is 2 to 6 % slower. One launch after the other: 17.3 us instead of 10.6 for
-// 300 queries and keys of 2 x 8 heads of 32, 511 instead of 507 for 4,096 of 32 heads of 64.
+// of one kind leave no SM idle. The kind whose blocks take longer is first (`first` blocks of
+// it). One launch after the other: 17.3 us instead of 11.1 for 300 queries and keys of 2 x 8
+// heads of 32, 511 instead of 502 for 4,096 of 32 heads of 64; the queries' first there: 510;
+// the keys' first for 60 queries of 4 x 8 heads of 32 over 600 keys: 17.5 instead of 14.4.
 template <typename T, int DP>
 __global__ void __launch_bounds__(Tc<kGradQ, DP, false>::THREADS, 1)
-attn_tc_back_kernel(const __grid_constant__ AttnArgs q, const __grid_constant__ TcMaps q_maps, int keys,
+attn_tc_back_kernel(const __grid_constant__ AttnArgs q, const __grid_constant__ TcMaps q_maps, int first, bool keys_first,
                     const __grid_constant__ AttnArgs kv, const __grid_constant__ TcMaps kv_maps) {
     static_assert((int)Tc<kGradQ, DP, false>::THREADS == (int)Tc<kGradKV, DP, false>::THREADS, "one launch");
-    if ((int)blockIdx.x < keys) attn_tc_block<T, kGradKV, DP, false>(kv, kv_maps, blockIdx.x);
-    else attn_tc_block<T, kGradQ, DP, false>(q, q_maps, blockIdx.x - keys);
+    const bool early = (int)blockIdx.x < first;
+    const int block = early ? blockIdx.x : blockIdx.x - first;
+    if (early == keys_first) attn_tc_block<T, kGradKV, DP, false>(kv, kv_maps, block);
+    else attn_tc_block<T, kGradQ, DP, false>(q, q_maps, block);
 }
 
 // ------------------------------------------------------------------ launch
@@ -824,13 +827,16 @@ cudaError_t launch_tc_back_d(const AttnArgs &q, int64_t q_blocks, const AttnArgs
     auto *kernel = attn_tc_back_kernel<T, DP>;
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
-    return launch_after(true, kernel, q_blocks + kv_blocks, Q::THREADS, bytes, stream, q, q_maps, (int)kv_blocks, kv, kv_maps);
+    // by column tiles a block; the keys' take a third longer
+    const int64_t q_walk = attn_column_tiles<kGradQ, Q::BN>(q) / q.splits, kv_walk = attn_column_tiles<kGradKV, KV::BN>(kv) / kv.splits;
+    const bool keys_first = 4 * kv_walk >= 3 * q_walk;
+    return launch_after(true, kernel, q_blocks + kv_blocks, Q::THREADS, bytes, stream, q, q_maps, (int)(keys_first ? kv_blocks : q_blocks), keys_first, kv, kv_maps);
 }
-// The gradients; no blocks of a kind that is not wanted. The small blocks of few queries have
-// a launch of their own.
+// The gradients; no blocks of a kind that is not wanted. The small blocks of few queries
+// (tc_short) have a launch of their own.
 template <typename T>
 cudaError_t launch_tc_back(const AttnArgs &q, int64_t q_blocks, const AttnArgs &kv, int64_t kv_blocks, cudaStream_t stream) {
-    if (q_blocks == 0 && tc_short(kGradKV, kv.D, kv.Q, kv.G))
+    if (q_blocks == 0 && tc_short(kv))
         return kv.D <= 32 ? launch_tc_d<T, kGradKV, 32, true>(kv, kv_blocks, stream) : launch_tc_d<T, kGradKV, 64, true>(kv, kv_blocks, stream);
     return q.D <= 32 ? launch_tc_back_d<T, 32>(q, q_blocks, kv, kv_blocks, stream)
          : q.D <= 64 ? launch_tc_back_d<T, 64>(q, q_blocks, kv, kv_blocks, stream)
