@@ -4,8 +4,8 @@
 //
 // What bounds it: the instructions around the multiply-adds (a shared-memory load of 16
 // bytes for every 8 of them, exponentials, addresses) and their latencies: 1024 x 1024 of
-// 16 heads, D 32 / 64 / 128: forward 96 / 150 / 342 us (22 to 29 TFLOP/s of 75), backward
-// 287 / 468 / 1,069. 300 queries of 16 heads, D 32, where a block has one tile or two:
+// 16 heads, D 32 / 64 / 128: forward 93 / 149 / 345 us (23 to 29 TFLOP/s of 75), backward
+// 291 / 469 / 1,070. 300 queries of 16 heads, D 32, where a block has one tile or two:
 // 19 and 50 us. 8 x 4 scores and 128 threads, with packed multiply-adds: 114 us forward
 // instead of 101, 617 instead of 467 at D 128. The next tile's loads under way during the
 // arithmetic: no gain at D 32 (95.6 us, 96.4), slower at D 64 (509 us backward, 468). Three

@@ -22,20 +22,20 @@
 // bf16 and by 2^-11 in fp16, as the second product's operands have
 // to be; all sums, maxima and statistics are fp32.
 //
-// What bounds it: exponentials and conversions, not the products. Of 4096 x 4096 scores
-// of 32 heads, bf16, D 32 / 64 / 128:
-//   forward     168 / 174 / 242 us, 408 / 790 / 1,130 TFLOP/s; 2^29 exponentials at 16 a
-//               clock and SM take 115 us alone
-//   backward    483 / 531 / 832 us for 5 products' worth, 356 / 647 / 826 TFLOP/s (it
-//               computes 7)
+// What bounds it: chains of waits between products, exponentials and conversions; no pipe is
+// full. Of 4096 x 4096 scores of 32 heads, bf16, D 32 / 64 / 128:
+//   forward     169 / 173 / 239 us, 406 / 793 / 1,150 TFLOP/s; 2^29 exponentials at 16 a
+//               clock and SM take 115 us alone (D 64: 63% of their pipe, 34% of the products')
+//   backward    458 / 501 / 793 us for 5 products' worth, 375 / 686 / 866 TFLOP/s (it
+//               computes 7; D 64: 47% of the exponentials' pipe, 45% of the products')
 // Tiles, by what was measured at D 64 unless said otherwise:
 //   forward     two blocks of an SM (one waits for its products while the other takes
 //               exponentials) of 128 columns. 64 or 96 columns: slower, or the registers
 //               spill. D 128: tensor memory leaves 64 columns, and two buffers of weights.
 //   backward    one block with two groups of row warps, a half of each row's columns each:
-//               531 us; four groups 578, and three that take tiles in turn were slower than two.
-//               D 128 in kGradKV: the weights lie over the scores, so P is released, and
-//               its product issued, before dP is waited for.
+//               531 us when four groups took 578, and three that take tiles in turn were slower
+//               than two. D 128 in kGradKV: the weights lie over the scores, so P is released,
+//               and its product issued, before dP is waited for.
 //   kGradKV for few queries: see tc_short.
 #pragma once
 
