@@ -336,8 +336,9 @@ MSDA_API msda_status_t msda_debug_corners(const int64_t *spatial_shapes,
  *   any checked access was out of range since the last call (never in the
  *   normal build), else MSDA_ERR_DEVICE_WAIT if a wait between the warps of an
  *   attention kernel ran out (two seconds where microseconds are enough: the
- *   outputs of that call are not complete; either build), MSDA_OK otherwise;
- *   MSDA_ERR_CUDA if the synchronization or the readback fails.
+ *   outputs of that call are not complete, NaN where they are not; either
+ *   build), MSDA_OK otherwise; MSDA_ERR_CUDA if the synchronization or the
+ *   readback fails.
  * msda_debug_bounds_self_test: enqueues one range check that must fail (no
  *   memory is accessed), so that the next msda_device_check of the checked
  *   build returns MSDA_ERR_DEVICE_BOUNDS; a no-op check in the normal build.

@@ -661,8 +661,12 @@ __device__ __forceinline__ void attn_tc_block(const AttnArgs &a, const TcMaps &m
         // ------------------------------------------------ results
         if (ok && it > 0) ok = bar_wait(tc_bar<K::WEIGHTS>(done, it - 1), tc_phase<K::WEIGHTS>(it - 1), dead, a.err);
         tmem_after_sync();
-        const int count = it;          // column tiles of the block
-        if (any_valid && __all_sync(0xffffffffu, ok && !*dead)) {
+        // column tiles of the block; a wait that ran out leaves NaN, not what was in the output
+        const bool lost = !__all_sync(0xffffffffu, ok && !*dead);
+        const int count = lost ? 0 : it;
+        const float none = lost ? __int_as_float(0x7fffffff) : 0.0f;
+        if (lost) sum = none;
+        if (any_valid) {
             const int64_t row = MODE == kGradKV ? ((int64_t)w.b * a.S + rpos) * a.N + rhead : ((int64_t)w.b * a.Q + rpos) * a.M + rhead;
             const float ref = tc_reference(top, c, up);
             const float down = BACK ? ex2(-TcScale<T>::backward) : 1.0f;   // of P; of dS also 1 / ds_scale
@@ -688,8 +692,8 @@ __device__ __forceinline__ void attn_tc_block(const AttnArgs &a, const TcMaps &m
                 float v[32];
                 if (count > 0) tmem_read<32>(o, at_acc + 32 * q);
 #pragma unroll
-                for (int k = 0; k < 32; ++k) v[k] = count > 0 ? __uint_as_float(o[k]) : 0.0f;
-                if (a.classes) {
+                for (int k = 0; k < 32; ++k) v[k] = count > 0 ? __uint_as_float(o[k]) : none;
+                if (a.classes && !lost) {
                     bool finite = true;
 #pragma unroll
                     for (int k = 0; k < 32; ++k) finite = finite && isfinite(v[k]);
